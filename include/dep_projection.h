@@ -359,6 +359,145 @@ dep_status_t dep_projection_selftest_timeout(int32_t limit_us, int32_t *code);
  */
 dep_status_t dep_projection_plan_selftest_exchange(dep_plan_t plan, int32_t limit_us, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the projections of a delta-attention layer: the norm that feeds a
+ * projection, the projection with 8-bit integers on both sides, and the gated
+ * delta rule between the packed input projection (96 heads of 128 channels in
+ * 49376 rows) and the output projection.  No counterpart in the pages.
+ *
+ * These calls are asynchronous on `stream`, allocate nothing, do not
+ * synchronise and can be captured in CUDA graphs (dep_int8_plan and
+ * dep_int8_device_status excepted).  Tensors lie in device memory of the
+ * current device; strides are in elements; nothing is retained.  Status codes
+ * as above; a null `args`, a null required pointer or a bad size is
+ * INVALID_ARG.
+ * ------------------------------------------------------------------------ */
+
+/* Formats of a stored row. */
+#define DEP_QUANT_NONE 0 /* BF16, no scales */
+#define DEP_QUANT_INT8 1 /* int8, one scale for each row */
+#define DEP_QUANT_E4M3 2 /* e4m3, one scale for each group of 128 columns (the last
+                            group of a row may be shorter) */
+#define DEP_QUANT_GROUP 128
+#define DEP_NORM_MAX_COLS 65536
+
+/*
+ * Root-mean-square norm of `rows` rows of `cols` columns, after the residual's
+ * addition:
+ *
+ *     h = BF16(x + residual)            (h = x where residual is null)
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ * h is stored to residual_out (which may be `residual` itself, with the same
+ * stride) and the norm is taken of h as stored.  y is stored in one format:
+ *   NONE  BF16 [rows, cols], one rounding.
+ *   INT8  q = rint(127 p / P) with p = h * weight (exact in FP32) and P the
+ *         row's largest |p|: 1/rms cancels out of q.  scale[row] = P/rms/127.
+ *   E4M3  q = e4m3(448 p / P), P the group's largest |p|;
+ *         scale[row, group] = P/rms/448, scales contiguous [rows, ceil(cols/128)].
+ * Both quotients are rounded as if they were exact (ties to even), so q is the
+ * same on every run and machine.  A row (group) whose P is below 2^-100 is
+ * stored as zeros with a scale of zero; one that holds an infinity or a NaN has
+ * a scale that is infinite or NaN.
+ * Sums and scales are FP32.  Any alignment and strides >= cols; 16-byte aligned
+ * rows (8-byte for q) are moved in wide loads and stores.  `out` may be x
+ * itself (format NONE, same stride).  Errors: INVALID_ARG also for an output
+ * that overlaps an input or another output in any other way; UNSUPPORTED for
+ * cols > DEP_NORM_MAX_COLS.  rows == 0 does nothing.
+ */
+typedef struct {
+    const void *x;        /* BF16 [rows, cols] */
+    const void *residual; /* BF16 [rows, cols] or null */
+    const void *weight;   /* BF16 [cols] or null (ones) */
+    void *residual_out;   /* BF16 [rows, cols]; required with `residual`, else null */
+    void *out;            /* [rows, cols] of `quant`'s type */
+    float *scale;         /* scales of an 8-bit format, else null */
+    int64_t x_stride, residual_stride, residual_out_stride, out_stride;
+    int64_t rows, cols;
+    int32_t quant; /* DEP_QUANT_* */
+    float eps;     /* >= 0 */
+} dep_norm_args_t;
+
+dep_status_t dep_add_rms_norm(const dep_norm_args_t *args, void *stream);
+
+/* The rows of x in 8 bits, by the same rules without a norm: p = x, rms = 1.
+ * residual, weight and residual_out must be null, quant INT8 or E4M3; eps is
+ * not used.  Prepares the input of a projection that no norm feeds, and the
+ * weight of dep_int8_run (a scale for each output channel). */
+dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream);
+
+/*
+ * The gated delta rule over sequences packed one after another.  For each
+ * sequence and value head, with a state S [Dv, Dk] and for every token
+ *
+ *     S <- S diag(exp(g)),   S <- S + beta (v - S k) k^T,   o = scale * S q
+ *
+ * q, k: BF16 [tokens, Hq, Dk]; v: BF16 [tokens, Hv, Dv]; o: BF16 [tokens, Hv, Dv];
+ * heads contiguous in a token, tokens q_stride etc. apart, so that slices of a
+ * packed projection are read in place.  Hv is a multiple of Hq; value head h
+ * takes query and key head h / (Hv / Hq).  g: FP32 natural logarithm of the
+ * decay, one for each head [tokens, Hv] or (DEP_DELTA_CHANNEL) for each key
+ * channel [tokens, Hv, Dk]; minus infinity empties the state.  beta: FP32
+ * [tokens, Hv].  With DEP_DELTA_L2NORM q and k are first divided by
+ * sqrt(sum of squares + 1e-6) over their Dk channels.
+ * Sequences: cu_seqlens, int32 [n_seq + 1] in device memory, first tokens and
+ * the end (lengths may be zero; values are clipped to 0..tokens), or null for
+ * n_seq sequences of tokens / n_seq each.
+ * States: FP32 [n_states, Hv, Dv, Dk], contiguous.  Sequence s starts from
+ * state_in[i] and leaves state_out[i], i = slots[s] (int32, device memory) or s
+ * where slots is null.  state_in null: from zeros.  state_out may be state_in.
+ * A slot outside 0..n_states-1 (padding) has no state read or written and zeros
+ * for its outputs.  Two sequences of a call may not share a slot.
+ * States stay in FP32; o is rounded once.  Fixed order, no atomics.
+ * Dk is 64 or 128, Dv a multiple of 16 up to 256 (else UNSUPPORTED).
+ * MISALIGNED unless q, k, v, g (per channel), o and the states are 16-byte
+ * aligned, the strides of q, k, v and o multiples of 8 and g's of 4 (per channel),
+ * and cu_seqlens, slots, beta and a per-head g 4-byte aligned.
+ */
+#define DEP_DELTA_CHANNEL 1u /* g for each key channel */
+#define DEP_DELTA_L2NORM 2u  /* normalise q and k */
+
+typedef struct {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const float *state_in; /* or null */
+    float *state_out;
+    void *o;
+    const int32_t *cu_seqlens; /* or null */
+    const int32_t *slots;      /* or null */
+    int64_t q_stride, k_stride, v_stride, g_stride, beta_stride, o_stride; /* between tokens */
+    int64_t tokens, n_states;
+    int32_t n_seq, Hq, Hv, Dk, Dv;
+    uint32_t flags;
+    float scale;
+} dep_delta_args_t;
+
+dep_status_t dep_delta_rule(const dep_delta_args_t *args, void *stream);
+
+/*
+ * y[B,N] = BF16(x_scale[b] * w_scale[n] * sum_k x[b,k] * W[n,k]) with x and W
+ * int8: the projection at half the weight bytes.  The sum is exact (32-bit
+ * integers; K <= 131056, so that it cannot overflow); the two scales are
+ * multiplied in FP32, then with the sum, and the product is rounded to BF16.
+ * x [B,K], W [N,K], y [B,N] row-major, contiguous and 16-byte aligned, K a
+ * multiple of 16 (else MISALIGNED); x_scale [B] and w_scale [N] FP32.  y must
+ * not overlap an input.  B == 0 does nothing.
+ * A plan owns the workspace of one weight shape and batches of up to max_rows
+ * rows (wider ones run in passes); two runs of one plan must not overlap on
+ * the GPU.
+ */
+typedef struct dep_int8_plan_s *dep_int8_plan_t;
+
+dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan_t *out);
+dep_status_t dep_int8_run(dep_int8_plan_t plan, const void *x, const float *x_scale, const void *W,
+                          const float *w_scale, void *y, int32_t B, void *stream);
+/* Bytes of device workspace the plan owns. */
+dep_status_t dep_int8_plan_workspace(dep_int8_plan_t plan, size_t *bytes);
+/* As dep_projection_device_status, for the plan's own status word. */
+dep_status_t dep_int8_device_status(dep_int8_plan_t plan, void *stream, int32_t *code);
+/* Free the plan (synchronises its device).  NULL is a no-op. */
+void dep_int8_plan_destroy(dep_int8_plan_t plan);
+
 /* The binning rule on its own: index into keys[0..n_keys) of the entry serving
  * B rows -- smallest key >= B, else the largest key; -1 if n_keys < 1.  The keys
  * need not be sorted.  Pure host function. */

@@ -12,4 +12,5 @@ The binding loads the library lazily, on first use, and raises if it is
 missing: there is no CPU or library fallback.
 """
 from ._binding import *  # noqa: F401,F403
-from ._binding import DepError, Projection, dep_tactic_t, lib, EXPORTS  # noqa: F401
+from ._binding import DepError, Int8Projection, Projection, dep_tactic_t, lib, EXPORTS  # noqa: F401
+from ._binding import add_rms_norm, gated_delta_rule, quantize_rows  # noqa: F401

@@ -38,6 +38,14 @@ DEP_PLAN_TUNE = 1
 DEP_PLAN_PDL = 2
 DEP_PLAN_KEEP_PIECES = 4
 
+DEP_QUANT_NONE = 0
+DEP_QUANT_INT8 = 1
+DEP_QUANT_E4M3 = 2
+DEP_QUANT_GROUP = 128
+DEP_NORM_MAX_COLS = 65536
+DEP_DELTA_CHANNEL = 1
+DEP_DELTA_L2NORM = 2
+
 DEP_DEV_TIMEOUT_PRODUCER = 1
 DEP_DEV_TIMEOUT_CONSUMER = 2
 DEP_DEV_TIMEOUT_MMA = 3
@@ -54,6 +62,8 @@ EXPORTS = (
     "dep_status_string", "dep_projection_version", "dep_projection_run_static",
     "dep_projection_plan_partials", "dep_projection_plan_exchange", "dep_projection_probe_read",
     "dep_projection_plan_selftest_exchange",
+    "dep_add_rms_norm", "dep_quantize_rows", "dep_delta_rule", "dep_int8_plan", "dep_int8_run",
+    "dep_int8_plan_workspace", "dep_int8_device_status", "dep_int8_plan_destroy",
 )
 
 
@@ -66,6 +76,22 @@ class dep_tactic_t(ctypes.Structure):
 
     def __repr__(self):
         return f"dep_tactic_t({self.as_dict()})"
+
+
+class dep_norm_args_t(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_void_p) for name in ("x", "residual", "weight", "residual_out", "out", "scale")]
+                + [(name, ctypes.c_int64) for name in
+                   ("x_stride", "residual_stride", "residual_out_stride", "out_stride", "rows", "cols")]
+                + [("quant", ctypes.c_int32), ("eps", ctypes.c_float)])
+
+
+class dep_delta_args_t(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_void_p) for name in
+                 ("q", "k", "v", "g", "beta", "state_in", "state_out", "o", "cu_seqlens", "slots")]
+                + [(name, ctypes.c_int64) for name in
+                   ("q_stride", "k_stride", "v_stride", "g_stride", "beta_stride", "o_stride", "tokens", "n_states")]
+                + [(name, ctypes.c_int32) for name in ("n_seq", "Hq", "Hv", "Dk", "Dv")]
+                + [("flags", ctypes.c_uint32), ("scale", ctypes.c_float)])
 
 
 class DepError(RuntimeError):
@@ -112,6 +138,14 @@ def lib():
         "dep_projection_plan_exchange": ([vp, vp, ctypes.c_size_t, P(ctypes.c_size_t)], i32),
         "dep_projection_probe_read": ([vp, ctypes.c_size_t, vp, vp], i32),
         "dep_projection_plan_selftest_exchange": ([vp, i32, vp], i32),
+        "dep_add_rms_norm": ([P(dep_norm_args_t), vp], i32),
+        "dep_quantize_rows": ([P(dep_norm_args_t), vp], i32),
+        "dep_delta_rule": ([P(dep_delta_args_t), vp], i32),
+        "dep_int8_plan": ([i64, i64, i32, P(vp)], i32),
+        "dep_int8_run": ([vp, vp, vp, vp, vp, vp, i32, vp], i32),
+        "dep_int8_plan_workspace": ([vp, P(ctypes.c_size_t)], i32),
+        "dep_int8_device_status": ([vp, vp, P(i32)], i32),
+        "dep_int8_plan_destroy": ([vp], None),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -300,6 +334,49 @@ def dep_projection_probe_read(p, nbytes: int, sink, stream=None) -> None:
            "dep_projection_probe_read")
 
 
+def dep_add_rms_norm(args: dep_norm_args_t, stream=None) -> None:
+    _check(lib().dep_add_rms_norm(ctypes.byref(args), _stream(stream)), "dep_add_rms_norm")
+
+
+def dep_quantize_rows(args: dep_norm_args_t, stream=None) -> None:
+    _check(lib().dep_quantize_rows(ctypes.byref(args), _stream(stream)), "dep_quantize_rows")
+
+
+def dep_delta_rule(args: dep_delta_args_t, stream=None) -> None:
+    _check(lib().dep_delta_rule(ctypes.byref(args), _stream(stream)), "dep_delta_rule")
+
+
+def dep_int8_plan(N: int, K: int, max_rows: int = 256):
+    out = ctypes.c_void_p()
+    _check(lib().dep_int8_plan(N, K, max_rows, ctypes.byref(out)), "dep_int8_plan")
+    return out.value
+
+
+def dep_int8_run(plan, x, x_scale, W, w_scale, y, B: int | None = None, stream=None) -> None:
+    if B is None:
+        B = x.shape[0]
+    _check(lib().dep_int8_run(plan, _ptr(x), _ptr(x_scale), _ptr(W), _ptr(w_scale), _ptr(y), B, _stream(stream)),
+           "dep_int8_run")
+
+
+def dep_int8_plan_workspace(plan) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().dep_int8_plan_workspace(plan, ctypes.byref(b)), "dep_int8_plan_workspace")
+    return b.value
+
+
+def dep_int8_device_status(plan, stream=None) -> int:
+    code = ctypes.c_int32()
+    st = lib().dep_int8_device_status(plan, _stream(stream), ctypes.byref(code))
+    if st not in (DEP_OK, DEP_ERR_TIMEOUT):
+        _check(st, "dep_int8_device_status")
+    return code.value
+
+
+def dep_int8_plan_destroy(plan) -> None:
+    lib().dep_int8_plan_destroy(plan)
+
+
 class Projection:
     """A TP1 decode linear over one resident BF16 weight W[N,K]: the library's
     counterpart of DepProjection (runtime.dep page).  ``run(x, out)`` writes
@@ -329,6 +406,206 @@ class Projection:
     def close(self):
         if getattr(self, "plan", None):
             dep_projection_plan_destroy(self.plan)
+            self.plan = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---- around the projections ---------------------------------------------------
+
+_QUANT = {None: DEP_QUANT_NONE, "int8": DEP_QUANT_INT8, "e4m3": DEP_QUANT_E4M3}
+
+
+def _need(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream of the call that writes it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, name, dtype, device, shape):
+    """Stride between the rows of a matrix whose rows are contiguous."""
+    _need(t.dtype == dtype and t.device == device and tuple(t.shape) == shape and (shape[1] <= 1 or t.stride(1) == 1),
+          f"{name} must be a {dtype} matrix of shape {shape} with contiguous rows on {device}")
+    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+
+
+def _norm_call(call, x, weight, residual, residual_out, eps, quant, out, out_scale, stream):
+    import torch
+    _need(quant in _QUANT, "quant must be None, 'int8' or 'e4m3'")
+    _need(x.dim() == 2 and x.is_cuda, "x must be a CUDA matrix [rows, cols]")
+    rows, cols = shape = tuple(x.shape)
+    dev = x.device
+    a = dep_norm_args_t(x=x.data_ptr(), x_stride=_rows(x, "x", torch.bfloat16, dev, shape), rows=rows, cols=cols,
+                        quant=_QUANT[quant], eps=eps)
+    if weight is not None:
+        _need(weight.dtype == torch.bfloat16 and weight.device == dev and weight.shape == (cols,)
+              and weight.is_contiguous(), f"weight must be a contiguous bfloat16 vector of {cols} on {dev}")
+        a.weight = weight.data_ptr()
+    if residual is not None:
+        if residual_out is None:
+            residual_out = residual
+        a.residual, a.residual_out = residual.data_ptr(), residual_out.data_ptr()
+        a.residual_stride = _rows(residual, "residual", torch.bfloat16, dev, shape)
+        a.residual_out_stride = _rows(residual_out, "residual_out", torch.bfloat16, dev, shape)
+    else:
+        _need(residual_out is None, "residual_out needs a residual")
+    dtype = {None: torch.bfloat16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}[quant]
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    a.out, a.out_stride = out.data_ptr(), _rows(out, "out", dtype, dev, shape)
+    if quant is not None:
+        want = (rows,) if quant == "int8" else (rows, -(-cols // DEP_QUANT_GROUP))
+        if out_scale is None:
+            out_scale = _empty(want, torch.float32, dev, stream)
+        _need(out_scale.dtype == torch.float32 and out_scale.device == dev and tuple(out_scale.shape) == want
+              and out_scale.is_contiguous(), f"out_scale must be a contiguous float32 tensor of shape {want} on {dev}")
+        a.scale = out_scale.data_ptr()
+    else:
+        _need(out_scale is None, "out_scale needs an 8-bit format")
+    with torch.cuda.device(dev):
+        call(a, stream)
+    return out if quant is None else (out, out_scale)
+
+
+def add_rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, quant=None, out=None, out_scale=None,
+                 residual_out=None, stream=None):
+    """h = x + residual (stored to residual_out, by default over residual), then
+    h / rms(h) * weight: BF16, or with quant="int8" / "e4m3" 8-bit values and their
+    scales (see dep_add_rms_norm in include/dep_projection.h).
+
+    x, residual: bfloat16 [rows, cols] with contiguous rows; weight: bfloat16 [cols].
+    Returns out, or (out, out_scale) for an 8-bit format; both are allocated where
+    omitted.  scale is [rows] (int8) or [rows, ceil(cols / 128)] (e4m3)."""
+    return _norm_call(dep_add_rms_norm, x, weight, residual, residual_out, eps, quant, out, out_scale, stream)
+
+
+def quantize_rows(x, *, quant="int8", out=None, out_scale=None, stream=None):
+    """The rows of a bfloat16 matrix in 8 bits: (values, scales), as add_rms_norm
+    stores them but without a norm."""
+    _need(quant is not None, "quant must be 'int8' or 'e4m3'")
+    return _norm_call(dep_quantize_rows, x, None, None, None, 0.0, quant, out, out_scale, stream)
+
+
+def _heads(t, name, dtype, device, tokens):
+    """Stride between the tokens of [tokens, heads, ...] whose inner dimensions are contiguous."""
+    inner, want = 1, True
+    for d in range(t.dim() - 1, 0, -1):
+        want = want and (t.shape[d] == 1 or t.stride(d) == inner)
+        inner *= t.shape[d]
+    _need(t.dtype == dtype and t.device == device and t.shape[0] == tokens and want,
+          f"{name} must be a {dtype} tensor of {tokens} tokens with contiguous heads on {device}")
+    return t.stride(0) if tokens > 1 else max(inner, t.stride(0))
+
+
+def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens=None, n_seq: int | None = None,
+                     slots=None, scale: float | None = None, l2norm: bool = False, out=None, stream=None):
+    """The gated delta rule over packed sequences (see dep_delta_rule in
+    include/dep_projection.h): for each token S <- S diag(exp(g)), then
+    S <- S + beta (v - S k) k^T, o = scale S q.
+
+    q, k: bfloat16 [tokens, Hq, Dk]; v: bfloat16 [tokens, Hv, Dv]; g: float32
+    [tokens, Hv] or, for a decay of each key channel, [tokens, Hv, Dk]; beta:
+    float32 [tokens, Hv].  Heads are contiguous, tokens any stride apart.
+    cu_seqlens: int32 [n_seq + 1] on the device, or None for n_seq (default 1)
+    sequences of equal length.  state, state_out: float32 [n_states, Hv, Dv, Dk];
+    state None starts from zeros, state_out defaults to state (updated in place).
+    slots: int32 [n_seq] on the device, each sequence's place among the states
+    (outside 0..n_states-1: padding).  scale defaults to Dk ** -0.5.  Returns out,
+    bfloat16 [tokens, Hv, Dv] (allocated where omitted)."""
+    import torch
+    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and q.is_cuda and q.shape == k.shape,
+          "q, k [tokens, Hq, Dk] and v [tokens, Hv, Dv] must be CUDA tensors of three dimensions")
+    dev = q.device
+    T, hq, dk = q.shape
+    hv, dv = v.shape[1], v.shape[2]
+    channel = g.dim() == 3
+    _need(tuple(g.shape) == ((T, hv, dk) if channel else (T, hv)) and tuple(beta.shape) == (T, hv),
+          "g must be [tokens, Hv] or [tokens, Hv, Dk], and beta [tokens, Hv]")
+    if state_out is None:
+        state_out = state
+    _need(state_out is not None, "state_out must be given where state is not")
+    for name, s in (("state", state), ("state_out", state_out)):
+        _need(s is None or (s.dtype == torch.float32 and s.device == dev and s.dim() == 4
+                            and tuple(s.shape[1:]) == (hv, dv, dk) and s.is_contiguous()
+                            and s.shape[0] == state_out.shape[0]),
+              f"{name} must be a contiguous float32 tensor [n_states, {hv}, {dv}, {dk}] on {dev}")
+    if cu_seqlens is not None:
+        _need(cu_seqlens.dtype == torch.int32 and cu_seqlens.device == dev and cu_seqlens.dim() == 1
+              and cu_seqlens.is_contiguous() and cu_seqlens.shape[0] >= 1
+              and n_seq in (None, cu_seqlens.shape[0] - 1),
+              f"cu_seqlens must be a contiguous int32 vector of n_seq + 1 on {dev}")
+        n_seq = cu_seqlens.shape[0] - 1
+    elif n_seq is None:
+        n_seq = 1
+    if slots is not None:
+        _need(slots.dtype == torch.int32 and slots.device == dev and tuple(slots.shape) == (n_seq,)
+              and slots.is_contiguous(), f"slots must be a contiguous int32 vector of {n_seq} on {dev}")
+    if out is None:
+        out = _empty((T, hv, dv), torch.bfloat16, dev, stream)
+    _need(tuple(out.shape) == (T, hv, dv), f"out must have shape {(T, hv, dv)}")
+    a = dep_delta_args_t(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state), state_out.data_ptr(),
+        out.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _heads(q, "q", torch.bfloat16, dev, T),
+        _heads(k, "k", torch.bfloat16, dev, T), _heads(v, "v", torch.bfloat16, dev, T),
+        _heads(g, "g", torch.float32, dev, T), _heads(beta, "beta", torch.float32, dev, T),
+        _heads(out, "out", torch.bfloat16, dev, T), T, state_out.shape[0], n_seq, hq, hv, dk, dv,
+        (DEP_DELTA_CHANNEL if channel else 0) | (DEP_DELTA_L2NORM if l2norm else 0),
+        dk ** -0.5 if scale is None else scale)
+    with torch.cuda.device(dev):
+        dep_delta_rule(a, stream)
+    return out
+
+
+class Int8Projection:
+    """A TP1 linear over one resident int8 weight W[N,K] with a scale for each
+    output channel: ``run(x, x_scale)`` writes
+    BF16(x_scale[b] * w_scale[n] * sum_k x[b,k] W[n,k]) for int8 x with a scale for
+    each row, as add_rms_norm(quant="int8") and quantize_rows make them.  Batches of
+    more than max_rows rows run in passes.  One projection per stream."""
+
+    def __init__(self, weight, weight_scale, max_rows: int = 256):
+        import torch
+        _need(weight.dtype == torch.int8 and weight.is_cuda and weight.dim() == 2 and weight.is_contiguous(),
+              "weight must be a contiguous CUDA int8 tensor [N, K]")
+        self.N, self.K = weight.shape
+        _need(weight_scale.dtype == torch.float32 and weight_scale.device == weight.device
+              and tuple(weight_scale.shape) == (self.N,) and weight_scale.is_contiguous(),
+              f"weight_scale must be a contiguous float32 vector of {self.N} on {weight.device}")
+        self.weight, self.weight_scale = weight, weight_scale
+        with torch.cuda.device(weight.device):
+            self.plan = dep_int8_plan(self.N, self.K, max_rows)
+
+    def run(self, x, x_scale, out=None, stream=None):
+        import torch
+        dev = self.weight.device
+        _need(x.dtype == torch.int8 and x.is_contiguous() and x.device == dev and x.dim() == 2
+              and x.shape[1] == self.K, f"x must be a contiguous int8 tensor [rows, {self.K}] on {dev}")
+        B = x.shape[0]
+        _need(x_scale.dtype == torch.float32 and x_scale.device == dev and x_scale.is_contiguous()
+              and x_scale.numel() == B, f"x_scale must be a contiguous float32 vector of {B} on {dev}")
+        if out is None:
+            out = _empty((B, self.N), torch.bfloat16, dev, stream)
+        else:
+            _need(out.dtype == torch.bfloat16 and out.device == dev and tuple(out.shape) == (B, self.N)
+                  and out.is_contiguous(), f"out must be a contiguous bfloat16 tensor {(B, self.N)} on {dev}")
+        dep_int8_run(self.plan, x, x_scale, self.weight, self.weight_scale, out, B, stream)
+        return out
+
+    def close(self):
+        if getattr(self, "plan", None):
+            dep_int8_plan_destroy(self.plan)
             self.plan = None
 
     def __del__(self):

@@ -1,0 +1,377 @@
+// rms_norm.cu -- RMS norm with the residual's addition and an 8-bit output, and
+// the 8-bit quantisation of rows without a norm.
+//
+//     h = bf16(x + r);  y = h * rstd * w,  rstd = 1 / sqrt(mean(h^2) + eps)
+//
+// One pass over memory: a row (or, for up to 1024 columns, a warp's row) stays
+// in registers between the reduction and the store.  The quantised values do
+// not depend on rstd: with p = h * w, int8 q = rint(127 p / max|p|), so one
+// reduction gives the sum of squares and max|p| together.
+//
+// Exact rounding.  h and w have 8 significant bits, so p is exact in FP32 (16
+// bits), and so are 127 p (23) and 448 p (19).
+//   int8: the quotient's nearest integer guess c = rint(127 p * (1 / P)) is
+//     settled by the remainder 127 p - c P, which FP32 holds exactly (7 + 16
+//     bits): compare twice its size with P, ties to even.
+//   e4m3: a quotient that is no tie (of 5 bits) differs from every tie by at
+//     least 2^-21 of itself (the integers 448 p 2^s and tie * P differ by one or
+//     more, and tie * P < 2^21), more than the 2^-23 of a product with a rounded
+//     reciprocal; one Newton step makes a quotient that is a tie exact, and the
+//     conversion then rounds ties to even.
+// P below 2^-100 is flushed (stored as zero), which keeps 1 / P finite.
+//
+// Bound: DRAM.  Bytes of a row: 2 cols (x) + 4 cols with a residual + the output.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "layer.h"
+
+namespace dep {
+namespace {
+
+struct NormParams {
+    const uint16_t *x, *r, *w;
+    uint16_t *h;
+    void *out;
+    float *scale;
+    int64_t xs, rs, hs, os;
+    int64_t rows;
+    int32_t cols;
+    float eps;
+};
+
+constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
+
+__device__ __forceinline__ float bf(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
+
+// Largest value; a NaN on either side gives a NaN.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Eight consecutive elements (16 bits each) from column c on; columns past n read as zero.
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t *p, int c, int n)
+{
+    if (VEC)
+        return c < n ? *reinterpret_cast<const uint4 *>(p + c) : make_uint4(0, 0, 0, 0);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = c + 2 * i < n ? p[c + 2 * i] : 0, hi = c + 2 * i + 1 < n ? p[c + 2 * i + 1] : 0;
+        v[i] = lo | hi << 16;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t *p, int c, int n, uint4 v)
+{
+    if (VEC) {
+        if (c < n)
+            *reinterpret_cast<uint4 *>(p + c) = v;
+        return;
+    }
+    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < n)
+            p[c + i] = (uint16_t)(a[i / 2] >> (16 * (i & 1)));
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8b(uint8_t *p, int c, int n, uint2 v)
+{
+    if (VEC) {
+        if (c < n)
+            *reinterpret_cast<uint2 *>(p + c) = v;
+        return;
+    }
+    const uint32_t a[2] = {v.x, v.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < n)
+            p[c + i] = (uint8_t)(a[i / 4] >> (8 * (i & 3)));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// rint(127 p / P), exactly (see above); inv = 1 / P rounded, or 0 for a flushed row.
+__device__ __forceinline__ uint32_t quant_int8(float p, float P, float inv)
+{
+    const float t = 127.0f * p;
+    float c = rintf(t * inv);
+    const float rem = fmaf(-c, P, t), two = fabsf(rem) * 2.0f;
+    const bool odd = ((int)c & 1) != 0;
+    if (inv != 0.0f && (two > P || (two == P && odd)))
+        c += rem > 0.0f ? 1.0f : -1.0f;
+    return (uint32_t)(int)c & 0xFFu;
+}
+
+// 448 p / P to within far less than half an e4m3 step, exact where it is a tie.
+__device__ __forceinline__ float quot_e4m3(float p, float P, float inv)
+{
+    const float t = 448.0f * p;
+    const float s = t * inv;
+    return fmaf(fmaf(-s, P, t), inv, s);
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// WARP_ROW: blockDim = (32, 8), a row for each warp; else blockDim = (THREADS, 1), a row for each block.
+// Thread t holds the eight columns from 8 (t + i * threads) on, i < VPT.
+template <int FMT, bool NORM, bool VEC, int VPT, bool WARP_ROW, int THREADS>
+__global__ void __launch_bounds__(WARP_ROW ? 256 : THREADS) norm_kernel(const NormParams a)
+{
+    const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * 8 + threadIdx.y : (int64_t)blockIdx.x;
+    if (WARP_ROW && row >= a.rows)
+        return;
+    const int t = threadIdx.x, threads = WARP_ROW ? 32 : THREADS, n = a.cols;
+    const uint16_t *x = a.x + row * a.xs;
+    uint4 hv[VPT], wv[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        hv[i] = load8<VEC>(x, 8 * (t + i * threads), n);
+    if (NORM) {
+        if (a.r) {
+            const uint16_t *r = a.r + row * a.rs;
+            uint4 rv[VPT];
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                rv[i] = load8<VEC>(r, 8 * (t + i * threads), n);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                uint32_t *h = &hv[i].x;
+                const uint32_t *q = &rv[i].x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    h[j] = pack_bf16(bf(h[j] & 0xFFFFu) + bf(q[j] & 0xFFFFu), bf(h[j] >> 16) + bf(q[j] >> 16));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            wv[i] = a.w ? load8<VEC>(a.w, 8 * (t + i * threads), n)
+                        : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        if (a.r) {
+            uint16_t *ho = a.h + row * a.hs;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                store8<VEC>(ho, 8 * (t + i * threads), n, hv[i]);
+        }
+    }
+    // p = h * w of element j of vector i
+    auto prod = [&](int i, int j) {
+        const uint32_t h = (&hv[i].x)[j / 2];
+        const float hf = bf(j & 1 ? h >> 16 : h & 0xFFFFu);
+        if (!NORM)
+            return hf;
+        const uint32_t w = (&wv[i].x)[j / 2];
+        return hf * bf(j & 1 ? w >> 16 : w & 0xFFFFu);
+    };
+    float ss = 0.0f, top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t h = (&hv[i].x)[j / 2];
+            const float hf = bf(j & 1 ? h >> 16 : h & 0xFFFFu);
+            if (NORM)
+                ss = fmaf(hf, hf, ss);
+            if (FMT == DEP_QUANT_INT8)
+                top = max_nan(top, fabsf(prod(i, j)));
+        }
+    }
+    if (NORM || FMT == DEP_QUANT_INT8) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            ss += __shfl_xor_sync(~0u, ss, o);
+            if (FMT == DEP_QUANT_INT8)
+                top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+        }
+        if (!WARP_ROW) {
+            constexpr int kWarps = THREADS / 32;
+            __shared__ float2 part[kWarps];
+            if ((t & 31) == 0)
+                part[t >> 5] = make_float2(ss, top);
+            __syncthreads();
+            ss = 0.0f;
+            top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {  // every thread adds the warps' parts in the same order
+                ss += part[i].x;
+                top = max_nan(top, part[i].y);
+            }
+        }
+    }
+    const float rstd = NORM ? 1.0f / sqrtf(ss / (float)n + a.eps) : 1.0f;
+    if (FMT == DEP_QUANT_NONE) {
+        uint16_t *o = static_cast<uint16_t *>(a.out) + row * a.os;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            uint4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                (&v.x)[j] = pack_bf16(prod(i, 2 * j) * rstd, prod(i, 2 * j + 1) * rstd);
+            store8<VEC>(o, 8 * (t + i * threads), n, v);
+        }
+    } else if (FMT == DEP_QUANT_INT8) {
+        const bool flush = top < kTiny;
+        const float inv = flush ? 0.0f : 1.0f / top;
+        if (t == 0)
+            a.scale[row] = flush ? 0.0f : top * rstd / 127.0f;
+        uint8_t *o = static_cast<uint8_t *>(a.out) + row * a.os;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            uint32_t v[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j / 4] |= quant_int8(prod(i, j), top, inv) << (8 * (j & 3));
+            store8b<VEC>(o, 8 * (t + i * threads), n, make_uint2(v[0], v[1]));
+        }
+    } else {
+        uint8_t *o = static_cast<uint8_t *>(a.out) + row * a.os;
+        float *sc = a.scale + row * ((n + DEP_QUANT_GROUP - 1) / DEP_QUANT_GROUP);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {  // 16 neighbouring threads hold a group
+            const int c = 8 * (t + i * threads);
+            float g = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                g = max_nan(g, fabsf(prod(i, j)));
+#pragma unroll
+            for (int d = 8; d; d >>= 1)
+                g = max_nan(g, __shfl_xor_sync(~0u, g, d));
+            const bool flush = g < kTiny;
+            const float inv = flush ? 0.0f : 1.0f / g;
+            if ((t & 15) == 0 && c < n)
+                sc[c / DEP_QUANT_GROUP] = flush ? 0.0f : g * rstd / 448.0f;
+            uint32_t v[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j / 2] |= pack_e4m3(quot_e4m3(prod(i, 2 * j), g, inv), quot_e4m3(prod(i, 2 * j + 1), g, inv))
+                            << (16 * (j & 1));
+            store8b<VEC>(o, c, n, make_uint2(v[0], v[1]));
+        }
+    }
+}
+
+template <int FMT, bool NORM, bool VEC>
+cudaError_t norm_launch(const NormParams &a, cudaStream_t s)
+{
+    const int vecs = (a.cols + 7) / 8;
+    const dim3 warp_grid((unsigned)((a.rows + 7) / 8)), grid((unsigned)a.rows);
+    if (vecs <= 32)
+        norm_kernel<FMT, NORM, VEC, 1, true, 256><<<warp_grid, dim3(32, 8), 0, s>>>(a);
+    else if (vecs <= 128)
+        norm_kernel<FMT, NORM, VEC, 4, true, 256><<<warp_grid, dim3(32, 8), 0, s>>>(a);
+    else if (vecs <= 512)
+        norm_kernel<FMT, NORM, VEC, 2, false, 256><<<grid, 256, 0, s>>>(a);
+    else if (vecs <= 1024)
+        norm_kernel<FMT, NORM, VEC, 4, false, 256><<<grid, 256, 0, s>>>(a);
+    else if (vecs <= 2048)
+        norm_kernel<FMT, NORM, VEC, 4, false, 512><<<grid, 512, 0, s>>>(a);
+    else
+        norm_kernel<FMT, NORM, VEC, 8, false, 1024><<<grid, 1024, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool VEC>
+cudaError_t norm_dispatch(const NormParams &a, int quant, bool norm, cudaStream_t s)
+{
+    if (!norm)
+        return quant == DEP_QUANT_INT8 ? norm_launch<DEP_QUANT_INT8, false, VEC>(a, s)
+                                       : norm_launch<DEP_QUANT_E4M3, false, VEC>(a, s);
+    return quant == DEP_QUANT_NONE   ? norm_launch<DEP_QUANT_NONE, true, VEC>(a, s)
+           : quant == DEP_QUANT_INT8 ? norm_launch<DEP_QUANT_INT8, true, VEC>(a, s)
+                                     : norm_launch<DEP_QUANT_E4M3, true, VEC>(a, s);
+}
+
+dep_status_t norm_entry(const dep_norm_args_t *p, bool norm, void *stream)
+{
+    if (!p || p->rows < 0 || p->cols < 1 || p->quant < DEP_QUANT_NONE || p->quant > DEP_QUANT_E4M3)
+        return DEP_ERR_INVALID_ARG;
+    const bool q8 = p->quant != DEP_QUANT_NONE;
+    if (norm ? !(p->eps >= 0.0f) || (p->residual != nullptr) != (p->residual_out != nullptr)
+             : p->residual || p->weight || p->residual_out || !q8)
+        return DEP_ERR_INVALID_ARG;
+    if (p->rows == 0)
+        return DEP_OK;
+    if (!p->x || !p->out || q8 != (p->scale != nullptr))
+        return DEP_ERR_INVALID_ARG;
+    if (p->cols > DEP_NORM_MAX_COLS || p->rows > INT32_MAX)
+        return DEP_ERR_UNSUPPORTED;
+    const int64_t C = p->cols, R = p->rows;
+    if (p->x_stride < C || p->out_stride < C ||
+        (p->residual && (p->residual_stride < C || p->residual_out_stride < C)))
+        return DEP_ERR_INVALID_ARG;
+    if (!aligned(p->x, 2) || !aligned(p->residual, 2) || !aligned(p->residual_out, 2) || !aligned(p->weight, 2) ||
+        (!q8 && !aligned(p->out, 2)) || !aligned(p->scale, 4))
+        return DEP_ERR_MISALIGNED;
+    const int64_t ob = q8 ? 1 : 2;
+    const Rows x{p->x, 2 * C, 2 * p->x_stride, R}, out{p->out, ob * C, ob * p->out_stride, R};
+    const Rows w{p->weight, 2 * C, 2 * C, p->weight ? 1 : 0};
+    const int64_t groups = p->quant == DEP_QUANT_INT8 ? 1 : (C + DEP_QUANT_GROUP - 1) / DEP_QUANT_GROUP;
+    const Rows sc{p->scale, 4 * groups, 4 * groups, q8 ? R : 0};
+    const Rows r{p->residual, 2 * C, 2 * p->residual_stride, p->residual ? R : 0};
+    const Rows h{p->residual_out, 2 * C, 2 * p->residual_out_stride, p->residual ? R : 0};
+    // Every block has read its row before it writes, so equal rows may be shared; anything else may not.
+    if ((overlap(out, x) && !(p->out == p->x && !q8 && p->out_stride == p->x_stride)) || overlap(out, w) ||
+        overlap(out, r) || overlap(out, h) || overlap(out, sc) || overlap(sc, x) || overlap(sc, w) ||
+        overlap(sc, r) || overlap(sc, h) || overlap(h, w) ||
+        (overlap(h, r) && !(p->residual_out == p->residual && p->residual_out_stride == p->residual_stride)) ||
+        overlap(h, x))
+        return DEP_ERR_INVALID_ARG;
+    NormParams a{static_cast<const uint16_t *>(p->x),
+                 static_cast<const uint16_t *>(p->residual),
+                 static_cast<const uint16_t *>(p->weight),
+                 static_cast<uint16_t *>(p->residual_out),
+                 p->out,
+                 p->scale,
+                 p->x_stride,
+                 p->residual_stride,
+                 p->residual_out_stride,
+                 p->out_stride,
+                 R,
+                 (int32_t)C,
+                 p->eps};
+    // Wide loads and stores where every row of every tensor allows them.
+    const bool vec = C % 8 == 0 && x.aligned(16) && r.aligned(16) && h.aligned(16) && w.aligned(16) &&
+                     out.aligned(q8 ? 8 : 16);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = vec ? norm_dispatch<true>(a, p->quant, norm, s) : norm_dispatch<false>(a, p->quant, norm, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return DEP_ERR_CUDA;
+    }
+    return DEP_OK;
+}
+
+}  // namespace
+}  // namespace dep
+
+extern "C" {
+
+dep_status_t dep_add_rms_norm(const dep_norm_args_t *args, void *stream)
+{
+    return dep::norm_entry(args, true, stream);
+}
+
+dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream)
+{
+    return dep::norm_entry(args, false, stream);
+}
+
+}  // extern "C"
