@@ -416,13 +416,11 @@ class Projection:
 
 
 # ---- around the projections ---------------------------------------------------
+#
+# Calls of a few microseconds of GPU work each: the checks below build no messages
+# and no contexts unless they refuse.
 
 _QUANT = {None: DEP_QUANT_NONE, "int8": DEP_QUANT_INT8, "e4m3": DEP_QUANT_E4M3}
-
-
-def _need(ok, message):
-    if not ok:
-        raise ValueError(message)
 
 
 def _empty(shape, dtype, device, stream):
@@ -434,48 +432,63 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, name, dtype, device, shape):
+def _on(device, call, args, stream):
+    """call(args, stream) with `device` current; stream None: its current stream."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        call(args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream)
+        return
+    with torch.cuda.device(device):
+        call(args, stream)
+
+
+def _rows(t, name, dtype, device, rows, cols):
     """Stride between the rows of a matrix whose rows are contiguous."""
-    _need(t.dtype == dtype and t.device == device and tuple(t.shape) == shape and (shape[1] <= 1 or t.stride(1) == 1),
-          f"{name} must be a {dtype} matrix of shape {shape} with contiguous rows on {device}")
-    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+    if t.dtype != dtype or t.device != device or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (
+            cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a {dtype} matrix [{rows}, {cols}] with contiguous rows on {device}")
+    return t.stride(0) if rows > 1 else cols
 
 
 def _norm_call(call, x, weight, residual, residual_out, eps, quant, out, out_scale, stream):
     import torch
-    _need(quant in _QUANT, "quant must be None, 'int8' or 'e4m3'")
-    _need(x.dim() == 2 and x.is_cuda, "x must be a CUDA matrix [rows, cols]")
-    rows, cols = shape = tuple(x.shape)
-    dev = x.device
-    a = dep_norm_args_t(x=x.data_ptr(), x_stride=_rows(x, "x", torch.bfloat16, dev, shape), rows=rows, cols=cols,
-                        quant=_QUANT[quant], eps=eps)
+    if quant not in _QUANT:
+        raise ValueError("quant must be None, 'int8' or 'e4m3'")
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("x must be a CUDA matrix [rows, cols]")
+    rows, cols = x.shape
+    dev, bf16 = x.device, torch.bfloat16
+    w_ptr = r_ptr = ro_ptr = s_ptr = None
+    r_stride = ro_stride = 0
     if weight is not None:
-        _need(weight.dtype == torch.bfloat16 and weight.device == dev and weight.shape == (cols,)
-              and weight.is_contiguous(), f"weight must be a contiguous bfloat16 vector of {cols} on {dev}")
-        a.weight = weight.data_ptr()
+        if weight.dtype != bf16 or weight.device != dev or weight.dim() != 1 or weight.shape[0] != cols or (
+                not weight.is_contiguous()):
+            raise ValueError(f"weight must be a contiguous bfloat16 vector of {cols} on {dev}")
+        w_ptr = weight.data_ptr()
     if residual is not None:
+        r_ptr, r_stride = residual.data_ptr(), _rows(residual, "residual", bf16, dev, rows, cols)
         if residual_out is None:
-            residual_out = residual
-        a.residual, a.residual_out = residual.data_ptr(), residual_out.data_ptr()
-        a.residual_stride = _rows(residual, "residual", torch.bfloat16, dev, shape)
-        a.residual_out_stride = _rows(residual_out, "residual_out", torch.bfloat16, dev, shape)
-    else:
-        _need(residual_out is None, "residual_out needs a residual")
-    dtype = {None: torch.bfloat16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}[quant]
+            ro_ptr, ro_stride = r_ptr, r_stride
+        else:
+            ro_ptr, ro_stride = residual_out.data_ptr(), _rows(residual_out, "residual_out", bf16, dev, rows, cols)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    dtype = bf16 if quant is None else torch.int8 if quant == "int8" else torch.float8_e4m3fn
     if out is None:
-        out = _empty(shape, dtype, dev, stream)
-    a.out, a.out_stride = out.data_ptr(), _rows(out, "out", dtype, dev, shape)
+        out = _empty((rows, cols), dtype, dev, stream)
     if quant is not None:
         want = (rows,) if quant == "int8" else (rows, -(-cols // DEP_QUANT_GROUP))
         if out_scale is None:
             out_scale = _empty(want, torch.float32, dev, stream)
-        _need(out_scale.dtype == torch.float32 and out_scale.device == dev and tuple(out_scale.shape) == want
-              and out_scale.is_contiguous(), f"out_scale must be a contiguous float32 tensor of shape {want} on {dev}")
-        a.scale = out_scale.data_ptr()
-    else:
-        _need(out_scale is None, "out_scale needs an 8-bit format")
-    with torch.cuda.device(dev):
-        call(a, stream)
+        elif out_scale.dtype != torch.float32 or out_scale.device != dev or out_scale.shape != want or (
+                not out_scale.is_contiguous()):
+            raise ValueError(f"out_scale must be a contiguous float32 tensor of shape {want} on {dev}")
+        s_ptr = out_scale.data_ptr()
+    elif out_scale is not None:
+        raise ValueError("out_scale needs an 8-bit format")
+    _on(dev, call, dep_norm_args_t(
+        x.data_ptr(), r_ptr, w_ptr, ro_ptr, out.data_ptr(), s_ptr, _rows(x, "x", bf16, dev, rows, cols), r_stride,
+        ro_stride, _rows(out, "out", dtype, dev, rows, cols), rows, cols, _QUANT[quant], eps), stream)
     return out if quant is None else (out, out_scale)
 
 
@@ -494,19 +507,22 @@ def add_rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, quant=None
 def quantize_rows(x, *, quant="int8", out=None, out_scale=None, stream=None):
     """The rows of a bfloat16 matrix in 8 bits: (values, scales), as add_rms_norm
     stores them but without a norm."""
-    _need(quant is not None, "quant must be 'int8' or 'e4m3'")
+    if quant is None:
+        raise ValueError("quant must be 'int8' or 'e4m3'")
     return _norm_call(dep_quantize_rows, x, None, None, None, 0.0, quant, out, out_scale, stream)
 
 
-def _heads(t, name, dtype, device, tokens):
+def _heads(t, name, dtype, device, shape):
     """Stride between the tokens of [tokens, heads, ...] whose inner dimensions are contiguous."""
-    inner, want = 1, True
-    for d in range(t.dim() - 1, 0, -1):
-        want = want and (t.shape[d] == 1 or t.stride(d) == inner)
-        inner *= t.shape[d]
-    _need(t.dtype == dtype and t.device == device and t.shape[0] == tokens and want,
-          f"{name} must be a {dtype} tensor of {tokens} tokens with contiguous heads on {device}")
-    return t.stride(0) if tokens > 1 else max(inner, t.stride(0))
+    inner, ok = 1, t.dtype == dtype and t.device == device and t.shape == shape
+    if ok:
+        strides = t.stride()
+        for d in range(len(shape) - 1, 0, -1):
+            ok = ok and (shape[d] == 1 or strides[d] == inner)
+            inner *= shape[d]
+    if not ok:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on {device}")
+    return strides[0] if shape[0] > 1 else inner
 
 
 def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens=None, n_seq: int | None = None,
@@ -525,46 +541,41 @@ def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens
     (outside 0..n_states-1: padding).  scale defaults to Dk ** -0.5.  Returns out,
     bfloat16 [tokens, Hv, Dv] (allocated where omitted)."""
     import torch
-    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and q.is_cuda and q.shape == k.shape,
-          "q, k [tokens, Hq, Dk] and v [tokens, Hv, Dv] must be CUDA tensors of three dimensions")
-    dev = q.device
-    T, hq, dk = q.shape
-    hv, dv = v.shape[1], v.shape[2]
-    channel = g.dim() == 3
-    _need(tuple(g.shape) == ((T, hv, dk) if channel else (T, hv)) and tuple(beta.shape) == (T, hv),
-          "g must be [tokens, Hv] or [tokens, Hv, Dk], and beta [tokens, Hv]")
+    if q.dim() != 3 or v.dim() != 3 or not q.is_cuda:
+        raise ValueError("q, k [tokens, Hq, Dk] and v [tokens, Hv, Dv] must be CUDA tensors of three dimensions")
+    dev, bf16, f32 = q.device, torch.bfloat16, torch.float32
+    T, hq, dk = qk_shape = q.shape
+    _, hv, dv = v.shape
+    v_shape, channel = (T, hv, dv), g.dim() == 3
     if state_out is None:
         state_out = state
-    _need(state_out is not None, "state_out must be given where state is not")
-    for name, s in (("state", state), ("state_out", state_out)):
-        _need(s is None or (s.dtype == torch.float32 and s.device == dev and s.dim() == 4
-                            and tuple(s.shape[1:]) == (hv, dv, dk) and s.is_contiguous()
-                            and s.shape[0] == state_out.shape[0]),
-              f"{name} must be a contiguous float32 tensor [n_states, {hv}, {dv}, {dk}] on {dev}")
+        if state is None:
+            raise ValueError("state_out must be given where state is not")
+    for s in (state_out,) if state is None or state is state_out else (state, state_out):
+        if s.dtype != f32 or s.device != dev or s.dim() != 4 or s.shape[1:] != (hv, dv, dk) or (
+                not s.is_contiguous()) or s.shape[0] != state_out.shape[0]:
+            raise ValueError(f"state and state_out must be contiguous float32 tensors [n_states, {hv}, {dv}, {dk}] on {dev}")
     if cu_seqlens is not None:
-        _need(cu_seqlens.dtype == torch.int32 and cu_seqlens.device == dev and cu_seqlens.dim() == 1
-              and cu_seqlens.is_contiguous() and cu_seqlens.shape[0] >= 1
-              and n_seq in (None, cu_seqlens.shape[0] - 1),
-              f"cu_seqlens must be a contiguous int32 vector of n_seq + 1 on {dev}")
-        n_seq = cu_seqlens.shape[0] - 1
+        n = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.device != dev or n < 0 or not cu_seqlens.is_contiguous() or (
+                n_seq is not None and n_seq != n):
+            raise ValueError(f"cu_seqlens must be a contiguous int32 vector of n_seq + 1 on {dev}")
+        n_seq = n
     elif n_seq is None:
         n_seq = 1
-    if slots is not None:
-        _need(slots.dtype == torch.int32 and slots.device == dev and tuple(slots.shape) == (n_seq,)
-              and slots.is_contiguous(), f"slots must be a contiguous int32 vector of {n_seq} on {dev}")
+    if slots is not None and (slots.dtype != torch.int32 or slots.device != dev or slots.shape != (n_seq,)
+                              or not slots.is_contiguous()):
+        raise ValueError(f"slots must be a contiguous int32 vector of {n_seq} on {dev}")
     if out is None:
-        out = _empty((T, hv, dv), torch.bfloat16, dev, stream)
-    _need(tuple(out.shape) == (T, hv, dv), f"out must have shape {(T, hv, dv)}")
-    a = dep_delta_args_t(
+        out = _empty(v_shape, bf16, dev, stream)
+    _on(dev, dep_delta_rule, dep_delta_args_t(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state), state_out.data_ptr(),
-        out.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _heads(q, "q", torch.bfloat16, dev, T),
-        _heads(k, "k", torch.bfloat16, dev, T), _heads(v, "v", torch.bfloat16, dev, T),
-        _heads(g, "g", torch.float32, dev, T), _heads(beta, "beta", torch.float32, dev, T),
-        _heads(out, "out", torch.bfloat16, dev, T), T, state_out.shape[0], n_seq, hq, hv, dk, dv,
+        out.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _heads(q, "q", bf16, dev, qk_shape),
+        _heads(k, "k", bf16, dev, qk_shape), _heads(v, "v", bf16, dev, v_shape),
+        _heads(g, "g", f32, dev, (T, hv, dk) if channel else (T, hv)), _heads(beta, "beta", f32, dev, (T, hv)),
+        _heads(out, "out", bf16, dev, v_shape), T, state_out.shape[0], n_seq, hq, hv, dk, dv,
         (DEP_DELTA_CHANNEL if channel else 0) | (DEP_DELTA_L2NORM if l2norm else 0),
-        dk ** -0.5 if scale is None else scale)
-    with torch.cuda.device(dev):
-        dep_delta_rule(a, stream)
+        dk ** -0.5 if scale is None else scale), stream)
     return out
 
 
@@ -577,31 +588,36 @@ class Int8Projection:
 
     def __init__(self, weight, weight_scale, max_rows: int = 256):
         import torch
-        _need(weight.dtype == torch.int8 and weight.is_cuda and weight.dim() == 2 and weight.is_contiguous(),
-              "weight must be a contiguous CUDA int8 tensor [N, K]")
+        if weight.dtype != torch.int8 or not weight.is_cuda or weight.dim() != 2 or not weight.is_contiguous():
+            raise ValueError("weight must be a contiguous CUDA int8 tensor [N, K]")
         self.N, self.K = weight.shape
-        _need(weight_scale.dtype == torch.float32 and weight_scale.device == weight.device
-              and tuple(weight_scale.shape) == (self.N,) and weight_scale.is_contiguous(),
-              f"weight_scale must be a contiguous float32 vector of {self.N} on {weight.device}")
+        if weight_scale.dtype != torch.float32 or weight_scale.device != weight.device or (
+                weight_scale.shape != (self.N,)) or not weight_scale.is_contiguous():
+            raise ValueError(f"weight_scale must be a contiguous float32 vector of {self.N} on {weight.device}")
         self.weight, self.weight_scale = weight, weight_scale
+        self.device = weight.device
         with torch.cuda.device(weight.device):
             self.plan = dep_int8_plan(self.N, self.K, max_rows)
 
     def run(self, x, x_scale, out=None, stream=None):
         import torch
-        dev = self.weight.device
-        _need(x.dtype == torch.int8 and x.is_contiguous() and x.device == dev and x.dim() == 2
-              and x.shape[1] == self.K, f"x must be a contiguous int8 tensor [rows, {self.K}] on {dev}")
+        dev = self.device
+        if x.dtype != torch.int8 or x.device != dev or x.dim() != 2 or x.shape[1] != self.K or not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous int8 tensor [rows, {self.K}] on {dev}")
         B = x.shape[0]
-        _need(x_scale.dtype == torch.float32 and x_scale.device == dev and x_scale.is_contiguous()
-              and x_scale.numel() == B, f"x_scale must be a contiguous float32 vector of {B} on {dev}")
+        if x_scale.dtype != torch.float32 or x_scale.device != dev or x_scale.numel() != B or (
+                not x_scale.is_contiguous()):
+            raise ValueError(f"x_scale must be a contiguous float32 vector of {B} on {dev}")
         if out is None:
             out = _empty((B, self.N), torch.bfloat16, dev, stream)
-        else:
-            _need(out.dtype == torch.bfloat16 and out.device == dev and tuple(out.shape) == (B, self.N)
-                  and out.is_contiguous(), f"out must be a contiguous bfloat16 tensor {(B, self.N)} on {dev}")
-        dep_int8_run(self.plan, x, x_scale, self.weight, self.weight_scale, out, B, stream)
+        elif out.dtype != torch.bfloat16 or out.device != dev or out.shape != (B, self.N) or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous bfloat16 tensor [{B}, {self.N}] on {dev}")
+        _on(dev, self._run, (x, x_scale, out, B), stream)
         return out
+
+    def _run(self, args, stream):
+        x, x_scale, out, B = args
+        dep_int8_run(self.plan, x, x_scale, self.weight, self.weight_scale, out, B, stream)
 
     def close(self):
         if getattr(self, "plan", None):

@@ -2,60 +2,548 @@
 //
 //     y[b, n] = bf16(x_scale[b] * w_scale[n] * sum_k x[b, k] W[n, k])
 //
-// One warp for a weight row and eight batch rows: 16 bytes a lane of the row and
-// of each batch row, four-way integer dot products, the lanes' 32-bit sums added
-// by shuffles (integers: exact in any order).
+// This GPU's tensor cores have no fast 8-bit integer mode, but an int8 is exact in
+// FP16, a product of two is an integer of at most 2^14, and 1024 of them add up to
+// at most 2^24: an FP32 accumulator holds every such sum exactly, in any order.  So
+// the products run as FP16 MMAs, and after at most 1024 columns the accumulators
+// are drained into 32-bit integers.
+//
+// Two kernels, chained by programmatic dependent launch:
+//  * int8_widen_kernel writes x as FP16 into the plan's workspace, padded with zero
+//    rows to the MMA's width and with zero columns to whole stages.
+//  * int8_kernel<NT>: persistent blocks over units of 128 weight rows x 128 columns.
+//      warp 0      TMA: weight stages (16 KB of int8) and x stages (NT x 128 FP16)
+//      warp 1      issues tcgen05.mma, eight a unit: A = the weight, from tensor
+//                  memory, B = x, from shared memory, M = 128, N = NT
+//      CONV warps  turn a weight stage into FP16 and store it into a ring of four
+//                  slots of tensor memory: lane = weight row, so that the operand
+//                  crosses shared memory once, as bytes.  A byte b becomes FP16
+//                  1024 + (b ^ 0x80) by one byte permutation, and minus 1152 exactly b.
+//      EPI warps   drain the accumulators into integers, and finish tiles
+//    Where whole tiles would leave blocks idle, the blocks take equal ranges of
+//    units, and the parts of a tile that several blocks share are added into the
+//    plan's workspace by integer atomics (exact, so any order gives the same bits);
+//    the block whose part arrives last rounds and stores, and clears the workspace.
+//    No block waits for another one.
+// Bound: the weight's bytes up to about 128 rows, the tensor cores above.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <new>
 
 #include "internal.h"
 #include "layer.h"
+#include "ptx.cuh"
 
 struct dep_int8_plan_s {
     int64_t N = 0, K = 0;
     int32_t max_rows = 0;
     int device = -1;
     int sm_count = 0;
-    void *block = nullptr;  // device memory
+    void *block = nullptr;  // device memory: status, counters, sums, x in FP16
     size_t bytes = 0;
     int *status = nullptr;
+    int *counters = nullptr;  // arrivals at shared tiles, zero between launches
+    int *sums = nullptr;      // sums of shared tiles, zero between launches
+    size_t clear_bytes = 0;   // status, counters and sums, from `block` on
+    uint16_t *xh = nullptr;
+    uint64_t wait_limit_ns = 1000000000ull;  // 1 s per wait
 };
 
 namespace dep {
 namespace {
 
 constexpr int64_t kMaxK = 131056;  // 131056 * 128 * 128 < 2^31
+constexpr int kBM = 128;           // weight rows of a tile (MMA M)
+constexpr int kKU = 128;           // columns of a unit
+constexpr int kExact = 1024 / kKU; // units whose sums FP32 holds exactly
+constexpr int kWBytes = kBM * kKU; // a weight stage
+constexpr int kSlots = 4;          // ring of FP16 weight units in tensor memory
+constexpr int kSlotCols = kKU / 2; // its 32-bit columns a unit
+constexpr int kWarps = 16;
 
-__global__ void __launch_bounds__(256)
-    int8_rows_kernel(const int8_t *__restrict__ x, const float *__restrict__ xs, const int8_t *__restrict__ W,
-                     const float *__restrict__ ws, uint16_t *__restrict__ y, int B, int64_t N, int K)
+template <int NT>
+struct Int8Shape {
+    static constexpr int CONV = NT <= 64 ? 8 : 4;        // converting warps (from warp 4 on)
+    static constexpr int EPI = 12 - CONV;                // draining warps (the last)
+    static constexpr int COLS = NT / (EPI / 4);          // batch columns of a draining thread
+    static constexpr int BUFS = NT <= 128 ? 2 : 1;       // accumulators
+    static constexpr int X_BYTES = NT * kKU * 2;         // an x stage
+    static constexpr int XS = NT <= 64 ? 4 : NT == 128 ? 3 : 2;
+    static constexpr int WS = (kMaxDynamicSmem - 1024 - 512 - XS * X_BYTES) / kWBytes;
+    static constexpr int TMEM_ACC = kSlots * kSlotCols;  // accumulators start behind the ring
+    static constexpr int TMEM = TMEM_ACC + BUFS * NT <= 512 ? 512 : 0;
+    static constexpr int BARS = 2 * WS + 2 * XS + 2 * kSlots + 2 * BUFS + 1;
+    static constexpr int SMEM = 1024 + WS * kWBytes + XS * X_BYTES + BARS * 8 + 16;
+    static_assert(TMEM == 512 && SMEM <= kMaxDynamicSmem, "");
+};
+
+// How a launch deals its units out: `whole` tiles to a block, or equal ranges of units.
+struct Int8Split {
+    int64_t tiles, units;  // units of a tile
+    int blocks;
+    int whole;
+    __host__ __device__ int64_t begin(int64_t c) const
+    {
+        return whole ? sk_begin(c, tiles, blocks) * units : sk_begin(c, tiles * units, blocks);
+    }
+    __host__ __device__ int64_t owner(int64_t u) const
+    {
+        return whole ? sk_owner(u / units, tiles, blocks) : sk_owner(u, tiles * units, blocks);
+    }
+};
+
+struct Int8Params {
+    const float *xs, *ws;
+    uint16_t *y;
+    int B;
+    int64_t N;
+    Int8Split split;
+    int *counters, *sums;
+    int *status;
+    uint64_t limit_ns;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, FP16 inputs, FP32 accumulation.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int b0 = blockIdx.y * 8;
-    if (n >= N)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 lanes x 32 columns of tensor memory from 32 registers.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four int8 -> four FP16, exactly.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 ha = __hsub2(*reinterpret_cast<__half2 *>(&a), off), hb = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
+    lo = *reinterpret_cast<uint32_t *>(&ha);
+    hi = *reinterpret_cast<uint32_t *>(&hb);
+}
+
+// x [B, K] int8 -> xh [gridDim.y rows, Kp] FP16, zeros past B and K (Kp a multiple of 128, K of 16).
+__global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restrict__ x, uint16_t *__restrict__ xh, int B,
+                                                         int K, int Kp)
+{
+    griddep_launch_dependents();
+    const int row = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 16;
+    if (c >= Kp)
         return;
-    int acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int k = lane * 16; k < K; k += 512) {
-        const int4 w = *reinterpret_cast<const int4 *>(W + n * K + k);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < B && c < K)
+        v = *reinterpret_cast<const uint4 *>(x + (int64_t)row * K + c);
+    uint4 o[2];
+    widen4(v.x, o[0].x, o[0].y);
+    widen4(v.y, o[0].z, o[0].w);
+    widen4(v.z, o[1].x, o[1].y);
+    widen4(v.w, o[1].z, o[1].w);
+    uint4 *d = reinterpret_cast<uint4 *>(xh + (int64_t)row * Kp + c);
+    d[0] = o[0];
+    d[1] = o[1];
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Int8Params p)
+{
+    using S = Int8Shape<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    const uint32_t w0 = base, x0 = base + S::WS * kWBytes;
+    const uint32_t bars = x0 + S::XS * S::X_BYTES;
+    const uint32_t wfull = bars, wempty = wfull + 8 * S::WS, xfull = wempty + 8 * S::WS, xempty = xfull + 8 * S::XS,
+                   afull = xempty + 8 * S::XS, aempty = afull + 8 * kSlots, accf = aempty + 8 * kSlots,
+                   acce = accf + 8 * S::BUFS, done = acce + 8 * S::BUFS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (done + 8 - base));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t KU = p.split.units;
+    const SegOrder order(p.split.begin(blockIdx.x), p.split.begin(blockIdx.x + 1), KU);
+    const int64_t n_units = order.u_end - order.u_begin;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::WS; ++i) {
+            mbar_init(wfull + 8 * i, 1);
+            mbar_init(wempty + 8 * i, 4);
+        }
+        for (int i = 0; i < S::XS; ++i) {
+            mbar_init(xfull + 8 * i, 1);
+            mbar_init(xempty + 8 * i, 1);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(afull + 8 * i, 4);
+            mbar_init(aempty + 8 * i, 1);
+        }
+        for (int i = 0; i < S::BUFS; ++i) {
+            mbar_init(accf + 8 * i, 1);
+            mbar_init(acce + 8 * i, S::EPI);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::alloc(smem_u32(tmem_slot), 512);
+        tc::relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto give_up = [&](int code) {
+        record_status(p.status, code);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0) {
+        // ---------------- copies: lane 0 the weight, lane 1 (one warp on: warp 2) x ----------------
+        if (lane == 0) {
+            prefetch_tmap(&tmW);
+            const uint64_t pol = policy_evict_first();
+            UnitCursor cur(order);
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t issued = 0;
+            for (; !cur.done(); cur.next()) {
+                if (*abort_flag)
+                    break;
+                if (!mbar_wait(wempty + 8 * s, ph ^ 1u, p.limit_ns)) {
+                    give_up(DEP_DEV_TIMEOUT_PRODUCER);
+                    break;
+                }
+                mbar_arrive_expect_tx(wfull + 8 * s, kWBytes);
+                tma_load_2d(w0 + s * kWBytes, &tmW, (int)(cur.u % KU) * kKU, (int)(cur.u / KU) * kBM, wfull + 8 * s, pol);
+                ++issued;
+                if (++s == S::WS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            for (int64_t i = issued < S::WS ? issued : S::WS; i > 0; --i) {  // copies in flight
+                if (--s < 0) {
+                    s = S::WS - 1;
+                    ph ^= 1u;
+                }
+                if (!mbar_wait(wfull + 8 * s, ph, p.limit_ns))
+                    record_status(p.status, DEP_DEV_TIMEOUT_PRODUCER);
+            }
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            prefetch_tmap(&tmX);
+            const uint64_t pol = policy_evict_last();
+            griddep_wait();  // x in FP16 is written by the preceding grid
+            UnitCursor cur(order);
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t issued = 0;
+            for (; !cur.done(); cur.next()) {
+                if (*abort_flag)
+                    break;
+                if (!mbar_wait(xempty + 8 * s, ph ^ 1u, p.limit_ns)) {
+                    give_up(DEP_DEV_TIMEOUT_PRODUCER);
+                    break;
+                }
+                mbar_arrive_expect_tx(xfull + 8 * s, S::X_BYTES);
+                tma_load_3d(x0 + s * S::X_BYTES, &tmX, 0, 0, (int)(cur.u % KU) * (kKU / 64), xfull + 8 * s, pol);
+                ++issued;
+                if (++s == S::XS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            for (int64_t i = issued < S::XS ? issued : S::XS; i > 0; --i) {
+                if (--s < 0) {
+                    s = S::XS - 1;
+                    ph ^= 1u;
+                }
+                if (!mbar_wait(xfull + 8 * s, ph, p.limit_ns))
+                    record_status(p.status, DEP_DEV_TIMEOUT_PRODUCER);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issue ----------------
+        if (lane == 0) {
+            // FP16 operands (format 0), FP32 accumulator, N >> 3 and M >> 4
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+            int xs = 0, as = 0, buf = 0;
+            uint32_t xph = 0, aph = 0, bph = 0;
+            bool ok = true;
+            for (int64_t seg = 0; seg < order.m && ok; ++seg) {
+                const int64_t t = order.tile(seg);
+                const int64_t end = order.seg_end(t);
+                for (int64_t u = order.seg_begin(t); u < end && ok;) {
+                    const int64_t stop = u + kExact < end ? u + kExact : end;
+                    if (!mbar_wait(acce + 8 * buf, bph ^ 1u, p.limit_ns)) {
+                        give_up(DEP_DEV_TIMEOUT_MMA);
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t d = tmem + (uint32_t)(S::TMEM_ACC + buf * NT);
+                    uint32_t accumulate = 0;
+                    for (; u < stop; ++u) {
+                        if (*abort_flag || !mbar_wait(xfull + 8 * xs, xph, p.limit_ns) ||
+                            !mbar_wait(afull + 8 * as, aph, p.limit_ns)) {
+                            give_up(DEP_DEV_TIMEOUT_MMA);
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const uint32_t a = tmem + (uint32_t)(as * kSlotCols);
+                        const uint64_t b = tc::desc_sw128(x0 + (uint32_t)(xs * S::X_BYTES));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (b0 + j < B) {
-                const int4 v = *reinterpret_cast<const int4 *>(x + (int64_t)(b0 + j) * K + k);
-                acc[j] = __dp4a(v.x, w.x, acc[j]);
-                acc[j] = __dp4a(v.y, w.y, acc[j]);
-                acc[j] = __dp4a(v.z, w.z, acc[j]);
-                acc[j] = __dp4a(v.w, w.w, acc[j]);
+                        for (int i = 0; i < kKU / 16; ++i) {
+                            mma_f16_ta(d, a + 8 * i, b + (uint64_t)(((i / 4) * NT * 128) >> 4) + 2 * (i % 4), idesc,
+                                       accumulate);
+                            accumulate = 1;
+                        }
+                        tc::commit(aempty + 8 * as);
+                        tc::commit(xempty + 8 * xs);
+                        if (++xs == S::XS) {
+                            xs = 0;
+                            xph ^= 1u;
+                        }
+                        if (++as == kSlots) {
+                            as = 0;
+                            aph ^= 1u;
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    tc::commit(accf + 8 * buf);
+                    if (++buf == S::BUFS) {
+                        buf = 0;
+                        bph ^= 1u;
+                    }
+                }
+            }
+            tc::commit(done);  // tensor memory is freed at the end: wait for every MMA
+            if (!mbar_wait(done, 0, p.limit_ns))
+                record_status(p.status, DEP_DEV_TIMEOUT_MMA);
+        }
+    } else if (warp >= 4 && warp < 4 + S::CONV) {
+        // ---------------- int8 -> FP16 into tensor memory ----------------
+        const int wg = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
+        constexpr int GROUPS = S::CONV / 4;
+        for (int64_t i = wg; i < n_units; i += GROUPS) {
+            const int s = (int)(i % S::WS), a = (int)(i % kSlots);
+            const uint32_t wph = (uint32_t)(i / S::WS) & 1u, aph = (uint32_t)(i / kSlots) & 1u;
+            bool ok = !*abort_flag && mbar_wait(wfull + 8 * s, wph, p.limit_ns) &&
+                      mbar_wait(aempty + 8 * a, aph ^ 1u, p.limit_ns);
+            ok = __all_sync(~0u, ok);
+            if (!ok) {
+                if (lane == 0)
+                    give_up(DEP_DEV_TIMEOUT_CONSUMER);
+                break;
+            }
+            tc::fence_after();
+            const uint32_t src = w0 + (uint32_t)(s * kWBytes + row * 128);
+            const uint32_t dst = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * kSlotCols);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t w[4];
+                    const uint32_t at = src + (uint32_t)(((4 * h + j) ^ (row & 7)) * 16);
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(at));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        widen4(w[e], v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+                }
+                tmem_st32(dst + 32 * h, v);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(wempty + 8 * s);
+            tmem_wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(afull + 8 * a);
+        }
+    } else if (warp >= 4 + S::CONV) {
+        // ---------------- drain and finish ----------------
+        const int e = warp - 4 - S::CONV, q = warp & 3, c0 = (e / 4) * S::COLS;
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(S::TMEM_ACC + c0);
+        const int cols = p.B - c0 < S::COLS ? p.B - c0 : S::COLS;  // of these, columns of the batch (may be <= 0)
+        int buf = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        griddep_wait();  // y and the workspace may be in use by the grids before
+        for (int64_t seg = 0; seg < order.m && ok; ++seg) {
+            const int64_t t = order.tile(seg), begin = order.seg_begin(t), end = order.seg_end(t);
+            int acc[S::COLS];
+#pragma unroll
+            for (int j = 0; j < S::COLS; ++j)
+                acc[j] = 0;
+            for (int64_t u = begin; u < end; u += kExact) {
+                ok = __all_sync(~0u, mbar_wait(accf + 8 * buf, bph, p.limit_ns));
+                if (!ok) {
+                    if (lane == 0)
+                        give_up(DEP_DEV_TIMEOUT_EPILOGUE);
+                    break;
+                }
+                tc::fence_after();
+#pragma unroll
+                for (int j = 0; j < S::COLS; j += 8) {
+                    if (j < cols) {
+                        uint32_t v[8];
+                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                                       "=r"(v[6]), "=r"(v[7])
+                                     : "r"(lane_addr + (uint32_t)(buf * NT + j)));
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(acce + 8 * buf);
+                if (++buf == S::BUFS) {
+                    buf = 0;
+                    bph ^= 1u;
+                }
+            }
+            if (!ok)
+                break;
+            const int64_t n = t * kBM + 32 * q + lane;
+            bool last = true;
+            int *sums = p.sums + (t * NT + c0) * kBM + 32 * q + lane;
+            const int64_t parts = p.split.owner((t + 1) * KU - 1) - p.split.owner(t * KU) + 1;
+            if (parts > 1) {
+#pragma unroll
+                for (int j = 0; j < S::COLS; ++j)
+                    if (j < cols)
+                        atomicAdd(sums + j * kBM, acc[j]);
+                __threadfence();
+                __syncwarp();
+                int old = 0;
+                if (lane == 0)
+                    old = atomicAdd(p.counters + t * 8 + e, 1);
+                last = __shfl_sync(~0u, old, 0) == parts - 1;
+                if (last) {
+                    __threadfence();
+#pragma unroll
+                    for (int j = 0; j < S::COLS; ++j)
+                        if (j < cols) {
+                            acc[j] = __ldcg(sums + j * kBM);
+                            __stcg(sums + j * kBM, 0);
+                        }
+                    if (lane == 0)
+                        p.counters[t * 8 + e] = 0;
+                }
+            }
+            if (last && n < p.N) {
+                const float ws = p.ws[n];
+#pragma unroll
+                for (int j = 0; j < S::COLS; ++j)
+                    if (j < cols)
+                        p.y[(int64_t)(c0 + j) * p.N + n] =
+                            __bfloat16_as_ushort(__float2bfloat16_rn((float)acc[j] * (p.xs[c0 + j] * ws)));
             }
         }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int s = __reduce_add_sync(~0u, acc[j]);
-        if (lane == 0 && b0 + j < B)
-            y[(int64_t)(b0 + j) * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn((float)s * (xs[b0 + j] * ws[n])));
+
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::dealloc(tmem, 512);
     }
+}
+
+// MMA width of a pass of B rows.
+int width(int32_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : 256; }
+
+Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
+{
+    Int8Split s;
+    s.tiles = (N + kBM - 1) / kBM;
+    s.units = (K + kKU - 1) / kKU;
+    const int64_t all = s.tiles * s.units, waves = (s.tiles + sms - 1) / sms;
+    // Equal ranges unless whole tiles keep nearly every block busy, or sums of 256
+    // columns (128 KB for each part of a tile) would cost more than the idle blocks.
+    s.whole = nt == 256 || s.tiles * 100 >= waves * sms * 95;
+    s.blocks = (int)(s.whole ? (s.tiles < sms ? s.tiles : sms) : (all < sms ? all : sms));
+    return s;
+}
+
+template <int NT>
+cudaError_t int8_launch(const dep_int8_plan_s &pl, const void *W, const Int8Params &p, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> devices{0};
+    cudaError_t e = set_smem_attr(int8_kernel<NT>, devices);
+    if (e != cudaSuccess)
+        return e;
+    CUtensorMap tmW, tmX;
+    const int64_t Kp = p.split.units * kKU;
+    if (encode_u8_2d(&tmW, W, (uint64_t)pl.K, (uint64_t)pl.N, kKU, kBM) != CUDA_SUCCESS ||
+        encode_bf16_3d_blocks(&tmX, pl.xh, (uint64_t)Kp, NT, NT, kKU / 64) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return launch(int8_kernel<NT>, dim3(p.split.blocks), dim3(kWarps * 32), (size_t)Int8Shape<NT>::SMEM, stream, true,
+                  tmW, tmX, p);
+}
+
+cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *xs, const void *W, const float *ws,
+                      uint16_t *y, int32_t B, cudaStream_t stream)
+{
+    const int nt = width(B);
+    const Int8Split split = split_for(pl.N, pl.K, nt, pl.sm_count);
+    const int Kp = (int)split.units * kKU;
+    const dim3 grid((unsigned)((Kp / 16 + 255) / 256), (unsigned)nt);
+    int8_widen_kernel<<<grid, 256, 0, stream>>>(x, pl.xh, B, (int)pl.K, Kp);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    const Int8Params p{xs, ws, y, B, pl.N, split, pl.counters, pl.sums, pl.status, pl.wait_limit_ns};
+    switch (nt) {
+    case 16: return int8_launch<16>(pl, W, p, stream);
+    case 32: return int8_launch<32>(pl, W, p, stream);
+    case 64: return int8_launch<64>(pl, W, p, stream);
+    case 128: return int8_launch<128>(pl, W, p, stream);
+    default: return int8_launch<256>(pl, W, p, stream);
+    }
+}
+
+// Raise every kernel's shared-memory limit now, so that no first launch does it inside a capture.
+cudaError_t int8_prepare_device()
+{
+    static std::atomic<uint64_t> d16{0}, d32{0}, d64{0}, d128{0}, d256{0};
+    for (cudaError_t e : {set_smem_attr(int8_kernel<16>, d16), set_smem_attr(int8_kernel<32>, d32),
+                          set_smem_attr(int8_kernel<64>, d64), set_smem_attr(int8_kernel<128>, d128),
+                          set_smem_attr(int8_kernel<256>, d256)})
+        if (e != cudaSuccess)
+            return e;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -91,19 +579,37 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
         delete p;
         return DEP_ERR_UNSUPPORTED;
     }
-    p->bytes = 256;
+    if (dep::int8_prepare_device() != cudaSuccess) {
+        cudaGetLastError();
+        delete p;
+        return DEP_ERR_CUDA;
+    }
+    // One block of device memory: status word, counters, sums of shared tiles, x in FP16.
+    const int64_t tiles = (N + dep::kBM - 1) / dep::kBM, Kp = (K + dep::kKU - 1) / dep::kKU * dep::kKU;
+    const int nt = dep::width(max_rows);
+    size_t sums = 0;
+    for (int w = 16; w <= nt; w *= 2)
+        if (!dep::split_for(N, K, w, p->sm_count).whole)
+            sums = (size_t)tiles * w * dep::kBM * sizeof(int);
+    const size_t counters = ((size_t)tiles * 8 * sizeof(int) + 255) / 256 * 256;
+    p->clear_bytes = 256 + counters + sums;
+    p->bytes = p->clear_bytes + (size_t)nt * Kp * 2;
     if (cudaMalloc(&p->block, p->bytes) != cudaSuccess) {
         cudaGetLastError();
         delete p;
         return DEP_ERR_OOM;
     }
-    if (cudaMemset(p->block, 0, p->bytes) != cudaSuccess) {
+    if (cudaMemset(p->block, 0, p->bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
         cudaFree(p->block);
         delete p;
         return DEP_ERR_CUDA;
     }
-    p->status = static_cast<int *>(p->block);
+    uint8_t *at = static_cast<uint8_t *>(p->block);
+    p->status = reinterpret_cast<int *>(at);
+    p->counters = reinterpret_cast<int *>(at + 256);
+    p->sums = reinterpret_cast<int *>(at + 256 + counters);
+    p->xh = reinterpret_cast<uint16_t *>(at + p->clear_bytes);
     *out = p;
     return DEP_OK;
 }
@@ -129,12 +635,16 @@ dep_status_t dep_int8_run(dep_int8_plan_t p, const void *x, const float *x_scale
         cudaGetLastError();
         return DEP_ERR_INVALID_ARG;
     }
-    const dim3 grid((unsigned)((p->N + 7) / 8), (unsigned)((B + 7) / 8));
-    dep::int8_rows_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const int8_t *>(x), x_scale, static_cast<const int8_t *>(W), w_scale, static_cast<uint16_t *>(y),
-        B, p->N, (int)p->K);
-    if (cudaGetLastError() != cudaSuccess)
-        return DEP_ERR_CUDA;
+    const int32_t step = dep::width(p->max_rows);  // rows of a pass
+    for (int32_t r0 = 0; r0 < B; r0 += step) {
+        const int32_t rows = B - r0 < step ? B - r0 : step;
+        if (dep::int8_pass(*p, static_cast<const uint8_t *>(x) + (int64_t)r0 * p->K, x_scale + r0, W, w_scale,
+                           static_cast<uint16_t *>(y) + (int64_t)r0 * p->N, rows,
+                           static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+            cudaGetLastError();
+            return DEP_ERR_CUDA;
+        }
+    }
     return DEP_OK;
 }
 
@@ -157,8 +667,8 @@ dep_status_t dep_int8_device_status(dep_int8_plan_t p, void *stream, int32_t *co
         cudaGetLastError();
         return DEP_ERR_CUDA;
     }
-    // After a give-up the exchange may be left mid-protocol: clear everything.
-    if (h && (cudaDeviceSynchronize() != cudaSuccess || cudaMemset(p->block, 0, p->bytes) != cudaSuccess)) {
+    // After a give-up counters and sums may be left mid-protocol: clear them.
+    if (h && (cudaDeviceSynchronize() != cudaSuccess || cudaMemset(p->block, 0, p->clear_bytes) != cudaSuccess)) {
         cudaGetLastError();
         return DEP_ERR_CUDA;
     }

@@ -246,4 +246,8 @@ CUresult encode_bf16_2d(CUtensorMap *map, const void *base, uint64_t inner, uint
 CUresult encode_bf16_3d_blocks(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer,
                                uint32_t box_rows, uint32_t blocks);
 
+// Tensor map over a row-major [outer, inner] matrix of bytes, 128-byte swizzle.
+CUresult encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                      uint32_t box_outer);
+
 }  // namespace dep

@@ -69,4 +69,21 @@ CUresult encode_bf16_3d_blocks(CUtensorMap *map, const void *base, uint64_t inne
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// A [outer, inner] matrix of bytes (inner a multiple of 16) in boxes of 128
+// columns, in the 128-byte swizzle; parts of a box past the matrix are zeros.
+CUresult encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                      uint32_t box_outer)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return CUDA_ERROR_NOT_FOUND;
+    const cuuint64_t dims[2] = {inner, outer};
+    const cuuint64_t strides[1] = {inner};
+    const cuuint32_t box[2] = {box_inner, box_outer};
+    const cuuint32_t elem_strides[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, elem_strides,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 }  // namespace dep
