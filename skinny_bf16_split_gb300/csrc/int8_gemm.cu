@@ -12,25 +12,33 @@
 //  * int8_widen_kernel writes x as FP16 into the plan's workspace, padded with zero
 //    rows to the MMA's width and with zero columns to whole stages.
 //  * int8_kernel<NT>: persistent blocks over units of 128 weight rows x 128 columns.
-//      warp 0      TMA: weight stages (16 KB of int8) and x stages (NT x 128 FP16)
-//      warp 1      issues tcgen05.mma, eight a unit: A = the weight, from tensor
-//                  memory, B = x, from shared memory, M = 128, N = NT
-//      CONV warps  turn a weight stage into FP16 and store it into a ring of four
-//                  slots of tensor memory: lane = weight row, so that the operand
-//                  crosses shared memory once, as bytes.  A byte b becomes FP16
+//      warp 0      TMA: weight stages, 16 KB of int8 each
+//      warp 2      TMA: x slots (NT x SK FP16).  From 64 rows on a cluster of two
+//                  blocks works on neighbouring tiles: each loads half of every x
+//                  slot and multicasts it to both, which halves what x takes out
+//                  of L2 (x of 128 rows is twice the weight's bytes).
+//      warp 1      issues tcgen05.mma: A = the weight, from tensor memory, B = x, from
+//                  shared memory, M = 128, N = NT
+//      CONV warps  turn a weight stage into FP16 and store it into a ring of slots
+//                  of tensor memory: lane = weight row, so that the operand crosses
+//                  shared memory once, as bytes.  A byte b becomes FP16
 //                  1024 + (b ^ 0x80) by one byte permutation, and minus 1152 exactly b.
 //      EPI warps   drain the accumulators into integers, and finish tiles
+//    A weight slot and its x slot share one pair of barriers: the issuing thread
+//    spends about 64 cycles on an MMA, 55 on a commit and 100 on a wait, so one wait
+//    (tested ahead, while the MMAs before it are issued) and one commit a slot.
 //    Where whole tiles would leave blocks idle, the blocks take equal ranges of
 //    units, and the parts of a tile that several blocks share are added into the
 //    plan's workspace by integer atomics (exact, so any order gives the same bits);
 //    the block whose part arrives last rounds and stores, and clears the workspace.
-//    No block waits for another one.
+//    Blocks wait for one another only inside a cluster.
 // Bound: the weight's bytes up to about 128 rows, the tensor cores above.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <new>
 
+#include "cluster.cuh"
 #include "internal.h"
 #include "layer.h"
 #include "ptx.cuh"
@@ -58,38 +66,40 @@ constexpr int kBM = 128;           // weight rows of a tile (MMA M)
 constexpr int kKU = 128;           // columns of a unit
 constexpr int kExact = 1024 / kKU; // units whose sums FP32 holds exactly
 constexpr int kWBytes = kBM * kKU; // a weight stage
-constexpr int kSlots = 4;          // ring of FP16 weight units in tensor memory
-constexpr int kSlotCols = kKU / 2; // its 32-bit columns a unit
-constexpr int kWarps = 16;
 
 template <int NT>
 struct Int8Shape {
+    static constexpr int CL = NT >= 64 ? 2 : 1;          // blocks of a cluster
     static constexpr int CONV = NT <= 64 ? 8 : 4;        // converting warps (from warp 4 on)
-    static constexpr int EPI = 12 - CONV;                // draining warps (the last)
+    static constexpr int EPI = NT == 256 ? 16 : 12 - CONV;  // draining warps (the last)
+    static constexpr int THREADS = (4 + CONV + EPI) * 32;
     static constexpr int COLS = NT / (EPI / 4);          // batch columns of a draining thread
     static constexpr int BUFS = NT <= 128 ? 2 : 1;       // accumulators
-    static constexpr int X_BYTES = NT * kKU * 2;         // an x stage
-    static constexpr int XS = NT <= 64 ? 4 : NT == 128 ? 3 : 2;
-    static constexpr int WS = (kMaxDynamicSmem - 1024 - 512 - XS * X_BYTES) / kWBytes;
-    static constexpr int TMEM_ACC = kSlots * kSlotCols;  // accumulators start behind the ring
-    static constexpr int TMEM = TMEM_ACC + BUFS * NT <= 512 ? 512 : 0;
-    static constexpr int BARS = 2 * WS + 2 * XS + 2 * kSlots + 2 * BUFS + 1;
-    static constexpr int SMEM = 1024 + WS * kWBytes + XS * X_BYTES + BARS * 8 + 16;
-    static_assert(TMEM == 512 && SMEM <= kMaxDynamicSmem, "");
+    static constexpr int SK = NT == 256 ? 64 : 128;      // columns of a slot
+    static constexpr int SLOTS = NT == 256 ? 5 : 4;      // slots of tensor memory, and of x
+    static constexpr int SLOT_COLS = SK / 2;             // a slot's 32-bit columns of tensor memory
+    static constexpr int PER = kKU / SK;                 // slots of a unit
+    static constexpr int X_BYTES = NT * SK * 2;          // an x slot
+    static constexpr int WS = (kMaxDynamicSmem - 1024 - 512 - SLOTS * X_BYTES) / kWBytes;
+    static constexpr int ACC0 = 256;                     // the accumulators' first column
+    static constexpr int BARS = 2 * WS + 2 * SLOTS + 2 * BUFS + 1;
+    static constexpr int SMEM = 1024 + WS * kWBytes + SLOTS * X_BYTES + BARS * 8 + 16;
+    static_assert(SLOTS * SLOT_COLS <= ACC0 && ACC0 + BUFS * NT <= 512 && SMEM <= kMaxDynamicSmem, "");
 };
 
-// How a launch deals its units out: `whole` tiles to a block, or equal ranges of units.
+// How a launch deals its units out to its clusters: `whole` groups of tiles (one tile
+// for each block of a cluster), or equal ranges of units.
 struct Int8Split {
-    int64_t tiles, units;  // units of a tile
-    int blocks;
+    int64_t groups, units;  // units of a tile
+    int clusters;
     int whole;
     __host__ __device__ int64_t begin(int64_t c) const
     {
-        return whole ? sk_begin(c, tiles, blocks) * units : sk_begin(c, tiles * units, blocks);
+        return whole ? sk_begin(c, groups, clusters) * units : sk_begin(c, groups * units, clusters);
     }
     __host__ __device__ int64_t owner(int64_t u) const
     {
-        return whole ? sk_owner(u / units, tiles, blocks) : sk_owner(u, tiles * units, blocks);
+        return whole ? sk_owner(u / units, groups, clusters) : sk_owner(u, groups * units, clusters);
     }
 };
 
@@ -103,6 +113,41 @@ struct Int8Params {
     int *status;
     uint64_t limit_ns;
 };
+
+// True if the barrier's phase of this parity has completed; never waits.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The three-dimensional load, into the same place of every block of `mask`; the bytes
+// count towards each block's own barrier.
+__device__ __forceinline__ void tma_load_3d_multicast(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1,
+                                                      int32_t c2, uint32_t bar, uint16_t mask, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "h"(mask), "l"(policy)
+        : "memory");
+}
+
+// Arrive on the barrier at this place in every block of `mask` when the MMAs so far complete.
+__device__ __forceinline__ void commit_multicast(uint32_t bar, uint16_t mask)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
+}
 
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, FP16 inputs, FP32 accumulation.
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
@@ -163,7 +208,7 @@ __global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restri
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Int8Params p)
 {
     using S = Int8Shape<NT>;
@@ -171,29 +216,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
     const uint32_t w0 = base, x0 = base + S::WS * kWBytes;
-    const uint32_t bars = x0 + S::XS * S::X_BYTES;
-    const uint32_t wfull = bars, wempty = wfull + 8 * S::WS, xfull = wempty + 8 * S::WS, xempty = xfull + 8 * S::XS,
-                   afull = xempty + 8 * S::XS, aempty = afull + 8 * kSlots, accf = aempty + 8 * kSlots,
-                   acce = accf + 8 * S::BUFS, done = acce + 8 * S::BUFS;
+    const uint32_t wfull = x0 + S::SLOTS * S::X_BYTES, wempty = wfull + 8 * S::WS;
+    const uint32_t sfull = wempty + 8 * S::WS, sempty = sfull + 8 * S::SLOTS;  // a weight slot and its x slot
+    const uint32_t accf = sempty + 8 * S::SLOTS, acce = accf + 8 * S::BUFS, done = acce + 8 * S::BUFS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (done + 8 - base));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = S::CL == 1 ? 0 : (int)cluster_rank();
+    const int64_t c = S::CL == 1 ? blockIdx.x : blockIdx.x / S::CL;
     const int64_t KU = p.split.units;
-    const SegOrder order(p.split.begin(blockIdx.x), p.split.begin(blockIdx.x + 1), KU);
-    const int64_t n_units = order.u_end - order.u_begin;
+    const SegOrder order(p.split.begin(c), p.split.begin(c + 1), KU);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::WS; ++i) {
             mbar_init(wfull + 8 * i, 1);
             mbar_init(wempty + 8 * i, 4);
         }
-        for (int i = 0; i < S::XS; ++i) {
-            mbar_init(xfull + 8 * i, 1);
-            mbar_init(xempty + 8 * i, 1);
-        }
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(afull + 8 * i, 4);
-            mbar_init(aempty + 8 * i, 1);
+        for (int i = 0; i < S::SLOTS; ++i) {
+            mbar_init(sfull + 8 * i, 4 + 1);    // four converting warps, and x
+            mbar_init(sempty + 8 * i, S::CL);  // the MMAs of every block that x went to
         }
         for (int i = 0; i < S::BUFS; ++i) {
             mbar_init(accf + 8 * i, 1);
@@ -209,15 +250,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     tc::fence_before();
     __syncthreads();
+    if (S::CL > 1)
+        cluster_sync();  // the peer's barriers exist before anything arrives on them
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     auto give_up = [&](int code) {
         record_status(p.status, code);
         *abort_flag = 1;
     };
-
     if (warp == 0) {
-        // ---------------- copies: lane 0 the weight, lane 1 (one warp on: warp 2) x ----------------
+        // ---------------- weight copies ----------------
         if (lane == 0) {
             prefetch_tmap(&tmW);
             const uint64_t pol = policy_evict_first();
@@ -233,7 +275,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     break;
                 }
                 mbar_arrive_expect_tx(wfull + 8 * s, kWBytes);
-                tma_load_2d(w0 + s * kWBytes, &tmW, (int)(cur.u % KU) * kKU, (int)(cur.u / KU) * kBM, wfull + 8 * s, pol);
+                tma_load_2d(w0 + s * kWBytes, &tmW, (int)(cur.u % KU) * kKU, ((int)(cur.u / KU) * S::CL + rank) * kBM,
+                            wfull + 8 * s, pol);
                 ++issued;
                 if (++s == S::WS) {
                     s = 0;
@@ -250,35 +293,49 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
         }
     } else if (warp == 2) {
+        // ---------------- x copies ----------------
         if (lane == 0) {
             prefetch_tmap(&tmX);
             const uint64_t pol = policy_evict_last();
             griddep_wait();  // x in FP16 is written by the preceding grid
+            constexpr int ROWS = NT / S::CL;  // x rows that this block loads
             UnitCursor cur(order);
             int s = 0;
             uint32_t ph = 0;
             int64_t issued = 0;
-            for (; !cur.done(); cur.next()) {
-                if (*abort_flag)
-                    break;
-                if (!mbar_wait(xempty + 8 * s, ph ^ 1u, p.limit_ns)) {
-                    give_up(DEP_DEV_TIMEOUT_PRODUCER);
-                    break;
-                }
-                mbar_arrive_expect_tx(xfull + 8 * s, S::X_BYTES);
-                tma_load_3d(x0 + s * S::X_BYTES, &tmX, 0, 0, (int)(cur.u % KU) * (kKU / 64), xfull + 8 * s, pol);
-                ++issued;
-                if (++s == S::XS) {
-                    s = 0;
-                    ph ^= 1u;
+            bool ok = true;
+            for (; ok && !cur.done(); cur.next()) {
+                for (int h = 0; h < S::PER; ++h) {
+                    if (*abort_flag || !mbar_wait_cluster(sempty + 8 * s, ph ^ 1u, p.limit_ns)) {
+                        give_up(DEP_DEV_TIMEOUT_PRODUCER);
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(sfull + 8 * s, S::X_BYTES);
+                    const int block64 = (int)(cur.u % KU) * (kKU / 64) + h * (S::SK / 64);
+                    if (S::CL == 1) {
+                        tma_load_3d(x0 + s * S::X_BYTES, &tmX, 0, 0, block64, sfull + 8 * s, pol);
+                    } else {  // one copy for each 64 columns: its rows are a part of the slice
+#pragma unroll
+                        for (int j = 0; j < S::SK / 64; ++j)
+                            tma_load_3d_multicast(x0 + s * S::X_BYTES + (j * NT + rank * ROWS) * 128, &tmX, 0,
+                                                  rank * ROWS, block64 + j, sfull + 8 * s, (1 << S::CL) - 1, pol);
+                    }
+                    ++issued;
+                    if (++s == S::SLOTS) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
-            for (int64_t i = issued < S::XS ? issued : S::XS; i > 0; --i) {
+            // Every slot used was consumed (by both blocks): no copy of this block's is in flight
+            // anywhere, and no arrival at its barriers is left.
+            for (int64_t i = issued < S::SLOTS ? issued : S::SLOTS; i > 0; --i) {
                 if (--s < 0) {
-                    s = S::XS - 1;
+                    s = S::SLOTS - 1;
                     ph ^= 1u;
                 }
-                if (!mbar_wait(xfull + 8 * s, ph, p.limit_ns))
+                if (!mbar_wait_cluster(sempty + 8 * s, ph, p.limit_ns))
                     record_status(p.status, DEP_DEV_TIMEOUT_PRODUCER);
             }
         }
@@ -287,9 +344,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (lane == 0) {
             // FP16 operands (format 0), FP32 accumulator, N >> 3 and M >> 4
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            int xs = 0, as = 0, buf = 0;
-            uint32_t xph = 0, aph = 0, bph = 0;
-            bool ok = true;
+            int s = 0, buf = 0;
+            uint32_t sph = 0, bph = 0;
+            bool ok = true, ready = false;
             for (int64_t seg = 0; seg < order.m && ok; ++seg) {
                 const int64_t t = order.tile(seg);
                 const int64_t end = order.seg_end(t);
@@ -301,37 +358,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         break;
                     }
                     tc::fence_after();
-                    const uint32_t d = tmem + (uint32_t)(S::TMEM_ACC + buf * NT);
+                    const uint32_t d = tmem + (uint32_t)(S::ACC0 + buf * NT);
                     uint32_t accumulate = 0;
-                    for (; u < stop; ++u) {
-                        if (*abort_flag || !mbar_wait(xfull + 8 * xs, xph, p.limit_ns) ||
-                            !mbar_wait(afull + 8 * as, aph, p.limit_ns)) {
+                    for (int n = (int)(stop - u) * S::PER; n > 0; --n) {
+                        if (!ready && (*abort_flag || !mbar_wait_cluster(sfull + 8 * s, sph, p.limit_ns))) {
                             give_up(DEP_DEV_TIMEOUT_MMA);
                             ok = false;
                             break;
                         }
                         tc::fence_after();
-                        const uint32_t a = tmem + (uint32_t)(as * kSlotCols);
-                        const uint64_t b = tc::desc_sw128(x0 + (uint32_t)(xs * S::X_BYTES));
+                        const uint32_t a = tmem + (uint32_t)(s * S::SLOT_COLS), freed = sempty + 8 * s;
+                        const uint64_t b = tc::desc_sw128(x0 + (uint32_t)(s * S::X_BYTES));
+                        if (++s == S::SLOTS) {
+                            s = 0;
+                            sph ^= 1u;
+                        }
+                        ready = mbar_test(sfull + 8 * s, sph);  // the next slot's
 #pragma unroll
-                        for (int i = 0; i < kKU / 16; ++i) {
+                        for (int i = 0; i < S::SK / 16; ++i) {
                             mma_f16_ta(d, a + 8 * i, b + (uint64_t)(((i / 4) * NT * 128) >> 4) + 2 * (i % 4), idesc,
                                        accumulate);
                             accumulate = 1;
                         }
-                        tc::commit(aempty + 8 * as);
-                        tc::commit(xempty + 8 * xs);
-                        if (++xs == S::XS) {
-                            xs = 0;
-                            xph ^= 1u;
-                        }
-                        if (++as == kSlots) {
-                            as = 0;
-                            aph ^= 1u;
-                        }
+                        if (S::CL == 1)
+                            tc::commit(freed);
+                        else
+                            commit_multicast(freed, (1 << S::CL) - 1);
                     }
                     if (!ok)
                         break;
+                    u = stop;
                     tc::commit(accf + 8 * buf);
                     if (++buf == S::BUFS) {
                         buf = 0;
@@ -345,24 +401,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
     } else if (warp >= 4 && warp < 4 + S::CONV) {
         // ---------------- int8 -> FP16 into tensor memory ----------------
+        constexpr int GROUPS = S::CONV / 4;  // four warps take a stage; two such groups take turns
         const int wg = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
-        constexpr int GROUPS = S::CONV / 4;
-        for (int64_t i = wg; i < n_units; i += GROUPS) {
-            const int s = (int)(i % S::WS), a = (int)(i % kSlots);
-            const uint32_t wph = (uint32_t)(i / S::WS) & 1u, aph = (uint32_t)(i / kSlots) & 1u;
-            bool ok = !*abort_flag && mbar_wait(wfull + 8 * s, wph, p.limit_ns) &&
-                      mbar_wait(aempty + 8 * a, aph ^ 1u, p.limit_ns);
-            ok = __all_sync(~0u, ok);
-            if (!ok) {
-                if (lane == 0)
-                    give_up(DEP_DEV_TIMEOUT_CONSUMER);
-                break;
-            }
-            tc::fence_after();
-            const uint32_t src = w0 + (uint32_t)(s * kWBytes + row * 128);
-            const uint32_t dst = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * kSlotCols);
+        const int n_units = (int)(order.u_end - order.u_begin);
+        int ws = wg % S::WS, s = (wg * S::PER) % S::SLOTS;
+        uint32_t wph = 0, sph = 0;
+        for (int i = wg; i < n_units; i += GROUPS) {
+            bool ok = !*abort_flag && mbar_wait(wfull + 8 * ws, wph, p.limit_ns);
+            const uint32_t src = w0 + (uint32_t)(ws * kWBytes + row * 128);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2; ++h) {  // 64 columns
+                if (S::PER == 2 || h == 0) {
+                    ok = ok && mbar_wait(sempty + 8 * s, sph ^ 1u, p.limit_ns);
+                    if (!__all_sync(~0u, ok))
+                        break;
+                    tc::fence_after();
+                }
                 uint32_t v[32];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -375,33 +429,52 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     for (int e = 0; e < 4; ++e)
                         widen4(w[e], v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
                 }
-                tmem_st32(dst + 32 * h, v);
+                tmem_st32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(s * S::SLOT_COLS + (S::PER == 2 ? 0 : 32 * h)), v);
+                if (h == 1) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(wempty + 8 * ws);
+                }
+                if (S::PER == 2 || h == 1) {
+                    tmem_wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(sfull + 8 * s);
+                    s += S::PER == 2 ? 1 : GROUPS;
+                    if (s >= S::SLOTS) {
+                        s -= S::SLOTS;
+                        sph ^= 1u;
+                    }
+                }
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(wempty + 8 * s);
-            tmem_wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(afull + 8 * a);
+            if (!__all_sync(~0u, ok)) {
+                if (lane == 0)
+                    give_up(DEP_DEV_TIMEOUT_CONSUMER);
+                break;
+            }
+            ws += GROUPS;
+            if (ws >= S::WS) {
+                ws -= S::WS;
+                wph ^= 1u;
+            }
         }
     } else if (warp >= 4 + S::CONV) {
         // ---------------- drain and finish ----------------
         const int e = warp - 4 - S::CONV, q = warp & 3, c0 = (e / 4) * S::COLS;
-        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(S::TMEM_ACC + c0);
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(S::ACC0 + c0);
         const int cols = p.B - c0 < S::COLS ? p.B - c0 : S::COLS;  // of these, columns of the batch (may be <= 0)
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
         griddep_wait();  // y and the workspace may be in use by the grids before
         for (int64_t seg = 0; seg < order.m && ok; ++seg) {
-            const int64_t t = order.tile(seg), begin = order.seg_begin(t), end = order.seg_end(t);
+            const int64_t g = order.tile(seg), t = g * S::CL + rank, end = order.seg_end(g);
             int acc[S::COLS];
 #pragma unroll
             for (int j = 0; j < S::COLS; ++j)
                 acc[j] = 0;
-            for (int64_t u = begin; u < end; u += kExact) {
+            for (int64_t u = order.seg_begin(g); u < end; u += kExact) {
                 ok = __all_sync(~0u, mbar_wait(accf + 8 * buf, bph, p.limit_ns));
                 if (!ok) {
                     if (lane == 0)
@@ -410,16 +483,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
                 tc::fence_after();
 #pragma unroll
-                for (int j = 0; j < S::COLS; j += 8) {
+                for (int j = 0; j < S::COLS; j += 16) {
                     if (j < cols) {
-                        uint32_t v[8];
-                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-                                       "=r"(v[6]), "=r"(v[7])
-                                     : "r"(lane_addr + (uint32_t)(buf * NT + j)));
+                        uint32_t v[16];
+                        tc::ld16(lane_addr + (uint32_t)(buf * NT + j), v);
                         tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                        for (int i = 0; i < 16; ++i)
                             acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
                     }
                 }
@@ -436,9 +506,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 break;
             const int64_t n = t * kBM + 32 * q + lane;
             bool last = true;
-            int *sums = p.sums + (t * NT + c0) * kBM + 32 * q + lane;
-            const int64_t parts = p.split.owner((t + 1) * KU - 1) - p.split.owner(t * KU) + 1;
+            const int64_t parts = p.split.owner((g + 1) * KU - 1) - p.split.owner(g * KU) + 1;
             if (parts > 1) {
+                int *sums = p.sums + (t * NT + c0) * kBM + 32 * q + lane;
 #pragma unroll
                 for (int j = 0; j < S::COLS; ++j)
                     if (j < cols)
@@ -447,7 +517,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 __syncwarp();
                 int old = 0;
                 if (lane == 0)
-                    old = atomicAdd(p.counters + t * 8 + e, 1);
+                    old = atomicAdd(p.counters + t * 16 + e, 1);
                 last = __shfl_sync(~0u, old, 0) == parts - 1;
                 if (last) {
                     __threadfence();
@@ -458,7 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                             __stcg(sums + j * kBM, 0);
                         }
                     if (lane == 0)
-                        p.counters[t * 8 + e] = 0;
+                        p.counters[t * 16 + e] = 0;
                 }
             }
             if (last && n < p.N) {
@@ -475,6 +545,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __syncwarp();
     tc::fence_before();
     __syncthreads();
+    if (S::CL > 1)
+        cluster_sync();  // neither block leaves while the other may still send to it
     if (warp == 1) {
         tc::fence_after();
         tc::dealloc(tmem, 512);
@@ -484,33 +556,57 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // MMA width of a pass of B rows.
 int width(int32_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : 256; }
 
+int cluster_of(int nt) { return nt >= 64 ? 2 : 1; }
+
 Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
 {
+    const int cl = cluster_of(nt);
     Int8Split s;
-    s.tiles = (N + kBM - 1) / kBM;
+    s.groups = ((N + kBM - 1) / kBM + cl - 1) / cl;
     s.units = (K + kKU - 1) / kKU;
-    const int64_t all = s.tiles * s.units, waves = (s.tiles + sms - 1) / sms;
+    const int64_t all = s.groups * s.units, most = sms / cl, waves = (s.groups + most - 1) / most;
     // Equal ranges unless whole tiles keep nearly every block busy, or sums of 256
     // columns (128 KB for each part of a tile) would cost more than the idle blocks.
-    s.whole = nt == 256 || s.tiles * 100 >= waves * sms * 95;
-    s.blocks = (int)(s.whole ? (s.tiles < sms ? s.tiles : sms) : (all < sms ? all : sms));
+    s.whole = nt == 256 || s.groups * 100 >= waves * most * 95;
+    s.clusters = (int)(s.whole ? (s.groups < most ? s.groups : most) : (all < most ? all : most));
     return s;
+}
+
+template <int NT>
+cudaError_t int8_prepare()
+{
+    static std::atomic<uint64_t> devices{0};
+    return set_smem_attr(int8_kernel<NT>, devices);
 }
 
 template <int NT>
 cudaError_t int8_launch(const dep_int8_plan_s &pl, const void *W, const Int8Params &p, cudaStream_t stream)
 {
-    static std::atomic<uint64_t> devices{0};
-    cudaError_t e = set_smem_attr(int8_kernel<NT>, devices);
+    using S = Int8Shape<NT>;
+    static_assert(S::CL == (NT >= 64 ? 2 : 1), "cluster_of");
+    cudaError_t e = int8_prepare<NT>();
     if (e != cudaSuccess)
         return e;
     CUtensorMap tmW, tmX;
     const int64_t Kp = p.split.units * kKU;
     if (encode_u8_2d(&tmW, W, (uint64_t)pl.K, (uint64_t)pl.N, kKU, kBM) != CUDA_SUCCESS ||
-        encode_bf16_3d_blocks(&tmX, pl.xh, (uint64_t)Kp, NT, NT, kKU / 64) != CUDA_SUCCESS)
+        encode_bf16_3d_blocks(&tmX, pl.xh, (uint64_t)Kp, NT, NT / S::CL, S::CL == 1 ? S::SK / 64 : 1) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    return launch(int8_kernel<NT>, dim3(p.split.blocks), dim3(kWarps * 32), (size_t)Int8Shape<NT>::SMEM, stream, true,
-                  tmW, tmX, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.split.clusters * S::CL);
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S::CL;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, int8_kernel<NT>, tmW, tmX, p);
 }
 
 cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *xs, const void *W, const float *ws,
@@ -537,10 +633,8 @@ cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *
 // Raise every kernel's shared-memory limit now, so that no first launch does it inside a capture.
 cudaError_t int8_prepare_device()
 {
-    static std::atomic<uint64_t> d16{0}, d32{0}, d64{0}, d128{0}, d256{0};
-    for (cudaError_t e : {set_smem_attr(int8_kernel<16>, d16), set_smem_attr(int8_kernel<32>, d32),
-                          set_smem_attr(int8_kernel<64>, d64), set_smem_attr(int8_kernel<128>, d128),
-                          set_smem_attr(int8_kernel<256>, d256)})
+    for (cudaError_t e : {int8_prepare<16>(), int8_prepare<32>(), int8_prepare<64>(), int8_prepare<128>(),
+                          int8_prepare<256>()})
         if (e != cudaSuccess)
             return e;
     return cudaSuccess;
@@ -588,10 +682,10 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
     const int64_t tiles = (N + dep::kBM - 1) / dep::kBM, Kp = (K + dep::kKU - 1) / dep::kKU * dep::kKU;
     const int nt = dep::width(max_rows);
     size_t sums = 0;
-    for (int w = 16; w <= nt; w *= 2)
+    for (int w = 16; w <= nt; w *= 2)  // (a cluster's last tile may lie past N)
         if (!dep::split_for(N, K, w, p->sm_count).whole)
-            sums = (size_t)tiles * w * dep::kBM * sizeof(int);
-    const size_t counters = ((size_t)tiles * 8 * sizeof(int) + 255) / 256 * 256;
+            sums = (size_t)(tiles + 1) * w * dep::kBM * sizeof(int);
+    const size_t counters = ((size_t)(tiles + 1) * 16 * sizeof(int) + 255) / 256 * 256;
     p->clear_bytes = 256 + counters + sums;
     p->bytes = p->clear_bytes + (size_t)nt * Kp * 2;
     if (cudaMalloc(&p->block, p->bytes) != cudaSuccess) {
