@@ -8,30 +8,31 @@
 // the products run as FP16 MMAs, and after at most 1024 columns the accumulators
 // are drained into 32-bit integers.
 //
-// Two kernels, chained by programmatic dependent launch:
-//  * int8_widen_kernel writes x as FP16 into the plan's workspace, padded with zero
-//    rows to the MMA's width and with zero columns to whole stages.
-//  * int8_kernel<NT>: persistent blocks over units of 128 weight rows x 128 columns.
-//      warp 0      TMA: weight stages, 16 KB of int8 each
-//      warp 2      TMA: x slots (NT x SK FP16).  From 64 rows on a cluster of two
-//                  blocks works on neighbouring tiles: each loads half of every x
-//                  slot and multicasts it to both, which halves what x takes out
-//                  of L2 (x of 128 rows is twice the weight's bytes).
-//      warp 1      issues tcgen05.mma: A = the weight, from tensor memory, B = x, from
-//                  shared memory, M = 128, N = NT
-//      CONV warps  turn a weight stage into FP16 and store it into a ring of slots
-//                  of tensor memory: lane = weight row, so that the operand crosses
-//                  shared memory once, as bytes.  A byte b becomes FP16
-//                  1024 + (b ^ 0x80) by one byte permutation, and minus 1152 exactly b.
-//      EPI warps   drain the accumulators into integers, and finish tiles
-//    A weight slot and its x slot share one pair of barriers: the issuing thread
-//    spends about 64 cycles on an MMA, 55 on a commit and 100 on a wait, so one wait
-//    (tested ahead, while the MMAs before it are issued) and one commit a slot.
-//    Where whole tiles would leave blocks idle, the blocks take equal ranges of
-//    units, and the parts of a tile that several blocks share are added into the
-//    plan's workspace by integer atomics (exact, so any order gives the same bits);
-//    the block whose part arrives last rounds and stores, and clears the workspace.
-//    Blocks wait for one another only inside a cluster.
+// int8_kernel<NT>: persistent blocks over units of 128 weight rows x 256 columns.
+//   warp 0      TMA: weight stages, 32 KB of int8 each (256 consecutive bytes a row).
+//   warps 2, 3  x, in slots of NT x SK columns as FP16.  Up to 32 rows they widen it
+//               from the caller's int8 themselves.  Above, int8_widen_kernel has
+//               written it as FP16 into the workspace (padded with zeros; the two are
+//               chained by programmatic dependent launch), and warp 2 copies it by
+//               TMA: a cluster of two blocks works on neighbouring tiles, each loads
+//               half of every x slot and multicasts it to both, which halves what x
+//               takes out of L2 (x of 128 rows is twice the weight's bytes).
+//   CONV warps  turn a weight stage into FP16 and store it into a ring of slots of
+//               tensor memory: lane = weight row, so that the operand crosses shared
+//               memory once, as bytes.  A byte b becomes FP16 1024 + (b ^ 0x80) by one
+//               byte permutation, and minus 1152 exactly b.
+//   warp 1      issues tcgen05.mma: A = the weight, from tensor memory, B = x, from
+//               shared memory, M = 128, N = NT.  Up to 64 rows a second warp (3, or the
+//               last one) issues too: they take turns at the slots, each with its own accumulator.
+//   EPI warps   drain the accumulators into integers, and finish tiles
+// A weight slot and its x slot share one pair of barriers: an issuing thread spends
+// about 64 cycles on an MMA, 55 on a commit and 100 on a wait, so one wait (tested
+// ahead, while the MMAs before it are issued) and one commit a slot.
+// Where whole tiles would leave blocks idle, the blocks take equal ranges of units, and
+// the parts of a tile that several blocks share are added into the plan's workspace by
+// integer atomics (exact, so any order gives the same bits); the block whose part
+// arrives last rounds and stores, and clears the workspace.  Blocks wait for one
+// another only inside a cluster.
 // Bound: the weight's bytes up to about 128 rows, the tensor cores above.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -63,28 +64,33 @@ namespace {
 
 constexpr int64_t kMaxK = 131056;  // 131056 * 128 * 128 < 2^31
 constexpr int kBM = 128;           // weight rows of a tile (MMA M)
-constexpr int kKU = 128;           // columns of a unit
-constexpr int kExact = 1024 / kKU; // units whose sums FP32 holds exactly
-constexpr int kWBytes = kBM * kKU; // a weight stage
+constexpr int kKU = 256;           // columns of a unit
+constexpr int kWBytes = kBM * kKU; // a weight stage: two boxes of 128 columns
 
 template <int NT>
 struct Int8Shape {
+    static constexpr bool DIRECT = NT <= 32;             // x comes straight from the caller
     static constexpr int CL = NT >= 64 ? 2 : 1;          // blocks of a cluster
     static constexpr int CONV = NT <= 64 ? 8 : 4;        // converting warps (from warp 4 on)
-    static constexpr int EPI = NT == 256 ? 16 : 12 - CONV;  // draining warps (the last)
-    static constexpr int THREADS = (4 + CONV + EPI) * 32;
+    static constexpr int GROUPS = CONV / 4;              // four warps take 128 columns
+    static constexpr int ISSUERS = GROUPS;               // issuer i takes the slots of group i
+    static constexpr int EPI = NT == 256 ? 16 : NT == 128 ? 8 : 4;  // draining warps
+    static constexpr int ISSUER1 = ISSUERS == 1 ? -1 : DIRECT ? 4 + CONV + EPI : 3;  // the second issuing warp
+    static constexpr int THREADS = (4 + CONV + EPI + (ISSUER1 > 3)) * 32;
     static constexpr int COLS = NT / (EPI / 4);          // batch columns of a draining thread
-    static constexpr int BUFS = NT <= 128 ? 2 : 1;       // accumulators
+    static constexpr int BUFS = NT <= 128 ? 2 : 1;       // sets of accumulators, one for each issuer
     static constexpr int SK = NT == 256 ? 64 : 128;      // columns of a slot
     static constexpr int SLOTS = NT == 256 ? 5 : 4;      // slots of tensor memory, and of x
     static constexpr int SLOT_COLS = SK / 2;             // a slot's 32-bit columns of tensor memory
     static constexpr int PER = kKU / SK;                 // slots of a unit
+    static constexpr int EXACT = 1024 * ISSUERS / kKU;   // units whose sums an FP32 accumulator holds exactly
     static constexpr int X_BYTES = NT * SK * 2;          // an x slot
     static constexpr int WS = (kMaxDynamicSmem - 1024 - 512 - SLOTS * X_BYTES) / kWBytes;
     static constexpr int ACC0 = 256;                     // the accumulators' first column
     static constexpr int BARS = 2 * WS + 2 * SLOTS + 2 * BUFS + 1;
     static constexpr int SMEM = 1024 + WS * kWBytes + SLOTS * X_BYTES + BARS * 8 + 16;
-    static_assert(SLOTS * SLOT_COLS <= ACC0 && ACC0 + BUFS * NT <= 512 && SMEM <= kMaxDynamicSmem, "");
+    static_assert(SLOTS * SLOT_COLS <= ACC0 && ACC0 + BUFS * ISSUERS * NT <= 512 && SMEM <= kMaxDynamicSmem, "");
+    static_assert(ISSUERS == 1 || (PER == 2 && SLOTS % 2 == 0), "an issuer's slots are its group's");
 };
 
 // How a launch deals its units out to its clusters: `whole` groups of tiles (one tile
@@ -104,9 +110,10 @@ struct Int8Split {
 };
 
 struct Int8Params {
+    const uint8_t *x;  // int8 [B, K]
     const float *xs, *ws;
     uint16_t *y;
-    int B;
+    int B, K;
     int64_t N;
     Int8Split split;
     int *counters, *sums;
@@ -186,7 +193,16 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
     hi = *reinterpret_cast<uint32_t *>(&hb);
 }
 
-// x [B, K] int8 -> xh [gridDim.y rows, Kp] FP16, zeros past B and K (Kp a multiple of 128, K of 16).
+// Sixteen int8 -> sixteen FP16.
+__device__ __forceinline__ void widen16(uint4 v, uint4 &lo, uint4 &hi)
+{
+    widen4(v.x, lo.x, lo.y);
+    widen4(v.y, lo.z, lo.w);
+    widen4(v.z, hi.x, hi.y);
+    widen4(v.w, hi.z, hi.w);
+}
+
+// x [B, K] int8 -> xh [gridDim.y rows, Kp] FP16, zeros past B and K (Kp a multiple of 256, K of 16).
 __global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restrict__ x, uint16_t *__restrict__ xh, int B,
                                                          int K, int Kp)
 {
@@ -198,10 +214,7 @@ __global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restri
     if (row < B && c < K)
         v = *reinterpret_cast<const uint4 *>(x + (int64_t)row * K + c);
     uint4 o[2];
-    widen4(v.x, o[0].x, o[0].y);
-    widen4(v.y, o[0].z, o[0].w);
-    widen4(v.z, o[1].x, o[1].y);
-    widen4(v.w, o[1].z, o[1].w);
+    widen16(v, o[0], o[1]);
     uint4 *d = reinterpret_cast<uint4 *>(xh + (int64_t)row * Kp + c);
     d[0] = o[0];
     d[1] = o[1];
@@ -227,21 +240,38 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     const int64_t KU = p.split.units;
     const SegOrder order(p.split.begin(c), p.split.begin(c + 1), KU);
 
+    // Weight copies (thread 0); the first ones start before anything else is set up.
+    UnitCursor wcur(order);
+    int wst = 0;
+    auto copy_w = [&](uint64_t pol) {
+        const int row = ((int)(wcur.u / KU) * S::CL + rank) * kBM, col = (int)(wcur.u % KU) * kKU;
+        const uint32_t dst = w0 + wst * kWBytes, bar = wfull + 8 * wst;
+        mbar_arrive_expect_tx(bar, kWBytes);
+        tma_load_2d(dst, &tmW, col, row, bar, pol);
+        tma_load_2d(dst + kWBytes / 2, &tmW, col + 128, row, bar, pol);
+        wcur.next();
+        ++wst;
+    };
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::WS; ++i) {
+        for (int i = 0; i < S::WS; ++i)
             mbar_init(wfull + 8 * i, 1);
-            mbar_init(wempty + 8 * i, 4);
-        }
-        for (int i = 0; i < S::SLOTS; ++i) {
-            mbar_init(sfull + 8 * i, 4 + 1);    // four converting warps, and x
-            mbar_init(sempty + 8 * i, S::CL);  // the MMAs of every block that x went to
-        }
-        for (int i = 0; i < S::BUFS; ++i) {
-            mbar_init(accf + 8 * i, 1);
-            mbar_init(acce + 8 * i, S::EPI);
-        }
-        mbar_init(done, 1);
+        fence_mbar_init();
+        const uint64_t pol = policy_evict_first();
+        while (wst < S::WS && !wcur.done())
+            copy_w(pol);
         *abort_flag = 0;
+    }
+    if (warp == 2) {
+        auto init = [&](uint32_t bar, int n, int count) {
+            for (int i = lane; i < n; i += 32)
+                mbar_init(bar + 8 * i, count);
+        };
+        init(wempty, S::WS, S::CONV);
+        init(sfull, S::SLOTS, 4 + 1);    // four converting warps, and x
+        init(sempty, S::SLOTS, S::CL);  // the MMAs of every block that x went to
+        init(accf, S::BUFS, S::ISSUERS);
+        init(acce, S::BUFS, S::EPI);
+        init(done, 1, S::ISSUERS);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -258,41 +288,91 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         record_status(p.status, code);
         *abort_flag = 1;
     };
+
     if (warp == 0) {
         // ---------------- weight copies ----------------
         if (lane == 0) {
-            prefetch_tmap(&tmW);
             const uint64_t pol = policy_evict_first();
-            UnitCursor cur(order);
-            int s = 0;
+            int filled = wst;  // stages that hold or await a copy
             uint32_t ph = 0;
-            int64_t issued = 0;
-            for (; !cur.done(); cur.next()) {
+            if (wst == S::WS) {
+                wst = 0;
+                ph = 1;
+            }
+            while (!wcur.done()) {
                 if (*abort_flag)
                     break;
-                if (!mbar_wait(wempty + 8 * s, ph ^ 1u, p.limit_ns)) {
+                if (!mbar_wait(wempty + 8 * wst, ph ^ 1u, p.limit_ns)) {
                     give_up(DEP_DEV_TIMEOUT_PRODUCER);
                     break;
                 }
-                mbar_arrive_expect_tx(wfull + 8 * s, kWBytes);
-                tma_load_2d(w0 + s * kWBytes, &tmW, (int)(cur.u % KU) * kKU, ((int)(cur.u / KU) * S::CL + rank) * kBM,
-                            wfull + 8 * s, pol);
-                ++issued;
-                if (++s == S::WS) {
-                    s = 0;
+                copy_w(pol);
+                if (wst == S::WS) {
+                    wst = 0;
                     ph ^= 1u;
                 }
             }
-            for (int64_t i = issued < S::WS ? issued : S::WS; i > 0; --i) {  // copies in flight
-                if (--s < 0) {
-                    s = S::WS - 1;
+            for (; filled > 0; --filled) {  // copies in flight
+                if (--wst < 0) {
+                    wst = S::WS - 1;
                     ph ^= 1u;
                 }
-                if (!mbar_wait(wfull + 8 * s, ph, p.limit_ns))
+                if (!mbar_wait(wfull + 8 * wst, ph, p.limit_ns))
                     record_status(p.status, DEP_DEV_TIMEOUT_PRODUCER);
             }
         }
-    } else if (warp == 2) {
+    } else if (S::DIRECT && (warp == 2 || warp == 3)) {
+        // ---------------- x, widened here: warp 2 the even slots, warp 3 the odd ones ----------------
+        constexpr int V = NT / 4;  // 16-byte pieces a lane: piece i is chunk (i % 8) of row i / 8
+        uint4 v[V];
+        UnitCursor cur(order);
+        auto fetch = [&]() {
+            const int col = (int)(cur.u % KU) * kKU + (warp - 2) * 128;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int row = 4 * i + (lane >> 3), k = col + (lane & 7) * 16;
+                v[i] = row < p.B && k < p.K ? __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)row * p.K + k))
+                                            : make_uint4(0, 0, 0, 0);
+            }
+        };
+        int s = warp - 2;
+        uint32_t ph = 0;
+        if (!cur.done())
+            fetch();
+        while (!cur.done()) {
+            const bool ok = !*abort_flag && mbar_wait(sempty + 8 * s, ph ^ 1u, p.limit_ns);
+            if (!__all_sync(~0u, ok)) {
+                if (lane == 0)
+                    give_up(DEP_DEV_TIMEOUT_PRODUCER);
+                break;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int row = 4 * i + (lane >> 3), ch = lane & 7;
+                uint4 lo, hi;
+                widen16(v[i], lo, hi);
+                // 64 columns a slice, rows of 128 bytes, 16-byte pieces in the 128-byte swizzle
+                const uint32_t at = x0 + s * S::X_BYTES + ((ch >> 2) * NT + row) * 128;
+                const uint32_t a0 = at + (((ch & 3) * 2) ^ (row & 7)) * 16, a1 = at + (((ch & 3) * 2 + 1) ^ (row & 7)) * 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w)
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                             : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads through the async proxy
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(sfull + 8 * s);
+            cur.next();
+            if (!cur.done())
+                fetch();
+            s += 2;
+            if (s >= S::SLOTS) {
+                s -= S::SLOTS;
+                ph ^= 1u;
+            }
+        }
+    } else if (!S::DIRECT && warp == 2) {
         // ---------------- x copies ----------------
         if (lane == 0) {
             prefetch_tmap(&tmX);
@@ -313,14 +393,10 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     }
                     mbar_arrive_expect_tx(sfull + 8 * s, S::X_BYTES);
                     const int block64 = (int)(cur.u % KU) * (kKU / 64) + h * (S::SK / 64);
-                    if (S::CL == 1) {
-                        tma_load_3d(x0 + s * S::X_BYTES, &tmX, 0, 0, block64, sfull + 8 * s, pol);
-                    } else {  // one copy for each 64 columns: its rows are a part of the slice
 #pragma unroll
-                        for (int j = 0; j < S::SK / 64; ++j)
-                            tma_load_3d_multicast(x0 + s * S::X_BYTES + (j * NT + rank * ROWS) * 128, &tmX, 0,
-                                                  rank * ROWS, block64 + j, sfull + 8 * s, (1 << S::CL) - 1, pol);
-                    }
+                    for (int j = 0; j < S::SK / 64; ++j)  // one copy for each 64 columns: its rows are a part of the slice
+                        tma_load_3d_multicast(x0 + s * S::X_BYTES + (j * NT + rank * ROWS) * 128, &tmX, 0, rank * ROWS,
+                                              block64 + j, sfull + 8 * s, (1 << S::CL) - 1, pol);
                     ++issued;
                     if (++s == S::SLOTS) {
                         s = 0;
@@ -339,28 +415,29 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     record_status(p.status, DEP_DEV_TIMEOUT_PRODUCER);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == S::ISSUER1) {
         // ---------------- MMA issue ----------------
+        const int mi = warp == 1 ? 0 : 1;
         if (lane == 0) {
             // FP16 operands (format 0), FP32 accumulator, N >> 3 and M >> 4
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            int s = 0, buf = 0;
+            int s = mi, buf = 0;
             uint32_t sph = 0, bph = 0;
             bool ok = true, ready = false;
             for (int64_t seg = 0; seg < order.m && ok; ++seg) {
                 const int64_t t = order.tile(seg);
                 const int64_t end = order.seg_end(t);
                 for (int64_t u = order.seg_begin(t); u < end && ok;) {
-                    const int64_t stop = u + kExact < end ? u + kExact : end;
+                    const int64_t stop = u + S::EXACT < end ? u + S::EXACT : end;
                     if (!mbar_wait(acce + 8 * buf, bph ^ 1u, p.limit_ns)) {
                         give_up(DEP_DEV_TIMEOUT_MMA);
                         ok = false;
                         break;
                     }
                     tc::fence_after();
-                    const uint32_t d = tmem + (uint32_t)(S::ACC0 + buf * NT);
+                    const uint32_t d = tmem + (uint32_t)(S::ACC0 + (buf * S::ISSUERS + mi) * NT);
                     uint32_t accumulate = 0;
-                    for (int n = (int)(stop - u) * S::PER; n > 0; --n) {
+                    for (int n = (int)(stop - u) * (S::PER / S::ISSUERS); n > 0; --n) {
                         if (!ready && (*abort_flag || !mbar_wait_cluster(sfull + 8 * s, sph, p.limit_ns))) {
                             give_up(DEP_DEV_TIMEOUT_MMA);
                             ok = false;
@@ -369,8 +446,9 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                         tc::fence_after();
                         const uint32_t a = tmem + (uint32_t)(s * S::SLOT_COLS), freed = sempty + 8 * s;
                         const uint64_t b = tc::desc_sw128(x0 + (uint32_t)(s * S::X_BYTES));
-                        if (++s == S::SLOTS) {
-                            s = 0;
+                        s += S::ISSUERS;
+                        if (s >= S::SLOTS) {
+                            s -= S::SLOTS;
                             sph ^= 1u;
                         }
                         ready = mbar_test(sfull + 8 * s, sph);  // the next slot's
@@ -401,17 +479,16 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         }
     } else if (warp >= 4 && warp < 4 + S::CONV) {
         // ---------------- int8 -> FP16 into tensor memory ----------------
-        constexpr int GROUPS = S::CONV / 4;  // four warps take a stage; two such groups take turns
         const int wg = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
         const int n_units = (int)(order.u_end - order.u_begin);
-        int ws = wg % S::WS, s = (wg * S::PER) % S::SLOTS;
+        int ws = 0, s = wg;  // two groups: group g takes columns [128 g, 128 g + 128) of every stage
         uint32_t wph = 0, sph = 0;
-        for (int i = wg; i < n_units; i += GROUPS) {
+        for (int i = 0; i < n_units; ++i) {
             bool ok = !*abort_flag && mbar_wait(wfull + 8 * ws, wph, p.limit_ns);
-            const uint32_t src = w0 + (uint32_t)(ws * kWBytes + row * 128);
+            const uint32_t src = w0 + (uint32_t)(ws * kWBytes + wg * (kWBytes / 2) + row * 128);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 64 columns
-                if (S::PER == 2 || h == 0) {
+            for (int h = 0; h < 4 / S::GROUPS; ++h) {  // 64 columns
+                if (S::SK == 64 || h % 2 == 0) {
                     ok = ok && mbar_wait(sempty + 8 * s, sph ^ 1u, p.limit_ns);
                     if (!__all_sync(~0u, ok))
                         break;
@@ -421,7 +498,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t w[4];
-                    const uint32_t at = src + (uint32_t)(((4 * h + j) ^ (row & 7)) * 16);
+                    const uint32_t at =
+                        src + (uint32_t)((h / 2) * (kWBytes / 2) + ((4 * (h % 2) + j) ^ (row & 7)) * 16);
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                                  : "r"(at));
@@ -429,19 +507,21 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     for (int e = 0; e < 4; ++e)
                         widen4(w[e], v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
                 }
-                tmem_st32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(s * S::SLOT_COLS + (S::PER == 2 ? 0 : 32 * h)), v);
-                if (h == 1) {
+                tmem_st32(tmem + ((uint32_t)(32 * q) << 16) +
+                              (uint32_t)(s * S::SLOT_COLS + (S::SK == 64 ? 0 : 32 * (h % 2))),
+                          v);
+                if (h == 4 / S::GROUPS - 1) {
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(wempty + 8 * ws);
                 }
-                if (S::PER == 2 || h == 1) {
+                if (S::SK == 64 || h % 2 == 1) {
                     tmem_wait_st();
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(sfull + 8 * s);
-                    s += S::PER == 2 ? 1 : GROUPS;
+                    s += S::GROUPS;
                     if (s >= S::SLOTS) {
                         s -= S::SLOTS;
                         sph ^= 1u;
@@ -453,9 +533,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     give_up(DEP_DEV_TIMEOUT_CONSUMER);
                 break;
             }
-            ws += GROUPS;
-            if (ws >= S::WS) {
-                ws -= S::WS;
+            if (++ws == S::WS) {
+                ws = 0;
                 wph ^= 1u;
             }
         }
@@ -467,14 +546,13 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
-        griddep_wait();  // y and the workspace may be in use by the grids before
         for (int64_t seg = 0; seg < order.m && ok; ++seg) {
             const int64_t g = order.tile(seg), t = g * S::CL + rank, end = order.seg_end(g);
             int acc[S::COLS];
 #pragma unroll
             for (int j = 0; j < S::COLS; ++j)
                 acc[j] = 0;
-            for (int64_t u = order.seg_begin(g); u < end; u += kExact) {
+            for (int64_t u = order.seg_begin(g); u < end; u += S::EXACT) {
                 ok = __all_sync(~0u, mbar_wait(accf + 8 * buf, bph, p.limit_ns));
                 if (!ok) {
                     if (lane == 0)
@@ -485,12 +563,15 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < S::COLS; j += 16) {
                     if (j < cols) {
-                        uint32_t v[16];
-                        tc::ld16(lane_addr + (uint32_t)(buf * NT + j), v);
-                        tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
+                        for (int m = 0; m < S::ISSUERS; ++m) {
+                            uint32_t v[16];
+                            tc::ld16(lane_addr + (uint32_t)((buf * S::ISSUERS + m) * NT + j), v);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
+                        }
                     }
                 }
                 tc::fence_before();
@@ -588,9 +669,11 @@ cudaError_t int8_launch(const dep_int8_plan_s &pl, const void *W, const Int8Para
     if (e != cudaSuccess)
         return e;
     CUtensorMap tmW, tmX;
-    const int64_t Kp = p.split.units * kKU;
-    if (encode_u8_2d(&tmW, W, (uint64_t)pl.K, (uint64_t)pl.N, kKU, kBM) != CUDA_SUCCESS ||
-        encode_bf16_3d_blocks(&tmX, pl.xh, (uint64_t)Kp, NT, NT / S::CL, S::CL == 1 ? S::SK / 64 : 1) != CUDA_SUCCESS)
+    if (encode_u8_2d(&tmW, W, (uint64_t)pl.K, (uint64_t)pl.N, 128, kBM) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    if (S::DIRECT)
+        tmX = tmW;  // not used
+    else if (encode_bf16_3d_blocks(&tmX, pl.xh, (uint64_t)(p.split.units * kKU), NT, NT / S::CL, 1) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.split.clusters * S::CL);
@@ -599,7 +682,7 @@ cudaError_t int8_launch(const dep_int8_plan_s &pl, const void *W, const Int8Para
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = S::DIRECT ? 0 : 1;  // after int8_widen_kernel
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = S::CL;
     attr[1].val.clusterDim.y = 1;
@@ -614,13 +697,15 @@ cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *
 {
     const int nt = width(B);
     const Int8Split split = split_for(pl.N, pl.K, nt, pl.sm_count);
-    const int Kp = (int)split.units * kKU;
-    const dim3 grid((unsigned)((Kp / 16 + 255) / 256), (unsigned)nt);
-    int8_widen_kernel<<<grid, 256, 0, stream>>>(x, pl.xh, B, (int)pl.K, Kp);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
-    const Int8Params p{xs, ws, y, B, pl.N, split, pl.counters, pl.sums, pl.status, pl.wait_limit_ns};
+    if (nt > 32) {
+        const int Kp = (int)split.units * kKU;
+        const dim3 grid((unsigned)((Kp / 16 + 255) / 256), (unsigned)nt);
+        int8_widen_kernel<<<grid, 256, 0, stream>>>(x, pl.xh, B, (int)pl.K, Kp);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return e;
+    }
+    const Int8Params p{x, xs, ws, y, B, (int)pl.K, pl.N, split, pl.counters, pl.sums, pl.status, pl.wait_limit_ns};
     switch (nt) {
     case 16: return int8_launch<16>(pl, W, p, stream);
     case 32: return int8_launch<32>(pl, W, p, stream);
@@ -633,6 +718,11 @@ cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *
 // Raise every kernel's shared-memory limit now, so that no first launch does it inside a capture.
 cudaError_t int8_prepare_device()
 {
+    // The same split of L1 and shared memory as the kernel it is chained to: no SM has to drain between them.
+    cudaError_t c = cudaFuncSetAttribute(int8_widen_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         (int)cudaSharedmemCarveoutMaxShared);
+    if (c != cudaSuccess)
+        return c;
     for (cudaError_t e : {int8_prepare<16>(), int8_prepare<32>(), int8_prepare<64>(), int8_prepare<128>(),
                           int8_prepare<256>()})
         if (e != cudaSuccess)
@@ -687,7 +777,7 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
             sums = (size_t)(tiles + 1) * w * dep::kBM * sizeof(int);
     const size_t counters = ((size_t)(tiles + 1) * 16 * sizeof(int) + 255) / 256 * 256;
     p->clear_bytes = 256 + counters + sums;
-    p->bytes = p->clear_bytes + (size_t)nt * Kp * 2;
+    p->bytes = p->clear_bytes + (nt > 32 ? (size_t)nt * Kp * 2 : 0);
     if (cudaMalloc(&p->block, p->bytes) != cudaSuccess) {
         cudaGetLastError();
         delete p;
