@@ -79,8 +79,8 @@ struct Int8Shape {
     static constexpr int THREADS = (4 + CONV + EPI + (ISSUER1 > 3)) * 32;
     static constexpr int COLS = NT / (EPI / 4);          // batch columns of a draining thread
     static constexpr int BUFS = NT <= 128 ? 2 : 1;       // sets of accumulators, one for each issuer
-    static constexpr int SK = NT == 256 ? 64 : 128;      // columns of a slot
-    static constexpr int SLOTS = NT == 256 ? 5 : 4;      // slots of tensor memory, and of x
+    static constexpr int SK = NT == 128 ? 128 : 64;      // columns of a slot
+    static constexpr int SLOTS = NT == 256 ? 5 : NT == 128 ? 4 : 8;  // slots of tensor memory, and of x
     static constexpr int SLOT_COLS = SK / 2;             // a slot's 32-bit columns of tensor memory
     static constexpr int PER = kKU / SK;                 // slots of a unit
     static constexpr int EXACT = 1024 * ISSUERS / kKU;   // units whose sums an FP32 accumulator holds exactly
@@ -90,22 +90,64 @@ struct Int8Shape {
     static constexpr int BARS = 2 * WS + 2 * SLOTS + 2 * BUFS + 1;
     static constexpr int SMEM = 1024 + WS * kWBytes + SLOTS * X_BYTES + BARS * 8 + 16;
     static_assert(SLOTS * SLOT_COLS <= ACC0 && ACC0 + BUFS * ISSUERS * NT <= 512 && SMEM <= kMaxDynamicSmem, "");
-    static_assert(ISSUERS == 1 || (PER == 2 && SLOTS % 2 == 0), "an issuer's slots are its group's");
+    static_assert(GROUPS == 1 || (PER == 4 && SLOTS == 8), "group g: slots 2g, 2g + 1 of the four of a unit");
+    // The slot after s among those of one group (and of one issuer), and whether the ring wraps.
+    __device__ static bool next(int &s)
+    {
+        s += GROUPS == 1 || (s & 1) == 0 ? 1 : 3;
+        if (s < SLOTS)
+            return false;
+        s -= SLOTS;
+        return true;
+    }
 };
 
 // How a launch deals its units out to its clusters: `whole` groups of tiles (one tile
-// for each block of a cluster), or equal ranges of units.
+// for each block of a cluster), or single units; the first `rem` clusters get one more
+// than `base` of them.
 struct Int8Split {
-    int64_t groups, units;  // units of a tile
-    int clusters;
-    int whole;
-    __host__ __device__ int64_t begin(int64_t c) const
+    int groups, units;  // units of a tile
+    int clusters, whole, base, rem;
+    __host__ __device__ int begin(int c) const  // cluster c's first unit
     {
-        return whole ? sk_begin(c, groups, clusters) * units : sk_begin(c, groups * units, clusters);
+        return (c * base + (c < rem ? c : rem)) * (whole ? units : 1);
     }
-    __host__ __device__ int64_t owner(int64_t u) const
+    __device__ int owner(int u) const  // the cluster of unit u
     {
-        return whole ? sk_owner(u / units, groups, clusters) : sk_owner(u, groups * units, clusters);
+        const uint32_t v = whole ? (uint32_t)u / (uint32_t)units : (uint32_t)u, big = (uint32_t)rem * (base + 1);
+        return (int)(v < big ? v / (uint32_t)(base + 1) : rem + (v - big) / (uint32_t)base);
+    }
+};
+
+// Walks a cluster's units [begin, end): the part of the last group first, then from the
+// first group on, so that the parts that clusters share are done early.
+struct Int8Walk {
+    int begin, end, units, first, last, m;
+    __device__ Int8Walk(int b, int e, int ku)
+        : begin(b), end(e), units(ku), first((uint32_t)b / (uint32_t)ku), last((uint32_t)(e - 1) / (uint32_t)ku),
+          m(last - first + 1)
+    {
+    }
+    __device__ int group(int i) const { return i == 0 ? last : first + i - 1; }
+    __device__ int from(int g) const { return begin > g * units ? begin - g * units : 0; }  // units inside the group
+    __device__ int to(int g) const { return end < (g + 1) * units ? end - g * units : units; }
+};
+
+struct Int8Cursor {
+    const Int8Walk &w;
+    int i = 0, g, u, stop;
+    __device__ explicit Int8Cursor(const Int8Walk &walk) : w(walk) { seek(); }
+    __device__ void seek()
+    {
+        g = w.group(i);
+        u = w.from(g);
+        stop = w.to(g);
+    }
+    __device__ bool done() const { return i >= w.m; }
+    __device__ void next()
+    {
+        if (++u == stop && ++i < w.m)
+            seek();
     }
 };
 
@@ -193,6 +235,31 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
     hi = *reinterpret_cast<uint32_t *>(&hb);
 }
 
+// Add sixteen accumulators (whole numbers of at most 2^24) to integers.  The conversion
+// instruction runs at an eighth of the rate of an addition, so numbers below 2^22 are
+// read off the mantissa of their sum with 1.5 * 2^23; if any of a warp's is larger, that
+// shows in the sum's exponent and the warp converts.
+__device__ __forceinline__ void drain16(const uint32_t (&v)[16], int *acc)
+{
+    constexpr int kMagic = 0x4B400000;  // 1.5 * 2^23
+    int s[16], seen = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        s[i] = __float_as_int(__uint_as_float(v[i]) + __int_as_float(kMagic));
+        seen |= s[i] ^ kMagic;
+    }
+    // |value| < 2^22 <=> the sum lies in [2^23, 2^24): sign and exponent as kMagic's
+    if (__all_sync(~0u, (seen & 0xFF800000) == 0)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc[i] += s[i] - kMagic;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc[i] += __float2int_rn(__uint_as_float(v[i]));
+    }
+}
+
 // Sixteen int8 -> sixteen FP16.
 __device__ __forceinline__ void widen16(uint4 v, uint4 &lo, uint4 &hi)
 {
@@ -236,15 +303,15 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S::CL == 1 ? 0 : (int)cluster_rank();
-    const int64_t c = S::CL == 1 ? blockIdx.x : blockIdx.x / S::CL;
-    const int64_t KU = p.split.units;
-    const SegOrder order(p.split.begin(c), p.split.begin(c + 1), KU);
+    const int c = S::CL == 1 ? blockIdx.x : blockIdx.x / S::CL;
+    const int KU = p.split.units;
+    const Int8Walk walk(p.split.begin(c), p.split.begin(c + 1), KU);
 
     // Weight copies (thread 0); the first ones start before anything else is set up.
-    UnitCursor wcur(order);
+    Int8Cursor wcur(walk);
     int wst = 0;
     auto copy_w = [&](uint64_t pol) {
-        const int row = ((int)(wcur.u / KU) * S::CL + rank) * kBM, col = (int)(wcur.u % KU) * kKU;
+        const int row = (wcur.g * S::CL + rank) * kBM, col = wcur.u * kKU;
         const uint32_t dst = w0 + wst * kWBytes, bar = wfull + 8 * wst;
         mbar_arrive_expect_tx(bar, kWBytes);
         tma_load_2d(dst, &tmW, col, row, bar, pol);
@@ -322,25 +389,25 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             }
         }
     } else if (S::DIRECT && (warp == 2 || warp == 3)) {
-        // ---------------- x, widened here: warp 2 the even slots, warp 3 the odd ones ----------------
-        constexpr int V = NT / 4;  // 16-byte pieces a lane: piece i is chunk (i % 8) of row i / 8
+        // ---------------- x, widened here: each warp 128 columns of a unit ----------------
+        constexpr int V = NT / 4;  // 16-byte pieces a lane: piece i is chunk (lane % 8) of row 4 i + lane / 8
         uint4 v[V];
-        UnitCursor cur(order);
+        Int8Cursor cur(walk);
         auto fetch = [&]() {
-            const int col = (int)(cur.u % KU) * kKU + (warp - 2) * 128;
+            const int k = cur.u * kKU + (warp - 2) * 128 + (lane & 7) * 16;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int row = 4 * i + (lane >> 3), k = col + (lane & 7) * 16;
+                const int row = 4 * i + (lane >> 3);
                 v[i] = row < p.B && k < p.K ? __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)row * p.K + k))
                                             : make_uint4(0, 0, 0, 0);
             }
         };
-        int s = warp - 2;
+        int s = 2 * (warp - 2);  // slots s and s + 1: 64 columns each
         uint32_t ph = 0;
-        if (!cur.done())
-            fetch();
+        fetch();
         while (!cur.done()) {
-            const bool ok = !*abort_flag && mbar_wait(sempty + 8 * s, ph ^ 1u, p.limit_ns);
+            const bool ok = !*abort_flag && mbar_wait(sempty + 8 * s, ph ^ 1u, p.limit_ns) &&
+                            mbar_wait(sempty + 8 * s + 8, ph ^ 1u, p.limit_ns);
             if (!__all_sync(~0u, ok)) {
                 if (lane == 0)
                     give_up(DEP_DEV_TIMEOUT_PRODUCER);
@@ -351,8 +418,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                 const int row = 4 * i + (lane >> 3), ch = lane & 7;
                 uint4 lo, hi;
                 widen16(v[i], lo, hi);
-                // 64 columns a slice, rows of 128 bytes, 16-byte pieces in the 128-byte swizzle
-                const uint32_t at = x0 + s * S::X_BYTES + ((ch >> 2) * NT + row) * 128;
+                // rows of 128 bytes, 16-byte pieces in the 128-byte swizzle
+                const uint32_t at = x0 + (s + (ch >> 2)) * S::X_BYTES + row * 128;
                 const uint32_t a0 = at + (((ch & 3) * 2) ^ (row & 7)) * 16, a1 = at + (((ch & 3) * 2 + 1) ^ (row & 7)) * 16;
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w)
                              : "memory");
@@ -361,16 +428,13 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads through the async proxy
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(sfull + 8 * s);
+            if (lane < 2)
+                mbar_arrive(sfull + 8 * (s + lane));
             cur.next();
             if (!cur.done())
                 fetch();
-            s += 2;
-            if (s >= S::SLOTS) {
-                s -= S::SLOTS;
-                ph ^= 1u;
-            }
+            s ^= 4;
+            ph ^= (uint32_t)((s & 4) == 0);
         }
     } else if (!S::DIRECT && warp == 2) {
         // ---------------- x copies ----------------
@@ -379,7 +443,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             const uint64_t pol = policy_evict_last();
             griddep_wait();  // x in FP16 is written by the preceding grid
             constexpr int ROWS = NT / S::CL;  // x rows that this block loads
-            UnitCursor cur(order);
+            Int8Cursor cur(walk);
             int s = 0;
             uint32_t ph = 0;
             int64_t issued = 0;
@@ -392,7 +456,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                         break;
                     }
                     mbar_arrive_expect_tx(sfull + 8 * s, S::X_BYTES);
-                    const int block64 = (int)(cur.u % KU) * (kKU / 64) + h * (S::SK / 64);
+                    const int block64 = cur.u * (kKU / 64) + h * (S::SK / 64);
 #pragma unroll
                     for (int j = 0; j < S::SK / 64; ++j)  // one copy for each 64 columns: its rows are a part of the slice
                         tma_load_3d_multicast(x0 + s * S::X_BYTES + (j * NT + rank * ROWS) * 128, &tmX, 0, rank * ROWS,
@@ -421,14 +485,13 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         if (lane == 0) {
             // FP16 operands (format 0), FP32 accumulator, N >> 3 and M >> 4
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            int s = mi, buf = 0;
+            int s = 2 * mi, buf = 0;
             uint32_t sph = 0, bph = 0;
             bool ok = true, ready = false;
-            for (int64_t seg = 0; seg < order.m && ok; ++seg) {
-                const int64_t t = order.tile(seg);
-                const int64_t end = order.seg_end(t);
-                for (int64_t u = order.seg_begin(t); u < end && ok;) {
-                    const int64_t stop = u + S::EXACT < end ? u + S::EXACT : end;
+            for (int seg = 0; seg < walk.m && ok; ++seg) {
+                const int g = walk.group(seg), end = walk.to(g);
+                for (int u = walk.from(g); u < end && ok;) {
+                    const int stop = u + S::EXACT < end ? u + S::EXACT : end;
                     if (!mbar_wait(acce + 8 * buf, bph ^ 1u, p.limit_ns)) {
                         give_up(DEP_DEV_TIMEOUT_MMA);
                         ok = false;
@@ -437,7 +500,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     tc::fence_after();
                     const uint32_t d = tmem + (uint32_t)(S::ACC0 + (buf * S::ISSUERS + mi) * NT);
                     uint32_t accumulate = 0;
-                    for (int n = (int)(stop - u) * (S::PER / S::ISSUERS); n > 0; --n) {
+                    for (int n = (stop - u) * (S::PER / S::ISSUERS); n > 0; --n) {
                         if (!ready && (*abort_flag || !mbar_wait_cluster(sfull + 8 * s, sph, p.limit_ns))) {
                             give_up(DEP_DEV_TIMEOUT_MMA);
                             ok = false;
@@ -446,11 +509,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                         tc::fence_after();
                         const uint32_t a = tmem + (uint32_t)(s * S::SLOT_COLS), freed = sempty + 8 * s;
                         const uint64_t b = tc::desc_sw128(x0 + (uint32_t)(s * S::X_BYTES));
-                        s += S::ISSUERS;
-                        if (s >= S::SLOTS) {
-                            s -= S::SLOTS;
-                            sph ^= 1u;
-                        }
+                        sph ^= (uint32_t)S::next(s);
                         ready = mbar_test(sfull + 8 * s, sph);  // the next slot's
 #pragma unroll
                         for (int i = 0; i < S::SK / 16; ++i) {
@@ -480,8 +539,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     } else if (warp >= 4 && warp < 4 + S::CONV) {
         // ---------------- int8 -> FP16 into tensor memory ----------------
         const int wg = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
-        const int n_units = (int)(order.u_end - order.u_begin);
-        int ws = 0, s = wg;  // two groups: group g takes columns [128 g, 128 g + 128) of every stage
+        const int n_units = walk.end - walk.begin;
+        int ws = 0, s = 2 * wg;  // two groups: group g takes columns [128 g, 128 g + 128) of every stage
         uint32_t wph = 0, sph = 0;
         for (int i = 0; i < n_units; ++i) {
             bool ok = !*abort_flag && mbar_wait(wfull + 8 * ws, wph, p.limit_ns);
@@ -521,11 +580,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(sfull + 8 * s);
-                    s += S::GROUPS;
-                    if (s >= S::SLOTS) {
-                        s -= S::SLOTS;
-                        sph ^= 1u;
-                    }
+                    sph ^= (uint32_t)S::next(s);
                 }
             }
             if (!__all_sync(~0u, ok)) {
@@ -546,13 +601,19 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
-        for (int64_t seg = 0; seg < order.m && ok; ++seg) {
-            const int64_t g = order.tile(seg), t = g * S::CL + rank, end = order.seg_end(g);
+        float xs[(S::COLS + 31) / 32];  // scale of column 32 i + lane
+#pragma unroll
+        for (int i = 0; i < (S::COLS + 31) / 32; ++i)
+            xs[i] = 32 * i + lane < cols ? p.xs[c0 + 32 * i + lane] : 0.0f;
+        for (int seg = 0; seg < walk.m && ok; ++seg) {
+            const int g = walk.group(seg), end = walk.to(g);
+            const int64_t t = (int64_t)g * S::CL + rank, n = t * kBM + 32 * q + lane;
+            const float ws = n < p.N ? p.ws[n] : 0.0f;
             int acc[S::COLS];
 #pragma unroll
             for (int j = 0; j < S::COLS; ++j)
                 acc[j] = 0;
-            for (int64_t u = order.seg_begin(g); u < end; u += S::EXACT) {
+            for (int u = walk.from(g); u < end; u += S::EXACT) {
                 ok = __all_sync(~0u, mbar_wait(accf + 8 * buf, bph, p.limit_ns));
                 if (!ok) {
                     if (lane == 0)
@@ -568,9 +629,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                             uint32_t v[16];
                             tc::ld16(lane_addr + (uint32_t)((buf * S::ISSUERS + m) * NT + j), v);
                             tc::wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
+                            drain16(v, acc + j);
                         }
                     }
                 }
@@ -585,9 +644,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             }
             if (!ok)
                 break;
-            const int64_t n = t * kBM + 32 * q + lane;
             bool last = true;
-            const int64_t parts = p.split.owner((g + 1) * KU - 1) - p.split.owner(g * KU) + 1;
+            const int parts = p.split.owner((g + 1) * KU - 1) - p.split.owner(g * KU) + 1;
             if (parts > 1) {
                 int *sums = p.sums + (t * NT + c0) * kBM + 32 * q + lane;
 #pragma unroll
@@ -603,22 +661,24 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                 if (last) {
                     __threadfence();
 #pragma unroll
-                    for (int j = 0; j < S::COLS; ++j)
-                        if (j < cols) {
+                    for (int j = 0; j < S::COLS; ++j)  // all loads, then all stores
+                        if (j < cols)
                             acc[j] = __ldcg(sums + j * kBM);
+#pragma unroll
+                    for (int j = 0; j < S::COLS; ++j)
+                        if (j < cols)
                             __stcg(sums + j * kBM, 0);
-                        }
                     if (lane == 0)
                         p.counters[t * 16 + e] = 0;
                 }
             }
-            if (last && n < p.N) {
-                const float ws = p.ws[n];
+            if (last) {
 #pragma unroll
-                for (int j = 0; j < S::COLS; ++j)
-                    if (j < cols)
-                        p.y[(int64_t)(c0 + j) * p.N + n] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn((float)acc[j] * (p.xs[c0 + j] * ws)));
+                for (int j = 0; j < S::COLS; ++j) {
+                    const float scale = __shfl_sync(~0u, xs[j / 32], j % 32) * ws;
+                    if (j < cols && n < p.N)
+                        p.y[(int64_t)(c0 + j) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn((float)acc[j] * scale));
+                }
             }
         }
     }
@@ -641,15 +701,18 @@ int cluster_of(int nt) { return nt >= 64 ? 2 : 1; }
 
 Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
 {
-    const int cl = cluster_of(nt);
+    const int cl = cluster_of(nt), most = sms / cl;
     Int8Split s;
-    s.groups = ((N + kBM - 1) / kBM + cl - 1) / cl;
-    s.units = (K + kKU - 1) / kKU;
-    const int64_t all = s.groups * s.units, most = sms / cl, waves = (s.groups + most - 1) / most;
+    s.groups = (int)(((N + kBM - 1) / kBM + cl - 1) / cl);
+    s.units = (int)((K + kKU - 1) / kKU);
+    const int all = s.groups * s.units, waves = (s.groups + most - 1) / most;
     // Equal ranges unless whole tiles keep nearly every block busy, or sums of 256
     // columns (128 KB for each part of a tile) would cost more than the idle blocks.
-    s.whole = nt == 256 || s.groups * 100 >= waves * most * 95;
-    s.clusters = (int)(s.whole ? (s.groups < most ? s.groups : most) : (all < most ? all : most));
+    s.whole = nt == 256 || s.groups * 100ll >= (int64_t)waves * most * 95;
+    const int n = s.whole ? s.groups : all;
+    s.clusters = n < most ? n : most;
+    s.base = n / s.clusters;
+    s.rem = n % s.clusters;
     return s;
 }
 
@@ -744,7 +807,7 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
         return DEP_ERR_INVALID_ARG;
     if (K % 16 != 0)
         return DEP_ERR_MISALIGNED;
-    if (K > dep::kMaxK || N > INT32_MAX)
+    if (K > dep::kMaxK || N > INT32_MAX || (N / dep::kBM + 2) * (K / dep::kKU + 1) > INT32_MAX)
         return DEP_ERR_UNSUPPORTED;
     dep_int8_plan_s *p = new (std::nothrow) dep_int8_plan_s;
     if (!p)
