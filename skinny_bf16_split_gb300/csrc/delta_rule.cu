@@ -11,6 +11,21 @@
 // together, so each token costs one reduction: with u = beta (v - S k),
 // o = scale (S q + u (k . q)) and S + u k^T.
 // Bound: DRAM, the state read and written once (8 Dk Dv bytes a head).
+//
+// Chunked kernel, for longer sequences: 16 tokens at a time as matrix products.
+// With P_i = a_0 .. a_i, R_j = a_(j+1) .. a_15 and M_ij = a_(j+1) .. a_i (products of
+// decays, channel by channel; never a quotient, so a decay of zero is as good as any),
+//     A_ij = beta_i sum_c k_i k_j M_ij  (j < i),    B_ij = sum_c q_i k_j M_ij  (j <= i)
+//     T = (I + A)^-1 diag(beta),                    U = T (V - (K.P) S^T)
+//     O = (Q.P) S^T + B U,                          S <- S diag(P_15) + U^T (K.R)
+// A block takes up to 128 rows of one head's state.  Its first warps hold 16 rows of S
+// each, as the accumulator of the last product, for the whole sequence: an accumulator
+// fragment is also a left operand of the next product (with the channels in another
+// order, the same on both sides), so S, U and the rest never leave the registers.  Four
+// more warps prepare the next chunk meanwhile: norms, decays, A, B and T, and K.P, Q.P,
+// K.R in two shared-memory stages.
+// FP32 operands are split into two TF32 parts, and three products are kept (the fourth is
+// below 2^-22): everything keeps FP32's precision, or nearly.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -189,6 +204,409 @@ cudaError_t recurrent_launch(const DeltaParams &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------------
+// chunked kernel
+
+constexpr int kC = 16;            // tokens of a chunk
+constexpr int kPrep = 128;        // preparing threads
+constexpr int kTS = 24;           // row stride of 16-wide matrices in shared memory: float2 reads without conflicts
+
+// Barrier `id` of the block's hardware barriers, for n threads.
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int n)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ uint32_t tf32_hi(float v)
+{
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void tf32_split(float v, uint32_t &hi, uint32_t &lo)
+{
+    hi = tf32_hi(v);
+    lo = __float_as_uint(v - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The accumulator fragment c as a left operand: its columns 2t and 2t + 1 become k = t and t + 4.
+__device__ __forceinline__ void split_a(const float (&c)[4], uint32_t (&hi)[4], uint32_t (&lo)[4])
+{
+    tf32_split(c[0], hi[0], lo[0]);
+    tf32_split(c[2], hi[1], lo[1]);
+    tf32_split(c[1], hi[2], lo[2]);
+    tf32_split(c[3], hi[3], lo[3]);
+}
+__device__ __forceinline__ void mma_tf32x3(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float2 b)
+{
+    uint32_t h0, l0, h1, l1;
+    tf32_split(b.x, h0, l0);
+    tf32_split(b.y, h1, l1);
+    mma_tf32(d, al, h0, h1);
+    mma_tf32(d, ah, l0, l1);
+    mma_tf32(d, ah, h0, h1);
+}
+
+template <int DK>
+struct ChunkStage {
+    static constexpr int KS = DK + 8;  // row stride of K.P and Q.P: float2 reads without conflicts
+    float kp[kC][KS], qp[kC][KS];      // [token][channel]
+    float kr[DK][kTS];                 // [channel][token]
+    float T[kC][kTS], B[kC][kTS];      // [token i][token j]
+    float last[DK];                    // P_15
+};
+template <int DK>
+struct ChunkShared {
+    ChunkStage<DK> stage[2];
+    float k[kC][DK], q[kC][DK], a[kC][DK];  // normalised rows and decays of the chunk in preparation
+    float A[kC][kC];
+    float part[4][32], norm[32], beta[kC];
+    uint4 out[8][kC][2];  // a warp's rows of O, [token][16 rows in BF16]
+};
+
+// Sum of v over the warp's lanes, for eight values: lane l returns the sum of v[l >> 2].
+__device__ __forceinline__ float reduce8(float (&v)[8], int lane)
+{
+#pragma unroll
+    for (int n = 4, bit = 16; n; n >>= 1, bit >>= 1) {
+        const bool up = (lane & bit) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(~0u, send, bit);
+        }
+    }
+    float r = v[0];
+    r += __shfl_xor_sync(~0u, r, 2);
+    r += __shfl_xor_sync(~0u, r, 1);
+    return r;
+}
+
+template <int DK, int MW>
+__global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const DeltaParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    ChunkShared<DK> &sm = *reinterpret_cast<ChunkShared<DK> *>(smem_raw);
+    constexpr int kThreads = kPrep + 32 * MW, kBarPrep = 1, kBarFull = 2, kBarEmpty = 4;
+    const int slices = (p.Dv + 16 * MW - 1) / (16 * MW);
+    const int slice = blockIdx.x % slices, sh = blockIdx.x / slices;
+    const int h = sh % p.Hv, s = sh / p.Hv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t t0, t1;
+    seq_range(p, s, t0, t1);
+    const int64_t slot = p.slots ? p.slots[s] : s;
+    const bool pad = slot < 0 || slot >= p.n_states;
+    const int64_t len = t1 - t0, chunks = pad ? 0 : (len + kC - 1) / kC;
+    const int64_t sbase = (slot * p.Hv + h) * (int64_t)p.Dv * DK;
+    const bool chan = (p.flags & DEP_DELTA_CHANNEL) != 0, l2 = (p.flags & DEP_DELTA_L2NORM) != 0;
+
+    if (pad) {  // zeros out, no state
+        const int rows = p.Dv - slice * 16 * MW < 16 * MW ? p.Dv - slice * 16 * MW : 16 * MW;
+        for (int64_t i = threadIdx.x; i < len * rows; i += kThreads)
+            p.o[(t0 + i / rows) * p.os + (int64_t)h * p.Dv + slice * 16 * MW + i % rows] = 0;
+        return;
+    }
+
+    if (warp < MW) {
+        // ---------------- state rows row0 .. row0 + 15 ----------------
+        const int row0 = (slice * MW + warp) * 16, g = lane >> 2, t = lane & 3;
+        const bool live = row0 < p.Dv;  // Dv is a multiple of 16
+        constexpr int NT = DK / 8;
+        float S[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float2 a = make_float2(0.f, 0.f), b = a;
+            if (live && p.s_in) {
+                a = *reinterpret_cast<const float2 *>(p.s_in + sbase + (int64_t)(row0 + g) * DK + 8 * n + 2 * t);
+                b = *reinterpret_cast<const float2 *>(p.s_in + sbase + (int64_t)(row0 + g + 8) * DK + 8 * n + 2 * t);
+            }
+            S[n][0] = a.x;
+            S[n][1] = a.y;
+            S[n][2] = b.x;
+            S[n][3] = b.y;
+        }
+        const uint16_t *vp = p.v + t0 * p.vs + (int64_t)h * p.Dv + row0 + g;
+        // V^T in accumulator layout: rows g and g + 8, tokens 8 n + 2 t and + 1
+        auto load_v = [&](int64_t c, uint16_t (&v)[2][4]) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t tok = c * kC + 8 * n + 2 * t + j;
+                    const bool in = live && tok < len;
+                    v[n][j] = in ? vp[tok * p.vs] : 0;
+                    v[n][2 + j] = in ? vp[tok * p.vs + 8] : 0;
+                }
+        };
+        uint16_t v[2][4];
+        if (chunks)
+            load_v(0, v);
+        for (int64_t c = 0; c < chunks; ++c) {
+            const int st = (int)(c & 1);
+            bar_sync(kBarFull + st, kThreads);
+            const ChunkStage<DK> &sg = sm.stage[st];
+            float X[2][4] = {}, O[2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < NT; ++ks) {
+                uint32_t ah[4], al[4];
+                split_a(S[ks], ah, al);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 kb = *reinterpret_cast<const float2 *>(&sg.kp[8 * n + g][8 * ks + 2 * t]);
+                    const float2 qb = *reinterpret_cast<const float2 *>(&sg.qp[8 * n + g][8 * ks + 2 * t]);
+                    mma_tf32x3(X[n], ah, al, kb);
+                    mma_tf32x3(O[n], ah, al, qb);
+                }
+            }
+            // Y = V - X, then U^T = Y^T T^T and O^T += U^T B^T (both lower triangular: tokens j <= i)
+            uint32_t yh[2][4], yl[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    X[n][j] = __uint_as_float((uint32_t)v[n][j] << 16) - X[n][j];
+                split_a(X[n], yh[n], yl[n]);
+            }
+            if (c + 1 < chunks)
+                load_v(c + 1, v);
+            float U[2][4] = {};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int ks = 0; ks <= n; ++ks)
+                    mma_tf32x3(U[n], yh[ks], yl[ks],
+                               *reinterpret_cast<const float2 *>(&sg.T[8 * n + g][8 * ks + 2 * t]));
+            uint32_t uh[2][4], ul[2][4];
+            split_a(U[0], uh[0], ul[0]);
+            split_a(U[1], uh[1], ul[1]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int ks = 0; ks <= n; ++ks) {
+                    const float2 b = *reinterpret_cast<const float2 *>(&sg.B[8 * n + g][8 * ks + 2 * t]);
+                    mma_tf32x3(O[n], uh[ks], ul[ks], b);
+                }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 a = *reinterpret_cast<const float2 *>(&sg.last[8 * n + 2 * t]);
+                S[n][0] *= a.x;
+                S[n][1] *= a.y;
+                S[n][2] *= a.x;
+                S[n][3] *= a.y;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    mma_tf32x3(S[n], uh[ks], ul[ks],
+                               *reinterpret_cast<const float2 *>(&sg.kr[8 * n + g][8 * ks + 2 * t]));
+            }
+            if (c + 2 < chunks)
+                bar_arrive(kBarEmpty + st, kThreads);
+            // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
+            uint32_t r[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n]) : "f"(O[n][1]), "f"(O[n][0]));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n + 1]) : "f"(O[n][3]), "f"(O[n][2]));
+            }
+            const uint32_t at =
+                (uint32_t)__cvta_generic_to_shared(&sm.out[warp][(lane >> 4) * 8 + (lane & 7)][(lane >> 3) & 1]);
+            __syncwarp();
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]),
+                         "r"(r[1]), "r"(r[2]), "r"(r[3])
+                         : "memory");
+            __syncwarp();
+            const int64_t tok = c * kC + (lane >> 1);
+            if (live && tok < len)
+                *reinterpret_cast<uint4 *>(p.o + (t0 + tok) * p.os + (int64_t)h * p.Dv + row0 + 8 * (lane & 1)) =
+                    sm.out[warp][lane >> 1][lane & 1];
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (live) {
+                *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g) * DK + 8 * n + 2 * t) =
+                    make_float2(S[n][0], S[n][1]);
+                *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g + 8) * DK + 8 * n + 2 * t) =
+                    make_float2(S[n][2], S[n][3]);
+            }
+    } else {
+        // ---------------- the next chunk's operands ----------------
+        const int pt = threadIdx.x - 32 * MW, pw = pt >> 5;
+        const bool ch = pt < DK;  // thread = channel
+        const int hq = h / (p.Hv / p.Hq);
+        const uint16_t *kp = p.k + t0 * p.ks + (int64_t)hq * DK + pt, *qp = p.q + t0 * p.qs + (int64_t)hq * DK + pt;
+        const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK + pt : h);
+        uint16_t kv[kC], qv[kC];
+        float gv[kC], bv = 0.f;
+        auto fetch = [&](int64_t c) {
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                const int64_t tok = c * kC + i;
+                const bool in = ch && tok < len;
+                kv[i] = in ? kp[tok * p.ks] : 0;
+                qv[i] = in ? qp[tok * p.qs] : 0;
+                gv[i] = in ? gp[tok * p.gs] : 0.f;
+            }
+            bv = pt < kC && c * kC + pt < len ? p.beta[(t0 + c * kC + pt) * p.bs + h] : 0.f;
+        };
+        for (int st = 0; st < 2; ++st)  // above the diagonal T and B stay zero
+            for (int i = pt; i < kC * kTS; i += kPrep) {
+                (&sm.stage[st].T[0][0])[i] = 0.f;
+                (&sm.stage[st].B[0][0])[i] = 0.f;
+            }
+        if (chunks)
+            fetch(0);
+        for (int64_t c = 0; c < chunks; ++c) {
+            const int st = (int)(c & 1);
+            ChunkStage<DK> &sg = sm.stage[st];
+            if (l2) {
+                // 32 sums over the channels: lane l of a warp gets token l % 16's, of k or q
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    const float a = __uint_as_float((uint32_t)kv[i] << 16), b = __uint_as_float((uint32_t)qv[i] << 16);
+                    v[i] = a * a;
+                    v[16 + i] = b * b;
+                }
+#pragma unroll
+                for (int n = 16; n; n >>= 1) {
+                    const bool up = (lane & n) != 0;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                        v[i] = keep + __shfl_xor_sync(~0u, send, n);
+                    }
+                }
+                sm.part[pw][lane] = v[0];
+                bar_sync(kBarPrep, kPrep);
+                if (pt < 32)
+                    sm.norm[pt] = (pt < 16 ? 1.f : p.scale) /
+                                  sqrtf((sm.part[0][pt] + sm.part[1][pt]) + (sm.part[2][pt] + sm.part[3][pt]) + 1e-6f);
+            } else if (pt < 32) {
+                sm.norm[pt] = pt < 16 ? 1.f : p.scale;
+            }
+            if (pt < kC)
+                sm.beta[pt] = bv;
+            bar_sync(kBarPrep, kPrep);
+            if (c >= 2)
+                bar_sync(kBarEmpty + st, kThreads);
+            if (ch) {
+                float P = 1.f, k[kC], a[kC];
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    k[i] = __uint_as_float((uint32_t)kv[i] << 16) * sm.norm[i];
+                    const float q = __uint_as_float((uint32_t)qv[i] << 16) * sm.norm[16 + i];
+                    a[i] = expf(gv[i]);
+                    P *= a[i];
+                    sm.k[i][pt] = k[i];
+                    sm.q[i][pt] = q;
+                    sm.a[i][pt] = a[i];
+                    sg.kp[i][pt] = k[i] * P;
+                    sg.qp[i][pt] = q * P;
+                }
+                sg.last[pt] = P;
+                float R = 1.f;
+#pragma unroll
+                for (int i = kC - 1; i >= 0; --i) {
+                    k[i] *= R;
+                    R *= a[i];
+                }
+#pragma unroll
+                for (int i = 0; i < kC; i += 4)
+                    *reinterpret_cast<float4 *>(&sg.kr[pt][i]) = make_float4(k[i], k[i + 1], k[i + 2], k[i + 3]);
+            }
+            bar_sync(kBarPrep, kPrep);
+            if (c + 1 < chunks)
+                fetch(c + 1);
+            // A and B: warp pw takes columns j = pw, 7 - pw, 8 + pw, 15 - pw; a lane DK / 32 channels
+            {
+                constexpr int CH = DK / 32;
+                const int js[4] = {pw, 7 - pw, 8 + pw, 15 - pw};
+                float w[4][CH] = {};
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    float a[CH], k[CH], q[CH];
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) {
+                        a[e] = sm.a[i][lane * CH + e];
+                        k[e] = sm.k[i][lane * CH + e];
+                        q[e] = sm.q[i][lane * CH + e];
+                    }
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float sa = 0.f, sb = 0.f;
+#pragma unroll
+                        for (int e = 0; e < CH; ++e) {
+                            w[j][e] *= a[e];
+                            sa = fmaf(k[e], w[j][e], sa);
+                            w[j][e] = i == js[j] ? k[e] : w[j][e];
+                            sb = fmaf(q[e], w[j][e], sb);
+                        }
+                        v[j] = sa;
+                        v[4 + j] = sb;
+                    }
+                    const float r = reduce8(v, lane);
+                    const int which = lane >> 2, j = which & 3;
+                    const int col = j == 0 ? js[0] : j == 1 ? js[1] : j == 2 ? js[2] : js[3];
+                    if ((lane & 3) == 0) {
+                        if (which < 4)
+                            sm.A[i][col] = r;  // zero for j >= i
+                        else if (col <= i)
+                            sg.B[i][col] = r;
+                    }
+                }
+            }
+            bar_sync(kBarPrep, kPrep);
+            if (pw == 0) {  // T: lane j solves (I + A) x = e_j, then times beta_j
+                const int j = lane & 15;
+                float x[kC];
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+                    for (int m = 0; m < i; ++m)
+                        (m & 1 ? d1 : d0) = fmaf(sm.A[i][m], x[m], m & 1 ? d1 : d0);
+                    x[i] = (i == j ? 1.f : 0.f) - sm.beta[i] * (d0 + d1);
+                }
+                const float b = sm.beta[j];
+                if (lane < 16)
+#pragma unroll
+                    for (int i = 0; i < kC; ++i)
+                        sg.T[i][j] = i >= j ? x[i] * b : 0.f;
+            }
+            bar_arrive(kBarFull + st, kThreads);
+        }
+    }
+}
+
+template <int DK, int MW>
+cudaError_t chunk_launch(const DeltaParams &p, cudaStream_t s)
+{
+    static std::atomic<uint64_t> devices{0};
+    cudaError_t e = set_smem_attr(delta_chunk_kernel<DK, MW>, devices);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t blocks = (int64_t)((p.Dv + 16 * MW - 1) / (16 * MW)) * p.Hv * p.n_seq;
+    if (blocks > INT32_MAX)
+        return cudaErrorInvalidConfiguration;
+    delta_chunk_kernel<DK, MW><<<(unsigned)blocks, kPrep + 32 * MW, sizeof(ChunkShared<DK>), s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DK>
+cudaError_t delta_launch(const DeltaParams &p, cudaStream_t s)
+{
+    if (p.tokens < 8ll * p.n_seq)
+        return recurrent_launch<DK>(p, s);
+    return chunk_launch<DK, 8>(p, s);
+}
+
 dep_status_t delta_entry(const dep_delta_args_t *a, void *stream)
 {
     if (!a || a->tokens < 0 || a->n_seq < 0 || a->n_states < 0 || a->Hq < 1 || a->Hv < 1 || a->Hv % a->Hq != 0 ||
@@ -249,7 +667,7 @@ dep_status_t delta_entry(const dep_delta_args_t *a, void *stream)
     p.flags = a->flags;
     p.scale = a->scale;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = a->Dk == 128 ? recurrent_launch<128>(p, s) : recurrent_launch<64>(p, s);
+    const cudaError_t e = a->Dk == 128 ? delta_launch<128>(p, s) : delta_launch<64>(p, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return e == cudaErrorInvalidConfiguration ? DEP_ERR_UNSUPPORTED : DEP_ERR_CUDA;
