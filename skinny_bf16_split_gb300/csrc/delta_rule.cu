@@ -264,29 +264,25 @@ struct ChunkStage {
 };
 template <int DK>
 struct ChunkShared {
+    static constexpr int KS = DK + 8;
     ChunkStage<DK> stage[2];
-    float k[kC][DK], q[kC][DK], a[kC][DK];  // normalised rows and decays of the chunk in preparation
+    struct {  // operands of the products of one level (see below): rows k_i then q_i, columns k_j
+        float row[16][KS], col[8][KS];
+    } level[4];
+    struct {  // the next chunks' tokens as they are
+        float g[kC][DK];
+        uint16_t k[kC][DK], q[kC][DK];
+    } raw[2];
     float A[kC][kC];
-    float part[4][32], norm[32], beta[kC];
+    float part[4][48], norm[4][48], beta[kC], g[kC];
     uint4 out[8][kC][2];  // a warp's rows of O, [token][16 rows in BF16]
 };
 
-// Sum of v over the warp's lanes, for eight values: lane l returns the sum of v[l >> 2].
-__device__ __forceinline__ float reduce8(float (&v)[8], int lane)
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
 {
-#pragma unroll
-    for (int n = 4, bit = 16; n; n >>= 1, bit >>= 1) {
-        const bool up = (lane & bit) != 0;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-            v[i] = keep + __shfl_xor_sync(~0u, send, bit);
-        }
-    }
-    float r = v[0];
-    r += __shfl_xor_sync(~0u, r, 2);
-    r += __shfl_xor_sync(~0u, r, 1);
-    return r;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
 }
 
 template <int DK, int MW>
@@ -436,42 +432,77 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
             }
     } else {
         // ---------------- the next chunk's operands ----------------
+        // A and B from matrix products, level by level.  At level b (1, 2, 4, 8) token i, whose
+        // bit b is set, is a row and meets the columns j that share its bits above b and have
+        // that bit clear: M_ij is the product of the decays from the row's group of b tokens
+        // on up to i, times that of the decays after j up to the group's end.  Every pair j < i
+        // meets at one level, the highest bit in which the two differ.
         const int pt = threadIdx.x - 32 * MW, pw = pt >> 5;
         const bool ch = pt < DK;  // thread = channel
         const int hq = h / (p.Hv / p.Hq);
-        const uint16_t *kp = p.k + t0 * p.ks + (int64_t)hq * DK + pt, *qp = p.q + t0 * p.qs + (int64_t)hq * DK + pt;
-        const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK + pt : h);
-        uint16_t kv[kC], qv[kC];
-        float gv[kC], bv = 0.f;
+        const uint16_t *kp = p.k + t0 * p.ks + (int64_t)hq * DK, *qp = p.q + t0 * p.qs + (int64_t)hq * DK;
+        const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK : h);
+        float bv = 0.f, gv = 0.f;  // of token pt
         auto fetch = [&](int64_t c) {
+            auto &raw = sm.raw[c & 1];
+            const int64_t first = c * kC;
+            const int left = (int)(len - first < kC ? len - first : kC);
+            constexpr int QC = DK / 8, GC = DK / 4;  // 16-byte pieces of a token
 #pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                const int64_t tok = c * kC + i;
-                const bool in = ch && tok < len;
-                kv[i] = in ? kp[tok * p.ks] : 0;
-                qv[i] = in ? qp[tok * p.qs] : 0;
-                gv[i] = in ? gp[tok * p.gs] : 0.f;
+            for (int i = pt; i < kC * QC; i += kPrep) {
+                const int tok = i / QC, e = i % QC * 8;
+                const int64_t at = first + (tok < left ? tok : 0);
+                cp_async16(&raw.k[tok][e], kp + at * p.ks + e, tok < left);
+                cp_async16(&raw.q[tok][e], qp + at * p.qs + e, tok < left);
             }
-            bv = pt < kC && c * kC + pt < len ? p.beta[(t0 + c * kC + pt) * p.bs + h] : 0.f;
+            if (chan)
+#pragma unroll
+                for (int i = pt; i < kC * GC; i += kPrep) {
+                    const int tok = i / GC, e = i % GC * 4;
+                    cp_async16(&raw.g[tok][e], gp + (first + (tok < left ? tok : 0)) * p.gs + e, tok < left);
+                }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (pt < kC) {
+                bv = pt < left ? p.beta[(t0 + first + pt) * p.bs + h] : 0.f;
+                gv = !chan && pt < left ? gp[(first + pt) * p.gs] : 0.f;
+            }
         };
         for (int st = 0; st < 2; ++st)  // above the diagonal T and B stay zero
             for (int i = pt; i < kC * kTS; i += kPrep) {
                 (&sm.stage[st].T[0][0])[i] = 0.f;
                 (&sm.stage[st].B[0][0])[i] = 0.f;
             }
+        for (int i = pt; i < kC * kC; i += kPrep)
+            (&sm.A[0][0])[i] = 0.f;
         if (chunks)
             fetch(0);
         for (int64_t c = 0; c < chunks; ++c) {
             const int st = (int)(c & 1);
             ChunkStage<DK> &sg = sm.stage[st];
-            if (l2) {
-                // 32 sums over the channels: lane l of a warp gets token l % 16's, of k or q
-                float v[32];
+            const auto &raw = sm.raw[c & 1];
+            if (pt < kC) {
+                sm.beta[pt] = bv;
+                sm.g[pt] = gv;
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            bar_sync(kBarPrep, kPrep);
+            if (c + 1 < chunks)
+                fetch(c + 1);
+            float k[kC], q[kC], a[kC];
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                k[i] = ch ? __uint_as_float((uint32_t)raw.k[i][pt] << 16) : 0.f;
+                q[i] = ch ? __uint_as_float((uint32_t)raw.q[i][pt] << 16) : 0.f;
+                a[i] = expf(!chan ? sm.g[i] : ch ? raw.g[i][pt] : 0.f);
+            }
+            {
+                // Sums over the channels: lane l of a warp gets token l % 16's, of k k or q q, and of k q
+                float v[32], w[16];
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
-                    const float a = __uint_as_float((uint32_t)kv[i] << 16), b = __uint_as_float((uint32_t)qv[i] << 16);
-                    v[i] = a * a;
-                    v[16 + i] = b * b;
+                    v[i] = k[i] * k[i];
+                    v[16 + i] = q[i] * q[i];
+                    w[i] = k[i] * q[i];
                 }
 #pragma unroll
                 for (int n = 16; n; n >>= 1) {
@@ -482,34 +513,64 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
                         v[i] = keep + __shfl_xor_sync(~0u, send, n);
                     }
                 }
+#pragma unroll
+                for (int n = 8; n; n >>= 1) {
+                    const bool up = (lane & n) != 0;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float send = up ? w[i] : w[i + n], keep = up ? w[i + n] : w[i];
+                        w[i] = keep + __shfl_xor_sync(~0u, send, n);
+                    }
+                }
+                w[0] += __shfl_xor_sync(~0u, w[0], 16);
                 sm.part[pw][lane] = v[0];
+                if (lane < 16)
+                    sm.part[pw][32 + lane] = w[0];
                 bar_sync(kBarPrep, kPrep);
-                if (pt < 32)
-                    sm.norm[pt] = (pt < 16 ? 1.f : p.scale) /
-                                  sqrtf((sm.part[0][pt] + sm.part[1][pt]) + (sm.part[2][pt] + sm.part[3][pt]) + 1e-6f);
-            } else if (pt < 32) {
-                sm.norm[pt] = pt < 16 ? 1.f : p.scale;
+                // every warp finishes the sums for itself
+                const float sum = (sm.part[0][lane] + sm.part[1][lane]) + (sm.part[2][lane] + sm.part[3][lane]);
+                sm.norm[pw][lane] = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
+                if (lane < 16)
+                    sm.norm[pw][32 + lane] = (sm.part[0][32 + lane] + sm.part[1][32 + lane]) +
+                                             (sm.part[2][32 + lane] + sm.part[3][32 + lane]);
+                __syncwarp();
             }
-            if (pt < kC)
-                sm.beta[pt] = bv;
-            bar_sync(kBarPrep, kPrep);
             if (c >= 2)
                 bar_sync(kBarEmpty + st, kThreads);
+            if (pt < kC)
+                sg.B[pt][pt] = sm.norm[pw][32 + pt] * sm.norm[pw][pt] * sm.norm[pw][16 + pt];
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                k[i] *= sm.norm[pw][i];
+                q[i] *= sm.norm[pw][16 + i];
+            }
             if (ch) {
-                float P = 1.f, k[kC], a[kC];
+                float P = 1.f;
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
-                    k[i] = __uint_as_float((uint32_t)kv[i] << 16) * sm.norm[i];
-                    const float q = __uint_as_float((uint32_t)qv[i] << 16) * sm.norm[16 + i];
-                    a[i] = expf(gv[i]);
                     P *= a[i];
-                    sm.k[i][pt] = k[i];
-                    sm.q[i][pt] = q;
-                    sm.a[i][pt] = a[i];
                     sg.kp[i][pt] = k[i] * P;
-                    sg.qp[i][pt] = q * P;
+                    sg.qp[i][pt] = q[i] * P;
                 }
                 sg.last[pt] = P;
+#pragma unroll
+                for (int l = 0; l < 4; ++l) {
+                    const int b = 1 << l;
+                    float f = 1.f;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const int i = (r & ~(b - 1)) << 1 | b | (r & (b - 1));
+                        f = i % b == 0 ? a[i] : f * a[i];
+                        sm.level[l].row[r][pt] = k[i] * f;
+                        sm.level[l].row[8 + r][pt] = q[i] * f;
+                    }
+#pragma unroll
+                    for (int n = 7; n >= 0; --n) {
+                        const int j = (n & ~(b - 1)) << 1 | (n & (b - 1));
+                        f = j % b == b - 1 ? 1.f : f * a[j + 1];
+                        sm.level[l].col[n][pt] = k[j] * f;
+                    }
+                }
                 float R = 1.f;
 #pragma unroll
                 for (int i = kC - 1; i >= 0; --i) {
@@ -521,44 +582,27 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
                     *reinterpret_cast<float4 *>(&sg.kr[pt][i]) = make_float4(k[i], k[i + 1], k[i + 2], k[i + 3]);
             }
             bar_sync(kBarPrep, kPrep);
-            if (c + 1 < chunks)
-                fetch(c + 1);
-            // A and B: warp pw takes columns j = pw, 7 - pw, 8 + pw, 15 - pw; a lane DK / 32 channels
-            {
-                constexpr int CH = DK / 32;
-                const int js[4] = {pw, 7 - pw, 8 + pw, 15 - pw};
-                float w[4][CH] = {};
+            {  // warp pw: level pw
+                const int g = lane >> 2, t = lane & 3, b = 1 << pw;
+                const auto &lv = sm.level[pw];
+                float d[2][4] = {};
 #pragma unroll
-                for (int i = 0; i < kC; ++i) {
-                    float a[CH], k[CH], q[CH];
+                for (int ks = 0; ks < DK / 8; ++ks) {
+                    const float2 lo = *reinterpret_cast<const float2 *>(&lv.row[g][8 * ks + 2 * t]);
+                    const float2 hi = *reinterpret_cast<const float2 *>(&lv.row[g + 8][8 * ks + 2 * t]);
+                    const float2 cb = *reinterpret_cast<const float2 *>(&lv.col[g][8 * ks + 2 * t]);
+                    const float c4[4] = {lo.x, lo.y, hi.x, hi.y};
+                    uint32_t ah[4], al[4];
+                    split_a(c4, ah, al);
+                    mma_tf32x3(d[ks & 1], ah, al, cb);
+                }
+                const int i = (g & ~(b - 1)) << 1 | b | (g & (b - 1));
 #pragma unroll
-                    for (int e = 0; e < CH; ++e) {
-                        a[e] = sm.a[i][lane * CH + e];
-                        k[e] = sm.k[i][lane * CH + e];
-                        q[e] = sm.q[i][lane * CH + e];
-                    }
-                    float v[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float sa = 0.f, sb = 0.f;
-#pragma unroll
-                        for (int e = 0; e < CH; ++e) {
-                            w[j][e] *= a[e];
-                            sa = fmaf(k[e], w[j][e], sa);
-                            w[j][e] = i == js[j] ? k[e] : w[j][e];
-                            sb = fmaf(q[e], w[j][e], sb);
-                        }
-                        v[j] = sa;
-                        v[4 + j] = sb;
-                    }
-                    const float r = reduce8(v, lane);
-                    const int which = lane >> 2, j = which & 3;
-                    const int col = j == 0 ? js[0] : j == 1 ? js[1] : j == 2 ? js[2] : js[3];
-                    if ((lane & 3) == 0) {
-                        if (which < 4)
-                            sm.A[i][col] = r;  // zero for j >= i
-                        else if (col <= i)
-                            sg.B[i][col] = r;
+                for (int e = 0; e < 2; ++e) {
+                    const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
+                    if ((n & ~(b - 1)) == (g & ~(b - 1))) {
+                        sm.A[i][j] = d[0][e] + d[1][e];
+                        sg.B[i][j] = d[0][2 + e] + d[1][2 + e];
                     }
                 }
             }
