@@ -21,9 +21,9 @@
 // A block takes up to 128 rows of one head's state.  Its first warps hold 16 rows of S
 // each, as the accumulator of the last product, for the whole sequence: an accumulator
 // fragment is also a left operand of the next product (with the channels in another
-// order, the same on both sides), so S, U and the rest never leave the registers.  Four
-// more warps prepare the next chunk meanwhile: norms, decays, A, B and T, and K.P, Q.P,
-// K.R in two shared-memory stages.
+// order, the same on both sides), so S, U and the rest never leave the registers.  Two
+// more groups of four warps prepare the chunks to come, in turn: norms, decays, A, B and
+// T, and K.P, Q.P, K.R, each group in a shared-memory stage of its own.
 // FP32 operands are split into two TF32 parts, and three products are kept (the fourth is
 // below 2^-22): everything keeps FP32's precision, or nearly.
 #include <cuda_bf16.h>
@@ -208,7 +208,7 @@ cudaError_t recurrent_launch(const DeltaParams &p, cudaStream_t s)
 // chunked kernel
 
 constexpr int kC = 16;            // tokens of a chunk
-constexpr int kPrep = 128;        // preparing threads
+constexpr int kPrep = 128;        // threads that prepare a chunk; two such groups take turns
 constexpr int kTS = 24;           // row stride of 16-wide matrices in shared memory: float2 reads without conflicts
 
 // Barrier `id` of the block's hardware barriers, for n threads.
@@ -218,23 +218,20 @@ __device__ __forceinline__ void bar_arrive(int id, int n)
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ uint32_t tf32_hi(float v)
-{
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-    return r;
-}
+// v = hi + lo, hi rounded to TF32's 11 bits (half away from zero) by integer arithmetic: the
+// conversion instruction runs at an eighth of its rate.  The MMA ignores what lo has below 11 bits.
+// A NaN may leave hi, but not lo.
 __device__ __forceinline__ void tf32_split(float v, uint32_t &hi, uint32_t &lo)
 {
-    hi = tf32_hi(v);
+    hi = (__float_as_uint(v) + 0x1000u) & 0xFFFFE000u;
     lo = __float_as_uint(v - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // The accumulator fragment c as a left operand: its columns 2t and 2t + 1 become k = t and t + 4.
 __device__ __forceinline__ void split_a(const float (&c)[4], uint32_t (&hi)[4], uint32_t (&lo)[4])
@@ -244,15 +241,29 @@ __device__ __forceinline__ void split_a(const float (&c)[4], uint32_t (&hi)[4], 
     tf32_split(c[1], hi[2], lo[2]);
     tf32_split(c[3], hi[3], lo[3]);
 }
-__device__ __forceinline__ void mma_tf32x3(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float2 b)
+// N products d[n] += a b[n], each as three: the small ones first, and those of one d N MMAs
+// apart (an MMA takes 24 cycles, a warp issues one in 8).
+template <int N>
+__device__ __forceinline__ void mma_tf32x3(float (*const (&d)[N])[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                           const float2 (&b)[N])
 {
-    uint32_t h0, l0, h1, l1;
-    tf32_split(b.x, h0, l0);
-    tf32_split(b.y, h1, l1);
-    mma_tf32(d, al, h0, h1);
-    mma_tf32(d, ah, l0, l1);
-    mma_tf32(d, ah, h0, h1);
+    uint32_t h[N][2], l[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        tf32_split(b[n].x, h[n][0], l[n][0]);
+        tf32_split(b[n].y, h[n][1], l[n][1]);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        mma_tf32(*d[n], al, h[n][0], h[n][1]);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        mma_tf32(*d[n], ah, l[n][0], l[n][1]);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        mma_tf32(*d[n], ah, h[n][0], h[n][1]);
 }
+__device__ __forceinline__ float2 ld2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
 template <int DK>
 struct ChunkStage {
@@ -266,15 +277,17 @@ template <int DK>
 struct ChunkShared {
     static constexpr int KS = DK + 8;
     ChunkStage<DK> stage[2];
-    struct {  // operands of the products of one level (see below): rows k_i then q_i, columns k_j
-        float row[16][KS], col[8][KS];
-    } level[4];
-    struct {  // the next chunks' tokens as they are
-        float g[kC][DK];
-        uint16_t k[kC][DK], q[kC][DK];
-    } raw[2];
-    float A[kC][kC];
-    float part[4][48], norm[4][48], beta[kC], g[kC];
+    struct {  // scratch of each group of preparing warps
+        struct {  // operands of the products of one level (see below): rows k_i then q_i, columns k_j
+            float row[16][KS], col[8][KS];
+        } level[4];
+        struct {  // a chunk's tokens as they are
+            float g[kC][DK];
+            uint16_t k[kC][DK], q[kC][DK];
+        } raw;
+        float A[kC][kC];
+        float part[4][48], norm[4][48], beta[kC], g[kC];
+    } prep[2];
     uint4 out[8][kC][2];  // a warp's rows of O, [token][16 rows in BF16]
 };
 
@@ -286,11 +299,12 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
 }
 
 template <int DK, int MW>
-__global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const DeltaParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     ChunkShared<DK> &sm = *reinterpret_cast<ChunkShared<DK> *>(smem_raw);
-    constexpr int kThreads = kPrep + 32 * MW, kBarPrep = 1, kBarFull = 2, kBarEmpty = 4;
+    constexpr int kThreads = kPrep + 32 * MW;  // that meet over a stage: its group, and the state's warps
+    constexpr int kBarFull = 2, kBarEmpty = 4;
     const int slices = (p.Dv + 16 * MW - 1) / (16 * MW);
     const int slice = blockIdx.x % slices, sh = blockIdx.x / slices;
     const int h = sh % p.Hv, s = sh / p.Hv;
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
 
     if (pad) {  // zeros out, no state
         const int rows = p.Dv - slice * 16 * MW < 16 * MW ? p.Dv - slice * 16 * MW : 16 * MW;
-        for (int64_t i = threadIdx.x; i < len * rows; i += kThreads)
+        for (int64_t i = threadIdx.x; i < len * rows; i += blockDim.x)
             p.o[(t0 + i / rows) * p.os + (int64_t)h * p.Dv + slice * 16 * MW + i % rows] = 0;
         return;
     }
@@ -330,18 +344,20 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
         }
         const uint16_t *vp = p.v + t0 * p.vs + (int64_t)h * p.Dv + row0 + g;
         // V^T in accumulator layout: rows g and g + 8, tokens 8 n + 2 t and + 1
-        auto load_v = [&](int64_t c, uint16_t (&v)[2][4]) {
+        auto load_v = [&](int c, uint32_t (&v)[2][2]) {
+            const int left = live ? (int)(len - (int64_t)c * kC < kC ? len - (int64_t)c * kC : kC) : 0;
+            const uint16_t *at = vp + (int64_t)c * kC * p.vs;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int64_t tok = c * kC + 8 * n + 2 * t + j;
-                    const bool in = live && tok < len;
-                    v[n][j] = in ? vp[tok * p.vs] : 0;
-                    v[n][2 + j] = in ? vp[tok * p.vs + 8] : 0;
-                }
+            for (int n = 0; n < 2; ++n) {
+                const int a = 8 * n + 2 * t, b = a + 1;
+                const uint16_t *pa = at + a * p.vs, *pb = pa + p.vs;
+                const uint32_t lo0 = a < left ? pa[0] : 0, lo1 = a < left ? pa[8] : 0, hi0 = b < left ? pb[0] : 0,
+                               hi1 = b < left ? pb[8] : 0;
+                v[n][0] = lo0 | hi0 << 16;
+                v[n][1] = lo1 | hi1 << 16;
+            }
         };
-        uint16_t v[2][4];
+        uint32_t v[2][2];
         if (chunks)
             load_v(0, v);
         for (int64_t c = 0; c < chunks; ++c) {
@@ -353,53 +369,59 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
             for (int ks = 0; ks < NT; ++ks) {
                 uint32_t ah[4], al[4];
                 split_a(S[ks], ah, al);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 kb = *reinterpret_cast<const float2 *>(&sg.kp[8 * n + g][8 * ks + 2 * t]);
-                    const float2 qb = *reinterpret_cast<const float2 *>(&sg.qp[8 * n + g][8 * ks + 2 * t]);
-                    mma_tf32x3(X[n], ah, al, kb);
-                    mma_tf32x3(O[n], ah, al, qb);
-                }
+                float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
+                const float2 b[4] = {ld2(&sg.kp[g][8 * ks + 2 * t]), ld2(&sg.qp[g][8 * ks + 2 * t]),
+                                     ld2(&sg.kp[8 + g][8 * ks + 2 * t]), ld2(&sg.qp[8 + g][8 * ks + 2 * t])};
+                mma_tf32x3(d, ah, al, b);
             }
             // Y = V - X, then U^T = Y^T T^T and O^T += U^T B^T (both lower triangular: tokens j <= i)
-            uint32_t yh[2][4], yl[2][4];
+            uint32_t uh[2][4], ul[2][4];
+            float U[2][4] = {};
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    X[n][j] = __uint_as_float((uint32_t)v[n][j] << 16) - X[n][j];
-                split_a(X[n], yh[n], yl[n]);
+                    X[n][j] = __uint_as_float(j & 1 ? v[n][j >> 1] & 0xFFFF0000u : v[n][j >> 1] << 16) - X[n][j];
+                split_a(X[n], uh[n], ul[n]);
             }
             if (c + 1 < chunks)
-                load_v(c + 1, v);
-            float U[2][4] = {};
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int ks = 0; ks <= n; ++ks)
-                    mma_tf32x3(U[n], yh[ks], yl[ks],
-                               *reinterpret_cast<const float2 *>(&sg.T[8 * n + g][8 * ks + 2 * t]));
-            uint32_t uh[2][4], ul[2][4];
+                load_v((int)c + 1, v);
+            {
+                float(*const d[2])[4] = {&U[0], &U[1]};
+                const float2 b[2] = {ld2(&sg.T[g][2 * t]), ld2(&sg.T[8 + g][2 * t])};
+                mma_tf32x3(d, uh[0], ul[0], b);
+                float(*const d1[1])[4] = {&U[1]};
+                const float2 b1[1] = {ld2(&sg.T[8 + g][8 + 2 * t])};
+                mma_tf32x3(d1, uh[1], ul[1], b1);
+            }
             split_a(U[0], uh[0], ul[0]);
             split_a(U[1], uh[1], ul[1]);
+            {
+                float(*const d[2])[4] = {&O[0], &O[1]};
+                const float2 b[2] = {ld2(&sg.B[g][2 * t]), ld2(&sg.B[8 + g][2 * t])};
+                mma_tf32x3(d, uh[0], ul[0], b);
+                float(*const d1[1])[4] = {&O[1]};
+                const float2 b1[1] = {ld2(&sg.B[8 + g][8 + 2 * t])};
+                mma_tf32x3(d1, uh[1], ul[1], b1);
+            }
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT; n += 4) {
+                float(*const d[4])[4] = {&S[n], &S[n + 1], &S[n + 2], &S[n + 3]};
 #pragma unroll
-                for (int ks = 0; ks <= n; ++ks) {
-                    const float2 b = *reinterpret_cast<const float2 *>(&sg.B[8 * n + g][8 * ks + 2 * t]);
-                    mma_tf32x3(O[n], uh[ks], ul[ks], b);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
+                    S[n + i][0] *= a.x;
+                    S[n + i][1] *= a.y;
+                    S[n + i][2] *= a.x;
+                    S[n + i][3] *= a.y;
                 }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 a = *reinterpret_cast<const float2 *>(&sg.last[8 * n + 2 * t]);
-                S[n][0] *= a.x;
-                S[n][1] *= a.y;
-                S[n][2] *= a.x;
-                S[n][3] *= a.y;
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-                    mma_tf32x3(S[n], uh[ks], ul[ks],
-                               *reinterpret_cast<const float2 *>(&sg.kr[8 * n + g][8 * ks + 2 * t]));
+                for (int ks = 0; ks < 2; ++ks) {
+                    const float2 b[4] = {ld2(&sg.kr[8 * n + g][8 * ks + 2 * t]), ld2(&sg.kr[8 * n + 8 + g][8 * ks + 2 * t]),
+                                         ld2(&sg.kr[8 * n + 16 + g][8 * ks + 2 * t]),
+                                         ld2(&sg.kr[8 * n + 24 + g][8 * ks + 2 * t])};
+                    mma_tf32x3(d, uh[ks], ul[ks], b);
+                }
             }
             if (c + 2 < chunks)
                 bar_arrive(kBarEmpty + st, kThreads);
@@ -437,14 +459,16 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
         // that bit clear: M_ij is the product of the decays from the row's group of b tokens
         // on up to i, times that of the decays after j up to the group's end.  Every pair j < i
         // meets at one level, the highest bit in which the two differ.
-        const int pt = threadIdx.x - 32 * MW, pw = pt >> 5;
+        const int grp = (threadIdx.x - 32 * MW) / kPrep, pt = (threadIdx.x - 32 * MW) % kPrep, pw = pt >> 5;
+        const int kBarPrep = 6 + grp;
+        auto &pr = sm.prep[grp];
         const bool ch = pt < DK;  // thread = channel
         const int hq = h / (p.Hv / p.Hq);
         const uint16_t *kp = p.k + t0 * p.ks + (int64_t)hq * DK, *qp = p.q + t0 * p.qs + (int64_t)hq * DK;
         const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK : h);
         float bv = 0.f, gv = 0.f;  // of token pt
         auto fetch = [&](int64_t c) {
-            auto &raw = sm.raw[c & 1];
+            auto &raw = pr.raw;
             const int64_t first = c * kC;
             const int left = (int)(len - first < kC ? len - first : kC);
             constexpr int QC = DK / 8, GC = DK / 4;  // 16-byte pieces of a token
@@ -467,33 +491,29 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
                 gv = !chan && pt < left ? gp[(first + pt) * p.gs] : 0.f;
             }
         };
-        for (int st = 0; st < 2; ++st)  // above the diagonal T and B stay zero
-            for (int i = pt; i < kC * kTS; i += kPrep) {
-                (&sm.stage[st].T[0][0])[i] = 0.f;
-                (&sm.stage[st].B[0][0])[i] = 0.f;
-            }
+        ChunkStage<DK> &sg = sm.stage[grp];
+        for (int i = pt; i < kC * kTS; i += kPrep) {  // above the diagonal T and B stay zero
+            (&sg.T[0][0])[i] = 0.f;
+            (&sg.B[0][0])[i] = 0.f;
+        }
         for (int i = pt; i < kC * kC; i += kPrep)
-            (&sm.A[0][0])[i] = 0.f;
-        if (chunks)
-            fetch(0);
-        for (int64_t c = 0; c < chunks; ++c) {
-            const int st = (int)(c & 1);
-            ChunkStage<DK> &sg = sm.stage[st];
-            const auto &raw = sm.raw[c & 1];
+            (&pr.A[0][0])[i] = 0.f;
+        if (grp < chunks)
+            fetch(grp);
+        for (int64_t c = grp; c < chunks; c += 2) {
+            const auto &raw = pr.raw;
             if (pt < kC) {
-                sm.beta[pt] = bv;
-                sm.g[pt] = gv;
+                pr.beta[pt] = bv;
+                pr.g[pt] = gv;
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             bar_sync(kBarPrep, kPrep);
-            if (c + 1 < chunks)
-                fetch(c + 1);
             float k[kC], q[kC], a[kC];
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
                 k[i] = ch ? __uint_as_float((uint32_t)raw.k[i][pt] << 16) : 0.f;
                 q[i] = ch ? __uint_as_float((uint32_t)raw.q[i][pt] << 16) : 0.f;
-                a[i] = expf(!chan ? sm.g[i] : ch ? raw.g[i][pt] : 0.f);
+                a[i] = expf(!chan ? pr.g[i] : ch ? raw.g[i][pt] : 0.f);
             }
             {
                 // Sums over the channels: lane l of a warp gets token l % 16's, of k k or q q, and of k q
@@ -523,26 +543,28 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
                     }
                 }
                 w[0] += __shfl_xor_sync(~0u, w[0], 16);
-                sm.part[pw][lane] = v[0];
+                pr.part[pw][lane] = v[0];
                 if (lane < 16)
-                    sm.part[pw][32 + lane] = w[0];
+                    pr.part[pw][32 + lane] = w[0];
                 bar_sync(kBarPrep, kPrep);
+                if (c + 2 < chunks)
+                    fetch(c + 2);
                 // every warp finishes the sums for itself
-                const float sum = (sm.part[0][lane] + sm.part[1][lane]) + (sm.part[2][lane] + sm.part[3][lane]);
-                sm.norm[pw][lane] = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
+                const float sum = (pr.part[0][lane] + pr.part[1][lane]) + (pr.part[2][lane] + pr.part[3][lane]);
+                pr.norm[pw][lane] = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
                 if (lane < 16)
-                    sm.norm[pw][32 + lane] = (sm.part[0][32 + lane] + sm.part[1][32 + lane]) +
-                                             (sm.part[2][32 + lane] + sm.part[3][32 + lane]);
+                    pr.norm[pw][32 + lane] = (pr.part[0][32 + lane] + pr.part[1][32 + lane]) +
+                                             (pr.part[2][32 + lane] + pr.part[3][32 + lane]);
                 __syncwarp();
             }
             if (c >= 2)
-                bar_sync(kBarEmpty + st, kThreads);
+                bar_sync(kBarEmpty + grp, kThreads);
             if (pt < kC)
-                sg.B[pt][pt] = sm.norm[pw][32 + pt] * sm.norm[pw][pt] * sm.norm[pw][16 + pt];
+                sg.B[pt][pt] = pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt];
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
-                k[i] *= sm.norm[pw][i];
-                q[i] *= sm.norm[pw][16 + i];
+                k[i] *= pr.norm[pw][i];
+                q[i] *= pr.norm[pw][16 + i];
             }
             if (ch) {
                 float P = 1.f;
@@ -561,14 +583,14 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
                     for (int r = 0; r < 8; ++r) {
                         const int i = (r & ~(b - 1)) << 1 | b | (r & (b - 1));
                         f = i % b == 0 ? a[i] : f * a[i];
-                        sm.level[l].row[r][pt] = k[i] * f;
-                        sm.level[l].row[8 + r][pt] = q[i] * f;
+                        pr.level[l].row[r][pt] = k[i] * f;
+                        pr.level[l].row[8 + r][pt] = q[i] * f;
                     }
 #pragma unroll
                     for (int n = 7; n >= 0; --n) {
                         const int j = (n & ~(b - 1)) << 1 | (n & (b - 1));
                         f = j % b == b - 1 ? 1.f : f * a[j + 1];
-                        sm.level[l].col[n][pt] = k[j] * f;
+                        pr.level[l].col[n][pt] = k[j] * f;
                     }
                 }
                 float R = 1.f;
@@ -584,7 +606,7 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
             bar_sync(kBarPrep, kPrep);
             {  // warp pw: level pw
                 const int g = lane >> 2, t = lane & 3, b = 1 << pw;
-                const auto &lv = sm.level[pw];
+                const auto &lv = pr.level[pw];
                 float d[2][4] = {};
 #pragma unroll
                 for (int ks = 0; ks < DK / 8; ++ks) {
@@ -594,14 +616,16 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
                     const float c4[4] = {lo.x, lo.y, hi.x, hi.y};
                     uint32_t ah[4], al[4];
                     split_a(c4, ah, al);
-                    mma_tf32x3(d[ks & 1], ah, al, cb);
+                    float(*const dd[1])[4] = {&d[ks & 1]};
+                    const float2 b1[1] = {cb};
+                    mma_tf32x3(dd, ah, al, b1);
                 }
                 const int i = (g & ~(b - 1)) << 1 | b | (g & (b - 1));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
                     if ((n & ~(b - 1)) == (g & ~(b - 1))) {
-                        sm.A[i][j] = d[0][e] + d[1][e];
+                        pr.A[i][j] = d[0][e] + d[1][e];
                         sg.B[i][j] = d[0][2 + e] + d[1][2 + e];
                     }
                 }
@@ -615,16 +639,16 @@ __global__ void __launch_bounds__(kPrep + 32 * MW) delta_chunk_kernel(const Delt
                     float d0 = 0.f, d1 = 0.f;
 #pragma unroll
                     for (int m = 0; m < i; ++m)
-                        (m & 1 ? d1 : d0) = fmaf(sm.A[i][m], x[m], m & 1 ? d1 : d0);
-                    x[i] = (i == j ? 1.f : 0.f) - sm.beta[i] * (d0 + d1);
+                        (m & 1 ? d1 : d0) = fmaf(pr.A[i][m], x[m], m & 1 ? d1 : d0);
+                    x[i] = (i == j ? 1.f : 0.f) - pr.beta[i] * (d0 + d1);
                 }
-                const float b = sm.beta[j];
+                const float b = pr.beta[j];
                 if (lane < 16)
 #pragma unroll
                     for (int i = 0; i < kC; ++i)
                         sg.T[i][j] = i >= j ? x[i] * b : 0.f;
             }
-            bar_arrive(kBarFull + st, kThreads);
+            bar_arrive(kBarFull + grp, kThreads);
         }
     }
 }
@@ -639,7 +663,7 @@ cudaError_t chunk_launch(const DeltaParams &p, cudaStream_t s)
     const int64_t blocks = (int64_t)((p.Dv + 16 * MW - 1) / (16 * MW)) * p.Hv * p.n_seq;
     if (blocks > INT32_MAX)
         return cudaErrorInvalidConfiguration;
-    delta_chunk_kernel<DK, MW><<<(unsigned)blocks, kPrep + 32 * MW, sizeof(ChunkShared<DK>), s>>>(p);
+    delta_chunk_kernel<DK, MW><<<(unsigned)blocks, 2 * kPrep + 32 * MW, sizeof(ChunkShared<DK>), s>>>(p);
     return cudaGetLastError();
 }
 
