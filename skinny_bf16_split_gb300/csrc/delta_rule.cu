@@ -265,6 +265,34 @@ __device__ __forceinline__ void mma_tf32x3(float (*const (&d)[N])[4], const uint
 }
 __device__ __forceinline__ float2 ld2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
+constexpr int kSort = 256;
+
+// The sequence of rank r by length, longest first: blocks start in order, and a long
+// sequence that starts last leaves the other SMs idle.  Tables of more than kSort
+// sequences are taken as they are.
+__device__ __forceinline__ int longest_first(const DeltaParams &p, int r, int (&len)[kSort + 1])
+{
+    const int n = p.n_seq, t = threadIdx.x;
+    if (!p.cu || n < 2 || n > kSort)
+        return r;
+    int mine = 0;
+    if (t < n) {
+        int64_t t0, t1;
+        seq_range(p, t, t0, t1);
+        len[t] = mine = (int)(t1 - t0);
+    }
+    __syncthreads();
+    if (t < n) {
+        int rank = 0;
+        for (int j = 0; j < n; ++j)
+            rank += len[j] > mine || (len[j] == mine && j < t);
+        if (rank == r)
+            len[kSort] = t;
+    }
+    __syncthreads();
+    return len[kSort];
+}
+
 template <int DK>
 struct ChunkStage {
     static constexpr int KS = DK + 8;  // row stride of K.P and Q.P: float2 reads without conflicts
@@ -288,6 +316,7 @@ struct ChunkShared {
         float A[kC][kC];
         float part[4][48], norm[4][48], beta[kC], g[kC];
     } prep[2];
+    int order[kSort + 1];
     uint4 out[8][kC][2];  // a warp's rows of O, [token][16 rows in BF16]
 };
 
@@ -307,7 +336,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
     constexpr int kBarFull = 2, kBarEmpty = 4;
     const int slices = (p.Dv + 16 * MW - 1) / (16 * MW);
     const int slice = blockIdx.x % slices, sh = blockIdx.x / slices;
-    const int h = sh % p.Hv, s = sh / p.Hv;
+    const int h = sh % p.Hv, s = longest_first(p, sh / p.Hv, sm.order);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t t0, t1;
     seq_range(p, s, t0, t1);
