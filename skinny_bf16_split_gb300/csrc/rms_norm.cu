@@ -52,12 +52,46 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// Rows that are not aligned, or not whole vectors (VEC false).  Eight elements that start
+// m elements past an aligned granule lie in two granules: they are loaded as those two and
+// shifted, and a lane stores the granule its elements start in, whose first m elements come
+// from the lane before.  What granules at the ends of a warp or row would take from outside
+// goes element by element.
+
+// Words [s / 2, s / 2 + 4) (in 16-bit steps s <= 8) of the eight words a, b.
+__device__ __forceinline__ uint4 shift16(uint4 a, uint4 b, int s)
+{
+    if (s & 8)
+        return b;
+    uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    if (s & 4) {
+        w[0] = a.z, w[1] = a.w, w[2] = b.x, w[3] = b.y, w[4] = b.z, w[5] = b.w;
+    }
+    if (s & 2) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            w[i] = w[i + 1];
+    }
+    if (s & 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Eight consecutive elements (16 bits each) from column c on; columns past n read as zero.
 template <bool VEC>
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int c, int n)
 {
     if (VEC)
         return c < n ? *reinterpret_cast<const uint4 *>(p + c) : make_uint4(0, 0, 0, 0);
+    const int m = (int)((reinterpret_cast<uintptr_t>(p) >> 1) & 7);  // c is a multiple of 8
+    const uint4 *g = reinterpret_cast<const uint4 *>(p + c - m);
+    if (m == 0 && c + 8 <= n)
+        return *g;
+    if (c >= m && c - m + 16 <= n)
+        return shift16(g[0], g[1], m);
     uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -67,6 +101,7 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, int c, int n)
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// Store them; every lane of the warp calls, with consecutive c.
 template <bool VEC>
 __device__ __forceinline__ void store8(uint16_t *p, int c, int n, uint4 v)
 {
@@ -75,13 +110,25 @@ __device__ __forceinline__ void store8(uint16_t *p, int c, int n, uint4 v)
             *reinterpret_cast<uint4 *>(p + c) = v;
         return;
     }
+    const int m = (int)((reinterpret_cast<uintptr_t>(p) >> 1) & 7), lane = threadIdx.x & 31;
+    uint4 before;
+    before.x = __shfl_up_sync(~0u, v.x, 1);
+    before.y = __shfl_up_sync(~0u, v.y, 1);
+    before.z = __shfl_up_sync(~0u, v.z, 1);
+    before.w = __shfl_up_sync(~0u, v.w, 1);
+    const bool own = (lane > 0 || m == 0) && c - m + 8 <= n;  // this lane stores its first granule whole
+    const bool next = m == 0 || (lane < 31 && c + 16 - m <= n);  // and the next lane the one after
+    if (own)
+        *reinterpret_cast<uint4 *>(p + c - m) = shift16(before, v, 8 - m);
     const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+    if (!own || !next)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < n)
-            p[c + i] = (uint16_t)(a[i / 2] >> (16 * (i & 1)));
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n && !(i < 8 - m ? own : next))
+                p[c + i] = (uint16_t)(a[i / 2] >> (16 * (i & 1)));
 }
 
+// The same for eight bytes in granules of eight.
 template <bool VEC>
 __device__ __forceinline__ void store8b(uint8_t *p, int c, int n, uint2 v)
 {
@@ -90,11 +137,18 @@ __device__ __forceinline__ void store8b(uint8_t *p, int c, int n, uint2 v)
             *reinterpret_cast<uint2 *>(p + c) = v;
         return;
     }
-    const uint32_t a[2] = {v.x, v.y};
+    const int m = (int)(reinterpret_cast<uintptr_t>(p) & 7), lane = threadIdx.x & 31;
+    const uint64_t mine = (uint64_t)v.y << 32 | v.x;
+    const uint64_t before = __shfl_up_sync(~0u, (unsigned long long)mine, 1);
+    const bool own = (lane > 0 || m == 0) && c - m + 8 <= n;
+    const bool next = m == 0 || (lane < 31 && c + 16 - m <= n);
+    if (own)
+        *reinterpret_cast<uint64_t *>(p + c - m) = m ? before >> (64 - 8 * m) | mine << (8 * m) : mine;
+    if (!own || !next)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < n)
-            p[c + i] = (uint8_t)(a[i / 4] >> (8 * (i & 3)));
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n && !(i < 8 - m ? own : next))
+                p[c + i] = (uint8_t)(mine >> (8 * i));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -104,16 +158,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// rint(127 p / P), exactly (see above); inv = 1 / P rounded, or 0 for a flushed row.
+// rint(127 p / P) in the low byte, exactly (see above); inv = 1 / P rounded.  The guess is read
+// off the mantissa of its sum with 1.5 * 2^23 (conversions run at an eighth of the rate of an
+// addition).  P infinite and inv zero (a flushed row): zero.
 __device__ __forceinline__ uint32_t quant_int8(float p, float P, float inv)
 {
-    const float t = 127.0f * p;
-    float c = rintf(t * inv);
-    const float rem = fmaf(-c, P, t), two = fabsf(rem) * 2.0f;
-    const bool odd = ((int)c & 1) != 0;
-    if (inv != 0.0f && (two > P || (two == P && odd)))
-        c += rem > 0.0f ? 1.0f : -1.0f;
-    return (uint32_t)(int)c & 0xFFu;
+    const float t = 127.0f * p, u = fmaf(t, inv, 12582912.0f);
+    const float rem = fmaf(-(u - 12582912.0f), P, t), two = fabsf(rem) * 2.0f;
+    const uint32_t c = __float_as_uint(u);
+    const uint32_t step = rem > 0.0f ? 1u : 0xFFFFFFFFu;
+    return two > P || (two == P && (c & 1)) ? c + step : c;
 }
 
 // 448 p / P to within far less than half an e4m3 step, exact where it is a tie.
@@ -131,15 +185,15 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi)
     return r;
 }
 
-// WARP_ROW: blockDim = (32, 8), a row for each warp; else blockDim = (THREADS, 1), a row for each block.
+// WARP_ROW: blockDim = (32, 8), a row for each warp; else a row for each block of up to MAXT threads.
 // Thread t holds the eight columns from 8 (t + i * threads) on, i < VPT.
-template <int FMT, bool NORM, bool VEC, int VPT, bool WARP_ROW, int THREADS>
-__global__ void __launch_bounds__(WARP_ROW ? 256 : THREADS) norm_kernel(const NormParams a)
+template <int FMT, bool NORM, bool VEC, int VPT, bool WARP_ROW, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
 {
     const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * 8 + threadIdx.y : (int64_t)blockIdx.x;
     if (WARP_ROW && row >= a.rows)
         return;
-    const int t = threadIdx.x, threads = WARP_ROW ? 32 : THREADS, n = a.cols;
+    const int t = threadIdx.x, threads = WARP_ROW ? 32 : blockDim.x, n = a.cols;
     const uint16_t *x = a.x + row * a.xs;
     uint4 hv[VPT], wv[VPT];
 #pragma unroll
@@ -202,17 +256,30 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : THREADS) norm_kernel(const No
                 top = max_nan(top, __shfl_xor_sync(~0u, top, o));
         }
         if (!WARP_ROW) {
-            constexpr int kWarps = THREADS / 32;
-            __shared__ float2 part[kWarps];
+            __shared__ float2 part[MAXT / 32];
             if ((t & 31) == 0)
                 part[t >> 5] = make_float2(ss, top);
             __syncthreads();
-            ss = 0.0f;
-            top = 0.0f;
+            if (MAXT <= 256) {  // every thread adds the warps' parts in the same order
+                ss = 0.0f;
+                top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {  // every thread adds the warps' parts in the same order
-                ss += part[i].x;
-                top = max_nan(top, part[i].y);
+                for (int i = 0; i < MAXT / 32; ++i) {
+                    const float2 v = i < threads / 32 ? part[i] : make_float2(0.0f, 0.0f);
+                    ss += v.x;
+                    if (FMT == DEP_QUANT_INT8)
+                        top = max_nan(top, v.y);
+                }
+            } else {  // every warp adds them by the same shuffles
+                const float2 v = (t & 31) < threads / 32 ? part[t & 31] : make_float2(0.0f, 0.0f);
+                ss = v.x;
+                top = v.y;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    ss += __shfl_xor_sync(~0u, ss, o);
+                    if (FMT == DEP_QUANT_INT8)
+                        top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+                }
             }
         }
     }
@@ -229,16 +296,20 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : THREADS) norm_kernel(const No
         }
     } else if (FMT == DEP_QUANT_INT8) {
         const bool flush = top < kTiny;
-        const float inv = flush ? 0.0f : 1.0f / top;
+        const float P = flush ? __int_as_float(0x7F800000) : top, inv = flush ? 0.0f : 1.0f / top;
         if (t == 0)
             a.scale[row] = flush ? 0.0f : top * rstd / 127.0f;
         uint8_t *o = static_cast<uint8_t *>(a.out) + row * a.os;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            uint32_t v[2] = {0, 0};
+            uint32_t v[2], b[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j / 4] |= quant_int8(prod(i, j), top, inv) << (8 * (j & 3));
+                b[j] = quant_int8(prod(i, j), P, inv);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                v[j] = __byte_perm(__byte_perm(b[4 * j], b[4 * j + 1], 0x0040), __byte_perm(b[4 * j + 2], b[4 * j + 3], 0x0040),
+                                   0x5410);
             store8b<VEC>(o, 8 * (t + i * threads), n, make_uint2(v[0], v[1]));
         }
     } else {
@@ -272,19 +343,21 @@ template <int FMT, bool NORM, bool VEC>
 cudaError_t norm_launch(const NormParams &a, cudaStream_t s)
 {
     const int vecs = (a.cols + 7) / 8;
-    const dim3 warp_grid((unsigned)((a.rows + 7) / 8)), grid((unsigned)a.rows);
+    const dim3 warp_grid((unsigned)((a.rows + 7) / 8)), grid((unsigned)a.rows), warps(32, 8);
+    const auto threads = [&](int vpt) { return dim3((unsigned)(((vecs + vpt - 1) / vpt + 31) / 32 * 32)); };
+    // A row for each warp up to 1024 columns; above, a row for each block, with just enough threads.
     if (vecs <= 32)
-        norm_kernel<FMT, NORM, VEC, 1, true, 256><<<warp_grid, dim3(32, 8), 0, s>>>(a);
+        norm_kernel<FMT, NORM, VEC, 1, true, 256><<<warp_grid, warps, 0, s>>>(a);
+    else if (vecs <= 64)
+        norm_kernel<FMT, NORM, VEC, 2, true, 256><<<warp_grid, warps, 0, s>>>(a);
     else if (vecs <= 128)
-        norm_kernel<FMT, NORM, VEC, 4, true, 256><<<warp_grid, dim3(32, 8), 0, s>>>(a);
-    else if (vecs <= 512)
-        norm_kernel<FMT, NORM, VEC, 2, false, 256><<<grid, 256, 0, s>>>(a);
+        norm_kernel<FMT, NORM, VEC, 4, true, 256><<<warp_grid, warps, 0, s>>>(a);
     else if (vecs <= 1024)
-        norm_kernel<FMT, NORM, VEC, 4, false, 256><<<grid, 256, 0, s>>>(a);
+        norm_kernel<FMT, NORM, VEC, 4, false, 256><<<grid, threads(4), 0, s>>>(a);
     else if (vecs <= 2048)
-        norm_kernel<FMT, NORM, VEC, 4, false, 512><<<grid, 512, 0, s>>>(a);
+        norm_kernel<FMT, NORM, VEC, 4, false, 512><<<grid, threads(4), 0, s>>>(a);
     else
-        norm_kernel<FMT, NORM, VEC, 8, false, 1024><<<grid, 1024, 0, s>>>(a);
+        norm_kernel<FMT, NORM, VEC, 8, false, 1024><<<grid, threads(8), 0, s>>>(a);
     return cudaGetLastError();
 }
 
