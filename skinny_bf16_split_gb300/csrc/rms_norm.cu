@@ -52,11 +52,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// Rows that are not aligned, or not whole vectors (VEC false).  Eight elements that start
-// m elements past an aligned granule lie in two granules: they are loaded as those two and
-// shifted, and a lane stores the granule its elements start in, whose first m elements come
-// from the lane before.  What granules at the ends of a warp or row would take from outside
-// goes element by element.
+// Rows that are not aligned, or not whole vectors (VEC false).  A thread's eight elements
+// start where a granule of x's row starts, so contiguous matrices with any number of columns,
+// whose rows are all misaligned alike, are still moved in whole granules, all but the row's
+// ends.  A tensor aligned otherwise (the weight, a view) is loaded as the two granules that
+// hold the eight elements, and shifted; it is stored as the granule that the eight start in,
+// whose first elements come from the lane before.  (e4m3: a thread's elements start at a
+// multiple of eight, so that they belong to one group.)  What granules at the ends of a warp
+// or row would take from outside goes element by element.
 
 // Words [s / 2, s / 2 + 4) (in 16-bit steps s <= 8) of the eight words a, b.
 __device__ __forceinline__ uint4 shift16(uint4 a, uint4 b, int s)
@@ -80,22 +83,23 @@ __device__ __forceinline__ uint4 shift16(uint4 a, uint4 b, int s)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight consecutive elements (16 bits each) from column c on; columns past n read as zero.
+// Eight consecutive elements (16 bits each) from column c on; columns outside 0..n-1 read as zero.
 template <bool VEC>
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int c, int n)
 {
     if (VEC)
         return c < n ? *reinterpret_cast<const uint4 *>(p + c) : make_uint4(0, 0, 0, 0);
-    const int m = (int)((reinterpret_cast<uintptr_t>(p) >> 1) & 7);  // c is a multiple of 8
-    const uint4 *g = reinterpret_cast<const uint4 *>(p + c - m);
-    if (m == 0 && c + 8 <= n)
+    const int s = (int)((reinterpret_cast<uintptr_t>(p) >> 1) + c) & 7;
+    const uint4 *g = reinterpret_cast<const uint4 *>(p + c - s);
+    if (s == 0 && c >= 0 && c + 8 <= n)
         return *g;
-    if (c >= m && c - m + 16 <= n)
-        return shift16(g[0], g[1], m);
+    if (c >= s && c - s + 16 <= n)
+        return shift16(g[0], g[1], s);
     uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = c + 2 * i < n ? p[c + 2 * i] : 0, hi = c + 2 * i + 1 < n ? p[c + 2 * i + 1] : 0;
+        const int e = c + 2 * i;
+        const uint32_t lo = e >= 0 && e < n ? p[e] : 0, hi = e + 1 >= 0 && e + 1 < n ? p[e + 1] : 0;
         v[i] = lo | hi << 16;
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
@@ -110,21 +114,25 @@ __device__ __forceinline__ void store8(uint16_t *p, int c, int n, uint4 v)
             *reinterpret_cast<uint4 *>(p + c) = v;
         return;
     }
-    const int m = (int)((reinterpret_cast<uintptr_t>(p) >> 1) & 7), lane = threadIdx.x & 31;
-    uint4 before;
-    before.x = __shfl_up_sync(~0u, v.x, 1);
-    before.y = __shfl_up_sync(~0u, v.y, 1);
-    before.z = __shfl_up_sync(~0u, v.z, 1);
-    before.w = __shfl_up_sync(~0u, v.w, 1);
-    const bool own = (lane > 0 || m == 0) && c - m + 8 <= n;  // this lane stores its first granule whole
-    const bool next = m == 0 || (lane < 31 && c + 16 - m <= n);  // and the next lane the one after
+    const int s = (int)((reinterpret_cast<uintptr_t>(p) >> 1) + c) & 7, lane = threadIdx.x & 31;
+    uint4 out = v;
+    if (s) {  // the same for all lanes
+        uint4 before;
+        before.x = __shfl_up_sync(~0u, v.x, 1);
+        before.y = __shfl_up_sync(~0u, v.y, 1);
+        before.z = __shfl_up_sync(~0u, v.z, 1);
+        before.w = __shfl_up_sync(~0u, v.w, 1);
+        out = shift16(before, v, 8 - s);
+    }
+    const bool own = (lane > 0 || s == 0) && c >= s && c - s + 8 <= n;  // this lane stores its first granule whole
+    const bool next = s == 0 || (lane < 31 && c + 8 >= s && c + 16 - s <= n);  // and the next lane the one after
     if (own)
-        *reinterpret_cast<uint4 *>(p + c - m) = shift16(before, v, 8 - m);
+        *reinterpret_cast<uint4 *>(p + c - s) = out;
     const uint32_t a[4] = {v.x, v.y, v.z, v.w};
     if (!own || !next)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < n && !(i < 8 - m ? own : next))
+            if (c + i >= 0 && c + i < n && !(i < 8 - s ? own : next))
                 p[c + i] = (uint16_t)(a[i / 2] >> (16 * (i & 1)));
 }
 
@@ -137,17 +145,21 @@ __device__ __forceinline__ void store8b(uint8_t *p, int c, int n, uint2 v)
             *reinterpret_cast<uint2 *>(p + c) = v;
         return;
     }
-    const int m = (int)(reinterpret_cast<uintptr_t>(p) & 7), lane = threadIdx.x & 31;
+    const int s = (int)(reinterpret_cast<uintptr_t>(p) + c) & 7, lane = threadIdx.x & 31;
     const uint64_t mine = (uint64_t)v.y << 32 | v.x;
-    const uint64_t before = __shfl_up_sync(~0u, (unsigned long long)mine, 1);
-    const bool own = (lane > 0 || m == 0) && c - m + 8 <= n;
-    const bool next = m == 0 || (lane < 31 && c + 16 - m <= n);
+    uint64_t out = mine;
+    if (s) {
+        const uint64_t before = __shfl_up_sync(~0u, (unsigned long long)mine, 1);
+        out = before >> (64 - 8 * s) | mine << (8 * s);
+    }
+    const bool own = (lane > 0 || s == 0) && c >= s && c - s + 8 <= n;
+    const bool next = s == 0 || (lane < 31 && c + 8 >= s && c + 16 - s <= n);
     if (own)
-        *reinterpret_cast<uint64_t *>(p + c - m) = m ? before >> (64 - 8 * m) | mine << (8 * m) : mine;
+        *reinterpret_cast<uint64_t *>(p + c - s) = out;
     if (!own || !next)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < n && !(i < 8 - m ? own : next))
+            if (c + i >= 0 && c + i < n && !(i < 8 - s ? own : next))
                 p[c + i] = (uint8_t)(mine >> (8 * i));
 }
 
@@ -186,7 +198,7 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi)
 }
 
 // WARP_ROW: blockDim = (32, 8), a row for each warp; else a row for each block of up to MAXT threads.
-// Thread t holds the eight columns from 8 (t + i * threads) on, i < VPT.
+// Thread t holds the eight columns from 8 (t + i * threads) on, i < VPT, less c0 where rows are not aligned.
 template <int FMT, bool NORM, bool VEC, int VPT, bool WARP_ROW, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
 {
@@ -195,17 +207,18 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
         return;
     const int t = threadIdx.x, threads = WARP_ROW ? 32 : blockDim.x, n = a.cols;
     const uint16_t *x = a.x + row * a.xs;
+    const int c0 = VEC || FMT == DEP_QUANT_E4M3 ? 0 : (int)(reinterpret_cast<uintptr_t>(x) >> 1) & 7;
     uint4 hv[VPT], wv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-        hv[i] = load8<VEC>(x, 8 * (t + i * threads), n);
+        hv[i] = load8<VEC>(x, 8 * (t + i * threads) - c0, n);
     if (NORM) {
         if (a.r) {
             const uint16_t *r = a.r + row * a.rs;
             uint4 rv[VPT];
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                rv[i] = load8<VEC>(r, 8 * (t + i * threads), n);
+                rv[i] = load8<VEC>(r, 8 * (t + i * threads) - c0, n);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 uint32_t *h = &hv[i].x;
@@ -217,13 +230,13 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            wv[i] = a.w ? load8<VEC>(a.w, 8 * (t + i * threads), n)
+            wv[i] = a.w ? load8<VEC>(a.w, 8 * (t + i * threads) - c0, n)
                         : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
         if (a.r) {
             uint16_t *ho = a.h + row * a.hs;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                store8<VEC>(ho, 8 * (t + i * threads), n, hv[i]);
+                store8<VEC>(ho, 8 * (t + i * threads) - c0, n, hv[i]);
         }
     }
     // p = h * w of element j of vector i
@@ -292,7 +305,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 (&v.x)[j] = pack_bf16(prod(i, 2 * j) * rstd, prod(i, 2 * j + 1) * rstd);
-            store8<VEC>(o, 8 * (t + i * threads), n, v);
+            store8<VEC>(o, 8 * (t + i * threads) - c0, n, v);
         }
     } else if (FMT == DEP_QUANT_INT8) {
         const bool flush = top < kTiny;
@@ -310,7 +323,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
             for (int j = 0; j < 2; ++j)
                 v[j] = __byte_perm(__byte_perm(b[4 * j], b[4 * j + 1], 0x0040), __byte_perm(b[4 * j + 2], b[4 * j + 3], 0x0040),
                                    0x5410);
-            store8b<VEC>(o, 8 * (t + i * threads), n, make_uint2(v[0], v[1]));
+            store8b<VEC>(o, 8 * (t + i * threads) - c0, n, make_uint2(v[0], v[1]));
         }
     } else {
         uint8_t *o = static_cast<uint8_t *>(a.out) + row * a.os;
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
 template <int FMT, bool NORM, bool VEC>
 cudaError_t norm_launch(const NormParams &a, cudaStream_t s)
 {
-    const int vecs = (a.cols + 7) / 8;
+    const int vecs = (a.cols + (VEC ? 7 : 14)) / 8;  // with what a row's first granule may start before it
     const dim3 warp_grid((unsigned)((a.rows + 7) / 8)), grid((unsigned)a.rows), warps(32, 8);
     const auto threads = [&](int vpt) { return dim3((unsigned)(((vecs + vpt - 1) / vpt + 31) / 32 * 32)); };
     // A row for each warp up to 1024 columns; above, a row for each block, with just enough threads.
@@ -356,8 +369,10 @@ cudaError_t norm_launch(const NormParams &a, cudaStream_t s)
         norm_kernel<FMT, NORM, VEC, 4, false, 256><<<grid, threads(4), 0, s>>>(a);
     else if (vecs <= 2048)
         norm_kernel<FMT, NORM, VEC, 4, false, 512><<<grid, threads(4), 0, s>>>(a);
-    else
-        norm_kernel<FMT, NORM, VEC, 8, false, 1024><<<grid, threads(8), 0, s>>>(a);
+    else {
+        constexpr int kMost = VEC ? 8 : 9;  // 65536 columns and a first granule that starts before them
+        norm_kernel<FMT, NORM, VEC, kMost, false, 1024><<<grid, threads(kMost), 0, s>>>(a);
+    }
     return cudaGetLastError();
 }
 

@@ -113,6 +113,24 @@ def test_strided_and_shifted_rows(dep, fmt, offset, extra):
 
 
 @pytest.mark.parametrize("fmt", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("cols", [257, 1018, 1023, 2047, 2050, 8185, 8191, 16383, 16386, 65535])
+def test_contiguous_rows_of_odd_length(dep, fmt, cols):
+    """Every row starts at another place of a 16-byte granule."""
+    check(dep, *inputs(9, cols, seed=cols), fmt)
+
+
+@pytest.mark.parametrize("fmt", [None, "int8", "e4m3"])
+def test_longest_rows_out_of_line(dep, fmt):
+    x, r, w = inputs(3, 65536, seed=15)
+    views = []
+    for a, off in ((x, 7), (r, 7), (w.unsqueeze(0), 3)):
+        b = torch.zeros(a.shape[0], 65536 + 9, device="cuda").bfloat16()
+        b[:, off:off + 65536] = a
+        views.append(b[:, off:off + 65536])
+    check(dep, views[0], views[1], views[2][0], fmt, residual_out=torch.empty_like(x))
+
+
+@pytest.mark.parametrize("fmt", [None, "int8", "e4m3"])
 def test_output_rows_keep_their_surroundings(dep, fmt):
     rows, cols = 5, 333
     dt = {None: torch.bfloat16, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt]
