@@ -24,8 +24,12 @@
 // order, the same on both sides), so S, U and the rest never leave the registers.  Two
 // more groups of four warps prepare the chunks to come, in turn: norms, decays, A, B and
 // T, and K.P, Q.P, K.R, each group in a shared-memory stage of its own.
-// FP32 operands are split into two TF32 parts, and three products are kept (the fourth is
-// below 2^-22): everything keeps FP32's precision, or nearly.
+// Precision: an FP32 operand is split into two parts of 11 bits, and three of the four products
+// are kept (the last is below 2^-22), so that everything keeps FP32's precision, or nearly.
+// In the products with S and its update the parts are FP16, whose MMAs do twice TF32's work;
+// what fits FP32's range is brought into FP16's by powers of two: one for each row of S and
+// of U, from its largest value, and one for each token's k and q, from its norm.  The small
+// products (A, B, T, with what the state's rows meet there) take TF32 parts.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -263,6 +267,50 @@ __device__ __forceinline__ void mma_tf32x3(float (*const (&d)[N])[4], const uint
     for (int n = 0; n < N; ++n)
         mma_tf32(*d[n], ah, h[n][0], h[n][1]);
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two values (low half first) as FP16, and what that leaves of them.
+__device__ __forceinline__ void f16_split2(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+// N products d[n] += a b[n] of FP16 parts, three MMAs each.
+template <int N>
+__device__ __forceinline__ void mma_f16x3(float (*const (&d)[N])[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          const uint4 (&b)[N])
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        mma_f16(*d[n], al, b[n].x, b[n].y);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        mma_f16(*d[n], ah, b[n].z, b[n].w);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        mma_f16(*d[n], ah, b[n].x, b[n].y);
+}
+// The power of two that brings values of up to `top` below 2^14 (top's exponent to 13), and its
+// reciprocal.  Tops below 2^-107 count as that.
+__device__ __forceinline__ float scale_for(float top, float &inv)
+{
+    const int e = max((int)(__float_as_uint(top) >> 23), 20);
+    inv = __uint_as_float((uint32_t)(e - 13) << 23);
+    return __uint_as_float((uint32_t)(267 - e) << 23);
+}
+__device__ __forceinline__ float row_max(float v)  // over the four lanes of a row
+{
+    v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
+    return fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+}
 __device__ __forceinline__ float2 ld2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
 constexpr int kSort = 256;
@@ -293,17 +341,21 @@ __device__ __forceinline__ int longest_first(const DeltaParams &p, int r, int (&
     return len[kSort];
 }
 
+// What an MMA's lane (g, t) takes of a right operand, 16 bytes: FP16 parts of the k's 2t, 2t + 1
+// (x) and 2t + 8, 2t + 9 (y) of its sixteen, and the parts that those leave (z, w).
 template <int DK>
 struct ChunkStage {
-    static constexpr int KS = DK + 8;  // row stride of K.P and Q.P: float2 reads without conflicts
-    float kp[kC][KS], qp[kC][KS];      // [token][channel]
-    float kr[DK][kTS];                 // [channel][token]
-    float T[kC][kTS], B[kC][kTS];      // [token i][token j]
-    float last[DK];                    // P_15
+    // K.P and Q.P by token, sixteen channels after another, four lanes t each.  Rows are 64 bytes
+    // off a multiple of 128, so that the eight lanes of a load phase meet no bank twice.
+    uint4 kp[kC][DK / 4 + 4], qp[kC][DK / 4 + 4];
+    uint4 kr[DK][4];               // K.R by channel; lane t at t ^ (channel / 2 % 4), for the same reason
+    float T[kC][kTS], B[kC][kTS];  // [token i][token j]
+    float last[DK];                // P_15
+    float ik[kC], iq[kC];          // what undoes the scales of k and q
 };
 template <int DK>
 struct ChunkShared {
-    static constexpr int KS = DK + 8;
+    static constexpr int KS = DK + 8;  // float2 reads without conflicts
     ChunkStage<DK> stage[2];
     struct {  // scratch of each group of preparing warps
         struct {  // operands of the products of one level (see below): rows k_i then q_i, columns k_j
@@ -314,7 +366,7 @@ struct ChunkShared {
             uint16_t k[kC][DK], q[kC][DK];
         } raw;
         float A[kC][kC];
-        float part[4][48], norm[4][48], beta[kC], g[kC];
+        float part[4][48], norm[4][48], pow2[4][32], beta[kC], g[kC];
     } prep[2];
     int order[kSort + 1];
     uint4 out[8][kC][2];  // a warp's rows of O, [token][16 rows in BF16]
@@ -371,6 +423,17 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             S[n][2] = b.x;
             S[n][3] = b.y;
         }
+        float r0, r1, i0, i1;  // scales of rows g and g + 8, and what undoes them
+        {
+            float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                m0 = fmaxf(m0, fmaxf(fabsf(S[n][0]), fabsf(S[n][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(S[n][2]), fabsf(S[n][3])));
+            }
+            r0 = scale_for(row_max(m0), i0);
+            r1 = scale_for(row_max(m1), i1);
+        }
         const uint16_t *vp = p.v + t0 * p.vs + (int64_t)h * p.Dv + row0 + g;
         // V^T in accumulator layout: rows g and g + 8, tokens 8 n + 2 t and + 1
         auto load_v = [&](int c, uint32_t (&v)[2][2]) {
@@ -395,13 +458,23 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             const ChunkStage<DK> &sg = sm.stage[st];
             float X[2][4] = {}, O[2][4] = {};
 #pragma unroll
-            for (int ks = 0; ks < NT; ++ks) {
+            for (int ks = 0; ks < NT / 2; ++ks) {
                 uint32_t ah[4], al[4];
-                split_a(S[ks], ah, al);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f16_split2(S[2 * ks + i][0] * r0, S[2 * ks + i][1] * r0, ah[2 * i], al[2 * i]);
+                    f16_split2(S[2 * ks + i][2] * r1, S[2 * ks + i][3] * r1, ah[2 * i + 1], al[2 * i + 1]);
+                }
                 float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
-                const float2 b[4] = {ld2(&sg.kp[g][8 * ks + 2 * t]), ld2(&sg.qp[g][8 * ks + 2 * t]),
-                                     ld2(&sg.kp[8 + g][8 * ks + 2 * t]), ld2(&sg.qp[8 + g][8 * ks + 2 * t])};
-                mma_tf32x3(d, ah, al, b);
+                const uint4 b[4] = {sg.kp[g][4 * ks + t], sg.qp[g][4 * ks + t], sg.kp[8 + g][4 * ks + t],
+                                    sg.qp[8 + g][4 * ks + t]};
+                mma_f16x3(d, ah, al, b);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 ik = ld2(&sg.ik[8 * n + 2 * t]), iq = ld2(&sg.iq[8 * n + 2 * t]);
+                X[n][0] *= ik.x * i0, X[n][1] *= ik.y * i0, X[n][2] *= ik.x * i1, X[n][3] *= ik.y * i1;
+                O[n][0] *= iq.x * i0, O[n][1] *= iq.y * i0, O[n][2] *= iq.x * i1, O[n][3] *= iq.y * i1;
             }
             // Y = V - X, then U^T = Y^T T^T and O^T += U^T B^T (both lower triangular: tokens j <= i)
             uint32_t uh[2][4], ul[2][4];
@@ -433,24 +506,42 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 const float2 b1[1] = {ld2(&sg.B[8 + g][8 + 2 * t])};
                 mma_tf32x3(d1, uh[1], ul[1], b1);
             }
+            // S <- S diag(P_15) + U^T (K.R): k's scale comes off U, whose rows get scales of their own
+            {
+                const float2 k0 = ld2(&sg.ik[2 * t]), k1 = ld2(&sg.ik[8 + 2 * t]);
+                const float u[8] = {U[0][0] * k0.x, U[0][1] * k0.y, U[1][0] * k1.x, U[1][1] * k1.y,
+                                    U[0][2] * k0.x, U[0][3] * k0.y, U[1][2] * k1.x, U[1][3] * k1.y};
+                float j0, j1;
+                const float s0 = scale_for(row_max(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3])))), j0);
+                const float s1 = scale_for(row_max(fmaxf(fmaxf(fabsf(u[4]), fabsf(u[5])), fmaxf(fabsf(u[6]), fabsf(u[7])))), j1);
+                uint32_t ah[4], al[4];
+                f16_split2(u[0] * s0, u[1] * s0, ah[0], al[0]);
+                f16_split2(u[4] * s1, u[5] * s1, ah[1], al[1]);
+                f16_split2(u[2] * s0, u[3] * s0, ah[2], al[2]);
+                f16_split2(u[6] * s1, u[7] * s1, ah[3], al[3]);
+                float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; n += 4) {
-                float(*const d[4])[4] = {&S[n], &S[n + 1], &S[n + 2], &S[n + 3]};
+                for (int n = 0; n < NT; n += 4) {
+                    float D[4][4] = {};
+                    float(*const d[4])[4] = {&D[0], &D[1], &D[2], &D[3]};
+                    const int sw = t ^ (g >> 1 & 3);
+                    const uint4 b[4] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw], sg.kr[8 * n + 16 + g][sw],
+                                        sg.kr[8 * n + 24 + g][sw]};
+                    mma_f16x3(d, ah, al, b);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
-                    S[n + i][0] *= a.x;
-                    S[n + i][1] *= a.y;
-                    S[n + i][2] *= a.x;
-                    S[n + i][3] *= a.y;
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
+                        float(&s)[4] = S[n + i];
+                        s[0] = fmaf(D[i][0], j0, s[0] * a.x);
+                        s[1] = fmaf(D[i][1], j0, s[1] * a.y);
+                        s[2] = fmaf(D[i][2], j1, s[2] * a.x);
+                        s[3] = fmaf(D[i][3], j1, s[3] * a.y);
+                        m0 = fmaxf(m0, fmaxf(fabsf(s[0]), fabsf(s[1])));
+                        m1 = fmaxf(m1, fmaxf(fabsf(s[2]), fabsf(s[3])));
+                    }
                 }
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const float2 b[4] = {ld2(&sg.kr[8 * n + g][8 * ks + 2 * t]), ld2(&sg.kr[8 * n + 8 + g][8 * ks + 2 * t]),
-                                         ld2(&sg.kr[8 * n + 16 + g][8 * ks + 2 * t]),
-                                         ld2(&sg.kr[8 * n + 24 + g][8 * ks + 2 * t])};
-                    mma_tf32x3(d, uh[ks], ul[ks], b);
-                }
+                r0 = scale_for(row_max(m0), i0);
+                r1 = scale_for(row_max(m1), i1);
             }
             if (c + 2 < chunks)
                 bar_arrive(kBarEmpty + st, kThreads);
@@ -580,7 +671,11 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     fetch(c + 2);
                 // every warp finishes the sums for itself
                 const float sum = (pr.part[0][lane] + pr.part[1][lane]) + (pr.part[2][lane] + pr.part[3][lane]);
-                pr.norm[pw][lane] = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
+                const float f = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
+                pr.norm[pw][lane] = f;
+                // 2^e > the norm of the normalised row >= its largest value; the power of two that makes it 2^8
+                const int e = (((int)(__float_as_uint(sum * f * f) >> 23) - 127 + 2) >> 1);
+                pr.pow2[pw][lane] = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
                 if (lane < 16)
                     pr.norm[pw][32 + lane] = (pr.part[0][32 + lane] + pr.part[1][32 + lane]) +
                                              (pr.part[2][32 + lane] + pr.part[3][32 + lane]);
@@ -590,6 +685,8 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 bar_sync(kBarEmpty + grp, kThreads);
             if (pt < kC)
                 sg.B[pt][pt] = pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt];
+            if (pt < 32)
+                (pt < 16 ? sg.ik : sg.iq)[pt & 15] = 1.f / pr.pow2[pw][pt];
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
                 k[i] *= pr.norm[pw][i];
@@ -597,11 +694,19 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             }
             if (ch) {
                 float P = 1.f;
+                // this channel's places: FP16 number `sub` of lane t's, in its sixteen channels
+                const int c16 = pt & 15, at = ((pt >> 4) * 4 + ((c16 & 7) >> 1)) * 8 + (c16 >> 3) * 2 + (c16 & 1);
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
                     P *= a[i];
-                    sg.kp[i][pt] = k[i] * P;
-                    sg.qp[i][pt] = q[i] * P;
+                    uint32_t hi, lo;  // k's and q's
+                    f16_split2(k[i] * (P * pr.pow2[pw][i]), q[i] * (P * pr.pow2[pw][16 + i]), hi, lo);
+                    uint16_t *kd = reinterpret_cast<uint16_t *>(&sg.kp[i][0]) + at;
+                    uint16_t *qd = reinterpret_cast<uint16_t *>(&sg.qp[i][0]) + at;
+                    kd[0] = (uint16_t)hi;
+                    kd[4] = (uint16_t)lo;
+                    qd[0] = (uint16_t)(hi >> 16);
+                    qd[4] = (uint16_t)(lo >> 16);
                 }
                 sg.last[pt] = P;
 #pragma unroll
@@ -625,12 +730,16 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 float R = 1.f;
 #pragma unroll
                 for (int i = kC - 1; i >= 0; --i) {
-                    k[i] *= R;
+                    k[i] *= R * pr.pow2[pw][i];
                     R *= a[i];
                 }
 #pragma unroll
-                for (int i = 0; i < kC; i += 4)
-                    *reinterpret_cast<float4 *>(&sg.kr[pt][i]) = make_float4(k[i], k[i + 1], k[i + 2], k[i + 3]);
+                for (int t = 0; t < 4; ++t) {
+                    uint4 v;
+                    f16_split2(k[2 * t], k[2 * t + 1], v.x, v.z);
+                    f16_split2(k[2 * t + 8], k[2 * t + 9], v.y, v.w);
+                    sg.kr[pt][t ^ (pt >> 1 & 3)] = v;
+                }
             }
             bar_sync(kBarPrep, kPrep);
             {  // warp pw: level pw
