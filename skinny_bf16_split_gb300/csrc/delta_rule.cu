@@ -16,20 +16,20 @@
 // With P_i = a_0 .. a_i, R_j = a_(j+1) .. a_15 and M_ij = a_(j+1) .. a_i (products of
 // decays, channel by channel; never a quotient, so a decay of zero is as good as any),
 //     A_ij = beta_i sum_c k_i k_j M_ij  (j < i),    B_ij = sum_c q_i k_j M_ij  (j <= i)
-//     T = (I + A)^-1 diag(beta),                    U = T (V - (K.P) S^T)
+//     T = (I + A)^-1 diag(beta),   W = T (K.P),     U = T V - W S^T
 //     O = (Q.P) S^T + B U,                          S <- S diag(P_15) + U^T (K.R)
 // A block takes up to 128 rows of one head's state.  Its first warps hold 16 rows of S
 // each, as the accumulator of the last product, for the whole sequence: an accumulator
 // fragment is also a left operand of the next product (with the channels in another
 // order, the same on both sides), so S, U and the rest never leave the registers.  Two
-// more groups of four warps prepare the chunks to come, in turn: norms, decays, A, B and
-// T, and K.P, Q.P, K.R, each group in a shared-memory stage of its own.
+// more groups of four warps prepare the chunks to come, in turn: norms, decays, A, B, T and
+// W, and Q.P, K.R, each group in a shared-memory stage of its own.
 // Precision: an FP32 operand is split into two parts of 11 bits, and three of the four products
 // are kept (the last is below 2^-22), so that everything keeps FP32's precision, or nearly.
 // In the products with S and its update the parts are FP16, whose MMAs do twice TF32's work;
 // what fits FP32's range is brought into FP16's by powers of two: one for each row of S and
-// of U, from its largest value, and one for each token's k and q, from its norm.  The small
-// products (A, B, T, with what the state's rows meet there) take TF32 parts.
+// of U, from its largest value, and one for each token's k, q and W, from bounds on theirs.
+// A, B and W are formed from TF32 parts; V is BF16, and T meets it in three BF16 parts.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -54,6 +54,9 @@ struct DeltaParams {
 
 __device__ __forceinline__ float lo_bf(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// exp(g), at most one: the chunked kernel's scales count on decays that do not grow.
+__device__ __forceinline__ float decay(float g) { return expf(g > 0.f ? 0.f : g); }
 
 // First token and end of sequence s, clipped to the tensors.
 __device__ __forceinline__ void seq_range(const DeltaParams &p, int s, int64_t &t0, int64_t &t1)
@@ -118,11 +121,11 @@ __global__ void __launch_bounds__(kRecWarps * 32) delta_recurrent_kernel(const D
             if (p.flags & DEP_DELTA_CHANNEL) {
                 const float4 g =
                     *reinterpret_cast<const float4 *>(p.g + t * p.gs + (int64_t)h * DK + 32 * c + 4 * l8);
-                a[c] = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+                a[c] = make_float4(decay(g.x), decay(g.y), decay(g.z), decay(g.w));
             }
         }
         if (!(p.flags & DEP_DELTA_CHANNEL)) {
-            const float e = expf(p.g[t * p.gs + h]);
+            const float e = decay(p.g[t * p.gs + h]);
 #pragma unroll
             for (int c = 0; c < NV; ++c)
                 a[c] = make_float4(e, e, e, e);
@@ -298,6 +301,27 @@ __device__ __forceinline__ void mma_f16x3(float (*const (&d)[N])[4], const uint3
     for (int n = 0; n < N; ++n)
         mma_f16(*d[n], ah, b[n].x, b[n].y);
 }
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Three BF16 parts of two values: all of FP32's 24 bits.
+__device__ __forceinline__ void bf16_split3(float a, float b, uint32_t &p0, uint32_t &p1, uint32_t &p2)
+{
+    const auto part = [](float &x, float &y) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&h);
+        x -= lo_bf(w);
+        y -= hi_bf(w);
+        return w;
+    };
+    p0 = part(a, b);
+    p1 = part(a, b);
+    p2 = part(a, b);
+}
 // The power of two that brings values of up to `top` below 2^14 (top's exponent to 13), and its
 // reciprocal.  Tops below 2^-107 count as that.
 __device__ __forceinline__ float scale_for(float top, float &inv)
@@ -313,6 +337,7 @@ __device__ __forceinline__ float row_max(float v)  // over the four lanes of a r
 }
 __device__ __forceinline__ float2 ld2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
+constexpr float kUnB = 16.f;  // B is stored times the scales of q and k, which make it up to 2^16, over this
 constexpr int kSort = 256;
 
 // The sequence of rank r by length, longest first: blocks start in order, and a long
@@ -343,20 +368,23 @@ __device__ __forceinline__ int longest_first(const DeltaParams &p, int r, int (&
 
 // What an MMA's lane (g, t) takes of a right operand, 16 bytes: FP16 parts of the k's 2t, 2t + 1
 // (x) and 2t + 8, 2t + 9 (y) of its sixteen, and the parts that those leave (z, w).
-template <int DK>
+template <int DK, int MW>
 struct ChunkStage {
-    // K.P and Q.P by token, sixteen channels after another, four lanes t each.  Rows are 64 bytes
+    // W and Q.P by token, sixteen channels after another, four lanes t each.  Rows are 64 bytes
     // off a multiple of 128, so that the eight lanes of a load phase meet no bank twice.
-    uint4 kp[kC][DK / 4 + 4], qp[kC][DK / 4 + 4];
-    uint4 kr[DK][4];               // K.R by channel; lane t at t ^ (channel / 2 % 4), for the same reason
-    float T[kC][kTS], B[kC][kTS];  // [token i][token j]
-    float last[DK];                // P_15
-    float ik[kC], iq[kC];          // what undoes the scales of k and q
+    uint4 w[kC][DK / 4 + 4], qp[kC][DK / 4 + 4];
+    uint4 kr[DK][4];  // K.R by channel; lane t at t ^ (channel / 2 % 4), for the same reason
+    uint4 B[kC][4];   // B by row
+    uint4 T01[kC][4]; // T by row, in BF16 parts: the first two,
+    uint2 T2[kC][4];  // and the third
+    uint16_t v[kC][16 * MW + 8];  // V as it is
+    float last[DK];               // P_15
+    float iw[kC], ik[kC], iq[kC]; // what undoes the scales of W, k and q
 };
-template <int DK>
+template <int DK, int MW>
 struct ChunkShared {
     static constexpr int KS = DK + 8;  // float2 reads without conflicts
-    ChunkStage<DK> stage[2];
+    ChunkStage<DK, MW> stage[2];
     struct {  // scratch of each group of preparing warps
         struct {  // operands of the products of one level (see below): rows k_i then q_i, columns k_j
             float row[16][KS], col[8][KS];
@@ -365,11 +393,10 @@ struct ChunkShared {
             float g[kC][DK];
             uint16_t k[kC][DK], q[kC][DK];
         } raw;
-        float A[kC][kC];
+        float A[kC][kC], T[kC][kTS];
         float part[4][48], norm[4][48], pow2[4][32], beta[kC], g[kC];
     } prep[2];
     int order[kSort + 1];
-    uint4 out[8][kC][2];  // a warp's rows of O, [token][16 rows in BF16]
 };
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
@@ -383,7 +410,7 @@ template <int DK, int MW>
 __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const DeltaParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    ChunkShared<DK> &sm = *reinterpret_cast<ChunkShared<DK> *>(smem_raw);
+    ChunkShared<DK, MW> &sm = *reinterpret_cast<ChunkShared<DK, MW> *>(smem_raw);
     constexpr int kThreads = kPrep + 32 * MW;  // that meet over a stage: its group, and the state's warps
     constexpr int kBarFull = 2, kBarEmpty = 4;
     const int slices = (p.Dv + 16 * MW - 1) / (16 * MW);
@@ -434,29 +461,28 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             r0 = scale_for(row_max(m0), i0);
             r1 = scale_for(row_max(m1), i1);
         }
-        const uint16_t *vp = p.v + t0 * p.vs + (int64_t)h * p.Dv + row0 + g;
-        // V^T in accumulator layout: rows g and g + 8, tokens 8 n + 2 t and + 1
-        auto load_v = [&](int c, uint32_t (&v)[2][2]) {
-            const int left = live ? (int)(len - (int64_t)c * kC < kC ? len - (int64_t)c * kC : kC) : 0;
-            const uint16_t *at = vp + (int64_t)c * kC * p.vs;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int a = 8 * n + 2 * t, b = a + 1;
-                const uint16_t *pa = at + a * p.vs, *pb = pa + p.vs;
-                const uint32_t lo0 = a < left ? pa[0] : 0, lo1 = a < left ? pa[8] : 0, hi0 = b < left ? pb[0] : 0,
-                               hi1 = b < left ? pb[8] : 0;
-                v[n][0] = lo0 | hi0 << 16;
-                v[n][1] = lo1 | hi1 << 16;
-            }
-        };
-        uint32_t v[2][2];
-        if (chunks)
-            load_v(0, v);
         for (int64_t c = 0; c < chunks; ++c) {
             const int st = (int)(c & 1);
             bar_sync(kBarFull + st, kThreads);
-            const ChunkStage<DK> &sg = sm.stage[st];
-            float X[2][4] = {}, O[2][4] = {};
+            const ChunkStage<DK, MW> &sg = sm.stage[st];
+            float U[2][4] = {}, X[2][4] = {}, O[2][4] = {};
+            {  // U^T = V^T T^T - S^T W^T, the first part
+                uint32_t a[4];
+                const uint32_t at = (uint32_t)__cvta_generic_to_shared(
+                    &sg.v[(lane >> 4) * 8 + (lane & 7)][16 * warp + 8 * (lane >> 3 & 1)]);
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                             : "r"(at)
+                             : "memory");
+                const uint4 b0 = sg.T01[g][t], b1 = sg.T01[8 + g][t];
+                const uint2 c0 = sg.T2[g][t], c1 = sg.T2[8 + g][t];
+                mma_bf16(U[0], a, c0.x, c0.y);
+                mma_bf16(U[1], a, c1.x, c1.y);
+                mma_bf16(U[0], a, b0.z, b0.w);
+                mma_bf16(U[1], a, b1.z, b1.w);
+                mma_bf16(U[0], a, b0.x, b0.y);
+                mma_bf16(U[1], a, b1.x, b1.y);
+            }
 #pragma unroll
             for (int ks = 0; ks < NT / 2; ++ks) {
                 uint32_t ah[4], al[4];
@@ -466,59 +492,39 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     f16_split2(S[2 * ks + i][2] * r1, S[2 * ks + i][3] * r1, ah[2 * i + 1], al[2 * i + 1]);
                 }
                 float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
-                const uint4 b[4] = {sg.kp[g][4 * ks + t], sg.qp[g][4 * ks + t], sg.kp[8 + g][4 * ks + t],
+                const uint4 b[4] = {sg.w[g][4 * ks + t], sg.qp[g][4 * ks + t], sg.w[8 + g][4 * ks + t],
                                     sg.qp[8 + g][4 * ks + t]};
                 mma_f16x3(d, ah, al, b);
             }
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float2 ik = ld2(&sg.ik[8 * n + 2 * t]), iq = ld2(&sg.iq[8 * n + 2 * t]);
-                X[n][0] *= ik.x * i0, X[n][1] *= ik.y * i0, X[n][2] *= ik.x * i1, X[n][3] *= ik.y * i1;
-                O[n][0] *= iq.x * i0, O[n][1] *= iq.y * i0, O[n][2] *= iq.x * i1, O[n][3] *= iq.y * i1;
-            }
-            // Y = V - X, then U^T = Y^T T^T and O^T += U^T B^T (both lower triangular: tokens j <= i)
-            uint32_t uh[2][4], ul[2][4];
-            float U[2][4] = {};
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    X[n][j] = __uint_as_float(j & 1 ? v[n][j >> 1] & 0xFFFF0000u : v[n][j >> 1] << 16) - X[n][j];
-                split_a(X[n], uh[n], ul[n]);
-            }
-            if (c + 1 < chunks)
-                load_v((int)c + 1, v);
+            // U' = U / (k's scale), in parts scaled by row: the left operand of B and of K.R
+            uint32_t uh[4], ul[4];
+            float j0, j1;
             {
-                float(*const d[2])[4] = {&U[0], &U[1]};
-                const float2 b[2] = {ld2(&sg.T[g][2 * t]), ld2(&sg.T[8 + g][2 * t])};
-                mma_tf32x3(d, uh[0], ul[0], b);
-                float(*const d1[1])[4] = {&U[1]};
-                const float2 b1[1] = {ld2(&sg.T[8 + g][8 + 2 * t])};
-                mma_tf32x3(d1, uh[1], ul[1], b1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 iw = ld2(&sg.iw[8 * n + 2 * t]), ik = ld2(&sg.ik[8 * n + 2 * t]);
+                    U[n][0] = fmaf(X[n][0] * i0, -iw.x, U[n][0]) * ik.x;
+                    U[n][1] = fmaf(X[n][1] * i0, -iw.y, U[n][1]) * ik.y;
+                    U[n][2] = fmaf(X[n][2] * i1, -iw.x, U[n][2]) * ik.x;
+                    U[n][3] = fmaf(X[n][3] * i1, -iw.y, U[n][3]) * ik.y;
+                }
+                const float s0 = scale_for(
+                    row_max(fmaxf(fmaxf(fabsf(U[0][0]), fabsf(U[0][1])), fmaxf(fabsf(U[1][0]), fabsf(U[1][1])))), j0);
+                const float s1 = scale_for(
+                    row_max(fmaxf(fmaxf(fabsf(U[0][2]), fabsf(U[0][3])), fmaxf(fabsf(U[1][2]), fabsf(U[1][3])))), j1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    f16_split2(U[n][0] * s0, U[n][1] * s0, uh[2 * n], ul[2 * n]);
+                    f16_split2(U[n][2] * s1, U[n][3] * s1, uh[2 * n + 1], ul[2 * n + 1]);
+                }
             }
-            split_a(U[0], uh[0], ul[0]);
-            split_a(U[1], uh[1], ul[1]);
+            float D[2][4] = {};  // U^T B^T
             {
-                float(*const d[2])[4] = {&O[0], &O[1]};
-                const float2 b[2] = {ld2(&sg.B[g][2 * t]), ld2(&sg.B[8 + g][2 * t])};
-                mma_tf32x3(d, uh[0], ul[0], b);
-                float(*const d1[1])[4] = {&O[1]};
-                const float2 b1[1] = {ld2(&sg.B[8 + g][8 + 2 * t])};
-                mma_tf32x3(d1, uh[1], ul[1], b1);
+                float(*const d[2])[4] = {&D[0], &D[1]};
+                const uint4 b[2] = {sg.B[g][t], sg.B[8 + g][t]};
+                mma_f16x3(d, uh, ul, b);
             }
-            // S <- S diag(P_15) + U^T (K.R): k's scale comes off U, whose rows get scales of their own
-            {
-                const float2 k0 = ld2(&sg.ik[2 * t]), k1 = ld2(&sg.ik[8 + 2 * t]);
-                const float u[8] = {U[0][0] * k0.x, U[0][1] * k0.y, U[1][0] * k1.x, U[1][1] * k1.y,
-                                    U[0][2] * k0.x, U[0][3] * k0.y, U[1][2] * k1.x, U[1][3] * k1.y};
-                float j0, j1;
-                const float s0 = scale_for(row_max(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3])))), j0);
-                const float s1 = scale_for(row_max(fmaxf(fmaxf(fabsf(u[4]), fabsf(u[5])), fmaxf(fabsf(u[6]), fabsf(u[7])))), j1);
-                uint32_t ah[4], al[4];
-                f16_split2(u[0] * s0, u[1] * s0, ah[0], al[0]);
-                f16_split2(u[4] * s1, u[5] * s1, ah[1], al[1]);
-                f16_split2(u[2] * s0, u[3] * s0, ah[2], al[2]);
-                f16_split2(u[6] * s1, u[7] * s1, ah[3], al[3]);
+            {  // S <- S diag(P_15) + U^T (K.R)
                 float m0 = 0.f, m1 = 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; n += 4) {
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     const int sw = t ^ (g >> 1 & 3);
                     const uint4 b[4] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw], sg.kr[8 * n + 16 + g][sw],
                                         sg.kr[8 * n + 24 + g][sw]};
-                    mma_f16x3(d, ah, al, b);
+                    mma_f16x3(d, uh, ul, b);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
@@ -540,11 +546,18 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                         m1 = fmaxf(m1, fmaxf(fabsf(s[2]), fabsf(s[3])));
                     }
                 }
+                // O = Q.P S^T + U' B', each with its scales
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
+                    O[n][0] = fmaf(D[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
+                    O[n][1] = fmaf(D[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
+                    O[n][2] = fmaf(D[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
+                    O[n][3] = fmaf(D[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
+                }
                 r0 = scale_for(row_max(m0), i0);
                 r1 = scale_for(row_max(m1), i1);
             }
-            if (c + 2 < chunks)
-                bar_arrive(kBarEmpty + st, kThreads);
             // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
             uint32_t r[4];
 #pragma unroll
@@ -552,9 +565,8 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n]) : "f"(O[n][1]), "f"(O[n][0]));
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n + 1]) : "f"(O[n][3]), "f"(O[n][2]));
             }
-            const uint32_t at =
-                (uint32_t)__cvta_generic_to_shared(&sm.out[warp][(lane >> 4) * 8 + (lane & 7)][(lane >> 3) & 1]);
-            __syncwarp();
+            const uint32_t at = (uint32_t)__cvta_generic_to_shared(
+                &sg.v[(lane >> 4) * 8 + (lane & 7)][16 * warp + 8 * (lane >> 3 & 1)]);  // over the warp's part of V
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]),
                          "r"(r[1]), "r"(r[2]), "r"(r[3])
                          : "memory");
@@ -562,7 +574,9 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             const int64_t tok = c * kC + (lane >> 1);
             if (live && tok < len)
                 *reinterpret_cast<uint4 *>(p.o + (t0 + tok) * p.os + (int64_t)h * p.Dv + row0 + 8 * (lane & 1)) =
-                    sm.out[warp][lane >> 1][lane & 1];
+                    *reinterpret_cast<const uint4 *>(&sg.v[lane >> 1][16 * warp + 8 * (lane & 1)]);
+            if (c + 2 < chunks)
+                bar_arrive(kBarEmpty + st, kThreads);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -611,13 +625,22 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 gv = !chan && pt < left ? gp[(first + pt) * p.gs] : 0.f;
             }
         };
-        ChunkStage<DK> &sg = sm.stage[grp];
-        for (int i = pt; i < kC * kTS; i += kPrep) {  // above the diagonal T and B stay zero
-            (&sg.T[0][0])[i] = 0.f;
-            (&sg.B[0][0])[i] = 0.f;
-        }
+        ChunkStage<DK, MW> &sg = sm.stage[grp];
+        for (int i = pt; i < kC * 4; i += kPrep)  // above the diagonal B stays zero
+            (&sg.B[0][0])[i] = make_uint4(0, 0, 0, 0);
         for (int i = pt; i < kC * kC; i += kPrep)
             (&pr.A[0][0])[i] = 0.f;
+        auto put_b = [&](int i, int j, float v) {  // B_ij into its lane's sixteen bytes
+            uint32_t hi, lo;
+            f16_split2(v * (pr.pow2[pw][16 + i] * pr.pow2[pw][j] * (1.f / kUnB)), 0.f, hi, lo);
+            uint16_t *d = reinterpret_cast<uint16_t *>(&sg.B[i][(j & 7) >> 1]) + (j >> 3) * 2 + (j & 1);
+            d[0] = (uint16_t)hi;
+            d[4] = (uint16_t)lo;
+        };
+        // this channel's place in a row of W or Q.P, in FP16 numbers: its lane's sixteen bytes
+        const int c16 = pt & 15, at = ((pt >> 4) * 4 + ((c16 & 7) >> 1)) * 8 + (c16 >> 3) * 2 + (c16 & 1);
+        const int rows0 = slice * 16 * MW, rows = p.Dv - rows0 < 16 * MW ? p.Dv - rows0 : 16 * MW;
+        const uint16_t *vp = p.v + t0 * p.vs + (int64_t)h * p.Dv + rows0;
         if (grp < chunks)
             fetch(grp);
         for (int64_t c = grp; c < chunks; c += 2) {
@@ -628,12 +651,12 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             bar_sync(kBarPrep, kPrep);
-            float k[kC], q[kC], a[kC];
+            float k[kC], q[kC], a[kC], kp[kC];  // kp: K.P
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
                 k[i] = ch ? __uint_as_float((uint32_t)raw.k[i][pt] << 16) : 0.f;
                 q[i] = ch ? __uint_as_float((uint32_t)raw.q[i][pt] << 16) : 0.f;
-                a[i] = expf(!chan ? pr.g[i] : ch ? raw.g[i][pt] : 0.f);
+                a[i] = decay(!chan ? pr.g[i] : ch ? raw.g[i][pt] : 0.f);
             }
             {
                 // Sums over the channels: lane l of a warp gets token l % 16's, of k k or q q, and of k q
@@ -683,8 +706,19 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             }
             if (c >= 2)
                 bar_sync(kBarEmpty + grp, kThreads);
+            {  // V, straight into the stage
+                const int64_t first = c * kC;
+                const int left = (int)(len - first < kC ? len - first : kC);
+#pragma unroll
+                for (int i = pt; i < kC * 2 * MW; i += kPrep) {
+                    const int tok = i / (2 * MW), e = i % (2 * MW) * 8;
+                    const bool in = tok < left && e < rows;
+                    cp_async16(&sg.v[tok][e], vp + (first + (in ? tok : 0)) * p.vs + (in ? e : 0), in);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
             if (pt < kC)
-                sg.B[pt][pt] = pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt];
+                put_b(pt, pt, pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt]);
             if (pt < 32)
                 (pt < 16 ? sg.ik : sg.iq)[pt & 15] = 1.f / pr.pow2[pw][pt];
 #pragma unroll
@@ -694,19 +728,15 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             }
             if (ch) {
                 float P = 1.f;
-                // this channel's places: FP16 number `sub` of lane t's, in its sixteen channels
-                const int c16 = pt & 15, at = ((pt >> 4) * 4 + ((c16 & 7) >> 1)) * 8 + (c16 >> 3) * 2 + (c16 & 1);
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
                     P *= a[i];
-                    uint32_t hi, lo;  // k's and q's
-                    f16_split2(k[i] * (P * pr.pow2[pw][i]), q[i] * (P * pr.pow2[pw][16 + i]), hi, lo);
-                    uint16_t *kd = reinterpret_cast<uint16_t *>(&sg.kp[i][0]) + at;
+                    kp[i] = k[i] * P;
+                    uint32_t hi, lo;
+                    f16_split2(q[i] * (P * pr.pow2[pw][16 + i]), 0.f, hi, lo);
                     uint16_t *qd = reinterpret_cast<uint16_t *>(&sg.qp[i][0]) + at;
-                    kd[0] = (uint16_t)hi;
-                    kd[4] = (uint16_t)lo;
-                    qd[0] = (uint16_t)(hi >> 16);
-                    qd[4] = (uint16_t)(lo >> 16);
+                    qd[0] = (uint16_t)hi;
+                    qd[4] = (uint16_t)lo;
                 }
                 sg.last[pt] = P;
 #pragma unroll
@@ -764,7 +794,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
                     if ((n & ~(b - 1)) == (g & ~(b - 1))) {
                         pr.A[i][j] = d[0][e] + d[1][e];
-                        sg.B[i][j] = d[0][2 + e] + d[1][2 + e];
+                        put_b(i, j, d[0][2 + e] + d[1][2 + e]);
                     }
                 }
             }
@@ -784,8 +814,45 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 if (lane < 16)
 #pragma unroll
                     for (int i = 0; i < kC; ++i)
-                        sg.T[i][j] = i >= j ? x[i] * b : 0.f;
+                        pr.T[i][j] = i >= j ? x[i] * b : 0.f;
             }
+            bar_sync(kBarPrep, kPrep);
+            if (pt < 4 * kC) {  // T for the state's warps
+                const int i = pt >> 2, t = pt & 3;
+                const float2 a = ld2(&pr.T[i][2 * t]), b = ld2(&pr.T[i][2 * t + 8]);
+                uint4 p01;
+                uint2 p2;
+                bf16_split3(a.x, a.y, p01.x, p01.z, p2.x);
+                bf16_split3(b.x, b.y, p01.y, p01.w, p2.y);
+                sg.T01[i][t] = p01;
+                sg.T2[i][t] = p2;
+            }
+            {
+                // |W_i| <= sum_j |T_ij| times the bound on k_j's values (2^8 over its scale)
+                float top = 0.f, inv;
+                if (lane < kC)
+#pragma unroll
+                    for (int j = 0; j < kC; ++j)
+                        top = fmaf(fabsf(pr.T[lane][j]), 256.f / pr.pow2[pw][j], top);
+                const float s = scale_for(top, inv);
+                if (pw == 0 && lane < kC)
+                    sg.iw[lane] = inv;
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    float w = 0.f;
+#pragma unroll
+                    for (int j = 0; j <= i; ++j)
+                        w = fmaf(pr.T[i][j], kp[j], w);
+                    uint32_t hi, lo;
+                    f16_split2(w * __shfl_sync(~0u, s, i), 0.f, hi, lo);
+                    if (ch) {
+                        uint16_t *d = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
+                        d[0] = (uint16_t)hi;
+                        d[4] = (uint16_t)lo;
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");  // V
             bar_arrive(kBarFull + grp, kThreads);
         }
     }
@@ -794,6 +861,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
 template <int DK, int MW>
 cudaError_t chunk_launch(const DeltaParams &p, cudaStream_t s)
 {
+    static_assert(sizeof(ChunkShared<DK, MW>) <= kMaxDynamicSmem, "");
     static std::atomic<uint64_t> devices{0};
     cudaError_t e = set_smem_attr(delta_chunk_kernel<DK, MW>, devices);
     if (e != cudaSuccess)
@@ -801,7 +869,7 @@ cudaError_t chunk_launch(const DeltaParams &p, cudaStream_t s)
     const int64_t blocks = (int64_t)((p.Dv + 16 * MW - 1) / (16 * MW)) * p.Hv * p.n_seq;
     if (blocks > INT32_MAX)
         return cudaErrorInvalidConfiguration;
-    delta_chunk_kernel<DK, MW><<<(unsigned)blocks, 2 * kPrep + 32 * MW, sizeof(ChunkShared<DK>), s>>>(p);
+    delta_chunk_kernel<DK, MW><<<(unsigned)blocks, 2 * kPrep + 32 * MW, sizeof(ChunkShared<DK, MW>), s>>>(p);
     return cudaGetLastError();
 }
 
