@@ -248,28 +248,6 @@ __device__ __forceinline__ void split_a(const float (&c)[4], uint32_t (&hi)[4], 
     tf32_split(c[1], hi[2], lo[2]);
     tf32_split(c[3], hi[3], lo[3]);
 }
-// N products d[n] += a b[n], each as three: the small ones first, and those of one d N MMAs
-// apart (an MMA takes 24 cycles, a warp issues one in 8).
-template <int N>
-__device__ __forceinline__ void mma_tf32x3(float (*const (&d)[N])[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
-                                           const float2 (&b)[N])
-{
-    uint32_t h[N][2], l[N][2];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        tf32_split(b[n].x, h[n][0], l[n][0]);
-        tf32_split(b[n].y, h[n][1], l[n][1]);
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        mma_tf32(*d[n], al, h[n][0], h[n][1]);
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        mma_tf32(*d[n], ah, l[n][0], l[n][1]);
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        mma_tf32(*d[n], ah, h[n][0], h[n][1]);
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -286,7 +264,8 @@ __device__ __forceinline__ void f16_split2(float a, float b, uint32_t &hi, uint3
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
-// N products d[n] += a b[n] of FP16 parts, three MMAs each.
+// N products d[n] += a b[n] of FP16 parts, each as three: the small ones first, and those of one d
+// N MMAs apart (an MMA takes 24 cycles, a warp issues one in 8).
 template <int N>
 __device__ __forceinline__ void mma_f16x3(float (*const (&d)[N])[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
                                           const uint4 (&b)[N])
@@ -330,6 +309,12 @@ __device__ __forceinline__ float scale_for(float top, float &inv)
     inv = __uint_as_float((uint32_t)(e - 13) << 23);
     return __uint_as_float((uint32_t)(267 - e) << 23);
 }
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float row_max(float v)  // over the four lanes of a row
 {
     v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
@@ -338,6 +323,7 @@ __device__ __forceinline__ float row_max(float v)  // over the four lanes of a r
 __device__ __forceinline__ float2 ld2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
 constexpr float kUnB = 16.f;  // B is stored times the scales of q and k, which make it up to 2^16, over this
+constexpr float kMostScale = 0x1p64f;  // of a row of S
 constexpr int kSort = 256;
 
 // The sequence of rank r by length, longest first: blocks start in order, and a long
@@ -389,12 +375,12 @@ struct ChunkShared {
         struct {  // operands of the products of one level (see below): rows k_i then q_i, columns k_j
             float row[16][KS], col[8][KS];
         } level[4];
-        struct {  // a chunk's tokens as they are
+        struct {  // a chunk's tokens as they are; rows off by 16 bytes for ldmatrix
             float g[kC][DK];
-            uint16_t k[kC][DK], q[kC][DK];
+            uint16_t k[kC][DK + 8], q[kC][DK + 8];
         } raw;
-        float A[kC][kC], T[kC][kTS];
-        float part[4][48], norm[4][48], pow2[4][32], beta[kC], g[kC];
+        alignas(16) float A[kC][kC], T[kC][kTS];
+        alignas(16) float part[4][48], norm[4][48], pow2[4][32], beta[kC], g[kC];
     } prep[2];
     int order[kSort + 1];
 };
@@ -450,16 +436,35 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             S[n][2] = b.x;
             S[n][3] = b.y;
         }
-        float r0, r1, i0, i1;  // scales of rows g and g + 8, and what undoes them
+        // S is held times a power of two for each row: r0 for row g, r1 for row g + 8, such that the row's largest
+        // value lies in [2^8, 2^15), or the scale at its limit.
+        float r0 = 1.f, r1 = 1.f, i0 = 1.f, i1 = 1.f;  // the scales, and what undoes them
+        auto rescale = [&](float f0, float f1) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                S[n][0] *= f0, S[n][1] *= f0, S[n][2] *= f1, S[n][3] *= f1;
+            r0 *= f0, r1 *= f1;
+            i0 = 1.f / r0, i1 = 1.f / r1;
+        };
+        auto factor = [](float top, float r) {  // what brings a row back into its range
+            float inv;
+            return top >= 32768.f || (top < 256.f && top > 0.f && r < kMostScale)
+                       ? fminf(scale_for(top, inv), kMostScale / r)
+                       : 1.f;
+        };
+        auto keep_range = [&](float m0, float m1) {  // the lane's largest values of both rows
+            const float f0 = factor(row_max(m0), r0), f1 = factor(row_max(m1), r1);
+            if (__any_sync(~0u, f0 != 1.f || f1 != 1.f))
+                rescale(f0, f1);
+        };
         {
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                m0 = fmaxf(m0, fmaxf(fabsf(S[n][0]), fabsf(S[n][1])));
-                m1 = fmaxf(m1, fmaxf(fabsf(S[n][2]), fabsf(S[n][3])));
+                m0 = max3_abs(m0, S[n][0], S[n][1]);
+                m1 = max3_abs(m1, S[n][2], S[n][3]);
             }
-            r0 = scale_for(row_max(m0), i0);
-            r1 = scale_for(row_max(m1), i1);
+            keep_range(m0, m1);
         }
         for (int64_t c = 0; c < chunks; ++c) {
             const int st = (int)(c & 1);
@@ -488,8 +493,8 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 uint32_t ah[4], al[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    f16_split2(S[2 * ks + i][0] * r0, S[2 * ks + i][1] * r0, ah[2 * i], al[2 * i]);
-                    f16_split2(S[2 * ks + i][2] * r1, S[2 * ks + i][3] * r1, ah[2 * i + 1], al[2 * i + 1]);
+                    f16_split2(S[2 * ks + i][0], S[2 * ks + i][1], ah[2 * i], al[2 * i]);
+                    f16_split2(S[2 * ks + i][2], S[2 * ks + i][3], ah[2 * i + 1], al[2 * i + 1]);
                 }
                 float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
                 const uint4 b[4] = {sg.w[g][4 * ks + t], sg.qp[g][4 * ks + t], sg.w[8 + g][4 * ks + t],
@@ -524,7 +529,21 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 const uint4 b[2] = {sg.B[g][t], sg.B[8 + g][t]};
                 mma_f16x3(d, uh, ul, b);
             }
+            // O = Q.P S^T + U' B', each with its scales
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
+                O[n][0] = fmaf(D[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
+                O[n][1] = fmaf(D[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
+                O[n][2] = fmaf(D[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
+                O[n][3] = fmaf(D[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
+            }
             {  // S <- S diag(P_15) + U^T (K.R)
+                if (__any_sync(~0u, j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
+                    // U beyond what S's scales leave room for: make room
+                    rescale(j0 > 0x1p60f * i0 ? 0x1p60f * i0 / j0 : 1.f, j1 > 0x1p60f * i1 ? 0x1p60f * i1 / j1 : 1.f);
+                }
+                const float f0 = j0 * r0, f1 = j1 * r1;
                 float m0 = 0.f, m1 = 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; n += 4) {
@@ -538,25 +557,15 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     for (int i = 0; i < 4; ++i) {
                         const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
                         float(&s)[4] = S[n + i];
-                        s[0] = fmaf(D[i][0], j0, s[0] * a.x);
-                        s[1] = fmaf(D[i][1], j0, s[1] * a.y);
-                        s[2] = fmaf(D[i][2], j1, s[2] * a.x);
-                        s[3] = fmaf(D[i][3], j1, s[3] * a.y);
-                        m0 = fmaxf(m0, fmaxf(fabsf(s[0]), fabsf(s[1])));
-                        m1 = fmaxf(m1, fmaxf(fabsf(s[2]), fabsf(s[3])));
+                        s[0] = fmaf(D[i][0], f0, s[0] * a.x);
+                        s[1] = fmaf(D[i][1], f0, s[1] * a.y);
+                        s[2] = fmaf(D[i][2], f1, s[2] * a.x);
+                        s[3] = fmaf(D[i][3], f1, s[3] * a.y);
+                        m0 = max3_abs(m0, s[0], s[1]);
+                        m1 = max3_abs(m1, s[2], s[3]);
                     }
                 }
-                // O = Q.P S^T + U' B', each with its scales
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
-                    O[n][0] = fmaf(D[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
-                    O[n][1] = fmaf(D[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
-                    O[n][2] = fmaf(D[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
-                    O[n][3] = fmaf(D[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
-                }
-                r0 = scale_for(row_max(m0), i0);
-                r1 = scale_for(row_max(m1), i1);
+                keep_range(m0, m1);
             }
             // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
             uint32_t r[4];
@@ -582,9 +591,9 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
         for (int n = 0; n < NT; ++n)
             if (live) {
                 *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g) * DK + 8 * n + 2 * t) =
-                    make_float2(S[n][0], S[n][1]);
+                    make_float2(S[n][0] * i0, S[n][1] * i0);
                 *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g + 8) * DK + 8 * n + 2 * t) =
-                    make_float2(S[n][2], S[n][3]);
+                    make_float2(S[n][2] * i1, S[n][3] * i1);
             }
     } else {
         // ---------------- the next chunk's operands ----------------
@@ -596,7 +605,10 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
         const int grp = (threadIdx.x - 32 * MW) / kPrep, pt = (threadIdx.x - 32 * MW) % kPrep, pw = pt >> 5;
         const int kBarPrep = 6 + grp;
         auto &pr = sm.prep[grp];
-        const bool ch = pt < DK;  // thread = channel
+        // A thread works on one channel; of 64 channels two threads each, one with what tokens need
+        // (Q.P, W), the other with what pairs need (the levels, K.R).
+        const int ch = pt % DK;
+        const bool tokens = pt < DK, pairs = pt >= kPrep - DK;
         const int hq = h / (p.Hv / p.Hq);
         const uint16_t *kp = p.k + t0 * p.ks + (int64_t)hq * DK, *qp = p.q + t0 * p.qs + (int64_t)hq * DK;
         const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK : h);
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             d[4] = (uint16_t)lo;
         };
         // this channel's place in a row of W or Q.P, in FP16 numbers: its lane's sixteen bytes
-        const int c16 = pt & 15, at = ((pt >> 4) * 4 + ((c16 & 7) >> 1)) * 8 + (c16 >> 3) * 2 + (c16 & 1);
+        const int c16 = ch & 15, at = ((ch >> 4) * 4 + ((c16 & 7) >> 1)) * 8 + (c16 >> 3) * 2 + (c16 & 1);
         const int rows0 = slice * 16 * MW, rows = p.Dv - rows0 < 16 * MW ? p.Dv - rows0 : 16 * MW;
         const uint16_t *vp = p.v + t0 * p.vs + (int64_t)h * p.Dv + rows0;
         if (grp < chunks)
@@ -654,41 +666,44 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             float k[kC], q[kC], a[kC], kp[kC];  // kp: K.P
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
-                k[i] = ch ? __uint_as_float((uint32_t)raw.k[i][pt] << 16) : 0.f;
-                q[i] = ch ? __uint_as_float((uint32_t)raw.q[i][pt] << 16) : 0.f;
-                a[i] = decay(!chan ? pr.g[i] : ch ? raw.g[i][pt] : 0.f);
+                k[i] = __uint_as_float((uint32_t)raw.k[i][ch] << 16);
+                q[i] = __uint_as_float((uint32_t)raw.q[i][ch] << 16);
+                a[i] = decay(chan ? raw.g[i][ch] : pr.g[i]);
             }
             {
-                // Sums over the channels: lane l of a warp gets token l % 16's, of k k or q q, and of k q
-                float v[32], w[16];
+                // Each token's sums of k k, q q and k q over the channels: the diagonals of products of the BF16
+                // rows with themselves, warp pw a quarter of the channels.  A left operand's registers hold the
+                // right operands of its two halves, too.
+                constexpr int KW = DK / 64;  // steps of 16 channels
+                float kk[2][4] = {}, qq[2][4] = {}, kq[2][4] = {};
 #pragma unroll
-                for (int i = 0; i < kC; ++i) {
-                    v[i] = k[i] * k[i];
-                    v[16 + i] = q[i] * q[i];
-                    w[i] = k[i] * q[i];
-                }
+                for (int i = 0; i < KW; ++i) {
+                    const int col = (pw * KW + i) * 16 + 8 * (lane >> 4), row = lane & 15;
+                    uint32_t x[4], y[4];
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                 : "r"((uint32_t)__cvta_generic_to_shared(&raw.k[row][col]))
+                                 : "memory");
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                                 : "r"((uint32_t)__cvta_generic_to_shared(&raw.q[row][col]))
+                                 : "memory");
 #pragma unroll
-                for (int n = 16; n; n >>= 1) {
-                    const bool up = (lane & n) != 0;
-#pragma unroll
-                    for (int i = 0; i < n; ++i) {
-                        const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-                        v[i] = keep + __shfl_xor_sync(~0u, send, n);
+                    for (int n = 0; n < 2; ++n) {
+                        mma_bf16(kk[n], x, x[n], x[2 + n]);
+                        mma_bf16(qq[n], y, y[n], y[2 + n]);
+                        mma_bf16(kq[n], x, y[n], y[2 + n]);
                     }
                 }
+                const int g = lane >> 2;
+                if ((lane & 3) == g >> 1) {  // this lane holds the diagonal at g and g + 8
 #pragma unroll
-                for (int n = 8; n; n >>= 1) {
-                    const bool up = (lane & n) != 0;
-#pragma unroll
-                    for (int i = 0; i < n; ++i) {
-                        const float send = up ? w[i] : w[i + n], keep = up ? w[i + n] : w[i];
-                        w[i] = keep + __shfl_xor_sync(~0u, send, n);
+                    for (int n = 0; n < 2; ++n) {
+                        pr.part[pw][8 * n + g] = g & 1 ? kk[n][2 * n + 1] : kk[n][2 * n];
+                        pr.part[pw][16 + 8 * n + g] = g & 1 ? qq[n][2 * n + 1] : qq[n][2 * n];
+                        pr.part[pw][32 + 8 * n + g] = g & 1 ? kq[n][2 * n + 1] : kq[n][2 * n];
                     }
                 }
-                w[0] += __shfl_xor_sync(~0u, w[0], 16);
-                pr.part[pw][lane] = v[0];
-                if (lane < 16)
-                    pr.part[pw][32 + lane] = w[0];
                 bar_sync(kBarPrep, kPrep);
                 if (c + 2 < chunks)
                     fetch(c + 2);
@@ -721,12 +736,20 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 put_b(pt, pt, pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt]);
             if (pt < 32)
                 (pt < 16 ? sg.ik : sg.iq)[pt & 15] = 1.f / pr.pow2[pw][pt];
+            float pk[kC];  // k's scales
 #pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                k[i] *= pr.norm[pw][i];
-                q[i] *= pr.norm[pw][16 + i];
+            for (int i = 0; i < kC; i += 4) {
+                const float4 nk = *reinterpret_cast<const float4 *>(&pr.norm[pw][i]);
+                const float4 nq = *reinterpret_cast<const float4 *>(&pr.norm[pw][16 + i]);
+                const float4 sk = *reinterpret_cast<const float4 *>(&pr.pow2[pw][i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    k[i + e] *= (&nk.x)[e];
+                    q[i + e] *= (&nq.x)[e];
+                    pk[i + e] = (&sk.x)[e];
+                }
             }
-            if (ch) {
+            if (tokens) {
                 float P = 1.f;
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
@@ -738,7 +761,9 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     qd[0] = (uint16_t)hi;
                     qd[4] = (uint16_t)lo;
                 }
-                sg.last[pt] = P;
+                sg.last[ch] = P;
+            }
+            if (pairs) {
 #pragma unroll
                 for (int l = 0; l < 4; ++l) {
                     const int b = 1 << l;
@@ -747,20 +772,20 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     for (int r = 0; r < 8; ++r) {
                         const int i = (r & ~(b - 1)) << 1 | b | (r & (b - 1));
                         f = i % b == 0 ? a[i] : f * a[i];
-                        pr.level[l].row[r][pt] = k[i] * f;
-                        pr.level[l].row[8 + r][pt] = q[i] * f;
+                        pr.level[l].row[r][ch] = k[i] * f;
+                        pr.level[l].row[8 + r][ch] = q[i] * f;
                     }
 #pragma unroll
                     for (int n = 7; n >= 0; --n) {
                         const int j = (n & ~(b - 1)) << 1 | (n & (b - 1));
                         f = j % b == b - 1 ? 1.f : f * a[j + 1];
-                        pr.level[l].col[n][pt] = k[j] * f;
+                        pr.level[l].col[n][ch] = k[j] * f;
                     }
                 }
                 float R = 1.f;
 #pragma unroll
                 for (int i = kC - 1; i >= 0; --i) {
-                    k[i] *= R * pr.pow2[pw][i];
+                    k[i] *= R * pk[i];
                     R *= a[i];
                 }
 #pragma unroll
@@ -768,14 +793,14 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     uint4 v;
                     f16_split2(k[2 * t], k[2 * t + 1], v.x, v.z);
                     f16_split2(k[2 * t + 8], k[2 * t + 9], v.y, v.w);
-                    sg.kr[pt][t ^ (pt >> 1 & 3)] = v;
+                    sg.kr[ch][t ^ (ch >> 1 & 3)] = v;
                 }
             }
             bar_sync(kBarPrep, kPrep);
             {  // warp pw: level pw
                 const int g = lane >> 2, t = lane & 3, b = 1 << pw;
                 const auto &lv = pr.level[pw];
-                float d[2][4] = {};
+                float d[3][4] = {};  // one for each of the three products
 #pragma unroll
                 for (int ks = 0; ks < DK / 8; ++ks) {
                     const float2 lo = *reinterpret_cast<const float2 *>(&lv.row[g][8 * ks + 2 * t]);
@@ -784,17 +809,20 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     const float c4[4] = {lo.x, lo.y, hi.x, hi.y};
                     uint32_t ah[4], al[4];
                     split_a(c4, ah, al);
-                    float(*const dd[1])[4] = {&d[ks & 1]};
-                    const float2 b1[1] = {cb};
-                    mma_tf32x3(dd, ah, al, b1);
+                    uint32_t h0, l0, h1, l1;
+                    tf32_split(cb.x, h0, l0);
+                    tf32_split(cb.y, h1, l1);
+                    mma_tf32(d[2], al, h0, h1);
+                    mma_tf32(d[1], ah, l0, l1);
+                    mma_tf32(d[0], ah, h0, h1);
                 }
                 const int i = (g & ~(b - 1)) << 1 | b | (g & (b - 1));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
                     if ((n & ~(b - 1)) == (g & ~(b - 1))) {
-                        pr.A[i][j] = d[0][e] + d[1][e];
-                        put_b(i, j, d[0][2 + e] + d[1][2 + e]);
+                        pr.A[i][j] = (d[2][e] + d[1][e]) + d[0][e];
+                        put_b(i, j, (d[2][2 + e] + d[1][2 + e]) + d[0][2 + e]);
                     }
                 }
             }
@@ -806,8 +834,12 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 for (int i = 0; i < kC; ++i) {
                     float d0 = 0.f, d1 = 0.f;
 #pragma unroll
-                    for (int m = 0; m < i; ++m)
-                        (m & 1 ? d1 : d0) = fmaf(pr.A[i][m], x[m], m & 1 ? d1 : d0);
+                    for (int m = 0; m < i; m += 4) {
+                        const float4 r = *reinterpret_cast<const float4 *>(&pr.A[i][m]);
+#pragma unroll
+                        for (int e = 0; e < 4 && m + e < i; ++e)
+                            (e & 1 ? d1 : d0) = fmaf((&r.x)[e], x[m + e], e & 1 ? d1 : d0);
+                    }
                     x[i] = (i == j ? 1.f : 0.f) - pr.beta[i] * (d0 + d1);
                 }
                 const float b = pr.beta[j];
@@ -841,11 +873,15 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 for (int i = 0; i < kC; ++i) {
                     float w = 0.f;
 #pragma unroll
-                    for (int j = 0; j <= i; ++j)
-                        w = fmaf(pr.T[i][j], kp[j], w);
+                    for (int j = 0; j <= i; j += 4) {
+                        const float4 r = *reinterpret_cast<const float4 *>(&pr.T[i][j]);
+#pragma unroll
+                        for (int e = 0; e < 4 && j + e <= i; ++e)
+                            w = fmaf((&r.x)[e], kp[j + e], w);
+                    }
                     uint32_t hi, lo;
                     f16_split2(w * __shfl_sync(~0u, s, i), 0.f, hi, lo);
-                    if (ch) {
+                    if (tokens) {
                         uint16_t *d = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
                         d[0] = (uint16_t)hi;
                         d[4] = (uint16_t)lo;
