@@ -7,7 +7,8 @@
 //
 // Recurrent kernel.  A group of eight lanes holds a row (Dk / 8 channels a lane,
 // in chunks of four so that a group reads 128 consecutive bytes); a warp holds
-// 4 * SETS rows.  The two dot products S k and S q are taken of the decayed state
+// 4 * SETS rows.  The block turns a token's k, q and g into what all its rows need,
+// once, through shared memory, and fetches the next token meanwhile.  The two dot products S k and S q are taken of the decayed state
 // together, so each token costs one reduction: with u = beta (v - S k),
 // o = scale (S q + u (k . q)) and S + u k^T.
 // Bound: DRAM, the state read and written once (8 Dk Dv bytes a head).
@@ -79,130 +80,144 @@ template <int DK, int SETS>
 __global__ void __launch_bounds__(kRecWarps * 32) delta_recurrent_kernel(const DeltaParams p)
 {
     constexpr int NV = DK / 32;  // float4 chunks a lane holds of a row
+    __shared__ struct {
+        float4 k[DK / 4], q[DK / 4], a[DK / 4];
+        float kk[kRecWarps], qq[kRecWarps], kq[kRecWarps];
+    } sm[2];  // the token's rows and their products, by turns
     const int slices = (p.Dv + kRecWarps * 4 * SETS - 1) / (kRecWarps * 4 * SETS);
-    const int slice = blockIdx.x % slices;
-    const int64_t sh = blockIdx.x / slices;
-    const int h = (int)(sh % p.Hv), s = (int)(sh / p.Hv);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7;
-    const int row0 = (slice * kRecWarps + warp) * 4 * SETS;  // the warp's first row
-    if (row0 >= p.Dv)
-        return;
+    const int slice = blockIdx.x % slices, sh = blockIdx.x / slices;
+    const int h = sh % p.Hv, s = sh / p.Hv;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, l8 = lane & 7;
+    const int row0 = (slice * kRecWarps + warp) * 4 * SETS + (lane >> 3);  // the lane's first row; the next are 4 on
     int64_t t0, t1;
     seq_range(p, s, t0, t1);
     const int64_t slot = p.slots ? p.slots[s] : s;
     if (slot < 0 || slot >= p.n_states) {  // padding: zeros out, no state
-        for (int64_t t = t0; t < t1; ++t)
-            for (int r = lane; r < 4 * SETS; r += 32)
-                if (row0 + r < p.Dv)
-                    p.o[t * p.os + (int64_t)h * p.Dv + row0 + r] = 0;
+        for (int64_t tok = t0; tok < t1; ++tok)
+#pragma unroll
+            for (int i = 0; i < SETS; ++i)
+                if (l8 == 0 && row0 + 4 * i < p.Dv)
+                    p.o[tok * p.os + (int64_t)h * p.Dv + row0 + 4 * i] = 0;
         return;
     }
     const int64_t sbase = (slot * p.Hv + h) * (int64_t)p.Dv * DK;
     float4 S[SETS][NV];
 #pragma unroll
-    for (int i = 0; i < SETS; ++i) {
-        const int row = row0 + 4 * i + (lane >> 3);
+    for (int i = 0; i < SETS; ++i)
 #pragma unroll
         for (int c = 0; c < NV; ++c)
-            S[i][c] = p.s_in && row < p.Dv
-                          ? *reinterpret_cast<const float4 *>(p.s_in + sbase + (int64_t)row * DK + 32 * c + 4 * l8)
+            S[i][c] = p.s_in && row0 + 4 * i < p.Dv
+                          ? __ldcs(reinterpret_cast<const float4 *>(p.s_in + sbase + (int64_t)(row0 + 4 * i) * DK + 32 * c +
+                                                                    4 * l8))
                           : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
     const int hq = h / (p.Hv / p.Hq);
-    for (int64_t t = t0; t < t1; ++t) {
-        float4 k[NV], q[NV], a[NV];
-        float kk = 0.f, qq = 0.f, kq = 0.f;
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const uint2 kb = *reinterpret_cast<const uint2 *>(p.k + t * p.ks + (int64_t)hq * DK + 32 * c + 4 * l8);
-            const uint2 qb = *reinterpret_cast<const uint2 *>(p.q + t * p.qs + (int64_t)hq * DK + 32 * c + 4 * l8);
-            k[c] = make_float4(lo_bf(kb.x), hi_bf(kb.x), lo_bf(kb.y), hi_bf(kb.y));
-            q[c] = make_float4(lo_bf(qb.x), hi_bf(qb.x), lo_bf(qb.y), hi_bf(qb.y));
-            if (p.flags & DEP_DELTA_CHANNEL) {
-                const float4 g =
-                    *reinterpret_cast<const float4 *>(p.g + t * p.gs + (int64_t)h * DK + 32 * c + 4 * l8);
-                a[c] = make_float4(decay(g.x), decay(g.y), decay(g.z), decay(g.w));
-            }
+    const bool chan = (p.flags & DEP_DELTA_CHANNEL) != 0;
+    // thread = channel for what a token brings; the lane's rows of v
+    float k = 0.f, q = 0.f, g = 0.f, beta = 0.f, v[SETS];
+    auto fetch = [&](int64_t tok) {
+        if (t < DK) {
+            k = __uint_as_float((uint32_t)p.k[tok * p.ks + (int64_t)hq * DK + t] << 16);
+            q = __uint_as_float((uint32_t)p.q[tok * p.qs + (int64_t)hq * DK + t] << 16);
+            g = p.g[tok * p.gs + (chan ? (int64_t)h * DK + t : h)];
         }
-        if (!(p.flags & DEP_DELTA_CHANNEL)) {
-            const float e = decay(p.g[t * p.gs + h]);
+        beta = p.beta[tok * p.bs + h];
 #pragma unroll
-            for (int c = 0; c < NV; ++c)
-                a[c] = make_float4(e, e, e, e);
+        for (int i = 0; i < SETS; ++i)
+            v[i] = row0 + 4 * i < p.Dv
+                       ? __uint_as_float((uint32_t)p.v[tok * p.vs + (int64_t)h * p.Dv + row0 + 4 * i] << 16)
+                       : 0.f;
+    };
+    if (t0 < t1)
+        fetch(t0);
+    for (int64_t tok = t0; tok < t1; ++tok) {
+        auto &m = sm[(tok - t0) & 1];
+        if (t < DK) {
+            reinterpret_cast<float *>(m.k)[t] = k;
+            reinterpret_cast<float *>(m.q)[t] = q;
+            reinterpret_cast<float *>(m.a)[t] = decay(g);
         }
+        float kk = k * k, qq = q * q, kq = k * q;
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const float *kp = &k[c].x, *qp = &q[c].x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                kk = fmaf(kp[j], kp[j], kk);
-                qq = fmaf(qp[j], qp[j], qq);
-                kq = fmaf(kp[j], qp[j], kq);
-            }
-        }
-#pragma unroll
-        for (int d = 4; d; d >>= 1) {
+        for (int d = 16; d; d >>= 1) {
             kk += __shfl_xor_sync(~0u, kk, d);
             qq += __shfl_xor_sync(~0u, qq, d);
             kq += __shfl_xor_sync(~0u, kq, d);
         }
+        if (lane == 0) {
+            m.kk[warp] = kk;
+            m.qq[warp] = qq;
+            m.kq[warp] = kq;
+        }
+        const float bt = beta;
+        float vt[SETS];
+#pragma unroll
+        for (int i = 0; i < SETS; ++i)
+            vt[i] = v[i];
+        if (tok + 1 < t1)
+            fetch(tok + 1);
+        __syncthreads();
+        kk = (m.kk[0] + m.kk[1]) + (m.kk[2] + m.kk[3]);
+        qq = (m.qq[0] + m.qq[1]) + (m.qq[2] + m.qq[3]);
+        kq = (m.kq[0] + m.kq[1]) + (m.kq[2] + m.kq[3]);
         float rq = p.scale, rk = 1.f;
         if (p.flags & DEP_DELTA_L2NORM) {
             rk = 1.0f / sqrtf(kk + 1e-6f);
             rq *= 1.0f / sqrtf(qq + 1e-6f);
         }
         kq *= rk * rq;
-        const float beta = p.beta[t * p.bs + h];
+        float dk[SETS] = {}, dq[SETS] = {};
 #pragma unroll
-        for (int i = 0; i < SETS; ++i) {
-            const int row = row0 + 4 * i + (lane >> 3);
-            float dk = 0.f, dq = 0.f;
+        for (int c = 0; c < NV; ++c) {
+            const float4 kc = m.k[8 * c + l8], qc = m.q[8 * c + l8], ac = m.a[8 * c + l8];
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
+            for (int i = 0; i < SETS; ++i) {
                 float *sp = &S[i][c].x;
-                const float *ap = &a[c].x, *kp = &k[c].x, *qp = &q[c].x;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    sp[j] *= ap[j];
-                    dk = fmaf(sp[j], kp[j], dk);
-                    dq = fmaf(sp[j], qp[j], dq);
+                    sp[j] *= (&ac.x)[j];
+                    dk[i] = fmaf(sp[j], (&kc.x)[j], dk[i]);
+                    dq[i] = fmaf(sp[j], (&qc.x)[j], dq[i]);
                 }
             }
+        }
 #pragma unroll
-            for (int d = 4; d; d >>= 1) {
-                dk += __shfl_xor_sync(~0u, dk, d);
-                dq += __shfl_xor_sync(~0u, dq, d);
+        for (int d = 4; d; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < SETS; ++i) {
+                dk[i] += __shfl_xor_sync(~0u, dk[i], d);
+                dq[i] += __shfl_xor_sync(~0u, dq[i], d);
             }
-            const float v =
-                row < p.Dv ? __uint_as_float((uint32_t)p.v[t * p.vs + (int64_t)h * p.Dv + row] << 16) : 0.f;
-            const float u = beta * (v - dk * rk), uk = u * rk;
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
+        for (int i = 0; i < SETS; ++i) {
+            const float u = bt * (vt[i] - dk[i] * rk);
+            if (l8 == 0 && row0 + 4 * i < p.Dv)
+                p.o[tok * p.os + (int64_t)h * p.Dv + row0 + 4 * i] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(u, kq, dq[i] * rq)));
+            dk[i] = u * rk;
+        }
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const float4 kc = m.k[8 * c + l8];
+#pragma unroll
+            for (int i = 0; i < SETS; ++i) {
                 float *sp = &S[i][c].x;
-                const float *kp = &k[c].x;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    sp[j] = fmaf(uk, kp[j], sp[j]);
+                    sp[j] = fmaf(dk[i], (&kc.x)[j], sp[j]);
             }
-            if (l8 == 0 && row < p.Dv)
-                p.o[t * p.os + (int64_t)h * p.Dv + row] =
-                    __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(u, kq, dq * rq)));
         }
     }
 #pragma unroll
-    for (int i = 0; i < SETS; ++i) {
-        const int row = row0 + 4 * i + (lane >> 3);
+    for (int i = 0; i < SETS; ++i)
 #pragma unroll
         for (int c = 0; c < NV; ++c)
-            if (row < p.Dv)
-                *reinterpret_cast<float4 *>(p.s_out + sbase + (int64_t)row * DK + 32 * c + 4 * l8) = S[i][c];
-    }
+            if (row0 + 4 * i < p.Dv)
+                __stcs(reinterpret_cast<float4 *>(p.s_out + sbase + (int64_t)(row0 + 4 * i) * DK + 32 * c + 4 * l8), S[i][c]);
 }
 
-template <int DK>
+template <int DK, int SETS>
 cudaError_t recurrent_launch(const DeltaParams &p, cudaStream_t s)
 {
-    constexpr int SETS = 2;  // 32 rows a block
     const int64_t slices = (p.Dv + kRecWarps * 4 * SETS - 1) / (kRecWarps * 4 * SETS);
     const int64_t blocks = slices * p.Hv * p.n_seq;
     if (blocks > INT32_MAX)
@@ -912,9 +927,12 @@ cudaError_t chunk_launch(const DeltaParams &p, cudaStream_t s)
 template <int DK>
 cudaError_t delta_launch(const DeltaParams &p, cudaStream_t s)
 {
-    if (p.tokens < 8ll * p.n_seq)
-        return recurrent_launch<DK>(p, s);
-    return chunk_launch<DK, 8>(p, s);
+    // A chunk costs the chunked kernel the same whether it holds one token or sixteen; the recurrent kernel
+    // pays by the token.  96 heads of 128 channels, measured: 64 sequences of 7 tokens 388 us (44 us a token),
+    // of up to 16 in one chunk 504 us; 4 sequences of 7 tokens 28 us (2.6 us a token), of up to 16 40 us.
+    if (p.tokens >= 12ll * p.n_seq)
+        return chunk_launch<DK, 8>(p, s);
+    return (int64_t)p.n_seq * p.Hv * p.Dv < 32768 ? recurrent_launch<DK, 2>(p, s) : recurrent_launch<DK, 4>(p, s);
 }
 
 dep_status_t delta_entry(const dep_delta_args_t *a, void *stream)

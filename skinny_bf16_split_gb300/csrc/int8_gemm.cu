@@ -8,6 +8,12 @@
 // the products run as FP16 MMAs, and after at most 1024 columns the accumulators
 // are drained into 32-bit integers.
 //
+// int8_rows_kernel<BT>, up to 8 rows: four-way integer dot products on whole weight rows.
+// A block takes four weight rows at a time; a thread loads 16 bytes of each, and 16 of each
+// batch row (which stay in L1), so a weight byte costs BT / 4 multiply-adds and next to
+// nothing else.  The sums of a block's threads meet by warp reductions and through shared
+// memory.  Bound: the weight's bytes.
+//
 // int8_kernel<NT>: persistent blocks over units of 128 weight rows x 256 columns.
 //   warp 0      TMA: weight stages, 32 KB of int8 each (256 consecutive bytes a row).
 //   warps 2, 3  x, in slots of NT x SK columns as FP16.  Up to 32 rows they widen it
@@ -285,6 +291,72 @@ __global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restri
     uint4 *d = reinterpret_cast<uint4 *>(xh + (int64_t)row * Kp + c);
     d[0] = o[0];
     d[1] = o[1];
+}
+
+constexpr int kRows = 4;           // weight rows of a block's tile
+constexpr int kRowThreads = 256;   // at most
+constexpr int kRowBlocks = 4;      // blocks of an SM
+
+// BT batch rows (B of them there).
+template <int BT>
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks)
+    int8_rows_kernel(const uint8_t *__restrict__ x, const float *__restrict__ xs, const uint8_t *__restrict__ W,
+                     const float *__restrict__ ws, uint16_t *__restrict__ y, int B, int64_t N, int K)
+{
+    constexpr int U = BT <= 4 ? 2 : 1;  // 16-byte pieces of a row that a thread has in flight
+    __shared__ int part[2][kRowThreads / 32][kRows * BT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, pieces = K / 16;
+    const int64_t tiles = (N + kRows - 1) / kRows;
+    int buf = 0;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+        const uint4 *w = reinterpret_cast<const uint4 *>(W + tile * kRows * K);
+        int acc[kRows][BT] = {};
+        for (int c0 = threadIdx.x; c0 < pieces; c0 += U * blockDim.x) {
+            int4 v[U][kRows];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const int c = c0 + u * blockDim.x;
+                    const uint4 z = c < pieces && tile * kRows + r < N ? __ldcs(w + (int64_t)r * pieces + c)
+                                                                       : make_uint4(0, 0, 0, 0);
+                    v[u][r] = make_int4((int)z.x, (int)z.y, (int)z.z, (int)z.w);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * blockDim.x;
+                if (c < pieces)
+#pragma unroll
+                    for (int b = 0; b < BT; ++b) {
+                        if (b < B) {
+                            const int4 a = __ldg(reinterpret_cast<const int4 *>(x) + (int64_t)b * pieces + c);
+#pragma unroll
+                            for (int r = 0; r < kRows; ++r)
+                                acc[r][b] = __dp4a(a.x, v[u][r].x,
+                                                   __dp4a(a.y, v[u][r].y, __dp4a(a.z, v[u][r].z, __dp4a(a.w, v[u][r].w, acc[r][b]))));
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int b = 0; b < BT; ++b) {
+                const int s = __reduce_add_sync(~0u, acc[r][b]);
+                if (lane == 0)
+                    part[buf][warp][r * BT + b] = s;
+            }
+        __syncthreads();  // (the other half of `part` is free: its readers have passed here since)
+        if (threadIdx.x < kRows * BT) {
+            const int r = threadIdx.x / BT, b = threadIdx.x % BT;
+            const int64_t row = tile * kRows + r;
+            int s = 0;
+            for (int i = 0; i < warps; ++i)
+                s += part[buf][i][threadIdx.x];
+            if (b < B && row < N)
+                y[(int64_t)b * N + row] = __bfloat16_as_ushort(__float2bfloat16_rn((float)s * (xs[b] * ws[row])));
+        }
+    }
 }
 
 template <int NT>
@@ -755,9 +827,30 @@ cudaError_t int8_launch(const dep_int8_plan_s &pl, const void *W, const Int8Para
     return cudaLaunchKernelEx(&cfg, int8_kernel<NT>, tmW, tmX, p);
 }
 
+template <int BT>
+cudaError_t rows_launch(const dep_int8_plan_s &pl, const uint8_t *x, const float *xs, const void *W, const float *ws,
+                        uint16_t *y, int32_t B, cudaStream_t stream)
+{
+    const int64_t tiles = (pl.N + kRows - 1) / kRows, most = (int64_t)pl.sm_count * kRowBlocks;
+    // As many threads as share a row's pieces most evenly.
+    const int pieces = (int)(pl.K / 16);
+    int threads = kRowThreads;
+    for (int n = kRowThreads - 32; n >= kRowThreads / 2; n -= 32)
+        if ((pieces + n - 1) / n * n < (pieces + threads - 1) / threads * threads)
+            threads = n;
+    int8_rows_kernel<BT><<<(unsigned)(tiles < most ? tiles : most), threads, 0, stream>>>(
+        x, xs, static_cast<const uint8_t *>(W), ws, y, B, pl.N, (int)pl.K);
+    return cudaGetLastError();
+}
+
 cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *xs, const void *W, const float *ws,
                       uint16_t *y, int32_t B, cudaStream_t stream)
 {
+    if (B <= 8)
+        return B == 1   ? rows_launch<1>(pl, x, xs, W, ws, y, B, stream)
+               : B == 2 ? rows_launch<2>(pl, x, xs, W, ws, y, B, stream)
+               : B <= 4 ? rows_launch<4>(pl, x, xs, W, ws, y, B, stream)
+                        : rows_launch<8>(pl, x, xs, W, ws, y, B, stream);
     const int nt = width(B);
     const Int8Split split = split_for(pl.N, pl.K, nt, pl.sm_count);
     if (nt > 32) {
