@@ -295,47 +295,53 @@ __global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restri
 
 constexpr int kRows = 4;           // weight rows of a block's tile
 constexpr int kRowThreads = 256;   // at most
-constexpr int kRowBlocks = 4;      // blocks of an SM
+constexpr int row_blocks(int bt) { return bt <= 4 ? 4 : 3; }  // blocks of an SM: what the registers allow
 
 // BT batch rows (B of them there).
 template <int BT>
-__global__ void __launch_bounds__(kRowThreads, kRowBlocks)
+__global__ void __launch_bounds__(kRowThreads, row_blocks(BT))
     int8_rows_kernel(const uint8_t *__restrict__ x, const float *__restrict__ xs, const uint8_t *__restrict__ W,
                      const float *__restrict__ ws, uint16_t *__restrict__ y, int B, int64_t N, int K)
 {
-    constexpr int U = BT <= 4 ? 2 : 1;  // 16-byte pieces of a row that a thread has in flight
     __shared__ int part[2][kRowThreads / 32][kRows * BT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, pieces = K / 16;
+    const int steps = (pieces + blockDim.x - 1) / blockDim.x;
     const int64_t tiles = (N + kRows - 1) / kRows;
+    auto load = [&](int64_t tile, int c, uint4 (&v)[kRows]) {
+        const uint4 *w = reinterpret_cast<const uint4 *>(W + tile * kRows * K);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            v[r] = c < pieces && tile * kRows + r < N ? __ldcs(w + r * pieces + c) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 next[kRows];
+    load(blockIdx.x, threadIdx.x, next);
     int buf = 0;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-        const uint4 *w = reinterpret_cast<const uint4 *>(W + tile * kRows * K);
         int acc[kRows][BT] = {};
-        for (int c0 = threadIdx.x; c0 < pieces; c0 += U * blockDim.x) {
-            int4 v[U][kRows];
+        for (int s = 0; s < steps; ++s) {
+            uint4 v[kRows];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int r = 0; r < kRows; ++r)
+                v[r] = next[r];
+            const int c = threadIdx.x + s * blockDim.x;
+            if (s + 1 < steps)
+                load(tile, c + blockDim.x, next);
+            else
+                load(tile + gridDim.x, threadIdx.x, next);  // (past the last tile: nothing)
+            if (c >= pieces)
+                continue;
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const int c = c0 + u * blockDim.x;
-                    const uint4 z = c < pieces && tile * kRows + r < N ? __ldcs(w + (int64_t)r * pieces + c)
-                                                                       : make_uint4(0, 0, 0, 0);
-                    v[u][r] = make_int4((int)z.x, (int)z.y, (int)z.z, (int)z.w);
-                }
+            for (int b = 0; b < BT; ++b) {
+                if (b < B) {
+                    const int4 a = __ldg(reinterpret_cast<const int4 *>(x) + b * pieces + c);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * blockDim.x;
-                if (c < pieces)
-#pragma unroll
-                    for (int b = 0; b < BT; ++b) {
-                        if (b < B) {
-                            const int4 a = __ldg(reinterpret_cast<const int4 *>(x) + (int64_t)b * pieces + c);
-#pragma unroll
-                            for (int r = 0; r < kRows; ++r)
-                                acc[r][b] = __dp4a(a.x, v[u][r].x,
-                                                   __dp4a(a.y, v[u][r].y, __dp4a(a.z, v[u][r].z, __dp4a(a.w, v[u][r].w, acc[r][b]))));
-                        }
+                    for (int r = 0; r < kRows; ++r) {
+                        acc[r][b] = __dp4a(a.x, (int)v[r].x, acc[r][b]);
+                        acc[r][b] = __dp4a(a.y, (int)v[r].y, acc[r][b]);
+                        acc[r][b] = __dp4a(a.z, (int)v[r].z, acc[r][b]);
+                        acc[r][b] = __dp4a(a.w, (int)v[r].w, acc[r][b]);
                     }
+                }
             }
         }
 #pragma unroll
@@ -831,7 +837,7 @@ template <int BT>
 cudaError_t rows_launch(const dep_int8_plan_s &pl, const uint8_t *x, const float *xs, const void *W, const float *ws,
                         uint16_t *y, int32_t B, cudaStream_t stream)
 {
-    const int64_t tiles = (pl.N + kRows - 1) / kRows, most = (int64_t)pl.sm_count * kRowBlocks;
+    const int64_t tiles = (pl.N + kRows - 1) / kRows, most = (int64_t)pl.sm_count * row_blocks(BT);
     // As many threads as share a row's pieces most evenly.
     const int pieces = (int)(pl.K / 16);
     int threads = kRowThreads;
