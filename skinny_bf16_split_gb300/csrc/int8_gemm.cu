@@ -35,9 +35,9 @@
 // about 64 cycles on an MMA, 55 on a commit and 100 on a wait, so one wait (tested
 // ahead, while the MMAs before it are issued) and one commit a slot.
 // Where whole tiles would leave blocks idle, the blocks take equal ranges of units, and
-// the parts of a tile that several blocks share are added into the plan's workspace by
-// integer atomics (exact, so any order gives the same bits); the block whose part
-// arrives last rounds and stores, and clears the workspace.  Blocks wait for one
+// every block stores its part of a tile that several share (integers: exact in any order);
+// the one that comes last adds the parts, rounds and stores.  (Adding them by integer
+// atomics took 18 us at 128 rows: about 200 billion a second.)  Blocks wait for one
 // another only inside a cluster.
 // Bound: the weight's bytes up to about 128 rows, the tensor cores above.
 #include <cuda_bf16.h>
@@ -55,12 +55,12 @@ struct dep_int8_plan_s {
     int32_t max_rows = 0;
     int device = -1;
     int sm_count = 0;
-    void *block = nullptr;  // device memory: status, counters, sums, x in FP16
+    void *block = nullptr;  // device memory: status, counters, parts, x in FP16
     size_t bytes = 0;
     int *status = nullptr;
     int *counters = nullptr;  // arrivals at shared tiles, zero between launches
-    int *sums = nullptr;      // sums of shared tiles, zero between launches
-    size_t clear_bytes = 0;   // status, counters and sums, from `block` on
+    int *parts = nullptr;     // parts of shared tiles
+    size_t clear_bytes = 0;   // status and counters, from `block` on
     uint16_t *xh = nullptr;
     uint64_t wait_limit_ns = 1000000000ull;  // 1 s per wait
 };
@@ -164,7 +164,7 @@ struct Int8Params {
     int B, K;
     int64_t N;
     Int8Split split;
-    int *counters, *sums;
+    int *counters, *parts;
     int *status;
     uint64_t limit_ns;
 };
@@ -241,29 +241,48 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
     hi = *reinterpret_cast<uint32_t *>(&hb);
 }
 
-// Add sixteen accumulators (whole numbers of at most 2^24) to integers.  The conversion
-// instruction runs at an eighth of the rate of an addition, so numbers below 2^22 are
-// read off the mantissa of their sum with 1.5 * 2^23; if any of a warp's is larger, that
-// shows in the sum's exponent and the warp converts.
-__device__ __forceinline__ void drain16(const uint32_t (&v)[16], int *acc)
+// Add N accumulators (whole numbers of at most 2^24) from tensor memory to integers.  FAST, where
+// the MMAs wait for it: the conversion instruction runs at an eighth of the rate of an addition,
+// so numbers below 2^22 are read off the mantissa of their sum with 1.5 * 2^23; if any of a
+// warp's is larger, that shows in the sum's exponent and the warp converts.
+template <int N, bool FAST>
+__device__ __forceinline__ void drain(uint32_t taddr, int *acc)
 {
+    static_assert(N == 8 || N == 16, "");
+    uint32_t v[16];
+    if (N == 16)
+        tc::ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "r"(taddr));
+    tc::wait_ld();
     constexpr int kMagic = 0x4B400000;  // 1.5 * 2^23
-    int s[16], seen = 0;
+    if (FAST) {
+        int seen = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        s[i] = __float_as_int(__uint_as_float(v[i]) + __int_as_float(kMagic));
-        seen |= s[i] ^ kMagic;
+        for (int i = 0; i < N; ++i)
+            seen |= __float_as_int(__uint_as_float(v[i]) + __int_as_float(kMagic)) ^ kMagic;
+        // |value| < 2^22 <=> the sum lies in [2^23, 2^24): sign and exponent as kMagic's
+        if (__all_sync(~0u, (seen & 0xFF800000) == 0)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                acc[i] += __float_as_int(__uint_as_float(v[i]) + __int_as_float(kMagic)) - kMagic;
+            return;
+        }
     }
-    // |value| < 2^22 <=> the sum lies in [2^23, 2^24): sign and exponent as kMagic's
-    if (__all_sync(~0u, (seen & 0xFF800000) == 0)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            acc[i] += s[i] - kMagic;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            acc[i] += __float2int_rn(__uint_as_float(v[i]));
-    }
+    for (int i = 0; i < N; ++i)
+        acc[i] += __float2int_rn(__uint_as_float(v[i]));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const int *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15, %16};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
 }
 
 // Sixteen int8 -> sixteen FP16.
@@ -679,10 +698,6 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
-        float xs[(S::COLS + 31) / 32];  // scale of column 32 i + lane
-#pragma unroll
-        for (int i = 0; i < (S::COLS + 31) / 32; ++i)
-            xs[i] = 32 * i + lane < cols ? p.xs[c0 + 32 * i + lane] : 0.0f;
         for (int seg = 0; seg < walk.m && ok; ++seg) {
             const int g = walk.group(seg), end = walk.to(g);
             const int64_t t = (int64_t)g * S::CL + rank, n = t * kBM + 32 * q + lane;
@@ -699,37 +714,52 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     break;
                 }
                 tc::fence_after();
+                constexpr int D = NT > 128 ? 8 : 16;  // columns at a time: what the registers allow
 #pragma unroll
-                for (int j = 0; j < S::COLS; j += 16) {
-                    if (j < cols) {
+                for (int j = 0; j < S::COLS; j += D)
+                    if (j < cols)
 #pragma unroll
-                        for (int m = 0; m < S::ISSUERS; ++m) {
-                            uint32_t v[16];
-                            tc::ld16(lane_addr + (uint32_t)((buf * S::ISSUERS + m) * NT + j), v);
-                            tc::wait_ld();
-                            drain16(v, acc + j);
-                        }
+                        for (int m = 0; m < S::ISSUERS; ++m)
+                            drain<D, (NT > 128)>(lane_addr + (uint32_t)((buf * S::ISSUERS + m) * NT + j), acc + j);
+                if (u + S::EXACT < end) {
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(acce + 8 * buf);
+                    if (++buf == S::BUFS) {
+                        buf = 0;
+                        bph ^= 1u;
                     }
-                }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(acce + 8 * buf);
-                if (++buf == S::BUFS) {
-                    buf = 0;
-                    bph ^= 1u;
                 }
             }
             if (!ok)
                 break;
-            bool last = true;
-            const int parts = p.split.owner((g + 1) * KU - 1) - p.split.owner(g * KU) + 1;
-            if (parts > 1) {
-                int *sums = p.sums + (t * NT + c0) * kBM + 32 * q + lane;
+            // The tile's end runs once or twice: its code, if unrolled over the columns, would cost more to fetch
+            // than to run.  So the sums go back over the accumulators, and loops read them from there.
+            const uint32_t back = lane_addr + (uint32_t)(buf * S::ISSUERS * NT);
 #pragma unroll
-                for (int j = 0; j < S::COLS; ++j)
-                    if (j < cols)
-                        atomicAdd(sums + j * kBM, acc[j]);
+            for (int j = 0; j < S::COLS; j += 16)
+                if (j < cols)
+                    tmem_st16(back + j, acc + j);
+            tmem_wait_st();
+            // A tile that several clusters share: every block stores its part, and the one that comes last adds them.
+            bool last = true;
+            const int ca = p.split.owner(g * KU), parts = p.split.owner((g + 1) * KU - 1) - ca + 1;
+            const auto part = [&](int cl) {  // this warp's part of the block of cluster cl
+                const int slot = p.split.begin(cl) > g * KU ? 0 : 1;  // the tile that its range starts in, or the last
+                return p.parts + (((int64_t)(cl * S::CL + rank) * 2 + slot) * NT + c0) * kBM + 32 * q + lane;
+            };
+            if (parts > 1) {
+                int *mine = part(c);
+#pragma unroll 1
+                for (int j = 0; j < cols; j += 16) {
+                    uint32_t v[16];
+                    tc::ld16(back + j, v);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        __stcg(mine + (j + i) * kBM, (int)v[i]);
+                }
                 __threadfence();
                 __syncwarp();
                 int old = 0;
@@ -738,25 +768,50 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                 last = __shfl_sync(~0u, old, 0) == parts - 1;
                 if (last) {
                     __threadfence();
-#pragma unroll
-                    for (int j = 0; j < S::COLS; ++j)  // all loads, then all stores
-                        if (j < cols)
-                            acc[j] = __ldcg(sums + j * kBM);
-#pragma unroll
-                    for (int j = 0; j < S::COLS; ++j)
-                        if (j < cols)
-                            __stcg(sums + j * kBM, 0);
                     if (lane == 0)
                         p.counters[t * 16 + e] = 0;
                 }
             }
             if (last) {
+                uint16_t *y = p.y + (int64_t)c0 * p.N + n;
+#pragma unroll 1
+                for (int j = 0; j < cols; j += 16, y += 16 * p.N) {
+                    uint32_t v[16];
+                    tc::ld16(back + j, v);
+                    tc::wait_ld();
+#pragma unroll 1
+                    for (int i0 = 0; i0 < parts; i0 += 2) {  // two parts in flight; this block's own is there already
+                        const int a0 = ca + i0, a1 = a0 + 1;
+                        const bool in0 = a0 != c, in1 = i0 + 1 < parts && a1 != c;
+                        const int *s0 = part(in0 ? a0 : c) + j * kBM, *s1 = part(in1 ? a1 : c) + j * kBM;
+                        if (parts == 1)
+                            break;
+                        int u0[16], u1[16];
 #pragma unroll
-                for (int j = 0; j < S::COLS; ++j) {
-                    const float scale = __shfl_sync(~0u, xs[j / 32], j % 32) * ws;
-                    if (j < cols && n < p.N)
-                        p.y[(int64_t)(c0 + j) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn((float)acc[j] * scale));
+                        for (int i = 0; i < 16; ++i) {
+                            u0[i] = in0 ? __ldcg(s0 + i * kBM) : 0;
+                            u1[i] = in1 ? __ldcg(s1 + i * kBM) : 0;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            v[i] += u0[i] + u1[i];
+                    }
+                    const float xs = j + (lane & 15) < cols ? p.xs[c0 + j + (lane & 15)] : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float scale = __shfl_sync(~0u, xs, i) * ws;
+                        if (j + i < cols && n < p.N)
+                            y[i * p.N] = __bfloat16_as_ushort(__float2bfloat16_rn((float)(int)v[i] * scale));
+                    }
                 }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(acce + 8 * buf);
+            if (++buf == S::BUFS) {
+                buf = 0;
+                bph ^= 1u;
             }
         }
     }
@@ -867,7 +922,7 @@ cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *
         if (e != cudaSuccess)
             return e;
     }
-    const Int8Params p{x, xs, ws, y, B, (int)pl.K, pl.N, split, pl.counters, pl.sums, pl.status, pl.wait_limit_ns};
+    const Int8Params p{x, xs, ws, y, B, (int)pl.K, pl.N, split, pl.counters, pl.parts, pl.status, pl.wait_limit_ns};
     switch (nt) {
     case 16: return int8_launch<16>(pl, W, p, stream);
     case 32: return int8_launch<32>(pl, W, p, stream);
@@ -930,16 +985,18 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
         delete p;
         return DEP_ERR_CUDA;
     }
-    // One block of device memory: status word, counters, sums of shared tiles, x in FP16.
+    // One block of device memory: status word, counters, parts of shared tiles, x in FP16.
     const int64_t tiles = (N + dep::kBM - 1) / dep::kBM, Kp = (K + dep::kKU - 1) / dep::kKU * dep::kKU;
     const int nt = dep::width(max_rows);
-    size_t sums = 0;
-    for (int w = 16; w <= nt; w *= 2)  // (a cluster's last tile may lie past N)
-        if (!dep::split_for(N, K, w, p->sm_count).whole)
-            sums = (size_t)(tiles + 1) * w * dep::kBM * sizeof(int);
-    const size_t counters = ((size_t)(tiles + 1) * 16 * sizeof(int) + 255) / 256 * 256;
-    p->clear_bytes = 256 + counters + sums;
-    p->bytes = p->clear_bytes + (nt > 32 ? (size_t)nt * Kp * 2 : 0);
+    size_t parts = 0;
+    for (int w = 16; w <= nt; w *= 2) {
+        const dep::Int8Split s = dep::split_for(N, K, w, p->sm_count);
+        if (!s.whole)  // two for each block
+            parts = (size_t)s.clusters * dep::cluster_of(w) * 2 * w * dep::kBM * sizeof(int);
+    }
+    const size_t counters = ((size_t)(tiles + 1) * 16 * sizeof(int) + 255) / 256 * 256;  // (a cluster's last tile may lie past N)
+    p->clear_bytes = 256 + counters;
+    p->bytes = p->clear_bytes + parts + (nt > 32 ? (size_t)nt * Kp * 2 : 0);
     if (cudaMalloc(&p->block, p->bytes) != cudaSuccess) {
         cudaGetLastError();
         delete p;
@@ -954,8 +1011,8 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
     uint8_t *at = static_cast<uint8_t *>(p->block);
     p->status = reinterpret_cast<int *>(at);
     p->counters = reinterpret_cast<int *>(at + 256);
-    p->sums = reinterpret_cast<int *>(at + 256 + counters);
-    p->xh = reinterpret_cast<uint16_t *>(at + p->clear_bytes);
+    p->parts = reinterpret_cast<int *>(at + p->clear_bytes);
+    p->xh = reinterpret_cast<uint16_t *>(at + p->clear_bytes + parts);
     *out = p;
     return DEP_OK;
 }
@@ -1013,7 +1070,7 @@ dep_status_t dep_int8_device_status(dep_int8_plan_t p, void *stream, int32_t *co
         cudaGetLastError();
         return DEP_ERR_CUDA;
     }
-    // After a give-up counters and sums may be left mid-protocol: clear them.
+    // After a give-up counters may be left mid-protocol: clear them.
     if (h && (cudaDeviceSynchronize() != cudaSuccess || cudaMemset(p->block, 0, p->clear_bytes) != cudaSuccess)) {
         cudaGetLastError();
         return DEP_ERR_CUDA;
