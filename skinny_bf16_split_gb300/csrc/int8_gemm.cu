@@ -61,7 +61,7 @@ struct dep_int8_plan_s {
     int *counters = nullptr;  // arrivals at shared tiles, zero between launches
     int *parts = nullptr;     // parts of shared tiles
     size_t clear_bytes = 0;   // status and counters, from `block` on
-    uint16_t *xh = nullptr;
+    uint16_t *xh = nullptr, *bounds = nullptr;
     uint64_t wait_limit_ns = 1000000000ull;  // 1 s per wait
 };
 
@@ -71,6 +71,7 @@ namespace {
 constexpr int64_t kMaxK = 131056;  // 131056 * 128 * 128 < 2^31
 constexpr int kBM = 128;           // weight rows of a tile (MMA M)
 constexpr int kKU = 256;           // columns of a unit
+constexpr int kMaxUnits = 512;     // kMaxK / kKU, rounded up
 constexpr int kWBytes = kBM * kKU; // a weight stage: two boxes of 128 columns
 
 template <int NT>
@@ -91,10 +92,11 @@ struct Int8Shape {
     static constexpr int PER = kKU / SK;                 // slots of a unit
     static constexpr int EXACT = 1024 * ISSUERS / kKU;   // units whose sums an FP32 accumulator holds exactly
     static constexpr int X_BYTES = NT * SK * 2;          // an x slot
-    static constexpr int WS = (kMaxDynamicSmem - 1024 - 512 - SLOTS * X_BYTES) / kWBytes;
+    static constexpr int WS = (kMaxDynamicSmem - 1024 - 512 - (DIRECT ? 0 : 1024) - SLOTS * X_BYTES) / kWBytes;
     static constexpr int ACC0 = 256;                     // the accumulators' first column
-    static constexpr int BARS = 2 * WS + 2 * SLOTS + 2 * BUFS + 1;
-    static constexpr int SMEM = 1024 + WS * kWBytes + SLOTS * X_BYTES + BARS * 8 + 16;
+    static constexpr int BARS = 2 * WS + 2 * SLOTS + 2 * BUFS + 2;
+    static constexpr int BOUNDS = DIRECT ? 0 : kMaxUnits * 2;  // bytes: bounds of x's units
+    static constexpr int SMEM = 1024 + WS * kWBytes + SLOTS * X_BYTES + BARS * 8 + 16 + BOUNDS;
     static_assert(SLOTS * SLOT_COLS <= ACC0 && ACC0 + BUFS * ISSUERS * NT <= 512 && SMEM <= kMaxDynamicSmem, "");
     static_assert(GROUPS == 1 || (PER == 4 && SLOTS == 8), "group g: slots 2g, 2g + 1 of the four of a unit");
     // The slot after s among those of one group (and of one issuer), and whether the ring wraps.
@@ -158,7 +160,8 @@ struct Int8Cursor {
 };
 
 struct Int8Params {
-    const uint8_t *x;  // int8 [B, K]
+    const uint8_t *x;       // int8 [B, K]
+    const uint16_t *bounds; // of x's units, where x was widened ahead
     const float *xs, *ws;
     uint16_t *y;
     int B, K;
@@ -294,22 +297,42 @@ __device__ __forceinline__ void widen16(uint4 v, uint4 &lo, uint4 &hi)
     widen4(v.w, hi.z, hi.w);
 }
 
-// x [B, K] int8 -> xh [gridDim.y rows, Kp] FP16, zeros past B and K (Kp a multiple of 256, K of 16).
-__global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restrict__ x, uint16_t *__restrict__ xh, int B,
-                                                         int K, int Kp)
+// x [B, K] int8 -> xh [rows, Kp] FP16, zeros past B and K (Kp a multiple of 256, K of 16, rows of 16),
+// and for each unit of 256 columns (a block) the largest sum of |x| that a row has there.
+__global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restrict__ x, uint16_t *__restrict__ xh,
+                                                         uint16_t *__restrict__ bounds, int B, int rows, int K, int Kp)
 {
     griddep_launch_dependents();
-    const int row = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 16;
-    if (c >= Kp)
-        return;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < B && c < K)
-        v = *reinterpret_cast<const uint4 *>(x + (int64_t)row * K + c);
-    uint4 o[2];
-    widen16(v, o[0], o[1]);
-    uint4 *d = reinterpret_cast<uint4 *>(xh + (int64_t)row * Kp + c);
-    d[0] = o[0];
-    d[1] = o[1];
+    __shared__ int top;
+    if (threadIdx.x == 0)
+        top = 0;
+    __syncthreads();
+    const int c = blockIdx.x * kKU + (threadIdx.x & 15) * 16;
+    int most = 0;
+#pragma unroll 4
+    for (int row = threadIdx.x >> 4; row < rows; row += 16) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < B && c < K)
+            v = *reinterpret_cast<const uint4 *>(x + (int64_t)row * K + c);
+        uint4 o[2];
+        widen16(v, o[0], o[1]);
+        uint4 *d = reinterpret_cast<uint4 *>(xh + (int64_t)row * Kp + c);
+        d[0] = o[0];
+        d[1] = o[1];
+        unsigned s = __dp4a(__vabs4(v.x), 0x01010101u, 0u);  // |-128| is 128, unsigned
+        s = __dp4a(__vabs4(v.y), 0x01010101u, s);
+        s = __dp4a(__vabs4(v.z), 0x01010101u, s);
+        s = __dp4a(__vabs4(v.w), 0x01010101u, s);
+#pragma unroll
+        for (int m = 8; m; m >>= 1)
+            s += __shfl_xor_sync(~0u, s, m);
+        most = max(most, (int)s);
+    }
+    if ((threadIdx.x & 15) == 0)
+        atomicMax(&top, most);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        bounds[blockIdx.x] = (uint16_t)top;  // at most 256 * 128
 }
 
 constexpr int kRows = 4;           // weight rows of a block's tile
@@ -395,9 +418,10 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     const uint32_t w0 = base, x0 = base + S::WS * kWBytes;
     const uint32_t wfull = x0 + S::SLOTS * S::X_BYTES, wempty = wfull + 8 * S::WS;
     const uint32_t sfull = wempty + 8 * S::WS, sempty = sfull + 8 * S::SLOTS;  // a weight slot and its x slot
-    const uint32_t accf = sempty + 8 * S::SLOTS, acce = accf + 8 * S::BUFS, done = acce + 8 * S::BUFS;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (done + 8 - base));
+    const uint32_t accf = sempty + 8 * S::SLOTS, acce = accf + 8 * S::BUFS, done = acce + 8 * S::BUFS, known = done + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (known + 8 - base));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    uint16_t *bounds = reinterpret_cast<uint16_t *>(tmem_slot + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S::CL == 1 ? 0 : (int)cluster_rank();
     const int c = S::CL == 1 ? blockIdx.x : blockIdx.x / S::CL;
@@ -436,6 +460,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         init(accf, S::BUFS, S::ISSUERS);
         init(acce, S::BUFS, S::EPI);
         init(done, 1, S::ISSUERS);
+        init(known, 1, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -451,6 +476,17 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     auto give_up = [&](int code) {
         record_status(p.status, code);
         *abort_flag = 1;
+    };
+
+    // The end of the run of units from u on (of `end`) that accumulators hold exactly: 1024 columns for each
+    // issuer; or, where the bounds are known, as many as keep the sum of |x| 128 within 2^24.
+    auto run_end = [&](int u, int end) {
+        if (S::DIRECT)
+            return u + S::EXACT < end ? u + S::EXACT : end;
+        int sum = 0;
+        while (u < end && (sum += bounds[u]) <= (1 << 24) / 128)
+            ++u;
+        return u;
     };
 
     if (warp == 0) {
@@ -584,11 +620,13 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
             int s = 2 * mi, buf = 0;
             uint32_t sph = 0, bph = 0;
-            bool ok = true, ready = false;
+            bool ok = S::DIRECT || mbar_wait(known, 0, p.limit_ns), ready = false;
+            if (!ok)
+                give_up(DEP_DEV_TIMEOUT_MMA);
             for (int seg = 0; seg < walk.m && ok; ++seg) {
                 const int g = walk.group(seg), end = walk.to(g);
                 for (int u = walk.from(g); u < end && ok;) {
-                    const int stop = u + S::EXACT < end ? u + S::EXACT : end;
+                    const int stop = run_end(u, end);
                     if (!mbar_wait(acce + 8 * buf, bph ^ 1u, p.limit_ns)) {
                         give_up(DEP_DEV_TIMEOUT_MMA);
                         ok = false;
@@ -697,7 +735,17 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         const int cols = p.B - c0 < S::COLS ? p.B - c0 : S::COLS;  // of these, columns of the batch (may be <= 0)
         int buf = 0;
         uint32_t bph = 0;
-        bool ok = true;
+        if (!S::DIRECT && e == 0) {  // bounds of x's units, for the issuers and the other draining warps
+            griddep_wait();
+            for (int i = lane; i < KU; i += 32)
+                bounds[i] = p.bounds[i];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(known);
+        }
+        bool ok = __all_sync(~0u, S::DIRECT || mbar_wait(known, 0, p.limit_ns));
+        if (!ok && lane == 0)
+            give_up(DEP_DEV_TIMEOUT_EPILOGUE);
         for (int seg = 0; seg < walk.m && ok; ++seg) {
             const int g = walk.group(seg), end = walk.to(g);
             const int64_t t = (int64_t)g * S::CL + rank, n = t * kBM + 32 * q + lane;
@@ -706,7 +754,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < S::COLS; ++j)
                 acc[j] = 0;
-            for (int u = walk.from(g); u < end; u += S::EXACT) {
+            for (int u = walk.from(g); u < end;) {
                 ok = __all_sync(~0u, mbar_wait(accf + 8 * buf, bph, p.limit_ns));
                 if (!ok) {
                     if (lane == 0)
@@ -721,7 +769,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
 #pragma unroll
                         for (int m = 0; m < S::ISSUERS; ++m)
                             drain<D, (NT > 128)>(lane_addr + (uint32_t)((buf * S::ISSUERS + m) * NT + j), acc + j);
-                if (u + S::EXACT < end) {
+                u = run_end(u, end);
+                if (u < end) {
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0)
@@ -839,11 +888,10 @@ Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
     s.groups = (int)(((N + kBM - 1) / kBM + cl - 1) / cl);
     s.units = (int)((K + kKU - 1) / kKU);
     const int all = s.groups * s.units, waves = (s.groups + most - 1) / most;
-    // Equal ranges unless whole tiles keep nearly every block busy, or sums of 256
-    // columns (128 KB for each part of a tile) would cost more than the idle blocks.
-    s.whole = nt == 256 || s.groups * 100ll >= (int64_t)waves * most * 95;
-    const int n = s.whole ? s.groups : all;
-    s.clusters = n < most ? n : most;
+    // Equal ranges, of at least four units, unless whole tiles keep nearly every block busy.
+    s.whole = s.groups * 100ll >= (int64_t)waves * most * 95;
+    const int n = s.whole ? s.groups : all, c = s.whole ? n : (all + 3) / 4;
+    s.clusters = c < most ? c : most;
     s.base = n / s.clusters;
     s.rem = n % s.clusters;
     return s;
@@ -916,13 +964,12 @@ cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *
     const Int8Split split = split_for(pl.N, pl.K, nt, pl.sm_count);
     if (nt > 32) {
         const int Kp = (int)split.units * kKU;
-        const dim3 grid((unsigned)((Kp / 16 + 255) / 256), (unsigned)nt);
-        int8_widen_kernel<<<grid, 256, 0, stream>>>(x, pl.xh, B, (int)pl.K, Kp);
+        int8_widen_kernel<<<(unsigned)split.units, 256, 0, stream>>>(x, pl.xh, pl.bounds, B, nt, (int)pl.K, Kp);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)
             return e;
     }
-    const Int8Params p{x, xs, ws, y, B, (int)pl.K, pl.N, split, pl.counters, pl.parts, pl.status, pl.wait_limit_ns};
+    const Int8Params p{x, pl.bounds, xs, ws, y, B, (int)pl.K, pl.N, split, pl.counters, pl.parts, pl.status, pl.wait_limit_ns};
     switch (nt) {
     case 16: return int8_launch<16>(pl, W, p, stream);
     case 32: return int8_launch<32>(pl, W, p, stream);
@@ -996,7 +1043,7 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
     }
     const size_t counters = ((size_t)(tiles + 1) * 16 * sizeof(int) + 255) / 256 * 256;  // (a cluster's last tile may lie past N)
     p->clear_bytes = 256 + counters;
-    p->bytes = p->clear_bytes + parts + (nt > 32 ? (size_t)nt * Kp * 2 : 0);
+    p->bytes = p->clear_bytes + parts + (nt > 32 ? (size_t)(nt + 1) * Kp * 2 : 0);
     if (cudaMalloc(&p->block, p->bytes) != cudaSuccess) {
         cudaGetLastError();
         delete p;
@@ -1013,6 +1060,7 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
     p->counters = reinterpret_cast<int *>(at + 256);
     p->parts = reinterpret_cast<int *>(at + p->clear_bytes);
     p->xh = reinterpret_cast<uint16_t *>(at + p->clear_bytes + parts);
+    p->bounds = p->xh + (size_t)nt * Kp;  // one for each unit
     *out = p;
     return DEP_OK;
 }
