@@ -8,11 +8,12 @@
 // the products run as FP16 MMAs, and after at most 1024 columns the accumulators
 // are drained into 32-bit integers.
 //
-// int8_rows_kernel<BT>, up to 8 rows: four-way integer dot products on whole weight rows.
-// A block takes four weight rows at a time; a thread loads 16 bytes of each, and 16 of each
-// batch row (which stay in L1), so a weight byte costs BT / 4 multiply-adds and next to
-// nothing else.  The sums of a block's threads meet by warp reductions and through shared
-// memory.  Bound: the weight's bytes.
+// int8_rows_kernel<BT>, up to 4 rows, and for small products: four-way integer dot products
+// on whole weight rows.  A block takes four weight rows at a time against BT batch rows; a
+// thread loads 16 bytes of each weight row, one step ahead, and 16 of each batch row (which
+// stay in L1), so a weight byte costs BT / 4 multiply-adds and next to nothing else.  The
+// sums of a block's threads meet by warp reductions and through shared memory.
+// Bound: the weight's bytes up to 2 rows, then the integer dot products (58 a cycle and SM).
 //
 // int8_kernel<NT>: persistent blocks over units of 128 weight rows x 256 columns.
 //   warp 0      TMA: weight stages, 32 KB of int8 each (256 consecutive bytes a row).
@@ -339,7 +340,6 @@ constexpr int kRows = 4;           // weight rows of a block's tile
 constexpr int kRowThreads = 256;   // at most
 constexpr int row_blocks(int bt) { return bt <= 4 ? 4 : 3; }  // blocks of an SM: what the registers allow
 
-// BT batch rows (B of them there).
 template <int BT>
 __global__ void __launch_bounds__(kRowThreads, row_blocks(BT))
     int8_rows_kernel(const uint8_t *__restrict__ x, const float *__restrict__ xs, const uint8_t *__restrict__ W,
@@ -349,6 +349,11 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(BT))
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, pieces = K / 16;
     const int steps = (pieces + blockDim.x - 1) / blockDim.x;
     const int64_t tiles = (N + kRows - 1) / kRows;
+    const int b0 = blockIdx.y * BT;  // this block's batch rows
+    B = B - b0 < BT ? B - b0 : BT;
+    x += (int64_t)b0 * K;
+    xs += b0;
+    y += b0 * N;
     auto load = [&](int64_t tile, int c, uint4 (&v)[kRows]) {
         const uint4 *w = reinterpret_cast<const uint4 *>(W + tile * kRows * K);
 #pragma unroll
@@ -888,8 +893,10 @@ Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
     s.groups = (int)(((N + kBM - 1) / kBM + cl - 1) / cl);
     s.units = (int)((K + kKU - 1) / kKU);
     const int all = s.groups * s.units, waves = (s.groups + most - 1) / most;
-    // Equal ranges, of at least four units, unless whole tiles keep nearly every block busy.
-    s.whole = s.groups * 100ll >= (int64_t)waves * most * 95;
+    // Equal ranges, of at least four units, unless whole tiles keep enough of the blocks busy: nearly all, or, at 256
+    // rows, where a part of a tile is 128 KB, three quarters.  14560 x 7168 (75 %), equal ranges and whole tiles:
+    // 25.8 and 27.9 us at 16 rows, 38 and 37 at 128, 65.5 and 58.6 at 256; 7168 x 12288 (37 %): 61.5 and 84 at 256.
+    s.whole = s.groups * 100ll >= (int64_t)waves * most * (nt == 256 ? 70 : 95);
     const int n = s.whole ? s.groups : all, c = s.whole ? n : (all + 3) / 4;
     s.clusters = c < most ? c : most;
     s.base = n / s.clusters;
@@ -940,14 +947,16 @@ template <int BT>
 cudaError_t rows_launch(const dep_int8_plan_s &pl, const uint8_t *x, const float *xs, const void *W, const float *ws,
                         uint16_t *y, int32_t B, cudaStream_t stream)
 {
-    const int64_t tiles = (pl.N + kRows - 1) / kRows, most = (int64_t)pl.sm_count * row_blocks(BT);
+    const int32_t groups = (B + BT - 1) / BT;
+    const int64_t tiles = (pl.N + kRows - 1) / kRows, room = (int64_t)pl.sm_count * row_blocks(BT) / groups,
+                  most = room < 1 ? 1 : room;
     // As many threads as share a row's pieces most evenly.
     const int pieces = (int)(pl.K / 16);
     int threads = kRowThreads;
     for (int n = kRowThreads - 32; n >= kRowThreads / 2; n -= 32)
         if ((pieces + n - 1) / n * n < (pieces + threads - 1) / threads * threads)
             threads = n;
-    int8_rows_kernel<BT><<<(unsigned)(tiles < most ? tiles : most), threads, 0, stream>>>(
+    int8_rows_kernel<BT><<<dim3((unsigned)(tiles < most ? tiles : most), (unsigned)groups), threads, 0, stream>>>(
         x, xs, static_cast<const uint8_t *>(W), ws, y, B, pl.N, (int)pl.K);
     return cudaGetLastError();
 }
@@ -955,7 +964,10 @@ cudaError_t rows_launch(const dep_int8_plan_s &pl, const uint8_t *x, const float
 cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *xs, const void *W, const float *ws,
                       uint16_t *y, int32_t B, cudaStream_t stream)
 {
-    if (B <= 8)
+    // Dot products, or tensor cores: 14560 x 7168, 21 and 26 us at 4 rows, 27.5 and 26 at 5; 49376 x 7168, 62 and 66 us
+    // at 4 rows, 83 and 66 at 5.  Small products have the shorter way through dot products, and read the weight once for
+    // every 8 rows: 7168 x 12288, 22 and 24 us at 5 rows; 2311 x 3056, 9 and 10 us at 16, 11.5 and 10.5 at 24.
+    if (B <= 4 || (double)pl.N * (double)pl.K * B * ((B + 7) / 8) < 5e8)
         return B == 1   ? rows_launch<1>(pl, x, xs, W, ws, y, B, stream)
                : B == 2 ? rows_launch<2>(pl, x, xs, W, ws, y, B, stream)
                : B <= 4 ? rows_launch<4>(pl, x, xs, W, ws, y, B, stream)
