@@ -21,9 +21,8 @@
 //               from the caller's int8 themselves.  Above, int8_widen_kernel has
 //               written it as FP16 into the workspace (padded with zeros; the two are
 //               chained by programmatic dependent launch), and warp 2 copies it by
-//               TMA: a cluster of two blocks works on neighbouring tiles, each loads
-//               half of every x slot and multicasts it to both, which halves what x
-//               takes out of L2 (x of 128 rows is twice the weight's bytes).
+//               TMA.  (x of 128 rows is twice the weight's bytes out of L2; sharing it
+//               by multicast in clusters of two blocks cost 1 to 9 us more than it saved.)
 //   CONV warps  turn a weight stage into FP16 and store it into a ring of slots of
 //               tensor memory: lane = weight row, so that the operand crosses shared
 //               memory once, as bytes.  A byte b becomes FP16 1024 + (b ^ 0x80) by one
@@ -38,15 +37,13 @@
 // Where whole tiles would leave blocks idle, the blocks take equal ranges of units, and
 // every block stores its part of a tile that several share (integers: exact in any order);
 // the one that comes last adds the parts, rounds and stores.  (Adding them by integer
-// atomics took 18 us at 128 rows: about 200 billion a second.)  Blocks wait for one
-// another only inside a cluster.
+// atomics took 18 us at 128 rows: about 200 billion a second.)  No block waits for another.
 // Bound: the weight's bytes up to about 128 rows, the tensor cores above.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <new>
 
-#include "cluster.cuh"
 #include "internal.h"
 #include "layer.h"
 #include "ptx.cuh"
@@ -78,7 +75,6 @@ constexpr int kWBytes = kBM * kKU; // a weight stage: two boxes of 128 columns
 template <int NT>
 struct Int8Shape {
     static constexpr bool DIRECT = NT <= 32;             // x comes straight from the caller
-    static constexpr int CL = NT >= 64 ? 2 : 1;          // blocks of a cluster
     static constexpr int CONV = NT <= 64 ? 8 : 4;        // converting warps (from warp 4 on)
     static constexpr int GROUPS = CONV / 4;              // four warps take 128 columns
     static constexpr int ISSUERS = GROUPS;               // issuer i takes the slots of group i
@@ -111,25 +107,24 @@ struct Int8Shape {
     }
 };
 
-// How a launch deals its units out to its clusters: `whole` groups of tiles (one tile
-// for each block of a cluster), or single units; the first `rem` clusters get one more
-// than `base` of them.
+// How a launch deals its units out to its blocks: `whole` tiles, or single units; the
+// first `rem` blocks get one more than `base` of them.
 struct Int8Split {
-    int groups, units;  // units of a tile
-    int clusters, whole, base, rem;
-    __host__ __device__ int begin(int c) const  // cluster c's first unit
+    int tiles, units;  // units of a tile
+    int blocks, whole, base, rem;
+    __host__ __device__ int begin(int c) const  // block c's first unit
     {
         return (c * base + (c < rem ? c : rem)) * (whole ? units : 1);
     }
-    __device__ int owner(int u) const  // the cluster of unit u
+    __device__ int owner(int u) const  // the block of unit u
     {
         const uint32_t v = whole ? (uint32_t)u / (uint32_t)units : (uint32_t)u, big = (uint32_t)rem * (base + 1);
         return (int)(v < big ? v / (uint32_t)(base + 1) : rem + (v - big) / (uint32_t)base);
     }
 };
 
-// Walks a cluster's units [begin, end): the part of the last group first, then from the
-// first group on, so that the parts that clusters share are done early.
+// Walks a block's units [begin, end): the part of the last tile first, then from the
+// first tile on, so that the parts that blocks share are done early.
 struct Int8Walk {
     int begin, end, units, first, last, m;
     __device__ Int8Walk(int b, int e, int ku)
@@ -137,20 +132,20 @@ struct Int8Walk {
           m(last - first + 1)
     {
     }
-    __device__ int group(int i) const { return i == 0 ? last : first + i - 1; }
-    __device__ int from(int g) const { return begin > g * units ? begin - g * units : 0; }  // units inside the group
-    __device__ int to(int g) const { return end < (g + 1) * units ? end - g * units : units; }
+    __device__ int tile(int i) const { return i == 0 ? last : first + i - 1; }
+    __device__ int from(int t) const { return begin > t * units ? begin - t * units : 0; }  // units inside the tile
+    __device__ int to(int t) const { return end < (t + 1) * units ? end - t * units : units; }
 };
 
 struct Int8Cursor {
     const Int8Walk &w;
-    int i = 0, g, u, stop;
+    int i = 0, t, u, stop;
     __device__ explicit Int8Cursor(const Int8Walk &walk) : w(walk) { seek(); }
     __device__ void seek()
     {
-        g = w.group(i);
-        u = w.from(g);
-        stop = w.to(g);
+        t = w.tile(i);
+        u = w.from(t);
+        stop = w.to(t);
     }
     __device__ bool done() const { return i >= w.m; }
     __device__ void next()
@@ -185,27 +180,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
-}
-
-// The three-dimensional load, into the same place of every block of `mask`; the bytes
-// count towards each block's own barrier.
-__device__ __forceinline__ void tma_load_3d_multicast(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1,
-                                                      int32_t c2, uint32_t bar, uint16_t mask, uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "h"(mask), "l"(policy)
-        : "memory");
-}
-
-// Arrive on the barrier at this place in every block of `mask` when the MMAs so far complete.
-__device__ __forceinline__ void commit_multicast(uint32_t bar, uint16_t mask)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(mask)
-        : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, FP16 inputs, FP32 accumulation.
@@ -428,16 +402,14 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     uint16_t *bounds = reinterpret_cast<uint16_t *>(tmem_slot + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = S::CL == 1 ? 0 : (int)cluster_rank();
-    const int c = S::CL == 1 ? blockIdx.x : blockIdx.x / S::CL;
-    const int KU = p.split.units;
+    const int c = blockIdx.x, KU = p.split.units;
     const Int8Walk walk(p.split.begin(c), p.split.begin(c + 1), KU);
 
     // Weight copies (thread 0); the first ones start before anything else is set up.
     Int8Cursor wcur(walk);
     int wst = 0;
     auto copy_w = [&](uint64_t pol) {
-        const int row = (wcur.g * S::CL + rank) * kBM, col = wcur.u * kKU;
+        const int row = wcur.t * kBM, col = wcur.u * kKU;
         const uint32_t dst = w0 + wst * kWBytes, bar = wfull + 8 * wst;
         mbar_arrive_expect_tx(bar, kWBytes);
         tma_load_2d(dst, &tmW, col, row, bar, pol);
@@ -460,8 +432,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                 mbar_init(bar + 8 * i, count);
         };
         init(wempty, S::WS, S::CONV);
-        init(sfull, S::SLOTS, 4 + 1);    // four converting warps, and x
-        init(sempty, S::SLOTS, S::CL);  // the MMAs of every block that x went to
+        init(sfull, S::SLOTS, 4 + 1);  // four converting warps, and x
+        init(sempty, S::SLOTS, 1);       // its MMAs
         init(accf, S::BUFS, S::ISSUERS);
         init(acce, S::BUFS, S::EPI);
         init(done, 1, S::ISSUERS);
@@ -474,8 +446,6 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     }
     tc::fence_before();
     __syncthreads();
-    if (S::CL > 1)
-        cluster_sync();  // the peer's barriers exist before anything arrives on them
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     auto give_up = [&](int code) {
@@ -580,7 +550,6 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             prefetch_tmap(&tmX);
             const uint64_t pol = policy_evict_last();
             griddep_wait();  // x in FP16 is written by the preceding grid
-            constexpr int ROWS = NT / S::CL;  // x rows that this block loads
             Int8Cursor cur(walk);
             int s = 0;
             uint32_t ph = 0;
@@ -588,17 +557,14 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             bool ok = true;
             for (; ok && !cur.done(); cur.next()) {
                 for (int h = 0; h < S::PER; ++h) {
-                    if (*abort_flag || !mbar_wait_cluster(sempty + 8 * s, ph ^ 1u, p.limit_ns)) {
+                    if (*abort_flag || !mbar_wait(sempty + 8 * s, ph ^ 1u, p.limit_ns)) {
                         give_up(DEP_DEV_TIMEOUT_PRODUCER);
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(sfull + 8 * s, S::X_BYTES);
                     const int block64 = cur.u * (kKU / 64) + h * (S::SK / 64);
-#pragma unroll
-                    for (int j = 0; j < S::SK / 64; ++j)  // one copy for each 64 columns: its rows are a part of the slice
-                        tma_load_3d_multicast(x0 + s * S::X_BYTES + (j * NT + rank * ROWS) * 128, &tmX, 0, rank * ROWS,
-                                              block64 + j, sfull + 8 * s, (1 << S::CL) - 1, pol);
+                    tma_load_3d(x0 + s * S::X_BYTES, &tmX, 0, 0, block64, sfull + 8 * s, pol);
                     ++issued;
                     if (++s == S::SLOTS) {
                         s = 0;
@@ -606,14 +572,12 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     }
                 }
             }
-            // Every slot used was consumed (by both blocks): no copy of this block's is in flight
-            // anywhere, and no arrival at its barriers is left.
             for (int64_t i = issued < S::SLOTS ? issued : S::SLOTS; i > 0; --i) {
                 if (--s < 0) {
                     s = S::SLOTS - 1;
                     ph ^= 1u;
                 }
-                if (!mbar_wait_cluster(sempty + 8 * s, ph, p.limit_ns))
+                if (!mbar_wait(sempty + 8 * s, ph, p.limit_ns))  // copied, and consumed
                     record_status(p.status, DEP_DEV_TIMEOUT_PRODUCER);
             }
         }
@@ -629,8 +593,8 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             if (!ok)
                 give_up(DEP_DEV_TIMEOUT_MMA);
             for (int seg = 0; seg < walk.m && ok; ++seg) {
-                const int g = walk.group(seg), end = walk.to(g);
-                for (int u = walk.from(g); u < end && ok;) {
+                const int t = walk.tile(seg), end = walk.to(t);
+                for (int u = walk.from(t); u < end && ok;) {
                     const int stop = run_end(u, end);
                     if (!mbar_wait(acce + 8 * buf, bph ^ 1u, p.limit_ns)) {
                         give_up(DEP_DEV_TIMEOUT_MMA);
@@ -641,7 +605,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                     const uint32_t d = tmem + (uint32_t)(S::ACC0 + (buf * S::ISSUERS + mi) * NT);
                     uint32_t accumulate = 0;
                     for (int n = (stop - u) * (S::PER / S::ISSUERS); n > 0; --n) {
-                        if (!ready && (*abort_flag || !mbar_wait_cluster(sfull + 8 * s, sph, p.limit_ns))) {
+                        if (!ready && (*abort_flag || !mbar_wait(sfull + 8 * s, sph, p.limit_ns))) {
                             give_up(DEP_DEV_TIMEOUT_MMA);
                             ok = false;
                             break;
@@ -657,10 +621,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                                        accumulate);
                             accumulate = 1;
                         }
-                        if (S::CL == 1)
-                            tc::commit(freed);
-                        else
-                            commit_multicast(freed, (1 << S::CL) - 1);
+                        tc::commit(freed);
                     }
                     if (!ok)
                         break;
@@ -752,14 +713,14 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         if (!ok && lane == 0)
             give_up(DEP_DEV_TIMEOUT_EPILOGUE);
         for (int seg = 0; seg < walk.m && ok; ++seg) {
-            const int g = walk.group(seg), end = walk.to(g);
-            const int64_t t = (int64_t)g * S::CL + rank, n = t * kBM + 32 * q + lane;
+            const int t = walk.tile(seg), end = walk.to(t);
+            const int64_t n = (int64_t)t * kBM + 32 * q + lane;
             const float ws = n < p.N ? p.ws[n] : 0.0f;
             int acc[S::COLS];
 #pragma unroll
             for (int j = 0; j < S::COLS; ++j)
                 acc[j] = 0;
-            for (int u = walk.from(g); u < end;) {
+            for (int u = walk.from(t); u < end;) {
                 ok = __all_sync(~0u, mbar_wait(accf + 8 * buf, bph, p.limit_ns));
                 if (!ok) {
                     if (lane == 0)
@@ -796,12 +757,12 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
                 if (j < cols)
                     tmem_st16(back + j, acc + j);
             tmem_wait_st();
-            // A tile that several clusters share: every block stores its part, and the one that comes last adds them.
+            // A tile that several blocks share: each stores its part, and the one that comes last adds them.
             bool last = true;
-            const int ca = p.split.owner(g * KU), parts = p.split.owner((g + 1) * KU - 1) - ca + 1;
-            const auto part = [&](int cl) {  // this warp's part of the block of cluster cl
-                const int slot = p.split.begin(cl) > g * KU ? 0 : 1;  // the tile that its range starts in, or the last
-                return p.parts + (((int64_t)(cl * S::CL + rank) * 2 + slot) * NT + c0) * kBM + 32 * q + lane;
+            const int ca = p.split.owner(t * KU), parts = p.split.owner((t + 1) * KU - 1) - ca + 1;
+            const auto part = [&](int b) {  // this warp's part of block b's
+                const int slot = p.split.begin(b) > t * KU ? 0 : 1;  // the tile that its range starts in, or the last
+                return p.parts + (((int64_t)b * 2 + slot) * NT + c0) * kBM + 32 * q + lane;
             };
             if (parts > 1) {
                 int *mine = part(c);
@@ -873,8 +834,6 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (S::CL > 1)
-        cluster_sync();  // neither block leaves while the other may still send to it
     if (warp == 1) {
         tc::fence_after();
         tc::dealloc(tmem, 512);
@@ -884,23 +843,20 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
 // MMA width of a pass of B rows.
 int width(int32_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : 256; }
 
-int cluster_of(int nt) { return nt >= 64 ? 2 : 1; }
-
 Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
 {
-    const int cl = cluster_of(nt), most = sms / cl;
     Int8Split s;
-    s.groups = (int)(((N + kBM - 1) / kBM + cl - 1) / cl);
+    s.tiles = (int)((N + kBM - 1) / kBM);
     s.units = (int)((K + kKU - 1) / kKU);
-    const int all = s.groups * s.units, waves = (s.groups + most - 1) / most;
+    const int all = s.tiles * s.units, waves = (s.tiles + sms - 1) / sms;
     // Equal ranges, of at least four units, unless whole tiles keep enough of the blocks busy: nearly all, or, at 256
     // rows, where a part of a tile is 128 KB, three quarters.  14560 x 7168 (75 %), equal ranges and whole tiles:
     // 25.8 and 27.9 us at 16 rows, 38 and 37 at 128, 65.5 and 58.6 at 256; 7168 x 12288 (37 %): 61.5 and 84 at 256.
-    s.whole = s.groups * 100ll >= (int64_t)waves * most * (nt == 256 ? 70 : 95);
-    const int n = s.whole ? s.groups : all, c = s.whole ? n : (all + 3) / 4;
-    s.clusters = c < most ? c : most;
-    s.base = n / s.clusters;
-    s.rem = n % s.clusters;
+    s.whole = s.tiles * 100ll >= (int64_t)waves * sms * (nt == 256 ? 70 : 95);
+    const int n = s.whole ? s.tiles : all, c = s.whole ? n : (all + 3) / 4;
+    s.blocks = c < sms ? c : sms;
+    s.base = n / s.blocks;
+    s.rem = n % s.blocks;
     return s;
 }
 
@@ -915,7 +871,6 @@ template <int NT>
 cudaError_t int8_launch(const dep_int8_plan_s &pl, const void *W, const Int8Params &p, cudaStream_t stream)
 {
     using S = Int8Shape<NT>;
-    static_assert(S::CL == (NT >= 64 ? 2 : 1), "cluster_of");
     cudaError_t e = int8_prepare<NT>();
     if (e != cudaSuccess)
         return e;
@@ -924,23 +879,10 @@ cudaError_t int8_launch(const dep_int8_plan_s &pl, const void *W, const Int8Para
         return cudaErrorInvalidValue;
     if (S::DIRECT)
         tmX = tmW;  // not used
-    else if (encode_bf16_3d_blocks(&tmX, pl.xh, (uint64_t)(p.split.units * kKU), NT, NT / S::CL, 1) != CUDA_SUCCESS)
+    else if (encode_bf16_3d_blocks(&tmX, pl.xh, (uint64_t)(p.split.units * kKU), NT, NT, S::SK / 64) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.split.clusters * S::CL);
-    cfg.blockDim = dim3(S::THREADS);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = S::DIRECT ? 0 : 1;  // after int8_widen_kernel
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = S::CL;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, int8_kernel<NT>, tmW, tmX, p);
+    return launch(int8_kernel<NT>, dim3(p.split.blocks), dim3(S::THREADS), (size_t)S::SMEM, stream,
+                  !S::DIRECT /* after int8_widen_kernel */, tmW, tmX, p);
 }
 
 template <int BT>
@@ -1051,9 +993,9 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
     for (int w = 16; w <= nt; w *= 2) {
         const dep::Int8Split s = dep::split_for(N, K, w, p->sm_count);
         if (!s.whole)  // two for each block
-            parts = (size_t)s.clusters * dep::cluster_of(w) * 2 * w * dep::kBM * sizeof(int);
+            parts = (size_t)s.blocks * 2 * w * dep::kBM * sizeof(int);
     }
-    const size_t counters = ((size_t)(tiles + 1) * 16 * sizeof(int) + 255) / 256 * 256;  // (a cluster's last tile may lie past N)
+    const size_t counters = ((size_t)tiles * 16 * sizeof(int) + 255) / 256 * 256;
     p->clear_bytes = 256 + counters;
     p->bytes = p->clear_bytes + parts + (nt > 32 ? (size_t)(nt + 1) * Kp * 2 : 0);
     if (cudaMalloc(&p->block, p->bytes) != cudaSuccess) {
