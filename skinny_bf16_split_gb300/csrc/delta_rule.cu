@@ -231,7 +231,7 @@ cudaError_t recurrent_launch(const DeltaParams &p, cudaStream_t s)
 
 constexpr int kC = 16;            // tokens of a chunk
 constexpr int kPrep = 128;        // threads that prepare a chunk; two such groups take turns
-constexpr int kTS = 24;           // row stride of 16-wide matrices in shared memory: float2 reads without conflicts
+constexpr int kTT = 20;           // row stride of 16-wide matrices in shared memory
 
 // Barrier `id` of the block's hardware barriers, for n threads.
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -394,8 +394,9 @@ struct ChunkShared {
             float g[kC][DK];
             uint16_t k[kC][DK + 8], q[kC][DK + 8];
         } raw;
-        alignas(16) float A[kC][kC], T[kC][kTS];
-        alignas(16) float part[4][48], norm[4][48], pow2[4][32], beta[kC], g[kC];
+        alignas(16) float A[kC][kC];
+        alignas(16) float T[kC][kTT], Tk[kC][kTT];  // columns of T, and of T over k's scales
+        alignas(16) float part[4][48], norm[4][48], inv[4][32], sw[4][kC], beta[kC], g[kC];
     } prep[2];
     int order[kSort + 1];
 };
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             (&pr.A[0][0])[i] = 0.f;
         auto put_b = [&](int i, int j, float v) {  // B_ij into its lane's sixteen bytes
             uint32_t hi, lo;
-            f16_split2(v * (pr.pow2[pw][16 + i] * pr.pow2[pw][j] * (1.f / kUnB)), 0.f, hi, lo);
+            f16_split2(v * (1.f / kUnB), 0.f, hi, lo);
             uint16_t *d = reinterpret_cast<uint16_t *>(&sg.B[i][(j & 7) >> 1]) + (j >> 3) * 2 + (j & 1);
             d[0] = (uint16_t)hi;
             d[4] = (uint16_t)lo;
@@ -725,10 +726,10 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 // every warp finishes the sums for itself
                 const float sum = (pr.part[0][lane] + pr.part[1][lane]) + (pr.part[2][lane] + pr.part[3][lane]);
                 const float f = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
-                pr.norm[pw][lane] = f;
-                // 2^e > the norm of the normalised row >= its largest value; the power of two that makes it 2^8
+                // 2^e > the norm of the normalised row >= its largest value; rows are taken times 2^(8 - e) from here on
                 const int e = (((int)(__float_as_uint(sum * f * f) >> 23) - 127 + 2) >> 1);
-                pr.pow2[pw][lane] = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+                pr.norm[pw][lane] = f * __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+                pr.inv[pw][lane] = __uint_as_float((uint32_t)(127 - 8 + e) << 23);
                 if (lane < 16)
                     pr.norm[pw][32 + lane] = (pr.part[0][32 + lane] + pr.part[1][32 + lane]) +
                                              (pr.part[2][32 + lane] + pr.part[3][32 + lane]);
@@ -750,31 +751,33 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             if (pt < kC)
                 put_b(pt, pt, pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt]);
             if (pt < 32)
-                (pt < 16 ? sg.ik : sg.iq)[pt & 15] = 1.f / pr.pow2[pw][pt];
-            float pk[kC];  // k's scales
+                (pt < 16 ? sg.ik : sg.iq)[pt & 15] = pr.inv[pw][pt];
 #pragma unroll
             for (int i = 0; i < kC; i += 4) {
                 const float4 nk = *reinterpret_cast<const float4 *>(&pr.norm[pw][i]);
                 const float4 nq = *reinterpret_cast<const float4 *>(&pr.norm[pw][16 + i]);
-                const float4 sk = *reinterpret_cast<const float4 *>(&pr.pow2[pw][i]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     k[i + e] *= (&nk.x)[e];
                     q[i + e] *= (&nq.x)[e];
-                    pk[i + e] = (&sk.x)[e];
                 }
             }
             if (tokens) {
                 float P = 1.f;
 #pragma unroll
-                for (int i = 0; i < kC; ++i) {
-                    P *= a[i];
-                    kp[i] = k[i] * P;
+                for (int i = 0; i < kC; i += 2) {
+                    const float P0 = P * a[i], P1 = P0 * a[i + 1];
+                    P = P1;
+                    kp[i] = k[i] * P0;
+                    kp[i + 1] = k[i + 1] * P1;
                     uint32_t hi, lo;
-                    f16_split2(q[i] * (P * pr.pow2[pw][16 + i]), 0.f, hi, lo);
-                    uint16_t *qd = reinterpret_cast<uint16_t *>(&sg.qp[i][0]) + at;
-                    qd[0] = (uint16_t)hi;
-                    qd[4] = (uint16_t)lo;
+                    f16_split2(q[i] * P0, q[i + 1] * P1, hi, lo);
+                    uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.qp[i][0]) + at;
+                    uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.qp[i + 1][0]) + at;
+                    d0[0] = (uint16_t)hi;
+                    d0[4] = (uint16_t)lo;
+                    d1[0] = (uint16_t)(hi >> 16);
+                    d1[4] = (uint16_t)(lo >> 16);
                 }
                 sg.last[ch] = P;
             }
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 float R = 1.f;
 #pragma unroll
                 for (int i = kC - 1; i >= 0; --i) {
-                    k[i] *= R * pk[i];
+                    k[i] *= R;
                     R *= a[i];
                 }
 #pragma unroll
@@ -836,7 +839,7 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 for (int e = 0; e < 2; ++e) {
                     const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
                     if ((n & ~(b - 1)) == (g & ~(b - 1))) {
-                        pr.A[i][j] = (d[2][e] + d[1][e]) + d[0][e];
+                        pr.A[i][j] = ((d[2][e] + d[1][e]) + d[0][e]) * (pr.inv[pw][i] * pr.inv[pw][j]);
                         put_b(i, j, (d[2][2 + e] + d[1][2 + e]) + d[0][2 + e]);
                     }
                 }
@@ -857,51 +860,61 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     }
                     x[i] = (i == j ? 1.f : 0.f) - pr.beta[i] * (d0 + d1);
                 }
-                const float b = pr.beta[j];
+                const float b = pr.beta[j], bk = b * pr.inv[pw][j];
                 if (lane < 16)
 #pragma unroll
-                    for (int i = 0; i < kC; ++i)
-                        pr.T[i][j] = i >= j ? x[i] * b : 0.f;
+                    for (int i = 0; i < kC; i += 4) {  // x is zero above its own row
+                        *reinterpret_cast<float4 *>(&pr.T[j][i]) = make_float4(x[i] * b, x[i + 1] * b, x[i + 2] * b, x[i + 3] * b);
+                        *reinterpret_cast<float4 *>(&pr.Tk[j][i]) =
+                            make_float4(x[i] * bk, x[i + 1] * bk, x[i + 2] * bk, x[i + 3] * bk);
+                    }
             }
             bar_sync(kBarPrep, kPrep);
             if (pt < 4 * kC) {  // T for the state's warps
                 const int i = pt >> 2, t = pt & 3;
-                const float2 a = ld2(&pr.T[i][2 * t]), b = ld2(&pr.T[i][2 * t + 8]);
                 uint4 p01;
                 uint2 p2;
-                bf16_split3(a.x, a.y, p01.x, p01.z, p2.x);
-                bf16_split3(b.x, b.y, p01.y, p01.w, p2.y);
+                bf16_split3(pr.T[2 * t][i], pr.T[2 * t + 1][i], p01.x, p01.z, p2.x);
+                bf16_split3(pr.T[2 * t + 8][i], pr.T[2 * t + 9][i], p01.y, p01.w, p2.y);
                 sg.T01[i][t] = p01;
                 sg.T2[i][t] = p2;
             }
             {
-                // |W_i| <= sum_j |T_ij| times the bound on k_j's values (2^8 over its scale)
+                // |W_i| <= sum_j |T_ij| times the bound on k_j's values, 2^8 over its scale
                 float top = 0.f, inv;
                 if (lane < kC)
 #pragma unroll
                     for (int j = 0; j < kC; ++j)
-                        top = fmaf(fabsf(pr.T[lane][j]), 256.f / pr.pow2[pw][j], top);
-                const float s = scale_for(top, inv);
+                        top += fabsf(pr.Tk[j][lane]);
+                const float s = scale_for(256.f * top, inv);
+                if (lane < kC)
+                    pr.sw[pw][lane] = s;
                 if (pw == 0 && lane < kC)
                     sg.iw[lane] = inv;
+                float w[kC] = {};
 #pragma unroll
-                for (int i = 0; i < kC; ++i) {
-                    float w = 0.f;
+                for (int j = 0; j < kC; ++j)
 #pragma unroll
-                    for (int j = 0; j <= i; j += 4) {
-                        const float4 r = *reinterpret_cast<const float4 *>(&pr.T[i][j]);
+                    for (int i = j & ~3; i < kC; i += 4) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(&pr.Tk[j][i]);
 #pragma unroll
-                        for (int e = 0; e < 4 && j + e <= i; ++e)
-                            w = fmaf((&r.x)[e], kp[j + e], w);
+                        for (int e = 0; e < 4; ++e)
+                            w[i + e] = fmaf((&c4.x)[e], kp[j], w[i + e]);
                     }
-                    uint32_t hi, lo;
-                    f16_split2(w * __shfl_sync(~0u, s, i), 0.f, hi, lo);
-                    if (tokens) {
-                        uint16_t *d = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
-                        d[0] = (uint16_t)hi;
-                        d[4] = (uint16_t)lo;
+                __syncwarp();
+                if (tokens)
+#pragma unroll
+                    for (int i = 0; i < kC; i += 2) {
+                        const float2 s2 = ld2(&pr.sw[pw][i]);
+                        uint32_t hi, lo;
+                        f16_split2(w[i] * s2.x, w[i + 1] * s2.y, hi, lo);
+                        uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
+                        uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.w[i + 1][0]) + at;
+                        d0[0] = (uint16_t)hi;
+                        d0[4] = (uint16_t)lo;
+                        d1[0] = (uint16_t)(hi >> 16);
+                        d1[4] = (uint16_t)(lo >> 16);
                     }
-                }
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");  // V
             bar_arrive(kBarFull + grp, kThreads);
