@@ -486,8 +486,22 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             const int st = (int)(c & 1);
             bar_sync(kBarFull + st, kThreads);
             const ChunkStage<DK, MW> &sg = sm.stage[st];
-            float U[2][4] = {}, X[2][4] = {}, O[2][4] = {};
-            {  // U^T = V^T T^T - S^T W^T, the first part
+            float X[2][4] = {}, O[2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < NT / 2; ++ks) {
+                uint32_t ah[4], al[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f16_split2(S[2 * ks + i][0], S[2 * ks + i][1], ah[2 * i], al[2 * i]);
+                    f16_split2(S[2 * ks + i][2], S[2 * ks + i][3], ah[2 * i + 1], al[2 * i + 1]);
+                }
+                float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
+                const uint4 b[4] = {sg.w[g][4 * ks + t], sg.qp[g][4 * ks + t], sg.w[8 + g][4 * ks + t],
+                                    sg.qp[8 + g][4 * ks + t]};
+                mma_f16x3(d, ah, al, b);
+            }
+            float U[2][4] = {};
+            {  // U^T = V^T T^T - S^T W^T, the part with V
                 uint32_t a[4];
                 const uint32_t at = (uint32_t)__cvta_generic_to_shared(
                     &sg.v[(lane >> 4) * 8 + (lane & 7)][16 * warp + 8 * (lane >> 3 & 1)]);
@@ -503,19 +517,6 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                 mma_bf16(U[1], a, b1.z, b1.w);
                 mma_bf16(U[0], a, b0.x, b0.y);
                 mma_bf16(U[1], a, b1.x, b1.y);
-            }
-#pragma unroll
-            for (int ks = 0; ks < NT / 2; ++ks) {
-                uint32_t ah[4], al[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    f16_split2(S[2 * ks + i][0], S[2 * ks + i][1], ah[2 * i], al[2 * i]);
-                    f16_split2(S[2 * ks + i][2], S[2 * ks + i][3], ah[2 * i + 1], al[2 * i + 1]);
-                }
-                float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
-                const uint4 b[4] = {sg.w[g][4 * ks + t], sg.qp[g][4 * ks + t], sg.w[8 + g][4 * ks + t],
-                                    sg.qp[8 + g][4 * ks + t]};
-                mma_f16x3(d, ah, al, b);
             }
             // U' = U / (k's scale), in parts scaled by row: the left operand of B and of K.R
             uint32_t uh[4], ul[4];
@@ -539,9 +540,9 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
                     f16_split2(U[n][2] * s1, U[n][3] * s1, uh[2 * n + 1], ul[2 * n + 1]);
                 }
             }
-            float D[2][4] = {};  // U^T B^T
+            float Y[2][4] = {};  // U^T B^T
             {
-                float(*const d[2])[4] = {&D[0], &D[1]};
+                float(*const d[2])[4] = {&Y[0], &Y[1]};
                 const uint4 b[2] = {sg.B[g][t], sg.B[8 + g][t]};
                 mma_f16x3(d, uh, ul, b);
             }
@@ -549,39 +550,10 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
-                O[n][0] = fmaf(D[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
-                O[n][1] = fmaf(D[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
-                O[n][2] = fmaf(D[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
-                O[n][3] = fmaf(D[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
-            }
-            {  // S <- S diag(P_15) + U^T (K.R)
-                if (__any_sync(~0u, j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
-                    // U beyond what S's scales leave room for: make room
-                    rescale(j0 > 0x1p60f * i0 ? 0x1p60f * i0 / j0 : 1.f, j1 > 0x1p60f * i1 ? 0x1p60f * i1 / j1 : 1.f);
-                }
-                const float f0 = j0 * r0, f1 = j1 * r1;
-                float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-                for (int n = 0; n < NT; n += 4) {
-                    float D[4][4] = {};
-                    float(*const d[4])[4] = {&D[0], &D[1], &D[2], &D[3]};
-                    const int sw = t ^ (g >> 1 & 3);
-                    const uint4 b[4] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw], sg.kr[8 * n + 16 + g][sw],
-                                        sg.kr[8 * n + 24 + g][sw]};
-                    mma_f16x3(d, uh, ul, b);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
-                        float(&s)[4] = S[n + i];
-                        s[0] = fmaf(D[i][0], f0, s[0] * a.x);
-                        s[1] = fmaf(D[i][1], f0, s[1] * a.y);
-                        s[2] = fmaf(D[i][2], f1, s[2] * a.x);
-                        s[3] = fmaf(D[i][3], f1, s[3] * a.y);
-                        m0 = max3_abs(m0, s[0], s[1]);
-                        m1 = max3_abs(m1, s[2], s[3]);
-                    }
-                }
-                keep_range(m0, m1);
+                O[n][0] = fmaf(Y[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
+                O[n][1] = fmaf(Y[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
+                O[n][2] = fmaf(Y[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
+                O[n][3] = fmaf(Y[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
             }
             // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
             uint32_t r[4];
@@ -600,6 +572,46 @@ __global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const 
             if (live && tok < len)
                 *reinterpret_cast<uint4 *>(p.o + (t0 + tok) * p.os + (int64_t)h * p.Dv + row0 + 8 * (lane & 1)) =
                     *reinterpret_cast<const uint4 *>(&sg.v[lane >> 1][16 * warp + 8 * (lane & 1)]);
+            {  // S <- S diag(P_15) + U^T (K.R)
+                if (__any_sync(~0u, j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
+                    // U beyond what S's scales leave room for: make room
+                    rescale(j0 > 0x1p60f * i0 ? 0x1p60f * i0 / j0 : 1.f, j1 > 0x1p60f * i1 ? 0x1p60f * i1 / j1 : 1.f);
+                }
+                const float f0 = j0 * r0, f1 = j1 * r1;
+                float m0 = 0.f, m1 = 0.f;
+                // two tiles of eight channels at a time, the products of the next two before the sums of these
+                const int sw = t ^ (g >> 1 & 3);
+                float D[2][2][4];
+                auto products = [&](int n, float (&d2)[2][4]) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            d2[i][e] = 0.f;
+                    float(*const d[2])[4] = {&d2[0], &d2[1]};
+                    const uint4 b[2] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw]};
+                    mma_f16x3(d, uh, ul, b);
+                };
+                products(0, D[0]);
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    if (n + 2 < NT)
+                        products(n + 2, D[(n / 2 + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
+                        float(&s)[4] = S[n + i];
+                        const float(&d)[4] = D[(n / 2) & 1][i];
+                        s[0] = fmaf(d[0], f0, s[0] * a.x);
+                        s[1] = fmaf(d[1], f0, s[1] * a.y);
+                        s[2] = fmaf(d[2], f1, s[2] * a.x);
+                        s[3] = fmaf(d[3], f1, s[3] * a.y);
+                        m0 = max3_abs(m0, s[0], s[1]);
+                        m1 = max3_abs(m1, s[2], s[3]);
+                    }
+                }
+                keep_range(m0, m1);
+            }
             if (c + 2 < chunks)
                 bar_arrive(kBarEmpty + st, kThreads);
         }
