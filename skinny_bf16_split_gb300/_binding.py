@@ -432,63 +432,64 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _on(device, call, args, stream):
-    """call(args, stream) with `device` current; stream None: its current stream."""
+def _on(index, call, args, stream):
+    """call(args, stream) with device `index` current; stream None: its current stream."""
     import torch
-    if device.index == torch.cuda.current_device():
-        call(args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream)
+    if index == torch.cuda.current_device():
+        call(args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
         return
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         call(args, stream)
 
 
-def _rows(t, name, dtype, device, rows, cols):
+def _rows(t, name, dtype, index, shape):
     """Stride between the rows of a matrix whose rows are contiguous."""
-    if t.dtype != dtype or t.device != device or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (
-            cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a {dtype} matrix [{rows}, {cols}] with contiguous rows on {device}")
-    return t.stride(0) if rows > 1 else cols
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        row, col = t.stride()
+        if col == 1 or shape[1] <= 1:
+            return row if shape[0] > 1 else shape[1]
+    raise ValueError(f"{name} must be a {dtype} matrix {tuple(shape)} with contiguous rows on cuda:{index}")
 
 
 def _norm_call(call, x, weight, residual, residual_out, eps, quant, out, out_scale, stream):
     import torch
     if quant not in _QUANT:
         raise ValueError("quant must be None, 'int8' or 'e4m3'")
-    if x.dim() != 2 or not x.is_cuda:
+    shape, dev, bf16 = x.shape, x.get_device(), torch.bfloat16
+    if len(shape) != 2 or dev < 0:
         raise ValueError("x must be a CUDA matrix [rows, cols]")
-    rows, cols = x.shape
-    dev, bf16 = x.device, torch.bfloat16
+    rows, cols = shape
     w_ptr = r_ptr = ro_ptr = s_ptr = None
     r_stride = ro_stride = 0
     if weight is not None:
-        if weight.dtype != bf16 or weight.device != dev or weight.dim() != 1 or weight.shape[0] != cols or (
+        if weight.dtype is not bf16 or weight.get_device() != dev or weight.shape != (cols,) or (
                 not weight.is_contiguous()):
-            raise ValueError(f"weight must be a contiguous bfloat16 vector of {cols} on {dev}")
+            raise ValueError(f"weight must be a contiguous bfloat16 vector of {cols} on cuda:{dev}")
         w_ptr = weight.data_ptr()
     if residual is not None:
-        r_ptr, r_stride = residual.data_ptr(), _rows(residual, "residual", bf16, dev, rows, cols)
+        r_ptr, r_stride = residual.data_ptr(), _rows(residual, "residual", bf16, dev, shape)
         if residual_out is None:
             ro_ptr, ro_stride = r_ptr, r_stride
         else:
-            ro_ptr, ro_stride = residual_out.data_ptr(), _rows(residual_out, "residual_out", bf16, dev, rows, cols)
+            ro_ptr, ro_stride = residual_out.data_ptr(), _rows(residual_out, "residual_out", bf16, dev, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     dtype = bf16 if quant is None else torch.int8 if quant == "int8" else torch.float8_e4m3fn
     if out is None:
-        out = _empty((rows, cols), dtype, dev, stream)
+        out = _empty((rows, cols), dtype, x.device, stream)
     if quant is not None:
         want = (rows,) if quant == "int8" else (rows, -(-cols // DEP_QUANT_GROUP))
         if out_scale is None:
-            out_scale = _empty(want, torch.float32, dev, stream)
-        elif out_scale.dtype != torch.float32 or out_scale.device != dev or out_scale.shape != want or (
+            out_scale = _empty(want, torch.float32, x.device, stream)
+        elif out_scale.dtype is not torch.float32 or out_scale.get_device() != dev or out_scale.shape != want or (
                 not out_scale.is_contiguous()):
-            raise ValueError(f"out_scale must be a contiguous float32 tensor of shape {want} on {dev}")
+            raise ValueError(f"out_scale must be a contiguous float32 tensor of shape {want} on cuda:{dev}")
         s_ptr = out_scale.data_ptr()
     elif out_scale is not None:
         raise ValueError("out_scale needs an 8-bit format")
     _on(dev, call, dep_norm_args_t(
-        x.data_ptr(), r_ptr, w_ptr, ro_ptr, out.data_ptr(), s_ptr, _rows(x, "x", bf16, dev, rows, cols), r_stride,
-        ro_stride, _rows(out, "out", dtype, dev, rows, cols), rows, cols, _QUANT[quant], eps), stream)
+        x.data_ptr(), r_ptr, w_ptr, ro_ptr, out.data_ptr(), s_ptr, _rows(x, "x", bf16, dev, shape), r_stride,
+        ro_stride, _rows(out, "out", dtype, dev, shape), rows, cols, _QUANT[quant], eps), stream)
     return out if quant is None else (out, out_scale)
 
 
@@ -512,17 +513,17 @@ def quantize_rows(x, *, quant="int8", out=None, out_scale=None, stream=None):
     return _norm_call(dep_quantize_rows, x, None, None, None, 0.0, quant, out, out_scale, stream)
 
 
-def _heads(t, name, dtype, device, shape):
+def _heads(t, name, dtype, index, shape):
     """Stride between the tokens of [tokens, heads, ...] whose inner dimensions are contiguous."""
-    inner, ok = 1, t.dtype == dtype and t.device == device and t.shape == shape
-    if ok:
-        strides = t.stride()
-        for d in range(len(shape) - 1, 0, -1):
-            ok = ok and (shape[d] == 1 or strides[d] == inner)
-            inner *= shape[d]
-    if not ok:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on {device}")
-    return strides[0] if shape[0] > 1 else inner
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        strides, inner = t.stride(), shape[-1]
+        ok = strides[-1] == 1 or inner == 1
+        if len(shape) == 3:
+            ok = ok and (strides[1] == inner or shape[1] == 1)
+            inner *= shape[1]
+        if ok:
+            return strides[0] if shape[0] > 1 else inner
+    raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on cuda:{index}")
 
 
 def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens=None, n_seq: int | None = None,
@@ -541,39 +542,43 @@ def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens
     (outside 0..n_states-1: padding).  scale defaults to Dk ** -0.5.  Returns out,
     bfloat16 [tokens, Hv, Dv] (allocated where omitted)."""
     import torch
-    if q.dim() != 3 or v.dim() != 3 or not q.is_cuda:
+    dev, bf16, f32 = q.get_device(), torch.bfloat16, torch.float32
+    qk_shape, v_shape = q.shape, v.shape
+    if len(qk_shape) != 3 or len(v_shape) != 3 or dev < 0:
         raise ValueError("q, k [tokens, Hq, Dk] and v [tokens, Hv, Dv] must be CUDA tensors of three dimensions")
-    dev, bf16, f32 = q.device, torch.bfloat16, torch.float32
-    T, hq, dk = qk_shape = q.shape
-    _, hv, dv = v.shape
-    v_shape, channel = (T, hv, dv), g.dim() == 3
+    T, hq, dk = qk_shape
+    _, hv, dv = v_shape
+    if v_shape[0] != T:
+        raise ValueError(f"v must have q's {T} tokens")
+    channel = g.dim() == 3
     if state_out is None:
         state_out = state
         if state is None:
             raise ValueError("state_out must be given where state is not")
+    n_states = state_out.shape[0]
     for s in (state_out,) if state is None or state is state_out else (state, state_out):
-        if s.dtype != f32 or s.device != dev or s.dim() != 4 or s.shape[1:] != (hv, dv, dk) or (
-                not s.is_contiguous()) or s.shape[0] != state_out.shape[0]:
-            raise ValueError(f"state and state_out must be contiguous float32 tensors [n_states, {hv}, {dv}, {dk}] on {dev}")
+        if s.dtype is not f32 or s.get_device() != dev or s.shape != (n_states, hv, dv, dk) or not s.is_contiguous():
+            raise ValueError(
+                f"state and state_out must be contiguous float32 tensors [n_states, {hv}, {dv}, {dk}] on cuda:{dev}")
     if cu_seqlens is not None:
         n = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
-        if cu_seqlens.dtype != torch.int32 or cu_seqlens.device != dev or n < 0 or not cu_seqlens.is_contiguous() or (
-                n_seq is not None and n_seq != n):
-            raise ValueError(f"cu_seqlens must be a contiguous int32 vector of n_seq + 1 on {dev}")
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.get_device() != dev or n < 0 or (
+                not cu_seqlens.is_contiguous() or (n_seq is not None and n_seq != n)):
+            raise ValueError(f"cu_seqlens must be a contiguous int32 vector of n_seq + 1 on cuda:{dev}")
         n_seq = n
     elif n_seq is None:
         n_seq = 1
-    if slots is not None and (slots.dtype != torch.int32 or slots.device != dev or slots.shape != (n_seq,)
+    if slots is not None and (slots.dtype is not torch.int32 or slots.get_device() != dev or slots.shape != (n_seq,)
                               or not slots.is_contiguous()):
-        raise ValueError(f"slots must be a contiguous int32 vector of {n_seq} on {dev}")
+        raise ValueError(f"slots must be a contiguous int32 vector of {n_seq} on cuda:{dev}")
     if out is None:
-        out = _empty(v_shape, bf16, dev, stream)
+        out = _empty(v_shape, bf16, q.device, stream)
     _on(dev, dep_delta_rule, dep_delta_args_t(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state), state_out.data_ptr(),
         out.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _heads(q, "q", bf16, dev, qk_shape),
         _heads(k, "k", bf16, dev, qk_shape), _heads(v, "v", bf16, dev, v_shape),
         _heads(g, "g", f32, dev, (T, hv, dk) if channel else (T, hv)), _heads(beta, "beta", f32, dev, (T, hv)),
-        _heads(out, "out", bf16, dev, v_shape), T, state_out.shape[0], n_seq, hq, hv, dk, dv,
+        _heads(out, "out", bf16, dev, v_shape), T, n_states, n_seq, hq, hv, dk, dv,
         (DEP_DELTA_CHANNEL if channel else 0) | (DEP_DELTA_L2NORM if l2norm else 0),
         dk ** -0.5 if scale is None else scale), stream)
     return out
@@ -595,23 +600,25 @@ class Int8Projection:
                 weight_scale.shape != (self.N,)) or not weight_scale.is_contiguous():
             raise ValueError(f"weight_scale must be a contiguous float32 vector of {self.N} on {weight.device}")
         self.weight, self.weight_scale = weight, weight_scale
-        self.device = weight.device
-        with torch.cuda.device(weight.device):
+        self.index = weight.get_device()
+        with torch.cuda.device(self.index):
             self.plan = dep_int8_plan(self.N, self.K, max_rows)
 
     def run(self, x, x_scale, out=None, stream=None):
         import torch
-        dev = self.device
-        if x.dtype != torch.int8 or x.device != dev or x.dim() != 2 or x.shape[1] != self.K or not x.is_contiguous():
-            raise ValueError(f"x must be a contiguous int8 tensor [rows, {self.K}] on {dev}")
-        B = x.shape[0]
-        if x_scale.dtype != torch.float32 or x_scale.device != dev or x_scale.numel() != B or (
+        dev, shape = self.index, x.shape
+        if x.dtype is not torch.int8 or x.get_device() != dev or len(shape) != 2 or shape[1] != self.K or (
+                not x.is_contiguous()):
+            raise ValueError(f"x must be a contiguous int8 tensor [rows, {self.K}] on cuda:{dev}")
+        B = shape[0]
+        if x_scale.dtype is not torch.float32 or x_scale.get_device() != dev or x_scale.numel() != B or (
                 not x_scale.is_contiguous()):
-            raise ValueError(f"x_scale must be a contiguous float32 vector of {B} on {dev}")
+            raise ValueError(f"x_scale must be a contiguous float32 vector of {B} on cuda:{dev}")
         if out is None:
-            out = _empty((B, self.N), torch.bfloat16, dev, stream)
-        elif out.dtype != torch.bfloat16 or out.device != dev or out.shape != (B, self.N) or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous bfloat16 tensor [{B}, {self.N}] on {dev}")
+            out = _empty((B, self.N), torch.bfloat16, x.device, stream)
+        elif out.dtype is not torch.bfloat16 or out.get_device() != dev or out.shape != (B, self.N) or (
+                not out.is_contiguous()):
+            raise ValueError(f"out must be a contiguous bfloat16 tensor [{B}, {self.N}] on cuda:{dev}")
         _on(dev, self._run, (x, x_scale, out, B), stream)
         return out
 
