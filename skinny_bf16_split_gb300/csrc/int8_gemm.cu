@@ -272,42 +272,40 @@ __device__ __forceinline__ void widen16(uint4 v, uint4 &lo, uint4 &hi)
     widen4(v.w, hi.z, hi.w);
 }
 
-// x [B, K] int8 -> xh [rows, Kp] FP16, zeros past B and K (Kp a multiple of 256, K of 16, rows of 16),
-// and for each unit of 256 columns (a block) the largest sum of |x| that a row has there.
+// x [B, K] int8 -> xh [16 gridDim.y, Kp] FP16, zeros past B and K (Kp a multiple of 256, K of 16); and for
+// each unit of 256 columns and 16 rows (a block) the largest sum of |x| that a row has there.
 __global__ void __launch_bounds__(256) int8_widen_kernel(const uint8_t *__restrict__ x, uint16_t *__restrict__ xh,
-                                                         uint16_t *__restrict__ bounds, int B, int rows, int K, int Kp)
+                                                         uint16_t *__restrict__ bounds, int B, int K, int Kp)
 {
     griddep_launch_dependents();
-    __shared__ int top;
-    if (threadIdx.x == 0)
-        top = 0;
-    __syncthreads();
-    const int c = blockIdx.x * kKU + (threadIdx.x & 15) * 16;
-    int most = 0;
-#pragma unroll 4
-    for (int row = threadIdx.x >> 4; row < rows; row += 16) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < B && c < K)
-            v = *reinterpret_cast<const uint4 *>(x + (int64_t)row * K + c);
-        uint4 o[2];
-        widen16(v, o[0], o[1]);
-        uint4 *d = reinterpret_cast<uint4 *>(xh + (int64_t)row * Kp + c);
-        d[0] = o[0];
-        d[1] = o[1];
-        unsigned s = __dp4a(__vabs4(v.x), 0x01010101u, 0u);  // |-128| is 128, unsigned
-        s = __dp4a(__vabs4(v.y), 0x01010101u, s);
-        s = __dp4a(__vabs4(v.z), 0x01010101u, s);
-        s = __dp4a(__vabs4(v.w), 0x01010101u, s);
+    __shared__ int top[8];
+    const int c = blockIdx.x * kKU + (threadIdx.x & 15) * 16, row = blockIdx.y * 16 + (threadIdx.x >> 4);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < B && c < K)
+        v = *reinterpret_cast<const uint4 *>(x + (int64_t)row * K + c);
+    uint4 o[2];
+    widen16(v, o[0], o[1]);
+    uint4 *d = reinterpret_cast<uint4 *>(xh + (int64_t)row * Kp + c);
+    d[0] = o[0];
+    d[1] = o[1];
+    unsigned s = __dp4a(__vabs4(v.x), 0x01010101u, 0u);  // |-128| is 128, unsigned
+    s = __dp4a(__vabs4(v.y), 0x01010101u, s);
+    s = __dp4a(__vabs4(v.z), 0x01010101u, s);
+    s = __dp4a(__vabs4(v.w), 0x01010101u, s);
 #pragma unroll
-        for (int m = 8; m; m >>= 1)
-            s += __shfl_xor_sync(~0u, s, m);
-        most = max(most, (int)s);
-    }
-    if ((threadIdx.x & 15) == 0)
-        atomicMax(&top, most);
+    for (int m = 8; m; m >>= 1)
+        s += __shfl_xor_sync(~0u, s, m);
+    s = max(s, __shfl_xor_sync(~0u, s, 16));
+    if ((threadIdx.x & 31) == 0)
+        top[threadIdx.x >> 5] = (int)s;
     __syncthreads();
-    if (threadIdx.x == 0)
-        bounds[blockIdx.x] = (uint16_t)top;  // at most 256 * 128
+    if (threadIdx.x == 0) {
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            most = max(most, top[i]);
+        bounds[blockIdx.y * gridDim.x + blockIdx.x] = (uint16_t)most;  // at most 256 * 128
+    }
 }
 
 constexpr int kRows = 4;           // weight rows of a block's tile
@@ -703,8 +701,12 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         uint32_t bph = 0;
         if (!S::DIRECT && e == 0) {  // bounds of x's units, for the issuers and the other draining warps
             griddep_wait();
-            for (int i = lane; i < KU; i += 32)
-                bounds[i] = p.bounds[i];
+            for (int i = lane; i < KU; i += 32) {
+                int most = 0;
+                for (int r = 0; r * 16 < p.B; ++r)
+                    most = max(most, (int)p.bounds[r * KU + i]);
+                bounds[i] = (uint16_t)most;
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(known);
@@ -918,7 +920,8 @@ cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *
     const Int8Split split = split_for(pl.N, pl.K, nt, pl.sm_count);
     if (nt > 32) {
         const int Kp = (int)split.units * kKU;
-        int8_widen_kernel<<<(unsigned)split.units, 256, 0, stream>>>(x, pl.xh, pl.bounds, B, nt, (int)pl.K, Kp);
+        int8_widen_kernel<<<dim3((unsigned)split.units, (unsigned)(nt / 16)), 256, 0, stream>>>(x, pl.xh, pl.bounds, B,
+                                                                                                (int)pl.K, Kp);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)
             return e;
@@ -1014,7 +1017,7 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
     p->counters = reinterpret_cast<int *>(at + 256);
     p->parts = reinterpret_cast<int *>(at + p->clear_bytes);
     p->xh = reinterpret_cast<uint16_t *>(at + p->clear_bytes + parts);
-    p->bounds = p->xh + (size_t)nt * Kp;  // one for each unit
+    p->bounds = p->xh + (size_t)nt * Kp;  // one for each unit and 16 rows
     *out = p;
     return DEP_OK;
 }
