@@ -438,7 +438,8 @@ dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream);
  * takes query and key head h / (Hv / Hq).  g: FP32 natural logarithm of the
  * decay, one for each head [tokens, Hv] or (DEP_DELTA_CHANNEL) for each key
  * channel [tokens, Hv, Dk]; minus infinity empties the state, and values above
- * zero count as zero (a decay is at most one).  beta: FP32 [tokens, Hv].  With DEP_DELTA_L2NORM q and k are first divided by
+ * zero count as zero (a decay is at most one).  beta: FP32 [tokens, Hv].
+ * With DEP_DELTA_L2NORM q and k are first divided by
  * sqrt(sum of squares + 1e-6) over their Dk channels.
  * Sequences: cu_seqlens, int32 [n_seq + 1] in device memory, first tokens and
  * the end (lengths may be zero; values are clipped to 0..tokens), or null for

@@ -39,7 +39,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     """Compile every translation unit and link the library; return its path.
 
     debug=True builds the bounds-checked variant (-DDEP_DEBUG) into _build_debug/:
-    every kernel checks each index into y, the plan's workspace and shared
+    every BF16 projection kernel checks each index into y, the plan's workspace and shared
     memory before using it, records DEP_DEV_BOUNDS in the status word and skips
     the access if it is out of range."""
     out_dir = DEBUG_DIR if debug else OUT_DIR

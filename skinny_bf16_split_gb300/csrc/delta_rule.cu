@@ -8,10 +8,11 @@
 // Recurrent kernel.  A group of eight lanes holds a row (Dk / 8 channels a lane,
 // in chunks of four so that a group reads 128 consecutive bytes); a warp holds
 // 4 * SETS rows.  The block turns a token's k, q and g into what all its rows need,
-// once, through shared memory, and fetches the next token meanwhile.  The two dot products S k and S q are taken of the decayed state
-// together, so each token costs one reduction: with u = beta (v - S k),
-// o = scale (S q + u (k . q)) and S + u k^T.
-// Bound: DRAM, the state read and written once (8 Dk Dv bytes a head).
+// once, through shared memory, and fetches the next token meanwhile.  The two dot
+// products S k and S q are taken of the decayed state together, so each token costs one
+// reduction: with u = beta (v - S k), o = scale (S q + u (k . q)) and S + u k^T.
+// Bound: DRAM, the state read and written once (8 Dk Dv bytes a head): 64 sequences of 96
+// heads of 128 x 128, 805 MB of states, 121 us (99 % of the copy rate); one sequence 4.1 us.
 //
 // Chunked kernel, for longer sequences: 16 tokens at a time as matrix products.
 // With P_i = a_0 .. a_i, R_j = a_(j+1) .. a_15 and M_ij = a_(j+1) .. a_i (products of
@@ -30,7 +31,11 @@
 // In the products with S and its update the parts are FP16, whose MMAs do twice TF32's work;
 // what fits FP32's range is brought into FP16's by powers of two: one for each row of S and
 // of U, from its largest value, and one for each token's k, q and W, from bounds on theirs.
-// A, B and W are formed from TF32 parts; V is BF16, and T meets it in three BF16 parts.
+// A and B are formed from TF32 parts, T and W in FP32; V is BF16, and T meets it in three BF16
+// parts.
+// Measured: 8192 tokens of 96 heads in 4 ragged sequences 1572 us, 3.8 us for a chunk of one head
+// on an SM.  Bound: the latencies of a chunk's chain; the MMAs fill a third of it (44 % of the
+// issue slots), preparing a chunk alone would take 2.6 us and the state's part alone 2.6.
 #include <cuda_bf16.h>
 
 #include "internal.h"
