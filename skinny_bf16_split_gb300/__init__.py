@@ -8,6 +8,10 @@ kernels with a thin ctypes binding.  Submodules:
   synth     seeded synthetic inputs shared by tests, benchmark and oracle checks
   build     nvcc build of the library
 
+Around the projections: ``add_rms_norm``, ``quantize_rows``, ``Int8Projection`` and
+``gated_delta_rule`` (norm with an 8-bit output, the projection in 8-bit integers and
+the gated delta rule of a delta-attention layer).
+
 The binding loads the library lazily, on first use, and raises if it is
 missing: there is no CPU or library fallback.
 """

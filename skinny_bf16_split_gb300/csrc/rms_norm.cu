@@ -20,7 +20,9 @@
 //     conversion then rounds ties to even.
 // P below 2^-100 is flushed (stored as zero), which keeps 1 / P finite.
 //
-// Bound: DRAM.  Bytes of a row: 2 cols (x) + 4 cols with a residual + the output.
+// Bound: DRAM.  Bytes of a row: 2 cols (x) + 4 cols with a residual + the output.  Measured
+// with a residual, of the copy rate: 8192 x 7168 to BF16 69.5 us (100 %), to int8 66.8 (91 %), to
+// e4m3 66.0 (92 %); 8192 x 7161, every row misaligned, to BF16 95.5 (72 %); one row 2.7 us.
 #include <cuda_bf16.h>
 
 #include "internal.h"
