@@ -18,7 +18,11 @@
 // rows 62 to 66 (80 to 84 %).
 //
 // int8_kernel<NT>: persistent blocks over units of 128 weight rows x 256 columns.
-//   warp 0      TMA: weight stages, 32 KB of int8 each (256 consecutive bytes a row).
+//   warp 0      TMA: weight stages, 32 KB of int8 each (256 consecutive bytes a row), at most two
+//               copies in flight: 10 MB over all blocks cover the memory's latency, and more only
+//               queue up behind each other, the copy that the block waits for among them.  (14560 x
+//               7168 at 16 rows: all of 6 stages in flight 25.9 us, 3 of 4 24.2, 2 of 4 23.9, 2 of 2
+//               25.1; 7168 x 12288 at 64 rows 32.7, 31.0, 30.2, 30.5.)
 //   warps 2, 3  x, in slots of NT x SK columns as FP16.  Up to 32 rows they widen it
 //               from the caller's int8 themselves.  Above, int8_widen_kernel has
 //               written it as FP16 into the workspace (padded with zeros; the two are
@@ -41,8 +45,8 @@
 // the one that comes last adds the parts, rounds and stores.  (Adding them by integer
 // atomics took 18 us at 128 rows: about 200 billion a second.)  No block waits for another.
 // Bound: up to 128 rows the latencies between the roles (1600 cycles a unit where its bytes take
-// 1400), above the MMAs one after another.  Measured: 49376 x 7168 at 16 rows 65.5 us (80 % of the
-// copy rate), at 128 rows 79; 14560 x 7168 at 16 rows 25.8, at 128 rows 34.3, at 256 rows 49 to 51
+// 1400), above the MMAs one after another.  Measured: 49376 x 7168 at 16 rows 63.9 us (82 % of the
+// copy rate), at 128 rows 78.6; 14560 x 7168 at 16 rows 23.9, at 128 rows 33.4, at 256 rows 49 to 50
 // (1060 TFLOP/s, 54 % of the BF16 rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -94,7 +98,9 @@ struct Int8Shape {
     static constexpr int PER = kKU / SK;                 // slots of a unit
     static constexpr int EXACT = 1024 * ISSUERS / kKU;   // units whose sums an FP32 accumulator holds exactly
     static constexpr int X_BYTES = NT * SK * 2;          // an x slot
-    static constexpr int WS = (kMaxDynamicSmem - 1024 - 512 - (DIRECT ? 0 : 1024) - SLOTS * X_BYTES) / kWBytes;
+    static constexpr int FIT = (kMaxDynamicSmem - 1024 - 512 - (DIRECT ? 0 : 1024) - SLOTS * X_BYTES) / kWBytes;
+    static constexpr int WS = FIT < 4 ? FIT : 4;         // weight stages
+    static constexpr int FLIGHT = 2;                     // weight copies in flight
     static constexpr int ACC0 = 256;                     // the accumulators' first column
     static constexpr int BARS = 2 * WS + 2 * SLOTS + 2 * BUFS + 2;
     static constexpr int BOUNDS = DIRECT ? 0 : kMaxUnits * 2;  // bytes: bounds of x's units
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             mbar_init(wfull + 8 * i, 1);
         fence_mbar_init();
         const uint64_t pol = policy_evict_first();
-        while (wst < S::WS && !wcur.done())
+        while (wst < S::FLIGHT && !wcur.done())
             copy_w(pol);
         *abort_flag = 0;
     }
@@ -471,8 +477,17 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
         // ---------------- weight copies ----------------
         if (lane == 0) {
             const uint64_t pol = policy_evict_first();
-            int filled = wst;  // stages that hold or await a copy
-            uint32_t ph = 0;
+            int flying = wst, first = 0;  // copies in flight, and the stage of the first of them
+            uint32_t ph = 0, first_ph = 0;
+            auto arrived = [&] {
+                const bool ok = mbar_wait(wfull + 8 * first, first_ph, p.limit_ns);
+                --flying;
+                if (++first == S::WS) {
+                    first = 0;
+                    first_ph ^= 1u;
+                }
+                return ok;
+            };
             if (wst == S::WS) {
                 wst = 0;
                 ph = 1;
@@ -480,24 +495,20 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
             while (!wcur.done()) {
                 if (*abort_flag)
                     break;
-                if (!mbar_wait(wempty + 8 * wst, ph ^ 1u, p.limit_ns)) {
+                if ((flying == S::FLIGHT && !arrived()) || !mbar_wait(wempty + 8 * wst, ph ^ 1u, p.limit_ns)) {
                     give_up(DEP_DEV_TIMEOUT_PRODUCER);
                     break;
                 }
                 copy_w(pol);
+                ++flying;
                 if (wst == S::WS) {
                     wst = 0;
                     ph ^= 1u;
                 }
             }
-            for (; filled > 0; --filled) {  // copies in flight
-                if (--wst < 0) {
-                    wst = S::WS - 1;
-                    ph ^= 1u;
-                }
-                if (!mbar_wait(wfull + 8 * wst, ph, p.limit_ns))
+            while (flying > 0)
+                if (!arrived())
                     record_status(p.status, DEP_DEV_TIMEOUT_PRODUCER);
-            }
         }
     } else if (S::DIRECT && (warp == 2 || warp == 3)) {
         // ---------------- x, widened here: each warp 128 columns of a unit ----------------
