@@ -451,7 +451,14 @@ dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream);
  * for its outputs.  Two sequences of a call may not share a slot.
  * States stay in FP32; o is rounded once.  Fixed order, no atomics.
  * Dk is 64 or 128, Dv a multiple of 16 up to 256 (else UNSUPPORTED).
- * MISALIGNED unless q, k, v, g (per channel), o and the states are 16-byte
+ * Workspace: device memory that the call overwrites.  With it, sequences of eight
+ * tokens and more on average go by chunks of sixteen tokens, whose shares that do
+ * not depend on the state are worked out there first, as many at once as it holds;
+ * without it, or with less than one chunk of every head takes, all go token by token.
+ * dep_delta_workspace gives the bytes that help: 0 for short sequences, else what
+ * holds all chunks, but at most 2 GiB (or one chunk, where that is more).  It reads
+ * tokens, n_seq, Hv and Dk alone.
+ * MISALIGNED unless q, k, v, g (per channel), o, the states and the workspace are 16-byte
  * aligned, the strides of q, k, v and o multiples of 8 and g's of 4 (per channel),
  * and cu_seqlens, slots, beta and a per-head g 4-byte aligned.
  */
@@ -471,9 +478,12 @@ typedef struct {
     int32_t n_seq, Hq, Hv, Dk, Dv;
     uint32_t flags;
     float scale;
+    void *workspace; /* or null */
+    int64_t workspace_bytes;
 } dep_delta_args_t;
 
 dep_status_t dep_delta_rule(const dep_delta_args_t *args, void *stream);
+dep_status_t dep_delta_workspace(const dep_delta_args_t *args, int64_t *bytes);
 
 /*
  * y[B,N] = BF16(x_scale[b] * w_scale[n] * sum_k x[b,k] * W[n,k]) with x and W

@@ -62,7 +62,7 @@ EXPORTS = (
     "dep_status_string", "dep_projection_version", "dep_projection_run_static",
     "dep_projection_plan_partials", "dep_projection_plan_exchange", "dep_projection_probe_read",
     "dep_projection_plan_selftest_exchange",
-    "dep_add_rms_norm", "dep_quantize_rows", "dep_delta_rule", "dep_int8_plan", "dep_int8_run",
+    "dep_add_rms_norm", "dep_quantize_rows", "dep_delta_rule", "dep_delta_workspace", "dep_int8_plan", "dep_int8_run",
     "dep_int8_plan_workspace", "dep_int8_device_status", "dep_int8_plan_destroy",
 )
 
@@ -91,7 +91,8 @@ class dep_delta_args_t(ctypes.Structure):
                 + [(name, ctypes.c_int64) for name in
                    ("q_stride", "k_stride", "v_stride", "g_stride", "beta_stride", "o_stride", "tokens", "n_states")]
                 + [(name, ctypes.c_int32) for name in ("n_seq", "Hq", "Hv", "Dk", "Dv")]
-                + [("flags", ctypes.c_uint32), ("scale", ctypes.c_float)])
+                + [("flags", ctypes.c_uint32), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                   ("workspace_bytes", ctypes.c_int64)])
 
 
 class DepError(RuntimeError):
@@ -141,6 +142,7 @@ def lib():
         "dep_add_rms_norm": ([P(dep_norm_args_t), vp], i32),
         "dep_quantize_rows": ([P(dep_norm_args_t), vp], i32),
         "dep_delta_rule": ([P(dep_delta_args_t), vp], i32),
+        "dep_delta_workspace": ([P(dep_delta_args_t), P(ctypes.c_int64)], i32),
         "dep_int8_plan": ([i64, i64, i32, P(vp)], i32),
         "dep_int8_run": ([vp, vp, vp, vp, vp, vp, i32, vp], i32),
         "dep_int8_plan_workspace": ([vp, P(ctypes.c_size_t)], i32),
@@ -359,6 +361,12 @@ def dep_int8_run(plan, x, x_scale, W, w_scale, y, B: int | None = None, stream=N
            "dep_int8_run")
 
 
+def dep_delta_workspace(args: dep_delta_args_t) -> int:
+    b = ctypes.c_int64()
+    _check(lib().dep_delta_workspace(ctypes.byref(args), ctypes.byref(b)), "dep_delta_workspace")
+    return b.value
+
+
 def dep_int8_plan_workspace(plan) -> int:
     b = ctypes.c_size_t()
     _check(lib().dep_int8_plan_workspace(plan, ctypes.byref(b)), "dep_int8_plan_workspace")
@@ -539,8 +547,9 @@ def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens
     sequences of equal length.  state, state_out: float32 [n_states, Hv, Dv, Dk];
     state None starts from zeros, state_out defaults to state (updated in place).
     slots: int32 [n_seq] on the device, each sequence's place among the states
-    (outside 0..n_states-1: padding).  scale defaults to Dk ** -0.5.  Returns out,
-    bfloat16 [tokens, Hv, Dv] (allocated where omitted)."""
+    (outside 0..n_states-1: padding).  scale defaults to Dk ** -0.5.  The workspace
+    is the allocator's (up to 2 GiB, for sequences of eight tokens and more on
+    average).  Returns out, bfloat16 [tokens, Hv, Dv] (allocated where omitted)."""
     import torch
     dev, bf16, f32 = q.get_device(), torch.bfloat16, torch.float32
     qk_shape, v_shape = q.shape, v.shape
@@ -573,14 +582,20 @@ def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens
         raise ValueError(f"slots must be a contiguous int32 vector of {n_seq} on cuda:{dev}")
     if out is None:
         out = _empty(v_shape, bf16, q.device, stream)
-    _on(dev, dep_delta_rule, dep_delta_args_t(
+    args = dep_delta_args_t(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state), state_out.data_ptr(),
         out.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _heads(q, "q", bf16, dev, qk_shape),
         _heads(k, "k", bf16, dev, qk_shape), _heads(v, "v", bf16, dev, v_shape),
         _heads(g, "g", f32, dev, (T, hv, dk) if channel else (T, hv)), _heads(beta, "beta", f32, dev, (T, hv)),
         _heads(out, "out", bf16, dev, v_shape), T, n_states, n_seq, hq, hv, dk, dv,
         (DEP_DELTA_CHANNEL if channel else 0) | (DEP_DELTA_L2NORM if l2norm else 0),
-        dk ** -0.5 if scale is None else scale), stream)
+        dk ** -0.5 if scale is None else scale)
+    if T > n_seq:  # more than single tokens
+        args.workspace_bytes = dep_delta_workspace(args)
+        if args.workspace_bytes:
+            workspace = _empty((args.workspace_bytes,), torch.uint8, q.device, stream)
+            args.workspace = workspace.data_ptr()
+    _on(dev, dep_delta_rule, args, stream)
     return out
 
 

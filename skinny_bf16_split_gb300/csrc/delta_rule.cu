@@ -20,12 +20,19 @@
 //     A_ij = beta_i sum_c k_i k_j M_ij  (j < i),    B_ij = sum_c q_i k_j M_ij  (j <= i)
 //     T = (I + A)^-1 diag(beta),   W = T (K.P),     U = T V - W S^T
 //     O = (Q.P) S^T + B U,                          S <- S diag(P_15) + U^T (K.R)
-// A block takes up to 128 rows of one head's state.  Its first warps hold 16 rows of S
-// each, as the accumulator of the last product, for the whole sequence: an accumulator
-// fragment is also a left operand of the next product (with the channels in another
-// order, the same on both sides), so S, U and the rest never leave the registers.  Two
-// more groups of four warps prepare the chunks to come, in turn: norms, decays, A, B, T and
-// W, and Q.P, K.R, each group in a shared-memory stage of its own.
+// Two kernels.  delta_prepare_kernel works out what does not depend on the state (norms, decays, B,
+// T, W, Q.P, K.R) for every chunk at once and leaves it in the workspace, as the operands of the
+// state's MMAs; its four blocks an SM hide each other's latencies.  delta_state_kernel carries the
+// states through the chunks: a warp holds 16 rows of S, as the accumulator of the last product, for
+// the whole sequence: an accumulator fragment is also a left operand of the next product (with the
+// channels in another order, the same on both sides), so S, U and the rest never leave the
+// registers.  Two blocks of four warps an SM, 233 registers a thread: with 128, sixteen warps an SM
+// take longer (a chunk of one warp alone 2.6 us instead of 1.7), for want of loads under way.  Both
+// in one kernel, preparing warps beside the state's, saved the way through memory (28 KB a chunk and
+// head), but left SMs without work where sequences are few or of different lengths, and was never
+// faster: one sequence of 2048 tokens and 32 heads 498 us (now 270), 8192 tokens of 96 heads in 4
+// ragged sequences 1571 (now 1488), two sequences of 512 tokens and 76 heads, one for each SM, 151
+// (now 151).
 // Precision: an FP32 operand is split into two parts of 11 bits, and three of the four products
 // are kept (the last is below 2^-22), so that everything keeps FP32's precision, or nearly.
 // In the products with S and its update the parts are FP16, whose MMAs do twice TF32's work;
@@ -33,10 +40,12 @@
 // of U, from its largest value, and one for each token's k, q and W, from bounds on theirs.
 // A and B are formed from TF32 parts, T and W in FP32; V is BF16, and T meets it in three BF16
 // parts.
-// Measured: 8192 tokens of 96 heads in 4 ragged sequences 1572 us, 3.8 us for a chunk of one head
-// on an SM.  Bound: the latencies of a chunk's chain; the MMAs fill a third of it (44 % of the
-// issue slots); preparing a chunk alone takes 2.4 us, and the state's part alone 2.7.
+// Measured: a chunk of one head takes 1.9 us of an SM to prepare (60 % of the issue slots), and 1.7
+// in the state's kernel with one block on the SM, 2.5 with two.  Bound: the instructions of the one,
+// the latencies of a chunk's chain in the other (the MMAs alone are 0.65 us a block).
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "layer.h"
@@ -56,6 +65,8 @@ struct DeltaParams {
     int32_t n_seq, Hq, Hv, Dv;
     uint32_t flags;
     float scale;
+    uint8_t *chunks;            // workspace
+    int64_t chunk0, n_chunks;  // of this launch
 };
 
 __device__ __forceinline__ float lo_bf(uint32_t v) { return __uint_as_float(v << 16); }
@@ -235,15 +246,11 @@ cudaError_t recurrent_launch(const DeltaParams &p, cudaStream_t s)
 // chunked kernel
 
 constexpr int kC = 16;            // tokens of a chunk
-constexpr int kPrep = 128;        // threads that prepare a chunk; two such groups take turns
+constexpr int kPrep = 128;        // threads that prepare a chunk
+constexpr int kStateWarps = 4;    // of a block, 16 rows of the state each
+constexpr int kRows = 16 * kStateWarps;
+constexpr int kStages = 3;        // chunks in a block's ring
 constexpr int kTT = 20;           // row stride of 16-wide matrices in shared memory
-
-// Barrier `id` of the block's hardware barriers, for n threads.
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void bar_arrive(int id, int n)
-{
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
 
 // v = hi + lo, hi rounded to TF32's 11 bits (half away from zero) by integer arithmetic: the
 // conversion instruction runs at an eighth of its rate.  The MMA ignores what lo has below 11 bits.
@@ -351,60 +358,25 @@ constexpr int kSort = 256;
 // sequences are taken as they are.
 __device__ __forceinline__ int longest_first(const DeltaParams &p, int r, int (&len)[kSort + 1])
 {
-    const int n = p.n_seq, t = threadIdx.x;
+    const int n = p.n_seq;
     if (!p.cu || n < 2 || n > kSort)
         return r;
-    int mine = 0;
-    if (t < n) {
+    for (int t = threadIdx.x; t < n; t += 32 * kStateWarps) {
         int64_t t0, t1;
         seq_range(p, t, t0, t1);
-        len[t] = mine = (int)(t1 - t0);
+        len[t] = (int)(t1 - t0);
     }
     __syncthreads();
-    if (t < n) {
+    for (int t = threadIdx.x; t < n; t += 32 * kStateWarps) {
         int rank = 0;
         for (int j = 0; j < n; ++j)
-            rank += len[j] > mine || (len[j] == mine && j < t);
+            rank += len[j] > len[t] || (len[j] == len[t] && j < t);
         if (rank == r)
             len[kSort] = t;
     }
     __syncthreads();
     return len[kSort];
 }
-
-// What an MMA's lane (g, t) takes of a right operand, 16 bytes: FP16 parts of the k's 2t, 2t + 1
-// (x) and 2t + 8, 2t + 9 (y) of its sixteen, and the parts that those leave (z, w).
-template <int DK, int MW>
-struct ChunkStage {
-    // W and Q.P by token, sixteen channels after another, four lanes t each.  Rows are 64 bytes
-    // off a multiple of 128, so that the eight lanes of a load phase meet no bank twice.
-    uint4 w[kC][DK / 4 + 4], qp[kC][DK / 4 + 4];
-    uint4 kr[DK][4];  // K.R by channel; lane t at t ^ (channel / 2 % 4), for the same reason
-    uint4 B[kC][4];   // B by row
-    uint4 T01[kC][4]; // T by row, in BF16 parts: the first two,
-    uint2 T2[kC][4];  // and the third
-    uint16_t v[kC][16 * MW + 8];  // V as it is
-    float last[DK];               // P_15
-    float iw[kC], ik[kC], iq[kC]; // what undoes the scales of W, k and q
-};
-template <int DK, int MW>
-struct ChunkShared {
-    static constexpr int KS = DK + 8;  // float2 reads without conflicts
-    ChunkStage<DK, MW> stage[2];
-    struct {  // scratch of each group of preparing warps
-        struct {  // operands of the products of one level (see below): rows k_i then q_i, columns k_j
-            float row[16][KS], col[8][KS];
-        } level[4];
-        struct {  // a chunk's tokens as they are; rows off by 16 bytes for ldmatrix
-            float g[kC][DK];
-            uint16_t k[kC][DK + 8], q[kC][DK + 8];
-        } raw;
-        alignas(16) float A[kC][kC];
-        alignas(16) float T[kC][kTT], Tk[kC][kTT];  // columns of T, and of T over k's scales
-        alignas(16) float part[4][48], norm[4][48], inv[4][32], sw[4][kC], beta[kC], g[kC];
-    } prep[2];
-    int order[kSort + 1];
-};
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
 {
@@ -413,562 +385,672 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
                  : "memory");
 }
 
-template <int DK, int MW>
-__global__ void __launch_bounds__(2 * kPrep + 32 * MW) delta_chunk_kernel(const DeltaParams p)
+// What an MMA's lane (g, t) takes of a right operand, 16 bytes: FP16 parts of the k's 2t, 2t + 1
+// (x) and 2t + 8, 2t + 9 (y) of its sixteen, and the parts that those leave (z, w).  Rows and lanes
+// are laid out such that the eight lanes of a load phase meet no bank twice.
+template <int DK>
+struct Chunk {  // of one head: what its state needs of sixteen tokens
+    uint4 qp[kC][DK / 4];  // Q.P by token, sixteen channels after another, four lanes t each, at ^ 4 in odd rows
+    uint4 B[kC][4];        // B by row
+    uint4 T01[kC][4];      // T by row, in BF16 parts: the first two,
+    uint2 T2[kC][4];       // and the third
+    float last[DK];        // P_15
+    float iw[kC], ik[kC], iq[kC], unused[kC];  // what undoes the scales of W, k and q
+    uint4 kr[DK][4];       // K.R by channel; lane t at t ^ (channel / 2 % 4)
+    uint4 w[kC][DK / 4];   // W, as Q.P
+};
+
+// Chunks are numbered through all sequences, from t0 / 16 + s on for sequence s: no two share a
+// number, and there are tokens / 16 + n_seq at most.
+__device__ __forceinline__ int64_t first_chunk(const DeltaParams &p, int s)
 {
-    extern __shared__ uint8_t smem_raw[];
-    ChunkShared<DK, MW> &sm = *reinterpret_cast<ChunkShared<DK, MW> *>(smem_raw);
-    constexpr int kThreads = kPrep + 32 * MW;  // that meet over a stage: its group, and the state's warps
-    constexpr int kBarFull = 2, kBarEmpty = 4;
-    const int slices = (p.Dv + 16 * MW - 1) / (16 * MW);
+    int64_t t0, t1;
+    seq_range(p, s, t0, t1);
+    return t0 / kC + s;
+}
+
+template <int DK>
+struct PrepShared {
+    static constexpr int KS = DK + 8;  // float2 reads without conflicts
+    struct Level {                     // operands of the products of one level: rows k_i then q_i, columns k_j
+        float row[16][KS], col[8][KS];
+    };
+    struct Raw {  // the tokens as they are; rows off by 16 bytes for ldmatrix
+        float g[kC][DK];
+        uint16_t k[kC][DK + 8], q[kC][DK + 8];
+    };
+    // One after another in this memory: the tokens and the levels, where the chunk's K.R and W come to lie.
+    static constexpr int HEAD = offsetof(Chunk<DK>, kr);
+    static constexpr int BODY = 2 * (int)sizeof(Level);
+    static_assert(sizeof(Raw) <= BODY && sizeof(Chunk<DK>) <= HEAD + BODY && HEAD % 16 == 0, "");
+    alignas(128) uint8_t mem[HEAD + BODY];
+    alignas(16) float A[kC][kC];
+    alignas(16) float T[kC][kTT], Tk[kC][kTT];  // columns of T, and of T over k's scales
+    alignas(16) float other[4][32][4];          // halves of the levels' products
+    alignas(16) float part[4][48], norm[4][48], inv[4][32], sw[4][kC], beta[kC], g[kC];
+};
+
+// One block for each chunk and head.
+// A and B come from matrix products, level by level.  At level b (1, 2, 4, 8) token i, whose
+// bit b is set, is a row and meets the columns j that share its bits above b and have
+// that bit clear: M_ij is the product of the decays from the row's group of b tokens
+// on up to i, times that of the decays after j up to the group's end.  Every pair j < i
+// meets at one level, the highest bit in which the two differ.
+// A thread works on one channel; of 64 channels two threads each, one with what tokens need
+// (Q.P, W), the other with what pairs need (the levels, K.R).
+template <int DK>
+__global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    auto &pr = *reinterpret_cast<PrepShared<DK> *>(smem_raw);
+    auto &sg = *reinterpret_cast<Chunk<DK> *>(pr.mem);
+    auto &raw = *reinterpret_cast<typename PrepShared<DK>::Raw *>(pr.mem + PrepShared<DK>::HEAD);
+    auto *level = reinterpret_cast<typename PrepShared<DK>::Level *>(pr.mem + PrepShared<DK>::HEAD);
+    const int h = blockIdx.x % p.Hv, pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
+    const int64_t local = blockIdx.x / p.Hv, number = p.chunk0 + local;
+    int s = 0;
+    for (int n = p.n_seq; n > 1;) {  // the last sequence that starts at or before this chunk
+        const int step = (n + 31) / 32;
+        const bool before = lane * step < n && first_chunk(p, s + lane * step) <= number;
+        const int at = max(31 - __clz(__ballot_sync(~0u, before)), 0) * step;
+        s += at;
+        n = min(step, n - at);
+    }
+    int64_t t0, t1;
+    seq_range(p, s, t0, t1);
+    const int64_t len = t1 - t0, first = (number - t0 / kC - s) * kC;  // of its tokens
+    if (first < 0 || first >= len)
+        return;
+    const int left = (int)(len - first < kC ? len - first : kC);
+    const bool chan = (p.flags & DEP_DELTA_CHANNEL) != 0, l2 = (p.flags & DEP_DELTA_L2NORM) != 0;
+    const int ch = pt % DK;
+    const bool tokens = pt < DK, pairs = pt >= kPrep - DK;
+    const int hq = h / (p.Hv / p.Hq);
+    const uint16_t *k0 = p.k + t0 * p.ks + (int64_t)hq * DK, *q0 = p.q + t0 * p.qs + (int64_t)hq * DK;
+    const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK : h);
+    {
+        constexpr int QC = DK / 8, GC = DK / 4;  // 16-byte pieces of a token
+#pragma unroll
+        for (int i = pt; i < kC * QC; i += kPrep) {
+            const int tok = i / QC, e = i % QC * 8;
+            const int64_t at = first + (tok < left ? tok : 0);
+            cp_async16(&raw.k[tok][e], k0 + at * p.ks + e, tok < left);
+            cp_async16(&raw.q[tok][e], q0 + at * p.qs + e, tok < left);
+        }
+        if (chan)
+#pragma unroll
+            for (int i = pt; i < kC * GC; i += kPrep) {
+                const int tok = i / GC, e = i % GC * 4;
+                cp_async16(&raw.g[tok][e], gp + (first + (tok < left ? tok : 0)) * p.gs + e, tok < left);
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (pt < kC) {
+            pr.beta[pt] = pt < left ? p.beta[(t0 + first + pt) * p.bs + h] : 0.f;
+            pr.g[pt] = !chan && pt < left ? gp[(first + pt) * p.gs] : 0.f;
+        }
+    }
+    for (int i = pt; i < kC * 4; i += kPrep)  // above the diagonal B stays zero
+        (&sg.B[0][0])[i] = make_uint4(0, 0, 0, 0);
+    for (int i = pt; i < kC * kC; i += kPrep)
+        (&pr.A[0][0])[i] = 0.f;
+    auto put_b = [&](int i, int j, float v) {  // B_ij into its lane's sixteen bytes
+        uint32_t hi, lo;
+        f16_split2(v * (1.f / kUnB), 0.f, hi, lo);
+        uint16_t *d = reinterpret_cast<uint16_t *>(&sg.B[i][(j & 7) >> 1]) + (j >> 3) * 2 + (j & 1);
+        d[0] = (uint16_t)hi;
+        d[4] = (uint16_t)lo;
+    };
+    // this channel's place in a row of W or Q.P, in FP16 numbers: its lane's sixteen bytes
+    const int c16 = ch & 15, at = ((ch >> 4) * 4 + ((c16 & 7) >> 1)) * 8 + (c16 >> 3) * 2 + (c16 & 1);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float k[kC], q[kC], a[kC], kp[kC];  // kp: K.P
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        k[i] = __uint_as_float((uint32_t)raw.k[i][ch] << 16);
+        q[i] = __uint_as_float((uint32_t)raw.q[i][ch] << 16);
+        a[i] = decay(chan ? raw.g[i][ch] : pr.g[i]);
+    }
+    {
+        // Each token's sums of k k, q q and k q over the channels: the diagonals of products of the BF16
+        // rows with themselves, warp pw a quarter of the channels.  A left operand's registers hold the
+        // right operands of its two halves, too.
+        constexpr int KW = DK / 64;  // steps of 16 channels
+        float kk[2][4] = {}, qq[2][4] = {}, kq[2][4] = {};
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+            const int col = (pw * KW + i) * 16 + 8 * (lane >> 4), row = lane & 15;
+            uint32_t x[4], y[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"((uint32_t)__cvta_generic_to_shared(&raw.k[row][col]))
+                         : "memory");
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                         : "r"((uint32_t)__cvta_generic_to_shared(&raw.q[row][col]))
+                         : "memory");
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                mma_bf16(kk[n], x, x[n], x[2 + n]);
+                mma_bf16(qq[n], y, y[n], y[2 + n]);
+                mma_bf16(kq[n], x, y[n], y[2 + n]);
+            }
+        }
+        const int g = lane >> 2;
+        if ((lane & 3) == g >> 1) {  // this lane holds the diagonal at g and g + 8
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                pr.part[pw][8 * n + g] = g & 1 ? kk[n][2 * n + 1] : kk[n][2 * n];
+                pr.part[pw][16 + 8 * n + g] = g & 1 ? qq[n][2 * n + 1] : qq[n][2 * n];
+                pr.part[pw][32 + 8 * n + g] = g & 1 ? kq[n][2 * n + 1] : kq[n][2 * n];
+            }
+        }
+        __syncthreads();
+        // every warp finishes the sums for itself
+        const float sum = (pr.part[0][lane] + pr.part[1][lane]) + (pr.part[2][lane] + pr.part[3][lane]);
+        const float f = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
+        // 2^e > the norm of the normalised row >= its largest value; rows are taken times 2^(8 - e) from here on
+        const int e = (((int)(__float_as_uint(sum * f * f) >> 23) - 127 + 2) >> 1);
+        pr.norm[pw][lane] = f * __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+        pr.inv[pw][lane] = __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+        if (lane < 16)
+            pr.norm[pw][32 + lane] = (pr.part[0][32 + lane] + pr.part[1][32 + lane]) +
+                                     (pr.part[2][32 + lane] + pr.part[3][32 + lane]);
+        __syncwarp();
+    }
+    if (pt < kC)
+        put_b(pt, pt, pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt]);
+    if (pt < 32)
+        (pt < 16 ? sg.ik : sg.iq)[pt & 15] = pr.inv[pw][pt];
+#pragma unroll
+    for (int i = 0; i < kC; i += 4) {
+        const float4 nk = *reinterpret_cast<const float4 *>(&pr.norm[pw][i]);
+        const float4 nq = *reinterpret_cast<const float4 *>(&pr.norm[pw][16 + i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            k[i + e] *= (&nk.x)[e];
+            q[i + e] *= (&nq.x)[e];
+        }
+    }
+    if (tokens) {
+        float P = 1.f;
+#pragma unroll
+        for (int i = 0; i < kC; i += 2) {
+            const float P0 = P * a[i], P1 = P0 * a[i + 1];
+            P = P1;
+            kp[i] = k[i] * P0;
+            kp[i + 1] = k[i + 1] * P1;
+            uint32_t hi, lo;
+            f16_split2(q[i] * P0, q[i + 1] * P1, hi, lo);
+            uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.qp[i][0]) + at;
+            uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.qp[i + 1][0]) + (at ^ 32);
+            d0[0] = (uint16_t)hi;
+            d0[4] = (uint16_t)lo;
+            d1[0] = (uint16_t)(hi >> 16);
+            d1[4] = (uint16_t)(lo >> 16);
+        }
+        sg.last[ch] = P;
+    }
+    float mine[4];  // of this warp's level
+#pragma unroll
+    for (int l0 = 0; l0 < 4; l0 += 2) {  // two levels at a time, half of the channels for each warp
+        if (pairs)
+#pragma unroll
+            for (int l = l0; l < l0 + 2; ++l) {
+                const int b = 1 << l;
+                float f = 1.f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int i = (r & ~(b - 1)) << 1 | b | (r & (b - 1));
+                    f = i % b == 0 ? a[i] : f * a[i];
+                    level[l & 1].row[r][ch] = k[i] * f;
+                    level[l & 1].row[8 + r][ch] = q[i] * f;
+                }
+#pragma unroll
+                for (int n = 7; n >= 0; --n) {
+                    const int j = (n & ~(b - 1)) << 1 | (n & (b - 1));
+                    f = j % b == b - 1 ? 1.f : f * a[j + 1];
+                    level[l & 1].col[n][ch] = k[j] * f;
+                }
+            }
+        __syncthreads();
+        const int g = lane >> 2, t = lane & 3;
+        const auto &lv = level[pw & 1];
+        float d[3][4] = {};  // one for each of the three products
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i) {
+            const int at = 8 * (pw / 2 * (DK / 16) + i) + 2 * t;
+            const float2 lo = ld2(&lv.row[g][at]), hi = ld2(&lv.row[g + 8][at]), cb = ld2(&lv.col[g][at]);
+            const float c4[4] = {lo.x, lo.y, hi.x, hi.y};
+            uint32_t ah[4], al[4];
+            split_a(c4, ah, al);
+            uint32_t h0, l0, h1, l1;
+            tf32_split(cb.x, h0, l0);
+            tf32_split(cb.y, h1, l1);
+            mma_tf32(d[2], al, h0, h1);
+            mma_tf32(d[1], ah, l0, l1);
+            mma_tf32(d[0], ah, h0, h1);
+        }
+        // one of the two warps of a level finishes it: of the first two levels 2 and 3, of the others 0 and 1
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            d[0][e] += d[2][e] + d[1][e];
+        if ((l0 == 0) == (pw >= 2))
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                mine[e] = d[0][e];
+        else
+            *reinterpret_cast<float4 *>(pr.other[pw ^ 2][lane]) = make_float4(d[0][0], d[0][1], d[0][2], d[0][3]);
+        __syncthreads();
+    }
+    {
+        const int g = lane >> 2, t = lane & 3, b = 1 << (pw ^ 2);
+        const float4 other = *reinterpret_cast<const float4 *>(pr.other[pw][lane]);
+        const int i = (g & ~(b - 1)) << 1 | b | (g & (b - 1));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
+            if ((n & ~(b - 1)) == (g & ~(b - 1))) {
+                pr.A[i][j] = (mine[e] + (&other.x)[e]) * (pr.inv[pw][i] * pr.inv[pw][j]);
+                put_b(i, j, mine[2 + e] + (&other.x)[2 + e]);
+            }
+        }
+    }
+    __syncthreads();
+    if (pairs) {
+        float R = 1.f;
+#pragma unroll
+        for (int i = kC - 1; i >= 0; --i) {
+            k[i] *= R;
+            R *= a[i];
+        }
+    }
+    if (pairs)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            uint4 v;
+            f16_split2(k[2 * t], k[2 * t + 1], v.x, v.z);
+            f16_split2(k[2 * t + 8], k[2 * t + 9], v.y, v.w);
+            sg.kr[ch][t ^ (ch >> 1 & 3)] = v;
+        }
+    if (pw == 0) {  // T: lane j solves (I + A) x = e_j, then times beta_j
+        const int j = lane & 15;
+        float x[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+            for (int m = 0; m < i; m += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(&pr.A[i][m]);
+#pragma unroll
+                for (int e = 0; e < 4 && m + e < i; ++e)
+                    (e & 1 ? d1 : d0) = fmaf((&r.x)[e], x[m + e], e & 1 ? d1 : d0);
+            }
+            x[i] = (i == j ? 1.f : 0.f) - pr.beta[i] * (d0 + d1);
+        }
+        const float b = pr.beta[j], bk = b * pr.inv[pw][j];
+        if (lane < 16)
+#pragma unroll
+            for (int i = 0; i < kC; i += 4) {  // x is zero above its own row
+                *reinterpret_cast<float4 *>(&pr.T[j][i]) = make_float4(x[i] * b, x[i + 1] * b, x[i + 2] * b, x[i + 3] * b);
+                *reinterpret_cast<float4 *>(&pr.Tk[j][i]) =
+                    make_float4(x[i] * bk, x[i + 1] * bk, x[i + 2] * bk, x[i + 3] * bk);
+            }
+    }
+    __syncthreads();
+    if (pt < 4 * kC) {  // T for the state's warps
+        const int i = pt >> 2, t = pt & 3;
+        uint4 p01;
+        uint2 p2;
+        bf16_split3(pr.T[2 * t][i], pr.T[2 * t + 1][i], p01.x, p01.z, p2.x);
+        bf16_split3(pr.T[2 * t + 8][i], pr.T[2 * t + 9][i], p01.y, p01.w, p2.y);
+        sg.T01[i][t] = p01;
+        sg.T2[i][t] = p2;
+    }
+    {
+        // |W_i| <= sum_j |T_ij| times the bound on k_j's values, 2^8 over its scale
+        float top = 0.f, inv;
+        if (lane < kC)
+#pragma unroll
+            for (int j = 0; j < kC; ++j)
+                top += fabsf(pr.Tk[j][lane]);
+        const float s = scale_for(256.f * top, inv);
+        if (lane < kC)
+            pr.sw[pw][lane] = s;
+        if (pw == 0 && lane < kC)
+            sg.iw[lane] = inv;
+        float w[kC] = {};
+#pragma unroll
+        for (int j = 0; j < kC; ++j)
+#pragma unroll
+            for (int i = j & ~3; i < kC; i += 4) {
+                const float4 c4 = *reinterpret_cast<const float4 *>(&pr.Tk[j][i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[i + e] = fmaf((&c4.x)[e], kp[j], w[i + e]);
+            }
+        __syncwarp();
+        if (tokens)
+#pragma unroll
+            for (int i = 0; i < kC; i += 2) {
+                const float2 s2 = ld2(&pr.sw[pw][i]);
+                uint32_t hi, lo;
+                f16_split2(w[i] * s2.x, w[i + 1] * s2.y, hi, lo);
+                uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
+                uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.w[i + 1][0]) + (at ^ 32);
+                d0[0] = (uint16_t)hi;
+                d0[4] = (uint16_t)lo;
+                d1[0] = (uint16_t)(hi >> 16);
+                d1[4] = (uint16_t)(lo >> 16);
+            }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (pt == 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                         p.chunks + (local * p.Hv + h) * (int64_t)sizeof(Chunk<DK>)),
+                     "r"((uint32_t)__cvta_generic_to_shared(pr.mem)), "r"((int)sizeof(Chunk<DK>))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+}
+
+template <int DK>
+struct StateShared {
+    Chunk<DK> stage[kStages];
+    uint16_t v[kStateWarps][kC][24];  // each warp's part of V, then of O; rows off a multiple of 128 bytes
+    int order[kSort + 1];
+};
+
+// One block for each sequence, head and kRows rows of its state.
+template <int DK>
+__global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const DeltaParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    auto &sm = *reinterpret_cast<StateShared<DK> *>(smem_raw);
+    const int slices = (p.Dv + kRows - 1) / kRows;
     const int slice = blockIdx.x % slices, sh = blockIdx.x / slices;
     const int h = sh % p.Hv, s = longest_first(p, sh / p.Hv, sm.order);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t t0, t1;
     seq_range(p, s, t0, t1);
     const int64_t slot = p.slots ? p.slots[s] : s;
-    const bool pad = slot < 0 || slot >= p.n_states;
-    const int64_t len = t1 - t0, chunks = pad ? 0 : (len + kC - 1) / kC;
-    const int64_t sbase = (slot * p.Hv + h) * (int64_t)p.Dv * DK;
-    const bool chan = (p.flags & DEP_DELTA_CHANNEL) != 0, l2 = (p.flags & DEP_DELTA_L2NORM) != 0;
-
-    if (pad) {  // zeros out, no state
-        const int rows = p.Dv - slice * 16 * MW < 16 * MW ? p.Dv - slice * 16 * MW : 16 * MW;
-        for (int64_t i = threadIdx.x; i < len * rows; i += blockDim.x)
-            p.o[(t0 + i / rows) * p.os + (int64_t)h * p.Dv + slice * 16 * MW + i % rows] = 0;
+    const int64_t len = t1 - t0, all = (len + kC - 1) / kC, base = t0 / kC + s - p.chunk0;
+    if (slot < 0 || slot >= p.n_states) {  // padding: zeros out, no state
+        const int rows = p.Dv - slice * kRows < kRows ? p.Dv - slice * kRows : kRows;
+        if (p.chunk0 == 0)
+            for (int64_t i = threadIdx.x; i < len * rows; i += blockDim.x)
+                p.o[(t0 + i / rows) * p.os + (int64_t)h * p.Dv + slice * kRows + i % rows] = 0;
         return;
     }
-
-    if (warp < MW) {
-        // ---------------- state rows row0 .. row0 + 15 ----------------
-        const int row0 = (slice * MW + warp) * 16, g = lane >> 2, t = lane & 3;
-        const bool live = row0 < p.Dv;  // Dv is a multiple of 16
-        constexpr int NT = DK / 8;
-        float S[NT][4];
+    // chunks from .. to of the sequence are among those of this launch
+    const int64_t from = base < 0 ? -base : 0, to = all < p.n_chunks - base ? all : p.n_chunks - base;
+    if (from >= to && !(all == 0 && base >= 0 && base < p.n_chunks))
+        return;
+    const int64_t chunks = to - from;
+    const float *s_in = from > 0 ? p.s_out : p.s_in;
+    const int64_t sbase = (slot * p.Hv + h) * (int64_t)p.Dv * DK;
+    const uint8_t *src = p.chunks + ((base + from) * p.Hv + h) * (int64_t)sizeof(Chunk<DK>);
+    auto fetch = [&](int64_t c) {
+        if (c < chunks) {
+            const uint8_t *at = src + c * p.Hv * (int64_t)sizeof(Chunk<DK>);
+            uint8_t *to = reinterpret_cast<uint8_t *>(&sm.stage[c % kStages]);
+#pragma unroll
+            for (int i = threadIdx.x * 16; i < (int)sizeof(Chunk<DK>); i += 32 * kStateWarps * 16)
+                cp_async16(to + i, at + i, true);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto &mine = sm.v[warp];
+    auto fetch_v = [&](int64_t c) {
+        const int64_t tok = (from + c) * kC + (lane >> 1);
+        const int row = (slice * kStateWarps + warp) * 16 + 8 * (lane & 1);
+        return c < chunks && tok < len && row < p.Dv
+                   ? *reinterpret_cast<const uint4 *>(p.v + (t0 + tok) * p.vs + (int64_t)h * p.Dv + row)
+                   : make_uint4(0, 0, 0, 0);
+    };
+    for (int c = 0; c < kStages - 1; ++c)
+        fetch(c);
+    uint4 v = fetch_v(0);
+    const int row0 = (slice * kStateWarps + warp) * 16, g = lane >> 2, t = lane & 3;
+    const bool live = row0 < p.Dv;  // Dv is a multiple of 16
+    constexpr int NT = DK / 8;
+    float S[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float2 a = make_float2(0.f, 0.f), b = a;
+        if (live && s_in) {
+            a = *reinterpret_cast<const float2 *>(s_in + sbase + (int64_t)(row0 + g) * DK + 8 * n + 2 * t);
+            b = *reinterpret_cast<const float2 *>(s_in + sbase + (int64_t)(row0 + g + 8) * DK + 8 * n + 2 * t);
+        }
+        S[n][0] = a.x;
+        S[n][1] = a.y;
+        S[n][2] = b.x;
+        S[n][3] = b.y;
+    }
+    // S is held times a power of two for each row: r0 for row g, r1 for row g + 8, such that the row's largest
+    // value lies in [2^8, 2^15), or the scale at its limit.
+    float r0 = 1.f, r1 = 1.f, i0 = 1.f, i1 = 1.f;  // the scales, and what undoes them
+    auto rescale = [&](float f0, float f1) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            S[n][0] *= f0, S[n][1] *= f0, S[n][2] *= f1, S[n][3] *= f1;
+        r0 *= f0, r1 *= f1;
+        i0 = 1.f / r0, i1 = 1.f / r1;
+    };
+    auto factor = [](float top, float r) {  // what brings a row back into its range
+        float inv;
+        return top >= 32768.f || (top < 256.f && top > 0.f && r < kMostScale)
+                   ? fminf(scale_for(top, inv), kMostScale / r)
+                   : 1.f;
+    };
+    auto keep_range = [&](float m0, float m1) {  // the lane's largest values of both rows
+        const float f0 = factor(row_max(m0), r0), f1 = factor(row_max(m1), r1);
+        if (__any_sync(~0u, f0 != 1.f || f1 != 1.f))
+            rescale(f0, f1);
+    };
+    {
+        float m0 = 0.f, m1 = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float2 a = make_float2(0.f, 0.f), b = a;
-            if (live && p.s_in) {
-                a = *reinterpret_cast<const float2 *>(p.s_in + sbase + (int64_t)(row0 + g) * DK + 8 * n + 2 * t);
-                b = *reinterpret_cast<const float2 *>(p.s_in + sbase + (int64_t)(row0 + g + 8) * DK + 8 * n + 2 * t);
-            }
-            S[n][0] = a.x;
-            S[n][1] = a.y;
-            S[n][2] = b.x;
-            S[n][3] = b.y;
+            m0 = max3_abs(m0, S[n][0], S[n][1]);
+            m1 = max3_abs(m1, S[n][2], S[n][3]);
         }
-        // S is held times a power of two for each row: r0 for row g, r1 for row g + 8, such that the row's largest
-        // value lies in [2^8, 2^15), or the scale at its limit.
-        float r0 = 1.f, r1 = 1.f, i0 = 1.f, i1 = 1.f;  // the scales, and what undoes them
-        auto rescale = [&](float f0, float f1) {
+        keep_range(m0, m1);
+    }
+    for (int64_t c = 0; c < chunks; ++c) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();
+        fetch(c + kStages - 1);
+        const Chunk<DK> &sg = sm.stage[c % kStages];
+        *reinterpret_cast<uint4 *>(&mine[lane >> 1][8 * (lane & 1)]) = v;
+        v = fetch_v(c + 1);
+        __syncwarp();
+        float X[2][4] = {}, O[2][4] = {};
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                S[n][0] *= f0, S[n][1] *= f0, S[n][2] *= f1, S[n][3] *= f1;
-            r0 *= f0, r1 *= f1;
-            i0 = 1.f / r0, i1 = 1.f / r1;
-        };
-        auto factor = [](float top, float r) {  // what brings a row back into its range
-            float inv;
-            return top >= 32768.f || (top < 256.f && top > 0.f && r < kMostScale)
-                       ? fminf(scale_for(top, inv), kMostScale / r)
-                       : 1.f;
-        };
-        auto keep_range = [&](float m0, float m1) {  // the lane's largest values of both rows
-            const float f0 = factor(row_max(m0), r0), f1 = factor(row_max(m1), r1);
-            if (__any_sync(~0u, f0 != 1.f || f1 != 1.f))
-                rescale(f0, f1);
-        };
+        for (int ks = 0; ks < NT / 2; ++ks) {
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f16_split2(S[2 * ks + i][0], S[2 * ks + i][1], ah[2 * i], al[2 * i]);
+                f16_split2(S[2 * ks + i][2], S[2 * ks + i][3], ah[2 * i + 1], al[2 * i + 1]);
+            }
+            float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
+            const int at = (4 * ks + t) ^ (g & 1) << 2;
+            const uint4 b[4] = {sg.w[g][at], sg.qp[g][at], sg.w[8 + g][at], sg.qp[8 + g][at]};
+            mma_f16x3(d, ah, al, b);
+        }
+        float U[2][4] = {};
+        {  // U^T = V^T T^T - S^T W^T, the part with V
+            uint32_t a[4];
+            const uint32_t at = (uint32_t)__cvta_generic_to_shared(
+                &mine[(lane >> 4) * 8 + (lane & 7)][8 * (lane >> 3 & 1)]);
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                         : "r"(at)
+                         : "memory");
+            const uint4 b0 = sg.T01[g][t], b1 = sg.T01[8 + g][t];
+            const uint2 c0 = sg.T2[g][t], c1 = sg.T2[8 + g][t];
+            mma_bf16(U[0], a, c0.x, c0.y);
+            mma_bf16(U[1], a, c1.x, c1.y);
+            mma_bf16(U[0], a, b0.z, b0.w);
+            mma_bf16(U[1], a, b1.z, b1.w);
+            mma_bf16(U[0], a, b0.x, b0.y);
+            mma_bf16(U[1], a, b1.x, b1.y);
+        }
+        // U' = U / (k's scale), in parts scaled by row: the left operand of B and of K.R
+        uint32_t uh[4], ul[4];
+        float j0, j1;
         {
-            float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                m0 = max3_abs(m0, S[n][0], S[n][1]);
-                m1 = max3_abs(m1, S[n][2], S[n][3]);
+            for (int n = 0; n < 2; ++n) {
+                const float2 iw = ld2(&sg.iw[8 * n + 2 * t]), ik = ld2(&sg.ik[8 * n + 2 * t]);
+                U[n][0] = fmaf(X[n][0] * i0, -iw.x, U[n][0]) * ik.x;
+                U[n][1] = fmaf(X[n][1] * i0, -iw.y, U[n][1]) * ik.y;
+                U[n][2] = fmaf(X[n][2] * i1, -iw.x, U[n][2]) * ik.x;
+                U[n][3] = fmaf(X[n][3] * i1, -iw.y, U[n][3]) * ik.y;
+            }
+            const float s0 = scale_for(
+                row_max(fmaxf(fmaxf(fabsf(U[0][0]), fabsf(U[0][1])), fmaxf(fabsf(U[1][0]), fabsf(U[1][1])))), j0);
+            const float s1 = scale_for(
+                row_max(fmaxf(fmaxf(fabsf(U[0][2]), fabsf(U[0][3])), fmaxf(fabsf(U[1][2]), fabsf(U[1][3])))), j1);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                f16_split2(U[n][0] * s0, U[n][1] * s0, uh[2 * n], ul[2 * n]);
+                f16_split2(U[n][2] * s1, U[n][3] * s1, uh[2 * n + 1], ul[2 * n + 1]);
+            }
+        }
+        float Y[2][4] = {};  // U^T B^T
+        {
+            float(*const d[2])[4] = {&Y[0], &Y[1]};
+            const uint4 b[2] = {sg.B[g][t], sg.B[8 + g][t]};
+            mma_f16x3(d, uh, ul, b);
+        }
+        // O = Q.P S^T + U' B', each with its scales
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
+            O[n][0] = fmaf(Y[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
+            O[n][1] = fmaf(Y[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
+            O[n][2] = fmaf(Y[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
+            O[n][3] = fmaf(Y[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
+        }
+        // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
+        uint32_t r[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n]) : "f"(O[n][1]), "f"(O[n][0]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n + 1]) : "f"(O[n][3]), "f"(O[n][2]));
+        }
+        const uint32_t at = (uint32_t)__cvta_generic_to_shared(
+            &mine[(lane >> 4) * 8 + (lane & 7)][8 * (lane >> 3 & 1)]);  // over V
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3])
+                     : "memory");
+        __syncwarp();
+        const int64_t tok = (from + c) * kC + (lane >> 1);
+        if (live && tok < len)
+            *reinterpret_cast<uint4 *>(p.o + (t0 + tok) * p.os + (int64_t)h * p.Dv + row0 + 8 * (lane & 1)) =
+                *reinterpret_cast<const uint4 *>(&mine[lane >> 1][8 * (lane & 1)]);
+        {  // S <- S diag(P_15) + U^T (K.R)
+            if (__any_sync(~0u, j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
+                // U beyond what S's scales leave room for: make room
+                rescale(j0 > 0x1p60f * i0 ? 0x1p60f * i0 / j0 : 1.f, j1 > 0x1p60f * i1 ? 0x1p60f * i1 / j1 : 1.f);
+            }
+            const float f0 = j0 * r0, f1 = j1 * r1;
+            float m0 = 0.f, m1 = 0.f;
+            // two tiles of eight channels at a time, the products of the next two before the sums of these
+            const int sw = t ^ (g >> 1 & 3);
+            float D[2][2][4];
+            auto products = [&](int n, float (&d2)[2][4]) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        d2[i][e] = 0.f;
+                float(*const d[2])[4] = {&d2[0], &d2[1]};
+                const uint4 b[2] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw]};
+                mma_f16x3(d, uh, ul, b);
+            };
+            products(0, D[0]);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                if (n + 2 < NT)
+                    products(n + 2, D[(n / 2 + 1) & 1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
+                    float(&s)[4] = S[n + i];
+                    const float(&d)[4] = D[(n / 2) & 1][i];
+                    s[0] = fmaf(d[0], f0, s[0] * a.x);
+                    s[1] = fmaf(d[1], f0, s[1] * a.y);
+                    s[2] = fmaf(d[2], f1, s[2] * a.x);
+                    s[3] = fmaf(d[3], f1, s[3] * a.y);
+                    m0 = max3_abs(m0, s[0], s[1]);
+                    m1 = max3_abs(m1, s[2], s[3]);
+                }
             }
             keep_range(m0, m1);
         }
-        for (int64_t c = 0; c < chunks; ++c) {
-            const int st = (int)(c & 1);
-            bar_sync(kBarFull + st, kThreads);
-            const ChunkStage<DK, MW> &sg = sm.stage[st];
-            float X[2][4] = {}, O[2][4] = {};
-#pragma unroll
-            for (int ks = 0; ks < NT / 2; ++ks) {
-                uint32_t ah[4], al[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    f16_split2(S[2 * ks + i][0], S[2 * ks + i][1], ah[2 * i], al[2 * i]);
-                    f16_split2(S[2 * ks + i][2], S[2 * ks + i][3], ah[2 * i + 1], al[2 * i + 1]);
-                }
-                float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
-                const uint4 b[4] = {sg.w[g][4 * ks + t], sg.qp[g][4 * ks + t], sg.w[8 + g][4 * ks + t],
-                                    sg.qp[8 + g][4 * ks + t]};
-                mma_f16x3(d, ah, al, b);
-            }
-            float U[2][4] = {};
-            {  // U^T = V^T T^T - S^T W^T, the part with V
-                uint32_t a[4];
-                const uint32_t at = (uint32_t)__cvta_generic_to_shared(
-                    &sg.v[(lane >> 4) * 8 + (lane & 7)][16 * warp + 8 * (lane >> 3 & 1)]);
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
-                             : "r"(at)
-                             : "memory");
-                const uint4 b0 = sg.T01[g][t], b1 = sg.T01[8 + g][t];
-                const uint2 c0 = sg.T2[g][t], c1 = sg.T2[8 + g][t];
-                mma_bf16(U[0], a, c0.x, c0.y);
-                mma_bf16(U[1], a, c1.x, c1.y);
-                mma_bf16(U[0], a, b0.z, b0.w);
-                mma_bf16(U[1], a, b1.z, b1.w);
-                mma_bf16(U[0], a, b0.x, b0.y);
-                mma_bf16(U[1], a, b1.x, b1.y);
-            }
-            // U' = U / (k's scale), in parts scaled by row: the left operand of B and of K.R
-            uint32_t uh[4], ul[4];
-            float j0, j1;
-            {
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 iw = ld2(&sg.iw[8 * n + 2 * t]), ik = ld2(&sg.ik[8 * n + 2 * t]);
-                    U[n][0] = fmaf(X[n][0] * i0, -iw.x, U[n][0]) * ik.x;
-                    U[n][1] = fmaf(X[n][1] * i0, -iw.y, U[n][1]) * ik.y;
-                    U[n][2] = fmaf(X[n][2] * i1, -iw.x, U[n][2]) * ik.x;
-                    U[n][3] = fmaf(X[n][3] * i1, -iw.y, U[n][3]) * ik.y;
-                }
-                const float s0 = scale_for(
-                    row_max(fmaxf(fmaxf(fabsf(U[0][0]), fabsf(U[0][1])), fmaxf(fabsf(U[1][0]), fabsf(U[1][1])))), j0);
-                const float s1 = scale_for(
-                    row_max(fmaxf(fmaxf(fabsf(U[0][2]), fabsf(U[0][3])), fmaxf(fabsf(U[1][2]), fabsf(U[1][3])))), j1);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    f16_split2(U[n][0] * s0, U[n][1] * s0, uh[2 * n], ul[2 * n]);
-                    f16_split2(U[n][2] * s1, U[n][3] * s1, uh[2 * n + 1], ul[2 * n + 1]);
-                }
-            }
-            float Y[2][4] = {};  // U^T B^T
-            {
-                float(*const d[2])[4] = {&Y[0], &Y[1]};
-                const uint4 b[2] = {sg.B[g][t], sg.B[8 + g][t]};
-                mma_f16x3(d, uh, ul, b);
-            }
-            // O = Q.P S^T + U' B', each with its scales
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
-                O[n][0] = fmaf(Y[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
-                O[n][1] = fmaf(Y[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
-                O[n][2] = fmaf(Y[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
-                O[n][3] = fmaf(Y[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
-            }
-            // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
-            uint32_t r[4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n]) : "f"(O[n][1]), "f"(O[n][0]));
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n + 1]) : "f"(O[n][3]), "f"(O[n][2]));
-            }
-            const uint32_t at = (uint32_t)__cvta_generic_to_shared(
-                &sg.v[(lane >> 4) * 8 + (lane & 7)][16 * warp + 8 * (lane >> 3 & 1)]);  // over the warp's part of V
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]),
-                         "r"(r[1]), "r"(r[2]), "r"(r[3])
-                         : "memory");
-            __syncwarp();
-            const int64_t tok = c * kC + (lane >> 1);
-            if (live && tok < len)
-                *reinterpret_cast<uint4 *>(p.o + (t0 + tok) * p.os + (int64_t)h * p.Dv + row0 + 8 * (lane & 1)) =
-                    *reinterpret_cast<const uint4 *>(&sg.v[lane >> 1][16 * warp + 8 * (lane & 1)]);
-            {  // S <- S diag(P_15) + U^T (K.R)
-                if (__any_sync(~0u, j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
-                    // U beyond what S's scales leave room for: make room
-                    rescale(j0 > 0x1p60f * i0 ? 0x1p60f * i0 / j0 : 1.f, j1 > 0x1p60f * i1 ? 0x1p60f * i1 / j1 : 1.f);
-                }
-                const float f0 = j0 * r0, f1 = j1 * r1;
-                float m0 = 0.f, m1 = 0.f;
-                // two tiles of eight channels at a time, the products of the next two before the sums of these
-                const int sw = t ^ (g >> 1 & 3);
-                float D[2][2][4];
-                auto products = [&](int n, float (&d2)[2][4]) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            d2[i][e] = 0.f;
-                    float(*const d[2])[4] = {&d2[0], &d2[1]};
-                    const uint4 b[2] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw]};
-                    mma_f16x3(d, uh, ul, b);
-                };
-                products(0, D[0]);
-#pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    if (n + 2 < NT)
-                        products(n + 2, D[(n / 2 + 1) & 1]);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
-                        float(&s)[4] = S[n + i];
-                        const float(&d)[4] = D[(n / 2) & 1][i];
-                        s[0] = fmaf(d[0], f0, s[0] * a.x);
-                        s[1] = fmaf(d[1], f0, s[1] * a.y);
-                        s[2] = fmaf(d[2], f1, s[2] * a.x);
-                        s[3] = fmaf(d[3], f1, s[3] * a.y);
-                        m0 = max3_abs(m0, s[0], s[1]);
-                        m1 = max3_abs(m1, s[2], s[3]);
-                    }
-                }
-                keep_range(m0, m1);
-            }
-            if (c + 2 < chunks)
-                bar_arrive(kBarEmpty + st, kThreads);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (live) {
-                *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g) * DK + 8 * n + 2 * t) =
-                    make_float2(S[n][0] * i0, S[n][1] * i0);
-                *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g + 8) * DK + 8 * n + 2 * t) =
-                    make_float2(S[n][2] * i1, S[n][3] * i1);
-            }
-    } else {
-        // ---------------- the next chunk's operands ----------------
-        // A and B from matrix products, level by level.  At level b (1, 2, 4, 8) token i, whose
-        // bit b is set, is a row and meets the columns j that share its bits above b and have
-        // that bit clear: M_ij is the product of the decays from the row's group of b tokens
-        // on up to i, times that of the decays after j up to the group's end.  Every pair j < i
-        // meets at one level, the highest bit in which the two differ.
-        const int grp = (threadIdx.x - 32 * MW) / kPrep, pt = (threadIdx.x - 32 * MW) % kPrep, pw = pt >> 5;
-        const int kBarPrep = 6 + grp;
-        auto &pr = sm.prep[grp];
-        // A thread works on one channel; of 64 channels two threads each, one with what tokens need
-        // (Q.P, W), the other with what pairs need (the levels, K.R).
-        const int ch = pt % DK;
-        const bool tokens = pt < DK, pairs = pt >= kPrep - DK;
-        const int hq = h / (p.Hv / p.Hq);
-        const uint16_t *kp = p.k + t0 * p.ks + (int64_t)hq * DK, *qp = p.q + t0 * p.qs + (int64_t)hq * DK;
-        const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK : h);
-        float bv = 0.f, gv = 0.f;  // of token pt
-        auto fetch = [&](int64_t c) {
-            auto &raw = pr.raw;
-            const int64_t first = c * kC;
-            const int left = (int)(len - first < kC ? len - first : kC);
-            constexpr int QC = DK / 8, GC = DK / 4;  // 16-byte pieces of a token
-#pragma unroll
-            for (int i = pt; i < kC * QC; i += kPrep) {
-                const int tok = i / QC, e = i % QC * 8;
-                const int64_t at = first + (tok < left ? tok : 0);
-                cp_async16(&raw.k[tok][e], kp + at * p.ks + e, tok < left);
-                cp_async16(&raw.q[tok][e], qp + at * p.qs + e, tok < left);
-            }
-            if (chan)
-#pragma unroll
-                for (int i = pt; i < kC * GC; i += kPrep) {
-                    const int tok = i / GC, e = i % GC * 4;
-                    cp_async16(&raw.g[tok][e], gp + (first + (tok < left ? tok : 0)) * p.gs + e, tok < left);
-                }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (pt < kC) {
-                bv = pt < left ? p.beta[(t0 + first + pt) * p.bs + h] : 0.f;
-                gv = !chan && pt < left ? gp[(first + pt) * p.gs] : 0.f;
-            }
-        };
-        ChunkStage<DK, MW> &sg = sm.stage[grp];
-        for (int i = pt; i < kC * 4; i += kPrep)  // above the diagonal B stays zero
-            (&sg.B[0][0])[i] = make_uint4(0, 0, 0, 0);
-        for (int i = pt; i < kC * kC; i += kPrep)
-            (&pr.A[0][0])[i] = 0.f;
-        auto put_b = [&](int i, int j, float v) {  // B_ij into its lane's sixteen bytes
-            uint32_t hi, lo;
-            f16_split2(v * (1.f / kUnB), 0.f, hi, lo);
-            uint16_t *d = reinterpret_cast<uint16_t *>(&sg.B[i][(j & 7) >> 1]) + (j >> 3) * 2 + (j & 1);
-            d[0] = (uint16_t)hi;
-            d[4] = (uint16_t)lo;
-        };
-        // this channel's place in a row of W or Q.P, in FP16 numbers: its lane's sixteen bytes
-        const int c16 = ch & 15, at = ((ch >> 4) * 4 + ((c16 & 7) >> 1)) * 8 + (c16 >> 3) * 2 + (c16 & 1);
-        const int rows0 = slice * 16 * MW, rows = p.Dv - rows0 < 16 * MW ? p.Dv - rows0 : 16 * MW;
-        const uint16_t *vp = p.v + t0 * p.vs + (int64_t)h * p.Dv + rows0;
-        if (grp < chunks)
-            fetch(grp);
-        for (int64_t c = grp; c < chunks; c += 2) {
-            const auto &raw = pr.raw;
-            if (pt < kC) {
-                pr.beta[pt] = bv;
-                pr.g[pt] = gv;
-            }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            bar_sync(kBarPrep, kPrep);
-            float k[kC], q[kC], a[kC], kp[kC];  // kp: K.P
-#pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                k[i] = __uint_as_float((uint32_t)raw.k[i][ch] << 16);
-                q[i] = __uint_as_float((uint32_t)raw.q[i][ch] << 16);
-                a[i] = decay(chan ? raw.g[i][ch] : pr.g[i]);
-            }
-            {
-                // Each token's sums of k k, q q and k q over the channels: the diagonals of products of the BF16
-                // rows with themselves, warp pw a quarter of the channels.  A left operand's registers hold the
-                // right operands of its two halves, too.
-                constexpr int KW = DK / 64;  // steps of 16 channels
-                float kk[2][4] = {}, qq[2][4] = {}, kq[2][4] = {};
-#pragma unroll
-                for (int i = 0; i < KW; ++i) {
-                    const int col = (pw * KW + i) * 16 + 8 * (lane >> 4), row = lane & 15;
-                    uint32_t x[4], y[4];
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                 : "r"((uint32_t)__cvta_generic_to_shared(&raw.k[row][col]))
-                                 : "memory");
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                                 : "r"((uint32_t)__cvta_generic_to_shared(&raw.q[row][col]))
-                                 : "memory");
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma_bf16(kk[n], x, x[n], x[2 + n]);
-                        mma_bf16(qq[n], y, y[n], y[2 + n]);
-                        mma_bf16(kq[n], x, y[n], y[2 + n]);
-                    }
-                }
-                const int g = lane >> 2;
-                if ((lane & 3) == g >> 1) {  // this lane holds the diagonal at g and g + 8
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        pr.part[pw][8 * n + g] = g & 1 ? kk[n][2 * n + 1] : kk[n][2 * n];
-                        pr.part[pw][16 + 8 * n + g] = g & 1 ? qq[n][2 * n + 1] : qq[n][2 * n];
-                        pr.part[pw][32 + 8 * n + g] = g & 1 ? kq[n][2 * n + 1] : kq[n][2 * n];
-                    }
-                }
-                bar_sync(kBarPrep, kPrep);
-                if (c + 2 < chunks)
-                    fetch(c + 2);
-                // every warp finishes the sums for itself
-                const float sum = (pr.part[0][lane] + pr.part[1][lane]) + (pr.part[2][lane] + pr.part[3][lane]);
-                const float f = (lane < 16 ? 1.f : p.scale) * (l2 ? 1.f / sqrtf(sum + 1e-6f) : 1.f);
-                // 2^e > the norm of the normalised row >= its largest value; rows are taken times 2^(8 - e) from here on
-                const int e = (((int)(__float_as_uint(sum * f * f) >> 23) - 127 + 2) >> 1);
-                pr.norm[pw][lane] = f * __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-                pr.inv[pw][lane] = __uint_as_float((uint32_t)(127 - 8 + e) << 23);
-                if (lane < 16)
-                    pr.norm[pw][32 + lane] = (pr.part[0][32 + lane] + pr.part[1][32 + lane]) +
-                                             (pr.part[2][32 + lane] + pr.part[3][32 + lane]);
-                __syncwarp();
-            }
-            if (c >= 2)
-                bar_sync(kBarEmpty + grp, kThreads);
-            {  // V, straight into the stage
-                const int64_t first = c * kC;
-                const int left = (int)(len - first < kC ? len - first : kC);
-#pragma unroll
-                for (int i = pt; i < kC * 2 * MW; i += kPrep) {
-                    const int tok = i / (2 * MW), e = i % (2 * MW) * 8;
-                    const bool in = tok < left && e < rows;
-                    cp_async16(&sg.v[tok][e], vp + (first + (in ? tok : 0)) * p.vs + (in ? e : 0), in);
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            }
-            if (pt < kC)
-                put_b(pt, pt, pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt]);
-            if (pt < 32)
-                (pt < 16 ? sg.ik : sg.iq)[pt & 15] = pr.inv[pw][pt];
-#pragma unroll
-            for (int i = 0; i < kC; i += 4) {
-                const float4 nk = *reinterpret_cast<const float4 *>(&pr.norm[pw][i]);
-                const float4 nq = *reinterpret_cast<const float4 *>(&pr.norm[pw][16 + i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    k[i + e] *= (&nk.x)[e];
-                    q[i + e] *= (&nq.x)[e];
-                }
-            }
-            if (tokens) {
-                float P = 1.f;
-#pragma unroll
-                for (int i = 0; i < kC; i += 2) {
-                    const float P0 = P * a[i], P1 = P0 * a[i + 1];
-                    P = P1;
-                    kp[i] = k[i] * P0;
-                    kp[i + 1] = k[i + 1] * P1;
-                    uint32_t hi, lo;
-                    f16_split2(q[i] * P0, q[i + 1] * P1, hi, lo);
-                    uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.qp[i][0]) + at;
-                    uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.qp[i + 1][0]) + at;
-                    d0[0] = (uint16_t)hi;
-                    d0[4] = (uint16_t)lo;
-                    d1[0] = (uint16_t)(hi >> 16);
-                    d1[4] = (uint16_t)(lo >> 16);
-                }
-                sg.last[ch] = P;
-            }
-            if (pairs) {
-#pragma unroll
-                for (int l = 0; l < 4; ++l) {
-                    const int b = 1 << l;
-                    float f = 1.f;
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const int i = (r & ~(b - 1)) << 1 | b | (r & (b - 1));
-                        f = i % b == 0 ? a[i] : f * a[i];
-                        pr.level[l].row[r][ch] = k[i] * f;
-                        pr.level[l].row[8 + r][ch] = q[i] * f;
-                    }
-#pragma unroll
-                    for (int n = 7; n >= 0; --n) {
-                        const int j = (n & ~(b - 1)) << 1 | (n & (b - 1));
-                        f = j % b == b - 1 ? 1.f : f * a[j + 1];
-                        pr.level[l].col[n][ch] = k[j] * f;
-                    }
-                }
-                float R = 1.f;
-#pragma unroll
-                for (int i = kC - 1; i >= 0; --i) {
-                    k[i] *= R;
-                    R *= a[i];
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    uint4 v;
-                    f16_split2(k[2 * t], k[2 * t + 1], v.x, v.z);
-                    f16_split2(k[2 * t + 8], k[2 * t + 9], v.y, v.w);
-                    sg.kr[ch][t ^ (ch >> 1 & 3)] = v;
-                }
-            }
-            bar_sync(kBarPrep, kPrep);
-            {  // warp pw: level pw
-                const int g = lane >> 2, t = lane & 3, b = 1 << pw;
-                const auto &lv = pr.level[pw];
-                float d[3][4] = {};  // one for each of the three products
-#pragma unroll
-                for (int ks = 0; ks < DK / 8; ++ks) {
-                    const float2 lo = *reinterpret_cast<const float2 *>(&lv.row[g][8 * ks + 2 * t]);
-                    const float2 hi = *reinterpret_cast<const float2 *>(&lv.row[g + 8][8 * ks + 2 * t]);
-                    const float2 cb = *reinterpret_cast<const float2 *>(&lv.col[g][8 * ks + 2 * t]);
-                    const float c4[4] = {lo.x, lo.y, hi.x, hi.y};
-                    uint32_t ah[4], al[4];
-                    split_a(c4, ah, al);
-                    uint32_t h0, l0, h1, l1;
-                    tf32_split(cb.x, h0, l0);
-                    tf32_split(cb.y, h1, l1);
-                    mma_tf32(d[2], al, h0, h1);
-                    mma_tf32(d[1], ah, l0, l1);
-                    mma_tf32(d[0], ah, h0, h1);
-                }
-                const int i = (g & ~(b - 1)) << 1 | b | (g & (b - 1));
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
-                    if ((n & ~(b - 1)) == (g & ~(b - 1))) {
-                        pr.A[i][j] = ((d[2][e] + d[1][e]) + d[0][e]) * (pr.inv[pw][i] * pr.inv[pw][j]);
-                        put_b(i, j, (d[2][2 + e] + d[1][2 + e]) + d[0][2 + e]);
-                    }
-                }
-            }
-            bar_sync(kBarPrep, kPrep);
-            if (pw == 0) {  // T: lane j solves (I + A) x = e_j, then times beta_j
-                const int j = lane & 15;
-                float x[kC];
-#pragma unroll
-                for (int i = 0; i < kC; ++i) {
-                    float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-                    for (int m = 0; m < i; m += 4) {
-                        const float4 r = *reinterpret_cast<const float4 *>(&pr.A[i][m]);
-#pragma unroll
-                        for (int e = 0; e < 4 && m + e < i; ++e)
-                            (e & 1 ? d1 : d0) = fmaf((&r.x)[e], x[m + e], e & 1 ? d1 : d0);
-                    }
-                    x[i] = (i == j ? 1.f : 0.f) - pr.beta[i] * (d0 + d1);
-                }
-                const float b = pr.beta[j], bk = b * pr.inv[pw][j];
-                if (lane < 16)
-#pragma unroll
-                    for (int i = 0; i < kC; i += 4) {  // x is zero above its own row
-                        *reinterpret_cast<float4 *>(&pr.T[j][i]) = make_float4(x[i] * b, x[i + 1] * b, x[i + 2] * b, x[i + 3] * b);
-                        *reinterpret_cast<float4 *>(&pr.Tk[j][i]) =
-                            make_float4(x[i] * bk, x[i + 1] * bk, x[i + 2] * bk, x[i + 3] * bk);
-                    }
-            }
-            bar_sync(kBarPrep, kPrep);
-            if (pt < 4 * kC) {  // T for the state's warps
-                const int i = pt >> 2, t = pt & 3;
-                uint4 p01;
-                uint2 p2;
-                bf16_split3(pr.T[2 * t][i], pr.T[2 * t + 1][i], p01.x, p01.z, p2.x);
-                bf16_split3(pr.T[2 * t + 8][i], pr.T[2 * t + 9][i], p01.y, p01.w, p2.y);
-                sg.T01[i][t] = p01;
-                sg.T2[i][t] = p2;
-            }
-            {
-                // |W_i| <= sum_j |T_ij| times the bound on k_j's values, 2^8 over its scale
-                float top = 0.f, inv;
-                if (lane < kC)
-#pragma unroll
-                    for (int j = 0; j < kC; ++j)
-                        top += fabsf(pr.Tk[j][lane]);
-                const float s = scale_for(256.f * top, inv);
-                if (lane < kC)
-                    pr.sw[pw][lane] = s;
-                if (pw == 0 && lane < kC)
-                    sg.iw[lane] = inv;
-                float w[kC] = {};
-#pragma unroll
-                for (int j = 0; j < kC; ++j)
-#pragma unroll
-                    for (int i = j & ~3; i < kC; i += 4) {
-                        const float4 c4 = *reinterpret_cast<const float4 *>(&pr.Tk[j][i]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[i + e] = fmaf((&c4.x)[e], kp[j], w[i + e]);
-                    }
-                __syncwarp();
-                if (tokens)
-#pragma unroll
-                    for (int i = 0; i < kC; i += 2) {
-                        const float2 s2 = ld2(&pr.sw[pw][i]);
-                        uint32_t hi, lo;
-                        f16_split2(w[i] * s2.x, w[i + 1] * s2.y, hi, lo);
-                        uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
-                        uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.w[i + 1][0]) + at;
-                        d0[0] = (uint16_t)hi;
-                        d0[4] = (uint16_t)lo;
-                        d1[0] = (uint16_t)(hi >> 16);
-                        d1[4] = (uint16_t)(lo >> 16);
-                    }
-            }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");  // V
-            bar_arrive(kBarFull + grp, kThreads);
-        }
+        __syncwarp();
     }
-}
-
-template <int DK, int MW>
-cudaError_t chunk_launch(const DeltaParams &p, cudaStream_t s)
-{
-    static_assert(sizeof(ChunkShared<DK, MW>) <= kMaxDynamicSmem, "");
-    static std::atomic<uint64_t> devices{0};
-    cudaError_t e = set_smem_attr(delta_chunk_kernel<DK, MW>, devices);
-    if (e != cudaSuccess)
-        return e;
-    const int64_t blocks = (int64_t)((p.Dv + 16 * MW - 1) / (16 * MW)) * p.Hv * p.n_seq;
-    if (blocks > INT32_MAX)
-        return cudaErrorInvalidConfiguration;
-    delta_chunk_kernel<DK, MW><<<(unsigned)blocks, 2 * kPrep + 32 * MW, sizeof(ChunkShared<DK, MW>), s>>>(p);
-    return cudaGetLastError();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        if (live) {
+            *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g) * DK + 8 * n + 2 * t) =
+                make_float2(S[n][0] * i0, S[n][1] * i0);
+            *reinterpret_cast<float2 *>(p.s_out + sbase + (int64_t)(row0 + g + 8) * DK + 8 * n + 2 * t) =
+                make_float2(S[n][2] * i1, S[n][3] * i1);
+        }
 }
 
 template <int DK>
-cudaError_t delta_launch(const DeltaParams &p, cudaStream_t s)
+cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
 {
-    // A chunk costs the chunked kernel the same whether it holds one token or sixteen; the recurrent kernel
-    // pays by the token.  96 heads of 128 channels, measured: 64 sequences of 7 tokens 388 us (44 us a token),
-    // of up to 16 in one chunk 504 us; 4 sequences of 7 tokens 28 us (2.6 us a token), of up to 16 40 us.
-    if (p.tokens >= 12ll * p.n_seq)
-        return chunk_launch<DK, 8>(p, s);
+    static std::atomic<uint64_t> devices[2] = {{0}, {0}};
+    cudaError_t e = set_smem_attr(delta_prepare_kernel<DK>, devices[0]);
+    if (e == cudaSuccess)
+        e = set_smem_attr(delta_state_kernel<DK>, devices[1]);
+    const int64_t all = p.tokens / kC + p.n_seq, most = bytes / (p.Hv * (int64_t)sizeof(Chunk<DK>));
+    const int64_t states = (int64_t)((p.Dv + kRows - 1) / kRows) * p.Hv * p.n_seq;
+    for (p.chunk0 = 0; e == cudaSuccess && p.chunk0 < all; p.chunk0 += p.n_chunks) {
+        p.n_chunks = all - p.chunk0 < most ? all - p.chunk0 : most;
+        if (p.n_chunks * p.Hv > INT32_MAX || states > INT32_MAX)
+            return cudaErrorInvalidConfiguration;
+        delta_prepare_kernel<DK><<<(unsigned)(p.n_chunks * p.Hv), kPrep, sizeof(PrepShared<DK>), s>>>(p);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) {
+            delta_state_kernel<DK><<<(unsigned)states, 32 * kStateWarps, sizeof(StateShared<DK>), s>>>(p);
+            e = cudaGetLastError();
+        }
+    }
+    return e;
+}
+
+// What dep_delta_workspace asks for at most.  A pass over part of the chunks has fewer sequences at work at once:
+// 8192 tokens of 96 heads in 4 ragged sequences took 1488 us in one pass (1.4 GB), with 1 GiB 1587, 256 MiB 1856.
+constexpr int64_t kMostWorkspace = 2ll << 30;
+
+// Chunks for sequences of eight tokens and more on average: a chunk costs the same whether it holds one token or
+// sixteen, while the recurrent kernel pays by the token.  Measured with 128 channels, 6, 8 and 12 tokens a sequence:
+// 64 sequences of 96 heads 343, 421 and 586 us token by token, 349, 352 and 358 by chunks; 4 of them 25, 30, 41 and
+// 31, 31, 31; one of 32 heads 7, 8, 11 and 12, 12, 12.
+bool in_chunks(int64_t tokens, int64_t n_seq) { return n_seq > 0 && tokens >= 8 * n_seq; }
+
+template <int DK>
+cudaError_t delta_launch(const DeltaParams &p, int64_t bytes, cudaStream_t s)
+{
+    if (in_chunks(p.tokens, p.n_seq) && bytes >= p.Hv * (int64_t)sizeof(Chunk<DK>))
+        return chunk_launch<DK>(p, bytes, s);
     return (int64_t)p.n_seq * p.Hv * p.Dv < 32768 ? recurrent_launch<DK, 2>(p, s) : recurrent_launch<DK, 4>(p, s);
 }
 
 dep_status_t delta_entry(const dep_delta_args_t *a, void *stream)
 {
     if (!a || a->tokens < 0 || a->n_seq < 0 || a->n_states < 0 || a->Hq < 1 || a->Hv < 1 || a->Hv % a->Hq != 0 ||
-        (a->flags & ~(DEP_DELTA_CHANNEL | DEP_DELTA_L2NORM)) != 0)
+        (a->flags & ~(DEP_DELTA_CHANNEL | DEP_DELTA_L2NORM)) != 0 || a->workspace_bytes < 0 ||
+        (a->workspace_bytes > 0 && !a->workspace))
         return DEP_ERR_INVALID_ARG;
     if ((a->Dk != 64 && a->Dk != 128) || a->Dv < 16 || a->Dv > 256 || a->Dv % 16 != 0)
         return DEP_ERR_UNSUPPORTED;
@@ -990,13 +1072,18 @@ dep_status_t delta_entry(const dep_delta_args_t *a, void *stream)
     const Rows q{a->q, 2 * qk, 2 * a->q_stride, T}, k{a->k, 2 * qk, 2 * a->k_stride, T},
         v{a->v, 2 * hv, 2 * a->v_stride, T}, o{a->o, 2 * hv, 2 * a->o_stride, T},
         g{a->g, 4 * gc, 4 * a->g_stride, T}, b{a->beta, 4 * (int64_t)a->Hv, 4 * a->beta_stride, T},
-        si{a->state_in, sb, sb, a->state_in ? a->n_states : 0}, so{a->state_out, sb, sb, a->n_states};
+        si{a->state_in, sb, sb, a->state_in ? a->n_states : 0}, so{a->state_out, sb, sb, a->n_states},
+        w{a->workspace, a->workspace_bytes, a->workspace_bytes, 1};
     if (!q.aligned(16) || !k.aligned(16) || !v.aligned(16) || !o.aligned(16) || !g.aligned(chan ? 16 : 4) ||
-        !b.aligned(4) || !si.aligned(16) || !so.aligned(16) || !aligned(a->cu_seqlens, 4) || !aligned(a->slots, 4))
+        !b.aligned(4) || !si.aligned(16) || !so.aligned(16) || !aligned(a->cu_seqlens, 4) || !aligned(a->slots, 4) || !aligned(a->workspace, 16))
         return DEP_ERR_MISALIGNED;
     for (const Rows *in : {&q, &k, &v, &g, &b})
         if (overlap(o, *in) || overlap(so, *in))
             return DEP_ERR_INVALID_ARG;
+    if (a->workspace_bytes > 0)
+        for (const Rows *t : {&q, &k, &v, &g, &b, &o, &si, &so})
+            if (overlap(w, *t))
+                return DEP_ERR_INVALID_ARG;
     if (overlap(o, so) || overlap(o, si) || (overlap(so, si) && a->state_in != a->state_out))
         return DEP_ERR_INVALID_ARG;
     DeltaParams p;
@@ -1024,8 +1111,10 @@ dep_status_t delta_entry(const dep_delta_args_t *a, void *stream)
     p.Dv = a->Dv;
     p.flags = a->flags;
     p.scale = a->scale;
+    p.chunks = static_cast<uint8_t *>(a->workspace);
+    p.chunk0 = p.n_chunks = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = a->Dk == 128 ? delta_launch<128>(p, s) : delta_launch<64>(p, s);
+    const cudaError_t e = a->Dk == 128 ? delta_launch<128>(p, a->workspace_bytes, s) : delta_launch<64>(p, a->workspace_bytes, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return e == cudaErrorInvalidConfiguration ? DEP_ERR_UNSUPPORTED : DEP_ERR_CUDA;
@@ -1035,6 +1124,17 @@ dep_status_t delta_entry(const dep_delta_args_t *a, void *stream)
 
 }  // namespace
 }  // namespace dep
+
+extern "C" dep_status_t dep_delta_workspace(const dep_delta_args_t *a, int64_t *bytes)
+{
+    if (!a || !bytes || a->tokens < 0 || a->n_seq < 0 || a->Hv < 1)
+        return DEP_ERR_INVALID_ARG;
+    *bytes = 0;
+    const int64_t chunk = a->Hv * (int64_t)(a->Dk == 128 ? sizeof(dep::Chunk<128>) : sizeof(dep::Chunk<64>));
+    if (dep::in_chunks(a->tokens, a->n_seq))
+        *bytes = std::max(chunk, std::min((a->tokens / dep::kC + a->n_seq) * chunk, dep::kMostWorkspace));
+    return DEP_OK;
+}
 
 extern "C" dep_status_t dep_delta_rule(const dep_delta_args_t *args, void *stream)
 {

@@ -235,6 +235,38 @@ def test_same_bits_again_in_a_graph_and_on_another_stream(dep, tokens):
     assert torch.equal(out, want[0]) and torch.equal(So, want[1])
 
 
+@pytest.mark.parametrize("channel,dk", [(True, 128), (False, 64)])
+def test_workspaces_of_any_size(dep, monkeypatch, channel, dk):
+    """The same bits from one pass over all chunks and from many, down to one chunk a pass; token by
+    token without a workspace."""
+    lengths, hv = (40, 0, 17, 1, 90, 33), 4
+    T, n = sum(lengths), len(lengths)
+    a = make(T, 2, hv, dk, 128, channel, seed=11)
+    S = torch.randn(n + 1, hv, 128, dk, device="cuda", generator=torch.Generator(device="cuda").manual_seed(12))
+    cu = torch.tensor([0] + list(lengths)).cumsum(0).int().cuda()
+    slots = torch.tensor([3, 0, 6, 9, 1, 2], dtype=torch.int32, device="cuda")  # sequence 3 is padding
+    size = dep.dep_delta_workspace(dep.dep_delta_args_t(tokens=T, n_seq=n, Hv=hv, Dk=dk))
+    chunk = size // (T // 16 + n)
+    assert size == chunk * (T // 16 + n) > 0
+
+    def run(size, in_place):
+        monkeypatch.setattr(dep._binding, "dep_delta_workspace", lambda args: size)
+        start, end = S.clone(), torch.full_like(S, 7.0)
+        end = start if in_place else end
+        out = dep.gated_delta_rule(*a, start, end, cu_seqlens=cu, slots=slots, l2norm=True)
+        return out, end
+
+    for in_place in (False, True):
+        out, end = run(size, in_place)
+        for part in (size - 16, 7 * chunk, 3 * chunk + 16, 2 * chunk, chunk):
+            o, e = run(part, in_place)
+            assert torch.equal(o, out) and torch.equal(e, end), part
+    o, e = run(0, True)
+    want = definition(*a, S, lengths, dk ** -0.5, True, slots.tolist())
+    for got in ((out, end), (o, e)):
+        close(*got, *want, max(lengths), dk)
+
+
 def test_python_refusals(dep):
     a = make(4, 2, 2, 64, 64, False)
     S = torch.zeros(1, 2, 64, 64, device="cuda")

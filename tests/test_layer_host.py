@@ -90,6 +90,31 @@ def test_delta_refusals(dep, change, status):
     assert e.value.status == getattr(dep, "DEP_ERR_" + status)
 
 
+@pytest.mark.parametrize("change,status", [
+    (dict(workspace_bytes=-1), "INVALID_ARG"), (dict(workspace_bytes=64), "INVALID_ARG"),
+    (dict(workspace=80 * A + 8, workspace_bytes=64), "MISALIGNED"),
+    (dict(workspace=A, workspace_bytes=64), "INVALID_ARG"),              # over q
+    (dict(workspace=6 * A - 64, workspace_bytes=128), "INVALID_ARG"),    # reaches into o
+    (dict(workspace=64 * A + 1024, workspace_bytes=64), "INVALID_ARG"),  # among the states
+])
+def test_delta_workspace_refusals(dep, change, status):
+    with pytest.raises(dep.DepError) as e:
+        dep.dep_delta_rule(delta_args(dep, **change), 0)
+    assert e.value.status == getattr(dep, "DEP_ERR_" + status)
+
+
+def test_delta_workspace_size(dep):
+    size = lambda **kw: dep.dep_delta_workspace(delta_args(dep, **kw))  # noqa: E731
+    assert size(tokens=64, n_seq=64) == 0 and size(tokens=0, n_seq=0) == 0
+    one = size(tokens=48, n_seq=1) // 4  # 48 tokens may touch four chunks
+    assert one > 0 and size(tokens=480, n_seq=2, Hv=4) == 32 * one and size(tokens=48, n_seq=1, Hv=8) == 8 * one
+    assert one < size(tokens=48, n_seq=1, Dk=128) // 4 and size(tokens=1 << 30, n_seq=1) <= 2 << 30
+    assert size(tokens=1 << 30, n_seq=1, Hv=1 << 20) == (1 << 20) * one // 4 > 2 << 30
+    for args in (delta_args(dep, tokens=-1), delta_args(dep, n_seq=-1), delta_args(dep, Hv=0)):
+        with pytest.raises(dep.DepError):
+            dep.dep_delta_workspace(args)
+
+
 def test_delta_nothing_to_do(dep):
     dep.dep_delta_rule(delta_args(dep, tokens=0, n_seq=0), 0)
     assert dep.lib().dep_delta_rule(None, None) == dep.DEP_ERR_INVALID_ARG
