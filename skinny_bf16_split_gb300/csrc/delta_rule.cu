@@ -792,16 +792,20 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
     const float *s_in = from > 0 ? p.s_out : p.s_in;
     const int64_t sbase = (slot * p.Hv + h) * (int64_t)p.Dv * DK;
     const uint8_t *src = p.chunks + ((base + from) * p.Hv + h) * (int64_t)sizeof(Chunk<DK>);
-    auto fetch = [&](int64_t c) {
-        if (c < chunks) {
-            const uint8_t *at = src + c * p.Hv * (int64_t)sizeof(Chunk<DK>);
-            uint8_t *to = reinterpret_cast<uint8_t *>(&sm.stage[c % kStages]);
+    constexpr int kPieces = ((int)sizeof(Chunk<DK>) / 16 + 32 * kStateWarps - 1) / (32 * kStateWarps);
+    // Pieces i0 .. i0 + n - 1 that this thread copies of chunk c.
+    auto fetch = [&](int64_t c, int i0, int n) {
+        const uint8_t *at = src + c * p.Hv * (int64_t)sizeof(Chunk<DK>) + 16 * threadIdx.x;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(&sm.stage[c % kStages]) + 16 * threadIdx.x;
 #pragma unroll
-            for (int i = threadIdx.x * 16; i < (int)sizeof(Chunk<DK>); i += 32 * kStateWarps * 16)
-                cp_async16(to + i, at + i, true);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int i = i0; i < i0 + n; ++i)
+            if (c < chunks && i < kPieces &&
+                (16 * 32 * kStateWarps * (i + 1) <= (int)sizeof(Chunk<DK>) ||
+                 16 * (32 * kStateWarps * i + (int)threadIdx.x) < (int)sizeof(Chunk<DK>)))
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * 32 * kStateWarps * i),
+                             "l"(at + 16 * 32 * kStateWarps * i));
     };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     auto &mine = sm.v[warp];
     auto fetch_v = [&](int64_t c) {
         const int64_t tok = (from + c) * kC + (lane >> 1);
@@ -810,8 +814,10 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
                    ? *reinterpret_cast<const uint4 *>(p.v + (t0 + tok) * p.vs + (int64_t)h * p.Dv + row)
                    : make_uint4(0, 0, 0, 0);
     };
-    for (int c = 0; c < kStages - 1; ++c)
-        fetch(c);
+    for (int c = 0; c < kStages - 1; ++c) {
+        fetch(c, 0, kPieces);
+        commit();
+    }
     uint4 v = fetch_v(0);
     const int row0 = (slice * kStateWarps + warp) * 16, g = lane >> 2, t = lane & 3;
     const bool live = row0 < p.Dv;  // Dv is a multiple of 16
@@ -846,9 +852,12 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
                    : 1.f;
     };
     auto keep_range = [&](float m0, float m1) {  // the lane's largest values of both rows
-        const float f0 = factor(row_max(m0), r0), f1 = factor(row_max(m1), r1);
-        if (__any_sync(~0u, f0 != 1.f || f1 != 1.f))
-            rescale(f0, f1);
+        // Mostly every row has a value of 2^8 or more, and none of 2^15: one bit in each row's four of `some`.
+        unsigned some = __ballot_sync(~0u, m0 >= 256.f), some1 = __ballot_sync(~0u, m1 >= 256.f);
+        some |= some >> 1, some1 |= some1 >> 1;
+        some = (some | some >> 2) & (some1 | some1 >> 2) & 0x11111111u;
+        if (__any_sync(~0u, !(fmaxf(m0, m1) < 32768.f)) || some != 0x11111111u)
+            rescale(factor(row_max(m0), r0), factor(row_max(m1), r1));
     };
     {
         float m0 = 0.f, m1 = 0.f;
@@ -859,10 +868,10 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
         }
         keep_range(m0, m1);
     }
+    constexpr int kPer = (kPieces + NT / 2 - 1) / (NT / 2);
     for (int64_t c = 0; c < chunks; ++c) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncthreads();
-        fetch(c + kStages - 1);
         const Chunk<DK> &sg = sm.stage[c % kStages];
         *reinterpret_cast<uint4 *>(&mine[lane >> 1][8 * (lane & 1)]) = v;
         v = fetch_v(c + 1);
@@ -880,7 +889,10 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
             const int at = (4 * ks + t) ^ (g & 1) << 2;
             const uint4 b[4] = {sg.w[g][at], sg.qp[g][at], sg.w[8 + g][at], sg.qp[8 + g][at]};
             mma_f16x3(d, ah, al, b);
+            // The copies among the products: all at once they hold the warps up for 500 cycles.
+            fetch(c + kStages - 1, ks * kPer, kPer);
         }
+        commit();
         float U[2][4] = {};
         {  // U^T = V^T T^T - S^T W^T, the part with V
             uint32_t a[4];
