@@ -49,6 +49,7 @@
 
 #include "internal.h"
 #include "layer.h"
+#include "ptx.cuh"
 
 namespace dep {
 namespace {
@@ -446,6 +447,7 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
     auto &sg = *reinterpret_cast<Chunk<DK> *>(pr.mem);
     auto &raw = *reinterpret_cast<typename PrepShared<DK>::Raw *>(pr.mem + PrepShared<DK>::HEAD);
     auto *level = reinterpret_cast<typename PrepShared<DK>::Level *>(pr.mem + PrepShared<DK>::HEAD);
+    griddep_launch_dependents();  // blocks of the state's kernel, as soon as all of these have started
     const int h = blockIdx.x % p.Hv, pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
     const int64_t local = blockIdx.x / p.Hv, number = p.chunk0 + local;
     int s = 0;
@@ -778,6 +780,7 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
     const int64_t slot = p.slots ? p.slots[s] : s;
     const int64_t len = t1 - t0, all = (len + kC - 1) / kC, base = t0 / kC + s - p.chunk0;
     if (slot < 0 || slot >= p.n_states) {  // padding: zeros out, no state
+        griddep_wait();
         const int rows = p.Dv - slice * kRows < kRows ? p.Dv - slice * kRows : kRows;
         if (p.chunk0 == 0)
             for (int64_t i = threadIdx.x; i < len * rows; i += blockDim.x)
@@ -786,8 +789,10 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
     }
     // chunks from .. to of the sequence are among those of this launch
     const int64_t from = base < 0 ? -base : 0, to = all < p.n_chunks - base ? all : p.n_chunks - base;
-    if (from >= to && !(all == 0 && base >= 0 && base < p.n_chunks))
+    if (from >= to && !(all == 0 && base >= 0 && base < p.n_chunks)) {
+        griddep_wait();  // no block ends before the chunks are done: what follows this kernel counts on both
         return;
+    }
     const int64_t chunks = to - from;
     const float *s_in = from > 0 ? p.s_out : p.s_in;
     const int64_t sbase = (slot * p.Hv + h) * (int64_t)p.Dv * DK;
@@ -814,10 +819,6 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
                    ? *reinterpret_cast<const uint4 *>(p.v + (t0 + tok) * p.vs + (int64_t)h * p.Dv + row)
                    : make_uint4(0, 0, 0, 0);
     };
-    for (int c = 0; c < kStages - 1; ++c) {
-        fetch(c, 0, kPieces);
-        commit();
-    }
     uint4 v = fetch_v(0);
     const int row0 = (slice * kStateWarps + warp) * 16, g = lane >> 2, t = lane & 3;
     const bool live = row0 < p.Dv;  // Dv is a multiple of 16
@@ -868,6 +869,11 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
         }
         keep_range(m0, m1);
     }
+    griddep_wait();  // the chunks; what came before them is done
+    for (int c = 0; c < kStages - 1; ++c) {
+        fetch(c, 0, kPieces);
+        commit();
+    }
     constexpr int kPer = (kPieces + NT / 2 - 1) / (NT / 2);
     for (int64_t c = 0; c < chunks; ++c) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -876,23 +882,6 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
         *reinterpret_cast<uint4 *>(&mine[lane >> 1][8 * (lane & 1)]) = v;
         v = fetch_v(c + 1);
         __syncwarp();
-        float X[2][4] = {}, O[2][4] = {};
-#pragma unroll
-        for (int ks = 0; ks < NT / 2; ++ks) {
-            uint32_t ah[4], al[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                f16_split2(S[2 * ks + i][0], S[2 * ks + i][1], ah[2 * i], al[2 * i]);
-                f16_split2(S[2 * ks + i][2], S[2 * ks + i][3], ah[2 * i + 1], al[2 * i + 1]);
-            }
-            float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
-            const int at = (4 * ks + t) ^ (g & 1) << 2;
-            const uint4 b[4] = {sg.w[g][at], sg.qp[g][at], sg.w[8 + g][at], sg.qp[8 + g][at]};
-            mma_f16x3(d, ah, al, b);
-            // The copies among the products: all at once they hold the warps up for 500 cycles.
-            fetch(c + kStages - 1, ks * kPer, kPer);
-        }
-        commit();
         float U[2][4] = {};
         {  // U^T = V^T T^T - S^T W^T, the part with V
             uint32_t a[4];
@@ -911,6 +900,23 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
             mma_bf16(U[0], a, b0.x, b0.y);
             mma_bf16(U[1], a, b1.x, b1.y);
         }
+        float X[2][4] = {}, O[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < NT / 2; ++ks) {
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f16_split2(S[2 * ks + i][0], S[2 * ks + i][1], ah[2 * i], al[2 * i]);
+                f16_split2(S[2 * ks + i][2], S[2 * ks + i][3], ah[2 * i + 1], al[2 * i + 1]);
+            }
+            float(*const d[4])[4] = {&X[0], &O[0], &X[1], &O[1]};
+            const int at = (4 * ks + t) ^ (g & 1) << 2;
+            const uint4 b[4] = {sg.w[g][at], sg.qp[g][at], sg.w[8 + g][at], sg.qp[8 + g][at]};
+            mma_f16x3(d, ah, al, b);
+            // The copies among the products: all at once they hold the warps up for 500 cycles.
+            fetch(c + kStages - 1, ks * kPer, kPer);
+        }
+        commit();
         // U' = U / (k's scale), in parts scaled by row: the left operand of B and of K.R
         uint32_t uh[4], ul[4];
         float j0, j1;
@@ -972,29 +978,31 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
             }
             const float f0 = j0 * r0, f1 = j1 * r1;
             float m0 = 0.f, m1 = 0.f;
-            // two tiles of eight channels at a time, the products of the next two before the sums of these
+            // kTiles tiles of eight channels at a time, the products of the next ones before the sums of these
+            constexpr int kTiles = 4;
             const int sw = t ^ (g >> 1 & 3);
-            float D[2][2][4];
-            auto products = [&](int n, float (&d2)[2][4]) {
+            float D[2][kTiles][4];
+            auto products = [&](int n, float (&d2)[kTiles][4]) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < kTiles; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         d2[i][e] = 0.f;
-                float(*const d[2])[4] = {&d2[0], &d2[1]};
-                const uint4 b[2] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw]};
+                float(*const d[kTiles])[4] = {&d2[0], &d2[1], &d2[2], &d2[3]};
+                const uint4 b[kTiles] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw], sg.kr[8 * n + 16 + g][sw],
+                                         sg.kr[8 * n + 24 + g][sw]};
                 mma_f16x3(d, uh, ul, b);
             };
             products(0, D[0]);
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                if (n + 2 < NT)
-                    products(n + 2, D[(n / 2 + 1) & 1]);
+            for (int n = 0; n < NT; n += kTiles) {
+                if (n + kTiles < NT)
+                    products(n + kTiles, D[(n / kTiles + 1) & 1]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < kTiles; ++i) {
                     const float2 a = ld2(&sg.last[8 * (n + i) + 2 * t]);
                     float(&s)[4] = S[n + i];
-                    const float(&d)[4] = D[(n / 2) & 1][i];
+                    const float(&d)[4] = D[(n / kTiles) & 1][i];
                     s[0] = fmaf(d[0], f0, s[0] * a.x);
                     s[1] = fmaf(d[1], f0, s[1] * a.y);
                     s[2] = fmaf(d[2], f1, s[2] * a.x);
@@ -1033,8 +1041,17 @@ cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
         delta_prepare_kernel<DK><<<(unsigned)(p.n_chunks * p.Hv), kPrep, sizeof(PrepShared<DK>), s>>>(p);
         e = cudaGetLastError();
         if (e == cudaSuccess) {
-            delta_state_kernel<DK><<<(unsigned)states, 32 * kStateWarps, sizeof(StateShared<DK>), s>>>(p);
-            e = cudaGetLastError();
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)states);
+            cfg.blockDim = dim3(32 * kStateWarps);
+            cfg.dynamicSmemBytes = sizeof(StateShared<DK>);
+            cfg.stream = s;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, delta_state_kernel<DK>, p);
         }
     }
     return e;
