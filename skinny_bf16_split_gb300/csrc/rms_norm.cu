@@ -21,8 +21,8 @@
 // P below 2^-100 is flushed (stored as zero), which keeps 1 / P finite.
 //
 // Bound: DRAM.  Bytes of a row: 2 cols (x) + 4 cols with a residual + the output.  Measured
-// with a residual, of the copy rate: 8192 x 7168 to BF16 69.5 us (100 %), to int8 66.8 (91 %), to
-// e4m3 66.0 (92 %); 8192 x 7161, every row misaligned, to BF16 95.5 (72 %); one row 2.7 us.
+// with a residual, of the copy rate: 8192 x 7168 to BF16 68.5 us (101 %), to int8 66.5 (91 %), to
+// e4m3 63.8 (95 %); 8192 x 7161, every row misaligned, to BF16 94.1 (74 %); one row 2.7 us.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -215,6 +215,17 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
     for (int i = 0; i < VPT; ++i)
         hv[i] = load8<VEC>(x, 8 * (t + i * threads) - c0, n);
     if (NORM) {
+        auto load_w = [&] {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                wv[i] = a.w ? load8<VEC>(a.w, 8 * (t + i * threads) - c0, n)
+                            : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        };
+        // The weight's loads with the others where that pays: 8192 x 7168 to e4m3 66.5 -> 64.4 us, to BF16 69.8 ->
+        // 68.8; but to int8 67.2 -> 83.1, and 8192 x 7161, with two granules for each vector, 94 -> 123.
+        constexpr bool kEarly = VEC && VPT <= 4 && FMT != DEP_QUANT_INT8;
+        if (kEarly)
+            load_w();
         if (a.r) {
             const uint16_t *r = a.r + row * a.rs;
             uint4 rv[VPT];
@@ -230,10 +241,8 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
                     h[j] = pack_bf16(bf(h[j] & 0xFFFFu) + bf(q[j] & 0xFFFFu), bf(h[j] >> 16) + bf(q[j] >> 16));
             }
         }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            wv[i] = a.w ? load8<VEC>(a.w, 8 * (t + i * threads) - c0, n)
-                        : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        if (!kEarly)
+            load_w();
         if (a.r) {
             uint16_t *ho = a.h + row * a.hs;
 #pragma unroll
