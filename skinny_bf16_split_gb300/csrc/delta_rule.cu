@@ -39,7 +39,8 @@
 // In the products with S and its update the parts are FP16, whose MMAs do twice TF32's work;
 // what fits FP32's range is brought into FP16's by powers of two: one for each row of S and
 // of U, from its largest value, and one for each token's k, q and W, from bounds on theirs.
-// A and B are formed from TF32 parts, T and W in FP32; V is BF16, and T meets it in three BF16
+// A and B are formed from TF32 parts, or, with one decay for all channels, from the BF16 tokens as
+// they are (exact products, and fewer: preparing 4096 tokens of 32 heads 102 -> 95 us), T and W in FP32; V is BF16, and T meets it in three BF16
 // parts.
 // Measured: a chunk of one head takes 2.0 us of an SM to prepare (60 % of the issue slots), and 1.6
 // in the state's kernel with one block on the SM, 2.5 for both of two.  Bound: the instructions of the
@@ -411,7 +412,7 @@ __device__ __forceinline__ int64_t first_chunk(const DeltaParams &p, int s)
     return t0 / kC + s;
 }
 
-template <int DK>
+template <int DK, bool CHAN>
 struct PrepShared {
     static constexpr int KS = DK + 8;  // float2 reads without conflicts
     struct Level {                     // operands of the products of one level: rows k_i then q_i, columns k_j
@@ -429,6 +430,7 @@ struct PrepShared {
     alignas(16) float A[kC][kC];
     alignas(16) float T[kC][kTT], Tk[kC][kTT];  // columns of T, and of T over k's scales
     alignas(16) float other[4][32][4];          // halves of the levels' products
+    alignas(16) float pair[CHAN ? 1 : 4][2][kC][kC];  // each warp's part of k_i k_j, and of q_i k_j
     alignas(16) float part[4][48], norm[4][48], inv[4][32], sw[4][kC], beta[kC], g[kC];
 };
 
@@ -437,18 +439,24 @@ struct PrepShared {
 // bit b is set, is a row and meets the columns j that share its bits above b and have
 // that bit clear: M_ij is the product of the decays from the row's group of b tokens
 // on up to i, times that of the decays after j up to the group's end.  Every pair j < i
-// meets at one level, the highest bit in which the two differ.
+// meets at one level, the highest bit in which the two differ.  (With one decay for all channels
+// M_ij is a number, and one product of all tokens with all will do.)
 // A thread works on one channel; of 64 channels two threads each, one with what tokens need
 // (Q.P, W), the other with what pairs need (the levels, K.R).
-template <int DK>
+template <int DK, bool CHAN>
 __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaParams p)
 {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    auto &pr = *reinterpret_cast<PrepShared<DK> *>(smem_raw);
+    auto &pr = *reinterpret_cast<PrepShared<DK, CHAN> *>(smem_raw);
     auto &sg = *reinterpret_cast<Chunk<DK> *>(pr.mem);
-    auto &raw = *reinterpret_cast<typename PrepShared<DK>::Raw *>(pr.mem + PrepShared<DK>::HEAD);
-    auto *level = reinterpret_cast<typename PrepShared<DK>::Level *>(pr.mem + PrepShared<DK>::HEAD);
-    griddep_launch_dependents();  // blocks of the state's kernel, as soon as all of these have started
+    auto &raw = *reinterpret_cast<typename PrepShared<DK, CHAN>::Raw *>(pr.mem + PrepShared<DK, CHAN>::HEAD);
+    auto *level = reinterpret_cast<typename PrepShared<DK, CHAN>::Level *>(pr.mem + PrepShared<DK, CHAN>::HEAD);
+    // The state's kernel may start at once if these blocks are few, two for an SM; else when all are done: while
+    // others still work its first blocks would meet on the few SMs that are free (one sequence of 4096 tokens and
+    // 32 heads: 522 us at once, 472 late; 16 tokens of 32 heads: 9.2 and 10.8).
+    const bool early = gridDim.x <= 2 * 152;
+    if (early)
+        griddep_launch_dependents();
     const int h = blockIdx.x % p.Hv, pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
     const int64_t local = blockIdx.x / p.Hv, number = p.chunk0 + local;
     int s = 0;
@@ -465,12 +473,12 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
     if (first < 0 || first >= len)
         return;
     const int left = (int)(len - first < kC ? len - first : kC);
-    const bool chan = (p.flags & DEP_DELTA_CHANNEL) != 0, l2 = (p.flags & DEP_DELTA_L2NORM) != 0;
+    const bool l2 = (p.flags & DEP_DELTA_L2NORM) != 0;
     const int ch = pt % DK;
     const bool tokens = pt < DK, pairs = pt >= kPrep - DK;
     const int hq = h / (p.Hv / p.Hq);
     const uint16_t *k0 = p.k + t0 * p.ks + (int64_t)hq * DK, *q0 = p.q + t0 * p.qs + (int64_t)hq * DK;
-    const float *gp = p.g + t0 * p.gs + (chan ? (int64_t)h * DK : h);
+    const float *gp = p.g + t0 * p.gs + (CHAN ? (int64_t)h * DK : h);
     {
         constexpr int QC = DK / 8, GC = DK / 4;  // 16-byte pieces of a token
 #pragma unroll
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
             cp_async16(&raw.k[tok][e], k0 + at * p.ks + e, tok < left);
             cp_async16(&raw.q[tok][e], q0 + at * p.qs + e, tok < left);
         }
-        if (chan)
+        if (CHAN)
 #pragma unroll
             for (int i = pt; i < kC * GC; i += kPrep) {
                 const int tok = i / GC, e = i % GC * 4;
@@ -489,7 +497,7 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (pt < kC) {
             pr.beta[pt] = pt < left ? p.beta[(t0 + first + pt) * p.bs + h] : 0.f;
-            pr.g[pt] = !chan && pt < left ? gp[(first + pt) * p.gs] : 0.f;
+            pr.g[pt] = !CHAN && pt < left ? decay(gp[(first + pt) * p.gs]) : 1.f;
         }
     }
     for (int i = pt; i < kC * 4; i += kPrep)  // above the diagonal B stays zero
@@ -512,14 +520,14 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
     for (int i = 0; i < kC; ++i) {
         k[i] = __uint_as_float((uint32_t)raw.k[i][ch] << 16);
         q[i] = __uint_as_float((uint32_t)raw.q[i][ch] << 16);
-        a[i] = decay(chan ? raw.g[i][ch] : pr.g[i]);
+        a[i] = CHAN ? decay(raw.g[i][ch]) : pr.g[i];
     }
     {
         // Each token's sums of k k, q q and k q over the channels: the diagonals of products of the BF16
         // rows with themselves, warp pw a quarter of the channels.  A left operand's registers hold the
         // right operands of its two halves, too.
         constexpr int KW = DK / 64;  // steps of 16 channels
-        float kk[2][4] = {}, qq[2][4] = {}, kq[2][4] = {};
+        float kk[2][4] = {}, qq[2][4] = {}, qk[2][4] = {};
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
             const int col = (pw * KW + i) * 16 + 8 * (lane >> 4), row = lane & 15;
@@ -536,7 +544,7 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
             for (int n = 0; n < 2; ++n) {
                 mma_bf16(kk[n], x, x[n], x[2 + n]);
                 mma_bf16(qq[n], y, y[n], y[2 + n]);
-                mma_bf16(kq[n], x, y[n], y[2 + n]);
+                mma_bf16(qk[n], y, x[n], x[2 + n]);
             }
         }
         const int g = lane >> 2;
@@ -545,9 +553,18 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
             for (int n = 0; n < 2; ++n) {
                 pr.part[pw][8 * n + g] = g & 1 ? kk[n][2 * n + 1] : kk[n][2 * n];
                 pr.part[pw][16 + 8 * n + g] = g & 1 ? qq[n][2 * n + 1] : qq[n][2 * n];
-                pr.part[pw][32 + 8 * n + g] = g & 1 ? kq[n][2 * n + 1] : kq[n][2 * n];
+                pr.part[pw][32 + 8 * n + g] = g & 1 ? qk[n][2 * n + 1] : qk[n][2 * n];
             }
         }
+        if (!CHAN)  // all pairs
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int i = g + 4 * e, j = 8 * n + 2 * (lane & 3);
+                    *reinterpret_cast<float2 *>(&pr.pair[pw][0][i][j]) = make_float2(kk[n][e], kk[n][e + 1]);
+                    *reinterpret_cast<float2 *>(&pr.pair[pw][1][i][j]) = make_float2(qk[n][e], qk[n][e + 1]);
+                }
         __syncthreads();
         // every warp finishes the sums for itself
         const float sum = (pr.part[0][lane] + pr.part[1][lane]) + (pr.part[2][lane] + pr.part[3][lane]);
@@ -594,68 +611,92 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
         }
         sg.last[ch] = P;
     }
-    float mine[4];  // of this warp's level
+    if (CHAN) {
+        float mine[4];  // of this warp's level
 #pragma unroll
-    for (int l0 = 0; l0 < 4; l0 += 2) {  // two levels at a time, half of the channels for each warp
-        if (pairs)
+        for (int l0 = 0; l0 < 4; l0 += 2) {  // two levels at a time, half of the channels for each warp
+            if (pairs)
 #pragma unroll
-            for (int l = l0; l < l0 + 2; ++l) {
-                const int b = 1 << l;
-                float f = 1.f;
+                for (int l = l0; l < l0 + 2; ++l) {
+                    const int b = 1 << l;
+                    float f = 1.f;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int i = (r & ~(b - 1)) << 1 | b | (r & (b - 1));
-                    f = i % b == 0 ? a[i] : f * a[i];
-                    level[l & 1].row[r][ch] = k[i] * f;
-                    level[l & 1].row[8 + r][ch] = q[i] * f;
+                    for (int r = 0; r < 8; ++r) {
+                        const int i = (r & ~(b - 1)) << 1 | b | (r & (b - 1));
+                        f = i % b == 0 ? a[i] : f * a[i];
+                        level[l & 1].row[r][ch] = k[i] * f;
+                        level[l & 1].row[8 + r][ch] = q[i] * f;
+                    }
+#pragma unroll
+                    for (int n = 7; n >= 0; --n) {
+                        const int j = (n & ~(b - 1)) << 1 | (n & (b - 1));
+                        f = j % b == b - 1 ? 1.f : f * a[j + 1];
+                        level[l & 1].col[n][ch] = k[j] * f;
+                    }
                 }
+            __syncthreads();
+            const int g = lane >> 2, t = lane & 3;
+            const auto &lv = level[pw & 1];
+            float d[3][4] = {};  // one for each of the three products
 #pragma unroll
-                for (int n = 7; n >= 0; --n) {
-                    const int j = (n & ~(b - 1)) << 1 | (n & (b - 1));
-                    f = j % b == b - 1 ? 1.f : f * a[j + 1];
-                    level[l & 1].col[n][ch] = k[j] * f;
-                }
+            for (int i = 0; i < DK / 16; ++i) {
+                const int at = 8 * (pw / 2 * (DK / 16) + i) + 2 * t;
+                const float2 lo = ld2(&lv.row[g][at]), hi = ld2(&lv.row[g + 8][at]), cb = ld2(&lv.col[g][at]);
+                const float c4[4] = {lo.x, lo.y, hi.x, hi.y};
+                uint32_t ah[4], al[4];
+                split_a(c4, ah, al);
+                uint32_t h0, l0, h1, l1;
+                tf32_split(cb.x, h0, l0);
+                tf32_split(cb.y, h1, l1);
+                mma_tf32(d[2], al, h0, h1);
+                mma_tf32(d[1], ah, l0, l1);
+                mma_tf32(d[0], ah, h0, h1);
             }
-        __syncthreads();
-        const int g = lane >> 2, t = lane & 3;
-        const auto &lv = level[pw & 1];
-        float d[3][4] = {};  // one for each of the three products
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-            const int at = 8 * (pw / 2 * (DK / 16) + i) + 2 * t;
-            const float2 lo = ld2(&lv.row[g][at]), hi = ld2(&lv.row[g + 8][at]), cb = ld2(&lv.col[g][at]);
-            const float c4[4] = {lo.x, lo.y, hi.x, hi.y};
-            uint32_t ah[4], al[4];
-            split_a(c4, ah, al);
-            uint32_t h0, l0, h1, l1;
-            tf32_split(cb.x, h0, l0);
-            tf32_split(cb.y, h1, l1);
-            mma_tf32(d[2], al, h0, h1);
-            mma_tf32(d[1], ah, l0, l1);
-            mma_tf32(d[0], ah, h0, h1);
-        }
-        // one of the two warps of a level finishes it: of the first two levels 2 and 3, of the others 0 and 1
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            d[0][e] += d[2][e] + d[1][e];
-        if ((l0 == 0) == (pw >= 2))
+            // one of the two warps of a level finishes it: of the first two levels 2 and 3, of the others 0 and 1
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                mine[e] = d[0][e];
-        else
-            *reinterpret_cast<float4 *>(pr.other[pw ^ 2][lane]) = make_float4(d[0][0], d[0][1], d[0][2], d[0][3]);
-        __syncthreads();
-    }
-    {
-        const int g = lane >> 2, t = lane & 3, b = 1 << (pw ^ 2);
-        const float4 other = *reinterpret_cast<const float4 *>(pr.other[pw][lane]);
-        const int i = (g & ~(b - 1)) << 1 | b | (g & (b - 1));
+                d[0][e] += d[2][e] + d[1][e];
+            if ((l0 == 0) == (pw >= 2))
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
-            if ((n & ~(b - 1)) == (g & ~(b - 1))) {
-                pr.A[i][j] = (mine[e] + (&other.x)[e]) * (pr.inv[pw][i] * pr.inv[pw][j]);
-                put_b(i, j, mine[2 + e] + (&other.x)[2 + e]);
+                for (int e = 0; e < 4; ++e)
+                    mine[e] = d[0][e];
+            else
+                *reinterpret_cast<float4 *>(pr.other[pw ^ 2][lane]) = make_float4(d[0][0], d[0][1], d[0][2], d[0][3]);
+            __syncthreads();
+        }
+        {
+            const int g = lane >> 2, t = lane & 3, b = 1 << (pw ^ 2);
+            const float4 other = *reinterpret_cast<const float4 *>(pr.other[pw][lane]);
+            const int i = (g & ~(b - 1)) << 1 | b | (g & (b - 1));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = 2 * t + e, j = (n & ~(b - 1)) << 1 | (n & (b - 1));
+                if ((n & ~(b - 1)) == (g & ~(b - 1))) {
+                    pr.A[i][j] = (mine[e] + (&other.x)[e]) * (pr.inv[pw][i] * pr.inv[pw][j]);
+                    put_b(i, j, mine[2 + e] + (&other.x)[2 + e]);
+                }
+            }
+        }
+    } else {
+        // One decay for all channels: M is a number, and the pairs' products are those of the tokens as they are.
+        const int i = pt >> 3, j0 = 2 * (pt & 7);
+        float2 kk2 = make_float2(0.f, 0.f), qk2 = kk2;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float2 a = ld2(&pr.pair[w][0][i][j0]), b = ld2(&pr.pair[w][1][i][j0]);
+            kk2.x += a.x, kk2.y += a.y;
+            qk2.x += b.x, qk2.y += b.y;
+        }
+#pragma unroll
+        for (int j = j0; j < j0 + 2; ++j) {
+            const float kk = j == j0 ? kk2.x : kk2.y, qk = j == j0 ? qk2.x : qk2.y;
+            float M = 1.f;
+#pragma unroll
+            for (int m = 1; m < kC; ++m)
+                M *= m > j && m <= i ? pr.g[m] : 1.f;
+            if (j < i) {
+                pr.A[i][j] = kk * M * ((pr.norm[pw][i] * pr.inv[pw][i]) * (pr.norm[pw][j] * pr.inv[pw][j]));
+                put_b(i, j, qk * M * (pr.norm[pw][16 + i] * pr.norm[pw][j]));
             }
         }
     }
@@ -710,7 +751,7 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
         sg.T01[i][t] = p01;
         sg.T2[i][t] = p2;
     }
-    {
+    if (tokens) {
         // |W_i| <= sum_j |T_ij| times the bound on k_j's values, 2^8 over its scale
         float top = 0.f, inv;
         if (lane < kC)
@@ -733,22 +774,23 @@ __global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaPara
                     w[i + e] = fmaf((&c4.x)[e], kp[j], w[i + e]);
             }
         __syncwarp();
-        if (tokens)
 #pragma unroll
-            for (int i = 0; i < kC; i += 2) {
-                const float2 s2 = ld2(&pr.sw[pw][i]);
-                uint32_t hi, lo;
-                f16_split2(w[i] * s2.x, w[i + 1] * s2.y, hi, lo);
-                uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
-                uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.w[i + 1][0]) + (at ^ 32);
-                d0[0] = (uint16_t)hi;
-                d0[4] = (uint16_t)lo;
-                d1[0] = (uint16_t)(hi >> 16);
-                d1[4] = (uint16_t)(lo >> 16);
-            }
+        for (int i = 0; i < kC; i += 2) {
+            const float2 s2 = ld2(&pr.sw[pw][i]);
+            uint32_t hi, lo;
+            f16_split2(w[i] * s2.x, w[i + 1] * s2.y, hi, lo);
+            uint16_t *d0 = reinterpret_cast<uint16_t *>(&sg.w[i][0]) + at;
+            uint16_t *d1 = reinterpret_cast<uint16_t *>(&sg.w[i + 1][0]) + (at ^ 32);
+            d0[0] = (uint16_t)hi;
+            d0[4] = (uint16_t)lo;
+            d1[0] = (uint16_t)(hi >> 16);
+            d1[4] = (uint16_t)(lo >> 16);
+        }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
+    if (!early)
+        griddep_launch_dependents();
     if (pt == 0) {
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
                          p.chunks + (local * p.Hv + h) * (int64_t)sizeof(Chunk<DK>)),
@@ -1026,11 +1068,11 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
         }
 }
 
-template <int DK>
+template <int DK, bool CHAN>
 cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
 {
     static std::atomic<uint64_t> devices[2] = {{0}, {0}};
-    cudaError_t e = set_smem_attr(delta_prepare_kernel<DK>, devices[0]);
+    cudaError_t e = set_smem_attr(delta_prepare_kernel<DK, CHAN>, devices[0]);
     if (e == cudaSuccess)
         e = set_smem_attr(delta_state_kernel<DK>, devices[1]);
     const int64_t all = p.tokens / kC + p.n_seq, most = bytes / (p.Hv * (int64_t)sizeof(Chunk<DK>));
@@ -1039,7 +1081,7 @@ cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
         p.n_chunks = all - p.chunk0 < most ? all - p.chunk0 : most;
         if (p.n_chunks * p.Hv > INT32_MAX || states > INT32_MAX)
             return cudaErrorInvalidConfiguration;
-        delta_prepare_kernel<DK><<<(unsigned)(p.n_chunks * p.Hv), kPrep, sizeof(PrepShared<DK>), s>>>(p);
+        delta_prepare_kernel<DK, CHAN><<<(unsigned)(p.n_chunks * p.Hv), kPrep, sizeof(PrepShared<DK, CHAN>), s>>>(p);
         e = cudaGetLastError();
         if (e == cudaSuccess) {
             cudaLaunchAttribute attr{};
@@ -1072,7 +1114,7 @@ template <int DK>
 cudaError_t delta_launch(const DeltaParams &p, int64_t bytes, cudaStream_t s)
 {
     if (in_chunks(p.tokens, p.n_seq) && bytes >= p.Hv * (int64_t)sizeof(Chunk<DK>))
-        return chunk_launch<DK>(p, bytes, s);
+        return p.flags & DEP_DELTA_CHANNEL ? chunk_launch<DK, true>(p, bytes, s) : chunk_launch<DK, false>(p, bytes, s);
     return (int64_t)p.n_seq * p.Hv * p.Dv < 32768 ? recurrent_launch<DK, 2>(p, s) : recurrent_launch<DK, 4>(p, s);
 }
 
