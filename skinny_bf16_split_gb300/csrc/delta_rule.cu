@@ -22,7 +22,7 @@
 //     O = (Q.P) S^T + B U,                          S <- S diag(P_15) + U^T (K.R)
 // Two kernels.  delta_prepare_kernel works out what does not depend on the state (norms, decays, B,
 // T, W, Q.P, K.R) for every chunk at once and leaves it in the workspace, as the operands of the
-// state's MMAs; its four blocks an SM hide each other's latencies.  delta_state_kernel carries the
+// state's MMAs; its four or five blocks an SM hide each other's latencies.  delta_state_kernel carries the
 // states through the chunks: a warp holds 16 rows of S, as the accumulator of the last product, for
 // the whole sequence: an accumulator fragment is also a left operand of the next product (with the
 // channels in another order, the same on both sides), so S, U and the rest never leave the
@@ -40,7 +40,7 @@
 // what fits FP32's range is brought into FP16's by powers of two: one for each row of S and
 // of U, from its largest value, and one for each token's k, q and W, from bounds on theirs.
 // A and B are formed from TF32 parts, or, with one decay for all channels, from the BF16 tokens as
-// they are (exact products, and fewer: preparing 4096 tokens of 32 heads 102 -> 95 us), T and W in FP32; V is BF16, and T meets it in three BF16
+// they are (exact products, fewer of them and less memory, for five blocks an SM instead of four), T and W in FP32; V is BF16, and T meets it in three BF16
 // parts.
 // Measured: a chunk of one head takes 2.0 us of an SM to prepare (60 % of the issue slots), and 1.6
 // in the state's kernel with one block on the SM, 2.5 for both of two.  Bound: the instructions of the
@@ -398,7 +398,7 @@ struct Chunk {  // of one head: what its state needs of sixteen tokens
     uint4 T01[kC][4];      // T by row, in BF16 parts: the first two,
     uint2 T2[kC][4];       // and the third
     float last[DK];        // P_15
-    float iw[kC], ik[kC], iq[kC], unused[kC];  // what undoes the scales of W, k and q
+    float iw[kC], ik[kC], iq[kC], unused[kC];  // what undoes the scales of W, k and q; to a multiple of 128 bytes
     uint4 kr[DK][4];       // K.R by channel; lane t at t ^ (channel / 2 % 4)
     uint4 w[kC][DK / 4];   // W, as Q.P
 };
@@ -419,12 +419,12 @@ struct PrepShared {
         float row[16][KS], col[8][KS];
     };
     struct Raw {  // the tokens as they are; rows off by 16 bytes for ldmatrix
-        float g[kC][DK];
         uint16_t k[kC][DK + 8], q[kC][DK + 8];
+        float g[CHAN ? kC : 1][DK];
     };
     // One after another in this memory: the tokens and the levels, where the chunk's K.R and W come to lie.
     static constexpr int HEAD = offsetof(Chunk<DK>, kr);
-    static constexpr int BODY = 2 * (int)sizeof(Level);
+    static constexpr int BODY = CHAN ? 2 * (int)sizeof(Level) : (int)sizeof(Chunk<DK>) - HEAD;
     static_assert(sizeof(Raw) <= BODY && sizeof(Chunk<DK>) <= HEAD + BODY && HEAD % 16 == 0, "");
     alignas(128) uint8_t mem[HEAD + BODY];
     alignas(16) float A[kC][kC];
@@ -444,7 +444,7 @@ struct PrepShared {
 // A thread works on one channel; of 64 channels two threads each, one with what tokens need
 // (Q.P, W), the other with what pairs need (the levels, K.R).
 template <int DK, bool CHAN>
-__global__ void __launch_bounds__(kPrep, 4) delta_prepare_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(kPrep, CHAN ? 4 : 5) delta_prepare_kernel(const DeltaParams p)
 {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     auto &pr = *reinterpret_cast<PrepShared<DK, CHAN> *>(smem_raw);
