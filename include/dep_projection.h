@@ -442,7 +442,7 @@ dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream);
  * With DEP_DELTA_L2NORM q and k are first divided by
  * sqrt(sum of squares + 1e-6) over their Dk channels.
  * Sequences: cu_seqlens, int32 [n_seq + 1] in device memory, first tokens and
- * the end (lengths may be zero; values are clipped to 0..tokens), or null for
+ * the end (never decreasing, so lengths may be zero; clipped to 0..tokens), or null for
  * n_seq sequences of tokens / n_seq each.
  * States: FP32 [n_states, Hv, Dv, Dk], contiguous.  Sequence s starts from
  * state_in[i] and leaves state_out[i], i = slots[s] (int32, device memory) or s

@@ -1075,12 +1075,13 @@ cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
     cudaError_t e = set_smem_attr(delta_prepare_kernel<DK, CHAN>, devices[0]);
     if (e == cudaSuccess)
         e = set_smem_attr(delta_state_kernel<DK>, devices[1]);
-    const int64_t all = p.tokens / kC + p.n_seq, most = bytes / (p.Hv * (int64_t)sizeof(Chunk<DK>));
+    const int64_t all = p.tokens / kC + p.n_seq,
+                  most = std::min<int64_t>(bytes / (p.Hv * (int64_t)sizeof(Chunk<DK>)), INT32_MAX / p.Hv);  // of a launch
     const int64_t states = (int64_t)((p.Dv + kRows - 1) / kRows) * p.Hv * p.n_seq;
+    if (states > INT32_MAX)
+        return cudaErrorInvalidConfiguration;
     for (p.chunk0 = 0; e == cudaSuccess && p.chunk0 < all; p.chunk0 += p.n_chunks) {
         p.n_chunks = all - p.chunk0 < most ? all - p.chunk0 : most;
-        if (p.n_chunks * p.Hv > INT32_MAX || states > INT32_MAX)
-            return cudaErrorInvalidConfiguration;
         delta_prepare_kernel<DK, CHAN><<<(unsigned)(p.n_chunks * p.Hv), kPrep, sizeof(PrepShared<DK, CHAN>), s>>>(p);
         e = cudaGetLastError();
         if (e == cudaSuccess) {
