@@ -87,13 +87,13 @@ struct Int8Shape {
     static constexpr int CONV = NT <= 64 ? 8 : 4;        // converting warps (from warp 4 on)
     static constexpr int GROUPS = CONV / 4;              // four warps take 128 columns
     static constexpr int ISSUERS = GROUPS;               // issuer i takes the slots of group i
-    static constexpr int EPI = NT == 256 ? 16 : NT == 128 ? 8 : 4;  // draining warps
+    static constexpr int EPI = NT > 128 ? 16 : NT > 64 ? 8 : 4;  // draining warps
     static constexpr int ISSUER1 = ISSUERS == 1 ? -1 : DIRECT ? 4 + CONV + EPI : 3;  // the second issuing warp
     static constexpr int THREADS = (4 + CONV + EPI + (ISSUER1 > 3)) * 32;
     static constexpr int COLS = NT / (EPI / 4);          // batch columns of a draining thread
     static constexpr int BUFS = NT <= 128 ? 2 : 1;       // sets of accumulators, one for each issuer
-    static constexpr int SK = NT == 128 ? 128 : 64;      // columns of a slot
-    static constexpr int SLOTS = NT == 256 ? 5 : NT == 128 ? 4 : 8;  // slots of tensor memory, and of x
+    static constexpr int SK = NT > 64 && NT <= 128 ? 128 : 64;  // columns of a slot
+    static constexpr int SLOTS = NT > 128 ? 5 : NT > 64 ? 4 : 8;  // slots of tensor memory, and of x
     static constexpr int SLOT_COLS = SK / 2;             // a slot's 32-bit columns of tensor memory
     static constexpr int PER = kKU / SK;                 // slots of a unit
     static constexpr int EXACT = 1024 * ISSUERS / kKU;   // units whose sums an FP32 accumulator holds exactly
@@ -859,7 +859,16 @@ __global__ void __launch_bounds__(Int8Shape<NT>::THREADS, 1)
 }
 
 // MMA width of a pass of B rows.
-int width(int32_t B) { return B <= 16 ? 16 : B <= 32 ? 32 : B <= 64 ? 64 : B <= 128 ? 128 : 256; }
+// NT: the least that holds the batch.  (96 instead of 128: 14560 x 7168 at 96 rows 33.0 -> 31.7 us; 192 instead of
+// 256: at 192 rows 48.3 -> 44.5.)
+constexpr int kWidths[] = {16, 32, 64, 96, 128, 192, 256};
+int width(int32_t B)
+{
+    int i = 0;
+    while (kWidths[i] < B && kWidths[i] < 256)
+        ++i;
+    return kWidths[i];
+}
 
 Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
 {
@@ -867,10 +876,11 @@ Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
     s.tiles = (int)((N + kBM - 1) / kBM);
     s.units = (int)((K + kKU - 1) / kKU);
     const int all = s.tiles * s.units, waves = (s.tiles + sms - 1) / sms;
-    // Equal ranges, of at least four units, unless whole tiles keep enough of the blocks busy: nearly all, or, at 256
-    // rows, where a part of a tile is 128 KB, three quarters.  14560 x 7168 (75 %), equal ranges and whole tiles:
-    // 25.8 and 27.9 us at 16 rows, 38 and 37 at 128, 65.5 and 58.6 at 256; 7168 x 12288 (37 %): 61.5 and 84 at 256.
-    s.whole = s.tiles * 100ll >= (int64_t)waves * sms * (nt == 256 ? 70 : 95);
+    // Equal ranges, of at least four units, unless whole tiles keep enough of the blocks busy: nearly all, or, above
+    // 128 rows, where a part of a tile is 96 or 128 KB, 70 %.  Equal ranges and whole tiles, 14560 x 7168 (75 %): 23.9
+    // and 26.8 us at 16 rows, 33.6 and 34.7 at 128, 44.3 and 44.4 at 192, 52.1 and 50.9 at 256; 16384 x 4096 (84 %):
+    // 35.5 and 30.6 at 192, 43.3 and 36.8 at 256; 7168 x 12288 (37 %): 61.5 and 84 at 256.
+    s.whole = s.tiles * 100ll >= (int64_t)waves * sms * (nt > 128 ? 70 : 95);
     const int n = s.whole ? s.tiles : all, c = s.whole ? n : (all + 3) / 4;
     s.blocks = c < sms ? c : sms;
     s.base = n / s.blocks;
@@ -947,7 +957,9 @@ cudaError_t int8_pass(const dep_int8_plan_s &pl, const uint8_t *x, const float *
     case 16: return int8_launch<16>(pl, W, p, stream);
     case 32: return int8_launch<32>(pl, W, p, stream);
     case 64: return int8_launch<64>(pl, W, p, stream);
+    case 96: return int8_launch<96>(pl, W, p, stream);
     case 128: return int8_launch<128>(pl, W, p, stream);
+    case 192: return int8_launch<192>(pl, W, p, stream);
     default: return int8_launch<256>(pl, W, p, stream);
     }
 }
@@ -960,8 +972,8 @@ cudaError_t int8_prepare_device()
                                          (int)cudaSharedmemCarveoutMaxShared);
     if (c != cudaSuccess)
         return c;
-    for (cudaError_t e : {int8_prepare<16>(), int8_prepare<32>(), int8_prepare<64>(), int8_prepare<128>(),
-                          int8_prepare<256>()})
+    for (cudaError_t e : {int8_prepare<16>(), int8_prepare<32>(), int8_prepare<64>(), int8_prepare<96>(),
+                          int8_prepare<128>(), int8_prepare<192>(), int8_prepare<256>()})
         if (e != cudaSuccess)
             return e;
     return cudaSuccess;
@@ -1009,7 +1021,9 @@ dep_status_t dep_int8_plan(int64_t N, int64_t K, int32_t max_rows, dep_int8_plan
     const int64_t tiles = (N + dep::kBM - 1) / dep::kBM, Kp = (K + dep::kKU - 1) / dep::kKU * dep::kKU;
     const int nt = dep::width(max_rows);
     size_t parts = 0;
-    for (int w = 16; w <= nt; w *= 2) {
+    for (const int w : dep::kWidths) {
+        if (w > nt)
+            break;
         const dep::Int8Split s = dep::split_for(N, K, w, p->sm_count);
         if (!s.whole)  // two for each block
             parts = (size_t)s.blocks * 2 * w * dep::kBM * sizeof(int);

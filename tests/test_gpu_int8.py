@@ -55,6 +55,25 @@ def test_batches(dep, B, N, K):
     check(run(dep, *a), *a)
 
 
+@pytest.mark.parametrize("B", [66, 95, 96, 97, 130, 191, 192, 193])
+@pytest.mark.parametrize("N,K", [(700, 2000), (2311, 7168), (20480, 1040)])
+def test_widths_between_powers_of_two(dep, B, N, K):
+    a = make(B, N, K, seed=B + 1)
+    check(run(dep, *a), *a)
+
+
+@pytest.mark.parametrize("most", [96, 130, 256])
+def test_narrower_batches_of_one_plan(dep, most):
+    """Every kernel that batches up to a plan's rows reach, in its workspace."""
+    x, w, xs, ws = make(most, 1500, 4000, seed=most)
+    p = dep.Int8Projection(dev(w, torch.int8), dev(ws, torch.float32), max_rows=most)
+    for B in (most, 5, 20, 60, 90, 96, 1):
+        out = p.run(dev(x[:B], torch.int8), dev(xs[:B], torch.float32))
+        check(out, x[:B], w, xs[:B], ws)
+    assert dep.dep_int8_device_status(p.plan) == 0
+    p.close()
+
+
 @pytest.mark.parametrize("N,K", [(1, 16), (1, 4096), (7, 32), (64, 48), (127, 64), (128, 80), (129, 128), (130, 1024),
                                  (255, 1040), (2311, 3056), (5, 20000), (20000, 64), (300, 131056)])
 @pytest.mark.parametrize("B", [1, 5, 37])
