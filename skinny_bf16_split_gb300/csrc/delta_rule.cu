@@ -252,7 +252,7 @@ constexpr int kC = 16;            // tokens of a chunk
 constexpr int kPrep = 128;        // threads that prepare a chunk
 constexpr int kStateWarps = 4;    // of a block, 16 rows of the state each
 constexpr int kRows = 16 * kStateWarps;
-constexpr int kStages = 3;        // chunks in a block's ring
+constexpr int kStages = 2;        // chunks in a block's ring
 constexpr int kTT = 20;           // row stride of 16-wide matrices in shared memory
 
 // v = hi + lo, hi rounded to TF32's 11 bits (half away from zero) by integer arithmetic: the
