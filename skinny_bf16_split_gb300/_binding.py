@@ -443,7 +443,7 @@ def _empty(shape, dtype, device, stream):
 def _on(index, call, args, stream):
     """call(args, stream) with device `index` current; stream None: its current stream."""
     import torch
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():  # (torch.cuda.current_device takes twice as long)
         call(args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
         return
     with torch.cuda.device(index):
@@ -525,12 +525,11 @@ def _heads(t, name, dtype, index, shape):
     """Stride between the tokens of [tokens, heads, ...] whose inner dimensions are contiguous."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == index:
         strides, inner = t.stride(), shape[-1]
-        ok = strides[-1] == 1 or inner == 1
-        if len(shape) == 3:
-            ok = ok and (strides[1] == inner or shape[1] == 1)
-            inner *= shape[1]
-        if ok:
-            return strides[0] if shape[0] > 1 else inner
+        if strides[-1] == 1 or inner == 1:
+            if len(strides) == 2:
+                return strides[0] if shape[0] > 1 else inner
+            if strides[1] == inner or shape[1] == 1:
+                return strides[0] if shape[0] > 1 else inner * shape[1]
     raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on cuda:{index}")
 
 
