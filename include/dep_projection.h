@@ -395,7 +395,8 @@ dep_status_t dep_projection_plan_selftest_exchange(dep_plan_t plan, int32_t limi
  *         row's largest |p|: 1/rms cancels out of q.  scale[row] = P/rms/127.
  *   E4M3  q = e4m3(448 p / P), P the group's largest |p|;
  *         scale[row, group] = P/rms/448, scales contiguous [rows, ceil(cols/128)].
- * Both quotients are rounded as if they were exact (ties to even), so q is the
+ * Both quotients are rounded as if they were exact (ties to even), up to the
+ * largest values (a p beyond FP32's range counts as an infinity), so q is the
  * same on every run and machine.  A row (group) whose P is below 2^-100 is
  * stored as zeros with a scale of zero; one that holds an infinity or a NaN has
  * a scale that is infinite or NaN.

@@ -18,7 +18,10 @@
 //     more, and tie * P < 2^21), more than the 2^-23 of a product with a rounded
 //     reciprocal; one Newton step makes a quotient that is a tie exact, and the
 //     conversion then rounds ties to even.
-// P below 2^-100 is flushed (stored as zero), which keeps 1 / P finite.
+// P below 2^-100 is flushed (stored as zero), which keeps 1 / P finite.  P and the 127 or 448 are both
+// taken times 2^-10, so that neither 448 p nor 1 / P leaves FP32's range for p up to 2^128.  At the
+// other end, P = 2^-100, that is exact for every p whose quotient does not round to zero (p > 2^-119),
+// the remainder 127 p - c P too; e4m3's is rounded at 2^-149, 2^-6 of itself at most.
 //
 // Bound: DRAM.  Bytes of a row: 2 cols (x) + 4 cols with a residual + the output.  Measured
 // with a residual, of the copy rate: 8192 x 7168 to BF16 68.5 us (101 %), to int8 66.5 (91 %), to
@@ -42,7 +45,8 @@ struct NormParams {
     float eps;
 };
 
-constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
+constexpr float kTiny = 0x1p-100f;
+constexpr float kDown = 0x1p-10f;  // of P, 127 and 448 in the quotients
 
 __device__ __forceinline__ float bf(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
 
@@ -172,22 +176,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// rint(127 p / P) in the low byte, exactly (see above); inv = 1 / P rounded.  The guess is read
+// rint(127 p / P) in the low byte, exactly (see above), from P times kDown; inv = 1 / that, rounded.  The guess is read
 // off the mantissa of its sum with 1.5 * 2^23 (conversions run at an eighth of the rate of an
 // addition).  P infinite and inv zero (a flushed row): zero.
 __device__ __forceinline__ uint32_t quant_int8(float p, float P, float inv)
 {
-    const float t = 127.0f * p, u = fmaf(t, inv, 12582912.0f);
+    const float t = 127.0f * kDown * p, u = fmaf(t, inv, 12582912.0f);
     const float rem = fmaf(-(u - 12582912.0f), P, t), two = fabsf(rem) * 2.0f;
     const uint32_t c = __float_as_uint(u);
     const uint32_t step = rem > 0.0f ? 1u : 0xFFFFFFFFu;
     return two > P || (two == P && (c & 1)) ? c + step : c;
 }
 
-// 448 p / P to within far less than half an e4m3 step, exact where it is a tie.
+// 448 p / P to within far less than half an e4m3 step, exact where it is a tie; P and inv as above.
 __device__ __forceinline__ float quot_e4m3(float p, float P, float inv)
 {
-    const float t = 448.0f * p;
+    const float t = 448.0f * kDown * p;
     const float s = t * inv;
     return fmaf(fmaf(-s, P, t), inv, s);
 }
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
         }
     } else if (FMT == DEP_QUANT_INT8) {
         const bool flush = top < kTiny;
-        const float P = flush ? __int_as_float(0x7F800000) : top, inv = flush ? 0.0f : 1.0f / top;
+        const float P = flush ? __int_as_float(0x7F800000) : top * kDown, inv = flush ? 0.0f : 1.0f / P;
         if (t == 0)
             a.scale[row] = flush ? 0.0f : top * rstd / 127.0f;
         uint8_t *o = static_cast<uint8_t *>(a.out) + row * a.os;
@@ -350,13 +354,13 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
             for (int d = 8; d; d >>= 1)
                 g = max_nan(g, __shfl_xor_sync(~0u, g, d));
             const bool flush = g < kTiny;
-            const float inv = flush ? 0.0f : 1.0f / g;
+            const float P = g * kDown, inv = flush ? 0.0f : 1.0f / P;
             if ((t & 15) == 0 && c < n)
                 sc[c / DEP_QUANT_GROUP] = flush ? 0.0f : g * rstd / 448.0f;
             uint32_t v[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[j / 2] |= pack_e4m3(quot_e4m3(prod(i, 2 * j), g, inv), quot_e4m3(prod(i, 2 * j + 1), g, inv))
+                v[j / 2] |= pack_e4m3(quot_e4m3(prod(i, 2 * j), P, inv), quot_e4m3(prod(i, 2 * j + 1), P, inv))
                             << (16 * (j & 1));
             store8b<VEC>(o, c, n, make_uint2(v[0], v[1]));
         }
