@@ -400,7 +400,9 @@ dep_status_t dep_projection_plan_selftest_exchange(dep_plan_t plan, int32_t limi
  * same on every run and machine.  A row (group) whose P is below 2^-100 is
  * stored as zeros with a scale of zero; one that holds an infinity or a NaN has
  * a scale that is infinite or NaN.
- * Sums and scales are FP32.  Any alignment and strides >= cols; 16-byte aligned
+ * Sums and scales are FP32; a row whose squares leave FP32's range is added up
+ * times a power of two, so 1/rms is right for any finite h (up to 2^127, what
+ * FP32 holds).  Any alignment and strides >= cols; 16-byte aligned
  * rows (8-byte for q) are moved in wide loads and stores.  `out` may be x
  * itself (format NONE, same stride).  Errors: INVALID_ARG also for an output
  * that overlaps an input or another output in any other way; UNSUPPORTED for

@@ -203,12 +203,65 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi)
     return r;
 }
 
+// Whether the squares of a row leave FP32's range, by the 1 / rms that they gave: values of 2^56 or so and more or, with
+// next to no eps, all below 2^-50.
+__device__ __forceinline__ bool outside(float rstd) { return rstd == 0.0f || rstd > 0x1p50f; }
+
+// Such a row: 1 / rms once more, of the row times a power of two, and what depends on it: BF16 values; scales, which
+// have been stored as if it were one.  By memory and apart from the way of all other rows, whose registers
+// it would take.  All threads of the row call.
+template <int FMT, bool WARP_ROW>
+__device__ __forceinline__ void norm_outside(const NormParams &a, uint32_t row, float rstd, float2 *part)
+{
+    const int t = threadIdx.x, threads = WARP_ROW ? 32 : blockDim.x, n = a.cols;
+    const float f = rstd > 1.0f ? 0x1p80f : 0x1p-80f;
+    const uint16_t *h = a.r ? a.h + row * a.hs : a.x + row * a.xs;
+    if (WARP_ROW)
+        __syncwarp();  // h is stored
+    else
+        __syncthreads();  // and the warps' first parts have been read
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int c = t; c < n; c += threads)
+        sum = fmaf(bf(h[c]) * f, bf(h[c]) * f, sum);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        sum += __shfl_xor_sync(~0u, sum, o);
+    if (!WARP_ROW) {
+        if ((t & 31) == 0)
+            part[t >> 5].x = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < threads / 32; ++i)
+            sum += part[i].x;
+    }
+    const float r = f / sqrtf(sum / (float)n + a.eps * f * f);
+    if (FMT == DEP_QUANT_NONE) {
+        uint16_t *o = static_cast<uint16_t *>(a.out) + row * a.os;
+#pragma unroll 1
+        for (int c = t; c < n; c += threads)  // (o may be x: an element is read and written by one thread)
+            o[c] = (uint16_t)pack_bf16(bf(h[c]) * (a.w ? bf(a.w[c]) : 1.0f) * r, 0.0f);
+    } else {
+        const int groups = FMT == DEP_QUANT_INT8 ? 1 : (n + DEP_QUANT_GROUP - 1) / DEP_QUANT_GROUP;
+        float *scale = a.scale + (int64_t)row * groups;
+        for (int i = t; i < groups; i += threads)
+            if (scale[i] != 0.0f)  // zero: flushed
+                scale[i] *= r;
+    }
+}
+
 // WARP_ROW: blockDim = (32, 8), a row for each warp; else a row for each block of up to MAXT threads.
 // Thread t holds the eight columns from 8 (t + i * threads) on, i < VPT, less c0 where rows are not aligned.
+// BF16 rows that are not aligned are held to 72 registers, as three blocks of 288 threads an SM would need: with 74 the
+// SM holds three blocks of seven warps instead of four, and 8192 x 7161 takes 108 us instead of 95.
+template <int FMT, bool VEC, int MAXT>
+constexpr bool held = FMT == DEP_QUANT_NONE && !VEC && MAXT == 256;
 template <int FMT, bool NORM, bool VEC, int VPT, bool WARP_ROW, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
+__global__ void __launch_bounds__(held<FMT, VEC, MAXT> ? 288 : MAXT, held<FMT, VEC, MAXT> ? 3 : 0)
+    norm_kernel(const __grid_constant__ NormParams a)
 {
-    const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * 8 + threadIdx.y : (int64_t)blockIdx.x;
+    const uint32_t row = WARP_ROW ? blockIdx.x * 8 + threadIdx.y : blockIdx.x;
     if (WARP_ROW && row >= a.rows)
         return;
     const int t = threadIdx.x, threads = WARP_ROW ? 32 : blockDim.x, n = a.cols;
@@ -263,6 +316,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
         const uint32_t w = (&wv[i].x)[j / 2];
         return hf * bf(j & 1 ? w >> 16 : w & 0xFFFFu);
     };
+    __shared__ float2 part[WARP_ROW ? 1 : MAXT / 32];
     float ss = 0.0f, top = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -284,7 +338,6 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
                 top = max_nan(top, __shfl_xor_sync(~0u, top, o));
         }
         if (!WARP_ROW) {
-            __shared__ float2 part[MAXT / 32];
             if ((t & 31) == 0)
                 part[t >> 5] = make_float2(ss, top);
             __syncthreads();
@@ -312,6 +365,12 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
         }
     }
     const float rstd = NORM ? 1.0f / sqrtf(ss / (float)n + a.eps) : 1.0f;
+    // (squares outside FP32's range: BF16 rows are finished here, 8-bit rows, whose values do not depend on rms, below)
+    if (NORM && FMT == DEP_QUANT_NONE && outside(rstd)) {
+        norm_outside<FMT, WARP_ROW>(a, row, rstd, part);
+        return;
+    }
+    const float per = NORM && outside(rstd) ? 1.0f : rstd;  // the scales' factor
     if (FMT == DEP_QUANT_NONE) {
         uint16_t *o = static_cast<uint16_t *>(a.out) + row * a.os;
 #pragma unroll
@@ -326,7 +385,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
         const bool flush = top < kTiny;
         const float P = flush ? __int_as_float(0x7F800000) : top * kDown, inv = flush ? 0.0f : 1.0f / P;
         if (t == 0)
-            a.scale[row] = flush ? 0.0f : top * rstd / 127.0f;
+            a.scale[row] = flush ? 0.0f : top * per / 127.0f;
         uint8_t *o = static_cast<uint8_t *>(a.out) + row * a.os;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -342,7 +401,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
         }
     } else {
         uint8_t *o = static_cast<uint8_t *>(a.out) + row * a.os;
-        float *sc = a.scale + row * ((n + DEP_QUANT_GROUP - 1) / DEP_QUANT_GROUP);
+        float *sc = a.scale + (int64_t)row * ((n + DEP_QUANT_GROUP - 1) / DEP_QUANT_GROUP);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {  // 16 neighbouring threads hold a group
             const int c = 8 * (t + i * threads);
@@ -356,7 +415,7 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
             const bool flush = g < kTiny;
             const float P = g * kDown, inv = flush ? 0.0f : 1.0f / P;
             if ((t & 15) == 0 && c < n)
-                sc[c / DEP_QUANT_GROUP] = flush ? 0.0f : g * rstd / 448.0f;
+                sc[c / DEP_QUANT_GROUP] = flush ? 0.0f : g * per / 448.0f;
             uint32_t v[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -365,6 +424,8 @@ __global__ void __launch_bounds__(MAXT) norm_kernel(const NormParams a)
             store8b<VEC>(o, c, n, make_uint2(v[0], v[1]));
         }
     }
+    if (NORM && FMT != DEP_QUANT_NONE && outside(rstd))
+        norm_outside<FMT, WARP_ROW>(a, row, rstd, part);
 }
 
 template <int FMT, bool NORM, bool VEC>

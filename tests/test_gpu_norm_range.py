@@ -1,4 +1,5 @@
-"""The norm and the 8-bit rows over all of BF16's range."""
+"""The norm and the 8-bit rows over all of BF16's range: values next to its largest,
+whose products and squares pass FP32's, and the smallest."""
 import numpy as np
 import pytest
 
@@ -80,3 +81,58 @@ def test_infinities_and_nans_show_in_the_scale(dep):
         s = s.view(4, -1).cpu()
         assert torch.isfinite(s[0]).all() and torch.isfinite(s[3]).all()
         assert not torch.isfinite(s[1, 0]) and torch.isnan(s[2, 0])
+
+
+# relative error of 1/rms: the longest chain of FP32 additions (64 of a thread, 5 + 32 of the block), then a
+# division, a square root and a reciprocal, half a step (2^-24) each
+RSTD = 2.0 ** -24 * (64 + 37 + 8)
+
+
+@pytest.mark.parametrize("size", [1e10, 1e19, 3e19, 1e25, 1e30, 1e37])
+@pytest.mark.parametrize("cols", [8, 129, 1000, 1024, 5001, 7168, 16384, 40000])
+@pytest.mark.parametrize("fmt", [None, "int8", "e4m3"])
+def test_norm_of_rows_whose_squares_pass_fp32(dep, fmt, cols, size):
+    """y = h / rms(h) * w is of ordinary size however large h is."""
+    g = torch.Generator().manual_seed(cols)
+    x = (torch.randn(3, cols, generator=g, dtype=torch.float64) * size).bfloat16()
+    r = (torch.randn(3, cols, generator=g, dtype=torch.float64) * size).bfloat16()
+    x[1], r[1] = torch.randn(cols, generator=g).bfloat16(), torch.randn(cols, generator=g).bfloat16()
+    w = (1 + 0.2 * torch.randn(cols, generator=g)).bfloat16()
+    h = (x.float() + r.float()).bfloat16()
+    rd = r.cuda()
+    got = dep.add_rms_norm(x.cuda(), w.cuda(), rd, quant=fmt)
+    assert torch.equal(rd.cpu().view(torch.int16), h.view(torch.int16))
+    hd = h.double().numpy()
+    p, rstd = hd * w.double().numpy(), 1 / np.sqrt((hd * hd).mean(1, keepdims=True) + 1e-6)
+    if fmt is None:
+        y, want = got.double().cpu().numpy(), p * rstd
+        assert np.all(np.abs(y - want) <= np.abs(want) * (2.0 ** -8 * (1 + RSTD) + RSTD + 2.0 ** -23))
+        return
+    q, s = got
+    want, P = quantised(p, fmt)
+    np.testing.assert_array_equal(q.float().cpu().numpy(), want.astype(np.float32))
+    want_s = P * (rstd[:, 0] if fmt == "int8" else rstd) / (127 if fmt == "int8" else 448)
+    s = s.double().cpu().numpy()
+    assert np.all(np.abs(s - want_s) <= np.abs(want_s) * (RSTD + 2.0 ** -22))
+
+
+@pytest.mark.parametrize("size", [1e-10, 1e-17, 1e-20, 1e-30, 1e-37])
+@pytest.mark.parametrize("cols", [8, 1000, 5001, 7168, 40000])
+def test_norm_of_tiny_rows_without_eps(dep, cols, size):
+    g = torch.Generator().manual_seed(cols)
+    x = (torch.randn(3, cols, generator=g, dtype=torch.float64) * size).bfloat16()
+    x[1] = torch.randn(cols, generator=g).bfloat16()
+    hd = x.double().numpy()
+    y = dep.add_rms_norm(x.cuda(), eps=0.0).double().cpu().numpy()
+    want = hd / np.sqrt((hd * hd).mean(1, keepdims=True))
+    assert np.all(np.abs(y - want) <= np.abs(want) * (2.0 ** -8 * (1 + RSTD) + RSTD + 2.0 ** -23))
+
+
+def test_an_infinity_in_a_norm(dep):
+    """rms is infinite: zeros, and a NaN (infinity over infinity) where the infinity stood."""
+    x = rows_up_to(2.0, 2, 300, seed=3)
+    x[1, 7] = float("inf")
+    y = dep.add_rms_norm(x.cuda()).cpu()
+    assert torch.isfinite(y[0]).all() and torch.isnan(y[1, 7])
+    y[1, 7] = 0
+    assert not y[1].any()
