@@ -1064,7 +1064,7 @@ dep_status_t dep_int8_run(dep_int8_plan_t p, const void *x, const float *x_scale
     if (!dep::aligned(x, 16) || !dep::aligned(W, 16) || !dep::aligned(y, 16) || !dep::aligned(x_scale, 4) ||
         !dep::aligned(w_scale, 4))
         return DEP_ERR_MISALIGNED;
-    const dep::Rows ry{y, 2 * B * p->N, 0, 1}, rx{x, B * p->K, 0, 1}, rw{W, p->N * p->K, 0, 1},
+    const dep::Rows ry{y, 2 * (int64_t)B * p->N, 0, 1}, rx{x, B * p->K, 0, 1}, rw{W, p->N * p->K, 0, 1},
         rxs{x_scale, 4 * (int64_t)B, 0, 1}, rws{w_scale, 4 * p->N, 0, 1};
     if (overlap(ry, rx) || overlap(ry, rw) || overlap(ry, rxs) || overlap(ry, rws))
         return DEP_ERR_INVALID_ARG;
@@ -1074,10 +1074,10 @@ dep_status_t dep_int8_run(dep_int8_plan_t p, const void *x, const float *x_scale
         return DEP_ERR_INVALID_ARG;
     }
     const int32_t step = dep::width(p->max_rows);  // rows of a pass
-    for (int32_t r0 = 0; r0 < B; r0 += step) {
-        const int32_t rows = B - r0 < step ? B - r0 : step;
-        if (dep::int8_pass(*p, static_cast<const uint8_t *>(x) + (int64_t)r0 * p->K, x_scale + r0, W, w_scale,
-                           static_cast<uint16_t *>(y) + (int64_t)r0 * p->N, rows,
+    for (int64_t r0 = 0; r0 < B; r0 += step) {  // (up to step - 1 beyond B, and B may be the largest int32)
+        const int32_t rows = B - r0 < step ? (int32_t)(B - r0) : step;
+        if (dep::int8_pass(*p, static_cast<const uint8_t *>(x) + r0 * p->K, x_scale + r0, W, w_scale,
+                           static_cast<uint16_t *>(y) + r0 * p->N, rows,
                            static_cast<cudaStream_t>(stream)) != cudaSuccess) {
             cudaGetLastError();
             return DEP_ERR_CUDA;
