@@ -353,6 +353,7 @@ __device__ __forceinline__ float row_max(float v)  // over the four lanes of a r
 __device__ __forceinline__ float2 ld2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
 constexpr float kUnB = 16.f;  // B is stored times the scales of q and k, which make it up to 2^16, over this
+constexpr float kUnO = 0x1p24f;  // outputs are added up over this: before q's scale they may be 2^35 times the state
 constexpr float kMostScale = 0x1p64f;  // of a row of S
 constexpr int kSort = 256;
 
@@ -398,7 +399,7 @@ struct Chunk {  // of one head: what its state needs of sixteen tokens
     uint4 T01[kC][4];      // T by row, in BF16 parts: the first two,
     uint2 T2[kC][4];       // and the third
     float last[DK];        // P_15
-    float iw[kC], ik[kC], iq[kC], unused[kC];  // what undoes the scales of W, k and q; to a multiple of 128 bytes
+    float iw[kC], ik[kC], iq[kC], unused[kC];  // what undoes the scales of W, k and q (and kUnO); to a multiple of 128 bytes
     uint4 kr[DK][4];       // K.R by channel; lane t at t ^ (channel / 2 % 4)
     uint4 w[kC][DK / 4];   // W, as Q.P
 };
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(kPrep, CHAN ? 4 : 5) delta_prepare_kernel(cons
     if (pt < kC)
         put_b(pt, pt, pr.norm[pw][32 + pt] * pr.norm[pw][pt] * pr.norm[pw][16 + pt]);
     if (pt < 32)
-        (pt < 16 ? sg.ik : sg.iq)[pt & 15] = pr.inv[pw][pt];
+        (pt < 16 ? sg.ik : sg.iq)[pt & 15] = pr.inv[pw][pt] * (pt < 16 ? 1.f : kUnO);
 #pragma unroll
     for (int i = 0; i < kC; i += 4) {
         const float4 nk = *reinterpret_cast<const float4 *>(&pr.norm[pw][i]);
@@ -967,10 +968,11 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float2 iw = ld2(&sg.iw[8 * n + 2 * t]), ik = ld2(&sg.ik[8 * n + 2 * t]);
-                U[n][0] = fmaf(X[n][0] * i0, -iw.x, U[n][0]) * ik.x;
-                U[n][1] = fmaf(X[n][1] * i0, -iw.y, U[n][1]) * ik.y;
-                U[n][2] = fmaf(X[n][2] * i1, -iw.x, U[n][2]) * ik.x;
-                U[n][3] = fmaf(X[n][3] * i1, -iw.y, U[n][3]) * ik.y;
+                // (the scales' product first: X over S's alone may pass FP32's range)
+                U[n][0] = fmaf(X[n][0], i0 * -iw.x, U[n][0]) * ik.x;
+                U[n][1] = fmaf(X[n][1], i0 * -iw.y, U[n][1]) * ik.y;
+                U[n][2] = fmaf(X[n][2], i1 * -iw.x, U[n][2]) * ik.x;
+                U[n][3] = fmaf(X[n][3], i1 * -iw.y, U[n][3]) * ik.y;
             }
             const float s0 = scale_for(
                 row_max(fmaxf(fmaxf(fabsf(U[0][0]), fabsf(U[0][1])), fmaxf(fabsf(U[1][0]), fabsf(U[1][1])))), j0);
@@ -989,13 +991,14 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
             mma_f16x3(d, uh, ul, b);
         }
         // O = Q.P S^T + U' B', each with its scales
+        const float o0 = i0 * (1.f / kUnO), o1 = i1 * (1.f / kUnO), y0 = j0 * (kUnB / kUnO), y1 = j1 * (kUnB / kUnO);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
-            O[n][0] = fmaf(Y[n][0], j0 * kUnB, O[n][0] * i0) * iq.x;
-            O[n][1] = fmaf(Y[n][1], j0 * kUnB, O[n][1] * i0) * iq.y;
-            O[n][2] = fmaf(Y[n][2], j1 * kUnB, O[n][2] * i1) * iq.x;
-            O[n][3] = fmaf(Y[n][3], j1 * kUnB, O[n][3] * i1) * iq.y;
+            O[n][0] = fmaf(Y[n][0], y0, O[n][0] * o0) * iq.x;
+            O[n][1] = fmaf(Y[n][1], y0, O[n][1] * o0) * iq.y;
+            O[n][2] = fmaf(Y[n][2], y1, O[n][2] * o1) * iq.x;
+            O[n][3] = fmaf(Y[n][3], y1, O[n][3] * o1) * iq.y;
         }
         // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
         uint32_t r[4];
