@@ -452,7 +452,10 @@ dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream);
  * where slots is null.  state_in null: from zeros.  state_out may be state_in.
  * A slot outside 0..n_states-1 (padding) has no state read or written and zeros
  * for its outputs.  Two sequences of a call may not share a slot.
- * States stay in FP32; o is rounded once.  Fixed order, no atomics.
+ * States stay in FP32; o is rounded once.  Fixed order, no atomics.  By chunks (see
+ * below) the operands of products are split into FP16 parts: they keep 22 bits, and
+ * what a chunk's outputs and state lose is counted against the largest that the state's
+ * row held within the chunk.  Rows of a state that are below 2^-92 altogether keep fewer.
  * Dk is 64 or 128, Dv a multiple of 16 up to 256 (else UNSUPPORTED).
  * Workspace: device memory that the call overwrites.  With it, sequences of eight
  * tokens and more on average go by chunks of sixteen tokens, whose shares that do

@@ -354,7 +354,9 @@ __device__ __forceinline__ float2 ld2(const float *p) { return *reinterpret_cast
 
 constexpr float kUnB = 16.f;  // B is stored times the scales of q and k, which make it up to 2^16, over this
 constexpr float kUnO = 0x1p24f;  // outputs are added up over this: before q's scale they may be 2^35 times the state
-constexpr float kMostScale = 0x1p64f;  // of a row of S
+// Of a row of S.  Rows whose largest value is below 2^-92 have fewer bits left in the products; S itself is as FP32
+// holds it.
+constexpr float kMostScale = 0x1p100f;
 constexpr int kSort = 256;
 
 // The sequence of rank r by length, longest first: blocks start in order, and a long
@@ -1020,7 +1022,8 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
         {  // S <- S diag(P_15) + U^T (K.R)
             if (__any_sync(~0u, j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
                 // U beyond what S's scales leave room for: make room
-                rescale(j0 > 0x1p60f * i0 ? 0x1p60f * i0 / j0 : 1.f, j1 > 0x1p60f * i1 ? 0x1p60f * i1 / j1 : 1.f);
+                rescale(j0 > 0x1p60f * i0 ? fmaxf(0x1p60f * i0 / j0, 0x1p-126f) : 1.f,
+                        j1 > 0x1p60f * i1 ? fmaxf(0x1p60f * i1 / j1, 0x1p-126f) : 1.f);
             }
             const float f0 = j0 * r0, f1 = j1 * r1;
             float m0 = 0.f, m1 = 0.f;

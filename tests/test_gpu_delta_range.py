@@ -103,7 +103,7 @@ def test_precision(dep, way, T, dk, dv, rate, channel):
 
 
 @pytest.mark.parametrize("channel", [True, False])
-@pytest.mark.parametrize("power", [-40, 40, 100])
+@pytest.mark.parametrize("power", [-85, -80, -60, -40, 40, 100])
 def test_values_far_from_one(dep, way, power, channel):
     """States and v of one size: o and the states are linear in them."""
     a, S = make(70, 2, 2, 128, 64, channel, seed=5, rate=0.1), states(1, 2, 64, 128) * 2.0 ** power
@@ -111,15 +111,15 @@ def test_values_far_from_one(dep, way, power, channel):
     close(*call(dep, a, S, **way), *definition(*a, S, [70]), 70)
 
 
-@pytest.mark.parametrize("power", [-40, 40, 100])
+@pytest.mark.parametrize("power", [-85, -60, -40, 40, 100])
 def test_states_alone_far_from_one(dep, way, power):
     a, S = make(70, 2, 2, 128, 64, True, seed=6, rate=0.01), states(1, 2, 64, 128) * 2.0 ** power
     a[2].zero_()
     close(*call(dep, a, S, **way), *definition(*a, S, [70]), 70)
 
 
-@pytest.mark.parametrize("start", [0.0, 2.0 ** -70, 1.0])
-@pytest.mark.parametrize("size", [1e36, 1e25])
+@pytest.mark.parametrize("start", [0.0, 2.0 ** -85, 2.0 ** -70, 1.0])
+@pytest.mark.parametrize("size", [1e36, 1e25, 1e-25])
 def test_states_and_values_of_different_size(dep, way, start, size):
     a, S = make(70, 2, 2, 128, 64, True, seed=7, rate=0.1), states(1, 2, 64, 128) * start
     a[2] = (a[2].float() * size).bfloat16()
