@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kPrep, CHAN ? 4 : 5) delta_prepare_kernel(cons
                 M *= m > j && m <= i ? pr.g[m] : 1.f;
             if (j < i) {
                 pr.A[i][j] = kk * M * ((pr.norm[pw][i] * pr.inv[pw][i]) * (pr.norm[pw][j] * pr.inv[pw][j]));
-                put_b(i, j, qk * M * (pr.norm[pw][16 + i] * pr.norm[pw][j]));
+                put_b(i, j, qk * M * pr.norm[pw][16 + i] * pr.norm[pw][j]);  // (the norms of zeros have no finite product)
             }
         }
     }

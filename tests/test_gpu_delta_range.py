@@ -138,18 +138,22 @@ def test_decays_above_one_count_as_one(dep, way, channel):
     close(*call(dep, a, S, **way), *definition(*want, S, [50]), 50)
 
 
+@pytest.mark.parametrize("channel", [True, False])
+@pytest.mark.parametrize("l2norm", [True, False])
 @pytest.mark.parametrize("zeros", ["q", "k", "v", "beta", "all"])
-def test_tokens_of_zeros(dep, way, zeros):
+def test_tokens_of_zeros(dep, way, zeros, l2norm, channel):
     """Some tokens, some value channels, and a whole chunk are zero."""
     T, d = 60, 64
-    a, S = make(T, 2, 2, d, d, True, seed=13), torch.zeros(1, 2, d, d)
+    a, S = make(T, 2, 2, d, d, channel, seed=13), torch.zeros(1, 2, d, d)
+    if not l2norm:  # beta |k|^2 below 2, where the rule contracts
+        a[1] = (a[1].float() / math.sqrt(d)).bfloat16()
     for i, name in enumerate(("q", "k", "v", "", "beta")):
         if zeros in (name, "all"):
             a[i][0:3] = 0
             a[i][16:32] = 0
             a[i][40] = 0
     a[2][..., 5] = 0
-    close(*call(dep, a, S, **way), *definition(*a, S, [T]), T)
+    close(*call(dep, a, S, l2norm=l2norm, **way), *definition(*a, S, [T], l2norm=l2norm), T)
 
 
 @pytest.mark.parametrize("n", [31, 33, 64, 100, 257, 300, 1100])
