@@ -456,6 +456,10 @@ dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream);
  * below) the operands of products are split into FP16 parts: they keep 22 bits, and
  * what a chunk's outputs and state lose is counted against the largest that the state's
  * row held within the chunk.  Rows of a state that are below 2^-92 altogether keep fewer.
+ * A chunk whose tokens are too far apart in size for that, or not all finite, goes token by
+ * token: an infinity or a NaN reaches no output of an earlier token.  With L2NORM the sums
+ * of squares are FP32: |q| and |k| up to 2^63.  Tokens that belong to no sequence of the
+ * table (before its first entry, from its last on) keep what their rows of o hold.
  * Dk is 64 or 128, Dv a multiple of 16 up to 256 (else UNSUPPORTED).
  * Workspace: device memory that the call overwrites.  With it, sequences of eight
  * tokens and more on average go by chunks of sixteen tokens, whose shares that do

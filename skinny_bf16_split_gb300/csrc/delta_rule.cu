@@ -359,6 +359,10 @@ constexpr float kUnO = 0x1p24f;  // outputs are added up over this: before q's s
 constexpr float kMostScale = 0x1p100f;
 constexpr int kSort = 256;
 
+// Least output (before q's scale) of a row whose U' has the scale 1 / j that does not have to be looked at: 16 in the units
+// of U' B'.  None where the row's U is zero (or below 2^-107).
+__device__ __forceinline__ float least_for(float j) { return j > 0x1p-120f ? j * (16.f * kUnB / kUnO) : 0.f; }
+
 // The sequence of rank r by length, longest first: blocks start in order, and a long
 // sequence that starts last leaves the other SMs idle.  Tables of more than kSort
 // sequences are taken as they are.
@@ -809,11 +813,13 @@ struct StateShared {
     Chunk<DK> stage[kStages];
     uint16_t v[kStateWarps][kC][24];  // each warp's part of V, then of O; rows off a multiple of 128 bytes
     int order[kSort + 1];
+    int head;
+    int64_t token, end;  // first of this launch's, and the sequence's end
 };
 
 // One block for each sequence, head and kRows rows of its state.
 template <int DK>
-__global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const DeltaParams p)
+__global__ void __launch_bounds__(32 * kStateWarps, DK == 64 ? 3 : 2) delta_state_kernel(const DeltaParams p)
 {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     auto &sm = *reinterpret_cast<StateShared<DK> *>(smem_raw);
@@ -906,7 +912,7 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
         if (__any_sync(~0u, !(fmaxf(m0, m1) < 32768.f)) || some != 0x11111111u)
             rescale(factor(row_max(m0), r0), factor(row_max(m1), r1));
     };
-    {
+    auto start_range = [&] {
         float m0 = 0.f, m1 = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -914,6 +920,111 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
             m1 = max3_abs(m1, S[n][2], S[n][3]);
         }
         keep_range(m0, m1);
+    };
+    start_range();
+    // Whether a chunk's tokens are too far apart for one product.  U' has one scale for each row, set by its largest token,
+    // and what is below 2^-25 in its units is lost.  So an output has to be 16 in the units of U' B' (2^20 is usual; an
+    // error of 2^-9 if every B is at its largest) or, where terms cancel, made of U' of 2^-10 or more.  If a
+    // token's U' is not finite, zeros of B times it are NaN in all outputs, those before it too.
+    // (From what is at hand anyway: the outputs as they were stored for their rows' copies, and U' in its first parts.)
+    auto apart = [&](const Chunk<DK> &sg, const uint32_t (&uh)[4], float j0, float j1) {
+        bool bad = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float before = 0.f;  // the largest |U'| of the tokens before this lane's two
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 u = __half22float2(__habs2(*reinterpret_cast<const __half2 *>(&uh[2 * n + r])));
+                float m = fmaxf(u.x, u.y);
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) {
+                    const float x = __shfl_up_sync(~0u, m, d, 4);
+                    m = t >= d ? fmaxf(m, x) : m;
+                }
+                float x = __shfl_up_sync(~0u, m, 1, 4);
+                x = fmaxf(before, t ? x : 0.f);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x = fmaxf(x, e ? u.y : u.x);
+                    const int token = 8 * n + 2 * t + e;
+                    const float o = fabsf(lo_bf(mine[token][g + 8 * r]));
+                    bad |= isnan(o) || (o < least_for(r ? j1 : j0) * sg.iq[token] && x < 0x1p-10f);
+                }
+                before = fmaxf(before, __shfl_sync(~0u, m, 3, 4));
+            }
+        }
+        return __any_sync(~0u, bad && live);
+    };
+    // The tokens of chunk c by the definition, in FP32, for chunks whose tokens are too far apart: a token then
+    // depends on those before it alone.  7 us a chunk instead of 1.6, so it is to be rare: by chance one of 10^7 rows, and
+    // the first chunk of an empty state if tokens that write nothing come before others in it.  A lane has 2 NT channels of its rows g and g + 8.
+    auto one_by_one = [&](int64_t c) {
+        __syncwarp();  // the outputs of the product are stored
+        rescale(i0, i1);
+        const int h = sm.head, hq = h / (p.Hv / p.Hq);  // (from shared memory: no registers over the loop for this)
+        const int64_t first = sm.token + c * kC, end = sm.end < first + kC ? sm.end : first + kC;
+#pragma unroll 1
+        for (int64_t tok = first; tok < end; ++tok) {
+            const uint16_t *kp = p.k + tok * p.ks + (int64_t)hq * DK + 2 * t;
+            const uint16_t *qp = p.q + tok * p.qs + (int64_t)hq * DK + 2 * t;
+            const bool chan = (p.flags & DEP_DELTA_CHANNEL) != 0;
+            const float *gp = p.g + tok * p.gs + (chan ? (int64_t)h * DK + 2 * t : h);
+            const float a = chan ? 0.f : decay(*gp);
+            float kk = 0.f, qq = 0.f, kq = 0.f, k0 = 0.f, k1 = 0.f, q0 = 0.f, q1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint32_t kw = *reinterpret_cast<const uint32_t *>(kp + 8 * n);
+                const uint32_t qw = *reinterpret_cast<const uint32_t *>(qp + 8 * n);
+                const float ax = chan ? decay(gp[8 * n]) : a, ay = chan ? decay(gp[8 * n + 1]) : a;
+                const float kx = lo_bf(kw), ky = hi_bf(kw), qx = lo_bf(qw), qy = hi_bf(qw);
+                S[n][0] *= ax, S[n][1] *= ay, S[n][2] *= ax, S[n][3] *= ay;
+                kk = fmaf(kx, kx, fmaf(ky, ky, kk));
+                qq = fmaf(qx, qx, fmaf(qy, qy, qq));
+                kq = fmaf(kx, qx, fmaf(ky, qy, kq));
+                k0 = fmaf(S[n][0], kx, fmaf(S[n][1], ky, k0));
+                q0 = fmaf(S[n][0], qx, fmaf(S[n][1], qy, q0));
+                k1 = fmaf(S[n][2], kx, fmaf(S[n][3], ky, k1));
+                q1 = fmaf(S[n][2], qx, fmaf(S[n][3], qy, q1));
+            }
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                kk += __shfl_xor_sync(~0u, kk, d);
+                qq += __shfl_xor_sync(~0u, qq, d);
+                kq += __shfl_xor_sync(~0u, kq, d);
+                k0 += __shfl_xor_sync(~0u, k0, d);
+                q0 += __shfl_xor_sync(~0u, q0, d);
+                k1 += __shfl_xor_sync(~0u, k1, d);
+                q1 += __shfl_xor_sync(~0u, q1, d);
+            }
+            float rq = p.scale, rk = 1.f;
+            if (p.flags & DEP_DELTA_L2NORM) {
+                rk = 1.0f / sqrtf(kk + 1e-6f);
+                rq *= 1.0f / sqrtf(qq + 1e-6f);
+            }
+            kq *= rk * rq;
+            const float beta = p.beta[tok * p.bs + h];
+            const uint16_t *vp = p.v + tok * p.vs + (int64_t)h * p.Dv + row0 + g;
+            const float u0 = beta * ((live ? lo_bf(vp[0]) : 0.f) - k0 * rk);
+            const float u1 = beta * ((live ? lo_bf(vp[8]) : 0.f) - k1 * rk);
+            if (live && t == 0) {
+                uint16_t *o = p.o + tok * p.os + (int64_t)h * p.Dv + row0 + g;
+                o[0] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(u0, kq, q0 * rq)));
+                o[8] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(u1, kq, q1 * rq)));
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint32_t kw = *reinterpret_cast<const uint32_t *>(kp + 8 * n);
+                const float kx = lo_bf(kw) * rk, ky = hi_bf(kw) * rk;
+                S[n][0] = fmaf(u0, kx, S[n][0]), S[n][1] = fmaf(u0, ky, S[n][1]);
+                S[n][2] = fmaf(u1, kx, S[n][2]), S[n][3] = fmaf(u1, ky, S[n][3]);
+            }
+        }
+        start_range();
+    };
+    if (threadIdx.x == 0) {
+        sm.head = h;
+        sm.token = t0 + from * kC;
+        sm.end = t1;
     }
     griddep_wait();  // the chunks; what came before them is done
     for (int c = 0; c < kStages - 1; ++c) {
@@ -976,10 +1087,9 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
                 U[n][2] = fmaf(X[n][2], i1 * -iw.x, U[n][2]) * ik.x;
                 U[n][3] = fmaf(X[n][3], i1 * -iw.y, U[n][3]) * ik.y;
             }
-            const float s0 = scale_for(
-                row_max(fmaxf(fmaxf(fabsf(U[0][0]), fabsf(U[0][1])), fmaxf(fabsf(U[1][0]), fabsf(U[1][1])))), j0);
-            const float s1 = scale_for(
-                row_max(fmaxf(fmaxf(fabsf(U[0][2]), fabsf(U[0][3])), fmaxf(fabsf(U[1][2]), fabsf(U[1][3])))), j1);
+            const float top0 = row_max(fmaxf(fmaxf(fabsf(U[0][0]), fabsf(U[0][1])), fmaxf(fabsf(U[1][0]), fabsf(U[1][1]))));
+            const float top1 = row_max(fmaxf(fmaxf(fabsf(U[0][2]), fabsf(U[0][3])), fmaxf(fabsf(U[1][2]), fabsf(U[1][3]))));
+            const float s0 = scale_for(top0, j0), s1 = scale_for(top1, j1);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 f16_split2(U[n][0] * s0, U[n][1] * s0, uh[2 * n], ul[2 * n]);
@@ -992,22 +1102,43 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
             const uint4 b[2] = {sg.B[g][t], sg.B[8 + g][t]};
             mma_f16x3(d, uh, ul, b);
         }
+        // The update's products, U^T (K.R): kTiles tiles of eight channels at a time, the next ones before the sums of
+        // these, and the first before O, which has to wait for Y.
+        constexpr int kTiles = 4;
+        const int sw = t ^ (g >> 1 & 3);
+        float D[2][kTiles][4];
+        auto products = [&](int n, float (&d2)[kTiles][4]) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    d2[i][e] = 0.f;
+            float(*const d[kTiles])[4] = {&d2[0], &d2[1], &d2[2], &d2[3]};
+            const uint4 b[kTiles] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw], sg.kr[8 * n + 16 + g][sw],
+                                     sg.kr[8 * n + 24 + g][sw]};
+            mma_f16x3(d, uh, ul, b);
+        };
+        products(0, D[0]);
         // O = Q.P S^T + U' B', each with its scales
         const float o0 = i0 * (1.f / kUnO), o1 = i1 * (1.f / kUnO), y0 = j0 * (kUnB / kUnO), y1 = j1 * (kUnB / kUnO);
+        const float least0 = least_for(j0), least1 = least_for(j1);
+        bool off = false;  // an output that apart() has to look at
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
-            O[n][0] = fmaf(Y[n][0], y0, O[n][0] * o0) * iq.x;
-            O[n][1] = fmaf(Y[n][1], y0, O[n][1] * o0) * iq.y;
-            O[n][2] = fmaf(Y[n][2], y1, O[n][2] * o1) * iq.x;
-            O[n][3] = fmaf(Y[n][3], y1, O[n][3] * o1) * iq.y;
+            O[n][0] = fmaf(Y[n][0], y0, O[n][0] * o0);
+            O[n][1] = fmaf(Y[n][1], y0, O[n][1] * o0);
+            O[n][2] = fmaf(Y[n][2], y1, O[n][2] * o1);
+            O[n][3] = fmaf(Y[n][3], y1, O[n][3] * o1);
+            off |= !(fabsf(O[n][0]) >= least0) || !(fabsf(O[n][1]) >= least0) || !(fabsf(O[n][2]) >= least1) ||
+                   !(fabsf(O[n][3]) >= least1);
         }
         // O^T [rows][tokens] -> [token][rows]: four transposed 8 x 8 blocks, then 32 bytes a token
         uint32_t r[4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n]) : "f"(O[n][1]), "f"(O[n][0]));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n + 1]) : "f"(O[n][3]), "f"(O[n][2]));
+            const float2 iq = ld2(&sg.iq[8 * n + 2 * t]);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n]) : "f"(O[n][1] * iq.y), "f"(O[n][0] * iq.x));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[2 * n + 1]) : "f"(O[n][3] * iq.y), "f"(O[n][2] * iq.x));
         }
         const uint32_t at = (uint32_t)__cvta_generic_to_shared(
             &mine[(lane >> 4) * 8 + (lane & 7)][8 * (lane >> 3 & 1)]);  // over V
@@ -1020,29 +1151,17 @@ __global__ void __launch_bounds__(32 * kStateWarps, 2) delta_state_kernel(const 
             *reinterpret_cast<uint4 *>(p.o + (t0 + tok) * p.os + (int64_t)h * p.Dv + row0 + 8 * (lane & 1)) =
                 *reinterpret_cast<const uint4 *>(&mine[lane >> 1][8 * (lane & 1)]);
         {  // S <- S diag(P_15) + U^T (K.R)
-            if (__any_sync(~0u, j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
+            if (__any_sync(~0u, (off && live) || j0 > 0x1p60f * i0 || j1 > 0x1p60f * i1)) {
+                if (apart(sg, uh, j0, j1)) {
+                    one_by_one(c);
+                    continue;
+                }
                 // U beyond what S's scales leave room for: make room
                 rescale(j0 > 0x1p60f * i0 ? fmaxf(0x1p60f * i0 / j0, 0x1p-126f) : 1.f,
                         j1 > 0x1p60f * i1 ? fmaxf(0x1p60f * i1 / j1, 0x1p-126f) : 1.f);
             }
             const float f0 = j0 * r0, f1 = j1 * r1;
             float m0 = 0.f, m1 = 0.f;
-            // kTiles tiles of eight channels at a time, the products of the next ones before the sums of these
-            constexpr int kTiles = 4;
-            const int sw = t ^ (g >> 1 & 3);
-            float D[2][kTiles][4];
-            auto products = [&](int n, float (&d2)[kTiles][4]) {
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        d2[i][e] = 0.f;
-                float(*const d[kTiles])[4] = {&d2[0], &d2[1], &d2[2], &d2[3]};
-                const uint4 b[kTiles] = {sg.kr[8 * n + g][sw], sg.kr[8 * n + 8 + g][sw], sg.kr[8 * n + 16 + g][sw],
-                                         sg.kr[8 * n + 24 + g][sw]};
-                mma_f16x3(d, uh, ul, b);
-            };
-            products(0, D[0]);
 #pragma unroll
             for (int n = 0; n < NT; n += kTiles) {
                 if (n + kTiles < NT)

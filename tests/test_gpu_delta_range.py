@@ -1,12 +1,13 @@
-"""The gated delta rule at the ends of its ranges: values far from one, decays above one, many
-sequences; and its precision on ordinary ones.
+"""The gated delta rule at the ends of its ranges: values far from one, tokens of very different
+size, infinities and NaN, decays above one, many sequences; and its precision on ordinary ones.
 
 Tolerances.  o is rounded once to BF16 (2^-8 of the value).  Before that every operand of a
 product keeps 2^-22 of itself or more, and FP32 sums half a step each.  An output is a sum over a
 row of the state, whose terms may cancel, and the row carries errors of what it held lately, so what such
 roundings leave is counted against |S_row| |q|, the largest of the last sixteen tokens (a chunk): a sum of dk
 terms with independent errors of 2^-22 is off by 2^-22 |S_row| |q| / sqrt(dk), states add up over a dozen
-chunks, and the largest of some 10^5 outputs is five times the usual: 2^-19 allows two to four times that.
+chunks, and the largest of some 10^5 outputs is five times the usual: 2^-19 allows two to four times that.  Where other
+tokens of the chunk are far larger, an output may have lost 2^-10 of itself.
 A state adds such errors up over its chunks of 16 tokens like a random walk: 2^-19 sqrt(1 + T / 16) of
 its norm, the largest of the last sixteen tokens, for each sequence and head."""
 import math
@@ -80,7 +81,7 @@ def close(o, S, want_o, want_S, size, norm, T):
     finite = torch.isfinite(want_o)
     assert torch.equal(torch.isfinite(o), finite), "outputs that are not finite, in other places"
     w, d = torch.where(finite, want_o, 0.0), torch.where(finite, o - want_o, 0.0).abs()
-    bad = ~(d <= 2.0 ** -8 * w.abs() + 2.0 ** -19 * size)
+    bad = ~(d <= (2.0 ** -8 + 2.0 ** -10) * w.abs() + 2.0 ** -19 * size)
     assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist(), float(d[bad].max()), float(w.abs()[bad].max()))
     finite = torch.isfinite(want_S)
     assert torch.equal(torch.isfinite(S), finite), "states that are not finite, in other places"
@@ -126,6 +127,61 @@ def test_states_and_values_of_different_size(dep, way, start, size):
     if start == 1.0 and size < 1:
         a[3] *= 0.1  # (what v brings is then below the state's precision)
     close(*call(dep, a, S, **way), *definition(*a, S, [70]), 70)
+
+
+@pytest.mark.parametrize("orders", [3, 6, 12])
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("zero", [True, False])
+def test_keys_of_different_norm(dep, way, zero, rising, orders):
+    """Without normalisation, k's norm runs over `orders` orders of magnitude within each chunk."""
+    T, d = 48, 64
+    a, S = make(T, 2, 2, d, d, True, seed=8, rate=0.1), states(1, 2, d, d)
+    i = torch.arange(T) % 16 / 15
+    f = 10.0 ** (-orders * (1 - i if rising else i))
+    a[1] = (a[1].float() / math.sqrt(d) * f[:, None, None]).bfloat16()
+    if zero:
+        S.zero_()
+    close(*call(dep, a, S, l2norm=False, **way), *definition(*a, S, [T], l2norm=False), T)
+
+
+@pytest.mark.parametrize("power", [10, 25, 35, 60])
+@pytest.mark.parametrize("at", [5, 16, 31])
+def test_a_token_of_another_size(dep, way, at, power):
+    """One token's v, far larger than all others in some value channels: those before it keep their outputs."""
+    T, d = 48, 128
+    a, S = make(T, 2, 2, d, d, False, seed=9, rate=0.1), 0.01 * states(1, 2, d, d)
+    a[2][at, :, ::3] *= 2.0 ** power
+    close(*call(dep, a, S, **way), *definition(*a, S, [T]), T)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("where", ["q", "k", "v", "v all", "beta", "g"])
+@pytest.mark.parametrize("at", [0, 5, 15, 30, 39])
+@pytest.mark.parametrize("channel", [True, False])
+def test_infinities_and_nans_reach_later_tokens_only(dep, way, channel, at, where, value):
+    lengths, d = (40, 9), 64
+    a, S = make(49, 2, 2, d, d, channel, seed=10, rate=0.1), states(2, 2, d, d)
+    if where == "q":
+        a[0][at, 0, 3] = value
+    elif where == "k":
+        a[1][at, 0, 3] = value
+    elif where == "v":
+        a[2][at, 0, 5:8] = value
+    elif where == "v all":
+        a[2][at] = value
+    elif where == "beta":
+        a[4][at, 0] = value
+    else:
+        a[3][at, 0] = value
+    want = a.copy()
+    want[3] = torch.where(want[3] > 0, 0.0, want[3])  # a decay is at most one
+    close(*call(dep, a, S, lengths, **way), *definition(*want, S, lengths), 40)
+
+
+def test_an_infinite_state_stays_in_its_row(dep, way):
+    a, S = make(40, 1, 2, 64, 64, True, seed=11), states(1, 2, 64, 64)
+    S[0, 1, 7, 3], S[0, 0, 20, 20] = math.inf, math.nan
+    close(*call(dep, a, S, **way), *definition(*a, S, [40]), 40)
 
 
 @pytest.mark.parametrize("channel", [True, False])
