@@ -72,6 +72,8 @@ struct DeltaParams {
     int64_t chunk0, n_chunks;  // of this launch
 };
 
+constexpr uint32_t kEarly = 1u << 31;  // in flags: few chunks, see delta_prepare_kernel
+
 __device__ __forceinline__ float lo_bf(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kPrep, CHAN ? 4 : 5) delta_prepare_kernel(cons
     // The state's kernel may start at once if these blocks are few, two for an SM; else when all are done: while
     // others still work its first blocks would meet on the few SMs that are free (one sequence of 4096 tokens and
     // 32 heads: 522 us at once, 472 late; 16 tokens of 32 heads: 9.2 and 10.8).
-    const bool early = gridDim.x <= 2 * 152;
+    const bool early = (p.flags & kEarly) != 0;
     if (early)
         griddep_launch_dependents();
     const int h = blockIdx.x % p.Hv, pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
@@ -1200,6 +1202,11 @@ cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
     cudaError_t e = set_smem_attr(delta_prepare_kernel<DK, CHAN>, devices[0]);
     if (e == cudaSuccess)
         e = set_smem_attr(delta_state_kernel<DK>, devices[1]);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess)
+        e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t all = p.tokens / kC + p.n_seq,
                   most = std::min<int64_t>(bytes / (p.Hv * (int64_t)sizeof(Chunk<DK>)), INT32_MAX / p.Hv);  // of a launch
     const int64_t states = (int64_t)((p.Dv + kRows - 1) / kRows) * p.Hv * p.n_seq;
@@ -1207,6 +1214,7 @@ cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     for (p.chunk0 = 0; e == cudaSuccess && p.chunk0 < all; p.chunk0 += p.n_chunks) {
         p.n_chunks = all - p.chunk0 < most ? all - p.chunk0 : most;
+        p.flags = p.n_chunks * p.Hv <= 2 * sms ? p.flags | kEarly : p.flags & ~kEarly;
         delta_prepare_kernel<DK, CHAN><<<(unsigned)(p.n_chunks * p.Hv), kPrep, sizeof(PrepShared<DK, CHAN>), s>>>(p);
         e = cudaGetLastError();
         if (e == cudaSuccess) {
