@@ -144,6 +144,15 @@ def test_keys_of_different_norm(dep, way, zero, rising, orders):
     close(*call(dep, a, S, l2norm=False, **way), *definition(*a, S, [T], l2norm=False), T)
 
 
+@pytest.mark.parametrize("channel", [True, False])
+@pytest.mark.parametrize("power", [-60, -20, 30, 55])
+def test_norm_of_large_and_small_queries_and_keys(dep, way, power, channel):
+    """With normalisation: up to |q|, |k| of 2^60 the unit vectors, down to zeros, where 1e-6 takes over."""
+    a, S = make(40, 2, 2, 128, 64, channel, seed=15), states(1, 2, 64, 128)
+    a[0], a[1] = ((t.float() * 2.0 ** power).bfloat16() for t in a[:2])
+    close(*call(dep, a, S, **way), *definition(*a, S, [40]), 40)
+
+
 @pytest.mark.parametrize("power", [10, 25, 35, 60])
 @pytest.mark.parametrize("at", [5, 16, 31])
 def test_a_token_of_another_size(dep, way, at, power):
@@ -176,6 +185,17 @@ def test_infinities_and_nans_reach_later_tokens_only(dep, way, channel, at, wher
     want = a.copy()
     want[3] = torch.where(want[3] > 0, 0.0, want[3])  # a decay is at most one
     close(*call(dep, a, S, lengths, **way), *definition(*want, S, lengths), 40)
+
+
+@pytest.mark.parametrize("chunks", [1, 2, 3])
+def test_causal_in_passes_over_a_small_workspace(dep, monkeypatch, chunks):
+    lengths, hv, d = (40, 0, 90, 7), 2, 64
+    T, n = sum(lengths), len(lengths)
+    a, S = make(T, hv, hv, d, d, True, seed=16, rate=0.1), states(n, hv, d, d)
+    a[2][21, 0, 9], a[2][100, 1, 5], a[2][60] = math.nan, math.inf, a[2][60] * 2.0 ** 40
+    chunk = dep.dep_delta_workspace(dep.dep_delta_args_t(tokens=T, n_seq=n, Hv=hv, Dk=d)) // (T // 16 + n)
+    monkeypatch.setattr(dep._binding, "dep_delta_workspace", lambda args: chunks * chunk)
+    close(*call(dep, a, S, lengths), *definition(*a, S, lengths), 90)
 
 
 def test_an_infinite_state_stays_in_its_row(dep, way):
