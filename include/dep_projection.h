@@ -457,7 +457,8 @@ dep_status_t dep_quantize_rows(const dep_norm_args_t *args, void *stream);
  * what a chunk's outputs and state lose is counted against the largest that the state's
  * row held within the chunk.  Rows of a state that are below 2^-92 altogether keep fewer.
  * A chunk whose tokens are too far apart in size for that, or not all finite, goes token by
- * token: an infinity or a NaN reaches no output of an earlier token.  With L2NORM the sums
+ * token: an infinity or a NaN reaches no output of an earlier token, and a decay to
+ * nothing leaves nothing of the state before it, however large.  With L2NORM the sums
  * of squares are FP32: |q| and |k| up to 2^63.  Tokens that belong to no sequence of the
  * table (before its first entry, from its last on) keep what their rows of o hold.
  * Dk is 64 or 128, Dv a multiple of 16 up to 256 (else UNSUPPORTED).

@@ -361,6 +361,8 @@ constexpr float kUnO = 0x1p24f;  // outputs are added up over this: before q's s
 constexpr float kMostScale = 0x1p100f;
 constexpr int kSort = 256;
 
+constexpr float kLeastQ = 0x1p-70f * kUnO;  // what undoes a q's scale is not less, but for a q of zeros (or below 2^-63)
+
 // Least output (before q's scale) of a row whose U' has the scale 1 / j that does not have to be looked at: 16 in the units
 // of U' B'.  None where the row's U is zero (or below 2^-107).
 __device__ __forceinline__ float least_for(float j) { return j > 0x1p-120f ? j * (16.f * kUnB / kUnO) : 0.f; }
@@ -924,42 +926,34 @@ __global__ void __launch_bounds__(32 * kStateWarps, DK == 64 ? 3 : 2) delta_stat
         keep_range(m0, m1);
     };
     start_range();
-    // Whether a chunk's tokens are too far apart for one product.  U' has one scale for each row, set by its largest token,
-    // and what is below 2^-25 in its units is lost.  So an output has to be 16 in the units of U' B' (2^20 is usual; an
-    // error of 2^-9 if every B is at its largest) or, where terms cancel, made of U' of 2^-10 or more.  If a
-    // token's U' is not finite, zeros of B times it are NaN in all outputs, those before it too.
-    // (From what is at hand anyway: the outputs as they were stored for their rows' copies, and U' in its first parts.)
+    // Whether a chunk's tokens are too far apart for one product.  U' has one scale for each row, set by its largest
+    // token, and what is below 2^-25 in its units is lost.  So an output has to be 16 in the units of U' B' (2^20 is
+    // usual; an error of 2^-9 if every B is at its largest) or, where its terms cancel, they have to add up to 1/8
+    // (2^-10).  Less is left of tokens far smaller than a later one, or than those before a decay to nothing.  If a
+    // token's U' is not finite, zeros of B times it are NaN in all outputs, those before it too.  The zeros of a zero q
+    // are right.  (From what is at hand anyway: the outputs as stored for their rows' copies, U' and B' in their first
+    // parts.)
     auto apart = [&](const Chunk<DK> &sg, const uint32_t (&uh)[4], float j0, float j1) {
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        const uint32_t u[4] = {uh[0] & kAbs, uh[1] & kAbs, uh[2] & kAbs, uh[3] & kAbs};
         bool bad = false;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float before = 0.f;  // the largest |U'| of the tokens before this lane's two
+        for (int n = 0; n < 2; ++n) {
+            const uint4 b = sg.B[8 * n + g][t];
+            float terms[4] = {};
+            mma_f16(terms, u, b.x & kAbs, b.y & kAbs);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float2 u = __half22float2(__habs2(*reinterpret_cast<const __half2 *>(&uh[2 * n + r])));
-                float m = fmaxf(u.x, u.y);
-#pragma unroll
-                for (int d = 1; d < 4; d <<= 1) {
-                    const float x = __shfl_up_sync(~0u, m, d, 4);
-                    m = t >= d ? fmaxf(m, x) : m;
-                }
-                float x = __shfl_up_sync(~0u, m, 1, 4);
-                x = fmaxf(before, t ? x : 0.f);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    x = fmaxf(x, e ? u.y : u.x);
-                    const int token = 8 * n + 2 * t + e;
-                    const float o = fabsf(lo_bf(mine[token][g + 8 * r]));
-                    bad |= isnan(o) || (o < least_for(r ? j1 : j0) * sg.iq[token] && x < 0x1p-10f);
-                }
-                before = fmaxf(before, __shfl_sync(~0u, m, 3, 4));
+            for (int e = 0; e < 4; ++e) {
+                const int token = 8 * n + 2 * t + (e & 1);
+                const float o = fabsf(lo_bf(mine[token][g + 8 * (e >> 1)])), iq = sg.iq[token];
+                bad |= isnan(o) || (iq >= kLeastQ && o < least_for(e < 2 ? j0 : j1) * iq && terms[e] < 0.125f);
             }
         }
         return __any_sync(~0u, bad && live);
     };
     // The tokens of chunk c by the definition, in FP32, for chunks whose tokens are too far apart: a token then
-    // depends on those before it alone.  7 us a chunk instead of 1.6, so it is to be rare: by chance one of 10^7 rows, and
-    // the first chunk of an empty state if tokens that write nothing come before others in it.  A lane has 2 NT channels of its rows g and g + 8.
+    // depends on those before it alone.  7 us a chunk instead of 1.6, so it is to be rare: by chance one of 10^6 rows that start
+    // empty, and chunks of an empty state, or a decay to nothing, where tokens that write nothing come before others.  A lane has 2 NT channels of its rows g and g + 8.
     auto one_by_one = [&](int64_t c) {
         __syncwarp();  // the outputs of the product are stored
         rescale(i0, i1);

@@ -198,6 +198,18 @@ def test_causal_in_passes_over_a_small_workspace(dep, monkeypatch, chunks):
     close(*call(dep, a, S, lengths), *definition(*a, S, lengths), 90)
 
 
+@pytest.mark.parametrize("channel", [True, False])
+@pytest.mark.parametrize("power", [-30, 0, 30, 60])
+@pytest.mark.parametrize("at", [0, 3, 15, 16, 20, 31, 33])
+def test_a_decay_to_nothing_forgets(dep, way, at, power, channel):
+    """After it everything is as from an empty state, however large the state was."""
+    T, d = 40, 64
+    a, S = make(T, 2, 2, d, d, channel, seed=17, rate=0.1), states(1, 2, d, d) * 2.0 ** power
+    a[3][at] = -math.inf
+    o, S = call(dep, a, S, **way)
+    close(o[at:], S, *definition(*(t[at:] for t in a), torch.zeros(1, 2, d, d), [T - at]), T - at)
+
+
 def test_an_infinite_state_stays_in_its_row(dep, way):
     a, S = make(40, 1, 2, 64, 64, True, seed=11), states(1, 2, 64, 64)
     S[0, 1, 7, 3], S[0, 0, 20, 20] = math.inf, math.nan
