@@ -543,7 +543,8 @@ def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens
     [tokens, Hv] or, for a decay of each key channel, [tokens, Hv, Dk]; beta:
     float32 [tokens, Hv].  Heads are contiguous, tokens any stride apart.
     cu_seqlens: int32 [n_seq + 1] on the device, or None for n_seq (default 1)
-    sequences of equal length.  state, state_out: float32 [n_states, Hv, Dv, Dk];
+    sequences of equal length; tokens outside the table keep what out holds there
+    (in a new out, anything).  state, state_out: float32 [n_states, Hv, Dv, Dk];
     state None starts from zeros, state_out defaults to state (updated in place).
     slots: int32 [n_seq] on the device, each sequence's place among the states
     (outside 0..n_states-1: padding).  scale defaults to Dk ** -0.5.  The workspace

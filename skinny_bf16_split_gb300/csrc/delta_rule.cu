@@ -26,16 +26,17 @@
 // states through the chunks: a warp holds 16 rows of S, as the accumulator of the last product, for
 // the whole sequence: an accumulator fragment is also a left operand of the next product (with the
 // channels in another order, the same on both sides), so S, U and the rest never leave the
-// registers.  Two blocks of four warps an SM, 210 registers a thread: with 128, sixteen warps an SM
+// registers.  Two blocks of four warps an SM, 214 registers a thread (of 64 channels three, 168): with 128, sixteen warps an SM
 // take longer (one sequence of 2048 tokens and 32 heads 403 us instead of 277, when both ran in 233),
 // for want of loads under way; two warps for the two halves of the channels of 16 rows, whose sums
 // have to meet in each chunk, 284 instead of 243.  Both kernels in one, preparing warps beside the
 // state's, saved the way through memory (28 KB a chunk and head), but left SMs without work where
 // sequences are few or of different lengths, and was never faster: that one sequence 498 us (now
-// 243), 8192 tokens of 96 heads in 4 ragged sequences 1571 (now 1430), two sequences of 512 tokens
-// and 76 heads, one for each SM, 151 (now 146).
+// 235), 8192 tokens of 96 heads in 4 ragged sequences 1571 (now 1419), two sequences of 512 tokens
+// and 76 heads, one for each SM, 151 (now 145).
 // Precision: an FP32 operand is split into two parts of 11 bits, and three of the four products
-// are kept (the last is below 2^-22), so that everything keeps FP32's precision, or nearly.
+// are kept (the last is below 2^-22): products of 22 bits instead of 24, sums and states in FP32.  On 8192 tokens the
+// state is within 2.3e-7 of 64 bits (1.5e-7 if all is FP32).
 // In the products with S and its update the parts are FP16, whose MMAs do twice TF32's work;
 // what fits FP32's range is brought into FP16's by powers of two: one for each row of S and
 // of U, from its largest value, and one for each token's k, q and W, from bounds on theirs.
@@ -45,6 +46,8 @@
 // Measured: a chunk of one head takes 2.0 us of an SM to prepare (60 % of the issue slots), and 1.6
 // in the state's kernel with one block on the SM, 2.5 for both of two.  Bound: the instructions of the
 // one, the latencies of a chunk's chain in the other (the MMAs alone are 0.65 us a block).
+// One scale for U and products with zeros above the diagonals join the tokens of a chunk: where that would show
+// (infinities, NaN, tokens or states of far different size) the chunk's rows go token by token, see apart().
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1229,7 +1232,8 @@ cudaError_t chunk_launch(DeltaParams p, int64_t bytes, cudaStream_t s)
 }
 
 // What dep_delta_workspace asks for at most.  A pass over part of the chunks has fewer sequences at work at once:
-// 8192 tokens of 96 heads in 4 ragged sequences took 1488 us in one pass (1.4 GB), with 1 GiB 1587 and with 256 MiB 1856.
+// 8192 tokens of 96 heads in 4 ragged sequences take 1405 us in one pass (1.4 GB), with 1 GiB 1613, 512 MiB 1729 and
+// 256 MiB 1812.
 constexpr int64_t kMostWorkspace = 2ll << 30;
 
 // Chunks for sequences of eight tokens and more on average: a chunk costs the same whether it holds one token or

@@ -46,8 +46,10 @@
 // atomics took 18 us at 128 rows: about 200 billion a second.)  No block waits for another.
 // Bound: up to 128 rows the latencies between the roles (1600 cycles a unit where its bytes take
 // 1400), above the MMAs one after another.  Measured: 49376 x 7168 at 16 rows 63.9 us (82 % of the
-// copy rate), at 128 rows 78.6; 14560 x 7168 at 16 rows 23.9, at 128 rows 33.4, at 256 rows 49 to 50
-// (1060 TFLOP/s, 54 % of the BF16 rate).
+// copy rate), at 128 rows 78.6; 14560 x 7168 at 16 rows 24.5, at 128 rows 33.7, at 256 rows 50 to 51
+// (1060 TFLOP/s, 54 % of the BF16 rate; its draining threads spill 332 bytes).  The BF16 projection of this library,
+// as eager launches in a graph like these: 49376 x 7168 at 16 rows 109 us, at 128 rows 114; 14560 x 7168 at 16 rows
+// 36, at 128 rows 37, at 256 rows 44.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -876,7 +878,7 @@ Int8Split split_for(int64_t N, int64_t K, int nt, int sms)
     s.tiles = (int)((N + kBM - 1) / kBM);
     s.units = (int)((K + kKU - 1) / kKU);
     const int all = s.tiles * s.units, waves = (s.tiles + sms - 1) / sms;
-    // Equal ranges, of at least four units, unless whole tiles keep enough of the blocks busy: nearly all, or, above
+    // Equal ranges, of about four units or more, unless whole tiles keep enough of the blocks busy: nearly all, or, above
     // 128 rows, where a part of a tile is 96 or 128 KB, 70 %.  Equal ranges and whole tiles, 14560 x 7168 (75 %): 23.9
     // and 26.8 us at 16 rows, 33.6 and 34.7 at 128, 44.3 and 44.4 at 192, 52.1 and 50.9 at 256; 16384 x 4096 (84 %):
     // 35.5 and 30.6 at 192, 43.3 and 36.8 at 256; 7168 x 12288 (37 %): 61.5 and 84 at 256.

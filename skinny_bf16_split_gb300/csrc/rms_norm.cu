@@ -24,8 +24,10 @@
 // the remainder 127 p - c P too; e4m3's is rounded at 2^-149, 2^-6 of itself at most.
 //
 // Bound: DRAM.  Bytes of a row: 2 cols (x) + 4 cols with a residual + the output.  Measured
-// with a residual, of the copy rate: 8192 x 7168 to BF16 68.5 us (101 %), to int8 66.5 (91 %), to
-// e4m3 63.8 (95 %); 8192 x 7161, every row misaligned, to BF16 94.1 (74 %); one row 2.7 us.
+// with a residual, of the copy rate: 8192 x 7168 to BF16 68.4 us (101 %), to int8 66.7 (91 %), to
+// e4m3 65.4 (93 %); 8192 x 7161, every row misaligned, to BF16 95.5 (72 %); one row 2.9 us.
+// Rows of more than 16384 columns have 64 or 72 elements a thread, of which 0.3 to 2.1 KB spill: 200 x 40000 to int8
+// 28 us (30 %).
 #include <cuda_bf16.h>
 
 #include "internal.h"
