@@ -25,7 +25,7 @@
 //
 // Bound: DRAM.  Bytes of a row: 2 cols (x) + 4 cols with a residual + the output.  Measured
 // with a residual, of the copy rate: 8192 x 7168 to BF16 68.4 us (101 %), to int8 66.7 (91 %), to
-// e4m3 65.4 (93 %); 8192 x 7161, every row misaligned, to BF16 95.5 (72 %); one row 2.9 us.
+// e4m3 64.2 (95 %); 8192 x 7161, every row misaligned, to BF16 95.5 (72 %); one row 2.9 us.
 // Rows of more than 16384 columns have 64 or 72 elements a thread, of which 0.3 to 2.1 KB spill: 200 x 40000 to int8
 // 28 us (30 %).
 #include <cuda_bf16.h>
@@ -255,10 +255,11 @@ __device__ __forceinline__ void norm_outside(const NormParams &a, uint32_t row, 
 
 // WARP_ROW: blockDim = (32, 8), a row for each warp; else a row for each block of up to MAXT threads.
 // Thread t holds the eight columns from 8 (t + i * threads) on, i < VPT, less c0 where rows are not aligned.
-// BF16 rows that are not aligned are held to 72 registers, as three blocks of 288 threads an SM would need: with 74 the
-// SM holds three blocks of seven warps instead of four, and 8192 x 7161 takes 108 us instead of 95.
+// Kernels held to 72 registers, as three blocks of 288 threads an SM would need.  BF16 rows that are not aligned: with 74
+// the SM holds three blocks of seven warps instead of four, and 8192 x 7161 takes 108 us instead of 95.  Aligned e4m3
+// rows: left to itself the compiler takes 64, and 8192 x 7168 65.1 us instead of 64.2.
 template <int FMT, bool VEC, int MAXT>
-constexpr bool held = FMT == DEP_QUANT_NONE && !VEC && MAXT == 256;
+constexpr bool held = MAXT == 256 && (VEC ? FMT == DEP_QUANT_E4M3 : FMT == DEP_QUANT_NONE);
 template <int FMT, bool NORM, bool VEC, int VPT, bool WARP_ROW, int MAXT>
 __global__ void __launch_bounds__(held<FMT, VEC, MAXT> ? 288 : MAXT, held<FMT, VEC, MAXT> ? 3 : 0)
     norm_kernel(const __grid_constant__ NormParams a)
