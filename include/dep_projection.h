@@ -520,6 +520,128 @@ dep_status_t dep_int8_device_status(dep_int8_plan_t plan, void *stream, int32_t 
 /* Free the plan (synchronises its device).  NULL is a no-op. */
 void dep_int8_plan_destroy(dep_int8_plan_t plan);
 
+/* ------------------------------------------------------------------------
+ * The core of a softmax-attention layer between the packed input projection
+ * and the output projection (7168 x 12288: 96 heads of 128 channels): the
+ * norm and rotation of the heads of q and k, the paged cache, and attention
+ * over it.  No counterpart in the pages.  The calls keep the rules of the
+ * group above (asynchronous, nothing allocated, capturable).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * For every token t and every head of q and of k, D channels x:
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * weight     (DEP_HEADS_NORM; else y = x)
+ *     (a, b) <- amplitude * (a cos u - b sin u, b cos u + a sin u),
+ *                                                u = positions[t] * freqs[i]
+ *
+ * for the pairs i = 0 .. rot/2 - 1 of the channels [first, first + rot): channels
+ * first + i and first + rot/2 + i, or with DEP_HEADS_INTERLEAVED first + 2i and
+ * first + 2i + 1.  The other channels keep y.  FP32 throughout, one rounding to
+ * BF16 at the end; the angle is reduced as a 64-bit fraction of a turn, so far
+ * positions lose nothing (2^-53 of position * frequency).  freqs: FP64 radians a
+ * position, rot/2 of them (not read where rot is 0).  1/rms is right for any
+ * finite x (up to 2^128).
+ *
+ * dep_norm_rotate stores the heads to q_out and k_out (each may be its input, with
+ * the same stride); k may be null (Hk is then 0).
+ * dep_append_kv stores k's heads, and v's as they are, to a cache of pages:
+ * token t's to slot slots[t] % page_size of page slots[t] / page_size.  A slot below
+ * 0 or at or past n_pages * page_size is padding: nothing of the token is stored to
+ * the cache.  Two tokens of a call may not share a slot.  q and q_out may both be null
+ * (Hq is then 0); where given, q is normed and rotated as in dep_norm_rotate, for every
+ * token.
+ *
+ * q [tokens, Hq, D], k and v [tokens, Hk, D] BF16, heads contiguous in a token and
+ * tokens q_stride etc. apart, so that columns of a packed projection are read in
+ * place.  Caches: BF16, channel c of head h at slot s of page p at
+ * p * page_stride + s * slot_stride + h * head_stride + c, so that a page may hold
+ * the heads of each token or the tokens of each head.  D, rot and first are multiples
+ * of 8, D at most 256 (else UNSUPPORTED).  q, k, v, outputs and caches are 16-byte
+ * aligned and their strides multiples of 8; the weights are 16-byte, freqs 8-byte and
+ * positions and slots 4-byte aligned (else MISALIGNED).  INVALID_ARG also for an
+ * output that overlaps an input or another output in any other way, and for a cache
+ * whose strides let two of its rows share bytes.
+ */
+#define DEP_HEADS_INTERLEAVED 1u /* pairs of neighbours, not of halves */
+#define DEP_HEADS_NORM 2u        /* RMS norm of each head */
+#define DEP_HEADS_MAX_D 256
+
+typedef struct {
+    const void *q, *k, *v;
+    const void *q_weight, *k_weight; /* BF16 [D], or null (ones); only with DEP_HEADS_NORM */
+    const double *freqs;             /* [rot / 2] */
+    const int32_t *positions;        /* [tokens], or null where rot is 0 */
+    const int32_t *slots;            /* [tokens]; dep_append_kv */
+    void *q_out, *k_out;             /* k_out: dep_norm_rotate */
+    void *k_cache, *v_cache;         /* dep_append_kv */
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride; /* between tokens */
+    int64_t k_page_stride, k_slot_stride, k_head_stride, v_page_stride, v_slot_stride, v_head_stride;
+    int64_t tokens, n_pages;
+    int32_t Hq, Hk, D, rot, first, page_size;
+    uint32_t flags;
+    float eps, amplitude;
+} dep_heads_args_t;
+
+dep_status_t dep_norm_rotate(const dep_heads_args_t *args, void *stream);
+dep_status_t dep_append_kv(const dep_heads_args_t *args, void *stream);
+
+/*
+ * Attention of the new tokens of several sequences over a paged cache.  For token t
+ * of sequence s and query head h (key and value head h / (Hq / Hk))
+ *
+ *     o = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q . k_j),
+ *     lse = log(sum_j p_j)
+ *
+ * over the positions j that the token sees.  The sequence has kv_lens[s] positions in
+ * the cache, position j in slot j % page_size of page page_table[s, j / page_size];
+ * the last n of them are those of its own n tokens, token i's at kv_lens[s] - n + i
+ * (they are stored before the call, as by dep_append_kv).  All its tokens see the
+ * positions before these.  Of these a token sees
+ *   tree null:  those up to its own (a decode token, a piece of a prompt; any n);
+ *   tree given: token i' of the sequence where bit i' of tree[t] is set (a tree of
+ *               drafted tokens: a node's ancestors and, to see itself, its own bit).
+ *               Tokens from the 64th on of a sequence are seen by none.
+ * What a token does not see does not reach its output, whatever the cache holds there.
+ * A token that sees nothing (or nothing but scores of minus infinity) has zeros and
+ * lse minus infinity.  Positions on a page outside 0..n_pages-1 are seen by none, and
+ * kv_lens is clipped to 0..table_width * page_size; a sequence may be shorter than its
+ * n tokens (those before position 0 are not in the cache).
+ *
+ * q, o: BF16 [tokens, Hq, D], heads contiguous, tokens q_stride and o_stride apart.
+ * lse: FP32 [tokens, Hq], contiguous, or null.  Caches as for dep_append_kv (rows may
+ * share bytes here).  cu_seqlens: int32 [n_seq + 1] in device memory (never decreasing;
+ * clipped to 0..tokens), or null for n_seq sequences of tokens / n_seq each.  Tokens
+ * that belong to no sequence keep what their rows of o and lse hold.  kv_lens int32
+ * [n_seq], page_table int32 [n_seq, table_width], rows table_stride apart, tree 64-bit
+ * words [tokens]: device memory.  Hq is a multiple of Hk, D 64 or 128 (else
+ * UNSUPPORTED), scale finite and not negative.
+ * Scores, sums and o's accumulators are FP32; the p_j are rounded to BF16 for the
+ * product with v.  The order of sums is fixed for given sizes and lengths.  No atomics.
+ * Workspace: device memory that the call overwrites, at least dep_attention_workspace
+ * bytes (of tokens, n_seq, Hq, Hk and D alone; else INVALID_ARG).
+ * MISALIGNED unless q, o, the caches and the workspace are 16-byte aligned, the strides
+ * of q, o and the caches multiples of 8, tree 8-byte and the rest 4-byte aligned.
+ */
+typedef struct {
+    const void *q, *k_cache, *v_cache;
+    const int32_t *page_table, *kv_lens;
+    const int32_t *cu_seqlens; /* or null */
+    const uint64_t *tree;      /* or null */
+    void *o;
+    float *lse; /* or null */
+    int64_t q_stride, o_stride;
+    int64_t k_page_stride, k_slot_stride, k_head_stride, v_page_stride, v_slot_stride, v_head_stride;
+    int64_t table_stride, tokens, n_pages;
+    int32_t n_seq, Hq, Hk, D, page_size, table_width;
+    float scale;
+    void *workspace;
+    int64_t workspace_bytes;
+} dep_attention_args_t;
+
+dep_status_t dep_paged_attention(const dep_attention_args_t *args, void *stream);
+dep_status_t dep_attention_workspace(const dep_attention_args_t *args, int64_t *bytes);
+
 /* The binning rule on its own: index into keys[0..n_keys) of the entry serving
  * B rows -- smallest key >= B, else the largest key; -1 if n_keys < 1.  The keys
  * need not be sorted.  Pure host function. */

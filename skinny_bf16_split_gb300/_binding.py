@@ -45,6 +45,9 @@ DEP_QUANT_GROUP = 128
 DEP_NORM_MAX_COLS = 65536
 DEP_DELTA_CHANNEL = 1
 DEP_DELTA_L2NORM = 2
+DEP_HEADS_INTERLEAVED = 1
+DEP_HEADS_NORM = 2
+DEP_HEADS_MAX_D = 256
 
 DEP_DEV_TIMEOUT_PRODUCER = 1
 DEP_DEV_TIMEOUT_CONSUMER = 2
@@ -64,6 +67,7 @@ EXPORTS = (
     "dep_projection_plan_selftest_exchange",
     "dep_add_rms_norm", "dep_quantize_rows", "dep_delta_rule", "dep_delta_workspace", "dep_int8_plan", "dep_int8_run",
     "dep_int8_plan_workspace", "dep_int8_device_status", "dep_int8_plan_destroy",
+    "dep_norm_rotate", "dep_append_kv", "dep_paged_attention", "dep_attention_workspace",
 )
 
 
@@ -93,6 +97,27 @@ class dep_delta_args_t(ctypes.Structure):
                 + [(name, ctypes.c_int32) for name in ("n_seq", "Hq", "Hv", "Dk", "Dv")]
                 + [("flags", ctypes.c_uint32), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
                    ("workspace_bytes", ctypes.c_int64)])
+
+
+class dep_heads_args_t(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_void_p) for name in
+                 ("q", "k", "v", "q_weight", "k_weight", "freqs", "positions", "slots", "q_out", "k_out", "k_cache",
+                  "v_cache")]
+                + [(name, ctypes.c_int64) for name in
+                   ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride", "k_page_stride", "k_slot_stride",
+                    "k_head_stride", "v_page_stride", "v_slot_stride", "v_head_stride", "tokens", "n_pages")]
+                + [(name, ctypes.c_int32) for name in ("Hq", "Hk", "D", "rot", "first", "page_size")]
+                + [("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("amplitude", ctypes.c_float)])
+
+
+class dep_attention_args_t(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_void_p) for name in
+                 ("q", "k_cache", "v_cache", "page_table", "kv_lens", "cu_seqlens", "tree", "o", "lse")]
+                + [(name, ctypes.c_int64) for name in
+                   ("q_stride", "o_stride", "k_page_stride", "k_slot_stride", "k_head_stride", "v_page_stride",
+                    "v_slot_stride", "v_head_stride", "table_stride", "tokens", "n_pages")]
+                + [(name, ctypes.c_int32) for name in ("n_seq", "Hq", "Hk", "D", "page_size", "table_width")]
+                + [("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)])
 
 
 class DepError(RuntimeError):
@@ -148,6 +173,10 @@ def lib():
         "dep_int8_plan_workspace": ([vp, P(ctypes.c_size_t)], i32),
         "dep_int8_device_status": ([vp, vp, P(i32)], i32),
         "dep_int8_plan_destroy": ([vp], None),
+        "dep_norm_rotate": ([P(dep_heads_args_t), vp], i32),
+        "dep_append_kv": ([P(dep_heads_args_t), vp], i32),
+        "dep_paged_attention": ([P(dep_attention_args_t), vp], i32),
+        "dep_attention_workspace": ([P(dep_attention_args_t), P(ctypes.c_int64)], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -383,6 +412,24 @@ def dep_int8_device_status(plan, stream=None) -> int:
 
 def dep_int8_plan_destroy(plan) -> None:
     lib().dep_int8_plan_destroy(plan)
+
+
+def dep_norm_rotate(args: dep_heads_args_t, stream=None) -> None:
+    _check(lib().dep_norm_rotate(ctypes.byref(args), _stream(stream)), "dep_norm_rotate")
+
+
+def dep_append_kv(args: dep_heads_args_t, stream=None) -> None:
+    _check(lib().dep_append_kv(ctypes.byref(args), _stream(stream)), "dep_append_kv")
+
+
+def dep_paged_attention(args: dep_attention_args_t, stream=None) -> None:
+    _check(lib().dep_paged_attention(ctypes.byref(args), _stream(stream)), "dep_paged_attention")
+
+
+def dep_attention_workspace(args: dep_attention_args_t) -> int:
+    b = ctypes.c_int64()
+    _check(lib().dep_attention_workspace(ctypes.byref(args), ctypes.byref(b)), "dep_attention_workspace")
+    return b.value
 
 
 class Projection:
@@ -651,3 +698,193 @@ class Int8Projection:
             self.close()
         except Exception:
             pass
+
+
+# ---- the attention core -------------------------------------------------------
+
+def rotary_freqs(rot: int, base: float = 10000.0, *, factor: float = 1.0, original: int | None = None,
+                 fast: float = 32.0, slow: float = 1.0, device=None):
+    """(freqs, amplitude) of a rotation of `rot` channels for norm_rotate and append_kv: float64
+    [rot / 2] radians a position, base ** (-2i / rot).
+
+    factor: the context is `factor` times the trained one.  With original None every frequency is
+    divided by it.  With the trained length in `original`, pairs that turn `fast` times or more within
+    it keep their frequency, those that turn `slow` times or less are divided by the factor, a linear
+    ramp (over the pair's index) lies between, and the amplitude is 0.1 ln(factor) + 1 ("YaRN", Peng et
+    al. 2023); otherwise it is 1."""
+    import math
+
+    import torch
+    if rot < 2 or rot % 2 != 0 or not base > 1 or not factor >= 1 or not fast > slow > 0 or (
+            original is not None and not original > 0):
+        raise ValueError("rot must be even, base above 1, factor at least 1, fast above slow above 0 and original above 0")
+    freqs = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    amplitude = 1.0
+    if original is None:
+        freqs = freqs / factor
+    elif factor > 1:
+        def pair(turns):  # (the index of) the pair that turns so often within `original`
+            return rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+        low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
+        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - low) / max(high - low, 0.001)).clamp(0, 1)
+        freqs = freqs * (1 - ramp) + freqs / factor * ramp
+        amplitude = 0.1 * math.log(factor) + 1.0
+    return freqs.to(device if device is not None else "cuda"), amplitude
+
+
+def _vector(t, name, dtype, index, n):
+    """Address of a contiguous vector of n."""
+    if t.dtype is dtype and t.shape == (n,) and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on cuda:{index}")
+
+
+def _cache(t, name, index, heads, d):
+    """Strides between pages, slots and heads of a cache [pages, page_size, heads, d]."""
+    import torch
+    if t.dtype is torch.bfloat16 and t.dim() == 4 and t.shape[2:] == (heads, d) and t.shape[1] > 0 and (
+            t.get_device() == index):
+        strides = t.stride()
+        if strides[3] == 1:
+            return strides[:3]
+    raise ValueError(f"{name} must be a bfloat16 tensor [pages, page_size, {heads}, {d}] with contiguous channels on "
+                     f"cuda:{index}")
+
+
+def _rotation(args, dev, tokens, positions, freqs, interleaved, amplitude, norm, eps, first, weights):
+    """Fill in what norm_rotate and append_kv share."""
+    import torch
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs must be given together")
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be a vector, a frequency for each pair of channels")
+        args.rot = 2 * freqs.shape[0]
+        args.freqs = _vector(freqs, "freqs", torch.float64, dev, freqs.shape[0])
+        args.positions = _vector(positions, "positions", torch.int32, dev, tokens)
+    for name, w in weights:
+        if w is not None:
+            if not norm:
+                raise ValueError(f"{name} needs norm")
+            setattr(args, name, _vector(w, name, torch.bfloat16, dev, args.D))
+    args.first, args.eps, args.amplitude = first, eps, amplitude
+    args.flags = (DEP_HEADS_INTERLEAVED if interleaved else 0) | (DEP_HEADS_NORM if norm else 0)
+
+
+def norm_rotate(q, k=None, positions=None, freqs=None, *, interleaved: bool = False, amplitude: float = 1.0,
+                norm: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6, first: int = 0, q_out=None,
+                k_out=None, stream=None):
+    """RMS norm of each head (with norm) and the rotary position in one pass (see dep_norm_rotate in
+    include/dep_projection.h).
+
+    q [tokens, Hq, D], k [tokens, Hk, D]: bfloat16, heads contiguous, tokens any stride apart.
+    positions: int32 [tokens]; freqs: float64 [rot / 2] radians a position (rotary_freqs), which rotate
+    the channels [first, first + rot) of each head by halves, or by neighbours (interleaved).
+    q_weight, k_weight: bfloat16 [D].  q_out and k_out are allocated where omitted; they may be q and k.
+    Returns (q_out, k_out), or q_out alone without k."""
+    import torch
+    dev, bf16 = q.get_device(), torch.bfloat16
+    if q.dim() != 3 or dev < 0 or (k is not None and k.dim() != 3):
+        raise ValueError("q [tokens, Hq, D] and k [tokens, Hk, D] must be CUDA tensors of three dimensions")
+    T, hq, d = q.shape
+    if q_out is None:
+        q_out = _empty((T, hq, d), bf16, q.device, stream)
+    args = dep_heads_args_t(q=q.data_ptr(), q_out=q_out.data_ptr(), q_stride=_heads(q, "q", bf16, dev, (T, hq, d)),
+                            q_out_stride=_heads(q_out, "q_out", bf16, dev, (T, hq, d)), tokens=T, Hq=hq, D=d, page_size=1)
+    if k is not None:
+        shape = (T, k.shape[1], d)
+        if k_out is None:
+            k_out = _empty(shape, bf16, q.device, stream)
+        args.k, args.k_out, args.Hk = k.data_ptr(), k_out.data_ptr(), shape[1]
+        args.k_stride, args.k_out_stride = _heads(k, "k", bf16, dev, shape), _heads(k_out, "k_out", bf16, dev, shape)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    _rotation(args, dev, T, positions, freqs, interleaved, amplitude, norm, eps, first,
+              (("q_weight", q_weight), ("k_weight", k_weight)))
+    _on(dev, dep_norm_rotate, args, stream)
+    return q_out if k is None else (q_out, k_out)
+
+
+def append_kv(k, v, k_cache, v_cache, slots, positions=None, freqs=None, *, interleaved: bool = False,
+              amplitude: float = 1.0, norm: bool = False, k_weight=None, eps: float = 1e-6, first: int = 0, q=None,
+              q_weight=None, q_out=None, stream=None):
+    """Keys and values of new tokens into a paged cache, the keys (and q, where given) normed and
+    rotated on the way as by norm_rotate (see dep_append_kv in include/dep_projection.h).
+
+    k, v [tokens, Hk, D]: bfloat16, heads contiguous, tokens any stride apart.  k_cache, v_cache:
+    bfloat16 [pages, page_size, Hk, D] with contiguous channels, any other strides (a transposed view
+    of [pages, Hk, page_size, D] is a cache by heads).  slots: int32 [tokens], page * page_size + place;
+    outside the cache: padding, not stored.  Returns q_out (allocated where omitted; may be q), or None
+    without q."""
+    import torch
+    dev, bf16 = k.get_device(), torch.bfloat16
+    if k.dim() != 3 or dev < 0 or (q is not None and q.dim() != 3):
+        raise ValueError("k, v [tokens, Hk, D] and q [tokens, Hq, D] must be CUDA tensors of three dimensions")
+    shape = T, hk, d = k.shape
+    ks, vs = _cache(k_cache, "k_cache", dev, hk, d), _cache(v_cache, "v_cache", dev, hk, d)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    args = dep_heads_args_t(
+        k=k.data_ptr(), v=v.data_ptr(), slots=_vector(slots, "slots", torch.int32, dev, T), k_cache=k_cache.data_ptr(),
+        v_cache=v_cache.data_ptr(), k_stride=_heads(k, "k", bf16, dev, shape), v_stride=_heads(v, "v", bf16, dev, shape),
+        k_page_stride=ks[0], k_slot_stride=ks[1], k_head_stride=ks[2], v_page_stride=vs[0], v_slot_stride=vs[1],
+        v_head_stride=vs[2], tokens=T, n_pages=k_cache.shape[0], Hk=hk, D=d, page_size=k_cache.shape[1])
+    if q is not None:
+        q_shape = (T, q.shape[1], d)
+        if q_out is None:
+            q_out = _empty(q_shape, bf16, q.device, stream)
+        args.q, args.q_out, args.Hq = q.data_ptr(), q_out.data_ptr(), q_shape[1]
+        args.q_stride, args.q_out_stride = _heads(q, "q", bf16, dev, q_shape), _heads(q_out, "q_out", bf16, dev, q_shape)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    _rotation(args, dev, T, positions, freqs, interleaved, amplitude, norm, eps, first,
+              (("q_weight", q_weight), ("k_weight", k_weight)))
+    _on(dev, dep_append_kv, args, stream)
+    return q_out
+
+
+def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, tree=None, scale: float | None = None,
+                    out=None, lse=None, stream=None):
+    """Attention of the new tokens of several sequences over a paged cache (see dep_paged_attention in
+    include/dep_projection.h): o = softmax(scale q k^T) v.
+
+    q: bfloat16 [tokens, Hq, D], heads contiguous, tokens any stride apart, D 64 or 128.  k_cache, v_cache:
+    as for append_kv.  page_table: int32 [n_seq, width] (rows may be strided), kv_lens: int32 [n_seq], the
+    positions of each sequence in the cache, its new tokens' among them (the last ones).  cu_seqlens: int32
+    [n_seq + 1], the sequences' first tokens, or None for n_seq equal ones; tokens outside the table keep
+    what out and lse hold there (in new ones, anything).  tree: int64 [tokens], bit i set where the token
+    sees its sequence's i-th new token (drafts of up to 64); None: every token sees those up to itself.
+    scale defaults to D ** -0.5.  lse: float32 [tokens, Hq], filled in where given.  The workspace is the
+    allocator's.  Returns out, bfloat16 [tokens, Hq, D] (allocated where omitted)."""
+    import torch
+    dev, bf16, i32 = q.get_device(), torch.bfloat16, torch.int32
+    shape = q.shape
+    if len(shape) != 3 or dev < 0:
+        raise ValueError("q must be a CUDA tensor [tokens, Hq, D]")
+    T, hq, d = shape
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same four dimensions")
+    pages, page, hk, _ = k_cache.shape
+    ks, vs = _cache(k_cache, "k_cache", dev, hk, d), _cache(v_cache, "v_cache", dev, hk, d)
+    if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != dev or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be an int32 matrix [n_seq, width] with contiguous rows on cuda:{dev}")
+    n, width = page_table.shape
+    if out is None:
+        out = _empty(shape, bf16, q.device, stream)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, hq) or lse.get_device() != dev or (
+            not lse.is_contiguous())):
+        raise ValueError(f"lse must be a contiguous float32 matrix [{T}, {hq}] on cuda:{dev}")
+    args = dep_attention_args_t(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), _vector(kv_lens, "kv_lens", i32, dev, n),
+        None if cu_seqlens is None else _vector(cu_seqlens, "cu_seqlens", i32, dev, n + 1),
+        None if tree is None else _vector(tree, "tree", torch.int64, dev, T), out.data_ptr(), _ptr(lse),
+        _heads(q, "q", bf16, dev, shape), _heads(out, "out", bf16, dev, shape), *ks, *vs,
+        page_table.stride(0) if n > 1 else width, T, pages, n, hq, hk, d, page, width,
+        d ** -0.5 if scale is None else scale)
+    args.workspace_bytes = dep_attention_workspace(args)
+    if args.workspace_bytes:
+        workspace = _empty((args.workspace_bytes,), torch.uint8, q.device, stream)
+        args.workspace = workspace.data_ptr()
+    _on(dev, dep_paged_attention, args, stream)
+    return out
