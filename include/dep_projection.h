@@ -620,6 +620,8 @@ dep_status_t dep_append_kv(const dep_heads_args_t *args, void *stream);
  * product with v.  The order of sums is fixed for given sizes and lengths.  No atomics.
  * Workspace: device memory that the call overwrites, at least dep_attention_workspace
  * bytes (of tokens, n_seq, Hq, Hk and D alone; else INVALID_ARG).
+ * Every wait in the kernel is bounded (1 s); if one gives up, a DEP_DEV_* code is stored to
+ * *status where that holds 0, and the outputs are not complete.
  * MISALIGNED unless q, o, the caches and the workspace are 16-byte aligned, the strides
  * of q, o and the caches multiples of 8, tree 8-byte and the rest 4-byte aligned.
  */
@@ -637,6 +639,7 @@ typedef struct {
     float scale;
     void *workspace;
     int64_t workspace_bytes;
+    int32_t *status; /* or null; device memory */
 } dep_attention_args_t;
 
 dep_status_t dep_paged_attention(const dep_attention_args_t *args, void *stream);

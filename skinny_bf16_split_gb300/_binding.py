@@ -117,7 +117,8 @@ class dep_attention_args_t(ctypes.Structure):
                    ("q_stride", "o_stride", "k_page_stride", "k_slot_stride", "k_head_stride", "v_page_stride",
                     "v_slot_stride", "v_head_stride", "table_stride", "tokens", "n_pages")]
                 + [(name, ctypes.c_int32) for name in ("n_seq", "Hq", "Hk", "D", "page_size", "table_width")]
-                + [("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)])
+                + [("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                   ("status", ctypes.c_void_p)])
 
 
 class DepError(RuntimeError):
