@@ -33,7 +33,19 @@
 namespace dep {
 namespace {
 
-constexpr int kTreeMost = 64;  // tokens of a sequence that a tree's words name
+constexpr int kTreeMost = 64;    // tokens of a sequence that a tree's words name
+constexpr int kTile = 128;       // positions of a tile; rows of an MMA
+constexpr int kBlockRows = 2 * kTile;  // rows of an item
+constexpr int kProducers = 2;    // warps that fetch, each half of a tile's rows
+constexpr int kWarps = 12;       // 4 + 4 softmax, 2 producing, 2 issuing MMAs
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSlotRing = 5 * 32768;  // bytes of keys and values in flight
+constexpr int kLag = 2;     // slots that a producing thread's copies may be behind what it issues
+constexpr int kMasks = 8;   // tiles whose masks are held
+constexpr int kAhead = 4;   // items whose descriptions are held
+constexpr int kCost = 2;    // tiles' worth of work that an item costs beside its tiles
+constexpr int kLeast = 4;   // units of a block at least: fewer are not worth the joining
+constexpr uint64_t kWaitNs = 1000000000ull;
 
 struct AttnParams {
     const uint16_t *q, *kc, *vc;
@@ -42,173 +54,175 @@ struct AttnParams {
     uint16_t *o;
     float *lse;
     int64_t qs, os, kps, kss, khs, vps, vss, vhs, ts;
-    int64_t tokens, n_pages;
-    int32_t n_seq, Hq, Hk, page, width;
+    int64_t tokens, each, n_pages;  // each: tokens of a sequence where there is no table of starts
+    int32_t n_seq, Hq, Hk, G, page, most;  // G = Hq / Hk; most: positions that a row of the table covers
+    uint32_t page_mul, page_shift;         // pos / page = pos * page_mul >> page_shift
     float scale;
     int *status;
     int32_t part_rows;
+    int32_t box;       // slots of a page in one box of the caches' maps; 0: no maps
     struct Cut *cuts;  // of every block
     float2 *part_ml;   // m and sum of a part's rows: [block][2][part_rows]
     float *parts;      // their channels
 };
 
-__device__ __forceinline__ int64_t seq_start(const AttnParams &p, int s)
-{
-    if (!p.cu)
-        return p.tokens / p.n_seq * s;
-    const int64_t t = p.cu[s];
-    return t < 0 ? 0 : t > p.tokens ? p.tokens : t;
-}
-
-constexpr int kLeast = 4;        // tiles of a block at least
-constexpr int kTile = 128;       // positions of a tile; rows of an MMA
-constexpr int kProducers = 128;  // threads that gather
-constexpr int kWarps = 13;       // 4 + 4 softmax, 4 producing, 1 issuing MMAs
-constexpr int kThreads = 32 * kWarps;
-constexpr int kSlotRing = 5 * 32768;  // bytes of keys and values in flight
-constexpr int kLag = 2;               // copies in flight behind the one being issued, of each producing thread
-constexpr int kMasks = 8;             // tiles whose masks are held
-constexpr int kBlockRows = 2 * kTile; // rows of an item
-constexpr uint64_t kWaitNs = 1000000000ull;
-
 // What a block leaves for the joining kernel where one of its items goes on in other blocks.
 struct Cut {
     int32_t parts;  // of the item; 0: none begins here and goes on
+    int32_t kv_head, row0, rows;
+    int64_t first;
+    int32_t pad[2];
+};
+
+// One key and value head of a sequence, up to kBlockRows of its rows, and the tiles [t0, t1) of their T.
+struct Item {
+    int64_t first;               // the sequence's first token
     int32_t seq, kv_head, row0, rows;
-    int32_t pad[3];
+    int32_t t0, t1, T;           // t1 = 0: no more items
+    int32_t own, end, len;       // positions: the first new token's; what is seen ends before `end`; the sequence's length
+    __device__ bool two() const { return rows > kTile; }  // both groups on the same tiles of positions
+    __device__ bool whole() const { return t0 == 0 && t1 == T; }
 };
 
 template <int D>
 struct Smem {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kSlots = kSlotRing / kTileBytes;
-    uint8_t q[2][kTileBytes];          // rows' tiles; the second also joins the groups' sums
+    uint8_t q[2][kTileBytes];          // tiles of rows
     uint8_t ring[kSlots][kTileBytes];  // keys and values
     uint64_t full[kSlots], empty[kSlots];
-    uint64_t q_full, q_empty, joined[2], x_full, x_free, drained;
-    uint64_t s_full[2], p_full[2], o_full[2];
-    uint32_t masks[kMasks][4];  // positions of a tile that are in the cache
-    float ml[2][kTile];         // the second group's m and sum
+    uint64_t q_full[2], q_empty[2], item_full[kAhead], done[kAhead];
+    uint64_t s_full[2], p_full[2], o_full[2], x_full, x_free, drained[2];
+    alignas(16) uint32_t masks[kMasks][4];  // positions of a tile that are in the cache
+    Item items[kAhead];
+    int32_t odd[kAhead];  // 1 + the last item of that place with values of new tokens that are not finite
+    float2 ml[kTile];     // the second group's m and sum
     int64_t scan[kWarps];
     int64_t begin, left, unit0;  // this block's range, and the units before its first sequence
-    int32_t seq, blocks;
+    int32_t seq;
     uint32_t tmem;
-    int32_t odd[2];  // 1 + the last (even, odd) item with values of new tokens that are not finite
-    int32_t dead;    // a wait gave up
+    int32_t dead;  // a wait gave up
 };
 
 // ---- a sequence, and the items of a range -----------------------------------------------------
 
+__device__ __forceinline__ int64_t seq_start(const AttnParams &p, int s)
+{
+    if (!p.cu)
+        return p.each * s;
+    const int64_t t = p.cu[s];
+    return t < 0 ? 0 : t > p.tokens ? p.tokens : t;
+}
+
 struct Seq {
     int64_t first;  // token
-    int32_t n, len, blocks, G;
+    int32_t n, len, rows, blocks;
     __device__ void load(const AttnParams &p, int s)
     {
+        const int32_t l = p.lens[s];
         first = seq_start(p, s);
-        const int64_t m = seq_start(p, s + 1) - first, most = (int64_t)p.width * p.page;
-        n = m > 0 ? (int32_t)m : 0;
-        const int64_t l = p.lens[s];
-        len = (int32_t)(l < 0 ? 0 : l < most ? l : most);
-        G = p.Hq / p.Hk;
-        blocks = (rows() + kBlockRows - 1) / kBlockRows;
+        n = (int32_t)max(seq_start(p, s + 1) - first, (int64_t)0);
+        len = min(max(l, 0), p.most);
+        rows = n * p.G;
+        blocks = (rows + kBlockRows - 1) / kBlockRows;
     }
-    __device__ int rows() const { return n * G; }
-    __device__ int own() const { return len - n; }  // position of the first new token
-    // Tiles of block rb of rows: up to the last position that one of them may see, at least one.
-    __device__ int tiles(const AttnParams &p, int rb) const
+    // What the rows of block rb see ends before this position.
+    __device__ int end(const AttnParams &p, int rb) const
     {
-        int end;
         if (p.tree)
-            end = len - max(0, n - kTreeMost);
-        else
-            end = own() + (min(rows(), (rb + 1) * kBlockRows) - 1) / G + 1;
-        return max(1, (end + kTile - 1) / kTile);
+            return len - max(0, n - kTreeMost);
+        return len - n + (int)((uint32_t)(min(rows, (rb + 1) * kBlockRows) - 1) / (uint32_t)p.G) + 1;
     }
-    __device__ int64_t units(const AttnParams &p) const
+    __device__ int tiles(const AttnParams &p, int rb) const { return max(1, (end(p, rb) + kTile - 1) / kTile); }
+    __device__ int64_t head_units(const AttnParams &p) const  // of one key and value head
     {
-        if (n == 0)
-            return 0;
+        if (p.tree)
+            return n == 0 ? 0 : (int64_t)blocks * (tiles(p, 0) + kCost);
         int64_t u = 0;
-        if (p.tree)
-            u = (int64_t)blocks * tiles(p, 0);
-        else
-            for (int rb = 0; rb < blocks; ++rb)
-                u += tiles(p, rb);
-        return u * p.Hk;
+        for (int rb = 0; rb < blocks; ++rb)
+            u += tiles(p, rb) + kCost;
+        return u;
     }
 };
 
-// The items of a block's range, one after another; every role goes through them by itself.
+// a / b, by 32 bits where they do.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
+{
+    return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Units in equal parts for blocks: block b has those from begin(b) on.
+struct Parts {
+    int64_t each, more;
+    __device__ Parts(int64_t units, int blocks) : each(divide(units, blocks)), more(units - each * blocks) {}
+    __device__ int64_t begin(int b) const { return b * each + min((int64_t)b, more); }
+};
+
+// The items of a block's range, one after another.  An item has kCost units before its tiles'.
 struct Items {
     Seq q;
-    int s, kv_head, rb, t0, t1, T;
-    int64_t left, unit;  // of the range; of the item's first tile
-    __device__ void tiles(const AttnParams &p)
-    {
-        T = q.tiles(p, rb);
-        t1 = (int)min((int64_t)T, t0 + left);
-        left -= t1 - t0;
-    }
+    int s, kv_head, rb, T;
+    int64_t unit, at, left;  // the item's first unit, where in it the range goes on, units left of the range
     // Go to unit `begin` of the units from sequence `seq` on, which starts at unit0.
     __device__ void start(const AttnParams &p, int seq, int64_t unit0, int64_t begin, int64_t count)
     {
-        s = seq, left = count, unit = unit0;
+        s = seq, left = count;
         q.load(p, s);
-        const int64_t head = q.units(p) / p.Hk, skip = (begin - unit0) / head;
+        const int64_t head = q.head_units(p), skip = divide(begin - unit0, head);
         kv_head = (int)skip;
-        unit += skip * head;
+        unit = unit0 + skip * head;
         for (rb = 0;; ++rb) {
             T = q.tiles(p, rb);
-            if (unit + T > begin)
+            if (unit + T + kCost > begin)
                 break;
-            unit += T;
+            unit += T + kCost;
         }
-        t0 = (int)(begin - unit);
-        tiles(p);
+        at = begin - unit;
     }
-    __device__ bool next(const AttnParams &p)
+    // The next item with tiles in the range, or one with t1 = 0.
+    __device__ Item take(const AttnParams &p)
     {
+        Item it;
+        it.t1 = 0;
+        if (left <= 0 || s >= p.n_seq)
+            return it;
+        const int64_t to = min((int64_t)T + kCost, at + left);
+        left -= to - at;
+        it.first = q.first, it.seq = s, it.kv_head = kv_head, it.row0 = rb * kBlockRows, it.rows = min(kBlockRows, q.rows - it.row0);
+        it.t0 = (int)max(at - kCost, (int64_t)0), it.t1 = (int)max(to - kCost, (int64_t)0), it.T = T;
+        it.own = q.len - q.n, it.end = q.end(p, rb), it.len = q.len;
+        return it;
+    }
+    __device__ void next(const AttnParams &p)
+    {
+        unit += T + kCost;
+        at = 0;
         if (left <= 0)
-            return false;
-        unit += T;
-        t0 = 0;
+            return;
         if (++rb == q.blocks) {
             rb = 0;
             if (++kv_head == p.Hk) {
                 kv_head = 0;
                 do {
                     if (++s >= p.n_seq)
-                        return false;
+                        return;
                     q.load(p, s);
                 } while (q.n == 0);
             }
         }
-        tiles(p);
-        return true;
+        T = q.tiles(p, rb);
     }
-    __device__ int row0() const { return rb * kBlockRows; }
-    __device__ int rows() const { return min(kBlockRows, q.rows() - row0()); }
-    __device__ bool two() const { return rows() > kTile; }  // both groups on the same tiles of positions
-    __device__ int count(int g) const { return two() ? t1 - t0 : (t1 - t0 + 1 - g) / 2; }  // tiles of a group
-    __device__ int tile(int g, int i) const { return two() ? t0 + i : t0 + 2 * i + g; }
 };
 
-__device__ __forceinline__ int64_t range_begin(int64_t units, int block, int blocks) { return units * block / blocks; }
-
-// The page of position pos and its slot; page -1: not in the cache.
-__device__ __forceinline__ int32_t page_of(const AttnParams &p, int s, int pos, int end)
-{
-    const int32_t pg = pos >= 0 && pos < end ? p.table[s * p.ts + pos / p.page] : -1;
-    return pg >= 0 && pg < p.n_pages ? pg : -1;
-}
+__device__ __forceinline__ int32_t page_of(const AttnParams &p, int pos) { return (int32_t)((uint64_t)(uint32_t)pos * p.page_mul >> p.page_shift); }
 
 // Bits of the 32 positions from `pos` on that token i of the sequence sees (word: its tree, or null).
-__device__ __forceinline__ uint32_t seen32(const AttnParams &p, int own, int i, uint64_t word, int pos)
+__device__ __forceinline__ uint32_t seen32(bool tree, int own, int i, uint64_t word, int pos)
 {
     const int at = pos - own;  // of the first position among the new tokens
     if (at <= -32)
         return ~0u;
-    if (!p.tree) {
+    if (!tree) {
         const int c = i + 1 - at;
         return c >= 32 ? ~0u : c <= 0 ? 0u : (1u << c) - 1;
     }
@@ -241,6 +255,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -249,7 +265,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
                  "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
                  : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem desc], BF16 inputs, FP32 accumulation.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
@@ -314,21 +329,34 @@ __device__ __forceinline__ bool wait_warp(Smem<D> &sm, uint64_t &bar, uint32_t p
     return __all_sync(~0u, wait(sm, bar, parity, p, code));
 }
 
+template <int D>
+__device__ __forceinline__ Item next_item(Smem<D> &sm, int item, const AttnParams &p, int code, bool &ok)
+{
+    ok = ok && wait_warp(sm, sm.item_full[item % kAhead], (uint32_t)(item / kAhead) & 1, p, code);
+    Item it = sm.items[item % kAhead];
+    if (!ok)
+        it.t1 = 0;
+    return it;
+}
+
+// Steps of 16 positions in which tile t of the values is multiplied: as far as something is seen.
+__device__ __forceinline__ int value_steps(const Item &it, int t) { return min(max((it.end - t * kTile + 15) / 16, 1), kTile / 16); }
+
 // ---- producing --------------------------------------------------------------------------------
 
-// Rows of 2 D bytes into a swizzled tile of kTile rows; a warp takes 32 of them, lane l knows row l's
-// source (null: zeros).
+// The rows [64 warp, 64 warp + 64) of a swizzled tile, 2 D bytes each, by 16-byte copies: lane l knows the
+// sources of rows l and 32 + l of them (null: zeros).  `rows`: how many of the tile's are wanted.
 template <int D>
-__device__ __forceinline__ void gather(uint32_t tile, const uint16_t *row, const void *any)
+__device__ __forceinline__ void gather(uint32_t tile, const uint16_t *row0, const uint16_t *row1, int rows, const void *any)
 {
     constexpr int CH = D / 8, RPI = 32 / CH;  // chunks of a row; rows an instruction
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 3, c = lane % CH;
-    const uint64_t mine = reinterpret_cast<uint64_t>(row);
-#pragma unroll
-    for (int i = 0; i < 32 / RPI; ++i) {
-        const int r = i * RPI + lane / CH;
-        const uint64_t src = __shfl_sync(~0u, mine, r);
-        const uint32_t dst = tile + (uint32_t)((c / 8) * kTile * 128 + (32 * warp + r) * 128 + ((c % 8) ^ (r & 7)) * 16);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - 8, c = lane % CH;
+    const int n = min(64, rows - 64 * warp);
+#pragma unroll 2
+    for (int i = 0; i < n; i += RPI) {
+        const int r = i + lane / CH;
+        const uint64_t src = __shfl_sync(~0u, reinterpret_cast<uint64_t>(i < 32 ? row0 : row1), r & 31);
+        const uint32_t dst = tile + (uint32_t)((c / 8) * kTile * 128 + (64 * warp + r) * 128 + ((c % 8) ^ (r & 7)) * 16);
         cp_async16(dst, src ? reinterpret_cast<const uint4 *>(src) + c : any, src != 0);
     }
 }
@@ -338,13 +366,13 @@ template <int D>
 __device__ __forceinline__ bool take_out(uint8_t *tile, int from)
 {
     constexpr int CH = D / 8, RPI = 32 / CH;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 3, c = lane % CH;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - 8, c = lane % CH;
     bool any = false;
-    for (int i = 0; i < 32 / RPI; ++i) {
+    for (int i = max(0, from - 64 * warp) / RPI; i < 64 / RPI; ++i) {
         const int r = i * RPI + lane / CH;
-        if (32 * warp + r < from)
+        if (64 * warp + r < from)
             continue;
-        uint4 *at = reinterpret_cast<uint4 *>(tile + (c / 8) * kTile * 128 + (32 * warp + r) * 128 + ((c % 8) ^ (r & 7)) * 16);
+        uint4 *at = reinterpret_cast<uint4 *>(tile + (c / 8) * kTile * 128 + (64 * warp + r) * 128 + ((c % 8) ^ (r & 7)) * 16);
         uint4 v = *at;
         uint32_t *w = &v.x;
         bool here = false;
@@ -361,28 +389,39 @@ __device__ __forceinline__ bool take_out(uint8_t *tile, int from)
     return any;
 }
 
+// One box of a cache's map: p.box slots of a page and head, 64 channels from c0 on.
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t slot, int32_t head, int32_t page, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(slot), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+
 template <int D>
-__device__ void produce(const AttnParams &p, Smem<D> &sm, Items it)
+__device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kmap, const CUtensorMap &vmap, const Parts &parts)
 {
     using S = Smem<D>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - 8;
     struct Flight {
         int32_t slot, from, item;  // from: first row among the new tokens' values, kTile: nothing to look at
     } fl[kLag + 1];
-    constexpr int kNone = -1, kRows = -2;
+    constexpr int kNone = -1, kRows = -2;  // kRows, kRows - 1: the tiles of rows
 #pragma unroll
     for (auto &f : fl)
         f.slot = kNone;
-    int c = 0, kt = 0, item = 0;
-    const auto land = [&](const Flight &f) {  // what was issued kLag copies ago has arrived
+    int c = 0, kt = 0, item = 0, qc = 0;
+    bool ok = true;
+    const auto land = [&](Flight &f) {  // copies of 16 bytes have arrived
         if (f.slot == kNone)
             return;
         if (f.from < kTile && take_out<D>(sm.ring[f.slot], f.from))
-            sm.odd[f.item & 1] = f.item + 1;
+            sm.odd[f.item % kAhead] = f.item + 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads through the async proxy
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(smem_u32(f.slot == kRows ? &sm.q_full : &sm.full[f.slot]));
+            mbar_arrive(smem_u32(f.slot <= kRows ? &sm.q_full[kRows - f.slot] : &sm.full[f.slot]));
+        f.slot = kNone;
     };
     const auto issued = [&](int slot, int from) {
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -390,250 +429,402 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, Items it)
         for (int i = 0; i < kLag; ++i)
             fl[i] = fl[i + 1];
         fl[kLag] = Flight{slot, from, item};
-        asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-        land(fl[0]);
+        if (fl[0].slot != kNone) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+            land(fl[0]);
+        }
     };
     const auto drain = [&] {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-        for (int i = 1; i <= kLag; ++i) {
+        for (int i = 1; i <= kLag; ++i)
             land(fl[i]);
-            fl[i].slot = kNone;
-        }
     };
-    bool ok = true;
-    do {
-        // The rows.  Their buffers are free once the item before has multiplied them all, the second one
-        // once its sums are joined.
-        drain();  // (the item before ends only with its last copies)
-        if (item > 1)
-            ok = ok && wait_warp(sm, sm.joined[item & 1], (uint32_t)(item - 2) >> 1 & 1, p, DEP_DEV_TIMEOUT_PRODUCER);
-        if (item > 0)
-            ok = ok && wait_warp(sm, sm.q_empty, (uint32_t)(item - 1) & 1, p, DEP_DEV_TIMEOUT_PRODUCER);
-        if (item > 0 && it.two())
-            ok = ok && wait_warp(sm, sm.joined[(item - 1) & 1], (uint32_t)(item - 1) >> 1 & 1, p, DEP_DEV_TIMEOUT_PRODUCER);
-        if (!ok)
+    // What is waited for may itself wait for copies that have not been announced yet.
+    const auto need = [&](uint64_t &bar, uint32_t parity) {
+        if (!ok || __all_sync(~0u, mbar_try_wait(smem_u32(&bar), parity)))
+            return;
+        drain();
+        ok = wait_warp(sm, bar, parity, p, DEP_DEV_TIMEOUT_PRODUCER);
+    };
+    Items list;
+    if (warp == 0)
+        list.start(p, sm.seq, sm.unit0, sm.begin, sm.left);
+    for (;; ++item) {
+        if (warp == 0) {  // tells the others
+            const Item it = list.take(p);
+            if (item >= kAhead)
+                need(sm.done[item % kAhead], (uint32_t)(item / kAhead - 1) & 1);
+            if (lane == 0) {
+                sm.items[item % kAhead] = it;
+                if (ok && it.t0 == 0 && it.t1 > 0 && it.t1 < it.T) {  // goes on in the blocks that follow
+                    int last = blockIdx.x + 1;
+                    while (parts.begin(last + 1) < list.unit + it.T + kCost)
+                        ++last;
+                    p.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, it.kv_head, it.row0, it.rows, it.first, {0, 0}};
+                }
+                mbar_arrive(smem_u32(&sm.item_full[item % kAhead]));
+            }
+            __syncwarp();
+        } else
+            need(sm.item_full[item % kAhead], (uint32_t)(item / kAhead) & 1);
+        const Item it = sm.items[item % kAhead];
+        if (!ok || it.t1 == 0)
             break;
-        for (int h = 0; h < (it.two() ? 2 : 1); ++h) {
-            const int r = kTile * h + 32 * warp + lane, row = it.row0() + r;
-            const uint16_t *src = r < it.rows() ? p.q + (it.q.first + row / it.q.G) * p.qs + (it.kv_head * it.q.G + row % it.q.G) * D : nullptr;
-            gather<D>(smem_u32(sm.q[h]), src, p.q);
-        }
-        issued(kRows, kTile);
-
-        const int n = it.t1 - it.t0, own = it.q.own(), end = p.tree ? it.q.len - max(0, it.q.n - kTreeMost) : it.q.len;
         const bool two = it.two();
+        // Pages of this warp's 64 rows of a tile: rows `lane` and 32 + lane of them, as the table has them.  Looked up a
+        // tile ahead; the values of a tile come after the keys of the next where the groups take turns.
+        struct Pages {
+            int32_t a, b;
+        } ahead, now{-1, -1}, before{-1, -1};
+        const int32_t *const table = p.table + it.seq * p.ts;
+        const auto look = [&](int t) {
+            const int pos = t * kTile + 64 * warp + lane;
+            return Pages{pos < it.end ? table[page_of(p, pos)] : -1, pos + 32 < it.end ? table[page_of(p, pos + 32)] : -1};
+        };
+        ahead = look(it.t0);
+        for (int h = 0; h < (two ? 2 : 1); ++h, ++qc) {
+            need(sm.q_empty[qc & 1], ((uint32_t)(qc >> 1) & 1) ^ 1);
+            if (!ok)
+                break;
+            const uint16_t *src[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = kTile * h + 64 * warp + 32 * i + lane;
+                const uint32_t row = it.row0 + r, tok = row / (uint32_t)p.G;
+                src[i] = r < it.rows ? p.q + (it.first + tok) * p.qs + (int32_t)(it.kv_head * p.G + (row - tok * p.G)) * D : nullptr;
+            }
+            gather<D>(smem_u32(sm.q[qc & 1]), src[0], src[1], it.rows - kTile * h, p.q);  // (the tile's other rows are nobody's)
+            issued(kRows - (qc & 1), kTile);
+        }
         const auto load = [&](int t, bool values) {
-            const int pos = t * kTile + 32 * warp + lane;
-            const int32_t pg = page_of(p, it.s, pos, end);
+            if (!values) {
+                before = now;
+                now.a = (uint32_t)ahead.a < (uint32_t)p.n_pages ? ahead.a : -1;
+                now.b = (uint32_t)ahead.b < (uint32_t)p.n_pages ? ahead.b : -1;
+                if (t + 1 < it.t1)
+                    ahead = look(t + 1);
+            }
+            const Pages pg = values && !two && t + 1 < it.t1 ? before : now;
             const int slot = c % S::kSlots;
-            ok = ok && wait_warp(sm, sm.empty[slot], ((uint32_t)(c / S::kSlots) & 1) ^ 1, p, DEP_DEV_TIMEOUT_PRODUCER);
+            need(sm.empty[slot], ((uint32_t)(c / S::kSlots) & 1) ^ 1);
             if (!ok)
                 return;
-            const int at = pos % p.page;
-            const uint16_t *src = nullptr;
-            if (pg >= 0)
-                src = values ? p.vc + pg * p.vps + at * p.vss + it.kv_head * p.vhs : p.kc + pg * p.kps + at * p.kss + it.kv_head * p.khs;
             if (!values) {
-                const uint32_t in = __ballot_sync(~0u, pg >= 0);
+                const uint32_t a = __ballot_sync(~0u, pg.a >= 0), b = __ballot_sync(~0u, pg.b >= 0);
                 if (lane == 0)
-                    sm.masks[kt % kMasks][warp] = in;
+                    *reinterpret_cast<uint2 *>(&sm.masks[kt % kMasks][2 * warp]) = make_uint2(a, b);
                 ++kt;
             }
-            gather<D>(smem_u32(sm.ring[slot]), src, p.q);
-            issued(slot, values && (t + 1) * kTile > own ? max(0, own - t * kTile) : kTile);
+            // Values past the sequence's end have to be zeros, and those of new tokens finite: such tiles come row by row.
+            if (p.box && (!values || (t + 1) * kTile <= min(it.own, it.end))) {
+                const int boxes = max(1, 64 / p.box), b = lane / (D / 64), half = lane % (D / 64);
+                const int r = min(b * p.box, 63), pos = t * kTile + 64 * warp + r;
+                const int32_t pa = __shfl_sync(~0u, pg.a, r & 31), pb = __shfl_sync(~0u, pg.b, r & 31), at = r < 32 ? pa : pb;
+                const uint32_t bar = smem_u32(&sm.full[slot]);
+                const bool mine = warp == 0 || p.box <= 64;
+                if (lane == 0) {
+                    if (mine)
+                        mbar_arrive_expect_tx(bar, (uint32_t)(max(64, p.box) * D * 2));
+                    else
+                        mbar_arrive(bar);
+                }
+                __syncwarp();
+                if (mine && b < boxes)  // (a page outside the pool gives zeros)
+                    tma_load_box(smem_u32(sm.ring[slot]) + (uint32_t)(half * kTile * 128 + (64 * warp + r) * 128), values ? &vmap : &kmap,
+                                 64 * half, pos - page_of(p, pos) * p.page, it.kv_head, at >= 0 ? at : (int32_t)p.n_pages, bar);
+                issued(kNone, kTile);
+            } else {
+                const uint16_t *src[2];
+                const uint16_t *const base = values ? p.vc + it.kv_head * p.vhs : p.kc + it.kv_head * p.khs;
+                const int64_t ps = values ? p.vps : p.kps, ss = values ? p.vss : p.kss;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int32_t g = i ? pg.b : pg.a;
+                    const int pos = t * kTile + 64 * warp + 32 * i + lane, at = pos - page_of(p, pos) * p.page;
+                    src[i] = g < 0 ? nullptr : base + g * ps + at * ss;
+                }
+                // (of the values only what the last product reads)
+                gather<D>(smem_u32(sm.ring[slot]), src[0], src[1], values ? 16 * value_steps(it, t) : kTile, p.q);
+                issued(slot, values && (t + 1) * kTile > it.own ? max(0, it.own - t * kTile) : kTile);
+            }
             ++c;
         };
-        if (two) {
-            for (int t = it.t0; ok && t < it.t1; ++t) {
-                load(t, false);
-                load(t, true);
-            }
-        } else {
-            load(it.t0, false);
-            if (n > 1)
-                load(it.t0 + 1, false);
-            for (int t = it.t0; ok && t < it.t1; ++t) {
-                load(t, true);
-                if (t + 2 < it.t1)
-                    load(t + 2, false);
-            }
+        const int n = it.t1 - it.t0;
+        for (int i = 0; ok && i < 2 * n; ++i) {
+            // In the order of the MMAs: keys, values, keys, ... or, in turns, two tiles' keys first.
+            const bool values = two ? i & 1 : n == 1 ? i == 1 : i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
+            const int t = two ? i / 2 : i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : values ? i / 2 - 1 : (i + 1) / 2;
+            load(it.t0 + t, values);
+            if (item == 0 && i == min(n, 2) - 1)
+                drain();  // (the first rows, at once)
         }
-        ++item;
-    } while (ok && it.next(p));
+        if (warp == 0)
+            list.next(p);
+    }
     drain();
 }
 
-// ---- multiplying (one thread) -----------------------------------------------------------------
+// ---- multiplying (one thread for each group) --------------------------------------------------
 
 template <int D>
-__device__ void multiply(const AttnParams &p, Smem<D> &sm, Items it, uint32_t tmem)
+__device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
 {
     using S = Smem<D>;
     constexpr uint32_t kScores = tc::idesc_bf16_f32(kTile, kTile), kValues = tc::idesc_bf16_f32(kTile, D) | (1u << 16);
-    int c = 0, item = 0, k[2] = {0, 0};  // tiles that each group was given
-    int sk = 0, sv = 0;  // slots of the first group's keys and values, which the second group shares
+    const uint32_t s_at = tmem + g * kTile, o_at = tmem + 2 * kTile + g * D;
+    int slot = 0, item = 0, qc = 0;
+    uint32_t lap = 0, k = 0;  // of the ring; tiles multiplied
     bool ok = true;
-    const auto take = [&] {  // the next slot of the ring, once it is full
-        const int slot = c % S::kSlots;
-        ok = ok && wait(sm, sm.full[slot], (uint32_t)(c / S::kSlots) & 1, p, DEP_DEV_TIMEOUT_MMA);
-        ++c;
-        return slot;
-    };
-    const auto scores = [&](int g, int slot, bool two) {
-        uint32_t acc = 0;
-        tc::mma_steps<D / 16, kTile * 128, kTile * 128>(tmem + g * kTile, tc::desc_sw128(smem_u32(sm.q[two ? g : 0])),
-                                                        tc::desc_sw128(smem_u32(sm.ring[slot])), kScores, acc);
-        tc::commit(smem_u32(&sm.s_full[g]));
-    };
-    const auto sums = [&](int g, int slot, bool first) {
-        ok = ok && wait(sm, sm.p_full[g], (uint32_t)k[g] & 1, p, DEP_DEV_TIMEOUT_MMA);
-        if (!ok)
-            return;
-        ++k[g];
-        tc::fence_after();
-        const uint64_t v = desc_values(smem_u32(sm.ring[slot]));
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-            mma_bf16_ta(tmem + 2 * kTile + g * D, tmem + g * kTile + 8 * i, v + (uint64_t)(i * 2048 >> 4), kValues, !(first && i == 0));
-    };
-    const auto release = [&](int slot) { tc::commit(smem_u32(&sm.empty[slot])); };
-    do {
-        const bool two = it.two();
-        const int n[2] = {it.count(0), it.count(1)};
-        ok = ok && wait(sm, sm.q_full, (uint32_t)item & 1, p, DEP_DEV_TIMEOUT_MMA);
-        if (!ok)
+    for (;; ++item) {
+        ok = ok && wait(sm, sm.item_full[item % kAhead], (uint32_t)(item / kAhead) & 1, p, DEP_DEV_TIMEOUT_MMA);
+        const Item it = sm.items[item % kAhead];
+        if (!ok || it.t1 == 0)
             break;
-        tc::fence_after();
-        for (int i = -1; ok && i < n[0]; ++i)
-            for (int g = 0; ok && g < 2; ++g) {
-                if (i >= 0 && i < n[g]) {
-                    const int slot_v = two && g == 1 ? sv : take();
-                    if (!ok)
-                        break;
-                    sums(g, slot_v, i == 0);
-                    if (!ok)
-                        break;
-                    sv = slot_v;
-                    if (!two || g == 1)
-                        release(slot_v);
-                    if (i + 1 == n[g])
-                        tc::commit(smem_u32(&sm.o_full[g]));
-                }
-                if (i + 1 < n[g]) {
-                    const int slot_k = two && g == 1 ? sk : take();
-                    if (!ok)
-                        break;
-                    tc::fence_after();
-                    scores(g, slot_k, two);
-                    sk = slot_k;
-                    if (!two || g == 1)
-                        release(slot_k);
-                }
+        const bool two = it.two();
+        const int n = it.t1 - it.t0;
+        // (both tiles of rows, also the other group's: the release below counts on it)
+        for (int h = 0; h < (two ? 2 : 1); ++h)
+            ok = ok && wait(sm, sm.q_full[(qc + h) & 1], (uint32_t)((qc + h) >> 1) & 1, p, DEP_DEV_TIMEOUT_MMA);
+        const uint64_t rows = tc::desc_sw128(smem_u32(sm.q[two ? (qc + g) & 1 : qc & 1]));
+        int last = two ? n - 1 : n - 1 - ((n - 1 - g) & 1);  // this group's last tile
+        uint32_t acc = 0;
+        for (int i = 0; ok && i < 2 * n; ++i) {
+            const bool values = two ? i & 1 : n == 1 ? i == 1 : i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
+            const int t = two ? i / 2 : i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : values ? i / 2 - 1 : (i + 1) / 2;
+            ok = wait(sm, sm.full[slot], lap, p, DEP_DEV_TIMEOUT_MMA);
+            if (!ok)
+                break;
+            const uint32_t at = smem_u32(sm.ring[slot]), freed = smem_u32(&sm.empty[slot]);
+            if (!two && (t & 1) != g)
+                mbar_arrive(freed);  // the other group's
+            else if (values) {
+                ok = wait(sm, sm.p_full[g], k & 1, p, DEP_DEV_TIMEOUT_MMA);
+                if (!ok)
+                    break;
+                ++k;
+                tc::fence_after();
+                const uint64_t v = desc_values(at);
+                const int steps = value_steps(it, it.t0 + t);
+                if (steps == kTile / 16) {
+#pragma unroll
+                    for (int j = 0; j < kTile / 16; ++j) {
+                        mma_bf16_ta(o_at, s_at + 8 * j, v + (uint64_t)(j * 2048 >> 4), kValues, acc);
+                        acc = 1;
+                    }
+                } else
+#pragma unroll 1
+                    for (int j = 0; j < steps; ++j) {
+                        mma_bf16_ta(o_at, s_at + 8 * j, v + (uint64_t)(j * 2048 >> 4), kValues, acc);
+                        acc = 1;
+                    }
+                tc::commit(freed);
+                if (t == last)
+                    tc::commit(smem_u32(&sm.o_full[g]));
+            } else {
+                tc::fence_after();
+                uint32_t first = 0;
+                tc::mma_steps<D / 16, kTile * 128, kTile * 128>(s_at, rows, tc::desc_sw128(at), kScores, first);
+                tc::commit(smem_u32(&sm.s_full[g]));
+                tc::commit(freed);
             }
-        tc::commit(smem_u32(&sm.q_empty));
-        ++item;
-    } while (ok && it.next(p));
+            if (++slot == S::kSlots)
+                slot = 0, lap ^= 1;
+        }
+        for (int h = 0; h < (two ? 2 : 1); ++h, ++qc)
+            tc::commit(smem_u32(&sm.q_empty[qc & 1]));
+    }
     if (!ok) {  // what is in flight ends before the tensor memory is given back
-        tc::commit(smem_u32(&sm.drained));
-        mbar_wait(smem_u32(&sm.drained), 0, kWaitNs);
+        tc::commit(smem_u32(&sm.drained[g]));
+        mbar_wait(smem_u32(&sm.drained[g]), 0, kWaitNs);
     }
 }
 
 // ---- softmax ----------------------------------------------------------------------------------
 
-template <int D>
-__device__ void soften(const AttnParams &p, Smem<D> &sm, Items it, uint32_t tmem, int64_t units, int blocks)
+// Largest of three; NaNs do not count.
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    const int g = threadIdx.x / kTile, r = threadIdx.x % kTile, warp = r / 32, lane = r % 32;
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16, s_at = tmem + lanes + g * kTile, o_at = tmem + lanes + 2 * kTile + g * D;
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t both(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(uint64_t r, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// p = exp2(c s + off) of the row's scores of a tile in BF16 pairs, their sum and the largest score.
+__device__ __forceinline__ void tile_exp(uint32_t s_at, float c, float off, uint32_t (&pk)[2][32], float &top, float &sum)
+{
+    float t[2] = {-INFINITY, -INFINITY};
+    const uint64_t c2 = both(c, c), off2 = both(off, off);
+    uint64_t s2[2] = {0, 0};
+    uint32_t v[2][16];
+    tc::ld16(s_at, v[0]);
+#pragma unroll
+    for (int w = 0; w < kTile / 16; ++w) {
+        tc::wait_ld();
+        if (w + 1 < kTile / 16)
+            tc::ld16(s_at + 16 * (w + 1), v[(w + 1) & 1]);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const float a = __uint_as_float(v[w & 1][j]), b = __uint_as_float(v[w & 1][j + 1]);
+            float x, y;
+            apart(fma2(both(a, b), c2, off2), x, y);
+            x = ex2(x), y = ex2(y);
+            t[j / 2 & 1] = max3(t[j / 2 & 1], a, b);
+            s2[j / 2 & 1] = add2(s2[j / 2 & 1], both(x, y));
+            pk[w / 4][8 * (w & 3) + j / 2] = pack16(x, y);
+        }
+    }
+    top = fmaxf(t[0], t[1]);
+    float x, y;
+    apart(add2(s2[0], s2[1]), x, y);
+    sum = x + y;
+}
+
+// Adds the values of new tokens that are not finite, which were left out of the product (it would have
+// given them to every row), to the channels of a row that sees them.  FP32 or BF16 in `row`.
+template <int D>
+__device__ __noinline__ void add_odd(const AttnParams &p, const Item &it, int tok, uint64_t word, uint16_t *out, float *part)
+{
+    for (int pos = max(max(it.own, it.t0 * kTile), 0); pos < min(it.t1 * kTile, it.end); ++pos) {
+        if (!(seen32(p.tree != nullptr, it.own, tok, word, pos) & 1))
+            continue;
+        const int32_t pi = page_of(p, pos), pg = p.table[it.seq * p.ts + pi];
+        if (pg < 0 || pg >= p.n_pages)
+            continue;
+        const uint16_t *src = p.vc + pg * p.vps + (pos - pi * p.page) * p.vss + it.kv_head * p.vhs;
+        for (int d = 0; d < D; ++d) {
+            const float v = __uint_as_float((uint32_t)src[d] << 16);
+            if (isfinite(v))
+                continue;
+            if (part)
+                part[d] += v;
+            else
+                out[d] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float((uint32_t)out[d] << 16) + v));
+        }
+    }
+}
+
+template <int D>
+__device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
+{
+    const int g = threadIdx.x / kTile, r = threadIdx.x % kTile, lane = r % 32;
+    const uint32_t lanes = (uint32_t)(r - lane) << 16, s_at = tmem + lanes + g * kTile, o_at = tmem + lanes + 2 * kTile + g * D;
     const float c = p.scale * 1.4426950408889634f;  // log2(e)
-    int k = 0, kt = 0, item = 0, done = 0, x = 0;  // x: exchanges between the groups
-    bool ok = true;
-    do {
+    const bool tree = p.tree != nullptr;
+    int kt = 0, item = 0;
+    uint32_t k = 0, items = 0, x = 0;  // tiles; items with tiles; exchanges between the groups
+    bool ok = true, lent = false;      // lent: the first group may still read this one's sums
+    for (;; ++item) {
+        const Item it = next_item(sm, item, p, DEP_DEV_TIMEOUT_CONSUMER, ok);
+        if (it.t1 == 0)
+            break;
         const bool two = it.two();
-        const int n = it.count(g), at = two ? g * kTile + r : r;
-        const bool live = at < it.rows(), warp_live = at - lane < it.rows();
-        const int row = it.row0() + at, tok = live ? row / it.q.G : 0, own = it.q.own();
-        const int64_t token = it.q.first + tok;
-        const uint64_t word = p.tree && live ? p.tree[token] : 0;
+        const int at = two ? g * kTile + r : r;
+        const bool live = at < it.rows, warp_live = at - lane < it.rows;
+        const uint32_t row = it.row0 + at;
+        const int tok = live ? (int)(row / (uint32_t)p.G) : 0, head = it.kv_head * p.G + (int)(row - tok * p.G);
+        const int64_t token = it.first + tok;
+        const uint64_t word = tree && live ? p.tree[token] : 0;
+        const int clear = it.own + (tree ? 0 : __shfl_sync(~0u, tok, 0) + 1);  // all positions before it are seen by all of the warp's rows
         float m = -INFINITY, l = 0.0f;  // m: log2 units
-        if (item > 1)  // (a group without tiles does not run ahead)
-            ok = wait_warp(sm, sm.joined[item & 1], (uint32_t)(item - 2) >> 1 & 1, p, DEP_DEV_TIMEOUT_CONSUMER);
-        for (int i = 0; ok && i < n; ++i, ++k) {
-            const int t = it.tile(g, i);
-            ok = wait_warp(sm, sm.s_full[g], (uint32_t)k & 1, p, DEP_DEV_TIMEOUT_CONSUMER);
+        int t = it.t0 + (two ? 0 : g);
+        const bool some = t < it.t1;
+        for (bool first = true; t < it.t1; t += two ? 1 : 2, first = false, ++k) {
+            ok = ok && wait_warp(sm, sm.s_full[g], k & 1, p, DEP_DEV_TIMEOUT_CONSUMER);
             if (!ok)
                 break;
             tc::fence_after();
             if (warp_live) {
-                // What the row sees of the tile.
-                const uint32_t *in = sm.masks[(kt + (t - it.t0)) % kMasks];
-                uint32_t see[4];
-                bool all = true;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    see[w] = in[w] & seen32(p, own, tok, word, t * kTile + 32 * w);
-                    all = all && see[w] == ~0u;
-                }
-                const bool masked = __any_sync(~0u, !all);
-                float top = -INFINITY;
-                uint32_t v[32];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    tmem_ld32(s_at + 32 * w, v);
-                    tc::wait_ld();
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            top = fmaxf(top, see[w] >> j & 1 ? __uint_as_float(v[j]) : -INFINITY);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            top = fmaxf(top, __uint_as_float(v[j]));
+                const uint4 in = *reinterpret_cast<const uint4 *>(sm.masks[(kt + (t - it.t0)) % kMasks]);
+                // The maximum that is taken off moves only where it has risen by 2^8: P stays below 2^8, O is
+                // seldom scaled, and P is worked out with the maximum found so far, anew if that has to move.
+                bool anew = first || (t + 1) * kTile > clear || (in.x & in.y & in.z & in.w) != ~0u;
+                if (!anew) {
+                    uint32_t pk[2][32];
+                    float top, sum;
+                    tile_exp(s_at, c, m == -INFINITY ? 0.0f : -m, pk, top, sum);
+                    const float tm = top * c;
+                    anew = __any_sync(~0u, live && (tm > m + 8.0f || (m == -INFINITY && tm > -INFINITY)));
+                    if (!anew) {
+                        l += sum;
+                        tmem_st32(s_at, pk[0]);
+                        tmem_st32(s_at + 32, pk[1]);
                     }
                 }
-                // The maximum that is taken off moves only where it has risen by 2^8: P stays below 2^8, and
-                // O is seldom scaled.
-                const float tm = top * c;
-                const bool up = tm > m + 8.0f || (m == -INFINITY && tm > -INFINITY);
-                if (__any_sync(~0u, up)) {
-                    const float f = up ? ex2(m - tm) : 1.0f;
-                    if (up)
-                        m = tm;
-                    l *= f;
-                    if (i > 0)  // (the product before is done: this tile's scores came after it)
+                if (anew) {  // with what the row sees; rolled up, since it is seldom run: its fetching costs more than its running
+                    const uint32_t *mask = sm.masks[(kt + (t - it.t0)) % kMasks];
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t v[32];
+                        tmem_ld32(s_at + 32 * w, v);
+                        const uint32_t see = mask[w] & seen32(tree, it.own, tok, word, t * kTile + 32 * w);
+                        tc::wait_ld();
 #pragma unroll
-                        for (int w = 0; w < D / 32; ++w) {
-                            tmem_ld32(o_at + 32 * w, v);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-                            tmem_st32(o_at + 32 * w, v);
-                        }
-                }
-                const float off = m == -INFINITY ? 0.0f : -m;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    tmem_ld32(s_at + 32 * w, v);
-                    tc::wait_ld();
-                    uint32_t pk[16];
-                    float add = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float a = ex2(fmaf(__uint_as_float(v[j]), c, off)), b = ex2(fmaf(__uint_as_float(v[j + 1]), c, off));
-                        if (masked) {
-                            a = see[w] >> j & 1 ? a : 0.0f;
-                            b = see[w] >> (j + 1) & 1 ? b : 0.0f;
-                        }
-                        add += a + b;
-                        pk[j / 2] = pack16(a, b);
+                        for (int j = 0; j < 32; ++j)
+                            top = fmaxf(top, see >> j & 1 ? __uint_as_float(v[j]) : -INFINITY);
                     }
-                    l += add;
-                    tmem_st16(s_at + 16 * w, pk);
+                    const float tm = top * c;
+                    const bool up = live && (tm > m + 8.0f || (m == -INFINITY && tm > -INFINITY));
+                    if (__any_sync(~0u, up)) {
+                        const float f = up ? ex2(m - tm) : 1.0f;
+                        if (up)
+                            m = tm;
+                        l *= f;
+                        if (!first)  // (the product before is done: this tile's scores came after it)
+#pragma unroll 1
+                            for (int w = 0; w < D / 16; ++w) {
+                                uint32_t v[16];
+                                tc::ld16(o_at + 16 * w, v);
+                                tc::wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                                tmem_st16(o_at + 16 * w, v);
+                            }
+                    }
+                    const float off = m == -INFINITY ? 0.0f : -m;
+#pragma unroll 1
+                    for (int w = 0; w < 4; ++w) {  // (P's columns lie in those of scores already read)
+                        uint32_t v[32], pk[16];
+                        tmem_ld32(s_at + 32 * w, v);
+                        const uint32_t see = mask[w] & seen32(tree, it.own, tok, word, t * kTile + 32 * w);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float a = ex2(fmaf(__uint_as_float(v[j]), c, off)), b = ex2(fmaf(__uint_as_float(v[j + 1]), c, off));
+                            a = see >> j & 1 ? a : 0.0f;
+                            b = see >> (j + 1) & 1 ? b : 0.0f;
+                            l += a + b;
+                            pk[j / 2] = pack16(a, b);
+                        }
+                        tmem_st16(s_at + 16 * w, pk);
+                    }
                 }
                 tmem_wait_st();
+            }
+            if (lent) {
+                ok = wait_warp(sm, sm.x_free, (x - 1) & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
+                lent = false;
             }
             tc::fence_before();
             __syncwarp();
@@ -641,133 +832,104 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, Items it, uint32_t tmem
                 mbar_arrive(smem_u32(&sm.p_full[g]));
         }
         kt += it.t1 - it.t0;
-        if (ok && n > 0) {
-            ok = wait_warp(sm, sm.o_full[g], (uint32_t)done & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
-            ++done;
+        if (some) {
+            ok = ok && wait_warp(sm, sm.o_full[g], items & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
+            ++items;
             tc::fence_after();
+        }
+        // Without a second tile of rows the first group joins the groups' sums: a warp reads the second group's in its
+        // own lanes of the tensor memory.
+        const bool join = !two && it.t1 - it.t0 > 1;
+        float f_own = 1.0f, f_other = 0.0f;
+        if (join && ok) {
+            if (g == 1) {
+                if (lent)
+                    ok = wait_warp(sm, sm.x_free, (x - 1) & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
+                sm.ml[r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm.x_full));
+                lent = true;
+            } else {
+                ok = wait_warp(sm, sm.x_full, x & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
+                tc::fence_after();
+                const float2 other = sm.ml[r];
+                const float top = fmaxf(m, other.x);
+                f_own = m == top ? 1.0f : ex2(m - top);
+                f_other = other.x == top ? 1.0f : ex2(other.x - top);
+                l = l * f_own + other.y * f_other;
+                m = top;
+            }
+            ++x;
         }
         if (!ok)
             break;
-        // Without a second tile of rows the groups' sums are joined: the second group's through shared memory.
-        const bool join = !two && it.count(1) > 0;
-        float *const scratch = reinterpret_cast<float *>(sm.q[1]);  // [D / 2][kTile]
-        float f_own = 1.0f, f_other = 0.0f;
-        const bool stores = two || g == 0;
-        const bool whole = it.t0 == 0 && it.t1 == it.T;
-        const int64_t part = ((int64_t)blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * p.part_rows + at;
-        float inv = 1.0f;
-        uint16_t *const out = p.o + token * p.os + (it.kv_head * it.q.G + row % it.q.G) * (int64_t)D;
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            __syncwarp();
-            if (join && w % (D / 64) == 0) {  // half of the channels at once
-                if (g == 1) {
-                    ok = ok && wait_warp(sm, sm.x_free, ((uint32_t)x & 1) ^ 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
-                    if (ok && warp_live) {
-                        sm.ml[0][r] = m;
-                        sm.ml[1][r] = l;
-#pragma unroll
-                        for (int u = w; u < w + D / 64; ++u) {
-                            uint32_t v[32];
-                            tmem_ld32(o_at + 32 * u, v);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                scratch[(32 * (u - w) + j) * kTile + r] = __uint_as_float(v[j]);
-                        }
-                    }
+        if (two || g == 0) {
+            const bool whole = it.whole();
+            const int64_t part = ((int64_t)blockIdx.x * 2 + (it.t0 > 0 ? 0 : 1)) * p.part_rows + at;
+            uint16_t *const out = p.o + token * p.os + (int64_t)head * D;
+            float *const rest = p.parts + part * D;
+            const float inv = l == 0.0f ? 0.0f : whole ? 1.0f / l : 1.0f;
+            f_own *= inv;
+            f_other *= inv;
+            if (warp_live)
+#pragma unroll 1
+                for (int w = 0; w < D / 16; ++w) {
+                    uint32_t v[16], u[16];
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_u32(&sm.x_full));
-                } else {
-                    ok = ok && wait_warp(sm, sm.x_full, (uint32_t)x & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
-                }
-                ++x;
-            }
-            if (w == 0 && stores) {
-                if (join) {
-                    const float m1 = sm.ml[0][r], l1 = sm.ml[1][r], top = fmaxf(m, m1);
-                    f_own = m == top ? 1.0f : ex2(m - top);
-                    f_other = m1 == top ? 1.0f : ex2(m1 - top);
-                    l = l * f_own + l1 * f_other;
-                    m = top;
-                }
-                if (whole)
-                    inv = l == 0.0f ? 0.0f : 1.0f / l;
-            }
-            if (!stores)
-                continue;
-            uint32_t v[32];
-            tmem_ld32(o_at + 32 * w, v);
-            tc::wait_ld();
-            float y[32];
+                    tc::ld16(o_at + 16 * w, v);
+                    if (join)
+                        tc::ld16(o_at + D + 16 * w, u);
+                    tc::wait_ld();
+                    float y[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                y[j] = __uint_as_float(v[j]);
-                if (join)
-                    y[j] = y[j] * f_own + scratch[(32 * (w % (D / 64)) + j) * kTile + r] * f_other;
-                y[j] *= inv;
-            }
-            if (join && (w + 1) % (D / 64) == 0) {
+                    for (int j = 0; j < 16; ++j) {
+                        y[j] = __uint_as_float(v[j]) * f_own;
+                        if (join)
+                            y[j] = fmaf(__uint_as_float(u[j]), f_other, y[j]);
+                        if (l == 0.0f)
+                            y[j] = 0.0f;
+                    }
+                    if (!live)
+                        continue;
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8)
+                            *reinterpret_cast<uint4 *>(out + 16 * w + j) = make_uint4(pack16(y[j], y[j + 1]), pack16(y[j + 2], y[j + 3]),
+                                                                                      pack16(y[j + 4], y[j + 5]), pack16(y[j + 6], y[j + 7]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<float4 *>(rest + 16 * w + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                    }
+                }
+            if (join) {
+                tc::fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sm.x_free));
             }
-            if (l == 0.0f)
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    y[j] = 0.0f;
-            // (both groups' tiles have arrived by now)
-            if (*reinterpret_cast<volatile int32_t *>(&sm.odd[item & 1]) == item + 1 && live) {
-                // Values that are not finite were left out of the product, which would have given them to every row.
-                for (int pos = max(max(own, it.t0 * kTile), 0); pos < min(it.t1 * kTile, it.q.len); ++pos) {
-                    const int32_t pg = seen32(p, own, tok, word, pos) & 1 ? page_of(p, it.s, pos, it.q.len) : -1;
-                    if (pg < 0)
-                        continue;
-                    const uint16_t *src = p.vc + pg * p.vps + pos % p.page * p.vss + it.kv_head * p.vhs + 32 * w;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if ((src[j] & 0x7F80u) == 0x7F80u)
-                            y[j] += __uint_as_float((uint32_t)src[j] << 16);
-                }
+            if (live) {
+                if (*reinterpret_cast<volatile int32_t *>(&sm.odd[item % kAhead]) == item + 1)
+                    add_odd<D>(p, it, tok, word, out, whole ? nullptr : rest);
+                if (!whole)
+                    p.part_ml[part] = make_float2(m, l);
+                else if (p.lse)
+                    p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             }
-            if (!live)
-                continue;
-            if (whole) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 8)
-                    *reinterpret_cast<uint4 *>(out + 32 * w + j) = make_uint4(pack16(y[j], y[j + 1]), pack16(y[j + 2], y[j + 3]),
-                                                                              pack16(y[j + 4], y[j + 5]), pack16(y[j + 6], y[j + 7]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4 *>(p.parts + part * D + 32 * w + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-            }
-        }
-        if (stores && live) {
-            if (!whole)
-                p.part_ml[part] = make_float2(m, l);
-            else if (p.lse)
-                p.lse[token * p.Hq + it.kv_head * it.q.G + row % it.q.G] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-        }
-        if (threadIdx.x == 0 && it.t0 == 0 && it.t1 < it.T) {  // the item goes on in the blocks that follow
-            int last = blockIdx.x + 1;
-            while (range_begin(units, last + 1, blocks) < it.unit + it.T)
-                ++last;
-            p.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, it.s, it.kv_head, it.row0(), it.rows(), {0, 0, 0}};
         }
         tc::fence_before();
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(smem_u32(&sm.joined[item & 1]));
-        ++item;
-    } while (ok && it.next(p));
+            mbar_arrive(smem_u32(&sm.done[item % kAhead]));
+    }
 }
 
 // ---- the kernels ------------------------------------------------------------------------------
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                                                               const __grid_constant__ CUtensorMap vmap)
 {
     using S = Smem<D>;
     extern __shared__ uint8_t raw[];
@@ -780,33 +942,37 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
-            mbar_init(smem_u32(&sm.full[i]), kProducers / 32);
-            mbar_init(smem_u32(&sm.empty[i]), 1);
+            mbar_init(smem_u32(&sm.full[i]), kProducers);
+            mbar_init(smem_u32(&sm.empty[i]), 2);
         }
-        mbar_init(smem_u32(&sm.q_full), kProducers / 32);
-        mbar_init(smem_u32(&sm.q_empty), 1);
-        mbar_init(smem_u32(&sm.x_full), 4);
-        mbar_init(smem_u32(&sm.x_free), 4);
-        mbar_init(smem_u32(&sm.drained), 1);
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(smem_u32(&sm.item_full[i]), 1);
+            mbar_init(smem_u32(&sm.done[i]), 8);
+            sm.odd[i] = 0;
+        }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(smem_u32(&sm.joined[g]), 8);
+            mbar_init(smem_u32(&sm.q_full[g]), kProducers);
+            mbar_init(smem_u32(&sm.q_empty[g]), 2);
             mbar_init(smem_u32(&sm.s_full[g]), 1);
             mbar_init(smem_u32(&sm.p_full[g]), 4);
             mbar_init(smem_u32(&sm.o_full[g]), 1);
+            mbar_init(smem_u32(&sm.drained[g]), 1);
         }
+        mbar_init(smem_u32(&sm.x_full), 4);
+        mbar_init(smem_u32(&sm.x_free), 4);
         fence_mbar_init();
         sm.dead = 0;
-        sm.odd[0] = sm.odd[1] = 0;
         sm.left = 0;
         p.cuts[blockIdx.x].parts = 0;
     }
     // The range.  Every thread adds up the units of its share of the sequences.
     const int per = (p.n_seq + kThreads - 1) / kThreads, s0 = min(p.n_seq, (int)threadIdx.x * per), s1 = min(p.n_seq, s0 + per);
     int64_t mine = 0;
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
         Seq q;
         q.load(p, s);
-        mine += q.units(p);
+        mine += q.head_units(p) * p.Hk;
     }
     int64_t before = mine;  // of the warp's lanes up to this one
 #pragma unroll
@@ -822,39 +988,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     int64_t units = 0;
     before -= mine;
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp)
-            before += sm.scan[w];
-        units += sm.scan[w];
+        const int64_t x = sm.scan[w];
+        before += w < warp ? x : 0;
+        units += x;
     }
-    // At least kLeast tiles a block: fewer are not worth the joining.
-    const int blocks = (int)min((int64_t)gridDim.x, max((int64_t)1, units / kLeast));
-    const int64_t begin = range_begin(units, blockIdx.x, blocks), end = range_begin(units, blockIdx.x + 1, blocks);
+    const int blocks = (int)min((int64_t)gridDim.x, max((int64_t)1, divide(units, kLeast)));
+    const Parts parts(units, blocks);
+    const int64_t begin = parts.begin(blockIdx.x), end = parts.begin(blockIdx.x + 1);
     if ((int)blockIdx.x < blocks && begin < end && begin >= before && begin < before + mine) {
         int s = s0;
-        for (;; ++s) {
+#pragma unroll 1
+        for (; s + 1 < s1; ++s) {
             Seq q;
             q.load(p, s);
-            const int64_t u = q.units(p);
+            const int64_t u = q.head_units(p) * p.Hk;
             if (begin < before + u)
                 break;
             before += u;
         }
         sm.seq = s;
         sm.unit0 = before;
+        sm.begin = begin;
         sm.left = end - begin;
     }
     __syncthreads();
     const uint32_t tmem = sm.tmem;
     if (sm.left > 0) {
-        Items it;
-        it.start(p, sm.seq, sm.unit0, begin, sm.left);
         if (warp < 8)
-            soften(p, sm, it, tmem, units, blocks);
-        else if (warp < 12)
-            produce(p, sm, it);
-        else if (lane == 0) {
-            multiply(p, sm, it, tmem);
-        }
+            soften(p, sm, tmem);
+        else if (warp < 8 + kProducers)
+            produce(p, sm, kmap, vmap, parts);
+        else if (lane == 0)
+            multiply(p, sm, tmem, warp - 8 - kProducers);
     }
     __syncwarp();
     tc::fence_before();
@@ -872,43 +1037,58 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
     griddep_wait();
     constexpr int E = D / 32;
     const Cut cut = p.cuts[blockIdx.x];
-    if (cut.parts == 0)
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + threadIdx.x / 32;
+    if (cut.parts == 0 || r >= cut.rows)
         return;
-    const int lane = threadIdx.x & 31;
-    const int64_t first = seq_start(p, cut.seq);
-    const int G = p.Hq / p.Hk;
-    for (int r = blockIdx.y * 8 + threadIdx.x / 32; r < cut.rows; r += 8 * gridDim.y) {
-        const auto at = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + r; };
-        float m = -INFINITY;
-        for (int i = lane; i < cut.parts; i += 32)
-            m = fmaxf(m, p.part_ml[at(i)].x);
+    const auto at = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + r; };
+    // Lane j: the j-th of 32 parts at once.
+    float m = -INFINITY;
+    for (int i = lane; i < cut.parts; i += 32)
+        m = fmaxf(m, p.part_ml[at(i)].x);
 #pragma unroll
-        for (int d = 16; d; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        float l = 0.0f, o[E] = {};
-        for (int i = 0; i < cut.parts; ++i) {
-            const float2 ml = p.part_ml[at(i)];
-            const float f = ml.x == m ? 1.0f : ex2(ml.x - m);
+    for (int d = 16; d; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    float l = 0.0f, o[E] = {};
+    for (int i0 = 0; i0 < cut.parts; i0 += 32) {
+        float f = 0.0f;
+        if (i0 + lane < cut.parts) {
+            const float2 ml = p.part_ml[at(i0 + lane)];
+            f = ml.x == m ? 1.0f : ex2(ml.x - m);
             l = fmaf(ml.y, f, l);
-            const float *src = p.parts + at(i) * D + lane * E;
+        }
+        const int n = min(32, cut.parts - i0);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(~0u, f, i);
+            const float *src = p.parts + at(i0 + i) * D + lane * E;
+            float v[E];
+            if (E == 4)
+                *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src);
+            else
+                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                o[e] = fmaf(src[e], f, o[e]);
+                o[e] = fmaf(v[e], w, o[e]);
         }
-        const int row = cut.row0 + r, h = cut.kv_head * G + row % G;
-        const int64_t token = first + row / G;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint32_t w[E / 2];
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            w[e / 2] = l == 0.0f ? 0u : pack16(o[e] * inv, o[e + 1] * inv);
-        uint32_t *out = reinterpret_cast<uint32_t *>(p.o + token * p.os + (int64_t)h * D) + lane * (E / 2);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e)
-            out[e] = w[e];
-        if (p.lse && lane == 0)
-            p.lse[token * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        l += __shfl_xor_sync(~0u, l, d);
+    const uint32_t row = cut.row0 + r, tok = row / (uint32_t)p.G;
+    const int h = cut.kv_head * p.G + (int)(row - tok * p.G);
+    const int64_t token = cut.first + tok;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        w[e / 2] = l == 0.0f ? 0u : pack16(o[e] * inv, o[e + 1] * inv);
+    uint32_t *out = reinterpret_cast<uint32_t *>(p.o + token * p.os + (int64_t)h * D) + lane * (E / 2);
+    if (E == 4)
+        *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[E / 2 - 1]);
+    else
+        out[0] = w[0];
+    if (p.lse && lane == 0)
+        p.lse[token * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 constexpr int kMostBlocks = 152;  // of a launch: one an SM
@@ -920,32 +1100,24 @@ int part_rows(int64_t tokens, int32_t Hq, int32_t Hk) { return (int)std::min<int
 int64_t parts_offset(int rows) { return kMostBlocks * (int64_t)(sizeof(Cut) + 2 * rows * sizeof(float2)); }
 int64_t workspace_bytes(int rows, int D) { return parts_offset(rows) + kMostBlocks * 2ll * rows * 4 * D; }
 
-cudaError_t device_blocks(int *blocks)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(blocks, cudaDevAttrMultiProcessorCount, dev);
-    return e;
-}
-
 template <int D>
-cudaError_t attn_launch(AttnParams p, uint8_t *w, cudaStream_t s)
+cudaError_t attn_launch(AttnParams p, uint8_t *w, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t s)
 {
+    static_assert(sizeof(Smem<D>) + 1024 <= kMaxDynamicSmem, "shared memory");
     static std::atomic<uint64_t> devices{0};
     cudaError_t e = set_smem_attr(attention_kernel<D>, devices);
-    int blocks = 0;
+    int dev = 0, blocks = 0;
     if (e == cudaSuccess)
-        e = device_blocks(&blocks);
+        e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&blocks, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    if (blocks > kMostBlocks)
-        blocks = kMostBlocks;
+    blocks = std::min(blocks, kMostBlocks);
     p.cuts = reinterpret_cast<Cut *>(w);
     p.part_ml = reinterpret_cast<float2 *>(w + kMostBlocks * sizeof(Cut));
     p.parts = reinterpret_cast<float *>(w + parts_offset(p.part_rows));
-    static_assert(sizeof(Smem<D>) + 1024 <= kMaxDynamicSmem, "shared memory");
-    attention_kernel<D><<<(unsigned)blocks, kThreads, sizeof(Smem<D>) + 1024, s>>>(p);
+    attention_kernel<D><<<(unsigned)blocks, kThreads, sizeof(Smem<D>) + 1024, s>>>(p, kmap, vmap);
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -953,7 +1125,7 @@ cudaError_t attn_launch(AttnParams p, uint8_t *w, cudaStream_t s)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks, 4);
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)((p.part_rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = &attr;
@@ -1012,12 +1184,26 @@ dep_status_t attn_entry(const dep_attention_args_t *a, void *stream)
     p.qs = a->q_stride, p.os = a->o_stride;
     p.kps = a->k_page_stride, p.kss = a->k_slot_stride, p.khs = a->k_head_stride;
     p.vps = a->v_page_stride, p.vss = a->v_slot_stride, p.vhs = a->v_head_stride;
-    p.ts = a->table_stride, p.tokens = T, p.n_pages = cache ? a->n_pages : 0;
-    p.n_seq = a->n_seq, p.Hq = a->Hq, p.Hk = a->Hk, p.page = a->page_size, p.width = a->table_width;
+    p.ts = a->table_stride, p.tokens = T, p.each = T / a->n_seq, p.n_pages = cache ? a->n_pages : 0;
+    p.n_seq = a->n_seq, p.Hq = a->Hq, p.Hk = a->Hk, p.G = a->Hq / a->Hk, p.page = a->page_size, p.most = a->table_width * a->page_size;
+    // Division of a number below 2^31: 2^k / page rounded up, with 2^(k - 31) no less than the page.
+    int k = 31;
+    while ((1ll << (k - 31)) < a->page_size)
+        ++k;
+    p.page_shift = k, p.page_mul = (uint32_t)(((1ull << k) + a->page_size - 1) / a->page_size);
     p.scale = a->scale, p.status = a->status, p.part_rows = part_rows(T, a->Hq, a->Hk);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // A tile in boxes that lie within a page: their slots divide both, and are whole groups of the swizzle.
+    int32_t box = kTile;
+    while (a->page_size % box != 0)
+        box /= 2;
+    CUtensorMap kmap{}, vmap{};
+    if (box >= 8 && cache &&
+        encode_bf16_cache(&kmap, a->k_cache, a->D, a->page_size, a->Hk, a->n_pages, a->k_slot_stride, a->k_head_stride, a->k_page_stride, box) == CUDA_SUCCESS &&
+        encode_bf16_cache(&vmap, a->v_cache, a->D, a->page_size, a->Hk, a->n_pages, a->v_slot_stride, a->v_head_stride, a->v_page_stride, box) == CUDA_SUCCESS)
+        p.box = box;
     uint8_t *const ws = static_cast<uint8_t *>(a->workspace);
-    const cudaError_t e = a->D == 128 ? attn_launch<128>(p, ws, s) : attn_launch<64>(p, ws, s);
+    const cudaError_t e = a->D == 128 ? attn_launch<128>(p, ws, kmap, vmap, s) : attn_launch<64>(p, ws, kmap, vmap, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return DEP_ERR_CUDA;

@@ -86,4 +86,23 @@ CUresult encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// A paged cache of BF16 rows of `d` channels (a multiple of 64), strides in elements, in boxes of 64 channels
+// and `box_slots` slots of one head and page, in the 128-byte swizzle; a page past the cache reads as zeros.
+CUresult encode_bf16_cache(CUtensorMap *map, const void *base, uint64_t d, uint64_t slots, uint64_t heads, uint64_t pages,
+                           int64_t slot_stride, int64_t head_stride, int64_t page_stride, uint32_t box_slots)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return CUDA_ERROR_NOT_FOUND;
+    const cuuint64_t dims[4] = {d, slots, heads, pages};
+    // (the stride of a dimension of one is not used, but has to be allowed)
+    const cuuint64_t strides[3] = {slots > 1 ? 2 * (cuuint64_t)slot_stride : 2 * d, heads > 1 ? 2 * (cuuint64_t)head_stride : 2 * d,
+                                   pages > 1 ? 2 * (cuuint64_t)page_stride : 2 * d};
+    const cuuint32_t box[4] = {64, box_slots, 1, 1};
+    const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, elem_strides,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 }  // namespace dep
