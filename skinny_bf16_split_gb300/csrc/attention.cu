@@ -36,14 +36,15 @@ namespace {
 constexpr int kTreeMost = 64;    // tokens of a sequence that a tree's words name
 constexpr int kTile = 128;       // positions of a tile; rows of an MMA
 constexpr int kBlockRows = 2 * kTile;  // rows of an item
-constexpr int kProducers = 2;    // warps that fetch, each half of a tile's rows
+constexpr int kProducers = 2;    // warps that fetch: one keys, one values
 constexpr int kWarps = 12;       // 4 + 4 softmax, 2 producing, 2 issuing MMAs
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSlotRing = 5 * 32768;  // bytes of keys and values in flight
-constexpr int kLag = 2;     // slots that a producing thread's copies may be behind what it issues
+constexpr int kLanded = 4;  // tiles of values that came in boxes and are looked at: more than are in flight
 constexpr int kMasks = 8;   // tiles whose masks are held
 constexpr int kAhead = 4;   // items whose descriptions are held
-constexpr int kCost = 2;    // tiles' worth of work that an item costs beside its tiles
+constexpr int kCost = 3;     // tiles' worth of work that an item costs beside its tiles,
+constexpr int kCostTwo = 5;  // and one with two tiles of rows
 constexpr int kLeast = 4;   // units of a block at least: fewer are not worth the joining
 constexpr uint64_t kWaitNs = 1000000000ull;
 
@@ -60,6 +61,7 @@ struct AttnParams {
     float scale;
     int *status;
     int32_t part_rows;
+    bool wide;         // rows of o start at multiples of 32 bytes
     int32_t box;       // slots of a page in one box of the caches' maps; 0: no maps
     struct Cut *cuts;  // of every block
     float2 *part_ml;   // m and sum of a part's rows: [block][2][part_rows]
@@ -79,7 +81,7 @@ struct Item {
     int64_t first;               // the sequence's first token
     int32_t seq, kv_head, row0, rows;
     int32_t t0, t1, T;           // t1 = 0: no more items
-    int32_t own, end, len;       // positions: the first new token's; what is seen ends before `end`; the sequence's length
+    int32_t own, shared, end;    // positions: the first new token's; those before `shared` are seen by all rows, from `end` on by none
     __device__ bool two() const { return rows > kTile; }  // both groups on the same tiles of positions
     __device__ bool whole() const { return t0 == 0 && t1 == T; }
 };
@@ -87,11 +89,12 @@ struct Item {
 template <int D>
 struct Smem {
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kSlots = kSlotRing / kTileBytes;
+    static constexpr int kSlots = kSlotRing / kTileBytes, kKeySlots = kSlots / 2;
     uint8_t q[2][kTileBytes];          // tiles of rows
-    uint8_t ring[kSlots][kTileBytes];  // keys and values
+    uint8_t ring[kSlots][kTileBytes];  // a ring of kKeySlots tiles of keys and one of values
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full[2], q_empty[2], item_full[kAhead], done[kAhead];
+    uint64_t landed[kLanded], turn[2];
     uint64_t s_full[2], p_full[2], o_full[2], x_full, x_free, drained[2];
     alignas(16) uint32_t masks[kMasks][4];  // positions of a tile that are in the cache
     Item items[kAhead];
@@ -134,13 +137,14 @@ struct Seq {
         return len - n + (int)((uint32_t)(min(rows, (rb + 1) * kBlockRows) - 1) / (uint32_t)p.G) + 1;
     }
     __device__ int tiles(const AttnParams &p, int rb) const { return max(1, (end(p, rb) + kTile - 1) / kTile); }
+    __device__ int cost(int rb) const { return rows - rb * kBlockRows > kTile ? kCostTwo : kCost; }
     __device__ int64_t head_units(const AttnParams &p) const  // of one key and value head
     {
         if (p.tree)
-            return n == 0 ? 0 : (int64_t)blocks * (tiles(p, 0) + kCost);
+            return n == 0 ? 0 : (int64_t)(blocks - 1) * (tiles(p, 0) + kCostTwo) + tiles(p, 0) + cost(blocks - 1);
         int64_t u = 0;
         for (int rb = 0; rb < blocks; ++rb)
-            u += tiles(p, rb) + kCost;
+            u += tiles(p, rb) + cost(rb);
         return u;
     }
 };
@@ -158,11 +162,12 @@ struct Parts {
     __device__ int64_t begin(int b) const { return b * each + min((int64_t)b, more); }
 };
 
-// The items of a block's range, one after another.  An item has kCost units before its tiles'.
+// The items of a block's range, one after another.  An item has its cost in units before its tiles'.
 struct Items {
     Seq q;
     int s, kv_head, rb, T;
     int64_t unit, at, left;  // the item's first unit, where in it the range goes on, units left of the range
+    __device__ int cost() const { return q.cost(rb); }
     // Go to unit `begin` of the units from sequence `seq` on, which starts at unit0.
     __device__ void start(const AttnParams &p, int seq, int64_t unit0, int64_t begin, int64_t count)
     {
@@ -173,9 +178,9 @@ struct Items {
         unit = unit0 + skip * head;
         for (rb = 0;; ++rb) {
             T = q.tiles(p, rb);
-            if (unit + T + kCost > begin)
+            if (unit + T + cost() > begin)
                 break;
-            unit += T + kCost;
+            unit += T + cost();
         }
         at = begin - unit;
     }
@@ -186,16 +191,17 @@ struct Items {
         it.t1 = 0;
         if (left <= 0 || s >= p.n_seq)
             return it;
-        const int64_t to = min((int64_t)T + kCost, at + left);
+        const int64_t to = min((int64_t)T + cost(), at + left);
         left -= to - at;
         it.first = q.first, it.seq = s, it.kv_head = kv_head, it.row0 = rb * kBlockRows, it.rows = min(kBlockRows, q.rows - it.row0);
-        it.t0 = (int)max(at - kCost, (int64_t)0), it.t1 = (int)max(to - kCost, (int64_t)0), it.T = T;
-        it.own = q.len - q.n, it.end = q.end(p, rb), it.len = q.len;
+        it.t0 = (int)max(at - cost(), (int64_t)0), it.t1 = (int)max(to - cost(), (int64_t)0), it.T = T;
+        it.own = q.len - q.n, it.end = q.end(p, rb);
+        it.shared = min(it.end, it.own + (p.tree ? 0 : (int)((uint32_t)it.row0 / (uint32_t)p.G) + 1));
         return it;
     }
     __device__ void next(const AttnParams &p)
     {
-        unit += T + kCost;
+        unit += T + cost();
         at = 0;
         if (left <= 0)
             return;
@@ -340,39 +346,42 @@ __device__ __forceinline__ Item next_item(Smem<D> &sm, int item, const AttnParam
 }
 
 // Steps of 16 positions in which tile t of the values is multiplied: as far as something is seen.
-__device__ __forceinline__ int value_steps(const Item &it, int t) { return min(max((it.end - t * kTile + 15) / 16, 1), kTile / 16); }
+__device__ __forceinline__ int value_steps(int end, int t) { return min(max((end - t * kTile + 15) / 16, 1), kTile / 16); }
 
 // ---- producing --------------------------------------------------------------------------------
 
-// The rows [64 warp, 64 warp + 64) of a swizzled tile, 2 D bytes each, by 16-byte copies: lane l knows the
-// sources of rows l and 32 + l of them (null: zeros).  `rows`: how many of the tile's are wanted.
-template <int D>
-__device__ __forceinline__ void gather(uint32_t tile, const uint16_t *row0, const uint16_t *row1, int rows, const void *any)
+// The first `rows` rows of a swizzled tile, 2 D bytes each, by 16-byte copies of one warp: source(i) is the lane's
+// row 32 i + lane (null: zeros).
+template <int D, typename Source>
+__device__ __forceinline__ void gather(uint32_t tile, int rows, const void *any, Source source)
 {
     constexpr int CH = D / 8, RPI = 32 / CH;  // chunks of a row; rows an instruction
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - 8, c = lane % CH;
-    const int n = min(64, rows - 64 * warp);
-#pragma unroll 2
-    for (int i = 0; i < n; i += RPI) {
-        const int r = i + lane / CH;
-        const uint64_t src = __shfl_sync(~0u, reinterpret_cast<uint64_t>(i < 32 ? row0 : row1), r & 31);
-        const uint32_t dst = tile + (uint32_t)((c / 8) * kTile * 128 + (64 * warp + r) * 128 + ((c % 8) ^ (r & 7)) * 16);
-        cp_async16(dst, src ? reinterpret_cast<const uint4 *>(src) + c : any, src != 0);
+    const int lane = threadIdx.x & 31, c = lane % CH;
+#pragma unroll 1
+    for (int i = 0; 32 * i < rows; ++i) {
+        const uint64_t mine = reinterpret_cast<uint64_t>(source(i));
+        const uint32_t to = tile + (uint32_t)((c / 8) * kTile * 128 + 32 * i * 128);
+#pragma unroll 4
+        for (int j = 0; j < CH; ++j) {
+            const int r = j * RPI + lane / CH;
+            const uint64_t src = __shfl_sync(~0u, mine, r);
+            cp_async16(to + (uint32_t)(r * 128 + ((c % 8) ^ (r & 7)) * 16), src ? reinterpret_cast<const uint4 *>(src) + c : any, src != 0);
+        }
     }
 }
 
-// Values of new tokens that are not finite become zeros; whether there were any.
+// Rows [from, to) of a swizzled tile of values: those from `end` on become zeros, and of the others what is not
+// finite; whether there was any such.
 template <int D>
-__device__ __forceinline__ bool take_out(uint8_t *tile, int from)
+__device__ __forceinline__ bool mend(uint8_t *tile, int from, int end, int to)
 {
     constexpr int CH = D / 8, RPI = 32 / CH;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - 8, c = lane % CH;
+    const int lane = threadIdx.x & 31, c = lane % CH;
     bool any = false;
-    for (int i = max(0, from - 64 * warp) / RPI; i < 64 / RPI; ++i) {
-        const int r = i * RPI + lane / CH;
-        if (64 * warp + r < from)
-            continue;
-        uint4 *at = reinterpret_cast<uint4 *>(tile + (c / 8) * kTile * 128 + (64 * warp + r) * 128 + ((c % 8) ^ (r & 7)) * 16);
+#pragma unroll 1
+    for (int i = from / RPI * RPI; i < to; i += RPI) {
+        const int r = i + lane / CH;
+        uint4 *at = reinterpret_cast<uint4 *>(tile + (c / 8) * kTile * 128 + r * 128 + ((c % 8) ^ (r & 7)) * 16);
         uint4 v = *at;
         uint32_t *w = &v.x;
         bool here = false;
@@ -382,9 +391,12 @@ __device__ __forceinline__ bool take_out(uint8_t *tile, int from)
             here |= (lo | hi) != 0;
             w[e] &= ~(lo | hi);
         }
-        if (here)
+        if (r >= end && r < to)
+            *at = make_uint4(0, 0, 0, 0);
+        else if (here && r >= from && r < to) {
             *at = v;
-        any |= here;
+            any = true;
+        }
     }
     return any;
 }
@@ -402,56 +414,57 @@ template <int D>
 __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kmap, const CUtensorMap &vmap, const Parts &parts)
 {
     using S = Smem<D>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - 8;
-    struct Flight {
-        int32_t slot, from, item;  // from: first row among the new tokens' values, kTile: nothing to look at
-    } fl[kLag + 1];
+    constexpr int H = D / 64;
+    const int lane = threadIdx.x & 31;
+    const bool values = threadIdx.x / 32 != 8;
+    // Copies of 16 bytes, and values that have to be looked at, are announced once the next copy has been issued.
     constexpr int kNone = -1, kRows = -2;  // kRows, kRows - 1: the tiles of rows
-#pragma unroll
-    for (auto &f : fl)
-        f.slot = kNone;
-    int c = 0, kt = 0, item = 0, qc = 0;
+    struct Flight {
+        int32_t slot, item, from, end, to;  // rows of values that have to be looked at, as for mend(); from = to: none
+        int32_t box;                        // the number of a tile that came in boxes, or -1
+    } flight;
+    flight.slot = kNone;
+    int ring = values ? S::kKeySlots : 0, item = 0, qc = 0, boxed = 0, kt = 0;
+    uint32_t lap = 1;  // of the ring, as the parity that its empty slots have
     bool ok = true;
-    const auto land = [&](Flight &f) {  // copies of 16 bytes have arrived
-        if (f.slot == kNone)
+    // Boxes: lane l issues half l % H of box l / H of a tile.
+    const int boxes = p.box ? kTile / p.box : 0, box_row = min(lane / H, boxes - 1) * p.box, half = lane % H;
+    const uint32_t box_at = (uint32_t)(half * kTile * 128 + box_row * 128);
+    const CUtensorMap *const map = values ? &vmap : &kmap;
+    const auto land = [&](bool more = false) {  // more: copies have been issued since
+        if (flight.slot == kNone)
             return;
-        if (f.from < kTile && take_out<D>(sm.ring[f.slot], f.from))
-            sm.odd[f.item % kAhead] = f.item + 1;
+        if (flight.box >= 0)
+            ok = wait_warp(sm, sm.landed[flight.box % kLanded], (uint32_t)(flight.box / kLanded) & 1, p, DEP_DEV_TIMEOUT_PRODUCER) && ok;
+        else if (more)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (ok && flight.from < flight.to && mend<D>(sm.ring[flight.slot], flight.from, flight.end, flight.to))
+            sm.odd[flight.item % kAhead] = flight.item + 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads through the async proxy
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(smem_u32(f.slot <= kRows ? &sm.q_full[kRows - f.slot] : &sm.full[f.slot]));
-        f.slot = kNone;
+            mbar_arrive(smem_u32(flight.slot <= kRows ? &sm.q_full[kRows - flight.slot] : &sm.full[flight.slot]));
+        flight.slot = kNone;
     };
-    const auto issued = [&](int slot, int from) {
+    const auto copied = [&](int slot, int from = 0, int end = 0, int to = 0, int box = -1) {
         asm volatile("cp.async.commit_group;" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < kLag; ++i)
-            fl[i] = fl[i + 1];
-        fl[kLag] = Flight{slot, from, item};
-        if (fl[0].slot != kNone) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-            land(fl[0]);
-        }
-    };
-    const auto drain = [&] {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-        for (int i = 1; i <= kLag; ++i)
-            land(fl[i]);
+        land(true);
+        flight = Flight{slot, item, from, end, to, box};
     };
     // What is waited for may itself wait for copies that have not been announced yet.
     const auto need = [&](uint64_t &bar, uint32_t parity) {
         if (!ok || __all_sync(~0u, mbar_try_wait(smem_u32(&bar), parity)))
             return;
-        drain();
-        ok = wait_warp(sm, bar, parity, p, DEP_DEV_TIMEOUT_PRODUCER);
+        land();
+        ok = ok && wait_warp(sm, bar, parity, p, DEP_DEV_TIMEOUT_PRODUCER);
     };
     Items list;
-    if (warp == 0)
+    if (!values)
         list.start(p, sm.seq, sm.unit0, sm.begin, sm.left);
     for (;; ++item) {
-        if (warp == 0) {  // tells the others
+        if (!values) {  // tells the others
             const Item it = list.take(p);
             if (item >= kAhead)
                 need(sm.done[item % kAhead], (uint32_t)(item / kAhead - 1) & 1);
@@ -459,7 +472,7 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
                 sm.items[item % kAhead] = it;
                 if (ok && it.t0 == 0 && it.t1 > 0 && it.t1 < it.T) {  // goes on in the blocks that follow
                     int last = blockIdx.x + 1;
-                    while (parts.begin(last + 1) < list.unit + it.T + kCost)
+                    while (parts.begin(last + 1) < list.unit + it.T + list.cost())
                         ++last;
                     p.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, it.kv_head, it.row0, it.rows, it.first, {0, 0}};
                 }
@@ -472,164 +485,247 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
         if (!ok || it.t1 == 0)
             break;
         const bool two = it.two();
-        // Pages of this warp's 64 rows of a tile: rows `lane` and 32 + lane of them, as the table has them.  Looked up a
-        // tile ahead; the values of a tile come after the keys of the next where the groups take turns.
-        struct Pages {
-            int32_t a, b;
-        } ahead, now{-1, -1}, before{-1, -1};
+        const int n = it.t1 - it.t0;
         const int32_t *const table = p.table + it.seq * p.ts;
-        const auto look = [&](int t) {
-            const int pos = t * kTile + 64 * warp + lane;
-            return Pages{pos < it.end ? table[page_of(p, pos)] : -1, pos + 32 < it.end ? table[page_of(p, pos + 32)] : -1};
+        // The page of the lane's box, as the table has it, and the box's slot there; looked up a tile ahead.
+        const auto look = [&](int t, int &slot) {
+            const int pos = t * kTile + box_row, i = page_of(p, pos);
+            slot = pos - i * p.page;
+            return boxes && pos < it.end ? table[i] : -1;
         };
-        ahead = look(it.t0);
-        for (int h = 0; h < (two ? 2 : 1); ++h, ++qc) {
-            need(sm.q_empty[qc & 1], ((uint32_t)(qc >> 1) & 1) ^ 1);
+        const auto page_at = [&](int pos) {
+            const int32_t g = pos < it.end ? table[page_of(p, pos)] : -1;
+            return (uint32_t)g < (uint32_t)p.n_pages ? g : -1;
+        };
+        int next_slot, next_page = look(it.t0, next_slot);
+        // Rows: each warp fetches half of a tile, the keys' after its first tile of keys.
+        const auto rows = [&] {
+            for (int h = 0; h < (two ? 2 : 1); ++h) {
+                const int b = (qc + h) & 1, r0 = kTile * h + (values ? kTile / 2 : 0);
+                need(sm.q_empty[b], ((uint32_t)((qc + h) >> 1) & 1) ^ 1);
+                if (!ok)
+                    return;
+                gather<D>(smem_u32(sm.q[b]) + (values ? kTile / 2 * 128 : 0), min(kTile / 2, it.rows - r0), p.q, [&](int i) -> const uint16_t * {
+                    const int r = r0 + 32 * i + lane;
+                    const uint32_t row = it.row0 + r, tok = row / (uint32_t)p.G;
+                    return r < it.rows ? p.q + (it.first + tok) * p.qs + (int32_t)(it.kv_head * p.G + (row - tok * p.G)) * D : nullptr;
+                });  // (the tile's other rows are nobody's)
+                copied(kRows - b);
+            }
+        };
+        if (values)
+            rows();
+        for (int i = 0; i < n; ++i) {
+            need(sm.empty[ring], lap);
             if (!ok)
                 break;
-            const uint16_t *src[2];
+            const int t = it.t0 + i, slot = ring;
+            if (++ring == (values ? S::kSlots : S::kKeySlots))
+                ring = values ? S::kKeySlots : 0, lap ^= 1;
+            const int32_t page = (uint32_t)next_page < (uint32_t)p.n_pages ? next_page : -1, in_page = next_slot;
+            if (t + 1 < it.t1)
+                next_page = look(t + 1, next_slot);
+            if (!values) {  // which of the positions are in the cache
+                uint32_t *const mask = sm.masks[kt++ % kMasks];
+                if (!boxes) {
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t m = __ballot_sync(~0u, page_at(t * kTile + 32 * w + lane) >= 0);
+                        if (lane == 0)
+                            mask[w] = m;
+                    }
+                } else if (__all_sync(~0u, page >= 0) && (t + 1) * kTile <= it.end) {
+                    if (lane < 4)
+                        mask[lane] = ~0u;
+                } else {
+                    const int here = page < 0 ? 0 : min(max(it.end - (t * kTile + box_row), 0), p.box);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = kTile * h + 64 * warp + 32 * i + lane;
-                const uint32_t row = it.row0 + r, tok = row / (uint32_t)p.G;
-                src[i] = r < it.rows ? p.q + (it.first + tok) * p.qs + (int32_t)(it.kv_head * p.G + (row - tok * p.G)) * D : nullptr;
-            }
-            gather<D>(smem_u32(sm.q[qc & 1]), src[0], src[1], it.rows - kTile * h, p.q);  // (the tile's other rows are nobody's)
-            issued(kRows - (qc & 1), kTile);
-        }
-        const auto load = [&](int t, bool values) {
-            if (!values) {
-                before = now;
-                now.a = (uint32_t)ahead.a < (uint32_t)p.n_pages ? ahead.a : -1;
-                now.b = (uint32_t)ahead.b < (uint32_t)p.n_pages ? ahead.b : -1;
-                if (t + 1 < it.t1)
-                    ahead = look(t + 1);
-            }
-            const Pages pg = values && !two && t + 1 < it.t1 ? before : now;
-            const int slot = c % S::kSlots;
-            need(sm.empty[slot], ((uint32_t)(c / S::kSlots) & 1) ^ 1);
-            if (!ok)
-                return;
-            if (!values) {
-                const uint32_t a = __ballot_sync(~0u, pg.a >= 0), b = __ballot_sync(~0u, pg.b >= 0);
-                if (lane == 0)
-                    *reinterpret_cast<uint2 *>(&sm.masks[kt % kMasks][2 * warp]) = make_uint2(a, b);
-                ++kt;
-            }
-            // Values past the sequence's end have to be zeros, and those of new tokens finite: such tiles come row by row.
-            if (p.box && (!values || (t + 1) * kTile <= min(it.own, it.end))) {
-                const int boxes = max(1, 64 / p.box), b = lane / (D / 64), half = lane % (D / 64);
-                const int r = min(b * p.box, 63), pos = t * kTile + 64 * warp + r;
-                const int32_t pa = __shfl_sync(~0u, pg.a, r & 31), pb = __shfl_sync(~0u, pg.b, r & 31), at = r < 32 ? pa : pb;
-                const uint32_t bar = smem_u32(&sm.full[slot]);
-                const bool mine = warp == 0 || p.box <= 64;
-                if (lane == 0) {
-                    if (mine)
-                        mbar_arrive_expect_tx(bar, (uint32_t)(max(64, p.box) * D * 2));
-                    else
-                        mbar_arrive(bar);
+                    for (int w = 0; w < 4; ++w) {  // rows [box_row, box_row + here) in those of the word
+                        const int lo = min(max(box_row - 32 * w, 0), 32), hi = min(max(box_row + here - 32 * w, 0), 32);
+                        const uint32_t m = __reduce_or_sync(~0u, (uint32_t)((1ull << hi) - (1ull << lo)) * (uint32_t)(hi > lo));
+                        if (lane == 0)
+                            mask[w] = m;
+                    }
                 }
                 __syncwarp();
-                if (mine && b < boxes)  // (a page outside the pool gives zeros)
-                    tma_load_box(smem_u32(sm.ring[slot]) + (uint32_t)(half * kTile * 128 + (64 * warp + r) * 128), values ? &vmap : &kmap,
-                                 64 * half, pos - page_of(p, pos) * p.page, it.kv_head, at >= 0 ? at : (int32_t)p.n_pages, bar);
-                issued(kNone, kTile);
+            }
+            // Values past the end have to be zeros, and those that not all rows see finite.
+            int from = 0, to = 0, end = 0;
+            if (values && (t + 1) * kTile > it.shared) {
+                to = 16 * value_steps(it.end, t), end = it.end - t * kTile;
+                from = max(0, min(it.shared - t * kTile, to));
+            }
+            if (boxes) {
+                const uint32_t bar = smem_u32(from < to ? &sm.landed[boxed % kLanded] : &sm.full[slot]);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, S::kTileBytes);
+                __syncwarp();
+                if (lane < boxes * H)  // (a page outside the pool gives zeros)
+                    tma_load_box(smem_u32(sm.ring[slot]) + box_at, map, 64 * half, in_page, it.kv_head, page >= 0 ? page : (int32_t)p.n_pages, bar);
+                if (from < to)
+                    copied(slot, from, end, to, boxed++);
+                else
+                    land();
             } else {
-                const uint16_t *src[2];
                 const uint16_t *const base = values ? p.vc + it.kv_head * p.vhs : p.kc + it.kv_head * p.khs;
                 const int64_t ps = values ? p.vps : p.kps, ss = values ? p.vss : p.kss;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int32_t g = i ? pg.b : pg.a;
-                    const int pos = t * kTile + 64 * warp + 32 * i + lane, at = pos - page_of(p, pos) * p.page;
-                    src[i] = g < 0 ? nullptr : base + g * ps + at * ss;
-                }
                 // (of the values only what the last product reads)
-                gather<D>(smem_u32(sm.ring[slot]), src[0], src[1], values ? 16 * value_steps(it, t) : kTile, p.q);
-                issued(slot, values && (t + 1) * kTile > it.own ? max(0, it.own - t * kTile) : kTile);
+                gather<D>(smem_u32(sm.ring[slot]), values ? 16 * value_steps(it.end, t) : kTile, p.q, [&](int w) -> const uint16_t * {
+                    const int pos = t * kTile + 32 * w + lane, g = page_at(pos);
+                    return g < 0 ? nullptr : base + g * ps + (pos - page_of(p, pos) * p.page) * ss;
+                });
+                copied(slot, from, end, to);
             }
-            ++c;
-        };
-        const int n = it.t1 - it.t0;
-        for (int i = 0; ok && i < 2 * n; ++i) {
-            // In the order of the MMAs: keys, values, keys, ... or, in turns, two tiles' keys first.
-            const bool values = two ? i & 1 : n == 1 ? i == 1 : i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
-            const int t = two ? i / 2 : i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : values ? i / 2 - 1 : (i + 1) / 2;
-            load(it.t0 + t, values);
-            if (item == 0 && i == min(n, 2) - 1)
-                drain();  // (the first rows, at once)
+            if (!values && i == 0)
+                rows();
         }
-        if (warp == 0)
+        qc += two ? 2 : 1;
+        if (!values)
             list.next(p);
     }
-    drain();
+    land();
 }
 
 // ---- multiplying (one thread for each group) --------------------------------------------------
 
 template <int D>
+__device__ __forceinline__ void multiply_scores(uint32_t s_at, uint64_t rows, uint32_t keys)
+{
+    constexpr uint32_t kScores = tc::idesc_bf16_f32(kTile, kTile);
+    uint32_t acc = 0;
+    tc::mma_steps<D / 16, kTile * 128, kTile * 128>(s_at, rows, tc::desc_sw128(keys), kScores, acc);
+}
+
+// The first `steps` of a tile's groups of 16 positions.
+template <int D>
+__device__ __forceinline__ void multiply_values(uint32_t o_at, uint32_t s_at, uint32_t values, int steps, uint32_t acc)
+{
+    constexpr uint32_t kValues = tc::idesc_bf16_f32(kTile, D) | (1u << 16);
+    const uint64_t v = desc_values(values);
+    if (steps == kTile / 16) {
+#pragma unroll
+        for (int j = 0; j < kTile / 16; ++j) {
+            mma_bf16_ta(o_at, s_at + 8 * j, v + (uint64_t)(j * 2048 >> 4), kValues, acc);
+            acc = 1;
+        }
+    } else
+#pragma unroll 1
+        for (int j = 0; j < steps; ++j) {
+            mma_bf16_ta(o_at, s_at + 8 * j, v + (uint64_t)(j * 2048 >> 4), kValues, acc);
+            acc = 1;
+        }
+}
+
+template <int D>
 __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
 {
     using S = Smem<D>;
-    constexpr uint32_t kScores = tc::idesc_bf16_f32(kTile, kTile), kValues = tc::idesc_bf16_f32(kTile, D) | (1u << 16);
-    const uint32_t s_at = tmem + g * kTile, o_at = tmem + 2 * kTile + g * D;
-    int slot = 0, item = 0, qc = 0;
-    uint32_t lap = 0, k = 0;  // of the ring; tiles multiplied
+    const uint32_t s_at = tmem + g * kTile, o_at = tmem + 2 * kTile + g * D, ring = smem_u32(sm.ring[0]);
+    const uint32_t empty = smem_u32(&sm.empty[0]);
     bool ok = true;
+    int key_slot = 0, value_slot = S::kKeySlots, item = 0, qc = 0;
+    uint32_t key_lap = 0, value_lap = 0, k = 0, u = 0;  // of the rings; tiles multiplied; turns taken
+    const auto next_keys = [&] {  // the next slot, once it is full
+        ok = ok && wait(sm, sm.full[key_slot], key_lap, p, DEP_DEV_TIMEOUT_MMA);
+        const int at = key_slot;
+        if (++key_slot == S::kKeySlots)
+            key_slot = 0, key_lap ^= 1;
+        return at;
+    };
+    const auto next_values = [&] {
+        ok = ok && wait(sm, sm.full[value_slot], value_lap, p, DEP_DEV_TIMEOUT_MMA);
+        const int at = value_slot;
+        if (++value_slot == S::kSlots)
+            value_slot = S::kKeySlots, value_lap ^= 1;
+        return at;
+    };
+    // Where both groups have the same tiles they take turns, each with the product of P and the next scores: so
+    // one group's products run while the other one softens, instead of both at once and then neither.
+    const auto turn = [&] { ok = ok && wait(sm, sm.turn[g], (u & 1) ^ (uint32_t)(g == 0), p, DEP_DEV_TIMEOUT_MMA); };
+    const auto pass = [&] {
+        mbar_arrive(smem_u32(&sm.turn[g ^ 1]));
+        ++u;
+    };
     for (;; ++item) {
         ok = ok && wait(sm, sm.item_full[item % kAhead], (uint32_t)(item / kAhead) & 1, p, DEP_DEV_TIMEOUT_MMA);
-        const Item it = sm.items[item % kAhead];
+        const Item &it = sm.items[item % kAhead];
+        const int n = it.t1 - it.t0, t0 = it.t0, to = it.end;
         if (!ok || it.t1 == 0)
             break;
         const bool two = it.two();
-        const int n = it.t1 - it.t0;
         // (both tiles of rows, also the other group's: the release below counts on it)
         for (int h = 0; h < (two ? 2 : 1); ++h)
             ok = ok && wait(sm, sm.q_full[(qc + h) & 1], (uint32_t)((qc + h) >> 1) & 1, p, DEP_DEV_TIMEOUT_MMA);
         const uint64_t rows = tc::desc_sw128(smem_u32(sm.q[two ? (qc + g) & 1 : qc & 1]));
-        int last = two ? n - 1 : n - 1 - ((n - 1 - g) & 1);  // this group's last tile
-        uint32_t acc = 0;
-        for (int i = 0; ok && i < 2 * n; ++i) {
-            const bool values = two ? i & 1 : n == 1 ? i == 1 : i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
-            const int t = two ? i / 2 : i == 0 ? 0 : i == 2 * n - 1 ? n - 1 : values ? i / 2 - 1 : (i + 1) / 2;
-            ok = wait(sm, sm.full[slot], lap, p, DEP_DEV_TIMEOUT_MMA);
+        if (two) {
+            int keys = next_keys();
+            turn();
             if (!ok)
                 break;
-            const uint32_t at = smem_u32(sm.ring[slot]), freed = smem_u32(&sm.empty[slot]);
-            if (!two && (t & 1) != g)
-                mbar_arrive(freed);  // the other group's
-            else if (values) {
-                ok = wait(sm, sm.p_full[g], k & 1, p, DEP_DEV_TIMEOUT_MMA);
+            tc::fence_after();
+            multiply_scores<D>(s_at, rows, ring + keys * S::kTileBytes);
+            pass();
+            tc::commit(smem_u32(&sm.s_full[g]));
+            tc::commit(empty + 8 * keys);
+            for (int t = 0; t < n; ++t) {
+                const int values = next_values();
+                if (t + 1 < n)
+                    keys = next_keys();
+                const uint32_t v_at = ring + values * S::kTileBytes, k_at = ring + keys * S::kTileBytes;
+                const int steps = value_steps(to, t0 + t);
+                ok = ok && wait(sm, sm.p_full[g], k & 1, p, DEP_DEV_TIMEOUT_MMA);
+                ++k;
+                turn();
                 if (!ok)
                     break;
-                ++k;
                 tc::fence_after();
-                const uint64_t v = desc_values(at);
-                const int steps = value_steps(it, it.t0 + t);
-                if (steps == kTile / 16) {
-#pragma unroll
-                    for (int j = 0; j < kTile / 16; ++j) {
-                        mma_bf16_ta(o_at, s_at + 8 * j, v + (uint64_t)(j * 2048 >> 4), kValues, acc);
-                        acc = 1;
-                    }
-                } else
-#pragma unroll 1
-                    for (int j = 0; j < steps; ++j) {
-                        mma_bf16_ta(o_at, s_at + 8 * j, v + (uint64_t)(j * 2048 >> 4), kValues, acc);
-                        acc = 1;
-                    }
-                tc::commit(freed);
-                if (t == last)
+                multiply_values<D>(o_at, s_at, v_at, steps, t > 0);
+                if (t + 1 < n) {
+                    multiply_scores<D>(s_at, rows, k_at);
+                    pass();
+                    tc::commit(smem_u32(&sm.s_full[g]));
+                    tc::commit(empty + 8 * keys);
+                } else {
+                    pass();
                     tc::commit(smem_u32(&sm.o_full[g]));
-            } else {
-                tc::fence_after();
-                uint32_t first = 0;
-                tc::mma_steps<D / 16, kTile * 128, kTile * 128>(s_at, rows, tc::desc_sw128(at), kScores, first);
-                tc::commit(smem_u32(&sm.s_full[g]));
-                tc::commit(freed);
+                }
+                tc::commit(empty + 8 * values);
             }
-            if (++slot == S::kSlots)
-                slot = 0, lap ^= 1;
+        } else {
+            // Every other tile: two tiles' keys first, then a tile's values and the keys of the one after the next.
+            const int last = n - 1 - ((n - 1 - g) & 1);  // this group's last tile
+            const auto scores = [&](int t) {
+                const int at = next_keys();
+                if (!ok)
+                    return;
+                if ((t & 1) != g) {
+                    mbar_arrive(empty + 8 * at);  // the other group's
+                    return;
+                }
+                tc::fence_after();
+                multiply_scores<D>(s_at, rows, ring + at * S::kTileBytes);
+                tc::commit(smem_u32(&sm.s_full[g]));
+                tc::commit(empty + 8 * at);
+            };
+            for (int t = -2; ok && t < n; ++t) {
+                if (t >= 0) {
+                    const int at = next_values();
+                    if (ok && (t & 1) != g)
+                        mbar_arrive(empty + 8 * at);
+                    else if (ok) {
+                        ok = wait(sm, sm.p_full[g], k & 1, p, DEP_DEV_TIMEOUT_MMA);
+                        if (!ok)
+                            break;
+                        ++k;
+                        tc::fence_after();
+                        multiply_values<D>(o_at, s_at, ring + at * S::kTileBytes, value_steps(to, t0 + t), t > 1);
+                        if (t == last)
+                            tc::commit(smem_u32(&sm.o_full[g]));
+                        tc::commit(empty + 8 * at);
+                    }
+                }
+                if (ok && t + 2 < n)
+                    scores(t + 2);
+            }
         }
         for (int h = 0; h < (two ? 2 : 1); ++h, ++qc)
             tc::commit(smem_u32(&sm.q_empty[qc & 1]));
@@ -699,12 +795,20 @@ __device__ __forceinline__ void tile_exp(uint32_t s_at, float c, float off, uint
     sum = x + y;
 }
 
+// 32 bytes at a multiple of 32.
+__device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Adds the values of new tokens that are not finite, which were left out of the product (it would have
 // given them to every row), to the channels of a row that sees them.  FP32 or BF16 in `row`.
 template <int D>
 __device__ __noinline__ void add_odd(const AttnParams &p, const Item &it, int tok, uint64_t word, uint16_t *out, float *part)
 {
-    for (int pos = max(max(it.own, it.t0 * kTile), 0); pos < min(it.t1 * kTile, it.end); ++pos) {
+    for (int pos = max(max(it.shared, it.t0 * kTile), 0); pos < min(it.t1 * kTile, it.end); ++pos) {
         if (!(seen32(p.tree != nullptr, it.own, tok, word, pos) & 1))
             continue;
         const int32_t pi = page_of(p, pos), pg = p.table[it.seq * p.ts + pi];
@@ -893,14 +997,25 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                     if (!live)
                         continue;
                     if (whole) {
+                        uint32_t b[8];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8)
-                            *reinterpret_cast<uint4 *>(out + 16 * w + j) = make_uint4(pack16(y[j], y[j + 1]), pack16(y[j + 2], y[j + 3]),
-                                                                                      pack16(y[j + 4], y[j + 5]), pack16(y[j + 6], y[j + 7]));
+                        for (int j = 0; j < 8; ++j)
+                            b[j] = pack16(y[2 * j], y[2 * j + 1]);
+                        if (p.wide)
+                            store32(out + 16 * w, b);
+                        else {
+                            *reinterpret_cast<uint4 *>(out + 16 * w) = make_uint4(b[0], b[1], b[2], b[3]);
+                            *reinterpret_cast<uint4 *>(out + 16 * w + 8) = make_uint4(b[4], b[5], b[6], b[7]);
+                        }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            *reinterpret_cast<float4 *>(rest + 16 * w + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t b[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                b[j] = __float_as_uint(y[8 * h + j]);
+                            store32(rest + 16 * w + 8 * h, b);
+                        }
                     }
                 }
             if (join) {
@@ -942,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
-            mbar_init(smem_u32(&sm.full[i]), kProducers);
+            mbar_init(smem_u32(&sm.full[i]), 1);
             mbar_init(smem_u32(&sm.empty[i]), 2);
         }
         for (int i = 0; i < kAhead; ++i) {
@@ -957,7 +1072,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             mbar_init(smem_u32(&sm.p_full[g]), 4);
             mbar_init(smem_u32(&sm.o_full[g]), 1);
             mbar_init(smem_u32(&sm.drained[g]), 1);
+            mbar_init(smem_u32(&sm.turn[g]), 1);
         }
+        for (int i = 0; i < kLanded; ++i)
+            mbar_init(smem_u32(&sm.landed[i]), 1);
         mbar_init(smem_u32(&sm.x_full), 4);
         mbar_init(smem_u32(&sm.x_free), 4);
         fence_mbar_init();
@@ -1096,9 +1214,9 @@ constexpr int kMostBlocks = 152;  // of a launch: one an SM
 // Rows that a part may have: no item has more than all tokens give.
 int part_rows(int64_t tokens, int32_t Hq, int32_t Hk) { return (int)std::min<int64_t>(kBlockRows, tokens * (Hq / Hk)); }
 
-// Of the cuts (a multiple of 16 bytes), the parts' m and sums, and the parts; the last on 16 bytes for any number of rows.
+// Of the cuts (a multiple of 16 bytes), the parts' m and sums, and the parts; the last at a multiple of 32 bytes.
 int64_t parts_offset(int rows) { return kMostBlocks * (int64_t)(sizeof(Cut) + 2 * rows * sizeof(float2)); }
-int64_t workspace_bytes(int rows, int D) { return parts_offset(rows) + kMostBlocks * 2ll * rows * 4 * D; }
+int64_t workspace_bytes(int rows, int D) { return parts_offset(rows) + kMostBlocks * 2ll * rows * 4 * D + 32; }
 
 template <int D>
 cudaError_t attn_launch(AttnParams p, uint8_t *w, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t s)
@@ -1116,7 +1234,7 @@ cudaError_t attn_launch(AttnParams p, uint8_t *w, const CUtensorMap &kmap, const
     blocks = std::min(blocks, kMostBlocks);
     p.cuts = reinterpret_cast<Cut *>(w);
     p.part_ml = reinterpret_cast<float2 *>(w + kMostBlocks * sizeof(Cut));
-    p.parts = reinterpret_cast<float *>(w + parts_offset(p.part_rows));
+    p.parts = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(w + parts_offset(p.part_rows)) + 31) & ~(uintptr_t)31);
     attention_kernel<D><<<(unsigned)blocks, kThreads, sizeof(Smem<D>) + 1024, s>>>(p, kmap, vmap);
     e = cudaGetLastError();
     if (e != cudaSuccess)
@@ -1202,6 +1320,7 @@ dep_status_t attn_entry(const dep_attention_args_t *a, void *stream)
         encode_bf16_cache(&kmap, a->k_cache, a->D, a->page_size, a->Hk, a->n_pages, a->k_slot_stride, a->k_head_stride, a->k_page_stride, box) == CUDA_SUCCESS &&
         encode_bf16_cache(&vmap, a->v_cache, a->D, a->page_size, a->Hk, a->n_pages, a->v_slot_stride, a->v_head_stride, a->v_page_stride, box) == CUDA_SUCCESS)
         p.box = box;
+    p.wide = o.aligned(32);
     uint8_t *const ws = static_cast<uint8_t *>(a->workspace);
     const cudaError_t e = a->D == 128 ? attn_launch<128>(p, ws, kmap, vmap, s) : attn_launch<64>(p, ws, kmap, vmap, s);
     if (e != cudaSuccess) {
