@@ -307,25 +307,27 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool i
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-// Wait for a phase; false if this wait or another one of the block gave up.
+// Wait for a phase; false if this wait or another one of the block gave up.  (Out of line: fetching code costs.)
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int32_t *dead, int *status, int code)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*dead)
+            return false;
+        if (globaltimer_ns() - t0 > kWaitNs) {
+            record_status(status, code);
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 template <int D>
 __device__ __forceinline__ bool wait(Smem<D> &sm, uint64_t &bar, uint32_t parity, const AttnParams &p, int code)
 {
     const uint32_t at = smem_u32(&bar);
-    if (mbar_try_wait(at, parity))
-        return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (mbar_try_wait(at, parity))
-            return true;
-        if (*reinterpret_cast<volatile int32_t *>(&sm.dead))
-            return false;
-        if (globaltimer_ns() - t0 > kWaitNs) {
-            record_status(p.status, code);
-            *reinterpret_cast<volatile int32_t *>(&sm.dead) = 1;
-            return false;
-        }
-    }
+    return mbar_try_wait(at, parity) || wait_long(at, parity, &sm.dead, p.status, code);
 }
 
 // The same for a warp that waits together, and stays together.
@@ -738,13 +740,6 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
 
 // ---- softmax ----------------------------------------------------------------------------------
 
-// Largest of three; NaNs do not count.
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 __device__ __forceinline__ uint64_t both(float a, float b)
 {
     uint64_t r;
@@ -765,10 +760,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
-// p = exp2(c s + off) of the row's scores of a tile in BF16 pairs, their sum and the largest score.
-__device__ __forceinline__ void tile_exp(uint32_t s_at, float c, float off, uint32_t (&pk)[2][32], float &top, float &sum)
+// p = exp2(c s + off) of the row's scores of a tile in BF16 pairs; their sum.
+__device__ __forceinline__ float tile_exp(uint32_t s_at, float c, float off, uint32_t (&pk)[2][32])
 {
-    float t[2] = {-INFINITY, -INFINITY};
     const uint64_t c2 = both(c, c), off2 = both(off, off);
     uint64_t s2[2] = {0, 0};
     uint32_t v[2][16];
@@ -780,19 +774,16 @@ __device__ __forceinline__ void tile_exp(uint32_t s_at, float c, float off, uint
             tc::ld16(s_at + 16 * (w + 1), v[(w + 1) & 1]);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-            const float a = __uint_as_float(v[w & 1][j]), b = __uint_as_float(v[w & 1][j + 1]);
             float x, y;
-            apart(fma2(both(a, b), c2, off2), x, y);
+            apart(fma2(both(__uint_as_float(v[w & 1][j]), __uint_as_float(v[w & 1][j + 1])), c2, off2), x, y);
             x = ex2(x), y = ex2(y);
-            t[j / 2 & 1] = max3(t[j / 2 & 1], a, b);
             s2[j / 2 & 1] = add2(s2[j / 2 & 1], both(x, y));
             pk[w / 4][8 * (w & 3) + j / 2] = pack16(x, y);
         }
     }
-    top = fmaxf(t[0], t[1]);
     float x, y;
     apart(add2(s2[0], s2[1]), x, y);
-    sum = x + y;
+    return x + y;
 }
 
 // 32 bytes at a multiple of 32.
@@ -859,15 +850,13 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
             tc::fence_after();
             if (warp_live) {
                 const uint4 in = *reinterpret_cast<const uint4 *>(sm.masks[(kt + (t - it.t0)) % kMasks]);
-                // The maximum that is taken off moves only where it has risen by 2^8: P stays below 2^8, O is
-                // seldom scaled, and P is worked out with the maximum found so far, anew if that has to move.
+                // What is taken off, m, moves only where P would grow past 2^12: then O is seldom scaled, and P is
+                // worked out with the m so far, anew if its sum (in which a NaN shows as well) says that m has to move.
                 bool anew = first || (t + 1) * kTile > clear || (in.x & in.y & in.z & in.w) != ~0u;
                 if (!anew) {
                     uint32_t pk[2][32];
-                    float top, sum;
-                    tile_exp(s_at, c, m == -INFINITY ? 0.0f : -m, pk, top, sum);
-                    const float tm = top * c;
-                    anew = __any_sync(~0u, live && (tm > m + 8.0f || (m == -INFINITY && tm > -INFINITY)));
+                    const float sum = tile_exp(s_at, c, -m, pk);
+                    anew = __any_sync(~0u, live && !(sum <= 4096.0f));
                     if (!anew) {
                         l += sum;
                         tmem_st32(s_at, pk[0]);
@@ -888,7 +877,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                             top = fmaxf(top, see >> j & 1 ? __uint_as_float(v[j]) : -INFINITY);
                     }
                     const float tm = top * c;
-                    const bool up = live && (tm > m + 8.0f || (m == -INFINITY && tm > -INFINITY));
+                    const bool up = live && (tm > m + 5.0f || (m == -INFINITY && tm > -INFINITY));
                     if (__any_sync(~0u, up)) {
                         const float f = up ? ex2(m - tm) : 1.0f;
                         if (up)
