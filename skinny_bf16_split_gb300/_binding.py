@@ -10,6 +10,7 @@ loudly when it is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -740,36 +741,44 @@ def _vector(t, name, dtype, index, n):
     raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on cuda:{index}")
 
 
-def _cache(t, name, index, heads, d):
+def _cache(t, name, index, shape):
     """Strides between pages, slots and heads of a cache [pages, page_size, heads, d]."""
     import torch
-    if t.dtype is torch.bfloat16 and t.dim() == 4 and t.shape[2:] == (heads, d) and t.shape[1] > 0 and (
-            t.get_device() == index):
-        strides = t.stride()
-        if strides[3] == 1:
-            return strides[:3]
-    raise ValueError(f"{name} must be a bfloat16 tensor [pages, page_size, {heads}, {d}] with contiguous channels on "
-                     f"cuda:{index}")
+    if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == index:
+        page, slot, head, channel = t.stride()
+        if channel == 1:
+            return page, slot, head
+    raise ValueError(f"{name} must be a bfloat16 tensor [pages, page_size, {shape[2]}, {shape[3]}] with contiguous channels "
+                     f"on cuda:{index}, like k_cache")
 
 
-def _rotation(args, dev, tokens, positions, freqs, interleaved, amplitude, norm, eps, first, weights):
-    """Fill in what norm_rotate and append_kv share."""
+def _cache_shape(k_cache, heads, d):
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] < 1 or shape[2] != heads or shape[3] != d:
+        raise ValueError(f"k_cache must be [pages, page_size, {heads}, {d}] with at least one slot a page")
+    return shape
+
+
+def _rotation(dev, tokens, d, positions, freqs, norm, q_weight, k_weight):
+    """(q_weight, k_weight, freqs, positions) as addresses, and how many channels are rotated."""
     import torch
     if (positions is None) != (freqs is None):
         raise ValueError("positions and freqs must be given together")
+    f = p = qw = kw = None
+    rot = 0
     if freqs is not None:
         if freqs.dim() != 1:
             raise ValueError("freqs must be a vector, a frequency for each pair of channels")
-        args.rot = 2 * freqs.shape[0]
-        args.freqs = _vector(freqs, "freqs", torch.float64, dev, freqs.shape[0])
-        args.positions = _vector(positions, "positions", torch.int32, dev, tokens)
-    for name, w in weights:
-        if w is not None:
-            if not norm:
-                raise ValueError(f"{name} needs norm")
-            setattr(args, name, _vector(w, name, torch.bfloat16, dev, args.D))
-    args.first, args.eps, args.amplitude = first, eps, amplitude
-    args.flags = (DEP_HEADS_INTERLEAVED if interleaved else 0) | (DEP_HEADS_NORM if norm else 0)
+        n = freqs.shape[0]
+        rot = 2 * n
+        f, p = _vector(freqs, "freqs", torch.float64, dev, n), _vector(positions, "positions", torch.int32, dev, tokens)
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("q_weight and k_weight need norm")
+    if q_weight is not None:
+        qw = _vector(q_weight, "q_weight", torch.bfloat16, dev, d)
+    if k_weight is not None:
+        kw = _vector(k_weight, "k_weight", torch.bfloat16, dev, d)
+    return qw, kw, f, p, rot
 
 
 def norm_rotate(q, k=None, positions=None, freqs=None, *, interleaved: bool = False, amplitude: float = 1.0,
@@ -784,25 +793,29 @@ def norm_rotate(q, k=None, positions=None, freqs=None, *, interleaved: bool = Fa
     q_weight, k_weight: bfloat16 [D].  q_out and k_out are allocated where omitted; they may be q and k.
     Returns (q_out, k_out), or q_out alone without k."""
     import torch
-    dev, bf16 = q.get_device(), torch.bfloat16
-    if q.dim() != 3 or dev < 0 or (k is not None and k.dim() != 3):
+    dev, bf16, shape = q.get_device(), torch.bfloat16, q.shape
+    if len(shape) != 3 or dev < 0 or (k is not None and len(k.shape) != 3):
         raise ValueError("q [tokens, Hq, D] and k [tokens, Hk, D] must be CUDA tensors of three dimensions")
-    T, hq, d = q.shape
+    T, hq, d = shape
     if q_out is None:
-        q_out = _empty((T, hq, d), bf16, q.device, stream)
-    args = dep_heads_args_t(q=q.data_ptr(), q_out=q_out.data_ptr(), q_stride=_heads(q, "q", bf16, dev, (T, hq, d)),
-                            q_out_stride=_heads(q_out, "q_out", bf16, dev, (T, hq, d)), tokens=T, Hq=hq, D=d, page_size=1)
+        q_out = _empty(shape, bf16, q.device, stream)
+    k_ptr = ko_ptr = None
+    ks = kos = hk = 0
     if k is not None:
-        shape = (T, k.shape[1], d)
+        hk = k.shape[1]
+        k_shape = (T, hk, d)
         if k_out is None:
-            k_out = _empty(shape, bf16, q.device, stream)
-        args.k, args.k_out, args.Hk = k.data_ptr(), k_out.data_ptr(), shape[1]
-        args.k_stride, args.k_out_stride = _heads(k, "k", bf16, dev, shape), _heads(k_out, "k_out", bf16, dev, shape)
+            k_out = _empty(k_shape, bf16, q.device, stream)
+        k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
+        ks, kos = _heads(k, "k", bf16, dev, k_shape), _heads(k_out, "k_out", bf16, dev, k_shape)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    _rotation(args, dev, T, positions, freqs, interleaved, amplitude, norm, eps, first,
-              (("q_weight", q_weight), ("k_weight", k_weight)))
-    _on(dev, dep_norm_rotate, args, stream)
+    qw, kw, f, p, rot = _rotation(dev, T, d, positions, freqs, norm, q_weight, k_weight)
+    _on(dev, dep_norm_rotate, dep_heads_args_t(
+        q.data_ptr(), k_ptr, None, qw, kw, f, p, None, q_out.data_ptr(), ko_ptr, None, None,
+        _heads(q, "q", bf16, dev, shape), ks, 0, _heads(q_out, "q_out", bf16, dev, shape), kos, 0, 0, 0, 0, 0, 0, T, 0,
+        hq, hk, d, rot, first, 1, (DEP_HEADS_INTERLEAVED if interleaved else 0) | (DEP_HEADS_NORM if norm else 0), eps,
+        amplitude), stream)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -818,30 +831,36 @@ def append_kv(k, v, k_cache, v_cache, slots, positions=None, freqs=None, *, inte
     outside the cache: padding, not stored.  Returns q_out (allocated where omitted; may be q), or None
     without q."""
     import torch
-    dev, bf16 = k.get_device(), torch.bfloat16
-    if k.dim() != 3 or dev < 0 or (q is not None and q.dim() != 3):
+    dev, bf16, shape = k.get_device(), torch.bfloat16, k.shape
+    if len(shape) != 3 or dev < 0 or (q is not None and len(q.shape) != 3):
         raise ValueError("k, v [tokens, Hk, D] and q [tokens, Hq, D] must be CUDA tensors of three dimensions")
-    shape = T, hk, d = k.shape
-    ks, vs = _cache(k_cache, "k_cache", dev, hk, d), _cache(v_cache, "v_cache", dev, hk, d)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    args = dep_heads_args_t(
-        k=k.data_ptr(), v=v.data_ptr(), slots=_vector(slots, "slots", torch.int32, dev, T), k_cache=k_cache.data_ptr(),
-        v_cache=v_cache.data_ptr(), k_stride=_heads(k, "k", bf16, dev, shape), v_stride=_heads(v, "v", bf16, dev, shape),
-        k_page_stride=ks[0], k_slot_stride=ks[1], k_head_stride=ks[2], v_page_stride=vs[0], v_slot_stride=vs[1],
-        v_head_stride=vs[2], tokens=T, n_pages=k_cache.shape[0], Hk=hk, D=d, page_size=k_cache.shape[1])
+    T, hk, d = shape
+    c_shape = _cache_shape(k_cache, hk, d)
+    q_ptr = qo_ptr = None
+    qs = qos = hq = 0
     if q is not None:
-        q_shape = (T, q.shape[1], d)
+        hq = q.shape[1]
+        q_shape = (T, hq, d)
         if q_out is None:
             q_out = _empty(q_shape, bf16, q.device, stream)
-        args.q, args.q_out, args.Hq = q.data_ptr(), q_out.data_ptr(), q_shape[1]
-        args.q_stride, args.q_out_stride = _heads(q, "q", bf16, dev, q_shape), _heads(q_out, "q_out", bf16, dev, q_shape)
+        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
+        qs, qos = _heads(q, "q", bf16, dev, q_shape), _heads(q_out, "q_out", bf16, dev, q_shape)
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
-    _rotation(args, dev, T, positions, freqs, interleaved, amplitude, norm, eps, first,
-              (("q_weight", q_weight), ("k_weight", k_weight)))
-    _on(dev, dep_append_kv, args, stream)
+    qw, kw, f, p, rot = _rotation(dev, T, d, positions, freqs, norm, q_weight, k_weight)
+    _on(dev, dep_append_kv, dep_heads_args_t(
+        q_ptr, k.data_ptr(), v.data_ptr(), qw, kw, f, p, _vector(slots, "slots", torch.int32, dev, T), qo_ptr, None,
+        k_cache.data_ptr(), v_cache.data_ptr(), qs, _heads(k, "k", bf16, dev, shape), _heads(v, "v", bf16, dev, shape), qos, 0,
+        *_cache(k_cache, "k_cache", dev, c_shape), *_cache(v_cache, "v_cache", dev, c_shape), T, c_shape[0], hq, hk, d, rot,
+        first, c_shape[1], (DEP_HEADS_INTERLEAVED if interleaved else 0) | (DEP_HEADS_NORM if norm else 0), eps, amplitude),
+        stream)
     return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(T, n, hq, hk, d):
+    """dep_attention_workspace by the sizes that it goes by."""
+    return dep_attention_workspace(dep_attention_args_t(tokens=T, n_seq=n, Hq=hq, Hk=hk, D=d))
 
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, tree=None, scale: float | None = None,
@@ -858,34 +877,31 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None
     scale defaults to D ** -0.5.  lse: float32 [tokens, Hq], filled in where given.  The workspace is the
     allocator's.  Returns out, bfloat16 [tokens, Hq, D] (allocated where omitted)."""
     import torch
-    dev, bf16, i32 = q.get_device(), torch.bfloat16, torch.int32
-    shape = q.shape
-    if len(shape) != 3 or dev < 0:
-        raise ValueError("q must be a CUDA tensor [tokens, Hq, D]")
+    dev, bf16, i32, shape = q.get_device(), torch.bfloat16, torch.int32, q.shape
+    if len(shape) != 3 or dev < 0 or len(k_cache.shape) != 4:
+        raise ValueError("q must be a CUDA tensor [tokens, Hq, D] and k_cache one of four dimensions")
     T, hq, d = shape
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same four dimensions")
-    pages, page, hk, _ = k_cache.shape
-    ks, vs = _cache(k_cache, "k_cache", dev, hk, d), _cache(v_cache, "v_cache", dev, hk, d)
-    if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != dev or (
-            page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be an int32 matrix [n_seq, width] with contiguous rows on cuda:{dev}")
-    n, width = page_table.shape
+    hk = k_cache.shape[2]
+    c_shape = _cache_shape(k_cache, hk, d)
+    if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != dev:
+        raise ValueError(f"page_table must be an int32 matrix [n_seq, width] on cuda:{dev}")
+    (n, width), (row, column) = page_table.shape, page_table.stride()
+    if width > 1 and column != 1:
+        raise ValueError("page_table must have contiguous rows")
     if out is None:
         out = _empty(shape, bf16, q.device, stream)
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, hq) or lse.get_device() != dev or (
-            not lse.is_contiguous())):
-        raise ValueError(f"lse must be a contiguous float32 matrix [{T}, {hq}] on cuda:{dev}")
-    args = dep_attention_args_t(
+    lse_ptr = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (T, hq) or lse.get_device() != dev or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 matrix [{T}, {hq}] on cuda:{dev}")
+        lse_ptr = lse.data_ptr()
+    size = _attention_workspace(T, n, hq, hk, d)
+    workspace = _empty((size,), torch.uint8, q.device, stream) if size else None
+    _on(dev, dep_paged_attention, dep_attention_args_t(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), _vector(kv_lens, "kv_lens", i32, dev, n),
         None if cu_seqlens is None else _vector(cu_seqlens, "cu_seqlens", i32, dev, n + 1),
-        None if tree is None else _vector(tree, "tree", torch.int64, dev, T), out.data_ptr(), _ptr(lse),
-        _heads(q, "q", bf16, dev, shape), _heads(out, "out", bf16, dev, shape), *ks, *vs,
-        page_table.stride(0) if n > 1 else width, T, pages, n, hq, hk, d, page, width,
-        d ** -0.5 if scale is None else scale)
-    args.workspace_bytes = dep_attention_workspace(args)
-    if args.workspace_bytes:
-        workspace = _empty((args.workspace_bytes,), torch.uint8, q.device, stream)
-        args.workspace = workspace.data_ptr()
-    _on(dev, dep_paged_attention, args, stream)
+        None if tree is None else _vector(tree, "tree", torch.int64, dev, T), out.data_ptr(), lse_ptr,
+        _heads(q, "q", bf16, dev, shape), _heads(out, "out", bf16, dev, shape), *_cache(k_cache, "k_cache", dev, c_shape),
+        *_cache(v_cache, "v_cache", dev, c_shape), row if n > 1 else width, T, c_shape[0], n, hq, hk, d, c_shape[1], width,
+        d ** -0.5 if scale is None else scale, workspace.data_ptr() if size else None, size, None), stream)
     return out

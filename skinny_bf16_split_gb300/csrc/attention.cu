@@ -1070,8 +1070,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         fence_mbar_init();
         sm.dead = 0;
         sm.left = 0;
-        p.cuts[blockIdx.x].parts = 0;
     }
+    griddep_wait();  // what comes before may write the inputs, and read the workspace
+    if (threadIdx.x == 0)
+        p.cuts[blockIdx.x].parts = 0;
     // The range.  Every thread adds up the units of its share of the sequences.
     const int per = (p.n_seq + kThreads - 1) / kThreads, s0 = min(p.n_seq, (int)threadIdx.x * per), s1 = min(p.n_seq, s0 + per);
     int64_t mine = 0;
@@ -1141,6 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
 {
+    griddep_launch_dependents();
     griddep_wait();
     constexpr int E = D / 32;
     const Cut cut = p.cuts[blockIdx.x];
@@ -1224,19 +1227,23 @@ cudaError_t attn_launch(AttnParams p, uint8_t *w, const CUtensorMap &kmap, const
     p.cuts = reinterpret_cast<Cut *>(w);
     p.part_ml = reinterpret_cast<float2 *>(w + kMostBlocks * sizeof(Cut));
     p.parts = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(w + parts_offset(p.part_rows)) + 31) & ~(uintptr_t)31);
-    attention_kernel<D><<<(unsigned)blocks, kThreads, sizeof(Smem<D>) + 1024, s>>>(p, kmap, vmap);
-    e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
+    // Both start early and wait inside: barriers and tensor memory are set up while the kernel before still runs.
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)((p.part_rows + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem<D>) + 1024;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attention_kernel<D>, p, kmap, vmap);
+    if (e != cudaSuccess)
+        return e;
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)((p.part_rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
 }
 

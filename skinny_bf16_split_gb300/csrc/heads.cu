@@ -4,30 +4,36 @@
 //     y = x * rstd * w,  rstd = 1 / sqrt(mean(x^2) + eps)
 //     (a, b) <- amplitude * (a cos u - b sin u, b cos u + a sin u),  u = position * freq
 //
-// A head is held by D / 8 neighbouring lanes, eight channels each: four from the first
-// half of the rotated channels and the same four of the second (or eight neighbours), so
-// both partners of every pair are in one lane and the rotation needs no exchange.  The
-// eight lanes' (or 16, 32) sum of squares is the only one.
+// A head is held by D / 16 neighbouring lanes, sixteen channels each: eight from the first half of
+// the rotated channels and the same eight of the second (or sixteen neighbours), so both partners of
+// every pair are in one lane and the rotation needs no exchange; the sum of squares is the only one.
+// (Eight channels a lane where D or the rotated part is no multiple of 16.)
 //
 // Angles.  A frequency becomes a 64-bit fraction of a turn, f / 2 pi modulo 1, once a
-// thread; times the position modulo 2^64 it is the angle without any reduction, to
+// block; times the position modulo 2^64 it is the angle without any reduction, to
 // 2^-53 of position * f (what FP64 holds of f / 2 pi) however far the position.  A block
-// works the rot / 2 angles of its token out once, for all heads.
+// works the angles of a few tokens out at once, for all their heads.
 //
-// Bound: DRAM, each byte read once and written once.
+// Bound: DRAM, each byte read once and written once; close behind it the instructions: of 8 channels
+// a lane 110 for eight, of 16 about 120 for sixteen.
 #include <cuda_bf16.h>
 
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "layer.h"
+#include "ptx.cuh"
 
 namespace dep {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocks = 3;    // of an SM
+constexpr int kMostTokens = 16;
+constexpr int kTokens = 4;    // whose angles a block has room for, of the widest heads
 
 struct HeadsParams {
     const uint16_t *q, *k, *v, *qw, *kw;
@@ -37,7 +43,8 @@ struct HeadsParams {
     int64_t qs, ks, vs, qos, kos;
     int64_t kps, kss, khs, vps, vss, vhs;
     int64_t tokens, n_pages;
-    int32_t Hq, Hk, D, rot, first, page, passes;  // passes: of kThreads / LPH heads, of a block
+    int32_t Hq, Hk, D, rot, first, page;
+    int32_t at_once, tasks;  // tokens at once; groups of heads of a token, a warp each
     float eps, amplitude;
 };
 
@@ -49,24 +56,76 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// A lane's eight channels as they are in memory: 8 bytes at o1 and 8 at o2.
+// Two FP32 operations at once.
+struct Two {
+    uint64_t v;
+    __device__ Two() {}
+    __device__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ void apart(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two mul(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two sub(Two a, Two b)
+{
+    Two r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// A lane's N channels: N / 2 pairs (a, b), two at once.
+template <int N>
+struct Pairs {
+    Two a[N / 4], b[N / 4];
+};
+
+// The same as they are in memory: N bytes at o1 and N at o2.
+template <int N>
 struct Lane {
-    uint32_t w[4];
+    uint32_t w[N / 2];
+    using Part = typename std::conditional<N == 16, uint4, uint2>::type;
     __device__ void load(const uint16_t *p, int o1, int o2)
     {
-        const uint2 a = *reinterpret_cast<const uint2 *>(p + o1), b = *reinterpret_cast<const uint2 *>(p + o2);
-        w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+        *reinterpret_cast<Part *>(w) = *reinterpret_cast<const Part *>(p + o1);
+        *reinterpret_cast<Part *>(w + N / 4) = *reinterpret_cast<const Part *>(p + o2);
     }
     __device__ void store(uint16_t *p, int o1, int o2) const
     {
-        *reinterpret_cast<uint2 *>(p + o1) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2 *>(p + o2) = make_uint2(w[2], w[3]);
+        *reinterpret_cast<Part *>(p + o1) = *reinterpret_cast<const Part *>(w);
+        *reinterpret_cast<Part *>(p + o2) = *reinterpret_cast<const Part *>(w + N / 4);
     }
-    __device__ void unpack(float (&f)[8]) const
+    // Pairs of neighbours, or of the first half of the channels and the second.
+    template <bool INTERLEAVED>
+    __device__ Pairs<N> unpack() const
+    {
+        Pairs<N> x;
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            x.a[i] = INTERLEAVED ? Two(lo16(w[2 * i]), lo16(w[2 * i + 1])) : Two(lo16(w[i]), hi16(w[i]));
+            x.b[i] = INTERLEAVED ? Two(hi16(w[2 * i]), hi16(w[2 * i + 1])) : Two(lo16(w[N / 4 + i]), hi16(w[N / 4 + i]));
+        }
+        return x;
+    }
+    template <bool INTERLEAVED>
+    __device__ void pack(const Pairs<N> &x)
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[2 * i] = lo16(w[i]), f[2 * i + 1] = hi16(w[i]);
+        for (int i = 0; i < N / 4; ++i) {
+            float a0, a1, b0, b1;
+            x.a[i].apart(a0, a1);
+            x.b[i].apart(b0, b1);
+            w[INTERLEAVED ? 2 * i : i] = INTERLEAVED ? pack16(a0, b0) : pack16(a0, a1);
+            w[INTERLEAVED ? 2 * i + 1 : N / 4 + i] = INTERLEAVED ? pack16(a1, b1) : pack16(b0, b1);
+        }
     }
 };
 
@@ -79,149 +138,202 @@ __device__ __forceinline__ float head_sum(float v)
     return v;
 }
 
-// 1 / rms of a head, and its channels times what goes with it.  Squares that leave FP32's range
-// (heads of 2^58 and more, or tiny ones with next to no eps) are taken of the head times a power of two.
-template <int LPH>
-__device__ __forceinline__ float head_rstd(float (&x)[8], int D, float eps)
+template <int N, int LPH>
+__device__ __forceinline__ float head_squares(const Pairs<N> &x)
 {
-    float ss = 0.0f;
+    Two s(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        ss = fmaf(x[i], x[i], ss);
-    ss = head_sum<LPH>(ss);
-    float rstd = rsqrtf(ss / (float)D + eps);
-    const bool outside = !(ss < 0x1p120f && fmaf(eps, (float)D, ss) > 0x1p-90f);
+    for (int i = 0; i < N / 4; ++i)
+        s = fma(x.b[i], x.b[i], fma(x.a[i], x.a[i], s));
+    float a, b;
+    s.apart(a, b);
+    return head_sum<LPH>(a + b);
+}
+
+template <int N>
+__device__ __forceinline__ void scale(Pairs<N> &x, float f)
+{
+    const Two f2(f, f);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+        x.a[i] = mul(x.a[i], f2), x.b[i] = mul(x.b[i], f2);
+}
+
+// 1 / rms of a head, applied.  Heads whose squares leave FP32's range (of 2^58 and more, or tiny ones with next to
+// no eps) are taken times a power of two.
+template <int N, int LPH>
+__device__ __forceinline__ void normalise(Pairs<N> &x, float inv_d, float D, float eps)
+{
+    const float ss = head_squares<N, LPH>(x);
+    float rstd = rsqrtf(fmaf(ss, inv_d, eps));
+    const bool outside = !(ss < 0x1p120f && fmaf(eps, D, ss) > 0x1p-90f);
     if (__any_sync(~0u, outside)) {
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            top = fmaxf(top, fabsf(x[i]));
+        for (int i = 0; i < N / 4; ++i) {
+            float a, b, c, d;
+            x.a[i].apart(a, b);
+            x.b[i].apart(c, d);
+            top = fmaxf(fmaxf(fmaxf(top, fabsf(a)), fmaxf(fabsf(b), fabsf(c))), fabsf(d));
+        }
 #pragma unroll
         for (int d = LPH / 2; d; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        const int e = top > 0.0f && top <= 0x1.fffffep127f ? ilogbf(top) : 0;
-        float y[8], sy = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] = scalbnf(x[i], -e);
-            sy = fmaf(y[i], y[i], sy);
-        }
-        sy = head_sum<LPH>(sy);
-        const float ey = scalbnf(scalbnf(eps, -e), -e);  // (2^-2e by steps that FP32 holds)
-        if (outside && e != 0 && sy < 0x1p120f) {  // (a NaN or an infinity stays what it was)
-            rstd = rsqrtf(sy / (float)D + ey);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = y[i];
+        // 2^-e in two factors that FP32 holds; nothing is rounded on the way up, nor what counts on the way down
+        const int e = outside && top > 0.0f && top <= 0x1.fffffep127f ? ilogbf(top) : 0;
+        const float f0 = scalbnf(1.0f, -(e / 2)), f1 = scalbnf(1.0f, -(e - e / 2));
+        Pairs<N> y = x;
+        scale(y, f0);
+        scale(y, f1);
+        const float sy = head_squares<N, LPH>(y);
+        if (e != 0 && sy < 0x1p120f) {  // (a NaN or an infinity stays what it was)
+            rstd = rsqrtf(fmaf(sy, inv_d, eps * f0 * f0 * f1 * f1));
+            x = y;
         }
     }
-    return rstd;
+    scale(x, rstd);
 }
 
-// Block: token blockIdx.x and every gridDim.x-th after it, `passes` times kThreads / LPH heads from
-// blockIdx.y's on, in the order q, k, v.
-template <int LPH, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const HeadsParams p)
+// Block: `at_once` tokens from blockIdx.x * at_once on and every gridDim.x-th such group after them; a warp takes
+// 32 / LPH heads of a token at a time, in the order q, k, v.
+template <int N, int LPH, bool INTERLEAVED, bool NORM>
+__global__ void __launch_bounds__(kThreads, kBlocks) heads_kernel(const HeadsParams p)
 {
-    constexpr int HPP = kThreads / LPH;
-    __shared__ float2 turn[2][DEP_HEADS_MAX_D / 2];  // cos, sin of a token's angles, times the amplitude
-    const int tid = threadIdx.x, c = tid % LPH, heads = p.Hq + p.Hk + (p.vc ? p.Hk : 0);
-    const int h0 = blockIdx.y * p.passes * HPP + tid / LPH;
-    const bool lane = 8 * c < p.D;
-    int o1 = 8 * c, o2 = 8 * c + 4, pair = -1;
-    if (8 * c >= p.first && 8 * c < p.first + p.rot) {
-        pair = 4 * c - p.first / 2;
+    constexpr int HPW = 32 / LPH, W = kThreads / 32;
+    // What a lane takes for two pairs at once, lanes side by side: cos, cos, sin, sin of their angles, times the
+    // amplitude, for each token; and the weights of q and of k, as a, a, b, b.
+    __shared__ float4 turn[2][kTokens * DEP_HEADS_MAX_D / 4];
+    __shared__ float4 weights[2][N / 4][LPH];
+    __shared__ uint64_t per[DEP_HEADS_MAX_D / 2];  // of a turn a position
+    const int tid = threadIdx.x, lane = tid % 32, c = lane % LPH, warp = tid / 32;
+    const int keys = p.Hq + p.Hk, heads = keys + (p.vc ? p.Hk : 0), pairs = p.rot / 2, lanes = p.rot / N;
+    const bool in = N * c < p.D;
+    int o1 = N * c, o2 = N * c + N / 2, pair = -1;
+    if (N * c >= p.first && N * c < p.first + p.rot) {
+        pair = N / 2 * c - p.first / 2;
         if (!INTERLEAVED)
-            o1 = p.first + pair, o2 = o1 + p.rot / 2;
+            o1 = p.first + pair, o2 = o1 + pairs;
     }
-    uint64_t per = 0;  // of a turn a position
-    if (tid < p.rot / 2) {
+    griddep_launch_dependents();
+    griddep_wait();  // what comes before may write the inputs, and read or write the outputs
+    if (tid < pairs) {
         double t = p.freqs[tid] * 0.15915494309189535;  // 1 / 2 pi
         t -= floor(t);
-        per = __double2ull_rn(t * 18446744073709551616.0);
+        per[tid] = __double2ull_rn(t * 18446744073709551616.0);
     }
-    Lane wq{{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}}, wk = wq;
-    if (NORM && lane && p.qw)
-        wq.load(p.qw, o1, o2);
-    if (NORM && lane && p.kw)
-        wk.load(p.kw, o1, o2);
-
-    int buf = 0;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x, buf ^= 1) {
-        const uint16_t *q = p.q + t * p.qs, *k = p.k + t * p.ks, *v = p.v + t * p.vs;
-        const auto source = [&](int h) {
-            return h < p.Hq ? q + h * p.D : h < p.Hq + p.Hk ? k + (h - p.Hq) * p.D : v + (h - p.Hq - p.Hk) * p.D;
-        };
-        Lane next{};
-        if (lane && h0 < heads)
-            next.load(source(h0), o1, o2);
-        int64_t ko = 0, vo = 0;
-        bool keep = true;
-        if (p.kc) {
-            const int32_t slot = p.slots[t];
-            const int32_t pg = slot / p.page, at = slot - pg * p.page;
-            keep = slot >= 0 && pg < p.n_pages;
-            ko = pg * p.kps + at * p.kss;
-            vo = pg * p.vps + at * p.vss;
+    if (NORM && tid < 2 * LPH && in) {  // (lane c of the first groups: its own channels)
+        const uint16_t *const w = tid < LPH ? p.qw : p.kw;
+        Lane<N> own;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            own.w[i] = 0x3F803F80u;
+        if (w)
+            own.load(w, o1, o2);
+        const Pairs<N> x = own.template unpack<INTERLEAVED>();
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            float4 f;
+            x.a[i].apart(f.x, f.y);
+            x.b[i].apart(f.z, f.w);
+            weights[tid / LPH][i][c] = f;
         }
-        if (tid < p.rot / 2) {
-            const uint64_t u = per * (uint64_t)(int64_t)p.positions[t];
+    }
+    const float inv_d = 1.0f / (float)p.D, dim = (float)p.D;
+
+    // This warp's tasks, one after another: token t0 + tok, heads HPW * g on, where t0 is a group's first token.
+    const int64_t stride = (int64_t)gridDim.x * p.at_once;
+    const int g0 = blockIdx.y * W + warp, step = gridDim.y * W;
+    int64_t t0 = (int64_t)blockIdx.x * p.at_once;
+    const auto count = [&](int64_t t0) { return (int)min((int64_t)p.at_once, p.tokens - t0); };
+    const auto settle = [&](int &tok, int &g, int n) {  // a group past a token's last goes on with the next token
+        while (g >= p.tasks && tok < n)
+            g -= p.tasks, ++tok;
+    };
+    Lane<N> next{};
+    const auto fetch = [&](int64_t t, int g) {
+        const int h = HPW * g + lane / LPH;
+        if (in && h < heads)
+            next.load(h < p.Hq ? p.q + t * p.qs + h * p.D : h < keys ? p.k + t * p.ks + (h - p.Hq) * p.D : p.v + t * p.vs + (h - keys) * p.D, o1, o2);
+    };
+    int n = count(t0), tok = 0, g = g0, buf = 0;
+    settle(tok, g, n);
+    if (tok < n)
+        fetch(t0 + tok, g);
+    __syncthreads();  // the frequencies
+    for (; t0 < p.tokens; t0 += stride, buf ^= 1) {
+        n = count(t0);
+        for (int i = tid; i < n * pairs; i += kThreads) {
+            const int j = i / pairs, k = i - j * pairs;
+            const uint64_t u = per[k] * (uint64_t)(int64_t)p.positions[t0 + j];
             float s, co;
             sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &s, &co);
-            turn[buf][tid] = make_float2(co * p.amplitude, s * p.amplitude);
+            const int l = k / (N / 2), m = k % (N / 2);
+            float *const at = reinterpret_cast<float *>(&turn[buf][j * (pairs / 2) + m / 2 * lanes + l]) + (m & 1);
+            at[0] = co * p.amplitude;
+            at[2] = s * p.amplitude;
         }
-        __syncthreads();  // (the other buffer is read by the token before, done where this one's is written again)
-        float2 cs[4] = {{1, 0}, {1, 0}, {1, 0}, {1, 0}};
-        if (pair >= 0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                cs[i] = turn[buf][pair + i];
-        for (int i = 0, h = h0; i < p.passes; ++i, h += HPP) {
-            Lane now = next;
-            if (i + 1 < p.passes && lane && h + HPP < heads)
-                next.load(source(h + HPP), o1, o2);
-            if (h < p.Hq + p.Hk || NORM) {  // (all lanes of a warp take part in a sum)
-                float x[8], w[8];
-                now.unpack(x);
-                if (NORM) {
-                    const float rstd = head_rstd<LPH>(x, p.D, p.eps);
-                    (h < p.Hq ? wq : wk).unpack(w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[j] = x[j] * rstd * w[j];
-                }
-                if (h < p.Hq + p.Hk) {
-                    if (pair >= 0)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float &a = x[INTERLEAVED ? 2 * j : j], &b = x[INTERLEAVED ? 2 * j + 1 : j + 4];
-                            const float a0 = a;
-                            a = fmaf(a0, cs[j].x, -(b * cs[j].y));
-                            b = fmaf(b, cs[j].x, a0 * cs[j].y);
-                        }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        now.w[j] = pack16(x[2 * j], x[2 * j + 1]);
-                }
+        __syncthreads();  // (the other buffer is read for the tokens before, done where this one's is written again)
+        while (tok < n) {
+            Lane<N> now = next;
+            const int h = HPW * g + lane / LPH, at = tok;
+            const bool values = HPW * g >= keys;  // all of the warp's heads
+            g += step;
+            settle(tok, g, n);
+            if (tok < n)
+                fetch(t0 + tok, g);
+            else if (t0 + stride < p.tokens) {  // the first task among the next tokens
+                int tok1 = 0, g1 = g0;
+                const int n1 = count(t0 + stride);
+                settle(tok1, g1, n1);
+                if (tok1 < n1)
+                    fetch(t0 + stride + tok1, g1);
             }
-            if (!lane || h >= heads)
+            if (!values) {
+                Pairs<N> x = now.template unpack<INTERLEAVED>();
+                if (NORM) {
+                    normalise<N, LPH>(x, inv_d, dim, p.eps);
+#pragma unroll
+                    for (int i = 0; i < N / 4; ++i) {
+                        const float4 f = weights[h >= p.Hq][i][c];
+                        x.a[i] = mul(x.a[i], Two(f.x, f.y)), x.b[i] = mul(x.b[i], Two(f.z, f.w));
+                    }
+                }
+                if (pair >= 0)
+#pragma unroll
+                    for (int i = 0; i < N / 4; ++i) {
+                        const float4 f = turn[buf][at * (pairs / 2) + i * lanes + pair / (N / 2)];
+                        const Two cos(f.x, f.y), sin(f.z, f.w), a = x.a[i];
+                        x.a[i] = sub(mul(a, cos), mul(x.b[i], sin));
+                        x.b[i] = fma(x.b[i], cos, mul(a, sin));
+                    }
+                if (h < keys)
+                    now.template pack<INTERLEAVED>(x);
+            }
+            if (!in || h >= heads)
                 continue;
+            const int64_t t = t0 + at;
             if (h < p.Hq)
                 now.store(p.q_out + t * p.qos + h * p.D, o1, o2);
             else if (!p.kc)
                 now.store(p.k_out + t * p.kos + (h - p.Hq) * p.D, o1, o2);
-            else if (keep) {
-                const int hk = h - p.Hq;
-                if (hk < p.Hk)
-                    now.store(p.kc + ko + hk * p.khs, o1, o2);
+            else {
+                const int32_t slot = p.slots[t], pg = slot / p.page, place = slot - pg * p.page;
+                if (slot < 0 || pg >= p.n_pages)
+                    continue;
+                if (h < keys)
+                    now.store(p.kc + pg * p.kps + place * p.kss + (h - p.Hq) * p.khs, o1, o2);
                 else
-                    now.store(p.vc + vo + (hk - p.Hk) * p.vhs, o1, o2);
+                    now.store(p.vc + pg * p.vps + place * p.vss + (h - keys) * p.vhs, o1, o2);
             }
+        }
+        if (t0 + stride < p.tokens) {
+            tok = 0, g = g0;
+            settle(tok, g, count(t0 + stride));
         }
     }
 }
 
-template <int LPH, bool INTERLEAVED, bool NORM>
+template <int N, int LPH, bool INTERLEAVED, bool NORM>
 cudaError_t heads_launch(HeadsParams p, cudaStream_t s)
 {
     int dev = 0, sms = 0;
@@ -230,24 +342,36 @@ cudaError_t heads_launch(HeadsParams p, cudaStream_t s)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    constexpr int HPP = kThreads / LPH;
-    const int heads = p.Hq + p.Hk + (p.vc ? p.Hk : 0), all = (heads + HPP - 1) / HPP;
-    // A token's heads are spread over blocks only while there are too few tokens to fill the GPU: each
-    // block works the angles out anew.
-    const int64_t x = std::min<int64_t>(p.tokens, 24ll * sms);
-    const int y = (int)std::min<int64_t>(all, (8ll * sms + x - 1) / x);
-    p.passes = (all + y - 1) / y;
-    heads_kernel<LPH, INTERLEAVED, NORM><<<dim3((unsigned)x, (unsigned)((all + p.passes - 1) / p.passes)), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    constexpr int HPW = 32 / LPH, W = kThreads / 32;
+    const int heads = p.Hq + p.Hk + (p.vc ? p.Hk : 0);
+    p.tasks = (heads + HPW - 1) / HPW;
+    // The tokens in rounds of equal size over all blocks; a token's heads are spread over blocks while there are
+    // too few tokens (each block works the angles out anew).
+    const int64_t most = (int64_t)kBlocks * sms;
+    const int64_t room = p.rot ? std::min(kTokens * DEP_HEADS_MAX_D / p.rot, kMostTokens) : kMostTokens,
+                  rounds = (p.tokens + most * room - 1) / (most * room);
+    p.at_once = (int)((p.tokens + most * rounds - 1) / (most * rounds));
+    const int64_t groups = (p.tokens + p.at_once - 1) / p.at_once, x = std::min(groups, most);
+    const int y = (int)std::min<int64_t>((p.tasks + W - 1) / W, (most + x - 1) / x);
+    cudaLaunchAttribute attr{};  // starts early, and waits inside
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)x, (unsigned)y);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, heads_kernel<N, LPH, INTERLEAVED, NORM>, p);
 }
 
-template <int LPH>
+template <int N, int LPH>
 cudaError_t heads_dispatch(const HeadsParams &p, uint32_t flags, cudaStream_t s)
 {
     const bool n = flags & DEP_HEADS_NORM;
     if (flags & DEP_HEADS_INTERLEAVED)
-        return n ? heads_launch<LPH, true, true>(p, s) : heads_launch<LPH, true, false>(p, s);
-    return n ? heads_launch<LPH, false, true>(p, s) : heads_launch<LPH, false, false>(p, s);
+        return n ? heads_launch<N, LPH, true, true>(p, s) : heads_launch<N, LPH, true, false>(p, s);
+    return n ? heads_launch<N, LPH, false, true>(p, s) : heads_launch<N, LPH, false, false>(p, s);
 }
 
 dep_status_t heads_entry(const dep_heads_args_t *a, bool append, void *stream)
@@ -328,9 +452,11 @@ dep_status_t heads_entry(const dep_heads_args_t *a, bool append, void *stream)
         p.Hk = 0;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = a->D <= 64    ? heads_dispatch<8>(p, a->flags, s)
-                          : a->D <= 128 ? heads_dispatch<16>(p, a->flags, s)
-                                        : heads_dispatch<32>(p, a->flags, s);
+    const bool wide = a->D % 16 == 0 && a->rot % 16 == 0 && a->first % 16 == 0;  // sixteen channels a lane
+    const cudaError_t e = a->D <= 64    ? wide ? heads_dispatch<16, 4>(p, a->flags, s) : heads_dispatch<8, 8>(p, a->flags, s)
+                          : a->D <= 128 ? wide ? heads_dispatch<16, 8>(p, a->flags, s) : heads_dispatch<8, 16>(p, a->flags, s)
+                          : wide        ? heads_dispatch<16, 16>(p, a->flags, s)
+                                        : heads_dispatch<8, 32>(p, a->flags, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return DEP_ERR_CUDA;
