@@ -45,7 +45,7 @@ constexpr int kMasks = 8;   // tiles whose masks are held
 constexpr int kAhead = 4;   // items whose descriptions are held
 constexpr int kCost = 3;     // tiles' worth of work that an item costs beside its tiles,
 constexpr int kCostTwo = 5;  // and one with two tiles of rows
-constexpr int kLeast = 4;   // units of a block at least: fewer are not worth the joining
+constexpr int kLeast = 1;   // units of a block at least
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 struct AttnParams {
@@ -840,7 +840,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
         const int64_t token = it.first + tok;
         const uint64_t word = tree && live ? p.tree[token] : 0;
         const int clear = it.own + (tree ? 0 : __shfl_sync(~0u, tok, 0) + 1);  // all positions before it are seen by all of the warp's rows
-        float m = -INFINITY, l = 0.0f;  // m: log2 units
+        float m = 0.0f, l = 0.0f;  // m: log2 units
         int t = it.t0 + (two ? 0 : g);
         const bool some = t < it.t1;
         for (bool first = true; t < it.t1; t += two ? 1 : 2, first = false, ++k) {
@@ -850,13 +850,15 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
             tc::fence_after();
             if (warp_live) {
                 const uint4 in = *reinterpret_cast<const uint4 *>(sm.masks[(kt + (t - it.t0)) % kMasks]);
-                // What is taken off, m, moves only where P would grow past 2^12: then O is seldom scaled, and P is
-                // worked out with the m so far, anew if its sum (in which a NaN shows as well) says that m has to move.
-                bool anew = first || (t + 1) * kTile > clear || (in.x & in.y & in.z & in.w) != ~0u;
+                // P and its sum keep their precision at any size, so what is taken off, m, is zero to begin with and moves
+                // only where P would grow past 2^12, or all that was seen stays below 2^-40: then O has seldom
+                // to be scaled, and one pass over the scores does.  The sum (in which a NaN shows as well) tells; with another m
+                // the tile is taken anew.
+                bool anew = (t + 1) * kTile > clear || (in.x & in.y & in.z & in.w) != ~0u;
                 if (!anew) {
                     uint32_t pk[2][32];
                     const float sum = tile_exp(s_at, c, -m, pk);
-                    anew = __any_sync(~0u, live && !(sum <= 4096.0f));
+                    anew = __any_sync(~0u, live && !(sum <= 4096.0f && l + sum >= 0x1p-40f));
                     if (!anew) {
                         l += sum;
                         tmem_st32(s_at, pk[0]);
@@ -877,9 +879,9 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                             top = fmaxf(top, see >> j & 1 ? __uint_as_float(v[j]) : -INFINITY);
                     }
                     const float tm = top * c;
-                    const bool up = live && (tm > m + 5.0f || (m == -INFINITY && tm > -INFINITY));
+                    const bool fresh = l == 0.0f, up = live && (tm > m + 5.0f || (fresh && tm > -INFINITY));
                     if (__any_sync(~0u, up)) {
-                        const float f = up ? ex2(m - tm) : 1.0f;
+                        const float f = !up ? 1.0f : fresh ? 0.0f : ex2(m - tm);
                         if (up)
                             m = tm;
                         l *= f;
@@ -895,7 +897,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                                 tmem_st16(o_at + 16 * w, v);
                             }
                     }
-                    const float off = m == -INFINITY ? 0.0f : -m;
+                    const float off = -m;
 #pragma unroll 1
                     for (int w = 0; w < 4; ++w) {  // (P's columns lie in those of scores already read)
                         uint32_t v[32], pk[16];
@@ -924,6 +926,8 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
             if (lane == 0)
                 mbar_arrive(smem_u32(&sm.p_full[g]));
         }
+        if (l == 0.0f)
+            m = -INFINITY;  // nothing seen
         kt += it.t1 - it.t0;
         if (some) {
             ok = ok && wait_warp(sm, sm.o_full[g], items & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);

@@ -395,3 +395,42 @@ def test_a_run_of_them_as_used(dep):
                 off = 8 * 2.0 ** -7 / math.sqrt(3 * d) * d ** -0.5 * float((yq[t: t + n, h].abs() @ K[:, h // 3].abs().T).max())
                 assert ((o[t: t + n, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2 * off) * size).all()
             t += n
+
+
+@pytest.mark.parametrize("shift", [-300.0, -60.0, -30.0, 30.0, 200.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_far_from_zero(dep, shift, d):
+    """All scores of a row near one value, low or high; and contexts where they change sides half way."""
+    c = Case([(2, 900), (70, 300), (1, 20)], 12, 2, d, 16)
+    c.q[...] = (c.q.float() * 0.1 + 1).bfloat16()
+    for s in range(3):
+        move = torch.full((c.lens[s], 1, 1), shift / d ** 0.5, device="cuda")
+        if s < 2:
+            move[c.lens[s] // 2:] *= 0.25 if shift < 0 else -0.5
+        c.keys[s] = (c.keys[s].float() * 0.2 + move).bfloat16()
+    c.fill()
+    c.check(c.run(dep))
+
+
+def test_runs_of_sequences_of_a_tile(dep):
+    """Many items of one or two tiles for each block, with and without a second tile of rows."""
+    g = torch.Generator().manual_seed(1)
+    seqs = [(1 if i % 4 else 30, int(torch.randint(0, 200, (1,), generator=g))) for i in range(300)]
+    go(dep, seqs, 12, 2, 128, 16)
+    go(dep, seqs, 12, 2, 64, 8, tree=True)
+
+
+def test_first_tiles_that_a_row_does_not_see(dep):
+    """Whole tiles outside the pool before scores far below zero."""
+    c = Case([(1, 700), (3, 500)], 8, 2, 128, 16)
+    seen = [c.seen(0), c.seen(1)]
+    for s in range(2):
+        c.keys[s] = (c.keys[s].float() * 0.1 - 25).bfloat16()
+        c.table[s, :20] = -1
+        seen[s][:, :320] = False
+    c.q[...] = (c.q.float() * 0.1 + 1).bfloat16()
+    for s in range(2):
+        at = torch.arange(320, c.lens[s], device="cuda")
+        pg = c.table[s].long()[at // 16]
+        c.k[pg, at % 16], c.v[pg, at % 16] = c.keys[s][320:], c.values[s][320:]
+    c.check(c.run(dep), seen)
