@@ -518,12 +518,7 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
         if (values)
             rows();
         for (int i = 0; i < n; ++i) {
-            need(sm.empty[ring], lap);
-            if (!ok)
-                break;
             const int t = it.t0 + i, slot = ring;
-            if (++ring == (values ? S::kSlots : S::kKeySlots))
-                ring = values ? S::kKeySlots : 0, lap ^= 1;
             const int32_t page = (uint32_t)next_page < (uint32_t)p.n_pages ? next_page : -1, in_page = next_slot;
             if (t + 1 < it.t1)
                 next_page = look(t + 1, next_slot);
@@ -556,6 +551,12 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
                 to = 16 * value_steps(it.end, t), end = it.end - t * kTile;
                 from = max(0, min(it.shared - t * kTile, to));
             }
+            // (everything is worked out by now: a slot that has come free is filled at once)
+            need(sm.empty[slot], lap);
+            if (!ok)
+                break;
+            if (++ring == (values ? S::kSlots : S::kKeySlots))
+                ring = values ? S::kKeySlots : 0, lap ^= 1;
             if (boxes) {
                 const uint32_t bar = smem_u32(from < to ? &sm.landed[boxed % kLanded] : &sm.full[slot]);
                 if (lane == 0)
