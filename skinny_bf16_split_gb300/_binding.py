@@ -11,7 +11,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
+from sys import modules as _modules
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libdep_projection.so")
@@ -480,9 +482,14 @@ class Projection:
 _QUANT = {None: DEP_QUANT_NONE, "int8": DEP_QUANT_INT8, "e4m3": DEP_QUANT_E4M3}
 
 
+def _torch():
+    """torch, which whoever has a tensor has imported (an import statement in a function takes five times as long)."""
+    return _modules.get("torch") or importlib.import_module("torch")
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to the stream of the call that writes it."""
-    import torch
+    torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
@@ -491,7 +498,7 @@ def _empty(shape, dtype, device, stream):
 
 def _on(index, call, args, stream):
     """call(args, stream) with device `index` current; stream None: its current stream."""
-    import torch
+    torch = _torch()
     if index == torch._C._cuda_getDevice():  # (torch.cuda.current_device takes twice as long)
         call(args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
         return
@@ -509,7 +516,7 @@ def _rows(t, name, dtype, index, shape):
 
 
 def _norm_call(call, x, weight, residual, residual_out, eps, quant, out, out_scale, stream):
-    import torch
+    torch = _torch()
     if quant not in _QUANT:
         raise ValueError("quant must be None, 'int8' or 'e4m3'")
     shape, dev, bf16 = x.shape, x.get_device(), torch.bfloat16
@@ -599,7 +606,7 @@ def gated_delta_rule(q, k, v, g, beta, state=None, state_out=None, *, cu_seqlens
     (outside 0..n_states-1: padding).  scale defaults to Dk ** -0.5.  The workspace
     is the allocator's (up to 2 GiB, for sequences of eight tokens and more on
     average).  Returns out, bfloat16 [tokens, Hv, Dv] (allocated where omitted)."""
-    import torch
+    torch = _torch()
     dev, bf16, f32 = q.get_device(), torch.bfloat16, torch.float32
     qk_shape, v_shape = q.shape, v.shape
     if len(qk_shape) != 3 or len(v_shape) != 3 or dev < 0:
@@ -743,7 +750,7 @@ def _vector(t, name, dtype, index, n):
 
 def _cache(t, name, index, shape):
     """Strides between pages, slots and heads of a cache [pages, page_size, heads, d]."""
-    import torch
+    torch = _torch()
     if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == index:
         page, slot, head, channel = t.stride()
         if channel == 1:
@@ -761,7 +768,7 @@ def _cache_shape(k_cache, heads, d):
 
 def _rotation(dev, tokens, d, positions, freqs, norm, q_weight, k_weight):
     """(q_weight, k_weight, freqs, positions) as addresses, and how many channels are rotated."""
-    import torch
+    torch = _torch()
     if (positions is None) != (freqs is None):
         raise ValueError("positions and freqs must be given together")
     f = p = qw = kw = None
@@ -792,7 +799,7 @@ def norm_rotate(q, k=None, positions=None, freqs=None, *, interleaved: bool = Fa
     the channels [first, first + rot) of each head by halves, or by neighbours (interleaved).
     q_weight, k_weight: bfloat16 [D].  q_out and k_out are allocated where omitted; they may be q and k.
     Returns (q_out, k_out), or q_out alone without k."""
-    import torch
+    torch = _torch()
     dev, bf16, shape = q.get_device(), torch.bfloat16, q.shape
     if len(shape) != 3 or dev < 0 or (k is not None and len(k.shape) != 3):
         raise ValueError("q [tokens, Hq, D] and k [tokens, Hk, D] must be CUDA tensors of three dimensions")
@@ -830,7 +837,7 @@ def append_kv(k, v, k_cache, v_cache, slots, positions=None, freqs=None, *, inte
     of [pages, Hk, page_size, D] is a cache by heads).  slots: int32 [tokens], page * page_size + place;
     outside the cache: padding, not stored.  Returns q_out (allocated where omitted; may be q), or None
     without q."""
-    import torch
+    torch = _torch()
     dev, bf16, shape = k.get_device(), torch.bfloat16, k.shape
     if len(shape) != 3 or dev < 0 or (q is not None and len(q.shape) != 3):
         raise ValueError("k, v [tokens, Hk, D] and q [tokens, Hq, D] must be CUDA tensors of three dimensions")
@@ -876,7 +883,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None
     sees its sequence's i-th new token (drafts of up to 64); None: every token sees those up to itself.
     scale defaults to D ** -0.5.  lse: float32 [tokens, Hq], filled in where given.  The workspace is the
     allocator's.  Returns out, bfloat16 [tokens, Hq, D] (allocated where omitted)."""
-    import torch
+    torch = _torch()
     dev, bf16, i32, shape = q.get_device(), torch.bfloat16, torch.int32, q.shape
     if len(shape) != 3 or dev < 0 or len(k_cache.shape) != 4:
         raise ValueError("q must be a CUDA tensor [tokens, Hq, D] and k_cache one of four dimensions")
