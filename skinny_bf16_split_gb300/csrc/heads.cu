@@ -33,6 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlocks = 3;    // of an SM
 constexpr int kMostTokens = 16;
+constexpr int kStages = 4;    // tasks of a warp in flight, where it has many
 constexpr int kTokens = 4;    // whose angles a block has room for, of the widest heads
 
 struct HeadsParams {
@@ -93,6 +94,19 @@ template <int N>
 struct Lane {
     uint32_t w[N / 2];
     using Part = typename std::conditional<N == 16, uint4, uint2>::type;
+    // On the way through shared memory: the lanes' first halves, then their second ones.
+    static __device__ void fetch(Part *to, const uint16_t *p, int o1, int o2)
+    {
+        const uint32_t at = smem_u32(to);
+        static_assert(N == 16, "copies of 16 bytes");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(p + o1) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 32 * N), "l"(p + o2) : "memory");
+    }
+    __device__ void arrive(const Part *from)
+    {
+        *reinterpret_cast<Part *>(w) = from[0];
+        *reinterpret_cast<Part *>(w + N / 4) = from[32];
+    }
     __device__ void load(const uint16_t *p, int o1, int o2)
     {
         *reinterpret_cast<Part *>(w) = *reinterpret_cast<const Part *>(p + o1);
@@ -196,7 +210,7 @@ __device__ __forceinline__ void normalise(Pairs<N> &x, float inv_d, float D, flo
 
 // Block: `at_once` tokens from blockIdx.x * at_once on and every gridDim.x-th such group after them; a warp takes
 // 32 / LPH heads of a token at a time, in the order q, k, v.
-template <int N, int LPH, bool INTERLEAVED, bool NORM>
+template <int N, int LPH, bool INTERLEAVED, bool NORM, bool STAGED>
 __global__ void __launch_bounds__(kThreads, kBlocks) heads_kernel(const HeadsParams p)
 {
     constexpr int HPW = 32 / LPH, W = kThreads / 32;
@@ -204,6 +218,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) heads_kernel(const HeadsPar
     // amplitude, for each token; and the weights of q and of k, as a, a, b, b.
     __shared__ float4 turn[2][kTokens * DEP_HEADS_MAX_D / 4];
     __shared__ float4 weights[2][N / 4][LPH];
+    using Part = typename Lane<N>::Part;
+    __shared__ Part flight[STAGED ? W : 1][kStages][64];  // what each lane has fetched for itself
     __shared__ uint64_t per[DEP_HEADS_MAX_D / 2];  // of a turn a position
     const int tid = threadIdx.x, lane = tid % 32, c = lane % LPH, warp = tid / 32;
     const int keys = p.Hq + p.Hk, heads = keys + (p.vc ? p.Hk : 0), pairs = p.rot / 2, lanes = p.rot / N;
@@ -249,16 +265,42 @@ __global__ void __launch_bounds__(kThreads, kBlocks) heads_kernel(const HeadsPar
         while (g >= p.tasks && tok < n)
             g -= p.tasks, ++tok;
     };
-    Lane<N> next{};
-    const auto fetch = [&](int64_t t, int g) {
-        const int h = HPW * g + lane / LPH;
-        if (in && h < heads)
-            next.load(h < p.Hq ? p.q + t * p.qs + h * p.D : h < keys ? p.k + t * p.ks + (h - p.Hq) * p.D : p.v + t * p.vs + (h - keys) * p.D, o1, o2);
+    const auto source = [&](int64_t t, int h) {
+        return h < p.Hq ? p.q + t * p.qs + h * p.D : h < keys ? p.k + t * p.ks + (h - p.Hq) * p.D : p.v + t * p.vs + (h - keys) * p.D;
     };
     int n = count(t0), tok = 0, g = g0, buf = 0;
     settle(tok, g, n);
-    if (tok < n)
-        fetch(t0 + tok, g);
+    // Loads run ahead of the tasks, over the groups' ends: one task in registers, or kStages - 1 of them in shared memory.
+    Lane<N> next{};
+    const auto load = [&](int64_t t, int g) {
+        const int h = HPW * g + lane / LPH;
+        if (in && h < heads)
+            next.load(source(t, h), o1, o2);
+    };
+    int64_t f0 = t0;
+    int fn = n, ftok = 0, fg = g0, in_stage = 0, out_stage = 0;
+    const auto fetch = [&] {
+        if constexpr (STAGED) {
+            settle(ftok, fg, fn);
+            while (ftok >= fn && f0 < p.tokens) {
+                f0 += stride;
+                fn = f0 < p.tokens ? count(f0) : 0, ftok = 0, fg = g0;
+                settle(ftok, fg, fn);
+            }
+            const int h = HPW * fg + lane / LPH;
+            if (f0 < p.tokens && in && h < heads)
+                Lane<N>::fetch(&flight[warp][in_stage][lane], source(f0 + ftok, h), o1, o2);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            in_stage = in_stage + 1 == kStages ? 0 : in_stage + 1;
+            fg += step;
+        }
+    };
+    if constexpr (STAGED) {
+#pragma unroll
+        for (int i = 0; i + 1 < kStages; ++i)
+            fetch();
+    } else if (tok < n)
+        load(t0 + tok, g);
     __syncthreads();  // the frequencies
     for (; t0 < p.tokens; t0 += stride, buf ^= 1) {
         n = count(t0);
@@ -279,14 +321,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks) heads_kernel(const HeadsPar
             const bool values = HPW * g >= keys;  // all of the warp's heads
             g += step;
             settle(tok, g, n);
-            if (tok < n)
-                fetch(t0 + tok, g);
+            if constexpr (STAGED) {
+                fetch();
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+                if (in && h < heads)
+                    now.arrive(&flight[warp][out_stage][lane]);
+                out_stage = out_stage + 1 == kStages ? 0 : out_stage + 1;
+            } else if (tok < n)
+                load(t0 + tok, g);
             else if (t0 + stride < p.tokens) {  // the first task among the next tokens
                 int tok1 = 0, g1 = g0;
                 const int n1 = count(t0 + stride);
                 settle(tok1, g1, n1);
                 if (tok1 < n1)
-                    fetch(t0 + stride + tok1, g1);
+                    load(t0 + stride + tok1, g1);
             }
             if (!values) {
                 Pairs<N> x = now.template unpack<INTERLEAVED>();
@@ -362,7 +410,12 @@ cudaError_t heads_launch(HeadsParams p, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, heads_kernel<N, LPH, INTERLEAVED, NORM>, p);
+    // Many tasks for a warp pay for the way through shared memory: 8192 tokens of 104 heads, 59 tasks a warp, 71.7 us
+    // against 79.1; 8192 of 16, nine a warp, 18.5 against 17.6, 1037 of 24, two a warp, 5.1 against 4.6.
+    if constexpr (N == 16)
+        if (rounds * p.at_once * p.tasks / ((int64_t)W * y) >= 24)
+            return cudaLaunchKernelEx(&cfg, heads_kernel<N, LPH, INTERLEAVED, NORM, true>, p);
+    return cudaLaunchKernelEx(&cfg, heads_kernel<N, LPH, INTERLEAVED, NORM, false>, p);
 }
 
 template <int N, int LPH>
