@@ -102,7 +102,8 @@ struct Smem {
     float2 ml[kTile];     // the second group's m and sum
     int64_t scan[kWarps];
     int64_t begin, left, unit0;  // this block's range, and the units before its first sequence
-    int32_t seq;
+    int64_t first;  // its first sequence: as in Seq
+    int32_t seq, n, len;
     uint32_t tmem;
     int32_t dead;  // a wait gave up
 };
@@ -126,6 +127,10 @@ struct Seq {
         first = seq_start(p, s);
         n = (int32_t)max(seq_start(p, s + 1) - first, (int64_t)0);
         len = min(max(l, 0), p.most);
+        derive(p);
+    }
+    __device__ void derive(const AttnParams &p)
+    {
         rows = n * p.G;
         blocks = (rows + kBlockRows - 1) / kBlockRows;
     }
@@ -169,10 +174,9 @@ struct Items {
     int64_t unit, at, left;  // the item's first unit, where in it the range goes on, units left of the range
     __device__ int cost() const { return q.cost(rb); }
     // Go to unit `begin` of the units from sequence `seq` on, which starts at unit0.
-    __device__ void start(const AttnParams &p, int seq, int64_t unit0, int64_t begin, int64_t count)
+    __device__ void start(const AttnParams &p, const Seq &first, int seq, int64_t unit0, int64_t begin, int64_t count)
     {
-        s = seq, left = count;
-        q.load(p, s);
+        s = seq, left = count, q = first;
         const int64_t head = q.head_units(p), skip = divide(begin - unit0, head);
         kv_head = (int)skip;
         unit = unit0 + skip * head;
@@ -464,7 +468,12 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
     };
     Items list;
     if (!values)
-        list.start(p, sm.seq, sm.unit0, sm.begin, sm.left);
+    {
+        Seq q;
+        q.first = sm.first, q.n = sm.n, q.len = sm.len;
+        q.derive(p);
+        list.start(p, q, sm.seq, sm.unit0, sm.begin, sm.left);
+    }
     for (;; ++item) {
         if (!values) {  // tells the others
             const Item it = list.take(p);
@@ -500,14 +509,14 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
             return (uint32_t)g < (uint32_t)p.n_pages ? g : -1;
         };
         int next_slot, next_page = look(it.t0, next_slot);
-        // Rows: each warp fetches half of a tile, the keys' after its first tile of keys.
+        // Rows: each warp fetches half of a tile, the values' the first one, the keys' its own after its first tile of keys.
         const auto rows = [&] {
             for (int h = 0; h < (two ? 2 : 1); ++h) {
-                const int b = (qc + h) & 1, r0 = kTile * h + (values ? kTile / 2 : 0);
+                const int b = (qc + h) & 1, r0 = kTile * h + (values ? 0 : kTile / 2);
                 need(sm.q_empty[b], ((uint32_t)((qc + h) >> 1) & 1) ^ 1);
                 if (!ok)
                     return;
-                gather<D>(smem_u32(sm.q[b]) + (values ? kTile / 2 * 128 : 0), min(kTile / 2, it.rows - r0), p.q, [&](int i) -> const uint16_t * {
+                gather<D>(smem_u32(sm.q[b]) + (values ? 0 : kTile / 2 * 128), min(kTile / 2, it.rows - r0), p.q, [&](int i) -> const uint16_t * {
                     const int r = r0 + 32 * i + lane;
                     const uint32_t row = it.row0 + r, tok = row / (uint32_t)p.G;
                     return r < it.rows ? p.q + (it.first + tok) * p.qs + (int32_t)(it.kv_head * p.G + (row - tok * p.G)) * D : nullptr;
@@ -1082,9 +1091,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // The range.  Every thread adds up the units of its share of the sequences.
     const int per = (p.n_seq + kThreads - 1) / kThreads, s0 = min(p.n_seq, (int)threadIdx.x * per), s1 = min(p.n_seq, s0 + per);
     int64_t mine = 0;
+    Seq q;
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-        Seq q;
         q.load(p, s);
         mine += q.head_units(p) * p.Hk;
     }
@@ -1111,16 +1120,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int64_t begin = parts.begin(blockIdx.x), end = parts.begin(blockIdx.x + 1);
     if ((int)blockIdx.x < blocks && begin < end && begin >= before && begin < before + mine) {
         int s = s0;
+        if (s1 - s0 > 1)  // (else q is still the sequence)
 #pragma unroll 1
-        for (; s + 1 < s1; ++s) {
-            Seq q;
-            q.load(p, s);
-            const int64_t u = q.head_units(p) * p.Hk;
-            if (begin < before + u)
-                break;
-            before += u;
-        }
-        sm.seq = s;
+            for (;; ++s) {
+                q.load(p, s);
+                const int64_t u = q.head_units(p) * p.Hk;
+                if (begin < before + u)
+                    break;
+                before += u;
+            }
+        sm.seq = s, sm.first = q.first, sm.n = q.n, sm.len = q.len;
         sm.unit0 = before;
         sm.begin = begin;
         sm.left = end - begin;
