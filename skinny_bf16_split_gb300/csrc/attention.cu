@@ -311,6 +311,19 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool i
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Wait for a phase; false if this wait or another one of the block gave up.  (Out of line: fetching code costs.)
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int32_t *dead, int *status, int code)
 {
@@ -384,24 +397,34 @@ __device__ __forceinline__ bool mend(uint8_t *tile, int from, int end, int to)
     constexpr int CH = D / 8, RPI = 32 / CH;
     const int lane = threadIdx.x & 31, c = lane % CH;
     bool any = false;
+    constexpr int kAtOnce = 2;
 #pragma unroll 1
-    for (int i = from / RPI * RPI; i < to; i += RPI) {
-        const int r = i + lane / CH;
-        uint4 *at = reinterpret_cast<uint4 *>(tile + (c / 8) * kTile * 128 + r * 128 + ((c % 8) ^ (r & 7)) * 16);
-        uint4 v = *at;
-        uint32_t *w = &v.x;
-        bool here = false;
+    for (int i0 = from / RPI * RPI; i0 < to; i0 += kAtOnce * RPI) {
+        const auto place = [&](int k) {
+            const int r = min(i0 + k * RPI + lane / CH, kTile - 1);
+            return reinterpret_cast<uint4 *>(tile + (c / 8) * kTile * 128 + r * 128 + ((c % 8) ^ (r & 7)) * 16);
+        };
+        uint4 v[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = (w[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (w[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-            here |= (lo | hi) != 0;
-            w[e] &= ~(lo | hi);
-        }
-        if (r >= end && r < to)
-            *at = make_uint4(0, 0, 0, 0);
-        else if (here && r >= from && r < to) {
-            *at = v;
-            any = true;
+        for (int k = 0; k < kAtOnce; ++k)
+            v[k] = *place(k);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int r = i0 + k * RPI + lane / CH;
+            uint32_t *const w = &v[k].x;
+            bool here = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = (w[e] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (w[e] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+                here |= (lo | hi) != 0;
+                w[e] &= ~(lo | hi);
+            }
+            if (r >= end && r < to)
+                *place(k) = make_uint4(0, 0, 0, 0);
+            else if (here && r >= from && r < to) {
+                *place(k) = v[k];
+                any = true;
+            }
         }
     }
     return any;
@@ -461,7 +484,7 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
     };
     // What is waited for may itself wait for copies that have not been announced yet.
     const auto need = [&](uint64_t &bar, uint32_t parity) {
-        if (!ok || __all_sync(~0u, mbar_try_wait(smem_u32(&bar), parity)))
+        if (!ok || __all_sync(~0u, mbar_test_wait(smem_u32(&bar), parity)))  // (try_wait would sleep on it)
             return;
         land();
         ok = ok && wait_warp(sm, bar, parity, p, DEP_DEV_TIMEOUT_PRODUCER);
@@ -667,6 +690,11 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
         // (both tiles of rows, also the other group's: the release below counts on it)
         for (int h = 0; h < (two ? 2 : 1); ++h)
             ok = ok && wait(sm, sm.q_full[(qc + h) & 1], (uint32_t)((qc + h) >> 1) & 1, p, DEP_DEV_TIMEOUT_MMA);
+        // The tiles of rows are free for the next item with this group's last scores.
+        const auto done_with_rows = [&] {
+            for (int h = 0; h < (two ? 2 : 1); ++h)
+                tc::commit(smem_u32(&sm.q_empty[(qc + h) & 1]));
+        };
         const uint64_t rows = tc::desc_sw128(smem_u32(sm.q[two ? (qc + g) & 1 : qc & 1]));
         if (two) {
             int keys = next_keys();
@@ -678,6 +706,8 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
             pass();
             tc::commit(smem_u32(&sm.s_full[g]));
             tc::commit(empty + 8 * keys);
+            if (n == 1)
+                done_with_rows();
             for (int t = 0; t < n; ++t) {
                 const int values = next_values();
                 if (t + 1 < n)
@@ -696,6 +726,8 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
                     pass();
                     tc::commit(smem_u32(&sm.s_full[g]));
                     tc::commit(empty + 8 * keys);
+                    if (t + 2 == n)
+                        done_with_rows();
                 } else {
                     pass();
                     tc::commit(smem_u32(&sm.o_full[g]));
@@ -717,7 +749,11 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
                 multiply_scores<D>(s_at, rows, ring + at * S::kTileBytes);
                 tc::commit(smem_u32(&sm.s_full[g]));
                 tc::commit(empty + 8 * at);
+                if (t == last)
+                    done_with_rows();
             };
+            if (last < 0)
+                done_with_rows();
             for (int t = -2; ok && t < n; ++t) {
                 if (t >= 0) {
                     const int at = next_values();
@@ -739,8 +775,7 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
                     scores(t + 2);
             }
         }
-        for (int h = 0; h < (two ? 2 : 1); ++h, ++qc)
-            tc::commit(smem_u32(&sm.q_empty[qc & 1]));
+        qc += two ? 2 : 1;
     }
     if (!ok) {  // what is in flight ends before the tensor memory is given back
         tc::commit(smem_u32(&sm.drained[g]));
