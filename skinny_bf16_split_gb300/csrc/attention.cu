@@ -43,8 +43,8 @@ constexpr int kSlotRing = 5 * 32768;  // bytes of keys and values in flight
 constexpr int kLanded = 4;  // tiles of values that came in boxes and are looked at: more than are in flight
 constexpr int kMasks = 8;   // tiles whose masks are held
 constexpr int kAhead = 4;   // items whose descriptions are held
-constexpr int kCost = 3;     // tiles' worth of work that an item costs beside its tiles,
-constexpr int kCostTwo = 5;  // and one with two tiles of rows
+constexpr int kCost = 2;     // tiles' worth of work that an item costs beside its tiles,
+constexpr int kCostTwo = 4;  // and one with two tiles of rows
 constexpr int kLeast = 1;   // units of a block at least
 constexpr uint64_t kWaitNs = 1000000000ull;
 
@@ -899,16 +899,19 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                 // only where P would grow past 2^12, or all that was seen stays below 2^-40: then O has seldom
                 // to be scaled, and one pass over the scores does.  The sum (in which a NaN shows as well) tells; with another m
                 // the tile is taken anew.
-                bool anew = (t + 1) * kTile > clear || (in.x & in.y & in.z & in.w) != ~0u;
-                if (!anew) {
+                const bool masked = (t + 1) * kTile > clear || (in.x & in.y & in.z & in.w) != ~0u;
+                bool wrong = masked, anew = masked;
+                float sum = 0.0f;
+                if (!masked) {
                     uint32_t pk[2][32];
-                    const float sum = tile_exp(s_at, c, -m, pk);
-                    anew = __any_sync(~0u, live && !(sum <= 4096.0f && l + sum >= 0x1p-40f));
-                    if (!anew) {
+                    sum = tile_exp(s_at, c, -m, pk);
+                    wrong = live && !(sum <= 4096.0f && l + sum >= 0x1p-40f);
+                    if (!__any_sync(~0u, wrong)) {
                         l += sum;
                         tmem_st32(s_at, pk[0]);
                         tmem_st32(s_at + 32, pk[1]);
-                    }
+                    } else
+                        anew = true;
                 }
                 if (anew) {  // with what the row sees; rolled up, since it is seldom run: its fetching costs more than its running
                     const uint32_t *mask = sm.masks[(kt + (t - it.t0)) % kMasks];
@@ -924,7 +927,8 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                             top = fmaxf(top, see >> j & 1 ? __uint_as_float(v[j]) : -INFINITY);
                     }
                     const float tm = top * c;
-                    const bool fresh = l == 0.0f, up = live && (tm > m + 5.0f || (fresh && tm > -INFINITY));
+                    // (what a row does goes by its own scores: where only others were wrong it comes to the same P again)
+                    const bool fresh = l == 0.0f, up = live && wrong && (tm > m + 5.0f || (fresh && tm > -INFINITY));
                     if (__any_sync(~0u, up)) {
                         const float f = !up ? 1.0f : fresh ? 0.0f : ex2(m - tm);
                         if (up)
@@ -943,6 +947,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                             }
                     }
                     const float off = -m;
+                    float again = 0.0f;
 #pragma unroll 1
                     for (int w = 0; w < 4; ++w) {  // (P's columns lie in those of scores already read)
                         uint32_t v[32], pk[16];
@@ -954,11 +959,12 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                             float a = ex2(fmaf(__uint_as_float(v[j]), c, off)), b = ex2(fmaf(__uint_as_float(v[j + 1]), c, off));
                             a = see >> j & 1 ? a : 0.0f;
                             b = see >> (j + 1) & 1 ? b : 0.0f;
-                            l += a + b;
+                            again += a + b;
                             pk[j / 2] = pack16(a, b);
                         }
                         tmem_st16(s_at + 16 * w, pk);
                     }
+                    l += wrong ? again : sum;
                 }
                 tmem_wait_st();
             }
