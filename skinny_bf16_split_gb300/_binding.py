@@ -871,7 +871,7 @@ def _attention_workspace(T, n, hq, hk, d):
 
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, tree=None, scale: float | None = None,
-                    out=None, lse=None, stream=None):
+                    out=None, lse=None, status=None, stream=None):
     """Attention of the new tokens of several sequences over a paged cache (see dep_paged_attention in
     include/dep_projection.h): o = softmax(scale q k^T) v.
 
@@ -881,8 +881,8 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None
     [n_seq + 1], the sequences' first tokens, or None for n_seq equal ones; tokens outside the table keep
     what out and lse hold there (in new ones, anything).  tree: int64 [tokens], bit i set where the token
     sees its sequence's i-th new token (drafts of up to 64); None: every token sees those up to itself.
-    scale defaults to D ** -0.5.  lse: float32 [tokens, Hq], filled in where given.  The workspace is the
-    allocator's.  Returns out, bfloat16 [tokens, Hq, D] (allocated where omitted)."""
+    scale defaults to D ** -0.5.  lse: float32 [tokens, Hq], filled in where given.  status: int32 [1], zero before;
+    a DEP_DEV_* code in it says that a wait in the kernel gave up.  The workspace is the allocator's.  Returns out, bfloat16 [tokens, Hq, D] (allocated where omitted)."""
     torch = _torch()
     dev, bf16, i32, shape = q.get_device(), torch.bfloat16, torch.int32, q.shape
     if len(shape) != 3 or dev < 0 or len(k_cache.shape) != 4:
@@ -910,5 +910,6 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None
         None if tree is None else _vector(tree, "tree", torch.int64, dev, T), out.data_ptr(), lse_ptr,
         _heads(q, "q", bf16, dev, shape), _heads(out, "out", bf16, dev, shape), *_cache(k_cache, "k_cache", dev, c_shape),
         *_cache(v_cache, "v_cache", dev, c_shape), row if n > 1 else width, T, c_shape[0], n, hq, hk, d, c_shape[1], width,
-        d ** -0.5 if scale is None else scale, workspace.data_ptr() if size else None, size, None), stream)
+        d ** -0.5 if scale is None else scale, workspace.data_ptr() if size else None, size,
+        None if status is None else _vector(status, "status", i32, dev, 1)), stream)
     return out

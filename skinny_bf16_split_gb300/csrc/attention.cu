@@ -2,24 +2,42 @@
 //
 //     o = sum_j p_j v_j / sum_j p_j,  p_j = exp2(c (q . k_j) - m),  c = scale log2(e)
 //
-// in one pass over the keys and values with the running maximum m and sum of a softmax.
+// in one pass over the keys and values, with any m: P and the sums are floating point, so m has only to
+// keep them in range (see soften()).
 //
-// Rows.  The n tokens of a sequence and the Hq / Hk query heads that share a key and value head are
+// Rows.  The n tokens of a sequence and the G = Hq / Hk query heads that share a key and value head are
 // the rows of one product: row r is token r / G, head r % G of the G.  A block takes up to 256 of them
 // (two tiles of 128, the MMA's M) against tiles of 128 positions: S = Q K^T into tensor memory, a warp
 // group for each tile of rows turns its S into P (BF16, in S's own columns, the MMA's A operand from
-// tensor memory) and the MMA adds P V to O, which stays in tensor memory.  With 128 rows or fewer the two groups take
-// every other tile of positions and their sums are joined at the end, so that both are at work
-// whatever the number of rows.
+// tensor memory) and the MMA adds P V to O, which stays in tensor memory.  With 128 rows or fewer the two
+// groups take every other tile of positions and the first one joins their sums at the end (both read the same lanes of
+// the tensor memory), so that both are at work whatever the number of rows: a tile of M = 128 that holds
+// twelve rows of a decode token costs the tensor cores 1024 cycles for the 64 KB that take HBM 2800.
 //
 // Work.  Every sequence, key and value head and block of rows is an item of ceil(positions seen / 128)
-// tiles; the items' tiles, laid end to end, are cut into equal ranges for the blocks, so contexts
-// of any lengths fill the GPU evenly.  A block works its range out from the lengths on the device.  An item that is
-// cut leaves FP32 parts with their m and sum in the workspace; a second kernel joins them in order.
+// tiles; the items' tiles, laid end to end with a few tiles' worth for the item itself, are cut into equal
+// ranges for one block an SM, so contexts of any lengths fill the GPU evenly.  A block works its range
+// out from the lengths on the device.  An item that is cut leaves FP32 parts with their m and sum in the
+// workspace; a second kernel joins them in order.
 //
-// Keys and values are gathered by cp.async, 16 bytes a lane, row by row from their pages into the
-// 128-byte-swizzled layout that the MMA reads (values as an operand whose N runs along memory), so pages may have any
-// size and strides.
+// Warps.  Two produce, one keys and one values, each a ring of its own (so neither can be a lap ahead): a tile comes in TMA
+// boxes of whole groups of eight slots of a page, or by 16-byte copies where pages have no such groups.  The
+// keys' warp also tells the others the items.  Two warps issue MMAs, one for each group; with two tiles of
+// rows they take turns.  Values past the end would turn P's zeros into NaN if they are not finite, and
+// those of new tokens that some rows do not see likewise: such rows of a tile are looked at on arrival, set to zero,
+// and what was not finite is added to the rows that see it at the end.
+//
+// Bound, with 8 key and value heads of 128 channels, pages of 64 and 96 query heads, of measured rates: one
+// token over 131072 positions 92 us (86 % of the copy rate; 82 in the kernel, 4 in the joining, the rest
+// between), 64 over 4096 on average, ragged, 180 (88 %): HBM; 8 trees of 64 over 16384 positions 310 to 350 us as
+// the clock allows (1.2 to 1.3 PFLOP/s, 62 to 70 % of the burst rate; the tensor pipe is active 62 % of the time):
+// the chain of a group's softmax (1200 cycles a tile) and its products (1600), which two groups only just hide;
+// one token over 512 positions 12.4 us: latencies, half of them the first fetching of code.
+//
+// What was tried and dropped: keys and values by 16-byte copies alone (27 cycles an instruction, 19 B a cycle
+// and SM); prefetches into the L2 (8 trees of 64: 322 -> 345 us and more); polls instead of sleeping waits (64 ragged contexts
+// 178 -> 279); part of the exponentials on the FMA pipe (337 -> 371, issue slots bound the softmax); blocks of rows of one head in
+// step over parts of the grid (a third of the DRAM reads, the same time); a masked form of the straight-line softmax (fetching).
 #include <cuda_bf16.h>
 
 #include <math.h>
@@ -47,6 +65,7 @@ constexpr int kCost = 2;     // tiles' worth of work that an item costs beside i
 constexpr int kCostTwo = 4;  // and one with two tiles of rows
 constexpr int kLeast = 1;   // units of a block at least
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
     const uint16_t *q, *kc, *vc;
@@ -868,7 +887,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
 {
     const int g = threadIdx.x / kTile, r = threadIdx.x % kTile, lane = r % 32;
     const uint32_t lanes = (uint32_t)(r - lane) << 16, s_at = tmem + lanes + g * kTile, o_at = tmem + lanes + 2 * kTile + g * D;
-    const float c = p.scale * 1.4426950408889634f;  // log2(e)
+    const float c = p.scale * kLog2e;
     const bool tree = p.tree != nullptr;
     int kt = 0, item = 0;
     uint32_t k = 0, items = 0, x = 0;  // tiles; items with tiles; exchanges between the groups
@@ -1074,7 +1093,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                 if (!whole)
                     p.part_ml[part] = make_float2(m, l);
                 else if (p.lse)
-                    p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                    p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
             }
         }
         tc::fence_before();
@@ -1253,7 +1272,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
     else
         out[0] = w[0];
     if (p.lse && lane == 0)
-        p.lse[token * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        p.lse[token * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 constexpr int kMostBlocks = 152;  // of a launch: one an SM
@@ -1305,7 +1324,7 @@ cudaError_t attn_launch(AttnParams p, uint8_t *w, const CUtensorMap &kmap, const
 dep_status_t attn_entry(const dep_attention_args_t *a, void *stream)
 {
     if (!a || a->tokens < 0 || a->n_seq < 0 || a->Hq < 1 || a->Hk < 1 || a->Hq % a->Hk != 0 || a->page_size < 1 ||
-        a->table_width < 0 || a->n_pages < 0 || a->workspace_bytes < 0 || !(a->scale >= 0.0f) || isinf(a->scale))
+        a->table_width < 0 || a->n_pages < 0 || a->workspace_bytes < 0 || !(a->scale >= 0.0f) || !isfinite(a->scale * kLog2e))
         return DEP_ERR_INVALID_ARG;
     if (a->D != 64 && a->D != 128)
         return DEP_ERR_UNSUPPORTED;
@@ -1326,7 +1345,7 @@ dep_status_t attn_entry(const dep_attention_args_t *a, void *stream)
     if (a->q_stride < qn || a->o_stride < qn || a->table_stride < a->table_width)
         return DEP_ERR_INVALID_ARG;
     // Lengths and rows of a sequence in 32 bits.
-    if ((int64_t)a->table_width * a->page_size > INT32_MAX - 4096 || T * (int64_t)a->Hq > INT32_MAX - 4096 || a->n_pages > INT32_MAX)
+    if ((int64_t)a->table_width * a->page_size > INT32_MAX - 4096 || T * (int64_t)a->Hq > INT32_MAX - 4096 || a->n_pages > INT32_MAX || a->n_seq > INT32_MAX - 4096)
         return DEP_ERR_UNSUPPORTED;
     const CacheRows kc{cache ? a->k_cache : nullptr, 2ll * a->D, {{2 * a->k_page_stride, a->n_pages}, {2 * a->k_slot_stride, a->page_size}, {2 * a->k_head_stride, a->Hk}}},
         vc{cache ? a->v_cache : nullptr, 2ll * a->D, {{2 * a->v_page_stride, a->n_pages}, {2 * a->v_slot_stride, a->page_size}, {2 * a->v_head_stride, a->Hk}}};

@@ -108,7 +108,7 @@ def attention_args(dep, **kw):
     (dict(tokens=-1), "INVALID_ARG"), (dict(n_seq=-1), "INVALID_ARG"), (dict(Hq=0), "INVALID_ARG"), (dict(Hk=0), "INVALID_ARG"),
     (dict(Hq=3), "INVALID_ARG"), (dict(page_size=0), "INVALID_ARG"), (dict(table_width=-1), "INVALID_ARG"),
     (dict(n_pages=-1), "INVALID_ARG"), (dict(scale=-1.0), "INVALID_ARG"), (dict(scale=INF), "INVALID_ARG"),
-    (dict(scale=float("nan")), "INVALID_ARG"), (dict(n_seq=0), "INVALID_ARG"), (dict(tokens=7, cu_seqlens=None), "INVALID_ARG"),
+    (dict(scale=float("nan")), "INVALID_ARG"), (dict(scale=3e38), "INVALID_ARG"), (dict(n_seq=0), "INVALID_ARG"), (dict(tokens=7, cu_seqlens=None), "INVALID_ARG"),
     (dict(D=96, q_stride=512, o_stride=512), "UNSUPPORTED"), (dict(D=256, q_stride=1024, o_stride=1024), "UNSUPPORTED"),
     (dict(table_width=1 << 30, table_stride=1 << 30), "UNSUPPORTED"), (dict(n_pages=1 << 40), "UNSUPPORTED"),
     (dict(q=None), "INVALID_ARG"), (dict(o=None), "INVALID_ARG"), (dict(kv_lens=None), "INVALID_ARG"),
@@ -121,11 +121,23 @@ def attention_args(dep, **kw):
     (dict(o=A), "INVALID_ARG"), (dict(o=16 * A + 2048), "INVALID_ARG"), (dict(o=32 * A), "INVALID_ARG"),
     (dict(lse=7 * A + 64), "INVALID_ARG"), (dict(lse=3 * A), "INVALID_ARG"), (dict(lse=6 * A), "INVALID_ARG"),
     (dict(o=4 * A), "INVALID_ARG"), (dict(lse=5 * A), "INVALID_ARG"),
+    (dict(n_seq=(1 << 31) - 1), "UNSUPPORTED"), (dict(tokens=1 << 30), "UNSUPPORTED"),
+    (dict(status=9 * A + 2), "MISALIGNED"), (dict(status=7 * A), "INVALID_ARG"), (dict(status=8 * A), "INVALID_ARG"),
+    (dict(workspace=64 * A, workspace_bytes=100), "INVALID_ARG"), (dict(workspace=None, workspace_bytes=1 << 28), "INVALID_ARG"),
+    (dict(workspace=64 * A + 8, workspace_bytes=1 << 28), "MISALIGNED"), (dict(workspace=A, workspace_bytes=1 << 28), "INVALID_ARG"),
 ])
 def test_attention_refusals(dep, change, status):
     with pytest.raises(dep.DepError) as e:
         dep.dep_paged_attention(attention_args(dep, **change), 0)
     assert e.value.status == getattr(dep, "DEP_ERR_" + status)
+
+
+def test_attention_workspace_size(dep):
+    size = lambda **kw: dep.dep_attention_workspace(attention_args(dep, workspace=64 * A, **kw))  # noqa: E731
+    assert size(tokens=0) == 0
+    assert size(tokens=1) < size(tokens=2) < size(tokens=127) < size(tokens=128) == size(tokens=1 << 20)  # 256 rows of an item at most
+    assert size(tokens=1, n_seq=1) == size(tokens=1, n_seq=1000) and size(tokens=64, D=128) > size(tokens=64, D=64)
+    assert size(tokens=1 << 20, D=128) < 64 << 20
 
 
 def test_attention_nothing_to_do(dep):

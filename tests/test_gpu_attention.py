@@ -434,3 +434,19 @@ def test_first_tiles_that_a_row_does_not_see(dep):
         pg = c.table[s].long()[at // 16]
         c.k[pg, at % 16], c.v[pg, at % 16] = c.keys[s][320:], c.values[s][320:]
     c.check(c.run(dep), seen)
+
+
+@pytest.mark.parametrize("n,hq,hk", [(64, 96, 8), (43, 14, 1), (30, 40, 1), (64, 32, 1), (25, 21, 1)])
+def test_many_rows_of_equal_trees(dep, n, hq, hk):
+    """Two to eight blocks of rows of every sequence, and over eight, enough of them to fill the GPU."""
+    for seqs in ([(n, 3000), (n, 900), (0, 70), (n, 2500)], [(n, 500 + 13 * i) for i in range(24 // hk + 1)]):
+        go(dep, seqs, hq, hk, 128, 16, tree=True, seed=n)
+        go(dep, seqs, hq, hk, 64, 16, seed=n)
+
+
+def test_no_wait_gives_up(dep):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for i in range(3):
+        c = Case([(1, 3000), (40, 100), (7, 0)], 24, 2, 64 * (1 + i % 2), 16, seed=i, tree=i == 2)
+        c.check(c.run(dep, status=status))
+    assert status.item() == 0
