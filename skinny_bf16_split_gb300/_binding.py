@@ -13,6 +13,7 @@ import ctypes
 import functools
 import importlib
 import os
+import struct
 from sys import modules as _modules
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -122,6 +123,24 @@ class dep_attention_args_t(ctypes.Structure):
                 + [(name, ctypes.c_int32) for name in ("n_seq", "Hq", "Hk", "D", "page_size", "table_width")]
                 + [("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
                    ("status", ctypes.c_void_p)])
+
+
+_FORMAT = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_uint32: "I", ctypes.c_float: "f"}
+
+
+def _filled(cls):
+    """cls(*fields), an address of none as 0, in half the time, and no field cut off to its bits: a ValueError."""
+    pack, wrap = struct.Struct("".join(_FORMAT[t] for _, t in cls._fields_) + "0q").pack, cls.from_buffer_copy
+
+    def fill(*fields):
+        try:
+            return wrap(pack(*fields))
+        except struct.error as e:
+            raise ValueError(f"{cls.__name__}: {e}") from None
+    return fill
+
+
+_heads_args, _attention_args = _filled(dep_heads_args_t), _filled(dep_attention_args_t)
 
 
 class DepError(RuntimeError):
@@ -506,6 +525,22 @@ def _on(index, call, args, stream):
         call(args, stream)
 
 
+def _on_with_workspace(index, call, args, size, stream):
+    """_on, with a workspace of `size` bytes that belongs to the call's stream.  (Asked of torch's allocator
+    itself: between launches a tensor costs five microseconds more.)"""
+    torch = _torch()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _on_with_workspace(index, call, args, size, stream)
+    stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    args.workspace = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, stream)
+    args.workspace_bytes = size
+    try:
+        call(args, stream)
+    finally:  # (whoever has it next on this stream comes after this call's kernels)
+        torch._C._cuda_cudaCachingAllocator_raw_delete(args.workspace)
+
+
 def _rows(t, name, dtype, index, shape):
     """Stride between the rows of a matrix whose rows are contiguous."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == index:
@@ -767,12 +802,11 @@ def _cache_shape(k_cache, heads, d):
 
 
 def _rotation(dev, tokens, d, positions, freqs, norm, q_weight, k_weight):
-    """(q_weight, k_weight, freqs, positions) as addresses, and how many channels are rotated."""
+    """(q_weight, k_weight, freqs, positions) as addresses, 0 for none, and how many channels are rotated."""
     torch = _torch()
     if (positions is None) != (freqs is None):
         raise ValueError("positions and freqs must be given together")
-    f = p = qw = kw = None
-    rot = 0
+    f = p = qw = kw = rot = 0
     if freqs is not None:
         if freqs.dim() != 1:
             raise ValueError("freqs must be a vector, a frequency for each pair of channels")
@@ -806,8 +840,7 @@ def norm_rotate(q, k=None, positions=None, freqs=None, *, interleaved: bool = Fa
     T, hq, d = shape
     if q_out is None:
         q_out = _empty(shape, bf16, q.device, stream)
-    k_ptr = ko_ptr = None
-    ks = kos = hk = 0
+    k_ptr = ko_ptr = ks = kos = hk = 0
     if k is not None:
         hk = k.shape[1]
         k_shape = (T, hk, d)
@@ -818,8 +851,8 @@ def norm_rotate(q, k=None, positions=None, freqs=None, *, interleaved: bool = Fa
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
     qw, kw, f, p, rot = _rotation(dev, T, d, positions, freqs, norm, q_weight, k_weight)
-    _on(dev, dep_norm_rotate, dep_heads_args_t(
-        q.data_ptr(), k_ptr, None, qw, kw, f, p, None, q_out.data_ptr(), ko_ptr, None, None,
+    _on(dev, dep_norm_rotate, _heads_args(
+        q.data_ptr(), k_ptr, 0, qw, kw, f, p, 0, q_out.data_ptr(), ko_ptr, 0, 0,
         _heads(q, "q", bf16, dev, shape), ks, 0, _heads(q_out, "q_out", bf16, dev, shape), kos, 0, 0, 0, 0, 0, 0, T, 0,
         hq, hk, d, rot, first, 1, (DEP_HEADS_INTERLEAVED if interleaved else 0) | (DEP_HEADS_NORM if norm else 0), eps,
         amplitude), stream)
@@ -843,8 +876,7 @@ def append_kv(k, v, k_cache, v_cache, slots, positions=None, freqs=None, *, inte
         raise ValueError("k, v [tokens, Hk, D] and q [tokens, Hq, D] must be CUDA tensors of three dimensions")
     T, hk, d = shape
     c_shape = _cache_shape(k_cache, hk, d)
-    q_ptr = qo_ptr = None
-    qs = qos = hq = 0
+    q_ptr = qo_ptr = qs = qos = hq = 0
     if q is not None:
         hq = q.shape[1]
         q_shape = (T, hq, d)
@@ -855,8 +887,8 @@ def append_kv(k, v, k_cache, v_cache, slots, positions=None, freqs=None, *, inte
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
     qw, kw, f, p, rot = _rotation(dev, T, d, positions, freqs, norm, q_weight, k_weight)
-    _on(dev, dep_append_kv, dep_heads_args_t(
-        q_ptr, k.data_ptr(), v.data_ptr(), qw, kw, f, p, _vector(slots, "slots", torch.int32, dev, T), qo_ptr, None,
+    _on(dev, dep_append_kv, _heads_args(
+        q_ptr, k.data_ptr(), v.data_ptr(), qw, kw, f, p, _vector(slots, "slots", torch.int32, dev, T), qo_ptr, 0,
         k_cache.data_ptr(), v_cache.data_ptr(), qs, _heads(k, "k", bf16, dev, shape), _heads(v, "v", bf16, dev, shape), qos, 0,
         *_cache(k_cache, "k_cache", dev, c_shape), *_cache(v_cache, "v_cache", dev, c_shape), T, c_shape[0], hq, hk, d, rot,
         first, c_shape[1], (DEP_HEADS_INTERLEAVED if interleaved else 0) | (DEP_HEADS_NORM if norm else 0), eps, amplitude),
@@ -897,19 +929,21 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None
         raise ValueError("page_table must have contiguous rows")
     if out is None:
         out = _empty(shape, bf16, q.device, stream)
-    lse_ptr = None
+    lse_ptr = 0
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.shape != (T, hq) or lse.get_device() != dev or not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous float32 matrix [{T}, {hq}] on cuda:{dev}")
         lse_ptr = lse.data_ptr()
-    size = _attention_workspace(T, n, hq, hk, d)
-    workspace = _empty((size,), torch.uint8, q.device, stream) if size else None
-    _on(dev, dep_paged_attention, dep_attention_args_t(
+    args = _attention_args(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), _vector(kv_lens, "kv_lens", i32, dev, n),
-        None if cu_seqlens is None else _vector(cu_seqlens, "cu_seqlens", i32, dev, n + 1),
-        None if tree is None else _vector(tree, "tree", torch.int64, dev, T), out.data_ptr(), lse_ptr,
+        0 if cu_seqlens is None else _vector(cu_seqlens, "cu_seqlens", i32, dev, n + 1),
+        0 if tree is None else _vector(tree, "tree", torch.int64, dev, T), out.data_ptr(), lse_ptr,
         _heads(q, "q", bf16, dev, shape), _heads(out, "out", bf16, dev, shape), *_cache(k_cache, "k_cache", dev, c_shape),
         *_cache(v_cache, "v_cache", dev, c_shape), row if n > 1 else width, T, c_shape[0], n, hq, hk, d, c_shape[1], width,
-        d ** -0.5 if scale is None else scale, workspace.data_ptr() if size else None, size,
-        None if status is None else _vector(status, "status", i32, dev, 1)), stream)
+        d ** -0.5 if scale is None else scale, 0, 0, 0 if status is None else _vector(status, "status", i32, dev, 1))
+    size = _attention_workspace(T, n, hq, hk, d)
+    if size:
+        _on_with_workspace(dev, dep_paged_attention, args, size, stream)
+    else:
+        _on(dev, dep_paged_attention, args, stream)
     return out

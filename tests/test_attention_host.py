@@ -162,3 +162,17 @@ def test_python_entry_points_refuse(dep):
         dep.append_kv(h, h, cache, cache, i32)
     with pytest.raises(ValueError):
         dep.paged_attention(h, cache, cache, i32[:, None], i32)
+
+
+def test_arguments_that_a_field_does_not_hold(dep):
+    """Sizes past their field's width are refused, not cut off to its bits."""
+    from skinny_bf16_split_gb300 import _binding as b
+    for cls, fill in ((dep.dep_heads_args_t, b._heads_args), (dep.dep_attention_args_t, b._attention_args)):
+        names = [n for n, _ in cls._fields_]
+        args = fill(*range(1, len(names) + 1))
+        assert [getattr(args, n) for n in names] == list(range(1, len(names) + 1))
+        for name, kind in cls._fields_:
+            for value in {ctypes.c_int32: ((1 << 32) + 16, -(1 << 31) - 1), ctypes.c_int64: (1 << 63,),
+                          ctypes.c_uint32: (1 << 32, -1), ctypes.c_float: (), ctypes.c_void_p: ()}[kind]:
+                with pytest.raises(ValueError):
+                    fill(*(value if n == name else 0 for n in names))

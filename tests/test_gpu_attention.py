@@ -450,3 +450,20 @@ def test_no_wait_gives_up(dep):
         c = Case([(1, 3000), (40, 100), (7, 0)], 24, 2, 64 * (1 + i % 2), 16, seed=i, tree=i == 2)
         c.check(c.run(dep, status=status))
     assert status.item() == 0
+
+
+def test_the_workspace_is_given_back(dep):
+    """After a call and after a refusal; on a stream of the caller's it is that stream's."""
+    c = Case([(1, 300), (3, 50)], 8, 2, 64, 16)
+    out, other = torch.empty_like(c.q), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for stream in (None, other, other.cuda_stream, 0):
+        dep.paged_attention(c.q, c.k, c.v, c.table, c.kv, cu_seqlens=c.cu, out=out, stream=stream)
+        assert torch.cuda.memory_allocated() == before
+    torch.cuda.synchronize()
+    with pytest.raises(dep.DepError):
+        dep.paged_attention(c.q, c.k, c.v, c.table, c.kv, cu_seqlens=c.cu, out=c.q)
+    with pytest.raises(dep.DepError):
+        dep.paged_attention(c.q, c.k, c.v, c.table, c.kv, cu_seqlens=c.cu, out=out, scale=1e300)
+    assert torch.cuda.memory_allocated() == before
