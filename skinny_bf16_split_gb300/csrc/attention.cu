@@ -36,8 +36,9 @@
 //
 // What was tried and dropped: keys and values by 16-byte copies alone (27 cycles an instruction, 19 B a cycle
 // and SM); prefetches into the L2 (8 trees of 64: 322 -> 345 us and more); polls instead of sleeping waits (64 ragged contexts
-// 178 -> 279); part of the exponentials on the FMA pipe (337 -> 371, issue slots bound the softmax); blocks of rows of one head in
-// step over parts of the grid (a third of the DRAM reads, the same time); a masked form of the straight-line softmax (fetching).
+// 178 -> 279); part of the exponentials on the FMA pipe (337 -> 371, issue slots bound the softmax); the blocks of rows of
+// one head side by side over parts of the grid, so that they would read a tile at about the same time (8 trees of 64 took as
+// long, and every call a microsecond more to find its range); a masked form of the straight-line softmax (fetching).
 #include <cuda_bf16.h>
 
 #include <math.h>
