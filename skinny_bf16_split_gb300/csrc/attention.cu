@@ -31,14 +31,18 @@
 // token over 131072 positions 92 us (86 % of the copy rate; 82 in the kernel, 4 in the joining, the rest
 // between), 64 over 4096 on average, ragged, 180 (88 %): HBM; 8 trees of 64 over 16384 positions 310 to 350 us as
 // the clock allows (1.2 to 1.3 PFLOP/s, 62 to 70 % of the burst rate; the tensor pipe is active 62 % of the time):
-// the chain of a group's softmax (1200 cycles a tile) and its products (1600), which two groups only just hide;
+// the chain of a group's softmax (820 cycles a tile alone, 1200 beside the other's) and its products, which two groups only
+// just hide: alone, an MMA of the scores takes 88 cycles instead of 64 (both operands from shared memory, 94 bytes a cycle)
+// and one of the values 80, so the 16 of a tile 1350 and their waits 100; only the two kinds side by side come to 65;
 // one token over 512 positions 12.4 us: latencies, half of them the first fetching of code.
 //
 // What was tried and dropped: keys and values by 16-byte copies alone (27 cycles an instruction, 19 B a cycle
 // and SM); prefetches into the L2 (8 trees of 64: 322 -> 345 us and more); polls instead of sleeping waits (64 ragged contexts
 // 178 -> 279); part of the exponentials on the FMA pipe (337 -> 371, issue slots bound the softmax); the blocks of rows of
 // one head side by side over parts of the grid, so that they would read a tile at about the same time (8 trees of 64 took as
-// long, and every call a microsecond more to find its range); a masked form of the straight-line softmax (fetching).
+// long, and every call a microsecond more to find its range); P handed over in halves, so that its product starts earlier (the
+// trees 306 to 317 -> 329: shorter runs of MMAs, a second wait; 64 ragged contexts 179 -> 183); a masked form of the
+// straight-line softmax (fetching).
 #include <cuda_bf16.h>
 
 #include <math.h>
