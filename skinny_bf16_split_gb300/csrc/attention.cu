@@ -114,12 +114,18 @@ template <int D>
 struct Smem {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kSlots = kSlotRing / kTileBytes, kKeySlots = kSlots / 2;
+    // Columns of tensor memory: scores (and P in them) 0 and 128, sums from 256; with 64 channels there is room for P in
+    // columns of its own.  Then a group that has every other tile gets its next scores while P is still being multiplied:
+    // one token over 131072 positions, 96 heads over 8, 66.0 -> 56.5 us, 64 over 4096 on average 151 -> 146.  Where both
+    // groups have the same tiles that order costs more than it gives (8 trees of 64 over 16384 254 -> 285, scores last 260).
+    static constexpr bool kApart = D == 64;
+    __device__ static constexpr uint32_t p_column(int g) { return kApart ? 2 * kTile + 2 * D + g * (kTile / 2) : g * kTile; }
     uint8_t q[2][kTileBytes];          // tiles of rows
     uint8_t ring[kSlots][kTileBytes];  // a ring of kKeySlots tiles of keys and one of values
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full[2], q_empty[2], item_full[kAhead], done[kAhead];
     uint64_t landed[kLanded], turn[2];
-    uint64_t s_full[2], p_full[2], o_full[2], x_full, x_free, drained[2];
+    uint64_t s_full[2], p_full[2], p_empty[2], o_full[2], x_full, x_free, drained[2];
     alignas(16) uint32_t masks[kMasks][4];  // positions of a tile that are in the cache
     Item items[kAhead];
     int32_t odd[kAhead];  // 1 + the last item of that place with values of new tokens that are not finite
@@ -678,7 +684,7 @@ template <int D>
 __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
 {
     using S = Smem<D>;
-    const uint32_t s_at = tmem + g * kTile, o_at = tmem + 2 * kTile + g * D, ring = smem_u32(sm.ring[0]);
+    const uint32_t s_at = tmem + g * kTile, o_at = tmem + 2 * kTile + g * D, p_at = tmem + S::p_column(g), ring = smem_u32(sm.ring[0]);
     const uint32_t empty = smem_u32(&sm.empty[0]);
     bool ok = true;
     int key_slot = 0, value_slot = S::kKeySlots, item = 0, qc = 0;
@@ -744,7 +750,7 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
                 if (!ok)
                     break;
                 tc::fence_after();
-                multiply_values<D>(o_at, s_at, v_at, steps, t > 0);
+                multiply_values<D>(o_at, p_at, v_at, steps, t > 0);
                 if (t + 1 < n) {
                     multiply_scores<D>(s_at, rows, k_at);
                     pass();
@@ -759,7 +765,8 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
                 tc::commit(empty + 8 * values);
             }
         } else {
-            // Every other tile: two tiles' keys first, then a tile's values and the keys of the one after the next.
+            // Every other tile: two tiles' keys first, then a tile's values and the keys of the one after the next (these
+            // first, where P has columns of its own).
             const int last = n - 1 - ((n - 1 - g) & 1);  // this group's last tile
             const auto scores = [&](int t) {
                 const int at = next_keys();
@@ -788,11 +795,19 @@ __device__ void multiply(const AttnParams &p, Smem<D> &sm, uint32_t tmem, int g)
                         if (!ok)
                             break;
                         ++k;
+                        if (S::kApart && t + 2 < n)
+                            scores(t + 2);
+                        if (!ok)
+                            break;
                         tc::fence_after();
-                        multiply_values<D>(o_at, s_at, ring + at * S::kTileBytes, value_steps(to, t0 + t), t > 1);
+                        multiply_values<D>(o_at, p_at, ring + at * S::kTileBytes, value_steps(to, t0 + t), t > 1);
+                        if (S::kApart)
+                            tc::commit(smem_u32(&sm.p_empty[g]));
                         if (t == last)
                             tc::commit(smem_u32(&sm.o_full[g]));
                         tc::commit(empty + 8 * at);
+                        if (S::kApart)
+                            continue;
                     }
                 }
                 if (ok && t + 2 < n)
@@ -895,13 +910,14 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
     const float c = p.scale * kLog2e;
     const bool tree = p.tree != nullptr;
     int kt = 0, item = 0;
-    uint32_t k = 0, items = 0, x = 0;  // tiles; items with tiles; exchanges between the groups
+    uint32_t k = 0, e = 0, items = 0, x = 0;  // tiles; those with P of its own; items with tiles; exchanges between the groups
     bool ok = true, lent = false;      // lent: the first group may still read this one's sums
     for (;; ++item) {
         const Item it = next_item(sm, item, p, DEP_DEV_TIMEOUT_CONSUMER, ok);
         if (it.t1 == 0)
             break;
-        const bool two = it.two();
+        const bool two = it.two(), apart = Smem<D>::kApart && !two;
+        const uint32_t p_at = tmem + lanes + Smem<D>::p_column(g);
         const int at = two ? g * kTile + r : r;
         const bool live = at < it.rows, warp_live = at - lane < it.rows;
         const uint32_t row = it.row0 + at;
@@ -912,11 +928,20 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
         float m = 0.0f, l = 0.0f;  // m: log2 units
         int t = it.t0 + (two ? 0 : g);
         const bool some = t < it.t1;
-        for (bool first = true; t < it.t1; t += two ? 1 : 2, first = false, ++k) {
+        for (bool first = true; t < it.t1; t += two ? 1 : 2, first = false, ++k, e += apart) {
             ok = ok && wait_warp(sm, sm.s_full[g], k & 1, p, DEP_DEV_TIMEOUT_CONSUMER);
             if (!ok)
                 break;
             tc::fence_after();
+            // P's own columns are free, and O is settled, once the product before is done (elsewhere that came before these
+            // scores).
+            const auto last_product = [&] {
+                if (apart && e > 0) {
+                    if (!wait_warp(sm, sm.p_empty[g], (e - 1) & 1, p, DEP_DEV_TIMEOUT_CONSUMER))
+                        ok = false;
+                    tc::fence_after();
+                }
+            };
             if (warp_live) {
                 const uint4 in = *reinterpret_cast<const uint4 *>(sm.masks[(kt + (t - it.t0)) % kMasks]);
                 // P and its sum keep their precision at any size, so what is taken off, m, is zero to begin with and moves
@@ -929,15 +954,18 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                 if (!masked) {
                     uint32_t pk[2][32];
                     sum = tile_exp(s_at, c, -m, pk);
+                    last_product();
                     wrong = live && !(sum <= 4096.0f && l + sum >= 0x1p-40f);
                     if (!__any_sync(~0u, wrong)) {
                         l += sum;
-                        tmem_st32(s_at, pk[0]);
-                        tmem_st32(s_at + 32, pk[1]);
+                        tmem_st32(p_at, pk[0]);
+                        tmem_st32(p_at + 32, pk[1]);
                     } else
                         anew = true;
                 }
                 if (anew) {  // with what the row sees; rolled up, since it is seldom run: its fetching costs more than its running
+                    if (masked)
+                        last_product();
                     const uint32_t *mask = sm.masks[(kt + (t - it.t0)) % kMasks];
                     float top = -INFINITY;
 #pragma unroll 1
@@ -986,7 +1014,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                             again += a + b;
                             pk[j / 2] = pack16(a, b);
                         }
-                        tmem_st16(s_at + 16 * w, pk);
+                        tmem_st16(p_at + 16 * w, pk);
                     }
                     l += wrong ? again : sum;
                 }
@@ -1006,6 +1034,8 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
         kt += it.t1 - it.t0;
         if (some) {
             ok = ok && wait_warp(sm, sm.o_full[g], items & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
+            if (apart)  // (a warp without rows has not waited for the products: the next item's wait is for the phase after this)
+                ok = ok && wait_warp(sm, sm.p_empty[g], (e - 1) & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
             ++items;
             tc::fence_after();
         }
@@ -1138,6 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             mbar_init(smem_u32(&sm.q_empty[g]), 2);
             mbar_init(smem_u32(&sm.s_full[g]), 1);
             mbar_init(smem_u32(&sm.p_full[g]), 4);
+            mbar_init(smem_u32(&sm.p_empty[g]), 1);
             mbar_init(smem_u32(&sm.o_full[g]), 1);
             mbar_init(smem_u32(&sm.drained[g]), 1);
             mbar_init(smem_u32(&sm.turn[g]), 1);
