@@ -71,6 +71,7 @@ constexpr int kCostTwo = 4;  // and one with two tiles of rows
 constexpr int kLeast = 1;   // units of a block at least
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kFar = 0x1p28f;  // log2 units; a maximum of that size is held to 16 units at best (see soften())
 
 struct AttnParams {
     const uint16_t *q, *kc, *vc;
@@ -955,7 +956,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                     uint32_t pk[2][32];
                     sum = tile_exp(s_at, c, -m, pk);
                     last_product();
-                    wrong = live && !(sum <= 4096.0f && l + sum >= 0x1p-40f);
+                    wrong = live && !(sum <= 4096.0f && l + sum >= 0x1p-40f && fabsf(m) < kFar);
                     if (!__any_sync(~0u, wrong)) {
                         l += sum;
                         tmem_st32(p_at, pk[0]);
@@ -978,7 +979,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                         for (int j = 0; j < 32; ++j)
                             top = fmaxf(top, see >> j & 1 ? __uint_as_float(v[j]) : -INFINITY);
                     }
-                    const float tm = top * c;
+                    const float tm = __fmul_rn(top, c);  // (nothing fused: the same as a far row's products below)
                     // (what a row does goes by its own scores: where only others were wrong it comes to the same P again)
                     const bool fresh = l == 0.0f, up = live && wrong && (tm > m + 5.0f || (fresh && tm > -INFINITY));
                     if (__any_sync(~0u, up)) {
@@ -998,7 +999,12 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                                 tmem_st16(o_at + 16 * w, v);
                             }
                     }
+                    // p = exp2(c s - m), rounded after the difference alone, is exact in whatever m is, and in range while m is
+                    // the row's maximum to a few units.  From 2^28 on FP32 rounds the maximum by eight units and more, in the end
+                    // by all that an exponential takes; there c s is rounded first, as the maximum was, and its own p is 1.
                     const float off = -m;
+                    const bool far = fabsf(m) >= kFar, any_far = __any_sync(~0u, far);
+                    const float c0 = far ? c : 1.0f, c1 = far ? 1.0f : c;
                     float again = 0.0f;
 #pragma unroll 1
                     for (int w = 0; w < 4; ++w) {  // (P's columns lie in those of scores already read)
@@ -1006,9 +1012,13 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                         tmem_ld32(s_at + 32 * w, v);
                         const uint32_t see = mask[w] & seen32(tree, it.own, tok, word, t * kTile + 32 * w);
                         tc::wait_ld();
+                        if (any_far)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), c0));
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            float a = ex2(fmaf(__uint_as_float(v[j]), c, off)), b = ex2(fmaf(__uint_as_float(v[j + 1]), c, off));
+                            float a = ex2(fmaf(__uint_as_float(v[j]), c1, off)), b = ex2(fmaf(__uint_as_float(v[j + 1]), c1, off));
                             a = see >> j & 1 ? a : 0.0f;
                             b = see >> (j + 1) & 1 ? b : 0.0f;
                             again += a + b;
