@@ -1133,7 +1133,8 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                     mbar_arrive(smem_u32(&sm.x_free));
             }
             if (live) {
-                if (*reinterpret_cast<volatile int32_t *>(&sm.odd[item % kAhead]) == item + 1)
+                // (a row whose scores are all minus infinity has zeros, whatever the values are; of parts the joining sees to it)
+                if ((l != 0.0f || !whole) && *reinterpret_cast<volatile int32_t *>(&sm.odd[item % kAhead]) == item + 1)
                     add_odd<D>(p, it, tok, word, out, whole ? nullptr : rest);
                 if (!whole)
                     p.part_ml[part] = make_float2(m, l);

@@ -47,6 +47,30 @@ def test_values_that_only_some_rows_see(dep, form, d, page, tree, what):
     assert (seen.isnan() if math.isnan(what) else seen == what).all()
 
 
+@pytest.mark.parametrize("what", [NAN, INF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tree", [False, True])
+def test_values_behind_scores_of_minus_infinity(dep, what, d, tree):
+    """A token whose scores are all minus infinity has zeros, whatever the values are; others are as they were."""
+    c = Case([(1, 0), (3, 0), (2, 150), (30, 0)], 12, 2, d, 16, tree=tree, seed=4)
+    if tree:
+        c.tree[...] = -1
+    c.q[...] = c.q.abs().clamp(min=0.01)
+    want, lse = c.run(dep).clone(), c.lse.clone()
+    for s in (0, 1, 3):
+        c.keys[s][:, 0, 0] = -INF
+        c.values[s][:, 0, ::2] = what
+    c.fill()
+    got = c.run(dep)
+    for s, n in enumerate(c.new):
+        rows = slice(c.first[s], c.first[s] + n)
+        if s == 2:
+            assert torch.equal(got[rows], want[rows]) and torch.equal(c.lse[rows], lse[rows])
+        else:
+            assert (got[rows, :6] == 0).all() and (c.lse[rows, :6] == -INF).all()
+            assert torch.equal(got[rows, 6:], want[rows, 6:]) and torch.equal(c.lse[rows, 6:], lse[rows, 6:])
+
+
 LONG = [
     ([(1, 5000)], 12, 1, 128, 64, False), ([(1, 40018)], 12, 1, 128, 64, False), ([(1, 70001)], 12, 1, 64, 64, False),
     ([(1, 131071)], 24, 2, 128, 64, False), ([(1, 131071)], 24, 2, 64, 128, False), ([(16, 40003)], 24, 2, 128, 128, True),
