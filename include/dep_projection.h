@@ -646,6 +646,18 @@ typedef struct {
 dep_status_t dep_paged_attention(const dep_attention_args_t *args, void *stream);
 dep_status_t dep_attention_workspace(const dep_attention_args_t *args, int64_t *bytes);
 
+/*
+ * Give-up self-test of the attention: dep_paged_attention in which waits of the kind
+ * `code` (a DEP_DEV_TIMEOUT_* code) are held up for good.  A block that comes to one
+ * gives up after the second that a wait may take, ends its copies and products in
+ * flight and returns; the first wait of the call that gave up (of this kind, or for what it
+ * holds up) stores its code to *status.  A call in which no such wait is needed (a ring that
+ * is never full) ends as ever.  The workspace serves later calls as it is.  Exercises the
+ * give-up path without faulting the GPU.  Errors: as dep_paged_attention; INVALID_ARG
+ * also for another code.
+ */
+dep_status_t dep_attention_selftest_timeout(const dep_attention_args_t *args, int32_t code, void *stream);
+
 /* The binning rule on its own: index into keys[0..n_keys) of the entry serving
  * B rows -- smallest key >= B, else the largest key; -1 if n_keys < 1.  The keys
  * need not be sorted.  Pure host function. */

@@ -71,7 +71,7 @@ EXPORTS = (
     "dep_projection_plan_selftest_exchange",
     "dep_add_rms_norm", "dep_quantize_rows", "dep_delta_rule", "dep_delta_workspace", "dep_int8_plan", "dep_int8_run",
     "dep_int8_plan_workspace", "dep_int8_device_status", "dep_int8_plan_destroy",
-    "dep_norm_rotate", "dep_append_kv", "dep_paged_attention", "dep_attention_workspace",
+    "dep_norm_rotate", "dep_append_kv", "dep_paged_attention", "dep_attention_workspace", "dep_attention_selftest_timeout",
 )
 
 
@@ -200,6 +200,7 @@ def lib():
         "dep_append_kv": ([P(dep_heads_args_t), vp], i32),
         "dep_paged_attention": ([P(dep_attention_args_t), vp], i32),
         "dep_attention_workspace": ([P(dep_attention_args_t), P(ctypes.c_int64)], i32),
+        "dep_attention_selftest_timeout": ([P(dep_attention_args_t), i32, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -447,6 +448,10 @@ def dep_append_kv(args: dep_heads_args_t, stream=None) -> None:
 
 def dep_paged_attention(args: dep_attention_args_t, stream=None) -> None:
     _check(lib().dep_paged_attention(ctypes.byref(args), _stream(stream)), "dep_paged_attention")
+
+
+def dep_attention_selftest_timeout(args: dep_attention_args_t, code: int, stream=None) -> None:
+    _check(lib().dep_attention_selftest_timeout(ctypes.byref(args), code, _stream(stream)), "dep_attention_selftest_timeout")
 
 
 def dep_attention_workspace(args: dep_attention_args_t) -> int:
