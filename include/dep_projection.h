@@ -622,7 +622,8 @@ dep_status_t dep_append_kv(const dep_heads_args_t *args, void *stream);
  * Workspace: device memory that the call overwrites, at least dep_attention_workspace
  * bytes (of tokens, n_seq, Hq, Hk and D alone; else INVALID_ARG).
  * Every wait in the kernel is bounded (1 s); if one gives up, a DEP_DEV_* code is stored to
- * *status where that holds 0, and the outputs are not complete.
+ * *status where that holds 0, and every row of o and lse that is not complete is NaN
+ * (complete ones may be).
  * MISALIGNED unless q, o, the caches and the workspace are 16-byte aligned, the strides
  * of q, o and the caches multiples of 8, tree 8-byte and the rest 4-byte aligned.
  */

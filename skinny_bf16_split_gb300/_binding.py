@@ -919,7 +919,9 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None
     what out and lse hold there (in new ones, anything).  tree: int64 [tokens], bit i set where the token
     sees its sequence's i-th new token (drafts of up to 64); None: every token sees those up to itself.
     scale defaults to D ** -0.5.  lse: float32 [tokens, Hq], filled in where given.  status: int32 [1], zero before;
-    a DEP_DEV_* code in it says that a wait in the kernel gave up.  The workspace is the allocator's.  Returns out, bfloat16 [tokens, Hq, D] (allocated where omitted)."""
+    a DEP_DEV_* code in it says that a wait in the kernel gave up (after a second).  With or without it the rows
+    that such a call leaves incomplete are NaN.  The workspace is the allocator's.  Returns out, bfloat16
+    [tokens, Hq, D] (allocated where omitted)."""
     torch = _torch()
     dev, bf16, i32, shape = q.get_device(), torch.bfloat16, torch.int32, q.shape
     if len(shape) != 3 or dev < 0 or len(k_cache.shape) != 4:

@@ -99,7 +99,8 @@ struct Cut {
     int32_t parts;  // of the item; 0: none begins here and goes on
     int32_t kv_head, row0, rows;
     int64_t first;
-    int32_t pad[2];
+    int32_t dead;  // a wait of the block gave up
+    int32_t pad;
 };
 
 // One key and value head of a sequence, up to kBlockRows of its rows, and the tiles [t0, t1) of their T.
@@ -110,6 +111,11 @@ struct Item {
     int32_t own, shared, end;    // positions: the first new token's; those before `shared` are seen by all rows, from `end` on by none
     __device__ bool two() const { return rows > kTile; }  // both groups on the same tiles of positions
     __device__ bool whole() const { return t0 == 0 && t1 == T; }
+};
+
+struct Dead {
+    int32_t here;      // a wait of the block gave up
+    int32_t *outside;  // where the joining kernel looks
 };
 
 template <int D>
@@ -137,7 +143,7 @@ struct Smem {
     int64_t first;  // its first sequence: as in Seq
     int32_t seq, n, len;
     uint32_t tmem;
-    int32_t dead;  // a wait gave up
+    Dead dead;
 };
 
 // ---- a sequence, and the items of a range -----------------------------------------------------
@@ -357,15 +363,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
 }
 
 // Wait for a phase; false if this wait or another one of the block gave up.  (Out of line: fetching code costs.)
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int32_t *dead, int *status, int code)
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile Dead *dead, int *status, int code)
 {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
-        if (*dead)
+        if (dead->here)
             return false;
         if (globaltimer_ns() - t0 > kWaitNs) {
             record_status(status, code);
-            *dead = 1;
+            *dead->outside = 1;
+            dead->here = 1;
             return false;
         }
     }
@@ -554,7 +561,9 @@ __device__ void produce(const AttnParams &p, Smem<D> &sm, const CUtensorMap &kma
                     int last = blockIdx.x + 1;
                     while (parts.begin(last + 1) < list.unit + it.T + list.cost())
                         ++last;
-                    p.cuts[blockIdx.x] = Cut{last - (int)blockIdx.x + 1, it.kv_head, it.row0, it.rows, it.first, {0, 0}};
+                    Cut &cut = p.cuts[blockIdx.x];
+                    cut.parts = last - (int)blockIdx.x + 1, cut.kv_head = it.kv_head, cut.row0 = it.row0, cut.rows = it.rows;
+                    cut.first = it.first;
                 }
                 mbar_arrive(smem_u32(&sm.item_full[item % kAhead]));
             }
@@ -1204,12 +1213,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         mbar_init(smem_u32(&sm.x_full), 4);
         mbar_init(smem_u32(&sm.x_free), 4);
         fence_mbar_init();
-        sm.dead = 0;
+        sm.dead = Dead{0, &p.cuts[blockIdx.x].dead};
         sm.left = 0;
     }
     griddep_wait();  // what comes before may write the inputs, and read the workspace
     if (threadIdx.x == 0)
-        p.cuts[blockIdx.x].parts = 0;
+        p.cuts[blockIdx.x].parts = p.cuts[blockIdx.x].dead = 0;
     // The range.  Every thread adds up the units of its share of the sequences.
     const int per = (p.n_seq + kThreads - 1) / kThreads, s0 = min(p.n_seq, (int)threadIdx.x * per), s1 = min(p.n_seq, s0 + per);
     int64_t mine = 0;
@@ -1275,6 +1284,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
 }
 
+// NaN to the rows of all sequences: a block that gave up does not say which of its own it has done.  Rows that are complete may be
+// joined at the same time and stay.
+template <int D>
+__device__ __noinline__ void spoil(const AttnParams &p)
+{
+    const int lane = threadIdx.x & 31, warp = blockIdx.y * 8 + threadIdx.x / 32, warps = gridDim.y * 8;
+    for (int64_t s = warp; s < p.n_seq; s += warps) {
+        const int64_t first = seq_start(p, (int)s), last = seq_start(p, (int)s + 1);
+        for (int64_t t = first; t < last; ++t) {
+            uint4 *const row = reinterpret_cast<uint4 *>(p.o + t * p.os);
+            for (int i = lane; i < p.Hq * (D / 8); i += 32)
+                row[i] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+            for (int h = lane; p.lse && h < p.Hq; h += 32)
+                p.lse[t * p.Hq + h] = __uint_as_float(0x7FFFFFFFu);
+        }
+    }
+}
+
 // The parts of the item that begins in block blockIdx.x, joined in the blocks' order; a warp takes a row.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
@@ -1284,17 +1311,22 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
     constexpr int E = D / 32;
     const Cut cut = p.cuts[blockIdx.x];
     const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + threadIdx.x / 32;
+    if (cut.dead)
+        return spoil<D>(p);
     if (cut.parts == 0 || r >= cut.rows)
         return;
     const auto at = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + r; };
     // Lane j: the j-th of 32 parts at once.
     float m = -INFINITY;
-    for (int i = lane; i < cut.parts; i += 32)
+    bool lost = false;  // a part that is not complete
+    for (int i = lane; i < cut.parts; i += 32) {
         m = fmaxf(m, p.part_ml[at(i)].x);
+        lost |= p.cuts[blockIdx.x + i].dead != 0;
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1)
         m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    float l = 0.0f, o[E] = {};
+    float l = lost ? __uint_as_float(0x7FFFFFFFu) : 0.0f, o[E] = {};
     for (int i0 = 0; i0 < cut.parts; i0 += 32) {
         float f = 0.0f;
         if (i0 + lane < cut.parts) {
@@ -1342,9 +1374,12 @@ constexpr int kMostBlocks = 152;  // of a launch: one an SM
 // Rows that a part may have: no item has more than all tokens give.
 int part_rows(int64_t tokens, int32_t Hq, int32_t Hk) { return (int)std::min<int64_t>(kBlockRows, tokens * (Hq / Hk)); }
 
-// Of the cuts (a multiple of 16 bytes), the parts' m and sums, and the parts; the last at a multiple of 32 bytes.
-int64_t parts_offset(int rows) { return kMostBlocks * (int64_t)(sizeof(Cut) + 2 * rows * sizeof(float2)); }
-int64_t workspace_bytes(int rows, int D) { return parts_offset(rows) + kMostBlocks * 2ll * rows * 4 * D + 32; }
+// Of the cuts, the parts' m and sums, and the parts, whole lines of 128 bytes each (a row of a part over one line more: one token
+// over 131072 positions 94.1 -> 94.9 us).
+constexpr int64_t kCutBytes = kMostBlocks * (int64_t)sizeof(Cut);
+static_assert(kCutBytes % 128 == 0 && kMostBlocks * 2 * sizeof(float2) % 128 == 0, "lines");
+int64_t parts_offset(int rows) { return kCutBytes + kMostBlocks * 2ll * rows * (int64_t)sizeof(float2); }
+int64_t workspace_bytes(int rows, int D) { return parts_offset(rows) + kMostBlocks * 2ll * rows * 4 * D + 128; }
 
 template <int D>
 cudaError_t attn_launch(AttnParams p, uint8_t *w, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t s)
@@ -1360,9 +1395,10 @@ cudaError_t attn_launch(AttnParams p, uint8_t *w, const CUtensorMap &kmap, const
     if (e != cudaSuccess)
         return e;
     blocks = std::min(blocks, kMostBlocks);
+    w = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(w) + 127) & ~(uintptr_t)127);
     p.cuts = reinterpret_cast<Cut *>(w);
-    p.part_ml = reinterpret_cast<float2 *>(w + kMostBlocks * sizeof(Cut));
-    p.parts = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(w + parts_offset(p.part_rows)) + 31) & ~(uintptr_t)31);
+    p.part_ml = reinterpret_cast<float2 *>(w + kCutBytes);
+    p.parts = reinterpret_cast<float *>(w + parts_offset(p.part_rows));
     // Both start early and wait inside: barriers and tensor memory are set up while the kernel before still runs.
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

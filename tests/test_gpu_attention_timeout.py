@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 CASES = {
     "long": dict(seqs=[(1, 70001)], hq=12, hk=1, d=128, page=64),
     "long, 64 channels": dict(seqs=[(1, 150001)], hq=12, hk=1, d=64, page=64),
-    "ragged": dict(seqs=[(1, 700 * i % 9000) for i in range(60)], hq=24, hk=2, d=128, page=16),
+    "ragged": dict(seqs=[(1, 700 * i % 9000) for i in range(60)], hq=24, hk=2, d=128, page=16, gap=(3, 2)),
     "trees": dict(seqs=[(30, 9000), (30, 12000), (64, 0)], hq=24, hk=2, d=128, page=16, tree=True),
     "trees, 64 channels": dict(seqs=[(30, 20000), (30, 12000), (64, 0)], hq=24, hk=2, d=64, page=64, tree=True),
     "causal": dict(seqs=[(300, 500), (150, 3000)], hq=24, hk=2, d=64, page=24),
@@ -42,6 +42,9 @@ def test_a_wait_that_runs_out(dep, case, code):
     want = c.run(dep).clone()
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     args, out, lse, work = arguments(dep, c, status)
+    row = torch.zeros(c.T, dtype=torch.bool, device="cuda")  # of a sequence
+    for f, n in zip(c.first, c.new):
+        row[f: f + n] = True
     dep.dep_attention_selftest_timeout(args, getattr(dep, "DEP_DEV_TIMEOUT_" + code))
     torch.cuda.synchronize()
     if (case, code) == ("causal", "PRODUCER"):
@@ -50,11 +53,22 @@ def test_a_wait_that_runs_out(dep, case, code):
         assert status.item() == 0 and torch.equal(out, want)
     else:
         assert 1 <= status.item() <= 4
+        # rows are complete or NaN, and some are; those of no sequence are left
+        gone = out.isnan().all(-1) & lse.isnan()
+        assert gone.any() and (out[~row] == 7).all() and (lse[~row] == 7).all()
+        assert (gone[row] | ((out == want).all(-1) & (lse == c.lse))[row]).all()
+        # without a status word the rows tell as well
+        again, args.status = out.clone().fill_(7.0), None
+        args.o = again.data_ptr()
+        dep.dep_attention_selftest_timeout(args, getattr(dep, "DEP_DEV_TIMEOUT_" + code))
+        args.o, args.status = out.data_ptr(), status.data_ptr()
+        torch.cuda.synchronize()
+        assert again.isnan().any()
     # the same arguments and workspace once more, without a wait that is held up
     status.zero_()
     dep.dep_paged_attention(args)
     torch.cuda.synchronize()
-    assert status.item() == 0 and torch.equal(out, want) and torch.equal(lse, c.lse)
+    assert status.item() == 0 and torch.equal(out[row], want[row]) and torch.equal(lse[row], c.lse[row])
 
 
 def test_a_wait_that_is_not_needed(dep):
