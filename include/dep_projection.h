@@ -615,7 +615,8 @@ dep_status_t dep_append_kv(const dep_heads_args_t *args, void *stream);
  * that belong to no sequence keep what their rows of o and lse hold.  kv_lens int32
  * [n_seq], page_table int32 [n_seq, table_width], rows table_stride apart, tree 64-bit
  * words [tokens]: device memory.  Hq is a multiple of Hk, D 64 or 128 (else
- * UNSUPPORTED), scale finite and not negative.
+ * UNSUPPORTED, as are Hq D, tokens Hq, n_seq, n_pages and table_width page_size from
+ * about 2^31 on), scale finite and not negative.
  * Scores, sums and o's accumulators are FP32 (scores of any finite size; from about 2^27
  * on scale * q . k is itself rounded to FP32); the p_j are rounded to BF16 for the
  * product with v.  The order of sums is fixed for given sizes and lengths.  No atomics.

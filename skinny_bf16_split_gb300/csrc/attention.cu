@@ -1372,7 +1372,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
 constexpr int kMostBlocks = 152;  // of a launch: one an SM
 
 // Rows that a part may have: no item has more than all tokens give.
-int part_rows(int64_t tokens, int32_t Hq, int32_t Hk) { return (int)std::min<int64_t>(kBlockRows, tokens * (Hq / Hk)); }
+int part_rows(int64_t tokens, int32_t Hq, int32_t Hk) { return (int)std::min<int64_t>(kBlockRows, std::min<int64_t>(tokens, kBlockRows) * (Hq / Hk)); }
 
 // Of the cuts, the parts' m and sums, and the parts, whole lines of 128 bytes each (a row of a part over one line more: one token
 // over 131072 positions 94.1 -> 94.9 us).
@@ -1432,6 +1432,10 @@ dep_status_t attn_entry(const dep_attention_args_t *a, void *stream, int32_t hol
         return DEP_ERR_INVALID_ARG;
     if (a->tokens == 0)
         return DEP_OK;
+    // Lengths, rows of a sequence and channels of a token in 32 bits.
+    if (a->tokens > INT32_MAX || a->tokens * a->Hq > INT32_MAX - 4096 || (int64_t)a->Hq * a->D > INT32_MAX ||
+        (int64_t)a->table_width * a->page_size > INT32_MAX - 4096 || a->n_pages > INT32_MAX || a->n_seq > INT32_MAX - 4096)
+        return DEP_ERR_UNSUPPORTED;
     int64_t need = 0;
     if (dep_attention_workspace(a, &need) != DEP_OK)
         return DEP_ERR_UNSUPPORTED;
@@ -1442,9 +1446,6 @@ dep_status_t attn_entry(const dep_attention_args_t *a, void *stream, int32_t hol
     const int64_t T = a->tokens, qn = (int64_t)a->Hq * a->D;
     if (a->q_stride < qn || a->o_stride < qn || a->table_stride < a->table_width)
         return DEP_ERR_INVALID_ARG;
-    // Lengths and rows of a sequence in 32 bits.
-    if ((int64_t)a->table_width * a->page_size > INT32_MAX - 4096 || T * (int64_t)a->Hq > INT32_MAX - 4096 || a->n_pages > INT32_MAX || a->n_seq > INT32_MAX - 4096)
-        return DEP_ERR_UNSUPPORTED;
     const CacheRows kc{cache ? a->k_cache : nullptr, 2ll * a->D, {{2 * a->k_page_stride, a->n_pages}, {2 * a->k_slot_stride, a->page_size}, {2 * a->k_head_stride, a->Hk}}},
         vc{cache ? a->v_cache : nullptr, 2ll * a->D, {{2 * a->v_page_stride, a->n_pages}, {2 * a->v_slot_stride, a->page_size}, {2 * a->v_head_stride, a->Hk}}};
     if (!kc.sound() || !vc.sound())
