@@ -530,20 +530,31 @@ def _on(index, call, args, stream):
         call(args, stream)
 
 
+@functools.lru_cache(maxsize=1)
+def _allocator():
+    """(alloc(size, stream), free(address)) of torch's allocator on the current device.  (Its own functions where torch has
+    them, else the public ones around them: between launches a tensor costs five microseconds more.)"""
+    torch = _torch()
+    try:
+        return torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
+    except AttributeError:
+        return (lambda size, stream: torch.cuda.caching_allocator_alloc(size, stream=stream)), torch.cuda.caching_allocator_delete
+
+
 def _on_with_workspace(index, call, args, size, stream):
-    """_on, with a workspace of `size` bytes that belongs to the call's stream.  (Asked of torch's allocator
-    itself: between launches a tensor costs five microseconds more.)"""
+    """_on, with a workspace of `size` bytes that belongs to the call's stream."""
     torch = _torch()
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _on_with_workspace(index, call, args, size, stream)
     stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-    args.workspace = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, stream)
+    alloc, free = _allocator()
+    args.workspace = address = alloc(size, stream)
     args.workspace_bytes = size
     try:
         call(args, stream)
     finally:  # (whoever has it next on this stream comes after this call's kernels)
-        torch._C._cuda_cudaCachingAllocator_raw_delete(args.workspace)
+        free(address)
 
 
 def _rows(t, name, dtype, index, shape):
