@@ -1003,7 +1003,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                         for (int j = 0; j < 32; ++j)
                             top = fmaxf(top, see >> j & 1 ? __uint_as_float(v[j]) : -INFINITY);
                     }
-                    const float tm = __fmul_rn(top, c);  // (nothing fused: the same as a far row's products below)
+                    const float tm = __fmul_rn(top, c);  // (nothing fused: as a far row's products are below)
                     // (what a row does goes by its own scores: where only others were wrong it comes to the same P again)
                     const bool fresh = l == 0.0f, up = live && wrong && (tm > m + 5.0f || (fresh && tm > -INFINITY));
                     if (__any_sync(~0u, up)) {
@@ -1027,8 +1027,21 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                     // the row's maximum to a few units.  From 2^28 on FP32 rounds the maximum by eight units and more, in the end
                     // by all that an exponential takes; there c s is rounded first, as the maximum was, and its own p is 1.
                     const float off = -m;
-                    const bool far = fabsf(m) >= kFar, any_far = __any_sync(~0u, far);
-                    const float c0 = far ? c : 1.0f, c1 = far ? 1.0f : c;
+                    const bool far = fabsf(m) >= kFar;
+                    const float c1 = far ? 1.0f : c;
+                    if (__any_sync(~0u, far)) {
+#pragma unroll 1
+                        for (int w = 0; w < kTile / 16; ++w) {
+                            uint32_t v[16];
+                            tc::ld16(s_at + 16 * w, v);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), far ? c : 1.0f));
+                            tmem_st16(s_at + 16 * w, v);
+                        }
+                        tmem_wait_st();
+                    }
                     float again = 0.0f;
 #pragma unroll 1
                     for (int w = 0; w < 4; ++w) {  // (P's columns lie in those of scores already read)
@@ -1036,10 +1049,6 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                         tmem_ld32(s_at + 32 * w, v);
                         const uint32_t see = mask[w] & seen32(tree, it.own, tok, word, t * kTile + 32 * w);
                         tc::wait_ld();
-                        if (any_far)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), c0));
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
                             float a = ex2(fmaf(__uint_as_float(v[j]), c1, off)), b = ex2(fmaf(__uint_as_float(v[j + 1]), c1, off));
@@ -1302,7 +1311,9 @@ __device__ __noinline__ void spoil(const AttnParams &p)
     }
 }
 
-// The parts of the item that begins in block blockIdx.x, joined in the blocks' order; a warp takes a row.
+// The parts of the item that begins in block blockIdx.x, joined in the blocks' order; a warp takes a row.  What it costs is the
+// fetching of its code, so that is kept short (loops unrolled by more, 64-bit indexes: one token over 512 positions 13.0 -> 13.6 us,
+// with 64 channels over 131072 58.4 -> 60.8).
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
 {
@@ -1315,10 +1326,11 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
         return spoil<D>(p);
     if (cut.parts == 0 || r >= cut.rows)
         return;
-    const auto at = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + r; };
+    const auto at = [&](int i) { return (int)((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + r; };
     // Lane j: the j-th of 32 parts at once.
     float m = -INFINITY;
     bool lost = false;  // a part that is not complete
+#pragma unroll 1
     for (int i = lane; i < cut.parts; i += 32) {
         m = fmaxf(m, p.part_ml[at(i)].x);
         lost |= p.cuts[blockIdx.x + i].dead != 0;
@@ -1327,6 +1339,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
     for (int d = 16; d; d >>= 1)
         m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
     float l = lost ? __uint_as_float(0x7FFFFFFFu) : 0.0f, o[E] = {};
+#pragma unroll 1
     for (int i0 = 0; i0 < cut.parts; i0 += 32) {
         float f = 0.0f;
         if (i0 + lane < cut.parts) {
@@ -1335,7 +1348,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
             l = fmaf(ml.y, f, l);
         }
         const int n = min(32, cut.parts - i0);
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < n; ++i) {
             const float w = __shfl_sync(~0u, f, i);
             const float *src = p.parts + at(i0 + i) * D + lane * E;
