@@ -414,10 +414,14 @@ cudaError_t heads_launch(HeadsParams p, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    // Many tasks for a warp pay for the way through shared memory: 8192 tokens of 104 heads, 59 tasks a warp, 71.7 us
-    // against 79.1; 8192 of 16, nine a warp, 18.5 against 17.6, 1037 of 24, two a warp, 5.1 against 4.6.
-    if constexpr (N == 16)
-        if (rounds * p.at_once * p.tasks / ((int64_t)W * y) >= 24)
+    // Many tasks for a warp pay for the way through shared memory, where all channels are rotated by halves in all lanes and
+    // a token has many heads.  104 heads of 128, by tasks a warp: 6 of them 12.8 us against 12.9 in registers, 13 19.7 against 20.8,
+    // 26 34.6 against 37.6, 59 73.3 against 79.3; 72 of 64: 12 22.2 against 21.9, 16 27.0 against 27.7, 40 52.5 against 57.5.
+    // With few heads a token, the angles' barriers are what counts: 24 of 64, 40 tasks a warp, 62.4 against 62.7, 16 of 128 into
+    // the cache, 54 a warp, 84.7 against 82.6.  By neighbours (40 a warp) it takes 73.6 against 59.3, half of the channels 61.1
+    // against 58.8, heads of 256 64.4 against 62.5.
+    if constexpr (N == 16 && LPH <= 8 && !INTERLEAVED)
+        if (p.rot == N * LPH && p.tasks >= 9 && rounds * p.at_once * p.tasks / ((int64_t)W * y) >= 16)
             return cudaLaunchKernelEx(&cfg, heads_kernel<N, LPH, INTERLEAVED, NORM, true>, p);
     return cudaLaunchKernelEx(&cfg, heads_kernel<N, LPH, INTERLEAVED, NORM, false>, p);
 }
