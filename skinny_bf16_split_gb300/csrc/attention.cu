@@ -71,6 +71,7 @@ constexpr int kCostTwo = 4;  // and one with two tiles of rows
 constexpr int kLeast = 1;   // units of a block at least
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLift = 12.0f;  // of m over a row's maximum (and zero), log2 units: then a tile's sum is at most one (see soften())
 constexpr float kFar = 0x1p28f;  // log2 units; a maximum of that size is held to 16 units at best (see soften())
 
 struct AttnParams {
@@ -950,7 +951,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
         const int64_t token = it.first + tok;
         const uint64_t word = tree && live ? p.tree[token] : 0;
         const int clear = it.own + (tree ? 0 : __shfl_sync(~0u, tok, 0) + 1);  // all positions before it are seen by all of the warp's rows
-        float m = 0.0f, l = 0.0f;  // m: log2 units
+        float m = kLift, l = 0.0f;  // m: log2 units
         int t = it.t0 + (two ? 0 : g);
         const bool some = t < it.t1;
         for (bool first = true; t < it.t1; t += two ? 1 : 2, first = false, ++k, e += apart) {
@@ -969,10 +970,11 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
             };
             if (warp_live) {
                 const uint4 in = *reinterpret_cast<const uint4 *>(sm.masks[(kt + (t - it.t0)) % kMasks]);
-                // P and its sum keep their precision at any size, so what is taken off, m, is zero to begin with and moves
-                // only where P would grow past 2^12, or all that was seen stays below 2^-40: then O has seldom
+                // P and its sum keep their precision at any size, so what is taken off, m, is the same for all rows to begin with
+                // and moves only where a tile's sum would pass one, or all that was seen stays below 2^-40: then O has seldom
                 // to be scaled, and one pass over the scores does.  The sum (in which a NaN shows as well) tells; with another m
-                // the tile is taken anew.
+                // the tile is taken anew.  (No p is more than one, as with the maximum itself, so O leaves FP32's range for no
+                // values for which it would not then.)
                 const bool masked = (t + 1) * kTile > clear || (in.x & in.y & in.z & in.w) != ~0u;
                 bool wrong = masked, anew = masked;
                 float sum = 0.0f;
@@ -980,7 +982,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                     uint32_t pk[2][32];
                     sum = tile_exp(s_at, c, -m, pk);
                     last_product();
-                    wrong = live && !(sum <= 4096.0f && l + sum >= 0x1p-40f && fabsf(m) < kFar);
+                    wrong = live && !(sum <= 1.0f && l + sum >= 0x1p-40f && fabsf(m) < kFar);
                     if (!__any_sync(~0u, wrong)) {
                         l += sum;
                         tmem_st32(p_at, pk[0]);
@@ -1005,11 +1007,10 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                     }
                     const float tm = __fmul_rn(top, c);  // (nothing fused: as a far row's products are below)
                     // (what a row does goes by its own scores: where only others were wrong it comes to the same P again)
-                    const bool fresh = l == 0.0f, up = live && wrong && (tm > m + 5.0f || (fresh && tm > -INFINITY));
+                    const bool fresh = l == 0.0f, up = live && wrong && (tm > m - (kLift - 5.0f) || (fresh && tm > -INFINITY));
                     if (__any_sync(~0u, up)) {
-                        const float f = !up ? 1.0f : fresh ? 0.0f : ex2(m - tm);
-                        if (up)
-                            m = tm;
+                        const float to = !up ? m : fabsf(tm) < kFar ? tm + kLift : tm, f = fresh ? 0.0f : ex2(m - to);
+                        m = to;
                         l *= f;
                         if (!first)  // (the product before is done: this tile's scores came after it)
 #pragma unroll 1

@@ -71,6 +71,20 @@ def test_values_behind_scores_of_minus_infinity(dep, what, d, tree):
             assert torch.equal(got[rows, 6:], want[rows, 6:]) and torch.equal(c.lse[rows, 6:], lse[rows, 6:])
 
 
+@pytest.mark.parametrize("power,seqs,tree", [
+    (125, [(1, 511), (1, 7), (1, 999)], False), (125, [(20, 300), (64, 600)], True), (125, [(300, 100), (40, 700)], False),
+    (116, [(1, 40018), (1, 3000)], False), (116, [(16, 30003)], True), (-100, [(1, 511), (3, 40000)], False),
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_up_to_the_ends_of_their_range(dep, power, seqs, tree, d):
+    """The sums before the division stay in FP32 wherever those of exp(score - maximum) do."""
+    c = Case(seqs, 12, 2, d, 16, tree=tree, seed=6)
+    for s in range(len(seqs)):
+        c.values[s] = ((1 + c.values[s].float().abs() % 1) * 2.0 ** power).bfloat16()
+    c.fill()
+    c.check(c.run(dep))
+
+
 LONG = [
     ([(1, 5000)], 12, 1, 128, 64, False), ([(1, 40018)], 12, 1, 128, 64, False), ([(1, 70001)], 12, 1, 64, 64, False),
     ([(1, 131071)], 24, 2, 128, 64, False), ([(1, 131071)], 24, 2, 64, 128, False), ([(16, 40003)], 24, 2, 128, 128, True),
