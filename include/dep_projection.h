@@ -539,7 +539,7 @@ void dep_int8_plan_destroy(dep_int8_plan_t plan);
  * first + i and first + rot/2 + i, or with DEP_HEADS_INTERLEAVED first + 2i and
  * first + 2i + 1.  The other channels keep y.  FP32 throughout, one rounding to
  * BF16 at the end; the angle is reduced as a 64-bit fraction of a turn, so far
- * positions lose nothing (2^-53 of position * frequency).  freqs: FP64 radians a
+ * positions lose nothing (2^-53 of position * frequency) before it is rounded to FP32.  freqs: FP64 radians a
  * position, rot/2 of them (not read where rot is 0).  1/rms is right for any
  * finite x (up to 2^128).
  *
@@ -617,9 +617,10 @@ dep_status_t dep_append_kv(const dep_heads_args_t *args, void *stream);
  * words [tokens]: device memory.  Hq is a multiple of Hk, D 64 or 128 (else
  * UNSUPPORTED, as are Hq D, tokens Hq, n_seq, n_pages and table_width page_size from
  * about 2^31 on), scale finite and not negative.
- * Scores, sums and o's accumulators are FP32 (scores of any finite size; from about 2^27
- * on scale * q . k is itself rounded to FP32); the p_j are rounded to BF16 for the
- * product with v.  The order of sums is fixed for given sizes and lengths.  No atomics.
+ * Scores, sums and o's accumulators are FP32 (q . k and scale q . k of any size in FP32's
+ * range; from about 2^27 on the latter is rounded to FP32 before anything else); the p_j,
+ * taken relative to the row's largest, are rounded to BF16 for the product with v, which
+ * puts o 0.0023 (rms) off where its own rounding alone puts it 0.0017.  The order of sums is fixed for given sizes and lengths.  No atomics.
  * Workspace: device memory that the call overwrites, at least dep_attention_workspace
  * bytes (of tokens, n_seq, Hq, Hk and D alone; else INVALID_ARG).
  * Every wait in the kernel is bounded (1 s); if one gives up, a DEP_DEV_* code is stored to

@@ -3,7 +3,10 @@
 //     o = sum_j p_j v_j / sum_j p_j,  p_j = exp2(c (q . k_j) - m),  c = scale log2(e)
 //
 // in one pass over the keys and values, with any m: P and the sums are floating point, so m has only to
-// keep them in range (see soften()).
+// keep them in range (see soften()).  P is rounded to BF16, as v is: an MMA takes both operands in one 16-bit
+// type, and a second product with what the rounding leaves would be half as much again for the tensor cores, which bound
+// the trees.  Errors of at most 2^-8 of each p, of either sign: o is 0.0023 (rms) off where its own rounding makes 0.0017.
+// The sum is that of the p before rounding; scores, sums and O are FP32.
 //
 // Rows.  The n tokens of a sequence and the G = Hq / Hk query heads that share a key and value head are
 // the rows of one product: row r is token r / G, head r % G of the G.  A block takes up to 256 of them
@@ -28,13 +31,15 @@
 // and what was not finite is added to the rows that see it at the end.
 //
 // Bound, with 8 key and value heads of 128 channels, pages of 64 and 96 query heads, of measured rates: one
-// token over 131072 positions 92 us (86 % of the copy rate; 82 in the kernel, 4 in the joining, the rest
-// between), 64 over 4096 on average, ragged, 180 (88 %): HBM; 8 trees of 64 over 16384 positions 310 to 350 us as
-// the clock allows (1.2 to 1.3 PFLOP/s, 62 to 70 % of the burst rate; the tensor pipe is active 62 % of the time):
-// the chain of a group's softmax (820 cycles a tile alone, 1200 beside the other's) and its products, which two groups only
-// just hide: alone, an MMA of the scores takes 88 cycles instead of 64 (both operands from shared memory, 94 bytes a cycle)
-// and one of the values 80, so the 16 of a tile 1350 and their waits 100; only the two kinds side by side come to 65;
-// one token over 512 positions 12.4 us: latencies, half of them the first fetching of code.
+// token over 131072 positions 94 us (84 % of the copy rate), 64 over 4096 on average, ragged, 183 (87 %): HBM;
+// 8 trees of 64 over 16384 positions 310 to 350 us as the clock allows (1.2 to 1.3 PFLOP/s, 62 to 70 % of the
+// burst rate; the tensor pipe is active 61 % of the time), a prompt of 8192 tokens 1240 (70 %): the chain of a group's softmax
+// (820 cycles a tile alone, 1200 beside the other's) and its products: alone, an MMA of the scores takes 88 cycles instead of
+// 64 (both operands from shared memory, 94 bytes a cycle) and one of the values 80, so the 16 of a tile 1350 and their waits
+// 100; only the two kinds side by side come to 65.  Two groups in turn make 2900 cycles of that for a pair of tiles, which take
+// 3500 to 3950; the rest is not accounted for.  One token over 512 positions 12.7 us: latencies of the lengths, the range, the first
+// tile, the softmax, the parts and the joining.  Heads of 64 channels: 58 and 153 us for the first two (68 and 52 % of the copy
+// rate), pages that hold no groups of eight slots 203 and 427: not accounted for either.
 //
 // What was tried and dropped: keys and values by 16-byte copies alone (27 cycles an instruction, 19 B a cycle
 // and SM); prefetches into the L2 (8 trees of 64: 322 -> 345 us and more); polls instead of sleeping waits (64 ragged contexts
@@ -125,7 +130,7 @@ struct Smem {
     static constexpr int kSlots = kSlotRing / kTileBytes, kKeySlots = kSlots / 2;
     // Columns of tensor memory: scores (and P in them) 0 and 128, sums from 256; with 64 channels there is room for P in
     // columns of its own.  Then a group that has every other tile gets its next scores while P is still being multiplied:
-    // one token over 131072 positions, 96 heads over 8, 66.0 -> 56.5 us, 64 over 4096 on average 151 -> 146.  Where both
+    // one token over 131072 positions, 96 heads over 8, 66.0 -> 56.5 us when it came, 64 over 4096 on average 151 -> 146.  Where both
     // groups have the same tiles that order costs more than it gives (8 trees of 64 over 16384 254 -> 285, scores last 260).
     static constexpr bool kApart = D == 64;
     __device__ static constexpr uint32_t p_column(int g) { return kApart ? 2 * kTile + 2 * D + g * (kTile / 2) : g * kTile; }
@@ -1313,7 +1318,7 @@ __device__ __noinline__ void spoil(const AttnParams &p)
 }
 
 // The parts of the item that begins in block blockIdx.x, joined in the blocks' order; a warp takes a row.  What it costs is the
-// fetching of its code, so that is kept short (loops unrolled by more, 64-bit indexes: one token over 512 positions 13.0 -> 13.6 us,
+// fetching of its code, it seems, so that is kept short (loops unrolled by more, 64-bit indexes: one token over 512 positions 13.0 -> 13.6 us,
 // with 64 channels over 131072 58.4 -> 60.8).
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)

@@ -11,15 +11,15 @@
 //
 // Angles.  A frequency becomes a 64-bit fraction of a turn, f / 2 pi modulo 1, once a
 // block; times the position modulo 2^64 it is the angle without any reduction, to
-// 2^-53 of position * f (what FP64 holds of f / 2 pi) however far the position.  A block
-// works the angles of a few tokens out at once, for all their heads.
+// 2^-53 of position * f (what FP64 holds of f / 2 pi) however far the position, and then rounded
+// to FP32.  A block works the angles of a few tokens out at once, for all their heads.
 //
 // Bound: DRAM, each byte read once and written once; close behind it the instructions: of 8 channels
 // a lane 110 for eight, of 16 about 120 for sixteen (8192 tokens of 96 and 8 heads of 128 channels 116 us
 // with eight, 79 with sixteen).  Many tasks a warp go through shared memory, three in flight and one at
-// work without registers for them: 73.2 us, 88 % of the copy rate, the issue slots 69 % busy; with few the
-// stages do not fill, and one task ahead in registers is no slower.  8192 tokens into the cache 17.5 us, one
-// token 2.8 (launch, one load, one store).
+// work without registers for them: 73.3 us, 88 % of the copy rate, the issue slots 69 % busy; where that was measured
+// to pay is at heads_launch.  8192 tokens into the cache 17.5 us (nine tasks a warp, one ahead, three rounds of angles and
+// a barrier each; 22 % of DRAM, 56 % of the issue slots), one token 2.8 (launch, one load, one store).
 #include <cuda_bf16.h>
 
 #include <math.h>

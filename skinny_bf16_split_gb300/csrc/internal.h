@@ -243,10 +243,12 @@ CUresult encode_bf16_2d(CUtensorMap *map, const void *base, uint64_t inner, uint
 // The same matrix as {64, outer, inner / 64} column blocks (inner % 64 == 0):
 // one box {64, box_rows, blocks} equals `blocks` 2-D boxes {64, box_rows} with
 // the 128-byte swizzle, side by side in shared memory.
-CUresult encode_bf16_cache(CUtensorMap *map, const void *base, uint64_t d, uint64_t slots, uint64_t heads, uint64_t pages,
-                           int64_t slot_stride, int64_t head_stride, int64_t page_stride, uint32_t box_slots);
 CUresult encode_bf16_3d_blocks(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer,
                                uint32_t box_rows, uint32_t blocks);
+// A paged cache of rows of `d` channels, strides in elements: boxes of 64 channels and
+// `box_slots` slots of one head and page, 128-byte swizzle; pages past the end read as zeros.
+CUresult encode_bf16_cache(CUtensorMap *map, const void *base, uint64_t d, uint64_t slots, uint64_t heads, uint64_t pages,
+                           int64_t slot_stride, int64_t head_stride, int64_t page_stride, uint32_t box_slots);
 
 // Tensor map over a row-major [outer, inner] matrix of bytes, 128-byte swizzle.
 CUresult encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint32_t box_inner,
