@@ -77,6 +77,7 @@ constexpr int kLeast = 1;   // units of a block at least
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLift = 12.0f;  // of m over a row's maximum (and zero), log2 units: then a tile's sum is at most one (see soften())
+constexpr float kLifted = 0x1p12f;  // 2^kLift
 constexpr float kFar = 0x1p28f;  // log2 units; a maximum of that size is held to 16 units at best (see soften())
 
 struct AttnParams {
@@ -909,6 +910,10 @@ __device__ __forceinline__ void store32(void *to, const uint32_t (&v)[8])
                  : "memory");
 }
 
+// The logarithm of the sum; m's lift goes into l again, where it is exact: sums of about one keep their precision.  (Out of line, with
+// 64 channels and 64 ragged contexts, 159 -> 152 us.)
+__device__ __noinline__ float log_sum(float m, float l) { return (m - kLift + log2f(l * kLifted)) * kLn2; }
+
 // Adds the values of new tokens that are not finite, which were left out of the product (it would have
 // given them to every row), to the channels of a row that sees them.  FP32 or BF16 in `row`.
 template <int D>
@@ -1070,7 +1075,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                 tmem_wait_st();
             }
             if (lent) {
-                ok = wait_warp(sm, sm.x_free, (x - 1) & 1, p, DEP_DEV_TIMEOUT_EPILOGUE) && ok;
+                ok = ok && wait_warp(sm, sm.x_free, (x - 1) & 1, p, DEP_DEV_TIMEOUT_EPILOGUE);
                 lent = false;
             }
             tc::fence_before();
@@ -1178,7 +1183,7 @@ __device__ void soften(const AttnParams &p, Smem<D> &sm, uint32_t tmem)
                 if (!whole)
                     p.part_ml[part] = make_float2(m, l);
                 else if (p.lse)
-                    p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : log_sum(m, l);
             }
         }
         tc::fence_before();
@@ -1385,7 +1390,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnParams p)
     else
         out[0] = w[0];
     if (p.lse && lane == 0)
-        p.lse[token * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        p.lse[token * p.Hq + h] = l == 0.0f ? -INFINITY : log_sum(m, l);
 }
 
 constexpr int kMostBlocks = 152;  // of a launch: one an SM

@@ -90,3 +90,27 @@ def test_small_differences_of_large_scores(dep, shape, d, power):
             assert ((got[f: f + n, h].double() - p @ v).abs() <= bound).all(), (s, h)
             gl = c.lse[f: f + n, h].double()
             assert torch.where(lse == -INF, gl == -INF, (gl - lse).abs() <= 2.0 ** -22 * lse.abs()).all(), (s, h)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("context", [0, 100, 40000])
+def test_log_sum_exp_near_zero(dep, d, context):
+    """Sums of almost one: their logarithm is as exact as FP32 numbers next to one are."""
+    c = Case([(1, context), (3, 0)], 4, 2, d, 16, scale=0.125, seed=5)
+    length = context + 1
+    c.q[...] = 0
+    c.q[..., 0] = 1.0
+    # exact scores: -8 ln(length) times the scale, as near as BF16 comes to it
+    for s, n in enumerate(c.lens):
+        c.keys[s] = torch.zeros_like(c.keys[s])
+        c.keys[s][..., 0] = -8 * math.log(length if s == 0 else 1)
+    c.fill()
+    c.run(dep)
+    for s, n in enumerate(c.new):
+        see = c.seen(s)
+        x = (c.q[c.first[s]: c.first[s] + n, 0].double() @ c.keys[s][:, 0].double().T * c.scale).masked_fill(~see, -INF)
+        # the score's product with log2 e, twenty of its size at most, the sum (of equal terms, added pairwise and in turn: 2^-17
+        # of it at this length), the logarithm and its products
+        limit = 2.0 ** -22 * x.masked_fill(~see, 0).abs().amax(-1) + 2.0 ** -24 * 2 * (1 + see.sum(-1) / 64) + 2.0 ** -22
+        got = c.lse[c.first[s]: c.first[s] + n].double()
+        assert ((got - x.logsumexp(-1)[:, None]).abs() <= limit[:, None]).all(), (got, x.logsumexp(-1))
