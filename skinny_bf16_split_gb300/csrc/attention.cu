@@ -38,8 +38,8 @@
 // 64 (both operands from shared memory, 94 bytes a cycle) and one of the values 80, so the 16 of a tile 1350 and their waits
 // 100; only the two kinds side by side come to 65.  Two groups in turn make 2900 cycles of that for a pair of tiles, which take
 // 3500 to 3950; the rest is not accounted for.  One token over 512 positions 12.7 us: latencies of the lengths, the range, the first
-// tile, the softmax, the parts and the joining.  Heads of 64 channels: 58 and 153 us for the first two (68 and 52 % of the copy
-// rate), pages that hold no groups of eight slots 203 and 427: not accounted for either.
+// tile, the softmax, the parts and the joining.  Heads of 64 channels: 58 and 152 us for the first two (68 and 52 % of the copy
+// rate), pages that hold no groups of eight slots 205 and 427: not accounted for either.
 //
 // What was tried and dropped: keys and values by 16-byte copies alone (27 cycles an instruction, 19 B a cycle
 // and SM); prefetches into the L2 (8 trees of 64: 322 -> 345 us and more); polls instead of sleeping waits (64 ragged contexts
