@@ -1504,12 +1504,13 @@ dep_status_t attn_entry(const dep_attention_args_t *a, void *stream, int32_t hol
     p.page_shift = k, p.page_mul = (uint32_t)(((1ull << k) + a->page_size - 1) / a->page_size);
     p.scale = a->scale, p.status = a->status, p.hold = hold, p.part_rows = part_rows(T, a->Hq, a->Hk);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // A tile in boxes that lie within a page: their slots divide both, and are whole groups of the swizzle.
+    // A tile in boxes that lie within a page: their slots divide both, and are whole groups of the swizzle.  (No maps of strides
+    // of zero, which nothing says that a map may have.)
     int32_t box = kTile;
     while (a->page_size % box != 0)
         box /= 2;
     CUtensorMap kmap{}, vmap{};
-    if (box >= 8 && cache &&
+    if (box >= 8 && cache && !kc.flat() && !vc.flat() &&
         encode_bf16_cache(&kmap, a->k_cache, a->D, a->page_size, a->Hk, a->n_pages, a->k_slot_stride, a->k_head_stride, a->k_page_stride, box) == CUDA_SUCCESS &&
         encode_bf16_cache(&vmap, a->v_cache, a->D, a->page_size, a->Hk, a->n_pages, a->v_slot_stride, a->v_head_stride, a->v_page_stride, box) == CUDA_SUCCESS)
         p.box = box;

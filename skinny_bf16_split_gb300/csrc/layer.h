@@ -49,6 +49,14 @@ struct CacheRows {
                 return false;
         return true;
     }
+    // Whether a dimension of more than one has no stride (rows that are all the same).
+    bool flat() const
+    {
+        for (const Dim &d : dim)
+            if (d.count > 1 && d.stride == 0)
+                return true;
+        return false;
+    }
     bool aligned(int64_t to) const
     {
         if (empty())
